@@ -229,7 +229,8 @@ def _linear_own(s):
     if p is None:  # what a program makes once for a layer
         p = s["plan"] = B.LinearParams(rows=c["rows"], in_features=c["in"], out_features=c["out"], dtype=c["dtype"],
                                        out_dtype=c["out_dtype"], activation=c["act"], alpha=c["alpha"])
-        s["workspace"] = torch.empty(max(1, p.workspace_bytes), dtype=torch.uint8, device="cuda")
+        need = p.fwd_workspace_bytes if c["direction"] == "fwd" else p.bwd_workspace_bytes
+        s["workspace"] = torch.empty(max(1, need), dtype=torch.uint8, device="cuda")
     if c["direction"] == "fwd":
         return {"y": B.csa_linear_fwd(p, s["x"], s["weight"], bias=s["bias"], residual=s["residual"], workspace=s["workspace"])}
     dx, dw, db = B.csa_linear_bwd(p, s["dy"], s["x"], s["weight"], preact=s["preact"], need_db=c["bias"],
@@ -318,8 +319,7 @@ def _adamw_own(s):
     from sparse_attention_indexer_tcgen05_gb300 import binding as B
     table = s.get("plan")
     if table is None:  # the optimizer's list of tensors, made once
-        columns = {k: [t[k] for t in s["tensors"]] for k in s["tensors"][0]}
-        table = s["plan"] = B.AdamWTensors(**{k + "s" if k in ("param", "grad", "master") else k: v for k, v in columns.items()})
+        table = s["plan"] = B.AdamWTensors(**{k: [t[k] for t in s["tensors"]] for k in s["tensors"][0]})
     h = s["hyper"]
     B.csa_adamw(table, step=h["step"], lr=h["lr"], beta1=h["beta1"], beta2=h["beta2"], eps=h["eps"],
                 weight_decay=h["weight_decay"], grad_scale=s["grad_scale"])
