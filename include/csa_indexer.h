@@ -224,6 +224,122 @@ csa_status csa_indexer_bwd_noalloc(const csa_params *p, const void *q_idx, const
                                    float *loss_out, float *row_loss_out, void *dq_idx, float *dw, void *dk_idx,
                                    void *stream);
 
+/* ------------------------------------------------------------------ around the step: projections, positions, weights */
+
+/* What makes q_idx, k_idx and w out of hidden states, and what carries the step's gradients back into the weights:
+ * the projections with their epilogue (csa_linear_*), the rotary positions on their outputs (csa_rope, its own
+ * inverse and so its own gradient) and the AdamW update of many tensors (csa_adamw).  The pages name these inputs
+ * (indexer.forward_before_topk, [BUG] sec. 1 excerpt) without showing how they are made; the formulas are below.
+ * Conventions as above; pointers are 16-byte aligned, outputs do not overlap inputs unless a comment allows it. */
+
+/* Elementwise function of a projection's epilogue.  s(u) = 1 / (1 + exp(-u)).
+ *   SILU: z s(z);  GELU_TANH: z (1 + tanh(c (z + 0.044715 z^3))) / 2 with c = sqrt(2 / pi), which is
+ *   z s(2 c (z + 0.044715 z^3)). */
+typedef enum { CSA_ACT_NONE = 0, CSA_ACT_RELU = 1, CSA_ACT_SILU = 2, CSA_ACT_GELU_TANH = 3 } csa_activation;
+
+/* One projection: rows M, in_features K, out_features N. */
+typedef struct {
+    int32_t dtype;              /* csa_dtype of x, weight, preact, dx and dw */
+    int32_t out_dtype;          /* csa_dtype of y, residual and dy: dtype, or CSA_F32 */
+    int32_t activation;         /* csa_activation */
+    int32_t in_features;        /* K >= 1 */
+    int32_t out_features;       /* N >= 1 */
+    float alpha;                /* scales the product (the indexer's scale of w, for one) */
+    int64_t rows;               /* M >= 0 */
+    int64_t x_stride;           /* elements from one row of x to the next; 0: K.  At least K */
+    int64_t residual_stride;    /* the same for residual; 0: N */
+    int64_t dy_stride;          /* the same for dy; 0: N */
+} csa_linear_params;
+
+/* Bytes of device workspace a call needs (may be 0).  0 on invalid params. */
+size_t csa_linear_fwd_workspace_size(const csa_linear_params *p);
+size_t csa_linear_bwd_workspace_size(const csa_linear_params *p);
+
+/* z = alpha x W^T + bias,  y = act(z) + residual.
+ *   x [M, K], weight [N, K] contiguous, bias [N] fp32 or NULL, residual [M, N] out_dtype or NULL
+ *   -> y [M, N] out_dtype contiguous, preact [M, N] dtype contiguous or NULL: z, which the backward of an
+ *      activation reads.
+ * Sums and the epilogue are fp32, rounded once.  fp32 values are multiplied as three bf16 parts each (six products,
+ * about 2^-23 relative to the terms); a row with an infinite fp32 value gives NaN or an infinity.  y may be the
+ * residual itself when their row strides agree. */
+csa_status csa_linear_fwd(const csa_linear_params *p, const void *x, const void *weight, const float *bias,
+                          const void *residual, void *y, void *preact, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/* The gradients of csa_linear_fwd for dy = dloss/dy (the residual's own gradient is dy itself):
+ *   dz = dy act'(z);  dx = alpha dz W [M, K];  dw = alpha dz^T x [N, K];  db = sum over rows of dz [N] fp32.
+ * Each of dx, dw, db may be NULL and is then not computed.  preact is z from the forward; NULL only without an
+ * activation.  ReLU'(0) = 0.  With bf16 values dz is rounded to bf16 before the two products (as dy is); db sums it
+ * unrounded.  M = 0 gives dw = 0 and db = 0.  The same call gives the same bits every time (no atomics). */
+csa_status csa_linear_bwd(const csa_linear_params *p, const void *dy, const void *x, const void *weight,
+                          const void *preact, void *dx, void *dw, float *db, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/* Rotary positions on [rows, heads, head_dim] values: in each head the rot_dim values from rot_offset on are pairs,
+ * (i, i + rot_dim / 2) or, with interleaved, (2 i, 2 i + 1); pair i turns by the angle positions[axis(i)][row] *
+ * inv_freq[i]: (a, b) -> (a cos - b sin, a sin + b cos).  The first sections[0] pairs take axis 0, the next
+ * sections[1] axis 1, and so on (time, height, width; one axis for text).  The other values are copied. */
+#define CSA_ROPE_MAX_AXES 4
+typedef struct {
+    int32_t dtype;                        /* csa_dtype of x and out */
+    int32_t heads, head_dim;              /* >= 1 */
+    int32_t rot_offset, rot_dim;          /* rot_dim even, >= 0, at most 1024; rot_offset + rot_dim <= head_dim */
+    int32_t interleaved;                  /* 0 or 1: how the pairs lie */
+    int32_t inverse;                      /* 0 or 1.  1 turns by minus the angle: the gradient of the forward */
+    int32_t positions_64;                 /* 0: positions are int32, 1: int64 */
+    int32_t axes;                         /* 1 to CSA_ROPE_MAX_AXES */
+    int32_t sections[CSA_ROPE_MAX_AXES];  /* pairs of each axis, >= 0; those of the axes sum to rot_dim / 2 */
+    int64_t rows;                         /* >= 0 */
+    int64_t x_row_stride, x_head_stride;      /* elements; 0: heads * x_head_stride, head_dim.  At least head_dim */
+    int64_t out_row_stride, out_head_stride;  /* the same for out */
+} csa_rope_params;
+
+/*   x, positions [axes, rows], inv_freq [rot_dim / 2] fp64 -> out.
+ * out may be x itself with the same strides (the values outside the rotation are then left as they are).  Angles are
+ * exact modulo one turn for every position the type holds, negative ones too: a frequency is kept as a 64-bit
+ * fraction of a turn and multiplied in integers.  inv_freq holds finite values. */
+csa_status csa_rope(const csa_rope_params *p, const void *x, const void *positions, const double *inv_freq, void *out,
+                    void *stream);
+
+/* Elements that share one scale of an 8-bit state. */
+#define CSA_ADAMW_BLOCK 256
+
+/* How the two moments are held.
+ *   CSA_STATE_F32:  m, v fp32.
+ *   CSA_STATE_E4M3: one e4m3 byte per element and one fp32 scale per CSA_ADAMW_BLOCK elements (the last block may be
+ *     short): m holds m / m_scale, v holds sqrt(v) / v_scale, each scale the block's largest magnitude / 448.  The
+ *     code of a v > 0 is never 0 (it is raised to the smallest one, 2^-9), so that a step is never divided by a
+ *     second moment that rounding lost. */
+typedef enum { CSA_STATE_F32 = 0, CSA_STATE_E4M3 = 1 } csa_state_dtype;
+
+/* One tensor of an AdamW step; device pointers.  A zero-filled state is the state before the first step. */
+typedef struct {
+    void *param;               /* [numel] param_dtype, updated */
+    const void *grad;          /* [numel] grad_dtype */
+    float *master;             /* [numel] fp32 or NULL: the weights that the step updates; param is their rounding */
+    void *m, *v;               /* [numel] fp32 or e4m3, updated */
+    float *m_scale, *v_scale;  /* [ceil(numel / CSA_ADAMW_BLOCK)] for CSA_STATE_E4M3, updated; else not read */
+    int64_t numel;             /* >= 0 */
+    int32_t param_dtype, grad_dtype, state_dtype;
+} csa_adamw_tensor;
+
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay;  /* finite; 0 <= beta < 1, eps >= 0 */
+    int64_t step;                /* 1 for the first step */
+    const float *lr_dev;         /* device scalar that replaces lr, or NULL (for a captured graph) */
+    const int64_t *step_dev;     /* device scalar that replaces step, or NULL */
+    const float *grad_scale;     /* device scalar that every gradient is multiplied by (clipping), or NULL */
+    const float *found_inf;      /* device scalar or NULL: not 0 leaves every tensor and state as it is */
+} csa_adamw_params;
+
+/* One AdamW step over `count` tensors, t = step:
+ *   g = grad_scale grad;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   p = p - lr weight_decay p - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * in fp32, with the unrounded m and v in the update.  `tensors` is a host array, read before the call returns.  No
+ * workspace.  Two tensors that name the same param, master, m, v or scale are refused; buffers that overlap in any
+ * other way are the caller's error. */
+csa_status csa_adamw(const csa_adamw_params *p, const csa_adamw_tensor *tensors, int32_t count, void *stream);
+
 /* ------------------------------------------------------------------ diagnostics */
 
 /* Test aid: the fp32 scores exactly as csa_indexer_fwd computes them, for rows

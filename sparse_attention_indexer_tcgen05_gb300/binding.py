@@ -10,7 +10,14 @@ device memory (outputs and workspace) and the current stream.  The functions kee
                                                                     -> (loss, dq_idx, dw, dk_idx)
     csa_scores_debug(params, q_idx, w, k_idx, row_begin, row_count) -> scores
 
-and ``CSAIndexerLoss`` wraps the step as an autograd function (forward returns ids and the loss; backward
+Around the step (what makes q_idx, w and k_idx out of hidden states, and updates the weights that do):
+
+    csa_linear_fwd(params, x, weight[, bias, residual])             -> y            (projection with its epilogue)
+    csa_linear_bwd(params, dy, x, weight[, preact])                 -> (dx, dw, db)
+    csa_rope(params, x, positions, inv_freq)                        -> out          (rotary positions; also their gradient)
+    csa_adamw(tensors, step, ...)                                                   (AdamW over many tensors, in place)
+
+with ``CSALinear`` / ``csa_linear`` and ``CSARope`` / ``csa_rotary`` as their autograd forms, and ``CSAIndexerLoss`` wraps the step as an autograd function (forward returns ids and the loss; backward
 returns the stored indexer gradients scaled by the incoming gradient).
 
 Importing this module loads the library and raises ImportError if it has not been built: there is no
@@ -60,7 +67,51 @@ class csa_params(ctypes.Structure):
     ]
 
 
+# csa_activation and csa_state_dtype
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu_tanh": 3}
+STATE_F32, STATE_E4M3 = 0, 1
+ADAMW_BLOCK = 256      # elements that share one scale of an 8-bit state
+ROPE_MAX_AXES = 4
+
+
+class csa_linear_params(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("activation", ctypes.c_int32),
+        ("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32), ("alpha", ctypes.c_float),
+        ("rows", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64),
+        ("dy_stride", ctypes.c_int64),
+    ]
+
+
+class csa_rope_params(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("rot_offset", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+        ("inverse", ctypes.c_int32), ("positions_64", ctypes.c_int32), ("axes", ctypes.c_int32),
+        ("sections", ctypes.c_int32 * ROPE_MAX_AXES), ("rows", ctypes.c_int64),
+        ("x_row_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
+        ("out_row_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+    ]
+
+
+class csa_adamw_tensor(ctypes.Structure):
+    _fields_ = [
+        ("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("master", ctypes.c_void_p), ("m", ctypes.c_void_p),
+        ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("numel", ctypes.c_int64),
+        ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("state_dtype", ctypes.c_int32),
+    ]
+
+
+class csa_adamw_params(ctypes.Structure):
+    _fields_ = [
+        ("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+        ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64), ("lr_dev", ctypes.c_void_p),
+        ("step_dev", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p), ("found_inf", ctypes.c_void_p),
+    ]
+
+
 _P = ctypes.POINTER(csa_params)
+_PL, _PR, _PA = (ctypes.POINTER(t) for t in (csa_linear_params, csa_rope_params, csa_adamw_params))
 _vp, _sz, _i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int64
 for _name, _args, _res in [
     ("csa_topk_width", [_P], ctypes.c_int32),
@@ -78,6 +129,12 @@ for _name, _args, _res in [
     ("csa_scores_debug", [_P, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _sz, _vp], ctypes.c_int),
     ("csa_indexer_bwd_noalloc", [_P, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
      ctypes.c_int),
+    ("csa_linear_fwd_workspace_size", [_PL], ctypes.c_size_t),
+    ("csa_linear_bwd_workspace_size", [_PL], ctypes.c_size_t),
+    ("csa_linear_fwd", [_PL, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    ("csa_linear_bwd", [_PL, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    ("csa_rope", [_PR, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
+    ("csa_adamw", [_PA, _vp, ctypes.c_int32, _vp], ctypes.c_int),
     ("csa_check_device_status", [_vp], ctypes.c_int),
     ("csa_selftest_bounded_wait", [_vp], ctypes.c_int),
     ("csa_last_timeout_site", [], ctypes.c_int32),
@@ -94,6 +151,8 @@ EXPORTED = ("csa_topk_width", "csa_key_width", "csa_teacher_width", "csa_rows", 
             "csa_workspace_size", "csa_indexer_fwd", "csa_teacher", "csa_teacher_from_lse", "csa_indexer_bwd",
             "csa_scores_debug",
             "csa_indexer_bwd_noalloc",
+            "csa_linear_fwd_workspace_size", "csa_linear_bwd_workspace_size", "csa_linear_fwd", "csa_linear_bwd",
+            "csa_rope", "csa_adamw",
             "csa_check_device_status", "csa_selftest_bounded_wait", "csa_last_timeout_site", "csa_last_path",
             "csa_last_cuda_error",
             "csa_kernel_launches",
@@ -397,3 +456,371 @@ class CSAIndexerLoss(torch.autograd.Function):
 
 def csa_indexer_loss(q_idx, w, k_idx, q, kv, kv_c, sink, params: Params):
     return CSAIndexerLoss.apply(q_idx, w, k_idx, q, kv, kv_c, sink, params)
+
+
+# ------------------------------------------------------------------ around the step
+
+@contextlib.contextmanager
+def _call(name, device):
+    """The NVTX range of a call, with the tensors' device as the current one (launches go to the current device)."""
+    torch.cuda.nvtx.range_push(name)
+    try:
+        if torch.cuda.current_device() == device.index:
+            yield
+        else:
+            with torch.cuda.device(device):
+                yield
+    finally:
+        torch.cuda.nvtx.range_pop()
+
+
+def _dtype(d):
+    if isinstance(d, int) and d in TORCH_DTYPE:
+        return d
+    if d not in DTYPES:
+        raise ValueError(f"dtype must be f32 or bf16, got {d}")
+    return DTYPES[d]
+
+
+def _check_rows(t, name, dtype, device, rows, cols, stride):
+    """A [rows, cols] tensor whose rows lie `stride` elements apart (leading dimensions may be folded into rows)."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() < 1 or t.shape[-1] != cols or t.numel() != rows * cols:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{rows}, {cols}]")
+    if t.numel() == 0:
+        return
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    expect = stride
+    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n > 1 and st != expect:
+            raise ValueError(f"{name} has row stride {st}, expected {expect}")
+        expect = expect * n
+
+
+class LinearParams:
+    """One projection y = act(alpha x W^T + bias) + residual (the C struct csa_linear_params): x [rows, in_features],
+    W [out_features, in_features].  dtype is that of x, W and their gradients; out_dtype that of y, residual and dy
+    (dtype, or f32).  Strides are elements from row to row, 0 for contiguous rows."""
+
+    def __init__(self, rows, in_features, out_features, dtype="bf16", out_dtype=None, activation="none", alpha=1.0,
+                 x_stride=0, residual_stride=0, dy_stride=0):
+        if isinstance(activation, str):
+            if activation not in ACTIVATIONS:
+                raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation}")
+            activation = ACTIVATIONS[activation]
+        dt = _dtype(dtype)
+        self.c = csa_linear_params(dt, dt if out_dtype is None else _dtype(out_dtype), int(activation),
+                                   int(in_features), int(out_features), float(alpha), int(rows), int(x_stride),
+                                   int(residual_stride), int(dy_stride))
+        self.ref = ctypes.byref(self.c)
+
+    @property
+    def fwd_workspace_bytes(self) -> int:
+        return _lib.csa_linear_fwd_workspace_size(self.ref)
+
+    @property
+    def bwd_workspace_bytes(self) -> int:
+        return _lib.csa_linear_bwd_workspace_size(self.ref)
+
+    @property
+    def workspace_bytes(self) -> int:
+        """Enough for either direction."""
+        return max(self.fwd_workspace_bytes, self.bwd_workspace_bytes)
+
+    @property
+    def value_dtype(self) -> torch.dtype:
+        return TORCH_DTYPE[self.c.dtype]
+
+    @property
+    def out_value_dtype(self) -> torch.dtype:
+        return TORCH_DTYPE[self.c.out_dtype]
+
+
+def _given_workspace(need, device, workspace):
+    if workspace is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace
+
+
+def csa_linear_fwd(p: LinearParams, x, weight, bias=None, residual=None, workspace=None, out=None, preact=None):
+    """y = act(alpha x weight^T + bias) + residual, in one pass with fp32 sums.  Returns y [rows, out_features].
+    preact (a [rows, out_features] tensor of p's dtype) receives the activation's argument, which csa_linear_bwd reads.
+    out may be the residual itself (contiguous)."""
+    c, dev = p.c, x.device
+    M, K, N = c.rows, c.in_features, c.out_features
+    _check_rows(x, "x", p.value_dtype, dev, M, K, c.x_stride or K)
+    _check_tensor(weight, "weight", p.value_dtype, dev, N * K)
+    if bias is not None:
+        _check_tensor(bias, "bias", torch.float32, dev, N)
+    if residual is not None:
+        _check_rows(residual, "residual", p.out_value_dtype, dev, M, N, c.residual_stride or N)
+    if out is None:
+        out = torch.empty((M, N), dtype=p.out_value_dtype, device=dev)
+    else:
+        _check_tensor(out, "out", p.out_value_dtype, dev, M * N)
+    if preact is not None:
+        _check_tensor(preact, "preact", p.value_dtype, dev, M * N)
+    with _call("csa_linear_fwd", dev):
+        ws = _given_workspace(p.fwd_workspace_bytes, dev, workspace)
+        st = _lib.csa_linear_fwd(p.ref, _ptr(x), _ptr(weight), _ptr(bias), _ptr(residual), _ptr(out), _ptr(preact),
+                                 _ptr(ws), ws.numel() * ws.element_size(), _stream(dev))
+    _check(st, "csa_linear_fwd")
+    return out
+
+
+def csa_linear_bwd(p: LinearParams, dy, x, weight, preact=None, need_dx=True, need_dw=True, need_db=True, workspace=None,
+                   out=None):
+    """The gradients of csa_linear_fwd for dy: (dx [rows, in_features], dw like weight, db [out_features] fp32), None
+    in the place of one that is not asked for.  preact is what the forward wrote there (not read without an
+    activation).  out: a tuple of the three to write to."""
+    c, dev = p.c, dy.device
+    M, K, N = c.rows, c.in_features, c.out_features
+    _check_rows(dy, "dy", p.out_value_dtype, dev, M, N, c.dy_stride or N)
+    if need_dw:
+        _check_rows(x, "x", p.value_dtype, dev, M, K, c.x_stride or K)
+    if need_dx:
+        _check_tensor(weight, "weight", p.value_dtype, dev, N * K)
+    if c.activation != 0:
+        _check_tensor(preact, "preact", p.value_dtype, dev, M * N)
+    else:
+        preact = None
+    want = (("dx", need_dx, (M, K), p.value_dtype), ("dw", need_dw, (N, K), p.value_dtype),
+            ("db", need_db, (N,), torch.float32))
+    got = []
+    for i, (name, need, shape, dtype) in enumerate(want):
+        t = out[i] if out is not None and need else None
+        if need and t is None:
+            t = torch.empty(shape, dtype=dtype, device=dev)
+        elif need:
+            _check_tensor(t, name, dtype, dev, shape[0] * shape[1] if len(shape) > 1 else shape[0])
+        got.append(t)
+    dx, dw, db = got
+    with _call("csa_linear_bwd", dev):
+        ws = _given_workspace(p.bwd_workspace_bytes, dev, workspace)
+        st = _lib.csa_linear_bwd(p.ref, _ptr(dy), _ptr(x), _ptr(weight), _ptr(preact), _ptr(dx), _ptr(dw), _ptr(db),
+                                 _ptr(ws), ws.numel() * ws.element_size(), _stream(dev))
+    _check(st, "csa_linear_bwd")
+    return dx, dw, db
+
+
+class RopeParams:
+    """Rotary positions on [rows, heads, head_dim] values (the C struct csa_rope_params).  rot_dim values from
+    rot_offset on rotate (default: all); sections gives the frequency pairs of each position axis (default: one axis);
+    interleaved pairs are (2 i, 2 i + 1), others (i, i + rot_dim / 2); inverse turns back (the gradient)."""
+
+    def __init__(self, rows, heads, head_dim, dtype="bf16", rot_dim=None, rot_offset=0, sections=None,
+                 interleaved=False, inverse=False, positions_64=False, x_row_stride=0, x_head_stride=0,
+                 out_row_stride=0, out_head_stride=0):
+        rot_dim = int(head_dim - rot_offset if rot_dim is None else rot_dim)
+        sections = [rot_dim // 2] if sections is None else [int(n) for n in sections]
+        if not 1 <= len(sections) <= ROPE_MAX_AXES:
+            raise ValueError(f"sections must name 1 to {ROPE_MAX_AXES} axes, got {len(sections)}")
+        self.c = csa_rope_params(_dtype(dtype), int(heads), int(head_dim), int(rot_offset), rot_dim,
+                                 1 if interleaved else 0, 1 if inverse else 0, 1 if positions_64 else 0, len(sections),
+                                 (ctypes.c_int32 * ROPE_MAX_AXES)(*sections), int(rows), int(x_row_stride),
+                                 int(x_head_stride), int(out_row_stride), int(out_head_stride))
+        self.ref = ctypes.byref(self.c)
+
+    def inverted(self) -> "RopeParams":
+        """The same rotation backwards, on contiguous values: what a gradient of out takes."""
+        c = self.c
+        return RopeParams(c.rows, c.heads, c.head_dim, c.dtype, c.rot_dim, c.rot_offset, list(c.sections[:c.axes]),
+                          c.interleaved, not c.inverse, c.positions_64)
+
+    @property
+    def value_dtype(self) -> torch.dtype:
+        return TORCH_DTYPE[self.c.dtype]
+
+
+def _check_heads(t, name, p, device, row_stride, head_stride):
+    c = p.c
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if t.dtype != p.value_dtype:
+        raise ValueError(f"{name} must be {p.value_dtype}, got {t.dtype}")
+    head_stride = head_stride or c.head_dim
+    row_stride = row_stride or c.heads * head_stride
+    if head_stride == c.head_dim and row_stride == c.heads * head_stride:  # contiguous: any shape of that many values
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous (or its strides given to RopeParams)")
+        if t.numel() != c.rows * c.heads * c.head_dim:
+            raise ValueError(f"{name} has {t.numel()} elements, expected {c.rows * c.heads * c.head_dim}")
+        return
+    if tuple(t.shape) != (c.rows, c.heads, c.head_dim):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(c.rows, c.heads, c.head_dim)}")
+    want = (row_stride, head_stride, 1)
+    if t.numel() and any(n > 1 and a != b for n, a, b in zip(t.shape, t.stride(), want)):
+        raise ValueError(f"{name} has strides {t.stride()}, expected {want}")
+
+
+def csa_rope(p: RopeParams, x, positions, inv_freq, out=None):
+    """x [rows, heads, head_dim] with its pairs turned by positions [axes, rows] (int32, or int64 with positions_64)
+    times inv_freq [rot_dim / 2] (fp64).  Returns out; out=x works in place."""
+    c, dev = p.c, x.device
+    _check_heads(x, "x", p, dev, c.x_row_stride, c.x_head_stride)
+    _check_tensor(positions, "positions", torch.int64 if c.positions_64 else torch.int32, dev, c.axes * c.rows)
+    _check_tensor(inv_freq, "inv_freq", torch.float64, dev, c.rot_dim // 2)
+    if out is None:
+        if c.out_row_stride or c.out_head_stride:
+            raise ValueError("out is required where RopeParams gives its strides")
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    else:
+        _check_heads(out, "out", p, dev, c.out_row_stride, c.out_head_stride)
+    with _call("csa_rope", dev):
+        st = _lib.csa_rope(p.ref, _ptr(x), _ptr(positions), _ptr(inv_freq), _ptr(out), _stream(dev))
+    _check(st, "csa_rope")
+    return out
+
+
+class AdamWTensors:
+    """The tensors of csa_adamw, checked and laid out once.  Lists of equal length: param (f32 or bf16), grad (f32 or
+    bf16), the moments m and v (both f32, or both float8_e4m3fn with their f32 scales m_scale and v_scale, one per
+    ADAMW_BLOCK elements, last block short), and master: an f32 copy that the step updates, param being its rounding
+    (a list, with None for a tensor that has none).  ``AdamWTensors.zero_state`` makes m, v and scales."""
+
+    def __init__(self, param, grad, m, v, m_scale=None, v_scale=None, master=None):
+        n = len(param)
+        none = [None] * n
+        columns = dict(param=list(param), grad=list(grad), m=list(m), v=list(v), m_scale=list(m_scale or none),
+                       v_scale=list(v_scale or none), master=list(master or none))
+        for name, c in columns.items():
+            if len(c) != n:
+                raise ValueError(f"{name} has {len(c)} tensors, param has {n}")
+        self.tensors = columns                       # keeps the buffers alive
+        self.device = param[0].device if n else None
+        self.count = n
+        self.table = (csa_adamw_tensor * n)()
+        for i, e in enumerate(self.table):
+            t = {name: c[i] for name, c in columns.items()}
+            numel = t["param"].numel()
+            for name in ("param", "grad"):
+                if t[name].dtype not in DTYPES:
+                    raise ValueError(f"{name}[{i}] must be f32 or bf16, got {t[name].dtype}")
+                _check_tensor(t[name], f"{name}[{i}]", t[name].dtype, self.device, numel)
+            eight = t["m"].dtype == torch.float8_e4m3fn
+            for name in ("m", "v"):
+                _check_tensor(t[name], f"{name}[{i}]", torch.float8_e4m3fn if eight else torch.float32, self.device, numel)
+            for name in ("m_scale", "v_scale") if eight else ():
+                _check_tensor(t[name], f"{name}[{i}]", torch.float32, self.device, -(-numel // ADAMW_BLOCK))
+            if t["master"] is not None:
+                _check_tensor(t["master"], f"master[{i}]", torch.float32, self.device, numel)
+            e.param, e.grad, e.master = _ptr(t["param"]), _ptr(t["grad"]), _ptr(t["master"])
+            e.m, e.v, e.m_scale, e.v_scale = _ptr(t["m"]), _ptr(t["v"]), _ptr(t["m_scale"]), _ptr(t["v_scale"])
+            e.numel, e.param_dtype, e.grad_dtype = numel, DTYPES[t["param"].dtype], DTYPES[t["grad"].dtype]
+            e.state_dtype = STATE_E4M3 if eight else STATE_F32
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name, i)
+                       for name, c in columns.items() if name != "grad" for i, t in enumerate(c)
+                       if t is not None and t.numel())
+        for (_, end, a, i), (begin, _, b, j) in zip(spans, spans[1:]):
+            if begin < end:
+                raise ValueError(f"{a}[{i}] and {b}[{j}] overlap")
+
+    @staticmethod
+    def zero_state(param, eight_bit=False):
+        """m, v (and their scales) before the first step, as keyword arguments of AdamWTensors."""
+        dt = torch.float8_e4m3fn if eight_bit else torch.float32
+        state = {k: [torch.zeros(t.shape, dtype=torch.uint8, device=t.device).view(dt) if eight_bit
+                     else torch.zeros(t.shape, dtype=dt, device=t.device) for t in param] for k in ("m", "v")}
+        if eight_bit:
+            state.update({k: [torch.zeros(-(-t.numel() // ADAMW_BLOCK), dtype=torch.float32, device=t.device)
+                              for t in param] for k in ("m_scale", "v_scale")})
+        return state
+
+    def set_grads(self, grad):
+        """Other gradient tensors of the same sizes (types may differ) for the next steps."""
+        if len(grad) != self.count:
+            raise ValueError(f"grad has {len(grad)} tensors, param has {self.count}")
+        for i, (g, e) in enumerate(zip(grad, self.table)):
+            if g.dtype not in DTYPES:
+                raise ValueError(f"grad[{i}] must be f32 or bf16, got {g.dtype}")
+            _check_tensor(g, f"grad[{i}]", g.dtype, self.device, e.numel)
+        for g, e in zip(grad, self.table):
+            e.grad, e.grad_dtype = g.data_ptr(), DTYPES[g.dtype]
+        self.tensors["grad"] = list(grad)
+
+
+def csa_adamw(tensors: AdamWTensors, step, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01,
+              grad_scale=None, found_inf=None):
+    """One AdamW step over all tensors, in place.  step (1 for the first) and lr are numbers, or device scalars (int64,
+    f32) that are read when the step runs, for a captured graph; grad_scale (f32 device scalar) multiplies every
+    gradient; found_inf (f32 device scalar), when not 0, leaves everything as it is."""
+    p = csa_adamw_params(0.0, float(beta1), float(beta2), float(eps), float(weight_decay), 1, None, None, None, None)
+    dev = tensors.device
+    for name, t, dtype in (("lr", lr, torch.float32), ("step", step, torch.int64), ("grad_scale", grad_scale, torch.float32),
+                           ("found_inf", found_inf, torch.float32)):
+        if isinstance(t, torch.Tensor):
+            _check_tensor(t, name, dtype, dev, 1)
+            setattr(p, name if name in ("grad_scale", "found_inf") else name + "_dev", t.data_ptr())
+        elif name in ("lr", "step"):
+            setattr(p, name, t)
+        elif t is not None:
+            raise ValueError(f"{name} must be a device scalar")
+    if dev is None:
+        return
+    with _call("csa_adamw", dev):
+        st = _lib.csa_adamw(ctypes.byref(p), tensors.table, tensors.count, _stream(dev))
+    _check(st, "csa_adamw")
+
+
+class CSALinear(torch.autograd.Function):
+    """y = CSALinear.apply(x, weight, bias, residual, params): gradients flow to all four tensors (bias and residual
+    may be None)."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, params):
+        c = params.c
+        preact = None
+        if c.activation != 0 and any(ctx.needs_input_grad[:3]):
+            preact = torch.empty((c.rows, c.out_features), dtype=params.value_dtype, device=x.device)
+        y = csa_linear_fwd(params, x, weight.contiguous(), bias, residual, preact=preact)
+        ctx.params, ctx.x_shape = params, x.shape
+        ctx.residual_shape = residual.shape if residual is not None else None
+        ctx.save_for_backward(x, weight, preact)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, preact = ctx.saved_tensors
+        c = ctx.params.c
+        need = ctx.needs_input_grad
+        dx = dw = db = None
+        dy = dy.contiguous()
+        if any(need[:3]):
+            p = ctx.params
+            if c.dy_stride:  # autograd hands contiguous gradients over
+                p = LinearParams(c.rows, c.in_features, c.out_features, c.dtype, c.out_dtype, c.activation, c.alpha,
+                                 c.x_stride)
+            dx, dw, db = csa_linear_bwd(p, dy, x, weight.contiguous(), preact, need[0], need[1], need[2])
+        return (dx.view(ctx.x_shape) if dx is not None else None, dw.view(weight.shape) if dw is not None else None, db,
+                dy.view(ctx.residual_shape) if need[3] else None, None)
+
+
+def csa_linear(x, weight, bias=None, residual=None, *, params: LinearParams):
+    return CSALinear.apply(x, weight, bias, residual, params)
+
+
+class CSARope(torch.autograd.Function):
+    """out = CSARope.apply(x, positions, inv_freq, params): the gradient of x is the inverse rotation of out's."""
+
+    @staticmethod
+    def forward(ctx, x, positions, inv_freq, params):
+        ctx.params = params
+        ctx.save_for_backward(positions, inv_freq)
+        return csa_rope(params, x, positions, inv_freq)
+
+    @staticmethod
+    def backward(ctx, dout):
+        positions, inv_freq = ctx.saved_tensors
+        return csa_rope(ctx.params.inverted(), dout.contiguous(), positions, inv_freq), None, None, None
+
+
+def csa_rotary(x, positions, inv_freq, params: RopeParams):
+    return CSARope.apply(x, positions, inv_freq, params)

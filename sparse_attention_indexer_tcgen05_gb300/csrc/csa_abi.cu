@@ -25,6 +25,10 @@ thread_local const char *t_last_path = "none";
 constexpr size_t kAlign = 256;
 inline size_t align_up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
 
+}  // namespace
+
+namespace csa {
+
 // Host-side fault injection for the error paths (CSA_FAULT=<site>): the named entry returns the
 // named status without enqueueing anything.  Sites: invalid_arg, unsupported, alignment, workspace,
 // cuda, timeout.  Read on every call so a test can set and clear it.
@@ -40,6 +44,12 @@ csa_status injected_fault()
     if (!strcmp(f, "timeout")) return CSA_ERR_TIMEOUT;
     return CSA_OK;
 }
+
+void note_path(const char *path) { t_last_path = path; }
+
+}  // namespace csa
+
+namespace {
 
 struct Plan {
     Geo g;
@@ -164,6 +174,18 @@ thread_local int32_t t_last_timeout_site = 0;
             return CSA_ERR_CUDA;                        \
         }                                               \
     } while (0)
+
+}  // namespace
+
+namespace csa {
+csa_status cuda_failed(cudaError_t e)
+{
+    t_last_cuda_error = cudaGetErrorString(e);
+    return CSA_ERR_CUDA;
+}
+}  // namespace csa
+
+namespace {
 
 int g_max_smem = -1;
 

@@ -208,6 +208,24 @@ __device__ __forceinline__ long long gd_row_of(const Geo &g, int b, int s, long 
 // Count of kernel launches made by the library in this process (diagnostics; see csa_kernel_launches).
 void note_launches(int n);
 
+// ---------------------------------------------------------------- shared by the entry points (csa_abi.cu)
+
+csa_status injected_fault();                 // the status CSA_FAULT asks for, CSA_OK without it
+csa_status cuda_failed(cudaError_t e);       // keeps the message for csa_last_cuda_error
+void note_path(const char *path);            // what csa_last_path returns on this host thread
+
+// ---------------------------------------------------------------- operators around the step
+
+size_t linear_fwd_workspace(const csa_linear_params &p);
+size_t linear_bwd_workspace(const csa_linear_params &p);
+cudaError_t launch_linear_fwd(const csa_linear_params &p, const void *x, const void *weight, const float *bias,
+                              const void *residual, void *y, void *preact, void *ws, cudaStream_t st);
+cudaError_t launch_linear_bwd(const csa_linear_params &p, const void *dy, const void *x, const void *weight,
+                              const void *preact, void *dx, void *dw, float *db, void *ws, cudaStream_t st);
+cudaError_t launch_rope(const csa_rope_params &p, const void *x, const void *positions, const double *inv_freq,
+                        void *out, cudaStream_t st);
+cudaError_t launch_adamw(const csa_adamw_params &p, const csa_adamw_tensor *t, int count, cudaStream_t st);
+
 // ---------------------------------------------------------------- launchers (k_generic.cu)
 
 cudaError_t launch_build_cu_c(const Geo &g, int *cu_c, cudaStream_t st);

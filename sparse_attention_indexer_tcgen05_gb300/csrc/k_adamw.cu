@@ -1,0 +1,335 @@
+// k_adamw.cu -- one AdamW step over many tensors in one launch per group of equal types.
+//
+//   g = s grad;  m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
+//   p = p - lr wd p - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
+//
+// in fp32.  The states are fp32, or 8 bits: e4m3 codes of m and of sqrt(v) with one fp32 scale per 256 elements,
+// the block's largest magnitude / 448.  The root is what is stored because the update divides by it: e4m3 then spans
+// a factor of 448 / 2^-9 = 2.3e5 of it (the square would leave a factor of 480 in the root).  A code of v > 0 is at
+// least the smallest one, 2^-9: a root that rounded to 0 while m did not would leave eps alone in the divisor.
+//
+// Bound by memory: every state, weight and gradient is read and written once.  A warp owns one block of 256 elements,
+// 8 consecutive ones per lane, so each tensor is read and written in 8- or 16-byte accesses, the block's two maxima
+// are warp reductions and no shared memory is needed.  The tensors' pointers travel in the kernel's parameters (no
+// copy, no device table that must outlive the call, any stream capture keeps them); a CTA finds its tensor by a
+// binary search over the first chunk of each.
+#include "csa_internal.cuh"
+
+#include <cuda_fp8.h>
+#include <math.h>
+
+namespace csa {
+namespace adamw {
+
+constexpr int THREADS = 256;
+constexpr int VEC = 8;                         // elements per lane: one warp covers a block of 256
+constexpr int STEP = THREADS * VEC;            // elements per CTA and iteration
+constexpr int ITER = 2;
+constexpr int CHUNK = STEP * ITER;             // elements per CTA
+constexpr float E4M3_MAX = 448.f;
+constexpr float E4M3_TINY = 0.001953125f;      // 2^-9
+
+struct Entry {
+    void *param;
+    const void *grad;
+    float *master;
+    void *m, *v;
+    float *m_scale, *v_scale;
+    long long numel;
+    unsigned first;  // the tensor's first chunk
+};
+
+struct Hyper {
+    float lr, lr_wd, b1, nb1, b2, nb2, eps;  // nb = 1 - b, rounded once from the doubles
+    float c1, rs2;                           // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+    float wd, log_b1, log_b2;                // for lr and step on the device
+    const float *lr_dev, *grad_scale, *found_inf;
+    const int64_t *step_dev;
+};
+
+template <int CAP> struct Table {
+    Entry e[CAP];
+    int n;
+};
+
+// 8 values from p (element i, n - i of them valid)
+template <typename T> __device__ __forceinline__ void load8(const T *p, long long i, long long n, float (&x)[VEC])
+{
+    if (i + VEC <= n) {
+        if constexpr (sizeof(T) == 4) {
+            const float4 a = __ldcs(reinterpret_cast<const float4 *>(p + i));
+            const float4 b = __ldcs(reinterpret_cast<const float4 *>(p + i) + 1);
+            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+            x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+        } else {
+            const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p + i));
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                x[2 * k] = __uint_as_float(w[k] << 16);
+                x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < VEC; k++) x[k] = i + k < n ? ldf<T>(p, i + k) : 0.f;
+    }
+}
+
+template <typename T> __device__ __forceinline__ void store8(T *p, long long i, long long n, const float (&x)[VEC])
+{
+    if (i + VEC <= n) {
+        if constexpr (sizeof(T) == 4) {
+            __stcs(reinterpret_cast<float4 *>(p + i), make_float4(x[0], x[1], x[2], x[3]));
+            __stcs(reinterpret_cast<float4 *>(p + i) + 1, make_float4(x[4], x[5], x[6], x[7]));
+        } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+                w[k] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+            __stcs(reinterpret_cast<uint4 *>(p + i), make_uint4(w[0], w[1], w[2], w[3]));
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < VEC; k++)
+            if (i + k < n) p[i + k] = from_f<T>(x[k]);
+    }
+}
+
+__device__ __forceinline__ uint2 load_codes(const void *p, long long i, long long n)
+{
+    const unsigned char *c = static_cast<const unsigned char *>(p);
+    if (i + VEC <= n) return __ldcs(reinterpret_cast<const uint2 *>(c + i));
+    uint2 r = make_uint2(0u, 0u);
+#pragma unroll
+    for (int k = 0; k < VEC; k++)
+        if (i + k < n) (k < 4 ? r.x : r.y) |= (uint32_t)c[i + k] << (8 * (k & 3));
+    return r;
+}
+
+__device__ __forceinline__ void store_codes(void *p, long long i, long long n, uint2 r)
+{
+    unsigned char *c = static_cast<unsigned char *>(p);
+    if (i + VEC <= n) {
+        __stcs(reinterpret_cast<uint2 *>(c + i), r);
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < VEC; k++)
+        if (i + k < n) c[i + k] = (unsigned char)((k < 4 ? r.x : r.y) >> (8 * (k & 3)));
+}
+
+__device__ __forceinline__ void decode8(uint2 r, float scale, float (&x)[VEC])
+{
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const __nv_fp8x2_storage_t c = (__nv_fp8x2_storage_t)(((k < 2 ? r.x : r.y) >> (16 * (k & 1))) & 0xffffu);
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        x[2 * k] = f.x * scale;
+        x[2 * k + 1] = f.y * scale;
+    }
+}
+
+__device__ __forceinline__ uint2 encode8(const float (&x)[VEC])
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++)
+        w[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[2 * k], x[2 * k + 1]), __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+template <typename PT, typename GT, bool E4M3, int CAP>
+__global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ Table<CAP> tab, const Hyper h)
+{
+    if (h.found_inf != nullptr && *h.found_inf != 0.f) return;
+    int lo = 0, hi = tab.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (tab.e[mid].first <= blockIdx.x) lo = mid; else hi = mid - 1;
+    }
+    const Entry &e = tab.e[lo];
+    const long long n = e.numel;
+    const long long i0 = (long long)(blockIdx.x - e.first) * CHUNK + threadIdx.x * VEC;
+    const float gs = h.grad_scale != nullptr ? *h.grad_scale : 1.f;
+    float c1 = h.c1, rs2 = h.rs2, lr_wd = h.lr_wd;
+    if (h.lr_dev != nullptr || h.step_dev != nullptr) {
+        // 1 - b^t without cancellation for small t: -expm1(t log b)
+        const float lr = h.lr_dev != nullptr ? *h.lr_dev : h.lr;
+        if (h.step_dev != nullptr) {
+            const float t = (float)*h.step_dev;
+            c1 = lr / -expm1f(t * h.log_b1);
+            rs2 = rsqrtf(-expm1f(t * h.log_b2));
+        } else {
+            c1 = lr * h.c1;  // the host left 1 / (1 - b1^t) there
+        }
+        lr_wd = lr * h.wd;
+    }
+    PT *param = static_cast<PT *>(e.param);
+    const GT *grad = static_cast<const GT *>(e.grad);
+
+#pragma unroll
+    for (int it = 0; it < ITER; it++) {
+        const long long i = i0 + (long long)it * STEP;
+        const bool some = i < n;
+        if (__ballot_sync(0xffffffffu, some) == 0u) return;  // the whole warp lies behind the end
+        float p[VEC], g[VEC], m[VEC], v[VEC];
+        const long long blk = i / CSA_ADAMW_BLOCK;  // the same for the whole warp
+        load8<GT>(grad, i, n, g);
+        if constexpr (E4M3) {
+            const uint2 cm = load_codes(e.m, i, n), cv = load_codes(e.v, i, n);
+            const float sm = e.m_scale[blk], sv = e.v_scale[blk];
+            if (e.master != nullptr) load8<float>(e.master, i, n, p); else load8<PT>(param, i, n, p);
+            decode8(cm, sm, m);
+            decode8(cv, sv, v);
+#pragma unroll
+            for (int k = 0; k < VEC; k++) v[k] *= v[k];
+        } else {
+            load8<float>(static_cast<const float *>(e.m), i, n, m);
+            load8<float>(static_cast<const float *>(e.v), i, n, v);
+            if (e.master != nullptr) load8<float>(e.master, i, n, p); else load8<PT>(param, i, n, p);
+        }
+        float r[VEC], top_m = 0.f, top_r = 0.f;
+#pragma unroll
+        for (int k = 0; k < VEC; k++) {
+            const float gk = g[k] * gs;
+            m[k] = h.b1 * m[k] + h.nb1 * gk;
+            v[k] = h.b2 * v[k] + h.nb2 * gk * gk;
+            r[k] = sqrtf(v[k]);
+            p[k] = p[k] - lr_wd * p[k] - c1 * m[k] / (r[k] * rs2 + h.eps);
+            top_m = fmaxf(top_m, fabsf(m[k]));
+            top_r = fmaxf(top_r, r[k]);
+        }
+        if (e.master != nullptr) store8<float>(e.master, i, n, p);
+        store8<PT>(param, i, n, p);
+        if constexpr (E4M3) {
+            top_m = warp_max(top_m);
+            top_r = warp_max(top_r);
+            const float sm = top_m / E4M3_MAX, sr = top_r / E4M3_MAX;
+            const float dm = sm > 0.f ? sm : 1.f, dr = sr > 0.f ? sr : 1.f;
+#pragma unroll
+            for (int k = 0; k < VEC; k++) {
+                m[k] = m[k] / dm;
+                const float c = r[k] / dr;
+                v[k] = r[k] > 0.f && !(c > E4M3_TINY) ? E4M3_TINY : c;
+            }
+            store_codes(e.m, i, n, encode8(m));
+            store_codes(e.v, i, n, encode8(v));
+            if ((threadIdx.x & 31) == 0) {
+                e.m_scale[blk] = sm;
+                e.v_scale[blk] = sr;
+            }
+        } else {
+            store8<float>(static_cast<float *>(e.m), i, n, m);
+            store8<float>(static_cast<float *>(e.v), i, n, v);
+        }
+    }
+}
+
+// The tensors of one launch: parameters of a kernel hold up to 32764 bytes; few tensors take the short table.
+constexpr int CAP_SMALL = 52, CAP_LARGE = 440;
+
+template <int CAP> void fill(Table<CAP> &tab, const csa_adamw_tensor *const *t, int n)
+{
+    unsigned first = 0;
+    for (int k = 0; k < n; k++) {
+        Entry &e = tab.e[k];
+        e.param = t[k]->param;
+        e.grad = t[k]->grad;
+        e.master = t[k]->master;
+        e.m = t[k]->m;
+        e.v = t[k]->v;
+        e.m_scale = t[k]->m_scale;
+        e.v_scale = t[k]->v_scale;
+        e.numel = t[k]->numel;
+        e.first = first;
+        first += (unsigned)((t[k]->numel + CHUNK - 1) / CHUNK);
+    }
+    tab.n = n;
+}
+
+template <typename PT, typename GT, bool Q>
+cudaError_t launch_group(const csa_adamw_tensor *const *t, int n, unsigned chunks, const Hyper &h, cudaStream_t st)
+{
+    if (n <= CAP_SMALL) {
+        Table<CAP_SMALL> tab;
+        fill(tab, t, n);
+        adamw_kernel<PT, GT, Q, CAP_SMALL><<<chunks, THREADS, 0, st>>>(tab, h);
+    } else {
+        Table<CAP_LARGE> tab;
+        fill(tab, t, n);
+        adamw_kernel<PT, GT, Q, CAP_LARGE><<<chunks, THREADS, 0, st>>>(tab, h);
+    }
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kind(int kind, const csa_adamw_tensor *const *t, int n, unsigned chunks, const Hyper &h,
+                        cudaStream_t st)
+{
+    using bf = __nv_bfloat16;
+    switch (kind) {
+    case 0: return launch_group<float, float, false>(t, n, chunks, h, st);
+    case 1: return launch_group<float, float, true>(t, n, chunks, h, st);
+    case 2: return launch_group<float, bf, false>(t, n, chunks, h, st);
+    case 3: return launch_group<float, bf, true>(t, n, chunks, h, st);
+    case 4: return launch_group<bf, float, false>(t, n, chunks, h, st);
+    case 5: return launch_group<bf, float, true>(t, n, chunks, h, st);
+    case 6: return launch_group<bf, bf, false>(t, n, chunks, h, st);
+    default: return launch_group<bf, bf, true>(t, n, chunks, h, st);
+    }
+}
+
+}  // namespace adamw
+
+cudaError_t launch_adamw(const csa_adamw_params &p, const csa_adamw_tensor *t, int count, cudaStream_t st)
+{
+    using namespace adamw;
+    Hyper h;
+    const double bc1 = 1.0 - pow(p.beta1, (double)p.step), bc2 = 1.0 - pow(p.beta2, (double)p.step);
+    h.lr = (float)p.lr;
+    h.wd = (float)p.weight_decay;
+    h.lr_wd = (float)(p.lr * p.weight_decay);
+    h.b1 = (float)p.beta1;
+    h.nb1 = (float)(1.0 - p.beta1);
+    h.b2 = (float)p.beta2;
+    h.nb2 = (float)(1.0 - p.beta2);
+    h.eps = (float)p.eps;
+    h.c1 = (float)((p.lr_dev != nullptr ? 1.0 : p.lr) / bc1);
+    h.rs2 = (float)(1.0 / sqrt(bc2));
+    h.log_b1 = (float)log(p.beta1);
+    h.log_b2 = (float)log(p.beta2);
+    h.lr_dev = p.lr_dev;
+    h.step_dev = p.step_dev;
+    h.grad_scale = p.grad_scale;
+    h.found_inf = p.found_inf;
+    for (int kind = 0; kind < 8; kind++) {
+        const csa_adamw_tensor *group[CAP_LARGE];
+        int n = 0;
+        unsigned long long chunks = 0;
+        for (int k = 0; k <= count; k++) {
+            if (k < count) {
+                const int kk = (t[k].param_dtype == CSA_BF16 ? 4 : 0) + (t[k].grad_dtype == CSA_BF16 ? 2 : 0) +
+                               (t[k].state_dtype == CSA_STATE_E4M3 ? 1 : 0);
+                if (kk != kind || t[k].numel == 0) continue;
+            }
+            const unsigned long long c = k < count ? (unsigned long long)(t[k].numel + CHUNK - 1) / CHUNK : 0;
+            if (n > 0 && (k == count || n == CAP_LARGE || chunks + c > 0x7fffffffull)) {
+                const cudaError_t e = launch_kind(kind, group, n, (unsigned)chunks, h, st);
+                if (e != cudaSuccess) return e;
+                n = 0;
+                chunks = 0;
+            }
+            if (k < count) {
+                group[n++] = t + k;
+                chunks += c;
+            }
+        }
+    }
+    return cudaSuccess;
+}
+
+}  // namespace csa
