@@ -508,11 +508,12 @@ csa_status csa_check_device_status(void *stream)
 {
     CSA_TRY(injected_fault());
     CSA_CUDA(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)));
-    int flag = 0, flag2 = 0;
+    int flag = 0, flag2 = 0, flag3 = 0;
     CSA_CUDA(tc_read_clear_error(&flag));
     CSA_CUDA(selftest_read_clear_error(&flag2));
-    if (flag == 0 && flag2 == 0) return CSA_OK;
-    t_last_timeout_site = flag != 0 ? flag : 900 + flag2;
+    CSA_CUDA(linear_tc_read_clear_error(&flag3));
+    if (flag == 0 && flag2 == 0 && flag3 == 0) return CSA_OK;
+    t_last_timeout_site = flag != 0 ? flag : flag3 != 0 ? 600 + flag3 % 100 : 900 + flag2;
     return CSA_ERR_TIMEOUT;
 }
 

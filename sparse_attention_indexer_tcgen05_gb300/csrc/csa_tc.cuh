@@ -84,6 +84,9 @@ cudaError_t launch_teacher_h128_tc(const Geo &g, const __nv_bfloat16 *q, const _
                                    const TeacherKl *kl, cudaStream_t st);
 cudaError_t teacher_h128_read_clear_error(int *flag);
 
+// The projections' products (k_linear_tc.cu).
+cudaError_t linear_tc_read_clear_error(int *flag);
+
 // One tiny kernel whose bounded wait (about 1 ms) on a barrier nothing arrives on runs out (k_selftest.cu), and
 // the read-and-clear of the word it sets.
 cudaError_t launch_bounded_wait_selftest(cudaStream_t st);

@@ -1,149 +1,360 @@
-// k_linear.cu -- projections: y = act(alpha x W^T + bias) + residual and its gradients.
-#include "csa_internal.cuh"
+// k_linear.cu -- projections: y = act(alpha x W^T + bias) + residual and its gradients.  This file holds what lies
+// around the products: operands made fit for TMA (rows on 16-byte boundaries, fp32 values as three bf16 planes),
+// dz = dy act'(z) with the bias gradient, and the join of a split k axis with the epilogue.
+#include "k_linear.cuh"
 
 namespace csa {
 namespace linear {
 
-__device__ __forceinline__ float act_fwd(float z, int act)
+using bf16 = __nv_bfloat16;
+
+// x = h + m + l with bf16 parts: 8 bits of the significand each.  What h cannot hold as a finite number stays in h.
+__device__ __forceinline__ void split3(float x, bf16 &h, bf16 &m, bf16 &l)
 {
-    if (act == CSA_ACT_RELU) return z > 0.f ? z : (z == z ? 0.f : z);
-    if (act == CSA_ACT_SILU) return z / (1.f + __expf(-z));
-    if (act == CSA_ACT_GELU_TANH) return z / (1.f + __expf(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
-    return z;
+    h = __float2bfloat16_rn(x);
+    const float r = x - __bfloat162float(h);
+    const bool fine = fabsf(r) <= 3.0e38f;  // false for NaN and infinities
+    m = __float2bfloat16_rn(fine ? r : 0.f);
+    l = __float2bfloat16_rn(fine ? r - __bfloat162float(m) : 0.f);
 }
 
-// act'(z)
-__device__ __forceinline__ float act_grad(float z, int act)
+template <typename V> struct Planes;
+template <> struct Planes<bf16> { static constexpr int N = 1; };
+template <> struct Planes<float> { static constexpr int N = 3; };
+
+template <typename V> __device__ __forceinline__ void put_planes(bf16 *out, long long plane, long long at, float x)
 {
-    if (act == CSA_ACT_RELU) return z > 0.f ? 1.f : 0.f;
-    if (act == CSA_ACT_SILU) {
-        const float s = 1.f / (1.f + __expf(-z));
-        return s * (1.f + z * (1.f - s));
+    if constexpr (sizeof(V) == 2) {
+        out[at] = __float2bfloat16_rn(x);
+    } else {
+        bf16 h, m, l;
+        split3(x, h, m, l);
+        out[at] = h;
+        out[plane + at] = m;
+        out[2 * plane + at] = l;
     }
-    if (act == CSA_ACT_GELU_TANH) {
-        const float c = 1.5957691216057308f, k = 0.044715f;
-        const float s = 1.f / (1.f + __expf(-c * (z + k * z * z * z)));
-        return s + z * s * (1.f - s) * c * (1.f + 3.f * k * z * z);
-    }
-    return 1.f;
 }
 
-constexpr int T = 64, KT = 16;
+// rows x cols values, rows `stride` apart -> planes of rows `ld` apart
+template <typename V>
+__global__ void stage_kernel(const V *x, long long stride, long long rows, int cols, bf16 *out, long long ld, long long plane)
+{
+    for (long long r = blockIdx.y; r < rows; r += gridDim.y)
+        for (int c = blockIdx.x * blockDim.x + threadIdx.x; c < cols; c += gridDim.x * blockDim.x)
+            put_planes<V>(out, plane, r * ld + c, ldf<V>(x, r * stride + c));
+}
 
-// D[m][n] = sum_k A[m sam + k sak] B[n sbn + k sbk]
-template <typename V, typename O>
+// dz = dy act'(z) for `per` rows of a block and 8 TX columns, and their column sums for db.
+template <typename V, typename O, int TX>
 __global__ void __launch_bounds__(256)
-gemm_simple(const V *A, long long sam, long long sak, const V *B, long long sbn, long long sbk, long long M, int N,
-            long long K, float alpha, const float *bias, int act, const O *res, long long ldr, O *out, V *preact)
+dz_kernel(const O *dy, long long ldy, const V *z, int act, bf16 *dz, long long ld, long long plane, float *sums,
+          long long M, int N, int per)
 {
-    __shared__ float sa[KT][T + 1], sb[KT][T + 1];
-    const long long m0 = (long long)blockIdx.x * T, n0 = (long long)blockIdx.y * T;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    for (long long k0 = 0; k0 < K; k0 += KT) {
-        for (int i = threadIdx.x; i < T * KT; i += 256) {
-            const int m = i / KT, k = i % KT;
-            sa[k][m] = m0 + m < M && k0 + k < K ? ldf<V>(A, (m0 + m) * sam + (k0 + k) * sak) : 0.f;
-            sb[k][m] = n0 + m < N && k0 + k < K ? ldf<V>(B, (n0 + m) * sbn + (k0 + k) * sbk) : 0.f;
+    constexpr int TY = 256 / TX;
+    __shared__ float part[TY][8 * TX + 1];
+    const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
+    const int n0 = blockIdx.x * 8 * TX;
+    const long long r0 = (long long)blockIdx.y * per, r1 = min(M, r0 + per);
+    float s[8] = {};
+    for (long long r = r0 + ty; r < r1; r += TY) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const int n = n0 + tx + TX * j;
+            if (n >= N) continue;
+            float d = ldf<O>(dy, r * ldy + n);
+            // rounded before it is added, whichever outputs are asked for
+            if (act != CSA_ACT_NONE) d = __fmul_rn(d, act_grad(ldf<V>(z, r * N + n), act));
+            if (dz != nullptr) put_planes<V>(dz, plane, r * ld + n, d);
+            s[j] += d;
         }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < KT; k++)
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-#pragma unroll
-                for (int j = 0; j < 4; j++) acc[i][j] += sa[k][ty + 16 * i] * sb[k][tx + 16 * j];
-        __syncthreads();
     }
-    for (int i = 0; i < 4; i++)
-        for (int j = 0; j < 4; j++) {
-            const long long m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-            if (m >= M || n >= N) continue;
-            float z = alpha * acc[i][j] + (bias != nullptr ? bias[n] : 0.f);
-            if (preact != nullptr) preact[m * N + n] = from_f<V>(z);
-            z = act_fwd(z, act);
-            if (res != nullptr) z += ldf<O>(res, m * ldr + n);
-            out[m * N + n] = from_f<O>(z);
-        }
+    if (sums == nullptr) return;
+#pragma unroll
+    for (int j = 0; j < 8; j++) part[ty][tx + TX * j] = s[j];
+    __syncthreads();
+    for (int c = threadIdx.x; c < 8 * TX; c += 256) {
+        float t = 0.f;
+        for (int k = 0; k < TY; k++) t += part[k][c];
+        if (n0 + c < N) sums[(long long)blockIdx.y * N + n0 + c] = t;
+    }
 }
 
-// dz = dy act'(z); db
-template <typename V, typename O>
-__global__ void dz_simple(const O *dy, long long ldy, const V *z, int act, V *dz, float *db, long long M, int N)
+__global__ void __launch_bounds__(256) db_kernel(const float *sums, int blocks, int N, float *db)
 {
-    const int n = blockIdx.x * blockDim.x + threadIdx.x;
-    if (n >= N) return;
-    float sum = 0.f;
-    for (long long m = 0; m < M; m++) {
-        float d = ldf<O>(dy, m * ldy + n);
-        if (act != CSA_ACT_NONE) d *= act_grad(ldf<V>(z, m * N + n), act);
-        dz[m * N + n] = from_f<V>(d);
-        sum += d;
+    __shared__ float part[8][33];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, n = blockIdx.x * 32 + tx;
+    float s = 0.f;
+    if (n < N)
+        for (int b = ty; b < blocks; b += 8) s += sums[(long long)b * N + n];
+    part[ty][tx] = s;
+    __syncthreads();
+    if (ty == 0 && n < N) {
+        float t = 0.f;
+        for (int k = 0; k < 8; k++) t += part[k][tx];
+        db[n] = t;
     }
-    if (db != nullptr) db[n] = sum;
 }
 
-template <typename V, typename O>
-cudaError_t fwd(const csa_linear_params &p, const void *x, const void *w, const float *bias, const void *res, void *y,
-                void *preact, cudaStream_t st)
+// The pieces of a split k axis joined, V columns a thread, and the epilogue.
+template <int V>
+__global__ void __launch_bounds__(256) join_kernel(const float *partial, int splits, long long M, long long N, const Epilogue e)
 {
-    const dim3 grid((unsigned)((p.rows + T - 1) / T), (p.out_features + T - 1) / T);
-    gemm_simple<V, O><<<grid, 256, 0, st>>>((const V *)x, p.x_stride, 1, (const V *)w, p.in_features, 1, p.rows,
-                                            p.out_features, p.in_features, p.alpha, bias, p.activation, (const O *)res,
-                                            p.residual_stride, (O *)y, (V *)preact);
+    const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * V;
+    if (i >= M * N) return;
+    const long long m = i / N, n = i - m * N;
+    float v[V] = {};
+    for (int s = 0; s < splits; s++) {
+        const float *p = partial + (long long)s * M * N + i;
+        if constexpr (V == 4) {
+            const float4 x = __ldcs(reinterpret_cast<const float4 *>(p));
+            v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        } else {
+            v[0] += __ldcs(p);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < V; k++) {
+        float z = e.alpha * v[k] + (e.bias != nullptr ? __ldg(e.bias + n + k) : 0.f);
+        if (e.preact != nullptr) {
+            if (e.preact_f32) ((float *)e.preact)[i + k] = z;
+            else ((bf16 *)e.preact)[i + k] = __float2bfloat16_rn(z);
+        }
+        z = act_fwd(z, e.act);
+        if (e.out_f32) {
+            if (e.res != nullptr) z += ((const float *)e.res)[m * e.ldr + n + k];
+            ((float *)e.out)[i + k] = z;
+        } else {
+            if (e.res != nullptr) z += __bfloat162float(((const bf16 *)e.res)[m * e.ldr + n + k]);
+            ((bf16 *)e.out)[i + k] = __float2bfloat16_rn(z);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+inline long long up8(long long x) { return (x + 7) & ~7LL; }
+
+// Rows that TMA cannot read where they are: fp32 values, or row strides off the 16-byte boundaries.
+inline bool staged(int dtype, long long stride) { return dtype == CSA_F32 || (stride & 7) != 0; }
+inline size_t staged_bytes(int dtype, long long rows, long long cols)
+{
+    return up256((size_t)rows * up8(cols) * 2 * (dtype == CSA_F32 ? 3 : 1));
+}
+
+constexpr int kSms = 152;  // the split of a k axis is chosen for the whole GPU, the same on every call
+
+inline int planes_of(const csa_linear_params &p) { return p.dtype == CSA_F32 ? 3 : 1; }
+
+struct Fwd {
+    bool stage_x, stage_w;
+    int splits;
+    size_t off_x, off_w, off_part, total;
+};
+Fwd plan_fwd(const csa_linear_params &p)
+{
+    Fwd f = {};
+    if (p.rows == 0) return f;
+    const long long M = p.rows, K = p.in_features, N = p.out_features;
+    f.stage_x = staged(p.dtype, p.x_stride);
+    f.stage_w = staged(p.dtype, K);
+    size_t at = 0;
+    f.off_x = at;
+    if (f.stage_x) at += staged_bytes(p.dtype, M, K);
+    f.off_w = at;
+    if (f.stage_w) at += staged_bytes(p.dtype, N, K);
+    f.splits = product_splits(M, N, K, planes_of(p), kSms);
+    f.off_part = at;
+    if (f.splits > 1) at += up256((size_t)f.splits * M * N * 4);
+    f.total = at;
+    return f;
+}
+
+// Every part that some choice of outputs needs: the workspace does not depend on which are asked for.
+struct Bwd {
+    bool stage_x, stage_w, stage_dz;
+    int splits_dx, splits_dw, per, blocks;
+    size_t off_x, off_w, off_dz, off_sums, off_part, total;
+};
+Bwd plan_bwd(const csa_linear_params &p)
+{
+    Bwd b = {};
+    const long long M = p.rows, K = p.in_features, N = p.out_features;
+    if (M == 0) return b;
+    b.stage_x = staged(p.dtype, p.x_stride);
+    b.stage_w = staged(p.dtype, K);
+    b.stage_dz = p.activation != CSA_ACT_NONE || p.dtype != p.out_dtype || staged(p.dtype, p.dy_stride);
+    // rows of a block of dz_kernel: enough blocks to fill the GPU a few times, 64 rows at least
+    const long long cols = (N + 255) / 256;
+    long long per = (M * cols + 4 * kSms - 1) / (4 * kSms);
+    if (per < 64) per = 64;
+    b.per = (int)(per < M ? per : M);
+    b.blocks = (int)((M + b.per - 1) / b.per);
+    size_t at = 0;
+    b.off_x = at;
+    if (b.stage_x) at += staged_bytes(p.dtype, M, K);
+    b.off_w = at;
+    if (b.stage_w) at += staged_bytes(p.dtype, N, K);
+    b.off_dz = at;
+    if (b.stage_dz) at += staged_bytes(p.dtype, M, N);
+    b.off_sums = at;
+    at += up256((size_t)b.blocks * N * 4);
+    b.off_part = at;
+    b.splits_dx = product_splits(M, K, N, planes_of(p), kSms);
+    b.splits_dw = product_splits(N, K, M, planes_of(p), kSms);
+    const size_t dx = b.splits_dx > 1 ? (size_t)b.splits_dx * M * K * 4 : 0;
+    const size_t dw = b.splits_dw > 1 ? (size_t)b.splits_dw * N * K * 4 : 0;
+    at += up256(dx > dw ? dx : dw);  // one product after the other
+    b.total = at;
+    return b;
+}
+
+// The operand of `rows` x `cols` values, where they are or staged.
+cudaError_t operand(Operand *o, const csa_linear_params &p, const void *x, long long stride, long long rows, int cols,
+                    bool stage, void *to, bool k_major, cudaStream_t st)
+{
+    o->k_major = k_major;
+    if (!stage) {
+        o->base = static_cast<const bf16 *>(x);
+        o->ld = stride;
+        o->plane = 0;
+        return cudaSuccess;
+    }
+    o->base = static_cast<bf16 *>(to);
+    o->ld = up8(cols);
+    o->plane = rows * o->ld;
+    const dim3 grid((cols + 255) / 256 < 64 ? (cols + 255) / 256 : 64, (unsigned)(rows < 32768 ? rows : 32768));
+    if (p.dtype == CSA_F32) stage_kernel<float><<<grid, 256, 0, st>>>((const float *)x, stride, rows, cols, (bf16 *)to, o->ld, o->plane);
+    else stage_kernel<bf16><<<grid, 256, 0, st>>>((const bf16 *)x, stride, rows, cols, (bf16 *)to, o->ld, o->plane);
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t product(const Product &p, cudaStream_t st)
+{
+    const cudaError_t e = launch_product_tc(p, kSms, st);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    const long long total = p.M * p.N;
+    const bool four = (p.N & 3) == 0;
+    const long long blocks = (total / (four ? 4 : 1) + 255) / 256;
+    if (four) join_kernel<4><<<(unsigned)blocks, 256, 0, st>>>(p.e.partial, p.splits, p.M, p.N, p.e);
+    else join_kernel<1><<<(unsigned)blocks, 256, 0, st>>>(p.e.partial, p.splits, p.M, p.N, p.e);
     note_launches(1);
     return cudaGetLastError();
 }
 
 template <typename V, typename O>
-cudaError_t bwd(const csa_linear_params &p, const void *dy, const void *x, const void *w, const void *z, void *dx,
-                void *dw, float *db, void *ws, cudaStream_t st)
+cudaError_t run_dz(const csa_linear_params &p, const Bwd &b, const void *dy, const void *z, bf16 *dz, float *sums,
+                   cudaStream_t st)
 {
-    V *dz = (V *)ws;
-    const int N = p.out_features, K = p.in_features;
-    dz_simple<V, O><<<(N + 127) / 128, 128, 0, st>>>((const O *)dy, p.dy_stride, (const V *)z, p.activation, dz, db, p.rows, N);
+    const int N = p.out_features;
+    const long long ld = up8(N);
+    if (N <= 64)
+        dz_kernel<V, O, 8><<<dim3((N + 63) / 64, b.blocks), 256, 0, st>>>((const O *)dy, p.dy_stride, (const V *)z, p.activation,
+                                                                          dz, ld, p.rows * ld, sums, p.rows, N, b.per);
+    else
+        dz_kernel<V, O, 32><<<dim3((N + 255) / 256, b.blocks), 256, 0, st>>>((const O *)dy, p.dy_stride, (const V *)z, p.activation,
+                                                                             dz, ld, p.rows * ld, sums, p.rows, N, b.per);
     note_launches(1);
-    if (dx != nullptr && p.rows > 0) {
-        const dim3 grid((unsigned)((p.rows + T - 1) / T), (K + T - 1) / T);
-        gemm_simple<V, V><<<grid, 256, 0, st>>>(dz, N, 1, (const V *)w, 1, K, p.rows, K, N, p.alpha, nullptr, 0,
-                                                (const V *)nullptr, 0, (V *)dx, (V *)nullptr);
-        note_launches(1);
-    }
-    if (dw != nullptr) {
-        const dim3 grid((N + T - 1) / T, (K + T - 1) / T);
-        gemm_simple<V, V><<<grid, 256, 0, st>>>(dz, 1, N, (const V *)x, 1, p.x_stride, N, K, p.rows, p.alpha, nullptr, 0,
-                                                (const V *)nullptr, 0, (V *)dw, (V *)nullptr);
-        note_launches(1);
-    }
     return cudaGetLastError();
 }
 
 }  // namespace linear
 
-size_t linear_fwd_workspace(const csa_linear_params &) { return 0; }
-size_t linear_bwd_workspace(const csa_linear_params &p)
-{
-    return (size_t)p.rows * p.out_features * (p.dtype == CSA_BF16 ? 2 : 4);
-}
+using namespace linear;
+
+size_t linear_fwd_workspace(const csa_linear_params &p) { return plan_fwd(p).total; }
+size_t linear_bwd_workspace(const csa_linear_params &p) { return plan_bwd(p).total; }
+
+#define LIN_TRY(x)                            \
+    do {                                      \
+        const cudaError_t e_ = (x);           \
+        if (e_ != cudaSuccess) return e_;     \
+    } while (0)
 
 cudaError_t launch_linear_fwd(const csa_linear_params &p, const void *x, const void *weight, const float *bias,
-                              const void *residual, void *y, void *preact, void *, cudaStream_t st)
+                              const void *residual, void *y, void *preact, void *ws, cudaStream_t st)
 {
-    using bf = __nv_bfloat16;
-    note_path("generic");
-    if (p.dtype == CSA_F32) return linear::fwd<float, float>(p, x, weight, bias, residual, y, preact, st);
-    if (p.out_dtype == CSA_F32) return linear::fwd<bf, float>(p, x, weight, bias, residual, y, preact, st);
-    return linear::fwd<bf, bf>(p, x, weight, bias, residual, y, preact, st);
+    note_path("tcgen05");
+    const Fwd f = plan_fwd(p);
+    char *w = static_cast<char *>(ws);
+    Product q = {};
+    LIN_TRY(operand(&q.a, p, x, p.x_stride, p.rows, p.in_features, f.stage_x, w + f.off_x, true, st));
+    LIN_TRY(operand(&q.b, p, weight, p.in_features, p.out_features, p.in_features, f.stage_w, w + f.off_w, true, st));
+    q.M = p.rows;
+    q.N = p.out_features;
+    q.K = p.in_features;
+    q.planes = planes_of(p);
+    q.splits = f.splits;
+    q.e.alpha = p.alpha;
+    q.e.act = p.activation;
+    q.e.bias = bias;
+    q.e.res = residual;
+    q.e.ldr = p.residual_stride;
+    q.e.out = y;
+    q.e.preact = preact;
+    q.e.out_f32 = p.out_dtype == CSA_F32;
+    q.e.preact_f32 = p.dtype == CSA_F32;
+    q.e.partial = reinterpret_cast<float *>(w + f.off_part);
+    return product(q, st);
 }
 
 cudaError_t launch_linear_bwd(const csa_linear_params &p, const void *dy, const void *x, const void *weight,
                               const void *preact, void *dx, void *dw, float *db, void *ws, cudaStream_t st)
 {
-    using bf = __nv_bfloat16;
-    note_path("generic");
-    if (p.dtype == CSA_F32) return linear::bwd<float, float>(p, dy, x, weight, preact, dx, dw, db, ws, st);
-    if (p.out_dtype == CSA_F32) return linear::bwd<bf, float>(p, dy, x, weight, preact, dx, dw, db, ws, st);
-    return linear::bwd<bf, bf>(p, dy, x, weight, preact, dx, dw, db, ws, st);
+    note_path("tcgen05");
+    const long long M = p.rows, K = p.in_features, N = p.out_features;
+    if (M == 0) {  // sums of nothing
+        if (dw != nullptr) LIN_TRY(cudaMemsetAsync(dw, 0, (size_t)N * K * (p.dtype == CSA_F32 ? 4 : 2), st));
+        if (db != nullptr) LIN_TRY(cudaMemsetAsync(db, 0, (size_t)N * 4, st));
+        return cudaSuccess;
+    }
+    const Bwd b = plan_bwd(p);
+    char *w = static_cast<char *>(ws);
+    bf16 *dz = b.stage_dz && (dx != nullptr || dw != nullptr) ? reinterpret_cast<bf16 *>(w + b.off_dz) : nullptr;
+    float *sums = db != nullptr ? reinterpret_cast<float *>(w + b.off_sums) : nullptr;
+    if (dz != nullptr || sums != nullptr) {
+        if (p.dtype == CSA_F32) LIN_TRY((run_dz<float, float>(p, b, dy, preact, dz, sums, st)));
+        else if (p.out_dtype == CSA_F32) LIN_TRY((run_dz<bf16, float>(p, b, dy, preact, dz, sums, st)));
+        else LIN_TRY((run_dz<bf16, bf16>(p, b, dy, preact, dz, sums, st)));
+    }
+    if (db != nullptr) {
+        db_kernel<<<(p.out_features + 31) / 32, 256, 0, st>>>(sums, b.blocks, p.out_features, db);
+        note_launches(1);
+        LIN_TRY(cudaGetLastError());
+    }
+    Operand d = {};
+    d.base = dz != nullptr ? dz : static_cast<const bf16 *>(dy);
+    d.ld = dz != nullptr ? up8(N) : p.dy_stride;
+    d.plane = dz != nullptr ? M * up8(N) : 0;
+    Product q = {};
+    q.planes = planes_of(p);
+    q.e.alpha = p.alpha;
+    q.e.out_f32 = p.dtype == CSA_F32;
+    q.e.partial = reinterpret_cast<float *>(w + b.off_part);
+    if (dx != nullptr) {
+        q.a = d;
+        q.a.k_major = true;
+        LIN_TRY(operand(&q.b, p, weight, K, N, (int)K, b.stage_w, w + b.off_w, false, st));
+        q.M = M;
+        q.N = K;
+        q.K = N;
+        q.splits = b.splits_dx;
+        q.e.out = dx;
+        LIN_TRY(product(q, st));
+    }
+    if (dw != nullptr) {
+        q.a = d;
+        q.a.k_major = false;
+        LIN_TRY(operand(&q.b, p, x, p.x_stride, M, (int)K, b.stage_x, w + b.off_x, false, st));
+        q.M = N;
+        q.N = K;
+        q.K = M;
+        q.splits = b.splits_dw;
+        q.e.out = dw;
+        LIN_TRY(product(q, st));
+    }
+    return cudaSuccess;
 }
 
 }  // namespace csa

@@ -1,0 +1,86 @@
+// k_linear.cuh -- what the projections' kernels share: the activations, the epilogue's arguments and the product.
+#pragma once
+
+#include "csa_internal.cuh"
+
+namespace csa {
+namespace linear {
+
+// s(u) = 1 / (1 + exp(-u)) with the hardware's base-2 exponential and reciprocal (2 units in the last place each)
+__device__ __forceinline__ float sigmoid(float u)
+{
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * u));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
+
+constexpr float kGelu = 1.5957691216057308f, kCubic = 0.044715f;  // 2 sqrt(2 / pi)
+
+template <int ACT> __device__ __forceinline__ float act_fwd(float z)
+{
+    if constexpr (ACT == CSA_ACT_RELU) return z < 0.f ? 0.f : z;  // keeps NaN
+    if constexpr (ACT == CSA_ACT_SILU) return z * sigmoid(z);
+    if constexpr (ACT == CSA_ACT_GELU_TANH) return z * sigmoid(kGelu * (z + kCubic * z * z * z));
+    return z;
+}
+__device__ __forceinline__ float act_fwd(float z, int act)
+{
+    if (act == CSA_ACT_RELU) return act_fwd<CSA_ACT_RELU>(z);
+    if (act == CSA_ACT_SILU) return act_fwd<CSA_ACT_SILU>(z);
+    if (act == CSA_ACT_GELU_TANH) return act_fwd<CSA_ACT_GELU_TANH>(z);
+    return z;
+}
+
+__device__ __forceinline__ float act_grad(float z, int act)
+{
+    if (act == CSA_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+    if (act == CSA_ACT_SILU) {
+        const float s = sigmoid(z);
+        return s * (1.f + z * (1.f - s));
+    }
+    if (act == CSA_ACT_GELU_TANH) {
+        const float s = sigmoid(kGelu * (z + kCubic * z * z * z));
+        const float q = s * (1.f - s);  // 0 far out, where z^2 may overflow
+        return q > 0.f ? s + z * q * kGelu * (1.f + 3.f * kCubic * z * z) : s;
+    }
+    return 1.f;
+}
+
+// Where a product's sums go.  y = act(alpha sum + bias[n]) + res; with `partial` the bare sums of split s go to
+// partial[s][M][N] instead.
+struct Epilogue {
+    float alpha;
+    int act;
+    const float *bias;
+    const void *res;
+    long long ldr;
+    void *out;           // [M][N]
+    void *preact;        // [M][N] bf16 or fp32 as `preact_f32` says, or null
+    int out_f32, preact_f32;
+    float *partial;
+};
+
+// One operand of a product over k: element (i, k) of plane q at base + q * plane + (k_major ? i ld + k : k ld + i).
+// fp32 values are held as three bf16 planes, x = h + m + l.
+struct Operand {
+    const __nv_bfloat16 *base;
+    long long ld, plane;   // elements; multiples of 8
+    bool k_major;
+};
+
+// D[m][n] = sum_k A(m, k) B(n, k), M x N x K, with `planes` = 1 or 3 and the k axis cut into `splits` pieces.
+struct Product {
+    Operand a, b;
+    long long M, N, K;
+    int planes, splits;
+    Epilogue e;
+};
+
+// How many pieces of the k axis the tensor-core kernel wants for this product (1: none; the caller provides
+// splits * M * N floats in e.partial and reduces them).
+int product_splits(long long M, long long N, long long K, int planes, int sms);
+cudaError_t launch_product_tc(const Product &p, int sms, cudaStream_t st);
+
+}  // namespace linear
+}  // namespace csa

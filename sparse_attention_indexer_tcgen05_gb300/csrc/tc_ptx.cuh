@@ -341,6 +341,79 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// ---------------------------------------------------------------- CTA pairs (clusters of two)
+// One tcgen05.mma of a pair reads each CTA's half of A (M / 2 rows) and of B (N / 2 rows) at the same shared-memory
+// offsets and leaves M / 2 rows of D in each CTA's TMEM; only the even CTA (the leader) issues it.
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// shared::cluster address of this CTA's shared-memory object in the CTA of rank r
+__device__ __forceinline__ uint32_t map_rank(const void *p, uint32_t r)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(su32(p)), "r"(r));
+    return a;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// Load into this CTA's shared memory, completion counted on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *map, uint32_t bar_cluster, int x, int y,
+                                                 int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+                 "[%1, {%3, %4, %5}], [%2];"
+                 ::"r"(su32(dst)), "l"(map), "r"(bar_cluster), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+// Four MMAs of K = 16 of a pair (as mma4_ss_w), then a commit that arrives on the barrier at the offset of `bar` in
+// both CTAs (bar == 0: none).
+__device__ __forceinline__ void mma4_ss_pair_w(uint32_t d, uint64_t a, uint64_t da, uint64_t b, uint64_t db,
+                                               uint32_t idesc, uint32_t acc0, uint32_t bar)
+{
+    asm volatile("{\n\t.reg .pred e, p, t, c, ec;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t.reg .b16 m;\n\t"
+                 "elect.sync _|e, 0xffffffff;\n\t"
+                 "setp.ne.b32 p, %6, 0;\n\t"
+                 "setp.ne.b32 t, %5, 0;\n\t"
+                 "setp.ne.b32 c, %7, 0;\n\t"
+                 "and.pred ec, e, c;\n\t"
+                 "mov.b16 m, 3;\n\t"
+                 "add.s64 a1, %1, %2;\n\tadd.s64 a2, a1, %2;\n\tadd.s64 a3, a2, %2;\n\t"
+                 "add.s64 b1, %3, %4;\n\tadd.s64 b2, b1, %4;\n\tadd.s64 b3, b2, %4;\n\t"
+                 "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %3, %5, p;\n\t"
+                 "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %5, t;\n\t"
+                 "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %5, t;\n\t"
+                 "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %5, t;\n\t"
+                 "@ec tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%7], m;\n\t}"
+                 ::"r"(d), "l"(a), "l"(da), "l"(b), "l"(db), "r"(idesc), "r"(acc0), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_commit_pair_w(uint64_t *bar)
+{
+    asm volatile("{\n\t.reg .pred e;\n\t.reg .b16 m;\n\telect.sync _|e, 0xffffffff;\n\tmov.b16 m, 3;\n\t"
+                 "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}"
+                 ::"r"(su32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t *slot, uint32_t cols)
+{
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(slot)), "r"(cols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t cols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols));
+}
+
 // 16-byte asynchronous global -> shared copy (L2 only), its commit group and the wait for all but the n most
 // recent groups; the proxy fence that makes completed generic-proxy writes of shared memory visible to the
 // tensor core's async proxy.
