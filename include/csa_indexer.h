@@ -282,7 +282,7 @@ csa_status csa_linear_bwd(const csa_linear_params *p, const void *dy, const void
 #define CSA_ROPE_MAX_AXES 4
 typedef struct {
     int32_t dtype;                        /* csa_dtype of x and out */
-    int32_t heads, head_dim;              /* >= 1 */
+    int32_t heads, head_dim;              /* >= 1; head_dim at most 2^18 */
     int32_t rot_offset, rot_dim;          /* rot_dim even, >= 0, at most 1024; rot_offset + rot_dim <= head_dim */
     int32_t interleaved;                  /* 0 or 1: how the pairs lie */
     int32_t inverse;                      /* 0 or 1.  1 turns by minus the angle: the gradient of the forward */

@@ -460,18 +460,40 @@ def csa_indexer_loss(q_idx, w, k_idx, q, kv, kv_c, sink, params: Params):
 
 # ------------------------------------------------------------------ around the step
 
-@contextlib.contextmanager
-def _call(name, device):
-    """The NVTX range of a call, with the tensors' device as the current one (launches go to the current device)."""
-    torch.cuda.nvtx.range_push(name)
+# These calls are short enough that the host side shows: one expression checks a tensor, the error is found afterwards.
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_push, _pop = torch.cuda.nvtx.range_push, torch.cuda.nvtx.range_pop
+_current_device = torch.cuda.current_device
+
+
+def _invoke(name, fn, device_index, *args):
+    """fn(*args, stream) with the tensors' device as the current one (launches go there), inside an NVTX range."""
+    _push(name)
     try:
-        if torch.cuda.current_device() == device.index:
-            yield
+        if _current_device() == device_index:
+            st = fn(*args, _raw_stream(device_index))
         else:
-            with torch.cuda.device(device):
-                yield
+            with torch.cuda.device(device_index):
+                st = fn(*args, _raw_stream(device_index))
     finally:
-        torch.cuda.nvtx.range_pop()
+        _pop()
+    if st != 0:
+        raise CSAError(st, name)
+
+
+def _on_cuda(t, name):
+    """The index of t's device."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _check_flat(t, name, dtype, index, numel):
+    """A contiguous tensor of `numel` values on device `index`."""
+    if t is not None and t.dtype is dtype and t.get_device() == index and t.numel() == numel and t.is_contiguous():
+        return
+    _check_tensor(t, name, dtype, torch.device("cuda", index), numel)
 
 
 def _dtype(d):
@@ -482,8 +504,13 @@ def _dtype(d):
     return DTYPES[d]
 
 
-def _check_rows(t, name, dtype, device, rows, cols, stride):
-    """A [rows, cols] tensor whose rows lie `stride` elements apart (leading dimensions may be folded into rows)."""
+def _check_rows(t, name, dtype, index, rows, cols, stride):
+    """A [rows, cols] tensor whose rows lie `stride` elements apart (0: cols; leading dimensions may be folded into
+    rows)."""
+    if (t is not None and t.dtype is dtype and t.get_device() == index and t.shape == (rows, cols) and
+            t.is_contiguous() and (not stride or stride == cols)):
+        return
+    device = torch.device("cuda", index)
     if t is None:
         raise ValueError(f"{name} is required")
     if not t.is_cuda or t.device != device:
@@ -496,7 +523,7 @@ def _check_rows(t, name, dtype, device, rows, cols, stride):
         return
     if cols > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    expect = stride
+    expect = stride or cols
     for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
         if n > 1 and st != expect:
             raise ValueError(f"{name} has row stride {st}, expected {expect}")
@@ -519,6 +546,7 @@ class LinearParams:
                                    int(in_features), int(out_features), float(alpha), int(rows), int(x_stride),
                                    int(residual_stride), int(dy_stride))
         self.ref = ctypes.byref(self.c)
+        self.value_dtype, self.out_value_dtype = TORCH_DTYPE[self.c.dtype], TORCH_DTYPE[self.c.out_dtype]
 
     @property
     def fwd_workspace_bytes(self) -> int:
@@ -533,46 +561,36 @@ class LinearParams:
         """Enough for either direction."""
         return max(self.fwd_workspace_bytes, self.bwd_workspace_bytes)
 
-    @property
-    def value_dtype(self) -> torch.dtype:
-        return TORCH_DTYPE[self.c.dtype]
 
-    @property
-    def out_value_dtype(self) -> torch.dtype:
-        return TORCH_DTYPE[self.c.out_dtype]
-
-
-def _given_workspace(need, device, workspace):
-    if workspace is None:
-        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
-    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return workspace
+def _check_workspace(workspace, index):
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def csa_linear_fwd(p: LinearParams, x, weight, bias=None, residual=None, workspace=None, out=None, preact=None):
     """y = act(alpha x weight^T + bias) + residual, in one pass with fp32 sums.  Returns y [rows, out_features].
     preact (a [rows, out_features] tensor of p's dtype) receives the activation's argument, which csa_linear_bwd reads.
     out may be the residual itself (contiguous)."""
-    c, dev = p.c, x.device
+    c, dev = p.c, _on_cuda(x, "x")
     M, K, N = c.rows, c.in_features, c.out_features
-    _check_rows(x, "x", p.value_dtype, dev, M, K, c.x_stride or K)
-    _check_tensor(weight, "weight", p.value_dtype, dev, N * K)
+    _check_rows(x, "x", p.value_dtype, dev, M, K, c.x_stride)
+    _check_flat(weight, "weight", p.value_dtype, dev, N * K)
     if bias is not None:
-        _check_tensor(bias, "bias", torch.float32, dev, N)
+        _check_flat(bias, "bias", torch.float32, dev, N)
     if residual is not None:
-        _check_rows(residual, "residual", p.out_value_dtype, dev, M, N, c.residual_stride or N)
+        _check_rows(residual, "residual", p.out_value_dtype, dev, M, N, c.residual_stride)
     if out is None:
-        out = torch.empty((M, N), dtype=p.out_value_dtype, device=dev)
+        out = x.new_empty((M, N), dtype=p.out_value_dtype)
     else:
-        _check_tensor(out, "out", p.out_value_dtype, dev, M * N)
+        _check_flat(out, "out", p.out_value_dtype, dev, M * N)
     if preact is not None:
-        _check_tensor(preact, "preact", p.value_dtype, dev, M * N)
-    with _call("csa_linear_fwd", dev):
-        ws = _given_workspace(p.fwd_workspace_bytes, dev, workspace)
-        st = _lib.csa_linear_fwd(p.ref, _ptr(x), _ptr(weight), _ptr(bias), _ptr(residual), _ptr(out), _ptr(preact),
-                                 _ptr(ws), ws.numel() * ws.element_size(), _stream(dev))
-    _check(st, "csa_linear_fwd")
+        _check_flat(preact, "preact", p.value_dtype, dev, M * N)
+    if workspace is None:
+        workspace = x.new_empty(p.fwd_workspace_bytes, dtype=torch.uint8)
+    ws, nws = _check_workspace(workspace, dev)
+    _invoke("csa_linear_fwd", _lib.csa_linear_fwd, dev, p.ref, x.data_ptr(), weight.data_ptr(), _ptr(bias),
+            _ptr(residual), out.data_ptr(), _ptr(preact), ws, nws)
     return out
 
 
@@ -581,33 +599,32 @@ def csa_linear_bwd(p: LinearParams, dy, x, weight, preact=None, need_dx=True, ne
     """The gradients of csa_linear_fwd for dy: (dx [rows, in_features], dw like weight, db [out_features] fp32), None
     in the place of one that is not asked for.  preact is what the forward wrote there (not read without an
     activation).  out: a tuple of the three to write to."""
-    c, dev = p.c, dy.device
+    c, dev = p.c, _on_cuda(dy, "dy")
     M, K, N = c.rows, c.in_features, c.out_features
-    _check_rows(dy, "dy", p.out_value_dtype, dev, M, N, c.dy_stride or N)
+    _check_rows(dy, "dy", p.out_value_dtype, dev, M, N, c.dy_stride)
     if need_dw:
-        _check_rows(x, "x", p.value_dtype, dev, M, K, c.x_stride or K)
+        _check_rows(x, "x", p.value_dtype, dev, M, K, c.x_stride)
     if need_dx:
-        _check_tensor(weight, "weight", p.value_dtype, dev, N * K)
+        _check_flat(weight, "weight", p.value_dtype, dev, N * K)
     if c.activation != 0:
-        _check_tensor(preact, "preact", p.value_dtype, dev, M * N)
+        _check_flat(preact, "preact", p.value_dtype, dev, M * N)
     else:
         preact = None
-    want = (("dx", need_dx, (M, K), p.value_dtype), ("dw", need_dw, (N, K), p.value_dtype),
-            ("db", need_db, (N,), torch.float32))
-    got = []
-    for i, (name, need, shape, dtype) in enumerate(want):
-        t = out[i] if out is not None and need else None
-        if need and t is None:
-            t = torch.empty(shape, dtype=dtype, device=dev)
-        elif need:
-            _check_tensor(t, name, dtype, dev, shape[0] * shape[1] if len(shape) > 1 else shape[0])
-        got.append(t)
-    dx, dw, db = got
-    with _call("csa_linear_bwd", dev):
-        ws = _given_workspace(p.bwd_workspace_bytes, dev, workspace)
-        st = _lib.csa_linear_bwd(p.ref, _ptr(dy), _ptr(x), _ptr(weight), _ptr(preact), _ptr(dx), _ptr(dw), _ptr(db),
-                                 _ptr(ws), ws.numel() * ws.element_size(), _stream(dev))
-    _check(st, "csa_linear_bwd")
+
+    def output(i, name, shape, dtype, numel):
+        if out is None or out[i] is None:
+            return dy.new_empty(shape, dtype=dtype)
+        _check_flat(out[i], name, dtype, dev, numel)
+        return out[i]
+
+    dx = output(0, "dx", (M, K), p.value_dtype, M * K) if need_dx else None
+    dw = output(1, "dw", (N, K), p.value_dtype, N * K) if need_dw else None
+    db = output(2, "db", (N,), torch.float32, N) if need_db else None
+    if workspace is None:
+        workspace = dy.new_empty(p.bwd_workspace_bytes, dtype=torch.uint8)
+    ws, nws = _check_workspace(workspace, dev)
+    _invoke("csa_linear_bwd", _lib.csa_linear_bwd, dev, p.ref, dy.data_ptr(), _ptr(x), _ptr(weight), _ptr(preact),
+            _ptr(dx), _ptr(dw), _ptr(db), ws, nws)
     return dx, dw, db
 
 
@@ -628,6 +645,7 @@ class RopeParams:
                                  (ctypes.c_int32 * ROPE_MAX_AXES)(*sections), int(rows), int(x_row_stride),
                                  int(x_head_stride), int(out_row_stride), int(out_head_stride))
         self.ref = ctypes.byref(self.c)
+        self.value_dtype = TORCH_DTYPE[self.c.dtype]
 
     def inverted(self) -> "RopeParams":
         """The same rotation backwards, on contiguous values: what a gradient of out takes."""
@@ -635,15 +653,14 @@ class RopeParams:
         return RopeParams(c.rows, c.heads, c.head_dim, c.dtype, c.rot_dim, c.rot_offset, list(c.sections[:c.axes]),
                           c.interleaved, not c.inverse, c.positions_64)
 
-    @property
-    def value_dtype(self) -> torch.dtype:
-        return TORCH_DTYPE[self.c.dtype]
 
-
-def _check_heads(t, name, p, device, row_stride, head_stride):
+def _check_heads(t, name, p, index, row_stride, head_stride):
     c = p.c
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be on {device}")
+    if (not row_stride and not head_stride and t.dtype is p.value_dtype and t.get_device() == index and
+            t.is_contiguous() and t.numel() == c.rows * c.heads * c.head_dim):
+        return
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}")
     if t.dtype != p.value_dtype:
         raise ValueError(f"{name} must be {p.value_dtype}, got {t.dtype}")
     head_stride = head_stride or c.head_dim
@@ -664,19 +681,17 @@ def _check_heads(t, name, p, device, row_stride, head_stride):
 def csa_rope(p: RopeParams, x, positions, inv_freq, out=None):
     """x [rows, heads, head_dim] with its pairs turned by positions [axes, rows] (int32, or int64 with positions_64)
     times inv_freq [rot_dim / 2] (fp64).  Returns out; out=x works in place."""
-    c, dev = p.c, x.device
+    c, dev = p.c, _on_cuda(x, "x")
     _check_heads(x, "x", p, dev, c.x_row_stride, c.x_head_stride)
-    _check_tensor(positions, "positions", torch.int64 if c.positions_64 else torch.int32, dev, c.axes * c.rows)
-    _check_tensor(inv_freq, "inv_freq", torch.float64, dev, c.rot_dim // 2)
+    _check_flat(positions, "positions", torch.int64 if c.positions_64 else torch.int32, dev, c.axes * c.rows)
+    _check_flat(inv_freq, "inv_freq", torch.float64, dev, c.rot_dim // 2)
     if out is None:
         if c.out_row_stride or c.out_head_stride:
             raise ValueError("out is required where RopeParams gives its strides")
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = x.new_empty(x.shape)
     else:
         _check_heads(out, "out", p, dev, c.out_row_stride, c.out_head_stride)
-    with _call("csa_rope", dev):
-        st = _lib.csa_rope(p.ref, _ptr(x), _ptr(positions), _ptr(inv_freq), _ptr(out), _stream(dev))
-    _check(st, "csa_rope")
+    _invoke("csa_rope", _lib.csa_rope, dev, p.ref, x.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), out.data_ptr())
     return out
 
 
@@ -754,20 +769,26 @@ def csa_adamw(tensors: AdamWTensors, step, lr=1e-3, beta1=0.9, beta2=0.999, eps=
     gradient; found_inf (f32 device scalar), when not 0, leaves everything as it is."""
     p = csa_adamw_params(0.0, float(beta1), float(beta2), float(eps), float(weight_decay), 1, None, None, None, None)
     dev = tensors.device
-    for name, t, dtype in (("lr", lr, torch.float32), ("step", step, torch.int64), ("grad_scale", grad_scale, torch.float32),
-                           ("found_inf", found_inf, torch.float32)):
-        if isinstance(t, torch.Tensor):
-            _check_tensor(t, name, dtype, dev, 1)
-            setattr(p, name if name in ("grad_scale", "found_inf") else name + "_dev", t.data_ptr())
-        elif name in ("lr", "step"):
-            setattr(p, name, t)
-        elif t is not None:
-            raise ValueError(f"{name} must be a device scalar")
     if dev is None:
         return
-    with _call("csa_adamw", dev):
-        st = _lib.csa_adamw(ctypes.byref(p), tensors.table, tensors.count, _stream(dev))
-    _check(st, "csa_adamw")
+    index = dev.index
+    if isinstance(lr, torch.Tensor):
+        _check_flat(lr, "lr", torch.float32, index, 1)
+        p.lr_dev = lr.data_ptr()
+    else:
+        p.lr = lr
+    if isinstance(step, torch.Tensor):
+        _check_flat(step, "step", torch.int64, index, 1)
+        p.step_dev = step.data_ptr()
+    else:
+        p.step = step
+    if grad_scale is not None:
+        _check_flat(grad_scale, "grad_scale", torch.float32, index, 1)
+        p.grad_scale = grad_scale.data_ptr()
+    if found_inf is not None:
+        _check_flat(found_inf, "found_inf", torch.float32, index, 1)
+        p.found_inf = found_inf.data_ptr()
+    _invoke("csa_adamw", _lib.csa_adamw, index, ctypes.byref(p), tensors.table, tensors.count)
 
 
 class CSALinear(torch.autograd.Function):

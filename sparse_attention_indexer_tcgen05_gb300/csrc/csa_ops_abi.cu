@@ -92,7 +92,7 @@ csa_status check_rope(const csa_rope_params *p, csa_rope_params *q)
     const bool rows_outer = q->out_row_stride - p->head_dim >= (p->heads - 1) * q->out_head_stride;
     const bool heads_outer = p->rows <= 1 || (q->out_head_stride - p->head_dim) / q->out_row_stride >= p->rows - 1;
     if (!rows_outer && !heads_outer) return CSA_ERR_INVALID_ARG;
-    if (p->rot_dim > 1024 || (p->rows > 0 && (q->x_row_stride > (1LL << 60) / p->rows || q->out_row_stride > (1LL << 60) / p->rows)))
+    if (p->rot_dim > 1024 || p->head_dim > (1 << 18) || (p->rows > 0 && (q->x_row_stride > (1LL << 60) / p->rows || q->out_row_stride > (1LL << 60) / p->rows)))
         return CSA_ERR_UNSUPPORTED;
     return CSA_OK;
 }

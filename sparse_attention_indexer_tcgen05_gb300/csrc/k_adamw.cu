@@ -142,6 +142,14 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[VEC])
     return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
+// The hardware's root (1 unit in the last place); subnormal arguments keep theirs.
+__device__ __forceinline__ float root(float v)
+{
+    float r;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 template <typename PT, typename GT, bool E4M3, int CAP>
 __global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ Table<CAP> tab, const Hyper h)
 {
@@ -198,8 +206,8 @@ __global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ 
             const float gk = g[k] * gs;
             m[k] = h.b1 * m[k] + h.nb1 * gk;
             v[k] = h.b2 * v[k] + h.nb2 * gk * gk;
-            r[k] = sqrtf(v[k]);
-            p[k] = p[k] - lr_wd * p[k] - c1 * m[k] / (r[k] * rs2 + h.eps);
+            r[k] = root(v[k]);
+            p[k] = fmaf(-lr_wd, p[k], p[k]) - c1 * __fdividef(m[k], fmaf(r[k], rs2, h.eps));
             top_m = fmaxf(top_m, fabsf(m[k]));
             top_r = fmaxf(top_r, r[k]);
         }
@@ -209,11 +217,11 @@ __global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ 
             top_m = warp_max(top_m);
             top_r = warp_max(top_r);
             const float sm = top_m / E4M3_MAX, sr = top_r / E4M3_MAX;
-            const float dm = sm > 0.f ? sm : 1.f, dr = sr > 0.f ? sr : 1.f;
+            const float im = sm > 0.f ? 1.f / sm : 0.f, ir = sr > 0.f ? 1.f / sr : 0.f;
 #pragma unroll
             for (int k = 0; k < VEC; k++) {
-                m[k] = m[k] / dm;
-                const float c = r[k] / dr;
+                m[k] *= im;
+                const float c = r[k] * ir;
                 v[k] = r[k] > 0.f && !(c > E4M3_TINY) ? E4M3_TINY : c;
             }
             store_codes(e.m, i, n, encode8(m));
@@ -229,8 +237,9 @@ __global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ 
     }
 }
 
-// The tensors of one launch: parameters of a kernel hold up to 32764 bytes; few tensors take the short table.
-constexpr int CAP_SMALL = 52, CAP_LARGE = 440;
+// The tensors of one launch: parameters of a kernel hold up to 32764 bytes; fewer tensors take a shorter
+// table, whose upload is part of every launch.
+constexpr int CAP_SMALL = 48, CAP_MIDDLE = 128, CAP_LARGE = 440;
 
 template <int CAP> void fill(Table<CAP> &tab, const csa_adamw_tensor *const *t, int n)
 {
@@ -258,6 +267,10 @@ cudaError_t launch_group(const csa_adamw_tensor *const *t, int n, unsigned chunk
         Table<CAP_SMALL> tab;
         fill(tab, t, n);
         adamw_kernel<PT, GT, Q, CAP_SMALL><<<chunks, THREADS, 0, st>>>(tab, h);
+    } else if (n <= CAP_MIDDLE) {
+        Table<CAP_MIDDLE> tab;
+        fill(tab, t, n);
+        adamw_kernel<PT, GT, Q, CAP_MIDDLE><<<chunks, THREADS, 0, st>>>(tab, h);
     } else {
         Table<CAP_LARGE> tab;
         fill(tab, t, n);

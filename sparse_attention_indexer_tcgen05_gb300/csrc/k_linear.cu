@@ -44,36 +44,96 @@ __global__ void stage_kernel(const V *x, long long stride, long long rows, int c
             put_planes<V>(out, plane, r * ld + c, ldf<V>(x, r * stride + c));
 }
 
-// dz = dy act'(z) for `per` rows of a block and 8 TX columns, and their column sums for db.
-template <typename V, typename O, int TX>
-__global__ void __launch_bounds__(256)
+// 8 columns of one row: V neighbours from n on where V = 8, else every TX-th from n on; 0 behind the end.
+template <typename T, int V, int TX> __device__ __forceinline__ void load_cols(const T *row, int n, int N, float (&x)[8])
+{
+    if constexpr (V == 8) {
+        if constexpr (sizeof(T) == 2) {
+            const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(row + n));
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                x[2 * k] = __uint_as_float(w[k] << 16);
+                x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+            }
+        } else {
+            const float4 a = __ldcs(reinterpret_cast<const float4 *>(row + n)), b = __ldcs(reinterpret_cast<const float4 *>(row + n) + 1);
+            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+            x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++) x[j] = n + TX * j < N ? ldf<T>(row, n + TX * j) : 0.f;
+    }
+}
+
+template <typename V> __device__ __forceinline__ void put_planes8(bf16 *out, long long plane, long long at, const float (&x)[8])
+{
+    constexpr int P = Planes<V>::N;
+    __nv_bfloat162 w[P][4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        if constexpr (P == 1) {
+            w[0][k] = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+        } else {
+            split3(x[2 * k], w[0][k].x, w[1][k].x, w[2][k].x);
+            split3(x[2 * k + 1], w[0][k].y, w[1][k].y, w[2][k].y);
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < P; q++) *reinterpret_cast<uint4 *>(out + q * plane + at) = *reinterpret_cast<const uint4 *>(w[q]);
+}
+
+// dz = dy act'(z) for `per` rows of a block and 8 TX columns, and their column sums for db.  Bound by memory: dy and
+// z are read once, dz is written once; two rows of a thread (bf16) are in flight together.  VEC: 8 neighbouring columns a
+// thread (16-byte accesses), where the row strides allow it.
+template <typename V, typename O, int TX, bool VEC>
+__global__ void __launch_bounds__(256, 3)
 dz_kernel(const O *dy, long long ldy, const V *z, int act, bf16 *dz, long long ld, long long plane, float *sums,
           long long M, int N, int per)
 {
-    constexpr int TY = 256 / TX;
+    constexpr int TY = 256 / TX, ROWS = sizeof(V) == 2 ? 2 : 1, W = VEC ? 8 : 1;
     __shared__ float part[TY][8 * TX + 1];
     const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
-    const int n0 = blockIdx.x * 8 * TX;
+    const int n0 = blockIdx.x * 8 * TX, n = n0 + W * tx;
     const long long r0 = (long long)blockIdx.y * per, r1 = min(M, r0 + per);
     float s[8] = {};
-    for (long long r = r0 + ty; r < r1; r += TY) {
+    if (n < N) {
+        for (long long r = r0 + ty; r < r1; r += TY * ROWS) {
+            float d[ROWS][8], q[ROWS][8];
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const int n = n0 + tx + TX * j;
-            if (n >= N) continue;
-            float d = ldf<O>(dy, r * ldy + n);
-            // rounded before it is added, whichever outputs are asked for
-            if (act != CSA_ACT_NONE) d = __fmul_rn(d, act_grad(ldf<V>(z, r * N + n), act));
-            if (dz != nullptr) put_planes<V>(dz, plane, r * ld + n, d);
-            s[j] += d;
+            for (int i = 0; i < ROWS; i++)
+                if (r + TY * i < r1) {
+                    load_cols<O, W, TX>(dy + (r + TY * i) * ldy, n, N, d[i]);
+                    if (act != CSA_ACT_NONE) load_cols<V, W, TX>(z + (r + TY * i) * N, n, N, q[i]);
+                }
+#pragma unroll
+            for (int i = 0; i < ROWS; i++) {
+                if (r + TY * i >= r1) break;
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    // rounded before it is added, whichever outputs are asked for
+                    if (act != CSA_ACT_NONE) d[i][j] = __fmul_rn(d[i][j], act_grad(q[i][j], act));
+                    s[j] += d[i][j];
+                }
+                if (dz == nullptr) continue;
+                if constexpr (VEC) {
+                    put_planes8<V>(dz, plane, (r + TY * i) * ld + n, d[i]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; j++)
+                        if (n + TX * j < N) put_planes<V>(dz, plane, (r + TY * i) * ld + n + TX * j, d[i][j]);
+                }
+            }
         }
     }
     if (sums == nullptr) return;
 #pragma unroll
-    for (int j = 0; j < 8; j++) part[ty][tx + TX * j] = s[j];
+    for (int j = 0; j < 8; j++) part[ty][VEC ? 8 * tx + j : tx + TX * j] = s[j];
     __syncthreads();
     for (int c = threadIdx.x; c < 8 * TX; c += 256) {
         float t = 0.f;
+#pragma unroll
         for (int k = 0; k < TY; k++) t += part[k][c];
         if (n0 + c < N) sums[(long long)blockIdx.y * N + n0 + c] = t;
     }
@@ -99,12 +159,13 @@ __global__ void __launch_bounds__(256) db_kernel(const float *sums, int blocks, 
 template <int V>
 __global__ void __launch_bounds__(256) join_kernel(const float *partial, int splits, long long M, long long N, const Epilogue e)
 {
-    const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * V;
-    if (i >= M * N) return;
-    const long long m = i / N, n = i - m * N;
+    const long long ldp = partial_stride(N), t = (long long)blockIdx.x * 256 + threadIdx.x;
+    const long long m = t / (ldp / V), n = (t - m * (ldp / V)) * V;
+    if (m >= M) return;
     float v[V] = {};
+#pragma unroll 4
     for (int s = 0; s < splits; s++) {
-        const float *p = partial + (long long)s * M * N + i;
+        const float *p = partial + (s * M + m) * ldp + n;
         if constexpr (V == 4) {
             const float4 x = __ldcs(reinterpret_cast<const float4 *>(p));
             v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
@@ -112,8 +173,10 @@ __global__ void __launch_bounds__(256) join_kernel(const float *partial, int spl
             v[0] += __ldcs(p);
         }
     }
+    const long long i = m * N + n;
 #pragma unroll
     for (int k = 0; k < V; k++) {
+        if (n + k >= N) break;
         float z = e.alpha * v[k] + (e.bias != nullptr ? __ldg(e.bias + n + k) : 0.f);
         if (e.preact != nullptr) {
             if (e.preact_f32) ((float *)e.preact)[i + k] = z;
@@ -154,7 +217,7 @@ struct Fwd {
 Fwd plan_fwd(const csa_linear_params &p)
 {
     Fwd f = {};
-    if (p.rows == 0) return f;
+    if (p.rows <= kSmallRows) return f;
     const long long M = p.rows, K = p.in_features, N = p.out_features;
     f.stage_x = staged(p.dtype, p.x_stride);
     f.stage_w = staged(p.dtype, K);
@@ -165,7 +228,7 @@ Fwd plan_fwd(const csa_linear_params &p)
     if (f.stage_w) at += staged_bytes(p.dtype, N, K);
     f.splits = product_splits(M, N, K, planes_of(p), kSms);
     f.off_part = at;
-    if (f.splits > 1) at += up256((size_t)f.splits * M * N * 4);
+    if (f.splits > 1) at += up256((size_t)f.splits * M * partial_stride(N) * 4);
     f.total = at;
     return f;
 }
@@ -184,10 +247,10 @@ Bwd plan_bwd(const csa_linear_params &p)
     b.stage_x = staged(p.dtype, p.x_stride);
     b.stage_w = staged(p.dtype, K);
     b.stage_dz = p.activation != CSA_ACT_NONE || p.dtype != p.out_dtype || staged(p.dtype, p.dy_stride);
-    // rows of a block of dz_kernel: enough blocks to fill the GPU a few times, 64 rows at least
-    const long long cols = (N + 255) / 256;
-    long long per = (M * cols + 4 * kSms - 1) / (4 * kSms);
-    if (per < 64) per = 64;
+    // rows of a block of dz_kernel: enough blocks to fill the GPU many times, four rows of each thread at least
+    const long long cols = N <= 64 ? 1 : (N + 255) / 256, least = N <= 64 ? 128 : 32;
+    long long per = (M * cols + 24 * kSms - 1) / (24 * kSms);
+    if (per < least) per = least;
     b.per = (int)(per < M ? per : M);
     b.blocks = (int)((M + b.per - 1) / b.per);
     size_t at = 0;
@@ -202,8 +265,8 @@ Bwd plan_bwd(const csa_linear_params &p)
     b.off_part = at;
     b.splits_dx = product_splits(M, K, N, planes_of(p), kSms);
     b.splits_dw = product_splits(N, K, M, planes_of(p), kSms);
-    const size_t dx = b.splits_dx > 1 ? (size_t)b.splits_dx * M * K * 4 : 0;
-    const size_t dw = b.splits_dw > 1 ? (size_t)b.splits_dw * N * K * 4 : 0;
+    const size_t dx = b.splits_dx > 1 ? (size_t)b.splits_dx * M * partial_stride(K) * 4 : 0;
+    const size_t dw = b.splits_dw > 1 ? (size_t)b.splits_dw * N * partial_stride(K) * 4 : 0;
     at += up256(dx > dw ? dx : dw);  // one product after the other
     b.total = at;
     return b;
@@ -234,8 +297,9 @@ cudaError_t product(const Product &p, cudaStream_t st)
 {
     const cudaError_t e = launch_product_tc(p, kSms, st);
     if (e != cudaSuccess || p.splits == 1) return e;
-    const long long total = p.M * p.N;
-    const bool four = (p.N & 3) == 0;
+    // four columns a thread where there are enough of them for that
+    const long long total = p.M * partial_stride(p.N);
+    const bool four = total >= 4 * 256 * kSms && (p.N & 3) == 0;
     const long long blocks = (total / (four ? 4 : 1) + 255) / 256;
     if (four) join_kernel<4><<<(unsigned)blocks, 256, 0, st>>>(p.e.partial, p.splits, p.M, p.N, p.e);
     else join_kernel<1><<<(unsigned)blocks, 256, 0, st>>>(p.e.partial, p.splits, p.M, p.N, p.e);
@@ -248,13 +312,15 @@ cudaError_t run_dz(const csa_linear_params &p, const Bwd &b, const void *dy, con
                    cudaStream_t st)
 {
     const int N = p.out_features;
-    const long long ld = up8(N);
-    if (N <= 64)
-        dz_kernel<V, O, 8><<<dim3((N + 63) / 64, b.blocks), 256, 0, st>>>((const O *)dy, p.dy_stride, (const V *)z, p.activation,
-                                                                          dz, ld, p.rows * ld, sums, p.rows, N, b.per);
-    else
-        dz_kernel<V, O, 32><<<dim3((N + 255) / 256, b.blocks), 256, 0, st>>>((const O *)dy, p.dy_stride, (const V *)z, p.activation,
-                                                                             dz, ld, p.rows * ld, sums, p.rows, N, b.per);
+    const long long ld = up8(N), plane = p.rows * ld;
+    const bool vec = (N & 7) == 0 && (p.dy_stride & 7) == 0;
+    const dim3 grid(N <= 64 ? 1 : (N + 255) / 256, b.blocks);
+    const O *g = (const O *)dy;
+    const V *q = (const V *)z;
+    if (N <= 64 && vec) dz_kernel<V, O, 8, true><<<grid, 256, 0, st>>>(g, p.dy_stride, q, p.activation, dz, ld, plane, sums, p.rows, N, b.per);
+    else if (N <= 64) dz_kernel<V, O, 8, false><<<grid, 256, 0, st>>>(g, p.dy_stride, q, p.activation, dz, ld, plane, sums, p.rows, N, b.per);
+    else if (vec) dz_kernel<V, O, 32, true><<<grid, 256, 0, st>>>(g, p.dy_stride, q, p.activation, dz, ld, plane, sums, p.rows, N, b.per);
+    else dz_kernel<V, O, 32, false><<<grid, 256, 0, st>>>(g, p.dy_stride, q, p.activation, dz, ld, plane, sums, p.rows, N, b.per);
     note_launches(1);
     return cudaGetLastError();
 }
@@ -275,17 +341,7 @@ size_t linear_bwd_workspace(const csa_linear_params &p) { return plan_bwd(p).tot
 cudaError_t launch_linear_fwd(const csa_linear_params &p, const void *x, const void *weight, const float *bias,
                               const void *residual, void *y, void *preact, void *ws, cudaStream_t st)
 {
-    note_path("tcgen05");
-    const Fwd f = plan_fwd(p);
-    char *w = static_cast<char *>(ws);
     Product q = {};
-    LIN_TRY(operand(&q.a, p, x, p.x_stride, p.rows, p.in_features, f.stage_x, w + f.off_x, true, st));
-    LIN_TRY(operand(&q.b, p, weight, p.in_features, p.out_features, p.in_features, f.stage_w, w + f.off_w, true, st));
-    q.M = p.rows;
-    q.N = p.out_features;
-    q.K = p.in_features;
-    q.planes = planes_of(p);
-    q.splits = f.splits;
     q.e.alpha = p.alpha;
     q.e.act = p.activation;
     q.e.bias = bias;
@@ -295,6 +351,20 @@ cudaError_t launch_linear_fwd(const csa_linear_params &p, const void *x, const v
     q.e.preact = preact;
     q.e.out_f32 = p.out_dtype == CSA_F32;
     q.e.preact_f32 = p.dtype == CSA_F32;
+    if (p.rows <= kSmallRows) {
+        note_path("generic");
+        return launch_linear_small(p, x, weight, q.e, kSms, st);
+    }
+    note_path("tcgen05");
+    const Fwd f = plan_fwd(p);
+    char *w = static_cast<char *>(ws);
+    LIN_TRY(operand(&q.a, p, x, p.x_stride, p.rows, p.in_features, f.stage_x, w + f.off_x, true, st));
+    LIN_TRY(operand(&q.b, p, weight, p.in_features, p.out_features, p.in_features, f.stage_w, w + f.off_w, true, st));
+    q.M = p.rows;
+    q.N = p.out_features;
+    q.K = p.in_features;
+    q.planes = planes_of(p);
+    q.splits = f.splits;
     q.e.partial = reinterpret_cast<float *>(w + f.off_part);
     return product(q, st);
 }

@@ -48,7 +48,7 @@ __device__ __forceinline__ float act_grad(float z, int act)
 }
 
 // Where a product's sums go.  y = act(alpha sum + bias[n]) + res; with `partial` the bare sums of split s go to
-// partial[s][M][N] instead.
+// partial[s][M][partial_stride(N)] instead.
 struct Epilogue {
     float alpha;
     int act;
@@ -58,8 +58,11 @@ struct Epilogue {
     void *out;           // [M][N]
     void *preact;        // [M][N] bf16 or fp32 as `preact_f32` says, or null
     int out_f32, preact_f32;
-    float *partial;
+    float *partial;      // rows partial_stride(N) apart
 };
+
+// Partial sums lie on 16-byte boundaries whatever N is.
+__host__ __device__ inline long long partial_stride(long long N) { return (N + 3) & ~3LL; }
 
 // One operand of a product over k: element (i, k) of plane q at base + q * plane + (k_major ? i ld + k : k ld + i).
 // fp32 values are held as three bf16 planes, x = h + m + l.
@@ -78,9 +81,14 @@ struct Product {
 };
 
 // How many pieces of the k axis the tensor-core kernel wants for this product (1: none; the caller provides
-// splits * M * N floats in e.partial and reduces them).
+// splits * M * partial_stride(N) floats in e.partial and reduces them).
 int product_splits(long long M, long long N, long long K, int planes, int sms);
 cudaError_t launch_product_tc(const Product &p, int sms, cudaStream_t st);
+
+// The forward of up to kSmallRows rows without tensor cores (k_linear_small.cu); operands where they are, no workspace.
+constexpr int kSmallRows = 8;
+cudaError_t launch_linear_small(const csa_linear_params &p, const void *x, const void *w, const Epilogue &e, int sms,
+                                cudaStream_t st);
 
 }  // namespace linear
 }  // namespace csa

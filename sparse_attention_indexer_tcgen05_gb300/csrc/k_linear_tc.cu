@@ -9,8 +9,9 @@
 // Mapping.  A unit is one output tile and one piece of the k axis.  A CTA pair (two SMs) computes 256 x BN: each CTA
 // loads its 128 rows of A and its BN / 2 rows of B, so an operand byte brought to an SM feeds twice the MMAs of a
 // lone CTA's 128 x BN tile.  Small M takes lone CTAs with 128 x 64 tiles (more of them, for the memory's sake).
-// Roles: warp 0 the TMA producer, warp 1 the MMA issue (the pair's even CTA), warps 2..9 the epilogue.  TMEM holds
-// two accumulators, so that a tile's epilogue runs under the next tile's MMAs.  Persistent: one CTA per SM, units
+// Roles: warp 0 the TMA producer, warp 1 the MMA issue (the pair's even CTA), warps 2..9 the epilogue, a row
+// a lane, whose 32 x 32 tiles go out through shared memory by TMA.  TMEM holds two accumulators, so that a
+// tile's epilogue runs under the next tile's MMAs.  Persistent: one CTA per SM, units
 // dealt round-robin in an order that keeps the running tiles' operands in L2.
 //
 // Every mbarrier wait is bounded (see tc_ptx.cuh); site codes 600 + n.
@@ -19,6 +20,7 @@
 #include "tc_ptx.cuh"
 
 #include <cuda.h>
+#include <string.h>
 
 namespace csa {
 
@@ -49,7 +51,8 @@ template <int CG, int BN> struct Cfg {
     static constexpr int A_BYTES = BM * BK * 2, B_BYTES = ROWS_B * BK * 2;
     static constexpr int STAGE = A_BYTES + B_BYTES;
     static constexpr int STAGES = STAGE == 32768 ? 6 : 8;       // 192 KB
-    static constexpr int MISC = STAGES * STAGE;
+    static constexpr int TURN = STAGES * STAGE;                 // a warp's 32 x 32 fp32 tile each, for the epilogue
+    static constexpr int MISC = TURN + EPI_WARPS * 4096;
     static constexpr int SMEM = MISC + 512 + 1024;              // + alignment
     static constexpr int TMEM = 2 * BN < 512 ? (2 * BN < 128 ? 128 : 2 * BN) : 512;
 };
@@ -60,28 +63,46 @@ struct Args {
     int passes;                 // plane pairs: 1 or 6
     int splits, per_split;      // k pieces, stages (over passes * ksteps) of each
     int mt, nt;                 // tiles
-    long long units;
+    long long whole, units;     // units that are whole tiles (times splits); the rest are halves of the last tiles
+    int tma_out;                // the outputs' rows lie on 16-byte boundaries: the epilogue stores by TMA
     Epilogue e;
 };
 
 struct Unit {
-    int m, n, s, it0, it1;
+    int m, s, it0, it1;
+    int bn;                     // columns: BN, or BN / 2 for half a tile
+    long long n0;               // first column
 };
 
 // Tiles in bands of 8 along m, m fastest: the tiles that run together share a few rows of A tiles and a few of B.
+// When the last round of whole tiles would leave half of the SMs idle or more, its tiles are cut in two along n.
 constexpr int BAND = 8;
-__device__ __forceinline__ Unit unit_of(const Args &a, long long u)
+template <int BN> __device__ __forceinline__ Unit unit_of(const Args &a, long long u)
 {
     Unit x;
     const long long tiles = (long long)a.mt * a.nt;
-    x.s = (int)(u / tiles);
-    const long long t = u - x.s * tiles;
+    long long t;
+    int half = 0;
+    x.bn = BN;
+    x.s = 0;
+    if (u < a.whole) {
+        if (a.splits > 1) {
+            x.s = (int)(u / tiles);
+            t = u - x.s * tiles;
+        } else {
+            t = u;
+        }
+    } else {
+        t = a.whole + ((u - a.whole) >> 1);
+        half = (int)((u - a.whole) & 1);
+        x.bn = BN / 2;
+    }
     const long long per_band = (long long)BAND * a.nt;
     const int band = (int)(t / per_band);
     const int r = (int)(t - band * per_band);
     const int h = min(BAND, a.mt - band * BAND);
     x.m = band * BAND + r % h;
-    x.n = r / h;
+    x.n0 = (long long)(r / h) * BN + half * (BN / 2);
     x.it0 = x.s * a.per_split;
     x.it1 = min(a.passes * a.ksteps, x.it0 + a.per_split);
     return x;
@@ -98,67 +119,114 @@ __device__ __forceinline__ void planes_of(int passes, int q, int &pa, int &pb)
     pb = (0x010120 >> (4 * q)) & 3;   // h l m h m h
 }
 
-template <typename O> __device__ __forceinline__ void store_chunk(O *row, long long n0, long long N, bool vec, const float (&v)[32])
-{
-    if (vec && n0 + 32 <= N) {
-        if constexpr (sizeof(O) == 2) {
-#pragma unroll
-            for (int k = 0; k < 4; k++) {
-                uint32_t w[4];
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * k + 2 * j], v[8 * k + 2 * j + 1]);
-                    w[j] = *reinterpret_cast<const uint32_t *>(&b);
-                }
-                reinterpret_cast<uint4 *>(row + n0)[k] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; k++)
-                reinterpret_cast<float4 *>(row + n0)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < 32; k++)
-            if (n0 + k < N) row[n0 + k] = from_f<O>(v[k]);
-    }
-}
+// ------------------------------------------------------------------ epilogue: 32 rows x 32 columns of a warp
 
-template <typename O> __device__ __forceinline__ void add_chunk(const O *row, long long n0, long long N, bool vec, float (&v)[32])
-{
-    if (vec && n0 + 32 <= N) {
-        if constexpr (sizeof(O) == 2) {
+// A lane's 32 neighbouring columns of one row of the residual, asked for before the sums are there.
+struct Residual {
+    uint4 r[8];
+    template <typename O> __device__ __forceinline__ void load(const Args &a, long long m, long long n0)
+    {
+        constexpr int E = 16 / sizeof(O);   // values of a vector
+        const O *p = (const O *)a.e.res + m * a.e.ldr + n0;
+        if (a.e.ldr % E == 0 && n0 + 32 <= a.N) {
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
-                const uint4 r = reinterpret_cast<const uint4 *>(row + n0)[k];
-                const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+            for (int k = 0; k < 32 / E; k++) r[k] = __ldcs(reinterpret_cast<const uint4 *>(p) + k);
+        } else {
+            O v[32];
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
+            for (int k = 0; k < 32; k++) v[k] = n0 + k < a.N ? p[k] : from_f<O>(0.f);
+#pragma unroll
+            for (int k = 0; k < 32 / E; k++) r[k] = *reinterpret_cast<const uint4 *>(v + E * k);
+        }
+    }
+    template <typename O> __device__ __forceinline__ void add_to(float (&v)[32]) const
+    {
+#pragma unroll
+        for (int k = 0; k < (int)(2 * sizeof(O)); k++) {
+            const uint32_t w[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                if constexpr (sizeof(O) == 2) {
                     v[8 * k + 2 * j] += __uint_as_float(w[j] << 16);
                     v[8 * k + 2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
+                } else {
+                    v[4 * k + j] += __uint_as_float(w[j]);
                 }
             }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; k++) {
-                const float4 r = reinterpret_cast<const float4 *>(row + n0)[k];
-                v[4 * k] += r.x; v[4 * k + 1] += r.y; v[4 * k + 2] += r.z; v[4 * k + 3] += r.w;
-            }
         }
-    } else {
-#pragma unroll
-        for (int k = 0; k < 32; k++)
-            if (n0 + k < N) v[k] += lds<O>(row + n0, k);
     }
+};
+
+template <int ACT> __device__ __forceinline__ void activate(float (&v)[32])
+{
+#pragma unroll
+    for (int k = 0; k < 32; k++) v[k] = act_fwd<ACT>(v[k]);
 }
 
-// The epilogue of 32 columns of one row: from sums to the output.
-__device__ __forceinline__ void finish_chunk(const Args &a, long long m, long long n0, float (&v)[32])
+// Where a warp puts a tile: 4 KB of shared memory, a whole fp32 tile or two bf16 ones in turn, from where TMA stores it.
+struct Store {
+    unsigned char *buf;
+    int lane, turn;
+    bool two;          // both halves of buf are in use: only bf16 tiles
+
+    template <typename O> __device__ __forceinline__ void tile(const Args &a, const CUtensorMap *map, const float (&v)[32], long long m0,
+                                                               long long n0, int z, O *out, long long ld)
+    {
+        if (a.tma_out) {
+            if (lane == 0) {  // the half's last store has been read
+                if (two) bulk_wait_read<1>();
+                else bulk_wait_read<0>();
+            }
+            __syncwarp();
+            unsigned char *b = buf + (two ? (turn & 1) * 2048 : 0);
+            turn++;
+            if constexpr (sizeof(O) == 2) {
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * k + 2 * j], v[8 * k + 2 * j + 1]);
+                        w[j] = *reinterpret_cast<const uint32_t *>(&h);
+                    }
+                    *reinterpret_cast<uint4 *>(b + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; k++)
+                    *reinterpret_cast<float4 *>(b + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                        make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                if (m0 < a.M && n0 < a.N) tma_store_3d(map, b, (int)n0, (int)m0, z);
+                bulk_commit();
+            }
+        } else {
+            // rows at any place: turned in shared memory so that a warp writes 32 neighbouring values at a time
+            float *t = reinterpret_cast<float *>(buf);
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 32; k++) t[lane * 32 + ((k + lane) & 31)] = v[k];
+            __syncwarp();
+            if (n0 + lane < a.N) {
+#pragma unroll 8
+                for (int r = 0; r < 32; r++)
+                    if (m0 + r < a.M) out[(m0 + r) * ld + n0 + lane] = from_f<O>(t[r * 32 + ((lane + r) & 31)]);
+            }
+        }
+    }
+};
+
+// From sums to the output: z = alpha sum + bias, kept if asked for; act(z) + res.
+template <typename O>
+__device__ __forceinline__ void finish(const Args &a, const CUtensorMap *map_out, const CUtensorMap *map_pre, Store &st, float (&v)[32],
+                                       const Residual &res, long long m0, long long n0)
 {
     const Epilogue &e = a.e;
-    const long long N = a.N;
     if (e.bias != nullptr) {
-        if (n0 + 32 <= N) {
+        if (n0 + 32 <= a.N) {
 #pragma unroll
             for (int k = 0; k < 8; k++) {
                 const float4 b = __ldg(reinterpret_cast<const float4 *>(e.bias + n0) + k);
@@ -169,38 +237,27 @@ __device__ __forceinline__ void finish_chunk(const Args &a, long long m, long lo
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < 32; k++) v[k] = fmaf(e.alpha, v[k], n0 + k < N ? __ldg(e.bias + n0 + k) : 0.f);
+            for (int k = 0; k < 32; k++) v[k] = fmaf(e.alpha, v[k], n0 + k < a.N ? __ldg(e.bias + n0 + k) : 0.f);
         }
     } else {
 #pragma unroll
         for (int k = 0; k < 32; k++) v[k] *= e.alpha;
     }
     if (e.preact != nullptr) {
-        if (e.preact_f32) store_chunk<float>((float *)e.preact + m * N, n0, N, (N & 3) == 0, v);
-        else store_chunk<__nv_bfloat16>((__nv_bfloat16 *)e.preact + m * N, n0, N, (N & 7) == 0, v);
+        if (e.preact_f32) st.tile<float>(a, map_pre, v, m0, n0, 0, (float *)e.preact, a.N);
+        else st.tile<__nv_bfloat16>(a, map_pre, v, m0, n0, 0, (__nv_bfloat16 *)e.preact, a.N);
     }
-    if (e.act == CSA_ACT_RELU) {
-#pragma unroll
-        for (int k = 0; k < 32; k++) v[k] = act_fwd<CSA_ACT_RELU>(v[k]);
-    } else if (e.act == CSA_ACT_SILU) {
-#pragma unroll
-        for (int k = 0; k < 32; k++) v[k] = act_fwd<CSA_ACT_SILU>(v[k]);
-    } else if (e.act == CSA_ACT_GELU_TANH) {
-#pragma unroll
-        for (int k = 0; k < 32; k++) v[k] = act_fwd<CSA_ACT_GELU_TANH>(v[k]);
-    }
-    if (e.out_f32) {
-        if (e.res != nullptr) add_chunk<float>((const float *)e.res + m * e.ldr, n0, N, (e.ldr & 3) == 0, v);
-        store_chunk<float>((float *)e.out + m * N, n0, N, (N & 3) == 0, v);
-    } else {
-        if (e.res != nullptr) add_chunk<__nv_bfloat16>((const __nv_bfloat16 *)e.res + m * e.ldr, n0, N, (e.ldr & 7) == 0, v);
-        store_chunk<__nv_bfloat16>((__nv_bfloat16 *)e.out + m * N, n0, N, (N & 7) == 0, v);
-    }
+    if (e.act == CSA_ACT_RELU) activate<CSA_ACT_RELU>(v);
+    else if (e.act == CSA_ACT_SILU) activate<CSA_ACT_SILU>(v);
+    else if (e.act == CSA_ACT_GELU_TANH) activate<CSA_ACT_GELU_TANH>(v);
+    if (e.res != nullptr) res.add_to<O>(v);
+    st.tile<O>(a, map_out, v, m0, n0, 0, (O *)e.out, a.N);
 }
 
 template <int CG, int BN, bool A_K, bool B_K>
 __global__ void __launch_bounds__(THREADS, 1)
-linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Args a)
+linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                 const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_pre, const Args a)
 {
     using C = Cfg<CG, BN>;
     constexpr int S = C::STAGES;
@@ -246,9 +303,10 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             bool wrapped = false;
             int used = 0;
             for (long long u = u0; u < a.units; u += ustep) {
-                const Unit x = unit_of(a, u);
+                const Unit x = unit_of<BN>(a, u);
                 const int am = (x.m * CG + (int)rank) * BM;
-                const int bn = x.n * BN + (int)rank * C::ROWS_B;
+                const int rows_b = x.bn / CG, bn = (int)x.n0 + (int)rank * rows_b;
+                const uint32_t bytes = CG * (C::A_BYTES + rows_b * BK * 2);
                 int q = x.it0 / a.ksteps, k = x.it0 - q * a.ksteps;
                 for (int it = x.it0; it < x.it1; it++) {
                     int pa, pb;
@@ -256,22 +314,24 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                     wait_bar(empty + st, ph ^ 1, abort_flag, &g_lin_error, 601);
                     unsigned char *sa = smem + st * C::STAGE, *sb = sa + C::A_BYTES;
                     if constexpr (CG == 2) {
-                        if (rank == 0) mbar_expect_tx(full + st, 2 * C::STAGE);
+                        if (rank == 0) mbar_expect_tx(full + st, bytes);
                         const uint32_t bar = map_rank(full + st, 0);
                         if constexpr (A_K) tma_load_3d_pair(sa, &map_a, bar, k * BK, am, pa);
                         else
                             for (int i = 0; i < BM / 64; i++) tma_load_3d_pair(sa + i * 8192, &map_a, bar, am + 64 * i, k * BK, pa);
-                        if constexpr (B_K) tma_load_3d_pair(sb, &map_b, bar, k * BK, bn, pb);
-                        else
-                            for (int i = 0; i < C::ROWS_B / 64; i++) tma_load_3d_pair(sb + i * 8192, &map_b, bar, bn + 64 * i, k * BK, pb);
+                        for (int i = 0; i < rows_b; i += 64) {
+                            if constexpr (B_K) tma_load_3d_pair(sb + i * 128, &map_b, bar, k * BK, bn + i, pb);
+                            else tma_load_3d_pair(sb + i * 128, &map_b, bar, bn + i, k * BK, pb);
+                        }
                     } else {
-                        mbar_expect_tx(full + st, C::STAGE);
+                        mbar_expect_tx(full + st, bytes);
                         if constexpr (A_K) tma_load_3d(sa, &map_a, full + st, k * BK, am, pa);
                         else
                             for (int i = 0; i < BM / 64; i++) tma_load_3d(sa + i * 8192, &map_a, full + st, am + 64 * i, k * BK, pa);
-                        if constexpr (B_K) tma_load_3d(sb, &map_b, full + st, k * BK, bn, pb);
-                        else
-                            for (int i = 0; i < C::ROWS_B / 64; i++) tma_load_3d(sb + i * 8192, &map_b, full + st, bn + 64 * i, k * BK, pb);
+                        for (int i = 0; i < rows_b; i += 64) {
+                            if constexpr (B_K) tma_load_3d(sb + i * 128, &map_b, full + st, k * BK, bn + i, pb);
+                            else tma_load_3d(sb + i * 128, &map_b, full + st, bn + i, k * BK, pb);
+                        }
                     }
                     if (++k == a.ksteps) {
                         k = 0;
@@ -292,11 +352,11 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMA issue (whole warp, the pair's even CTA)
         if (rank == 0) {
-            constexpr uint32_t IDESC = idesc_bf16(BM * CG, BN, !A_K, !B_K);
             int st = 0, tc = 0;
             uint32_t ph = 0;
             for (long long u = u0; u < a.units; u += ustep) {
-                const Unit x = unit_of(a, u);
+                const Unit x = unit_of<BN>(a, u);
+                const uint32_t idesc = x.bn == BN ? idesc_bf16(BM * CG, BN, !A_K, !B_K) : idesc_bf16(BM * CG, BN / 2, !A_K, !B_K);
                 const int tb = tc & 1;
                 wait_bar(t_empty + tb, ((tc >> 1) & 1) ^ 1, abort_flag, &g_lin_error, 602);
                 fence_after();
@@ -309,9 +369,9 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                     const uint64_t da = A_K ? desc_kmajor(sa) : desc_sw128(sa, 8192, 1024);
                     const uint64_t db = B_K ? desc_kmajor(sb) : desc_sw128(sb, 8192, 1024);
                     if constexpr (CG == 2)
-                        mma4_ss_pair_w(d, da, A_K ? 2 : 128, db, B_K ? 2 : 128, IDESC, it != x.it0, su32(empty + st));
+                        mma4_ss_pair_w(d, da, A_K ? 2 : 128, db, B_K ? 2 : 128, idesc, it != x.it0, su32(empty + st));
                     else
-                        mma4_ss_w(d, da, A_K ? 2 : 128, db, B_K ? 2 : 128, IDESC, it != x.it0, su32(empty + st));
+                        mma4_ss_w(d, da, A_K ? 2 : 128, db, B_K ? 2 : 128, idesc, it != x.it0, su32(empty + st));
                     if (++st == S) {
                         st = 0;
                         ph ^= 1;
@@ -329,21 +389,32 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         // ---------------------------------------------------------- epilogue (warps 2..9)
         const int quad = warp & 3;               // TMEM lanes this warp may access
         const int half = (warp - 2) >> 2;        // half of the columns
-        constexpr int COLS = BN / 2;
+        Store out;
+        out.buf = smem + C::TURN + (warp - 2) * 4096;
+        out.lane = lane;
+        out.turn = 0;
+        out.two = a.splits == 1 && !a.e.out_f32;
         int tc = 0;
         for (long long u = u0; u < a.units; u += ustep, tc++) {
-            const Unit x = unit_of(a, u);
-            const int tb = tc & 1;
-            wait_bar(t_full + tb, (tc >> 1) & 1, abort_flag, &g_lin_error, 604);
-            fence_after();
-            const long long m = ((long long)x.m * CG + rank) * BM + quad * 32 + lane;
-            const uint32_t t = tmem + (uint32_t)(tb * BN + half * COLS) + ((uint32_t)(quad * 32) << 16);
+            const Unit x = unit_of<BN>(a, u);
+            const int tb = tc & 1, cols = x.bn / 2;
+            const long long m0 = ((long long)x.m * CG + rank) * BM + quad * 32;
+            const uint32_t t = tmem + (uint32_t)(tb * BN + half * cols) + ((uint32_t)(quad * 32) << 16);
 #pragma unroll 1
-            for (int c = 0; c < COLS; c += 32) {
-                const long long n0 = (long long)x.n * BN + half * COLS + c;
+            for (int c = 0; c < cols; c += 32) {
+                const long long n0 = x.n0 + half * cols + c;
+                Residual res;
+                if (a.e.res != nullptr && a.splits == 1 && m0 + lane < a.M && n0 < a.N) {
+                    if (a.e.out_f32) res.load<float>(a, m0 + lane, n0);
+                    else res.load<__nv_bfloat16>(a, m0 + lane, n0);
+                }
+                if (c == 0) {
+                    wait_bar(t_full + tb, (tc >> 1) & 1, abort_flag, &g_lin_error, 604);
+                    fence_after();
+                }
                 float v[32];
                 tmem_ld32(t + c, v);
-                if (c + 32 == COLS) {  // the accumulator is in registers: the next tile's MMAs may have it
+                if (c + 32 == cols) {  // the accumulator is in registers: the next tile's MMAs may have it
                     fence_before();
                     __syncwarp();
                     if (lane == 0) {
@@ -351,14 +422,13 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                         else mbar_arrive(t_empty + tb);
                     }
                 }
-                if (m < a.M && n0 < a.N) {
-                    if (a.splits > 1)
-                        store_chunk<float>(a.e.partial + ((long long)x.s * a.M + m) * a.N, n0, a.N, (a.N & 3) == 0, v);
-                    else
-                        finish_chunk(a, m, n0, v);
-                }
+                if (m0 >= a.M || n0 >= a.N) continue;
+                if (a.splits > 1) out.tile<float>(a, &map_out, v, m0, n0, x.s, nullptr, 0);
+                else if (a.e.out_f32) finish<float>(a, &map_out, &map_pre, out, v, res, m0, n0);
+                else finish<__nv_bfloat16>(a, &map_out, &map_pre, out, v, res, m0, n0);
             }
         }
+        if (lane == 0) bulk_wait<0>();
     }
     __syncwarp();
     fence_before();
@@ -375,12 +445,13 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
 
 enum Shape { LONE_64, PAIR_128, PAIR_256 };
 
-// Which tile a product takes.  Lone CTAs of 128 x 64 when m fits one of them or when there are too few 256-wide tiles
-// to give every SM one; pairs otherwise, 256 wide where n is.
-static Shape shape_of(long long M, long long N)
+// Which tile a product takes.  Lone CTAs of 128 x 64 when m fits one of them; pairs otherwise, 256 wide where that
+// leaves a tile for more than half of them (a 256-wide tile moves 64 bytes of operands per SM and cycle of MMAs, a
+// 128-wide one 96).
+static Shape shape_of(long long M, long long N, int sms)
 {
     if (M <= 128) return LONE_64;
-    return N > 128 ? PAIR_256 : PAIR_128;
+    return N > 128 && (M + 255) / 256 * ((N + 255) / 256) * 2 > sms / 2 ? PAIR_256 : PAIR_128;
 }
 
 static void tile_counts(Shape s, long long M, long long N, int &mt, int &nt)
@@ -393,7 +464,7 @@ static void tile_counts(Shape s, long long M, long long N, int &mt, int &nt)
 int product_splits(long long M, long long N, long long K, int planes, int sms)
 {
     int mt, nt;
-    const Shape s = shape_of(M, N);
+    const Shape s = shape_of(M, N, sms);
     tile_counts(s, M, N, mt, nt);
     const long long tiles = (long long)mt * nt, slots = s == LONE_64 ? sms : sms / 2;
     const long long steps = (K + BK - 1) / BK * (planes == 3 ? 6 : 1);
@@ -404,7 +475,7 @@ int product_splits(long long M, long long N, long long K, int planes, int sms)
 }
 
 template <int CG, int BN, bool A_K, bool B_K>
-static cudaError_t launch(const CUtensorMap &ma, const CUtensorMap &mb, const Args &a, int sms, cudaStream_t st)
+static cudaError_t launch(const CUtensorMap (&map)[4], const Args &a, int sms, cudaStream_t st)
 {
     using C = Cfg<CG, BN>;
     auto *kernel = linear_tc_kernel<CG, BN, A_K, B_K>;
@@ -422,17 +493,26 @@ static cudaError_t launch(const CUtensorMap &ma, const CUtensorMap &mb, const Ar
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = CG == 2 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, kernel, ma, mb, a);
+    e = cudaLaunchKernelEx(&cfg, kernel, map[0], map[1], map[2], map[3], a);
     if (e == cudaSuccess) note_launches(1);
     return e;
 }
 
 template <int CG, int BN>
-static cudaError_t launch_majors(const Product &p, const CUtensorMap &ma, const CUtensorMap &mb, const Args &a, int sms,
-                                 cudaStream_t st)
+static cudaError_t launch_majors(const Product &p, const CUtensorMap (&map)[4], const Args &a, int sms, cudaStream_t st)
 {
-    if (p.a.k_major) return p.b.k_major ? launch<CG, BN, true, true>(ma, mb, a, sms, st) : launch<CG, BN, true, false>(ma, mb, a, sms, st);
-    return launch<CG, BN, false, false>(ma, mb, a, sms, st);
+    if (p.a.k_major) return p.b.k_major ? launch<CG, BN, true, true>(map, a, sms, st) : launch<CG, BN, true, false>(map, a, sms, st);
+    return launch<CG, BN, false, false>(map, a, sms, st);
+}
+
+// The outputs' tiles: `n` values a row, rows `ld` apart, `z` matrices of M rows.
+static bool encode_out(CUtensorMap *m, bool f32, const void *base, long long n, long long ld, long long M, int z)
+{
+    const long long size = f32 ? 4 : 2;
+    const cuuint64_t dims[3] = {(cuuint64_t)n, (cuuint64_t)M, (cuuint64_t)z};
+    const cuuint64_t strides[2] = {(cuuint64_t)(ld * size), (cuuint64_t)(M * ld * size)};
+    const cuuint32_t box[3] = {32, 32, 1};
+    return tc_encode_store(m, f32, base, 3, dims, strides, box);
 }
 
 // A map over {contiguous, strided, plane} of an operand of `n` rows (m or n) and K; boxes of 64 contiguous values.
@@ -449,7 +529,7 @@ static bool encode(CUtensorMap *m, const Operand &o, long long n, long long K, i
 
 cudaError_t launch_product_tc(const Product &p, int sms, cudaStream_t st)
 {
-    const Shape s = shape_of(p.M, p.N);
+    const Shape s = shape_of(p.M, p.N, sms);
     Args a = {};
     a.M = p.M;
     a.N = p.N;
@@ -459,14 +539,29 @@ cudaError_t launch_product_tc(const Product &p, int sms, cudaStream_t st)
     a.per_split = (steps + p.splits - 1) / p.splits;
     a.splits = p.splits;
     tile_counts(s, p.M, p.N, a.mt, a.nt);
-    a.units = (long long)a.mt * a.nt * p.splits;
+    a.units = a.whole = (long long)a.mt * a.nt * p.splits;
+    const long long slots = sms / 2, rest = a.units % slots;
+    if (s == PAIR_256 && p.splits == 1 && a.units > slots && rest > 0 && 2 * rest <= slots) {
+        a.whole -= rest;
+        a.units += rest;
+    }
     a.e = p.e;
-    CUtensorMap ma, mb;
-    const int rows_b = s == PAIR_256 ? 128 : 64;
-    if (!encode(&ma, p.a, p.M, p.K, p.planes, BM) || !encode(&mb, p.b, p.N, p.K, p.planes, rows_b)) return cudaErrorInvalidValue;
-    if (s == LONE_64) return launch_majors<1, 64>(p, ma, mb, a, sms, st);
-    if (s == PAIR_128) return launch_majors<2, 128>(p, ma, mb, a, sms, st);
-    return launch_majors<2, 256>(p, ma, mb, a, sms, st);
+    CUtensorMap map[4];
+    memset(map, 0, sizeof map);
+    if (!encode(&map[0], p.a, p.M, p.K, p.planes, BM) || !encode(&map[1], p.b, p.N, p.K, p.planes, 64)) return cudaErrorInvalidValue;
+    if (p.splits > 1) {
+        a.tma_out = 1;
+        if (!encode_out(&map[2], true, p.e.partial, p.N, partial_stride(p.N), p.M, p.splits)) return cudaErrorInvalidValue;
+    } else {
+        a.tma_out = p.N % (p.e.out_f32 ? 4 : 8) == 0 && (p.e.preact == nullptr || p.N % (p.e.preact_f32 ? 4 : 8) == 0);
+        if (a.tma_out) {
+            if (!encode_out(&map[2], p.e.out_f32, p.e.out, p.N, p.N, p.M, 1)) return cudaErrorInvalidValue;
+            if (p.e.preact != nullptr && !encode_out(&map[3], p.e.preact_f32, p.e.preact, p.N, p.N, p.M, 1)) return cudaErrorInvalidValue;
+        }
+    }
+    if (s == LONE_64) return launch_majors<1, 64>(p, map, a, sms, st);
+    if (s == PAIR_128) return launch_majors<2, 128>(p, map, a, sms, st);
+    return launch_majors<2, 256>(p, map, a, sms, st);
 }
 
 }  // namespace linear

@@ -20,7 +20,7 @@ namespace csa {
 namespace rope {
 
 constexpr int THREADS = 256;
-constexpr int UNROLL = 4;                       // items of a thread whose loads are in flight together
+constexpr int UNROLL = 2;                       // items of a thread whose loads are in flight together
 constexpr int TABLE = 2048;                     // cosine and sine pairs in shared memory
 
 struct Args {
@@ -34,6 +34,8 @@ struct Args {
     int copy_lo;                                // vectors before the rotated part
     int copy_half;                              // copy item c moves vectors c and c + copy_half
     int copy_vecs;
+    int copy_skip;                              // elements from a copied vector's number to its place behind the pairs
+    unsigned long long magic_pairs, magic_row, magic_head;  // see quotient()
     int rows_cta, heads_cta;                    // rows and heads of one CTA
     int slices;                                 // CTAs that share the heads of their rows
     int copy;                                   // the values outside the rotation move (not in place)
@@ -54,34 +56,47 @@ template <typename T, int V> union Vec {
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 
+// i / d for i < 2^20 and d < 2^20, with magic = 2^40 / d + 1
+__device__ __forceinline__ int quotient(int i, unsigned long long magic) { return (int)((unsigned long long)i * magic >> 40); }
+
 template <typename T, int V, bool PAIRED>
-__global__ void __launch_bounds__(THREADS) rope_kernel(const Args a)
+__global__ void __launch_bounds__(THREADS, 4) rope_kernel(const Args a)
 {
     __shared__ float2 cs[TABLE];  // (cos, sin) of [row of the CTA][pair]
     const long long row0 = (long long)(blockIdx.x / a.slices) * a.rows_cta;
     const int head0 = (int)(blockIdx.x % a.slices) * a.heads_cta;
     const int nrow = (int)min((long long)a.rows_cta, a.rows - row0);
     const int nhead = min(a.heads_cta, a.heads - head0);
-    const int row_items = nhead * a.head_items;
+    const int row_items = a.heads_cta * a.head_items;  // the last slice of a row leaves some out
     const int total = nrow * row_items;
-    const T *x = static_cast<const T *>(a.x);
-    T *out = static_cast<T *>(a.out);
-    bool have_table = false;
+    const T *x = static_cast<const T *>(a.x) + row0 * a.xr + head0 * a.xh;
+    T *out = static_cast<T *>(a.out) + row0 * a.yr + head0 * a.yh;
+
+    // the first angle's inputs are asked for before the values: they are needed first
+    const int angles = nrow * a.pairs;
+    long long pos = 0;
+    double freq = 0.0;
+    auto fetch = [&](int t) {
+        const int r = quotient(t, a.magic_pairs), i = t - r * a.pairs;
+        const int axis = (i >= a.end0) + (i >= a.end1) + (i >= a.end2);
+        const long long at = axis * a.rows + row0 + r;
+        pos = a.pos64 ? static_cast<const long long *>(a.positions)[at] : (long long)static_cast<const int *>(a.positions)[at];
+        freq = a.inv_freq[i];
+    };
+    if ((int)threadIdx.x < angles) fetch(threadIdx.x);
 
     for (int base = 0; base < total; base += THREADS * UNROLL) {
         Vec<T, V> u[UNROLL], v[UNROLL];
-        long long yo[UNROLL];        // element offset of the item's first vector in out; -1: nothing to do
+        T *to[UNROLL];               // the item's first vector in out; null: nothing to do
         int second[UNROLL];          // elements from the first vector to the second (0: there is none)
         int pair[UNROLL];            // index into cs of the item's first pair; -1: a copy
 #pragma unroll
         for (int k = 0; k < UNROLL; k++) {
             const int it = base + k * THREADS + threadIdx.x;
-            yo[k] = -1;
-            if (it >= total) continue;
-            const int r = it / row_items, rest = it - r * row_items;
-            const int hd = rest / a.head_items, c = rest - hd * a.head_items;
-            const long long xo0 = (row0 + r) * a.xr + (long long)(head0 + hd) * a.xh;
-            const long long yo0 = (row0 + r) * a.yr + (long long)(head0 + hd) * a.yh;
+            to[k] = nullptr;
+            const int r = quotient(it, a.magic_row), rest = it - r * row_items;
+            const int hd = quotient(rest, a.magic_head), c = rest - hd * a.head_items;
+            if (it >= total || hd >= nhead) continue;
             int el;
             if (c < a.rot_items) {
                 if constexpr (PAIRED && V == 1) {
@@ -97,24 +112,19 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const Args a)
                 pair[k] = r * a.pairs + V * c;
             } else {
                 const int q = c - a.rot_items, q2 = q + a.copy_half;
-                const int e1 = V * (q < a.copy_lo ? q : q - a.copy_lo) + (q < a.copy_lo ? 0 : a.offset + 2 * a.pairs);
-                const int e2 = V * (q2 < a.copy_lo ? q2 : q2 - a.copy_lo) + (q2 < a.copy_lo ? 0 : a.offset + 2 * a.pairs);
-                el = e1;
-                second[k] = q2 < a.copy_vecs ? e2 - e1 : 0;
+                el = V * q + (q < a.copy_lo ? 0 : a.copy_skip);
+                second[k] = q2 < a.copy_vecs ? V * q2 + (q2 < a.copy_lo ? 0 : a.copy_skip) - el : 0;
                 pair[k] = -1;
             }
-            yo[k] = yo0 + el;
-            u[k].w = *reinterpret_cast<const decltype(u[k].w) *>(x + xo0 + el);
-            if (second[k] != 0) v[k].w = *reinterpret_cast<const decltype(v[k].w) *>(x + xo0 + el + second[k]);
+            const T *from = x + (r * a.xr + hd * a.xh + el);
+            to[k] = out + (r * a.yr + hd * a.yh + el);
+            u[k].w = *reinterpret_cast<const decltype(u[k].w) *>(from);
+            if (second[k] != 0) v[k].w = *reinterpret_cast<const decltype(v[k].w) *>(from + second[k]);
         }
-        if (!have_table) {
-            for (int t = threadIdx.x; t < nrow * a.pairs; t += THREADS) {
-                const int r = t / a.pairs, i = t - r * a.pairs;
-                const int axis = (i >= a.end0) + (i >= a.end1) + (i >= a.end2);
-                const long long at = axis * a.rows + row0 + r;
-                const long long pos = a.pos64 ? static_cast<const long long *>(a.positions)[at]
-                                              : (long long)static_cast<const int *>(a.positions)[at];
-                double turns = a.inv_freq[i] * 0.15915494309189533577;  // 1 / 2 pi
+        if (base == 0) {
+            for (int t = threadIdx.x; t < angles; t += THREADS) {
+                if (t >= THREADS) fetch(t);
+                double turns = freq * 0.15915494309189533577;  // 1 / 2 pi
                 turns -= floor(turns);
                 const unsigned long long f = __double2ull_rn(turns * 18446744073709551616.0);
                 const int half = (int)(((unsigned long long)pos * f) >> 32);  // 2^-31 half turns, whole turns dropped
@@ -123,11 +133,10 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const Args a)
                 cs[t] = make_float2(c, a.inverse ? -s : s);
             }
             __syncthreads();
-            have_table = true;
         }
 #pragma unroll
         for (int k = 0; k < UNROLL; k++) {
-            if (yo[k] < 0) continue;
+            if (to[k] == nullptr) continue;
             if (pair[k] >= 0) {
                 const float2 *t = cs + pair[k];
                 if constexpr (PAIRED && V > 1) {
@@ -157,8 +166,8 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const Args a)
                     }
                 }
             }
-            *reinterpret_cast<decltype(u[k].w) *>(out + yo[k]) = u[k].w;
-            if (second[k] != 0) *reinterpret_cast<decltype(v[k].w) *>(out + yo[k] + second[k]) = v[k].w;
+            *reinterpret_cast<decltype(u[k].w) *>(to[k]) = u[k].w;
+            if (second[k] != 0) *reinterpret_cast<decltype(v[k].w) *>(to[k] + second[k]) = v[k].w;
         }
     }
 }
@@ -171,6 +180,7 @@ template <typename T, int V> cudaError_t launch(const csa_rope_params &p, Args &
     a.copy_lo = p.rot_offset / V;
     a.copy_vecs = a.copy ? (p.head_dim - p.rot_dim) / V : 0;
     a.copy_half = (a.copy_vecs + 1) / 2;
+    a.copy_skip = p.rot_dim;
     a.head_items = a.rot_items + a.copy_half;
     if (a.head_items == 0) return cudaSuccess;  // in place and nothing rotates
     // A CTA's share: UNROLL items a thread when there are enough of them for every SM, by whole rows while their
@@ -190,6 +200,10 @@ template <typename T, int V> cudaError_t launch(const csa_rope_params &p, Args &
         a.rows_cta = (int)r;
     }
     a.slices = (a.heads + a.heads_cta - 1) / a.heads_cta;
+    const auto magic = [](long long d) { return (1ull << 40) / (unsigned long long)(d > 0 ? d : 1) + 1; };
+    a.magic_pairs = magic(a.pairs);
+    a.magic_row = magic((long long)a.heads_cta * a.head_items);
+    a.magic_head = magic(a.head_items);
     const long long ctas = (a.rows + a.rows_cta - 1) / a.rows_cta * a.slices;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     if (paired) {

@@ -141,6 +141,18 @@ __device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, u
                  : "memory");
 }
 
+// Shared memory -> global, in this thread's bulk group; the group's commit and the wait until all but the n most
+// recent groups have been read (so that their shared memory may be written) or written.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 ::"l"(map), "r"(su32(src)), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
+template <int N> __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group %0;" ::"n"(N) : "memory"); }
+
 // Shared-memory matrix descriptor, 128-byte swizzle, version 1 (bits 46-47), layout SWIZZLE_128B (bits 61-63 = 2).
 //   K-major:  rows of 128 B (64 bf16 of K) per M/N index, 8-row atoms of 1024 B: SBO = 1024 B; LBO unused.
 //   MN-major: 64 consecutive M/N elements per 128-B row, one row per K index, 8-row atoms of 1024 B along K:
@@ -362,9 +374,11 @@ __device__ __forceinline__ uint32_t map_rank(const void *p, uint32_t r)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(su32(p)), "r"(r));
     return a;
 }
+// Arrival on a barrier of either CTA that hands over nothing but TMEM (ordered by the tcgen05 fences): relaxed, since a
+// release at cluster scope would first wait for every global store of the thread.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 // Load into this CTA's shared memory, completion counted on a barrier of either CTA of the pair.
 __device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *map, uint32_t bar_cluster, int x, int y,
