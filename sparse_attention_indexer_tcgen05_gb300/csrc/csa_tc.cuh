@@ -32,9 +32,8 @@ bool tc_encode_q_map(CUtensorMap *m, const void *q_idx, const Geo &g);
 bool tc_encode_f32(CUtensorMap *m, const float *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
                    const cuuint32_t *box);
 bool tc_encode_k_map(CUtensorMap *m, const void *k_idx, const Geo &g);
-// Tiles of 32 values a row for stores: fp32 with the 128-byte swizzle, bf16 with the 64-byte one.
-bool tc_encode_store(CUtensorMap *m, bool f32, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
-                     const cuuint32_t *box);
+// For stores (rank 3): boxes of 32 rows of 128 bytes, 128-byte swizzle.
+bool tc_encode_store(CUtensorMap *m, bool f32, const void *base, const cuuint64_t *dims, const cuuint64_t *strides);
 
 // Tensor-core backward (dQ_idx, dW, dK) for bf16, H_I = 64, D_I = 128: any key axis with the sparse loss, key
 // axes up to 1024 with the dense loss.

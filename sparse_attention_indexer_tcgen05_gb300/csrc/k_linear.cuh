@@ -6,22 +6,29 @@
 namespace csa {
 namespace linear {
 
-// s(u) = 1 / (1 + exp(-u)) with the hardware's base-2 exponential and reciprocal (2 units in the last place each)
-__device__ __forceinline__ float sigmoid(float u)
+// s(u) = 1 / (1 + 2^t), t = -u log2(e), with the hardware's base-2 exponential and reciprocal (2 units in the last
+// place each)
+__device__ __forceinline__ float sigmoid2(float t)
 {
     float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * u));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
     return r;
 }
-
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGelu = 1.5957691216057308f, kCubic = 0.044715f;  // 2 sqrt(2 / pi)
+__device__ __forceinline__ float sigmoid(float u) { return sigmoid2(-kLog2e * u); }
+// s(kGelu (z + kCubic z^3))
+__device__ __forceinline__ float gelu_sigmoid(float z)
+{
+    return sigmoid2(z * fmaf(-kLog2e * kGelu * kCubic, z * z, -kLog2e * kGelu));
+}
 
 template <int ACT> __device__ __forceinline__ float act_fwd(float z)
 {
     if constexpr (ACT == CSA_ACT_RELU) return z < 0.f ? 0.f : z;  // keeps NaN
     if constexpr (ACT == CSA_ACT_SILU) return z * sigmoid(z);
-    if constexpr (ACT == CSA_ACT_GELU_TANH) return z * sigmoid(kGelu * (z + kCubic * z * z * z));
+    if constexpr (ACT == CSA_ACT_GELU_TANH) return z * gelu_sigmoid(z);
     return z;
 }
 __device__ __forceinline__ float act_fwd(float z, int act)
@@ -40,7 +47,7 @@ __device__ __forceinline__ float act_grad(float z, int act)
         return s * (1.f + z * (1.f - s));
     }
     if (act == CSA_ACT_GELU_TANH) {
-        const float s = sigmoid(kGelu * (z + kCubic * z * z * z));
+        const float s = gelu_sigmoid(z);
         const float q = s * (1.f - s);  // 0 far out, where z^2 may overflow
         return q > 0.f ? s + z * q * kGelu * (1.f + 3.f * kCubic * z * z) : s;
     }
@@ -61,8 +68,8 @@ struct Epilogue {
     float *partial;      // rows partial_stride(N) apart
 };
 
-// Partial sums lie on 16-byte boundaries whatever N is.
-__host__ __device__ inline long long partial_stride(long long N) { return (N + 3) & ~3LL; }
+// Rows of partial sums start on 32-byte sectors whatever N is.
+__host__ __device__ inline long long partial_stride(long long N) { return (N + 7) & ~7LL; }
 
 // One operand of a product over k: element (i, k) of plane q at base + q * plane + (k_major ? i ld + k : k ld + i).
 // fp32 values are held as three bf16 planes, x = h + m + l.

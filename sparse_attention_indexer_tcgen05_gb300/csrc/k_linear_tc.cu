@@ -10,7 +10,7 @@
 // loads its 128 rows of A and its BN / 2 rows of B, so an operand byte brought to an SM feeds twice the MMAs of a
 // lone CTA's 128 x BN tile.  Small M takes lone CTAs with 128 x 64 tiles (more of them, for the memory's sake).
 // Roles: warp 0 the TMA producer, warp 1 the MMA issue (the pair's even CTA), warps 2..9 the epilogue, a row
-// a lane, whose 32 x 32 tiles go out through shared memory by TMA.  TMEM holds two accumulators, so that a
+// of the tile a lane.  TMEM holds two accumulators, so that a
 // tile's epilogue runs under the next tile's MMAs.  Persistent: one CTA per SM, units
 // dealt round-robin in an order that keeps the running tiles' operands in L2.
 //
@@ -20,7 +20,6 @@
 #include "tc_ptx.cuh"
 
 #include <cuda.h>
-#include <string.h>
 
 namespace csa {
 
@@ -51,20 +50,22 @@ template <int CG, int BN> struct Cfg {
     static constexpr int A_BYTES = BM * BK * 2, B_BYTES = ROWS_B * BK * 2;
     static constexpr int STAGE = A_BYTES + B_BYTES;
     static constexpr int STAGES = STAGE == 32768 ? 6 : 8;       // 192 KB
-    static constexpr int TURN = STAGES * STAGE;                 // a warp's 32 x 32 fp32 tile each, for the epilogue
+    static constexpr int TURN = STAGES * STAGE;                 // the epilogue's buffers, 32 rows of 128 bytes a warp
     static constexpr int MISC = TURN + EPI_WARPS * 4096;
     static constexpr int SMEM = MISC + 512 + 1024;              // + alignment
     static constexpr int TMEM = 2 * BN < 512 ? (2 * BN < 128 ? 128 : 2 * BN) : 512;
 };
 
 struct Args {
-    long long M, N;
+    long long M, N, ldo;        // the output's row stride
     int ksteps;                 // stages of one plane pair over the whole k axis
     int passes;                 // plane pairs: 1 or 6
     int splits, per_split;      // k pieces, stages (over passes * ksteps) of each
     int mt, nt;                 // tiles
-    long long whole, units;     // units that are whole tiles (times splits); the rest are halves of the last tiles
-    int tma_out;                // the outputs' rows lie on 16-byte boundaries: the epilogue stores by TMA
+    int whole, units;           // units that are whole tiles (times splits); the rest are halves of the last tiles
+    int blocks_a, blocks_b;     // an m/n-contiguous operand's map has 64-wide blocks as an axis of their own
+    int tma_out;                // the output goes by TMA
+    int res32;                  // the residual's rows start on 32-byte sectors
     Epilogue e;
 };
 
@@ -77,29 +78,28 @@ struct Unit {
 // Tiles in bands of 8 along m, m fastest: the tiles that run together share a few rows of A tiles and a few of B.
 // When the last round of whole tiles would leave half of the SMs idle or more, its tiles are cut in two along n.
 constexpr int BAND = 8;
-template <int BN> __device__ __forceinline__ Unit unit_of(const Args &a, long long u)
+template <int BN> __device__ __forceinline__ Unit unit_of(const Args &a, int u)
 {
     Unit x;
-    const long long tiles = (long long)a.mt * a.nt;
-    long long t;
-    int half = 0;
+    const int tiles = a.mt * a.nt;
+    int t, half = 0;
     x.bn = BN;
     x.s = 0;
     if (u < a.whole) {
         if (a.splits > 1) {
-            x.s = (int)(u / tiles);
+            x.s = u / tiles;
             t = u - x.s * tiles;
         } else {
             t = u;
         }
     } else {
         t = a.whole + ((u - a.whole) >> 1);
-        half = (int)((u - a.whole) & 1);
+        half = (u - a.whole) & 1;
         x.bn = BN / 2;
     }
-    const long long per_band = (long long)BAND * a.nt;
-    const int band = (int)(t / per_band);
-    const int r = (int)(t - band * per_band);
+    const int per_band = BAND * a.nt;
+    const int band = t / per_band;
+    const int r = t - band * per_band;
     const int h = min(BAND, a.mt - band * BAND);
     x.m = band * BAND + r % h;
     x.n0 = (long long)(r / h) * BN + half * (BN / 2);
@@ -121,156 +121,192 @@ __device__ __forceinline__ void planes_of(int passes, int q, int &pa, int &pb)
 
 // ------------------------------------------------------------------ epilogue: 32 rows x 32 columns of a warp
 
-// A lane's 32 neighbouring columns of one row of the residual, asked for before the sums are there.
-struct Residual {
-    uint4 r[8];
-    template <typename O> __device__ __forceinline__ void load(const Args &a, long long m, long long n0)
-    {
-        constexpr int E = 16 / sizeof(O);   // values of a vector
-        const O *p = (const O *)a.e.res + m * a.e.ldr + n0;
-        if (a.e.ldr % E == 0 && n0 + 32 <= a.N) {
-#pragma unroll
-            for (int k = 0; k < 32 / E; k++) r[k] = __ldcs(reinterpret_cast<const uint4 *>(p) + k);
-        } else {
-            O v[32];
-#pragma unroll
-            for (int k = 0; k < 32; k++) v[k] = n0 + k < a.N ? p[k] : from_f<O>(0.f);
-#pragma unroll
-            for (int k = 0; k < 32 / E; k++) r[k] = *reinterpret_cast<const uint4 *>(v + E * k);
-        }
-    }
-    template <typename O> __device__ __forceinline__ void add_to(float (&v)[32]) const
-    {
-#pragma unroll
-        for (int k = 0; k < (int)(2 * sizeof(O)); k++) {
-            const uint32_t w[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                if constexpr (sizeof(O) == 2) {
-                    v[8 * k + 2 * j] += __uint_as_float(w[j] << 16);
-                    v[8 * k + 2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
-                } else {
-                    v[4 * k + j] += __uint_as_float(w[j]);
-                }
-            }
-        }
-    }
+// Shared memory a warp stores from: 32 rows of 128 bytes.
+struct Buffer {
+    unsigned char *p;
+    int lane;
 };
 
-template <int ACT> __device__ __forceinline__ void activate(float (&v)[32])
+// 256-bit accesses, whole sectors
+__device__ __forceinline__ void st32(void *p, const uint32_t (&w)[8])
 {
-#pragma unroll
-    for (int k = 0; k < 32; k++) v[k] = act_fwd<ACT>(v[k]);
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+__device__ __forceinline__ void ld32(const void *p, uint32_t *w)
+{
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p)
+                 : "memory");
 }
 
-// Where a warp puts a tile: 4 KB of shared memory, a whole fp32 tile or two bf16 ones in turn, from where TMA stores it.
-struct Store {
-    unsigned char *buf;
-    int lane, turn;
-    bool two;          // both halves of buf are in use: only bf16 tiles
+constexpr int C = 32;   // columns of an epilogue step
 
-    template <typename O> __device__ __forceinline__ void tile(const Args &a, const CUtensorMap *map, const float (&v)[32], long long m0,
-                                                               long long n0, int z, O *out, long long ld)
+// 32 columns of one row of the residual (those behind N: 0), asked for a step before they are used.
+template <typename O> struct Residual {
+    uint32_t r[C * sizeof(O) / 4];
+    __device__ __forceinline__ void load(const Args &a, long long m, long long n0)
     {
-        if (a.tma_out) {
-            if (lane == 0) {  // the half's last store has been read
-                if (two) bulk_wait_read<1>();
-                else bulk_wait_read<0>();
-            }
-            __syncwarp();
-            unsigned char *b = buf + (two ? (turn & 1) * 2048 : 0);
-            turn++;
-            if constexpr (sizeof(O) == 2) {
+        constexpr int E = 32 / sizeof(O);   // values of a sector
+        const O *p = (const O *)a.e.res + m * a.e.ldr + n0;
+        if (a.res32 && n0 + C <= a.N) {
 #pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * k + 2 * j], v[8 * k + 2 * j + 1]);
-                        w[j] = *reinterpret_cast<const uint32_t *>(&h);
-                    }
-                    *reinterpret_cast<uint4 *>(b + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; k++)
-                    *reinterpret_cast<float4 *>(b + lane * 128 + ((k ^ (lane & 7)) << 4)) =
-                        make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-            }
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) {
-                if (m0 < a.M && n0 < a.N) tma_store_3d(map, b, (int)n0, (int)m0, z);
-                bulk_commit();
-            }
+            for (int k = 0; k < C / E; k++) ld32(p + E * k, r + 8 * k);
         } else {
-            // rows at any place: turned in shared memory so that a warp writes 32 neighbouring values at a time
-            float *t = reinterpret_cast<float *>(buf);
-            __syncwarp();
 #pragma unroll
-            for (int k = 0; k < 32; k++) t[lane * 32 + ((k + lane) & 31)] = v[k];
-            __syncwarp();
-            if (n0 + lane < a.N) {
-#pragma unroll 8
-                for (int r = 0; r < 32; r++)
-                    if (m0 + r < a.M) out[(m0 + r) * ld + n0 + lane] = from_f<O>(t[r * 32 + ((lane + r) & 31)]);
+            for (int k = 0; k < C; k++) {
+                if constexpr (sizeof(O) == 4) {
+                    r[k] = n0 + k < a.N ? __float_as_uint(p[k]) : 0u;
+                } else {
+                    const uint32_t h = n0 + k < a.N ? (uint32_t)reinterpret_cast<const unsigned short *>(p)[k] : 0u;
+                    if (k % 2 == 0) r[k / 2] = h;
+                    else r[k / 2] |= h << 16;
+                }
             }
+        }
+    }
+    __device__ __forceinline__ void add_to(float (&v)[C]) const
+    {
+#pragma unroll
+        for (int k = 0; k < C; k++) {
+            if constexpr (sizeof(O) == 4) v[k] += __uint_as_float(r[k]);
+            else v[k] += __uint_as_float(k % 2 == 0 ? r[k / 2] << 16 : r[k / 2] & 0xffff0000u);
         }
     }
 };
 
-// From sums to the output: z = alpha sum + bias, kept if asked for; act(z) + res.
+template <int ACT> __device__ __forceinline__ void activate(float (&v)[C])
+{
+#pragma unroll
+    for (int k = 0; k < C; k++) v[k] = act_fwd<ACT>(v[k]);
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// A warp's 32 rows x 32 columns, a row a lane, to memory by the lanes' own stores; rows from M and columns from N on
+// are left out.  Rows on 32-byte boundaries: each lane its own sectors.  Else: turned in shared memory so that a warp
+// writes 32 neighbouring values at a time.
 template <typename O>
-__device__ __forceinline__ void finish(const Args &a, const CUtensorMap *map_out, const CUtensorMap *map_pre, Store &st, float (&v)[32],
-                                       const Residual &res, long long m0, long long n0)
+__device__ __forceinline__ void store_tile(O *out, long long ld, long long M, long long N, const float (&v)[C], long long m0, long long n0,
+                                           const Buffer &b)
+{
+    const int lane = b.lane;
+    constexpr int E = 32 / sizeof(O);
+    if (ld % E == 0 && (reinterpret_cast<uintptr_t>(out) & 31) == 0) {
+        if (m0 + lane >= M) return;
+        O *p = out + (m0 + lane) * ld + n0;
+#pragma unroll
+        for (int k = 0; k < C / E; k++) {
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; j++) w[j] = sizeof(O) == 2 ? pack2(v[E * k + 2 * j % E], v[E * k + (2 * j + 1) % E]) : __float_as_uint(v[E * k + j]);
+            if (n0 + E * k < N) st32(p + E * k, w);
+        }
+    } else {
+        float *turn = reinterpret_cast<float *>(b.p);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < C; k++) turn[lane * 32 + ((k + lane) & 31)] = v[k];
+        __syncwarp();
+        if (n0 + lane < N) {
+#pragma unroll 8
+            for (int r = 0; r < 32; r++)
+                if (m0 + r < M) out[(m0 + r) * ld + n0 + lane] = from_f<O>(turn[r * 32 + ((lane + r) & 31)]);
+        }
+    }
+}
+
+// The same by TMA, from rows of 128 bytes in shared memory (32 fp32 columns, or 64 bf16 ones: two steps), so that a
+// request to L2 carries four sectors.  (The lanes' own sectors slowed the loads of the next tile: 150 us a product
+// of 8192 x 8192 x 2048 instead of 148, and 640 instead of 572 at k = 8192.)  `second`: the right 64 bytes of bf16
+// rows; `go`: the rows are complete.
+template <typename O>
+__device__ __forceinline__ void tma_tile(const CUtensorMap *map, const float (&v)[C], long long m0, long long n0, int s, bool second, bool go,
+                                         const Buffer &b)
+{
+    const int lane = b.lane;
+    if (!second) {
+        if (lane == 0) bulk_wait_read();  // the last tile has left the buffer
+        __syncwarp();
+    }
+    const int first = sizeof(O) == 2 && second ? 4 : 0;
+#pragma unroll
+    for (int k = 0; k < (int)(2 * sizeof(O)); k++) {
+        uint4 w;
+        if constexpr (sizeof(O) == 2)
+            w = make_uint4(pack2(v[8 * k], v[8 * k + 1]), pack2(v[8 * k + 2], v[8 * k + 3]), pack2(v[8 * k + 4], v[8 * k + 5]),
+                           pack2(v[8 * k + 6], v[8 * k + 7]));
+        else
+            w = make_uint4(__float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]), __float_as_uint(v[4 * k + 2]), __float_as_uint(v[4 * k + 3]));
+        *reinterpret_cast<uint4 *>(b.p + lane * 128 + (((first + k) ^ (lane & 7)) << 4)) = w;
+    }
+    if (!go) return;
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) {
+        tma_store_3d(map, b.p, (int)n0 - (sizeof(O) == 2 && second ? C : 0), (int)m0, s);
+        bulk_commit();
+    }
+}
+
+// z = alpha sum + bias, kept if asked for; then act(z), in place.
+__device__ __forceinline__ void to_activation(const Args &a, float (&v)[C], long long m0, long long n0, const Buffer &b)
 {
     const Epilogue &e = a.e;
     if (e.bias != nullptr) {
-        if (n0 + 32 <= a.N) {
 #pragma unroll
-            for (int k = 0; k < 8; k++) {
-                const float4 b = __ldg(reinterpret_cast<const float4 *>(e.bias + n0) + k);
-                v[4 * k] = fmaf(e.alpha, v[4 * k], b.x);
-                v[4 * k + 1] = fmaf(e.alpha, v[4 * k + 1], b.y);
-                v[4 * k + 2] = fmaf(e.alpha, v[4 * k + 2], b.z);
-                v[4 * k + 3] = fmaf(e.alpha, v[4 * k + 3], b.w);
+        for (int k = 0; k < C / 4; k++) {
+            float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float *p = e.bias + n0 + 4 * k;
+            const long long left = a.N - n0 - 4 * k;
+            if (left >= 4) {
+                q = __ldg(reinterpret_cast<const float4 *>(p));
+            } else {
+                if (left > 0) q.x = __ldg(p);
+                if (left > 1) q.y = __ldg(p + 1);
+                if (left > 2) q.z = __ldg(p + 2);
             }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 32; k++) v[k] = fmaf(e.alpha, v[k], n0 + k < a.N ? __ldg(e.bias + n0 + k) : 0.f);
+            v[4 * k] = fmaf(e.alpha, v[4 * k], q.x);
+            v[4 * k + 1] = fmaf(e.alpha, v[4 * k + 1], q.y);
+            v[4 * k + 2] = fmaf(e.alpha, v[4 * k + 2], q.z);
+            v[4 * k + 3] = fmaf(e.alpha, v[4 * k + 3], q.w);
         }
-    } else {
+    } else if (e.alpha != 1.f) {
 #pragma unroll
-        for (int k = 0; k < 32; k++) v[k] *= e.alpha;
+        for (int k = 0; k < C; k++) v[k] *= e.alpha;
     }
     if (e.preact != nullptr) {
-        if (e.preact_f32) st.tile<float>(a, map_pre, v, m0, n0, 0, (float *)e.preact, a.N);
-        else st.tile<__nv_bfloat16>(a, map_pre, v, m0, n0, 0, (__nv_bfloat16 *)e.preact, a.N);
+        if (e.preact_f32) store_tile<float>((float *)e.preact, a.N, a.M, a.N, v, m0, n0, b);
+        else store_tile<__nv_bfloat16>((__nv_bfloat16 *)e.preact, a.N, a.M, a.N, v, m0, n0, b);
     }
     if (e.act == CSA_ACT_RELU) activate<CSA_ACT_RELU>(v);
     else if (e.act == CSA_ACT_SILU) activate<CSA_ACT_SILU>(v);
     else if (e.act == CSA_ACT_GELU_TANH) activate<CSA_ACT_GELU_TANH>(v);
-    if (e.res != nullptr) res.add_to<O>(v);
-    st.tile<O>(a, map_out, v, m0, n0, 0, (O *)e.out, a.N);
 }
 
 template <int CG, int BN, bool A_K, bool B_K>
 __global__ void __launch_bounds__(THREADS, 1)
 linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                 const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_pre, const Args a)
+                 const __grid_constant__ CUtensorMap map_half, const __grid_constant__ CUtensorMap map_out, const Args a)
 {
-    using C = Cfg<CG, BN>;
-    constexpr int S = C::STAGES;
+    using Z = Cfg<CG, BN>;
+    constexpr int S = Z::STAGES;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = smem_align1024(smem_raw);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::MISC);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Z::MISC);
     uint64_t *full = bars, *empty = bars + S, *t_full = bars + 2 * S, *t_empty = bars + 2 * S + 2, *done = bars + 2 * S + 4;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::MISC + 256);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::MISC + 264);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Z::MISC + 256);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Z::MISC + 264);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
-    const long long u0 = blockIdx.x / CG, ustep = gridDim.x / CG;
+    const int u0 = blockIdx.x / CG, ustep = gridDim.x / CG;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; i++) {
@@ -286,8 +322,8 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         init_fence();
     }
     if (warp == 1) {
-        if constexpr (CG == 2) tmem_alloc_pair(tmem_slot, C::TMEM);
-        else tmem_alloc(tmem_slot, C::TMEM);
+        if constexpr (CG == 2) tmem_alloc_pair(tmem_slot, Z::TMEM);
+        else tmem_alloc(tmem_slot, Z::TMEM);
     }
     fence_before();
     if constexpr (CG == 2) cluster_sync();
@@ -297,41 +333,49 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
 
     if (warp == 0) {
         // ---------------------------------------------------------- TMA producer
+        // Few and large copies: with B in two boxes of 64 rows instead of one of 128 the same product took 164 us
+        // instead of 150 (8192 x 8192 x 2048).
         if (lane == 0) {
             int st = 0;
             uint32_t ph = 0;
             bool wrapped = false;
             int used = 0;
-            for (long long u = u0; u < a.units; u += ustep) {
+            const uint32_t bar0 = CG == 2 ? map_rank(full, 0) : su32(full);  // the barriers are the even CTA's
+            auto load3 = [&](void *to, const CUtensorMap *map, int i, int x, int y, int z) {
+                if constexpr (CG == 2) tma_load_3d_pair(to, map, bar0 + 8 * i, x, y, z);
+                else tma_load_3d(to, map, full + i, x, y, z);
+            };
+            auto load4 = [&](void *to, const CUtensorMap *map, int i, int x, int y, int z, int w) {
+                if constexpr (CG == 2) tma_load_4d_pair(to, map, bar0 + 8 * i, x, y, z, w);
+                else tma_load_4d(to, map, full + i, x, y, z, w);
+            };
+            for (int u = u0; u < a.units; u += ustep) {
                 const Unit x = unit_of<BN>(a, u);
+                const bool half = x.bn != BN;
                 const int am = (x.m * CG + (int)rank) * BM;
                 const int rows_b = x.bn / CG, bn = (int)x.n0 + (int)rank * rows_b;
-                const uint32_t bytes = CG * (C::A_BYTES + rows_b * BK * 2);
+                const uint32_t bytes = CG * (Z::A_BYTES + rows_b * BK * 2);
+                const CUtensorMap *mb = half ? &map_half : &map_b;
                 int q = x.it0 / a.ksteps, k = x.it0 - q * a.ksteps;
                 for (int it = x.it0; it < x.it1; it++) {
                     int pa, pb;
                     planes_of(a.passes, q, pa, pb);
                     wait_bar(empty + st, ph ^ 1, abort_flag, &g_lin_error, 601);
-                    unsigned char *sa = smem + st * C::STAGE, *sb = sa + C::A_BYTES;
-                    if constexpr (CG == 2) {
-                        if (rank == 0) mbar_expect_tx(full + st, bytes);
-                        const uint32_t bar = map_rank(full + st, 0);
-                        if constexpr (A_K) tma_load_3d_pair(sa, &map_a, bar, k * BK, am, pa);
-                        else
-                            for (int i = 0; i < BM / 64; i++) tma_load_3d_pair(sa + i * 8192, &map_a, bar, am + 64 * i, k * BK, pa);
-                        for (int i = 0; i < rows_b; i += 64) {
-                            if constexpr (B_K) tma_load_3d_pair(sb + i * 128, &map_b, bar, k * BK, bn + i, pb);
-                            else tma_load_3d_pair(sb + i * 128, &map_b, bar, bn + i, k * BK, pb);
-                        }
+                    unsigned char *sa = smem + st * Z::STAGE, *sb = sa + Z::A_BYTES;
+                    if (rank == 0) mbar_expect_tx(full + st, bytes);
+                    if constexpr (A_K) {
+                        load3(sa, &map_a, st, k * BK, am, pa);
+                    } else if (a.blocks_a) {
+                        load4(sa, &map_a, st, 0, k * BK, am >> 6, pa);
                     } else {
-                        mbar_expect_tx(full + st, bytes);
-                        if constexpr (A_K) tma_load_3d(sa, &map_a, full + st, k * BK, am, pa);
-                        else
-                            for (int i = 0; i < BM / 64; i++) tma_load_3d(sa + i * 8192, &map_a, full + st, am + 64 * i, k * BK, pa);
-                        for (int i = 0; i < rows_b; i += 64) {
-                            if constexpr (B_K) tma_load_3d(sb + i * 128, &map_b, full + st, k * BK, bn + i, pb);
-                            else tma_load_3d(sb + i * 128, &map_b, full + st, bn + i, k * BK, pb);
-                        }
+                        for (int i = 0; i < BM; i += 64) load3(sa + i * 128, &map_a, st, am + i, k * BK, pa);
+                    }
+                    if constexpr (B_K) {
+                        load3(sb, mb, st, k * BK, bn, pb);
+                    } else if (a.blocks_b) {
+                        load4(sb, mb, st, 0, k * BK, bn >> 6, pb);
+                    } else {
+                        for (int i = 0; i < rows_b; i += 64) load3(sb + i * 128, mb, st, bn + i, k * BK, pb);
                     }
                     if (++k == a.ksteps) {
                         k = 0;
@@ -354,7 +398,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         if (rank == 0) {
             int st = 0, tc = 0;
             uint32_t ph = 0;
-            for (long long u = u0; u < a.units; u += ustep) {
+            for (int u = u0; u < a.units; u += ustep) {
                 const Unit x = unit_of<BN>(a, u);
                 const uint32_t idesc = x.bn == BN ? idesc_bf16(BM * CG, BN, !A_K, !B_K) : idesc_bf16(BM * CG, BN / 2, !A_K, !B_K);
                 const int tb = tc & 1;
@@ -364,7 +408,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                 for (int it = x.it0; it < x.it1; it++) {
                     wait_bar(full + st, ph, abort_flag, &g_lin_error, 603);
                     fence_after();
-                    const unsigned char *sa = smem + st * C::STAGE, *sb = sa + C::A_BYTES;
+                    const unsigned char *sa = smem + st * Z::STAGE, *sb = sa + Z::A_BYTES;
                     // along k (16 values): 32 bytes of a k-major row, 16 rows of 128 bytes of an m/n-major tile
                     const uint64_t da = A_K ? desc_kmajor(sa) : desc_sw128(sa, 8192, 1024);
                     const uint64_t db = B_K ? desc_kmajor(sb) : desc_sw128(sb, 8192, 1024);
@@ -388,47 +432,54 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     } else {
         // ---------------------------------------------------------- epilogue (warps 2..9)
         const int quad = warp & 3;               // TMEM lanes this warp may access
-        const int half = (warp - 2) >> 2;        // half of the columns
-        Store out;
-        out.buf = smem + C::TURN + (warp - 2) * 4096;
-        out.lane = lane;
-        out.turn = 0;
-        out.two = a.splits == 1 && !a.e.out_f32;
-        int tc = 0;
-        for (long long u = u0; u < a.units; u += ustep, tc++) {
-            const Unit x = unit_of<BN>(a, u);
-            const int tb = tc & 1, cols = x.bn / 2;
-            const long long m0 = ((long long)x.m * CG + rank) * BM + quad * 32;
-            const uint32_t t = tmem + (uint32_t)(tb * BN + half * cols) + ((uint32_t)(quad * 32) << 16);
+        const int side = (warp - 2) >> 2;        // half of the columns
+        const Buffer b = {smem + Z::TURN + (warp - 2) * 4096, lane};
+        auto run = [&](auto type) {
+            using O = decltype(type);
+            int tc = 0;
+            for (int u = u0; u < a.units; u += ustep, tc++) {
+                const Unit x = unit_of<BN>(a, u);
+                const int tb = tc & 1, cols = x.bn / 2;
+                const long long m0 = ((long long)x.m * CG + rank) * BM + quad * 32, nb = x.n0 + side * cols;
+                const uint32_t t = tmem + (uint32_t)(tb * BN + side * cols) + ((uint32_t)(quad * 32) << 16);
+                Residual<O> res;
+                auto ask = [&](long long n0) {
+                    if (a.e.res != nullptr && m0 + lane < a.M && n0 < a.N) res.load(a, m0 + lane, n0);
+                };
+                ask(nb);
+                wait_bar(t_full + tb, (tc >> 1) & 1, abort_flag, &g_lin_error, 604);
+                fence_after();
 #pragma unroll 1
-            for (int c = 0; c < cols; c += 32) {
-                const long long n0 = x.n0 + half * cols + c;
-                Residual res;
-                if (a.e.res != nullptr && a.splits == 1 && m0 + lane < a.M && n0 < a.N) {
-                    if (a.e.out_f32) res.load<float>(a, m0 + lane, n0);
-                    else res.load<__nv_bfloat16>(a, m0 + lane, n0);
-                }
-                if (c == 0) {
-                    wait_bar(t_full + tb, (tc >> 1) & 1, abort_flag, &g_lin_error, 604);
-                    fence_after();
-                }
-                float v[32];
-                tmem_ld32(t + c, v);
-                if (c + 32 == cols) {  // the accumulator is in registers: the next tile's MMAs may have it
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (CG == 2) mbar_arrive_cluster(map_rank(t_empty + tb, 0));
-                        else mbar_arrive(t_empty + tb);
+                for (int c = 0; c < cols; c += C) {
+                    const long long n0 = nb + c;
+                    float v[C];
+                    tmem_ld32(t + c, v);
+                    if (c + C == cols) {  // the accumulator is in registers: the next tile's MMAs may have it
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if constexpr (CG == 2) mbar_arrive_cluster(map_rank(t_empty + tb, 0));
+                            else mbar_arrive(t_empty + tb);
+                        }
+                    }
+                    if (m0 >= a.M || n0 >= a.N) continue;
+                    to_activation(a, v, m0, n0, b);
+                    if (a.e.res != nullptr) {
+                        res.add_to(v);
+                        if (c + C < cols) ask(n0 + C);
+                    }
+                    if (a.tma_out) {
+                        const bool second = sizeof(O) == 2 && (c & C) != 0;
+                        tma_tile<O>(&map_out, v, m0, n0, x.s, second, sizeof(O) == 4 || second || n0 + C >= a.N, b);
+                    } else {
+                        store_tile<O>((O *)a.e.out + (long long)x.s * a.M * a.ldo, a.ldo, a.M, a.N, v, m0, n0, b);
                     }
                 }
-                if (m0 >= a.M || n0 >= a.N) continue;
-                if (a.splits > 1) out.tile<float>(a, &map_out, v, m0, n0, x.s, nullptr, 0);
-                else if (a.e.out_f32) finish<float>(a, &map_out, &map_pre, out, v, res, m0, n0);
-                else finish<__nv_bfloat16>(a, &map_out, &map_pre, out, v, res, m0, n0);
             }
-        }
-        if (lane == 0) bulk_wait<0>();
+        };
+        if (a.e.out_f32) run(float());
+        else run(__nv_bfloat16());
+        if (lane == 0) bulk_wait();
     }
     __syncwarp();
     fence_before();
@@ -436,8 +487,8 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     else __syncthreads();
     fence_after();
     if (warp == 1) {
-        if constexpr (CG == 2) tmem_dealloc_pair(tmem, C::TMEM);
-        else tmem_dealloc(tmem, C::TMEM);
+        if constexpr (CG == 2) tmem_dealloc_pair(tmem, Z::TMEM);
+        else tmem_dealloc(tmem, Z::TMEM);
     }
 }
 
@@ -474,18 +525,22 @@ int product_splits(long long M, long long N, long long K, int planes, int sms)
     return (int)((steps + per - 1) / per);  // no piece is empty
 }
 
+struct Maps {
+    CUtensorMap a, b, half, out;
+};
+
 template <int CG, int BN, bool A_K, bool B_K>
-static cudaError_t launch(const CUtensorMap (&map)[4], const Args &a, int sms, cudaStream_t st)
+static cudaError_t launch(const Maps &m, const Args &a, int sms, cudaStream_t st)
 {
-    using C = Cfg<CG, BN>;
+    using Z = Cfg<CG, BN>;
     auto *kernel = linear_tc_kernel<CG, BN, A_K, B_K>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::SMEM);
     if (e != cudaSuccess) return e;
-    const long long slots = sms / CG;
+    const int slots = sms / CG;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((a.units < slots ? a.units : slots) * CG));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.dynamicSmemBytes = Z::SMEM;
     cfg.stream = st;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -493,38 +548,43 @@ static cudaError_t launch(const CUtensorMap (&map)[4], const Args &a, int sms, c
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = CG == 2 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, kernel, map[0], map[1], map[2], map[3], a);
+    e = cudaLaunchKernelEx(&cfg, kernel, m.a, m.b, m.half, m.out, a);
     if (e == cudaSuccess) note_launches(1);
     return e;
 }
 
 template <int CG, int BN>
-static cudaError_t launch_majors(const Product &p, const CUtensorMap (&map)[4], const Args &a, int sms, cudaStream_t st)
+static cudaError_t launch_majors(const Product &p, const Maps &m, const Args &a, int sms, cudaStream_t st)
 {
-    if (p.a.k_major) return p.b.k_major ? launch<CG, BN, true, true>(map, a, sms, st) : launch<CG, BN, true, false>(map, a, sms, st);
-    return launch<CG, BN, false, false>(map, a, sms, st);
+    if (p.a.k_major) return p.b.k_major ? launch<CG, BN, true, true>(m, a, sms, st) : launch<CG, BN, true, false>(m, a, sms, st);
+    return launch<CG, BN, false, false>(m, a, sms, st);
 }
 
-// The outputs' tiles: `n` values a row, rows `ld` apart, `z` matrices of M rows.
+// Boxes of `rows` m or n indices and 64 values of k of an operand with `n` of them.  {contiguous, strided, plane}; an
+// m/n-contiguous operand of whole 64-wide blocks has these as an axis of their own (one copy then brings several).
+static bool encode(CUtensorMap *m, const Operand &o, long long n, long long K, int planes, int rows, bool blocks)
+{
+    const long long inner = o.k_major ? K : n, outer = o.k_major ? n : K;
+    // one plane: its stride is never used, but has to be a legal one (below 2^40 bytes)
+    const long long far = 1LL << 38, whole = outer > far / o.ld ? far : outer * o.ld;
+    const cuuint64_t ld = (cuuint64_t)o.ld * 2, plane = (cuuint64_t)(planes > 1 ? o.plane : whole) * 2;
+    if (blocks) {
+        const cuuint64_t dims[4] = {64, (cuuint64_t)K, (cuuint64_t)(n / 64), (cuuint64_t)planes}, strides[3] = {ld, 128, plane};
+        const cuuint32_t box[4] = {64, 64, (cuuint32_t)(rows / 64), 1};
+        return tc_encode_bf16(m, o.base, 4, dims, strides, box);
+    }
+    const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)outer, (cuuint64_t)planes}, strides[2] = {ld, plane};
+    const cuuint32_t box[3] = {64, (cuuint32_t)(o.k_major ? rows : 64), 1};
+    return tc_encode_bf16(m, o.base, 3, dims, strides, box);
+}
+
+// An output of M rows of n values, `ld` apart, z of them.
 static bool encode_out(CUtensorMap *m, bool f32, const void *base, long long n, long long ld, long long M, int z)
 {
     const long long size = f32 ? 4 : 2;
     const cuuint64_t dims[3] = {(cuuint64_t)n, (cuuint64_t)M, (cuuint64_t)z};
     const cuuint64_t strides[2] = {(cuuint64_t)(ld * size), (cuuint64_t)(M * ld * size)};
-    const cuuint32_t box[3] = {32, 32, 1};
-    return tc_encode_store(m, f32, base, 3, dims, strides, box);
-}
-
-// A map over {contiguous, strided, plane} of an operand of `n` rows (m or n) and K; boxes of 64 contiguous values.
-static bool encode(CUtensorMap *m, const Operand &o, long long n, long long K, int planes, int rows)
-{
-    const long long inner = o.k_major ? K : n, outer = o.k_major ? n : K;
-    const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)outer, (cuuint64_t)planes};
-    // one plane: its stride is never used, but has to be a legal one (below 2^40 bytes)
-    const long long far = 1LL << 38, whole = outer > far / o.ld ? far : outer * o.ld;
-    const cuuint64_t strides[2] = {(cuuint64_t)o.ld * 2, (cuuint64_t)(planes > 1 ? o.plane : whole) * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)(o.k_major ? rows : 64), 1};
-    return tc_encode_bf16(m, o.base, 3, dims, strides, box);
+    return tc_encode_store(m, f32, base, dims, strides);
 }
 
 cudaError_t launch_product_tc(const Product &p, int sms, cudaStream_t st)
@@ -539,29 +599,37 @@ cudaError_t launch_product_tc(const Product &p, int sms, cudaStream_t st)
     a.per_split = (steps + p.splits - 1) / p.splits;
     a.splits = p.splits;
     tile_counts(s, p.M, p.N, a.mt, a.nt);
-    a.units = a.whole = (long long)a.mt * a.nt * p.splits;
-    const long long slots = sms / 2, rest = a.units % slots;
-    if (s == PAIR_256 && p.splits == 1 && a.units > slots && rest > 0 && 2 * rest <= slots) {
-        a.whole -= rest;
-        a.units += rest;
+    const long long units = (long long)a.mt * a.nt * p.splits, slots = sms / 2, rest = units % slots;
+    if (units > 0x3fffffffLL || (long long)BAND * a.nt > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
+    a.units = a.whole = (int)units;
+    if (s == PAIR_256 && p.splits == 1 && units > slots && rest > 0 && 2 * rest <= slots) {
+        a.whole -= (int)rest;
+        a.units += (int)rest;
     }
     a.e = p.e;
-    CUtensorMap map[4];
-    memset(map, 0, sizeof map);
-    if (!encode(&map[0], p.a, p.M, p.K, p.planes, BM) || !encode(&map[1], p.b, p.N, p.K, p.planes, 64)) return cudaErrorInvalidValue;
-    if (p.splits > 1) {
-        a.tma_out = 1;
-        if (!encode_out(&map[2], true, p.e.partial, p.N, partial_stride(p.N), p.M, p.splits)) return cudaErrorInvalidValue;
-    } else {
-        a.tma_out = p.N % (p.e.out_f32 ? 4 : 8) == 0 && (p.e.preact == nullptr || p.N % (p.e.preact_f32 ? 4 : 8) == 0);
-        if (a.tma_out) {
-            if (!encode_out(&map[2], p.e.out_f32, p.e.out, p.N, p.N, p.M, 1)) return cudaErrorInvalidValue;
-            if (p.e.preact != nullptr && !encode_out(&map[3], p.e.preact_f32, p.e.preact, p.N, p.N, p.M, 1)) return cudaErrorInvalidValue;
-        }
+    a.ldo = p.N;
+    if (p.splits > 1) {  // bare fp32 sums, piece by piece
+        a.e = Epilogue();
+        a.e.alpha = 1.f;
+        a.e.out = p.e.partial;
+        a.e.out_f32 = 1;
+        a.ldo = partial_stride(p.N);
     }
-    if (s == LONE_64) return launch_majors<1, 64>(p, map, a, sms, st);
-    if (s == PAIR_128) return launch_majors<2, 128>(p, map, a, sms, st);
-    return launch_majors<2, 256>(p, map, a, sms, st);
+    a.res32 = (reinterpret_cast<uintptr_t>(a.e.res) & 31) == 0 && a.e.ldr % (a.e.out_f32 ? 8 : 16) == 0;
+    // a warp of the 128 x 64 tile has half a row of bf16 columns; a kept z off the sectors needs the buffer for itself
+    a.tma_out = s != LONE_64 && a.ldo % (a.e.out_f32 ? 4 : 8) == 0 && 
+                (a.e.preact == nullptr || (p.N % (a.e.preact_f32 ? 8 : 16) == 0 && (reinterpret_cast<uintptr_t>(a.e.preact) & 31) == 0));
+    a.blocks_a = !p.a.k_major && p.M % 64 == 0;
+    a.blocks_b = !p.b.k_major && p.N % 64 == 0;
+    Maps m = {};
+    const int rows_b = s == PAIR_256 ? 128 : 64;
+    bool ok = encode(&m.a, p.a, p.M, p.K, p.planes, BM, a.blocks_a) && encode(&m.b, p.b, p.N, p.K, p.planes, rows_b, a.blocks_b);
+    if (a.units > a.whole) ok = ok && encode(&m.half, p.b, p.N, p.K, p.planes, rows_b / 2, a.blocks_b);
+    if (a.tma_out) ok = ok && encode_out(&m.out, a.e.out_f32, a.e.out, p.N, a.ldo, p.M, p.splits);
+    if (!ok) return cudaErrorInvalidValue;
+    if (s == LONE_64) return launch_majors<1, 64>(p, m, a, sms, st);
+    if (s == PAIR_128) return launch_majors<2, 128>(p, m, a, sms, st);
+    return launch_majors<2, 256>(p, m, a, sms, st);
 }
 
 }  // namespace linear

@@ -1054,15 +1054,13 @@ bool tc_encode_bf16(CUtensorMap *m, const void *base, int rank, const cuuint64_t
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool tc_encode_store(CUtensorMap *m, bool f32, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
-                     const cuuint32_t *box)
+bool tc_encode_store(CUtensorMap *m, bool f32, const void *base, const cuuint64_t *dims, const cuuint64_t *strides)
 {
     auto fn = encode_fn();
     if (fn == nullptr) return false;
-    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
-    return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims,
-              strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+    const cuuint32_t es[3] = {1, 1, 1}, box[3] = {f32 ? 32u : 64u, 32, 1};
+    return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims,
+              strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

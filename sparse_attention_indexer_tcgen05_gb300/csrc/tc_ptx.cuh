@@ -141,8 +141,8 @@ __device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, u
                  : "memory");
 }
 
-// Shared memory -> global, in this thread's bulk group; the group's commit and the wait until all but the n most
-// recent groups have been read (so that their shared memory may be written) or written.
+// Shared memory -> global, in this thread's bulk group; the group's commit and the waits until its groups' shared
+// memory has been read (and may be written again), or until they are done.
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int x, int y, int z)
 {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
@@ -150,8 +150,8 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void 
                  : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
-template <int N> __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Shared-memory matrix descriptor, 128-byte swizzle, version 1 (bits 46-47), layout SWIZZLE_128B (bits 61-63 = 2).
 //   K-major:  rows of 128 B (64 bf16 of K) per M/N index, 8-row atoms of 1024 B: SBO = 1024 B; LBO unused.
@@ -387,6 +387,14 @@ __device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *m
     asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
                  "[%1, {%3, %4, %5}], [%2];"
                  ::"r"(su32(dst)), "l"(map), "r"(bar_cluster), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_load_4d_pair(void *dst, const CUtensorMap *map, uint32_t bar_cluster, int x, int y,
+                                                 int z, int w)
+{
+    asm volatile("cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+                 "[%1, {%3, %4, %5, %6}], [%2];"
+                 ::"r"(su32(dst)), "l"(map), "r"(bar_cluster), "r"(x), "r"(y), "r"(z), "r"(w)
                  : "memory");
 }
 // Four MMAs of K = 16 of a pair (as mma4_ss_w), then a commit that arrives on the barrier at the offset of `bar` in
