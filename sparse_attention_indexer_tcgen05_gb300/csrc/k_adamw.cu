@@ -14,6 +14,7 @@
 // copy, no device table that must outlive the call, any stream capture keeps them); a CTA finds its tensor by a
 // binary search over the first chunk of each.
 #include "csa_internal.cuh"
+#include "tc_ptx.cuh"
 
 #include <cuda_fp8.h>
 #include <math.h>
@@ -21,8 +22,12 @@
 namespace csa {
 namespace adamw {
 
+using ptx::add2;
+using ptx::fma2;
+using ptx::mul2;
+
 constexpr int THREADS = 128;
-constexpr int VEC = 8;                         // elements per lane: one warp covers a block of 256
+constexpr int VEC = 8, PAIRS = VEC / 2;        // elements per lane: one warp covers a block of 256
 constexpr int CHUNK = THREADS * VEC;           // elements per CTA
 constexpr float E4M3_MAX = 448.f;
 constexpr float E4M3_TINY = 0.001953125f;      // 2^-9
@@ -51,48 +56,50 @@ template <int CAP> struct Table {
 };
 
 // 8 values from p (element i, n - i of them valid)
-template <typename T> __device__ __forceinline__ void load8(const T *p, long long i, long long n, float (&x)[VEC])
+template <typename T> __device__ __forceinline__ void load8(const T *p, long long i, long long n, float2 (&x)[PAIRS])
 {
     if (i + VEC <= n) {
         if constexpr (sizeof(T) == 4) {
             const float4 a = __ldcs(reinterpret_cast<const float4 *>(p + i));
             const float4 b = __ldcs(reinterpret_cast<const float4 *>(p + i) + 1);
-            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-            x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+            x[0] = make_float2(a.x, a.y);
+            x[1] = make_float2(a.z, a.w);
+            x[2] = make_float2(b.x, b.y);
+            x[3] = make_float2(b.z, b.w);
         } else {
             const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p + i));
             const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
-                x[2 * k] = __uint_as_float(w[k] << 16);
-                x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-            }
+            for (int k = 0; k < PAIRS; k++) x[k] = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < VEC; k++) x[k] = i + k < n ? ldf<T>(p, i + k) : 0.f;
+        for (int k = 0; k < PAIRS; k++)
+            x[k] = make_float2(i + 2 * k < n ? ldf<T>(p, i + 2 * k) : 0.f, i + 2 * k + 1 < n ? ldf<T>(p, i + 2 * k + 1) : 0.f);
     }
 }
 
-template <typename T> __device__ __forceinline__ void store8(T *p, long long i, long long n, const float (&x)[VEC])
+template <typename T> __device__ __forceinline__ void store8(T *p, long long i, long long n, const float2 (&x)[PAIRS])
 {
     if (i + VEC <= n) {
         if constexpr (sizeof(T) == 4) {
-            __stcs(reinterpret_cast<float4 *>(p + i), make_float4(x[0], x[1], x[2], x[3]));
-            __stcs(reinterpret_cast<float4 *>(p + i) + 1, make_float4(x[4], x[5], x[6], x[7]));
+            __stcs(reinterpret_cast<float4 *>(p + i), make_float4(x[0].x, x[0].y, x[1].x, x[1].y));
+            __stcs(reinterpret_cast<float4 *>(p + i) + 1, make_float4(x[2].x, x[2].y, x[3].x, x[3].y));
         } else {
             uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; k++) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+                const __nv_bfloat162 b = __floats2bfloat162_rn(x[k].x, x[k].y);
                 w[k] = *reinterpret_cast<const uint32_t *>(&b);
             }
             __stcs(reinterpret_cast<uint4 *>(p + i), make_uint4(w[0], w[1], w[2], w[3]));
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < VEC; k++)
-            if (i + k < n) p[i + k] = from_f<T>(x[k]);
+        for (int k = 0; k < PAIRS; k++) {
+            if (i + 2 * k < n) p[i + 2 * k] = from_f<T>(x[k].x);
+            if (i + 2 * k + 1 < n) p[i + 2 * k + 1] = from_f<T>(x[k].y);
+        }
     }
 }
 
@@ -119,24 +126,23 @@ __device__ __forceinline__ void store_codes(void *p, long long i, long long n, u
         if (i + k < n) c[i + k] = (unsigned char)((k < 4 ? r.x : r.y) >> (8 * (k & 3)));
 }
 
-__device__ __forceinline__ void decode8(uint2 r, float scale, float (&x)[VEC])
+__device__ __forceinline__ void decode8(uint2 r, float scale, float2 (&x)[PAIRS])
 {
 #pragma unroll
     for (int k = 0; k < 4; k++) {
         const __nv_fp8x2_storage_t c = (__nv_fp8x2_storage_t)(((k < 2 ? r.x : r.y) >> (16 * (k & 1))) & 0xffffu);
         const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3);
         const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-        x[2 * k] = f.x * scale;
-        x[2 * k + 1] = f.y * scale;
+        x[k] = mul2(f, make_float2(scale, scale));
     }
 }
 
-__device__ __forceinline__ uint2 encode8(const float (&x)[VEC])
+__device__ __forceinline__ uint2 encode8(const float2 (&x)[PAIRS])
 {
     uint32_t w[4];
 #pragma unroll
     for (int k = 0; k < 4; k++)
-        w[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[2 * k], x[2 * k + 1]), __NV_SATFINITE, __NV_E4M3);
+        w[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(x[k], __NV_SATFINITE, __NV_E4M3);
     return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
@@ -144,34 +150,36 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[VEC])
 // with the residual v - r^2 taken exactly by a fused multiply-add (Markstein, IBM J. Res. Dev. 34, 1990).  Values
 // outside the normal range take the library's root.  (The library's for all of them: 170 us of 1220 us for the 412
 // million elements below.)
-__device__ __forceinline__ void roots(const float (&v)[VEC], float (&r)[VEC])
+__device__ __forceinline__ void roots(const float2 (&v)[PAIRS], float2 (&r)[PAIRS])
 {
-    float lo = v[0], hi = v[0];
+    float lo = v[0].x, hi = v[0].x;
 #pragma unroll
-    for (int k = 1; k < VEC; k++) {
-        lo = fminf(lo, v[k]);
-        hi = fmaxf(hi, v[k]);
+    for (int k = 0; k < PAIRS; k++) {
+        lo = fminf(lo, fminf(v[k].x, v[k].y));
+        hi = fmaxf(hi, fmaxf(v[k].x, v[k].y));
     }
     if (lo >= 1.17549435e-38f && hi <= 3.40282347e38f) {
 #pragma unroll
-        for (int k = 0; k < VEC; k++) {
-            float y;
-            asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v[k]));
-            const float r0 = __fmul_rn(v[k], y);
-            r[k] = fmaf(fmaf(-r0, r0, v[k]), 0.5f * y, r0);
+        for (int k = 0; k < PAIRS; k++) {
+            float2 y;
+            asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(v[k].x));
+            asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(v[k].y));
+            const float2 r0 = mul2(v[k], y);
+            const float2 e = fma2(make_float2(-r0.x, -r0.y), r0, v[k]);
+            r[k] = fma2(e, mul2(y, make_float2(0.5f, 0.5f)), r0);
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < VEC; k++) r[k] = __fsqrt_rn(v[k]);
+        for (int k = 0; k < PAIRS; k++) r[k] = make_float2(__fsqrt_rn(v[k].x), __fsqrt_rn(v[k].y));
     }
 }
 
 // x / d with y = 1 / d rounded: the product corrected by its exact residual (the same source), so that a code does not
 // depend on y's last bit.
-__device__ __forceinline__ float quotient(float x, float d, float y)
+__device__ __forceinline__ float2 quotient(float2 x, float d, float y)
 {
-    const float q = __fmul_rn(x, y);
-    return fmaf(fmaf(-q, d, x), y, q);
+    const float2 yy = make_float2(y, y), q = mul2(x, yy);
+    return fma2(fma2(q, make_float2(-d, -d), x), yy, q);
 }
 
 template <typename PT, typename GT, bool E4M3, int CAP>
@@ -204,7 +212,7 @@ __global__ void __launch_bounds__(THREADS, 12) adamw_kernel(const __grid_constan
     const GT *grad = static_cast<const GT *>(e.grad);
 
     if ((i & ~(long long)(CSA_ADAMW_BLOCK - 1)) >= n) return;  // the whole warp lies behind the end
-    float p[VEC], g[VEC], m[VEC], v[VEC];
+    float2 p[PAIRS], g[PAIRS], m[PAIRS], v[PAIRS];
     const long long blk = i / CSA_ADAMW_BLOCK;  // the same for the whole warp
     load8<GT>(grad, i, n, g);
     if constexpr (E4M3) {
@@ -214,27 +222,34 @@ __global__ void __launch_bounds__(THREADS, 12) adamw_kernel(const __grid_constan
         decode8(cm, sm, m);
         decode8(cv, sv, v);
 #pragma unroll
-        for (int k = 0; k < VEC; k++) v[k] *= v[k];
+        for (int k = 0; k < PAIRS; k++) v[k] = mul2(v[k], v[k]);
     } else {
         load8<float>(static_cast<const float *>(e.m), i, n, m);
         load8<float>(static_cast<const float *>(e.v), i, n, v);
         if (e.master != nullptr) load8<float>(e.master, i, n, p); else load8<PT>(param, i, n, p);
     }
-    float r[VEC], top_m = 0.f, top_r = 0.f;
+    // The moments as the formula has them, each operation rounded: an 8-bit code then depends on the tensors alone.
+    // (Not in pairs: a paired product and a paired sum were joined into one rounding.)
+    const auto both = [](float x) { return make_float2(x, x); };
+    const auto blend = [](float b, float old, float nb, float x) { return __fadd_rn(__fmul_rn(b, old), __fmul_rn(nb, x)); };
 #pragma unroll
-    for (int k = 0; k < VEC; k++) {
-        // the moments and the root as the formula has them, each operation rounded: an 8-bit code then depends on the
-        // tensors alone and not on how a compiler joins multiplications and additions
-        const float gk = __fmul_rn(g[k], gs);
-        m[k] = __fadd_rn(__fmul_rn(h.b1, m[k]), __fmul_rn(h.nb1, gk));
-        v[k] = __fadd_rn(__fmul_rn(h.b2, v[k]), __fmul_rn(__fmul_rn(h.nb2, gk), gk));
+    for (int k = 0; k < PAIRS; k++) {
+        const float2 gk = mul2(g[k], both(gs));
+        m[k] = make_float2(blend(h.b1, m[k].x, h.nb1, gk.x), blend(h.b1, m[k].y, h.nb1, gk.y));
+        // (1 - b2) g g from the left
+        v[k].x = __fadd_rn(__fmul_rn(h.b2, v[k].x), __fmul_rn(__fmul_rn(h.nb2, gk.x), gk.x));
+        v[k].y = __fadd_rn(__fmul_rn(h.b2, v[k].y), __fmul_rn(__fmul_rn(h.nb2, gk.y), gk.y));
     }
+    float2 r[PAIRS];
     roots(v, r);
+    float top_m = 0.f, top_r = 0.f;
 #pragma unroll
-    for (int k = 0; k < VEC; k++) {
-        p[k] = fmaf(-lr_wd, p[k], p[k]) - c1 * __fdividef(m[k], fmaf(r[k], rs2, h.eps));
-        top_m = fmaxf(top_m, fabsf(m[k]));
-        top_r = fmaxf(top_r, r[k]);
+    for (int k = 0; k < PAIRS; k++) {
+        const float2 d = fma2(r[k], both(rs2), both(h.eps));
+        const float2 step = make_float2(__fdividef(m[k].x, d.x), __fdividef(m[k].y, d.y));
+        p[k] = fma2(both(-c1), step, fma2(both(-lr_wd), p[k], p[k]));
+        top_m = fmaxf(top_m, fmaxf(fabsf(m[k].x), fabsf(m[k].y)));
+        top_r = fmaxf(top_r, fmaxf(r[k].x, r[k].y));
     }
     if (e.master != nullptr) store8<float>(e.master, i, n, p);
     store8<PT>(param, i, n, p);
@@ -245,10 +260,11 @@ __global__ void __launch_bounds__(THREADS, 12) adamw_kernel(const __grid_constan
         // a block of magnitudes below 448e-36 keeps the codes of zeros (its reciprocal would leave the normal range)
         const float ym = sm >= 1e-36f ? 1.f / sm : 0.f, yr = sr >= 1e-36f ? 1.f / sr : 0.f;
 #pragma unroll
-        for (int k = 0; k < VEC; k++) {
+        for (int k = 0; k < PAIRS; k++) {
             m[k] = quotient(m[k], sm, ym);
-            const float c = quotient(r[k], sr, yr);
-            v[k] = r[k] > 0.f && !(c > E4M3_TINY) ? E4M3_TINY : c;
+            const float2 c = quotient(r[k], sr, yr);
+            v[k].x = r[k].x > 0.f ? fmaxf(c.x, E4M3_TINY) : c.x;  // keeps NaN
+            v[k].y = r[k].y > 0.f ? fmaxf(c.y, E4M3_TINY) : c.y;
         }
         store_codes(e.m, i, n, encode8(m));
         store_codes(e.v, i, n, encode8(v));
