@@ -464,7 +464,15 @@ def csa_indexer_loss(q_idx, w, k_idx, q, kv, kv_c, sink, params: Params):
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _push, _pop = torch.cuda.nvtx.range_push, torch.cuda.nvtx.range_pop
-_current_device = torch.cuda.current_device
+_current_device = torch._C._cuda_getDevice
+# torch's allocation without its dispatcher (on the current device), 4 us less in a call; not every build has it
+_quick_empty = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+
+
+def _empty(shape, strides, dtype, index):
+    if _quick_empty is not None and _current_device() == index:
+        return _quick_empty(shape, strides, dtype)
+    return torch.empty_strided(shape, strides, dtype=dtype, device=torch.device("cuda", index))
 
 
 def _invoke(name, fn, device_index, *args):
@@ -581,13 +589,13 @@ def csa_linear_fwd(p: LinearParams, x, weight, bias=None, residual=None, workspa
     if residual is not None:
         _check_rows(residual, "residual", p.out_value_dtype, dev, M, N, c.residual_stride)
     if out is None:
-        out = x.new_empty((M, N), dtype=p.out_value_dtype)
+        out = _empty((M, N), (N, 1), p.out_value_dtype, dev)
     else:
         _check_flat(out, "out", p.out_value_dtype, dev, M * N)
     if preact is not None:
         _check_flat(preact, "preact", p.value_dtype, dev, M * N)
     if workspace is None:
-        workspace = x.new_empty(p.fwd_workspace_bytes, dtype=torch.uint8)
+        workspace = _empty((p.fwd_workspace_bytes,), (1,), torch.uint8, dev)
     ws, nws = _check_workspace(workspace, dev)
     _invoke("csa_linear_fwd", _lib.csa_linear_fwd, dev, p.ref, x.data_ptr(), weight.data_ptr(), _ptr(bias),
             _ptr(residual), out.data_ptr(), _ptr(preact), ws, nws)
@@ -611,17 +619,17 @@ def csa_linear_bwd(p: LinearParams, dy, x, weight, preact=None, need_dx=True, ne
     else:
         preact = None
 
-    def output(i, name, shape, dtype, numel):
+    def output(i, name, shape, strides, dtype, numel):
         if out is None or out[i] is None:
-            return dy.new_empty(shape, dtype=dtype)
+            return _empty(shape, strides, dtype, dev)
         _check_flat(out[i], name, dtype, dev, numel)
         return out[i]
 
-    dx = output(0, "dx", (M, K), p.value_dtype, M * K) if need_dx else None
-    dw = output(1, "dw", (N, K), p.value_dtype, N * K) if need_dw else None
-    db = output(2, "db", (N,), torch.float32, N) if need_db else None
+    dx = output(0, "dx", (M, K), (K, 1), p.value_dtype, M * K) if need_dx else None
+    dw = output(1, "dw", (N, K), (K, 1), p.value_dtype, N * K) if need_dw else None
+    db = output(2, "db", (N,), (1,), torch.float32, N) if need_db else None
     if workspace is None:
-        workspace = dy.new_empty(p.bwd_workspace_bytes, dtype=torch.uint8)
+        workspace = _empty((p.bwd_workspace_bytes,), (1,), torch.uint8, dev)
     ws, nws = _check_workspace(workspace, dev)
     _invoke("csa_linear_bwd", _lib.csa_linear_bwd, dev, p.ref, dy.data_ptr(), _ptr(x), _ptr(weight), _ptr(preact),
             _ptr(dx), _ptr(dw), _ptr(db), ws, nws)
@@ -688,7 +696,8 @@ def csa_rope(p: RopeParams, x, positions, inv_freq, out=None):
     if out is None:
         if c.out_row_stride or c.out_head_stride:
             raise ValueError("out is required where RopeParams gives its strides")
-        out = x.new_empty(x.shape)
+        out = _empty(tuple(x.shape), x.stride(), x.dtype, dev) if x.is_contiguous() else \
+            _empty((c.rows, c.heads, c.head_dim), (c.heads * c.head_dim, c.head_dim, 1), x.dtype, dev)
     else:
         _check_heads(out, "out", p, dev, c.out_row_stride, c.out_head_stride)
     _invoke("csa_rope", _lib.csa_rope, dev, p.ref, x.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), out.data_ptr())
