@@ -35,14 +35,14 @@ template <typename V> __device__ __forceinline__ void put_planes(bf16 *out, long
     }
 }
 
-// rows x cols values, rows `stride` apart -> planes of rows `ld` apart
-template <typename V>
-__global__ void stage_kernel(const V *x, long long stride, long long rows, int cols, bf16 *out, long long ld, long long plane)
-{
-    for (long long r = blockIdx.y; r < rows; r += gridDim.y)
-        for (int c = blockIdx.x * blockDim.x + threadIdx.x; c < cols; c += gridDim.x * blockDim.x)
-            put_planes<V>(out, plane, r * ld + c, ldf<V>(x, r * stride + c));
-}
+// What a staged operand is made of: rows x cols values, rows `stride` apart -> planes of rows `ld` apart.
+struct Stage {
+    const void *x;
+    bf16 *out;
+    long long stride, rows, ld, plane;
+    int cols, vec;       // vec: whole vectors of 8, aligned
+    unsigned blocks;     // of 256 threads, 8 values each
+};
 
 // 8 columns of one row: V neighbours from n on where V = 8, else every TX-th from n on; 0 behind the end.
 template <typename T, int V, int TX> __device__ __forceinline__ void load_cols(const T *row, int n, int N, float (&x)[8])
@@ -84,12 +84,47 @@ template <typename V> __device__ __forceinline__ void put_planes8(bf16 *out, lon
     for (int q = 0; q < P; q++) *reinterpret_cast<uint4 *>(out + q * plane + at) = *reinterpret_cast<const uint4 *>(w[q]);
 }
 
+// Up to two operands in one launch.
+template <typename V> __global__ void __launch_bounds__(256) stage_kernel(const Stage s0, const Stage s1)
+{
+    const Stage &s = blockIdx.x < s0.blocks ? s0 : s1;
+    const long long t = ((long long)(blockIdx.x - (blockIdx.x < s0.blocks ? 0u : s0.blocks)) * 256 + threadIdx.x) * (s.vec ? 8 : 1);
+    const V *x = static_cast<const V *>(s.x);
+    if (s.vec) {
+        const long long r = t / s.cols, c = t - r * s.cols;
+        if (r >= s.rows) return;
+        float v[8];
+        load_cols<V, 8, 1>(x + r * s.stride, (int)c, s.cols, v);
+        put_planes8<V>(s.out, s.plane, r * s.ld + c, v);
+    } else {
+        // 8 values a thread, 256 apart
+        const long long first = (t / 256) * 2048 + t % 256;
+        long long r = first / s.cols;
+        int c = (int)(first - r * s.cols);
+        float v[8];
+        long long at[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            at[k] = r < s.rows ? r * s.ld + c : -1;
+            v[k] = r < s.rows ? ldf<V>(x, r * s.stride + c) : 0.f;
+            c += 256;
+            while (c >= s.cols) {
+                c -= s.cols;
+                r++;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            if (at[k] >= 0) put_planes<V>(s.out, s.plane, at[k], v[k]);
+    }
+}
+
 // dz = dy act'(z) for `per` rows of a block and 8 TX columns, and their column sums for db.  Bound by memory: dy and
 // z are read once, dz is written once.  VEC: 8 neighbouring columns a thread (16-byte accesses), where the row strides
-// allow it.  One row of a thread in flight and 6 CTAs on an SM: with two rows and the registers of 3 CTAs, db alone of
-// 8192 x 8192 values took 52 us instead of 28, with silu 80 instead of 76.
-template <typename V, typename O, int TX, bool VEC>
-__global__ void __launch_bounds__(256, 6)
+// allow it.  ROWS of a thread are in flight together: two with an activation, one (and twice the CTAs on an SM) without:
+// db alone of 8192 x 8192 values takes 28 us so, and 52 with two.
+template <typename V, typename O, int TX, bool VEC, int ROWS>
+__global__ void __launch_bounds__(256, ROWS == 1 ? 6 : 3)
 dz_kernel(const O *dy, long long ldy, const V *z, int act, bf16 *dz, long long ld, long long plane, float *sums,
           long long M, int N, int per)
 {
@@ -100,23 +135,31 @@ dz_kernel(const O *dy, long long ldy, const V *z, int act, bf16 *dz, long long l
     const long long r0 = (long long)blockIdx.y * per, r1 = min(M, r0 + per);
     float s[8] = {};
     if (n < N) {
-        for (long long r = r0 + ty; r < r1; r += TY) {
-            float d[8], q[8];
-            load_cols<O, W, TX>(dy + r * ldy, n, N, d);
-            if (act != CSA_ACT_NONE) load_cols<V, W, TX>(z + r * N, n, N, q);
+        for (long long r = r0 + ty; r < r1; r += TY * ROWS) {
+            float d[ROWS][8], q[ROWS][8];
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                // rounded before it is added, whichever outputs are asked for
-                if (act != CSA_ACT_NONE) d[j] = __fmul_rn(d[j], act_grad(q[j], act));
-                s[j] += d[j];
-            }
-            if (dz == nullptr) continue;
-            if constexpr (VEC) {
-                put_planes8<V>(dz, plane, r * ld + n, d);
-            } else {
+            for (int i = 0; i < ROWS; i++)
+                if (r + TY * i < r1) {
+                    load_cols<O, W, TX>(dy + (r + TY * i) * ldy, n, N, d[i]);
+                    if (act != CSA_ACT_NONE) load_cols<V, W, TX>(z + (r + TY * i) * N, n, N, q[i]);
+                }
 #pragma unroll
-                for (int j = 0; j < 8; j++)
-                    if (n + TX * j < N) put_planes<V>(dz, plane, r * ld + n + TX * j, d[j]);
+            for (int i = 0; i < ROWS; i++) {
+                if (r + TY * i >= r1) break;
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    // rounded before it is added, whichever outputs are asked for
+                    if (act != CSA_ACT_NONE) d[i][j] = __fmul_rn(d[i][j], act_grad(q[i][j], act));
+                    s[j] += d[i][j];
+                }
+                if (dz == nullptr) continue;
+                if constexpr (VEC) {
+                    put_planes8<V>(dz, plane, (r + TY * i) * ld + n, d[i]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; j++)
+                        if (n + TX * j < N) put_planes<V>(dz, plane, (r + TY * i) * ld + n + TX * j, d[i][j]);
+                }
             }
         }
     }
@@ -148,42 +191,48 @@ __global__ void __launch_bounds__(256) db_kernel(const float *sums, int blocks, 
     }
 }
 
-// The pieces of a split k axis joined, V columns a thread, and the epilogue.
-template <int V>
+// The pieces of a split k axis joined, 4 columns a thread, and the epilogue.  VEC: rows of y, preact and the residual
+// hold whole vectors of 4.
+template <bool VEC>
 __global__ void __launch_bounds__(256) join_kernel(const float *partial, int splits, long long M, long long N, const Epilogue e)
 {
     const long long ldp = partial_stride(N), t = (long long)blockIdx.x * 256 + threadIdx.x;
-    const long long m = t / (ldp / V), n = (t - m * (ldp / V)) * V;
-    if (m >= M) return;
-    float v[V] = {};
+    const long long m = t / (ldp / 4), n = (t - m * (ldp / 4)) * 4;
+    if (m >= M || n >= N) return;
+    float v[4] = {};
 #pragma unroll 4
     for (int s = 0; s < splits; s++) {
-        const float *p = partial + (s * M + m) * ldp + n;
-        if constexpr (V == 4) {
-            const float4 x = __ldcs(reinterpret_cast<const float4 *>(p));
-            v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-        } else {
-            v[0] += __ldcs(p);
-        }
+        const float4 x = __ldcs(reinterpret_cast<const float4 *>(partial + (s * M + m) * ldp + n));
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
     }
     const long long i = m * N + n;
+    float z[4];
 #pragma unroll
-    for (int k = 0; k < V; k++) {
-        if (n + k >= N) break;
-        float z = e.alpha * v[k] + (e.bias != nullptr ? __ldg(e.bias + n + k) : 0.f);
-        if (e.preact != nullptr) {
-            if (e.preact_f32) ((float *)e.preact)[i + k] = z;
-            else ((bf16 *)e.preact)[i + k] = __float2bfloat16_rn(z);
-        }
-        z = act_fwd(z, e.act);
-        if (e.out_f32) {
-            if (e.res != nullptr) z += ((const float *)e.res)[m * e.ldr + n + k];
-            ((float *)e.out)[i + k] = z;
-        } else {
-            if (e.res != nullptr) z += __bfloat162float(((const bf16 *)e.res)[m * e.ldr + n + k]);
-            ((bf16 *)e.out)[i + k] = __float2bfloat16_rn(z);
-        }
+    for (int k = 0; k < 4; k++) {
+        z[k] = e.alpha * v[k] + (e.bias != nullptr && n + k < N ? __ldg(e.bias + n + k) : 0.f);
+        v[k] = act_fwd(z[k], e.act);
+        if (e.res != nullptr && n + k < N)
+            v[k] += e.out_f32 ? ((const float *)e.res)[m * e.ldr + n + k] : __bfloat162float(((const bf16 *)e.res)[m * e.ldr + n + k]);
     }
+    const auto put = [&](void *out, bool f32, const float (&x)[4]) {
+        if constexpr (VEC) {
+            if (f32) {
+                *reinterpret_cast<float4 *>((float *)out + i) = make_float4(x[0], x[1], x[2], x[3]);
+            } else {
+                const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+                *reinterpret_cast<uint2 *>((bf16 *)out + i) = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                if (n + k >= N) break;
+                if (f32) ((float *)out)[i + k] = x[k];
+                else ((bf16 *)out)[i + k] = __float2bfloat16_rn(x[k]);
+            }
+        }
+    };
+    if (e.preact != nullptr) put(e.preact, e.preact_f32, z);
+    put(e.out, e.out_f32, v);
 }
 
 // ------------------------------------------------------------------ host side
@@ -204,7 +253,7 @@ inline int planes_of(const csa_linear_params &p) { return p.dtype == CSA_F32 ? 3
 
 struct Fwd {
     bool stage_x, stage_w;
-    int splits;
+    linear::Plan plan;
     size_t off_x, off_w, off_part, total;
 };
 Fwd plan_fwd(const csa_linear_params &p)
@@ -219,9 +268,9 @@ Fwd plan_fwd(const csa_linear_params &p)
     if (f.stage_x) at += staged_bytes(p.dtype, M, K);
     f.off_w = at;
     if (f.stage_w) at += staged_bytes(p.dtype, N, K);
-    f.splits = product_splits(M, N, K, planes_of(p), kSms);
+    f.plan = plan_product(M, N, K, planes_of(p), p.out_dtype == CSA_F32, kSms);
     f.off_part = at;
-    if (f.splits > 1) at += up256((size_t)f.splits * M * partial_stride(N) * 4);
+    if (f.plan.splits > 1) at += up256((size_t)f.plan.splits * M * partial_stride(N) * 4);
     f.total = at;
     return f;
 }
@@ -229,7 +278,8 @@ Fwd plan_fwd(const csa_linear_params &p)
 // Every part that some choice of outputs needs: the workspace does not depend on which are asked for.
 struct Bwd {
     bool stage_x, stage_w, stage_dz;
-    int splits_dx, splits_dw, per, blocks;
+    linear::Plan dx, dw;
+    int per, blocks;
     size_t off_x, off_w, off_dz, off_sums, off_part, total;
 };
 Bwd plan_bwd(const csa_linear_params &p)
@@ -240,9 +290,10 @@ Bwd plan_bwd(const csa_linear_params &p)
     b.stage_x = staged(p.dtype, p.x_stride);
     b.stage_w = staged(p.dtype, K);
     b.stage_dz = p.activation != CSA_ACT_NONE || p.dtype != p.out_dtype || staged(p.dtype, p.dy_stride);
-    // rows of a block of dz_kernel: enough blocks to fill the GPU (6 an SM run at once), four rows of each thread at least
-    const long long cols = N <= 64 ? 1 : (N + 255) / 256, least = N <= 64 ? 128 : 32;
-    long long per = (M * cols + 8 * kSms - 1) / (8 * kSms);
+    // rows of a block of dz_kernel: enough blocks to fill the GPU many times, a row of each thread at least
+    const long long cols = N <= 64 ? 1 : (N + 255) / 256, least = N <= 64 ? 32 : 8;
+    const long long want = (p.activation != CSA_ACT_NONE ? 24 : 8) * kSms;
+    long long per = (M * cols + want - 1) / want;
     if (per < least) per = least;
     b.per = (int)(per < M ? per : M);
     b.blocks = (int)((M + b.per - 1) / b.per);
@@ -256,32 +307,48 @@ Bwd plan_bwd(const csa_linear_params &p)
     b.off_sums = at;
     at += up256((size_t)b.blocks * N * 4);
     b.off_part = at;
-    b.splits_dx = product_splits(M, K, N, planes_of(p), kSms);
-    b.splits_dw = product_splits(N, K, M, planes_of(p), kSms);
-    const size_t dx = b.splits_dx > 1 ? (size_t)b.splits_dx * M * partial_stride(K) * 4 : 0;
-    const size_t dw = b.splits_dw > 1 ? (size_t)b.splits_dw * N * partial_stride(K) * 4 : 0;
+    b.dx = plan_product(M, K, N, planes_of(p), p.dtype == CSA_F32, kSms);
+    b.dw = plan_product(N, K, M, planes_of(p), p.dtype == CSA_F32, kSms);
+    const size_t dx = b.dx.splits > 1 ? (size_t)b.dx.splits * M * partial_stride(K) * 4 : 0;
+    const size_t dw = b.dw.splits > 1 ? (size_t)b.dw.splits * N * partial_stride(K) * 4 : 0;
     at += up256(dx > dw ? dx : dw);  // one product after the other
     b.total = at;
     return b;
 }
 
-// The operand of `rows` x `cols` values, where they are or staged.
-cudaError_t operand(Operand *o, const csa_linear_params &p, const void *x, long long stride, long long rows, int cols,
-                    bool stage, void *to, bool k_major, cudaStream_t st)
+// The operand of `rows` x `cols` values, where they are or staged (`job` then says how; no blocks: it is not).
+Operand operand(const csa_linear_params &p, const void *x, long long stride, long long rows, int cols, bool stage, void *to, bool k_major,
+                Stage *job)
 {
-    o->k_major = k_major;
+    Operand o;
+    o.k_major = k_major;
     if (!stage) {
-        o->base = static_cast<const bf16 *>(x);
-        o->ld = stride;
-        o->plane = 0;
-        return cudaSuccess;
+        o.base = static_cast<const bf16 *>(x);
+        o.ld = stride;
+        o.plane = 0;
+        return o;
     }
-    o->base = static_cast<bf16 *>(to);
-    o->ld = up8(cols);
-    o->plane = rows * o->ld;
-    const dim3 grid((cols + 255) / 256 < 64 ? (cols + 255) / 256 : 64, (unsigned)(rows < 32768 ? rows : 32768));
-    if (p.dtype == CSA_F32) stage_kernel<float><<<grid, 256, 0, st>>>((const float *)x, stride, rows, cols, (bf16 *)to, o->ld, o->plane);
-    else stage_kernel<bf16><<<grid, 256, 0, st>>>((const bf16 *)x, stride, rows, cols, (bf16 *)to, o->ld, o->plane);
+    o.base = static_cast<bf16 *>(to);
+    o.ld = up8(cols);
+    o.plane = rows * o.ld;
+    job->x = x;
+    job->out = static_cast<bf16 *>(to);
+    job->stride = stride;
+    job->rows = rows;
+    job->ld = o.ld;
+    job->plane = o.plane;
+    job->cols = cols;
+    job->vec = cols % 8 == 0 && stride % (p.dtype == CSA_F32 ? 4 : 8) == 0;
+    job->blocks = (unsigned)((rows * cols + 2047) / 2048);
+    return o;
+}
+
+cudaError_t run_stages(const csa_linear_params &p, const Stage (&job)[2], cudaStream_t st)
+{
+    const unsigned blocks = job[0].blocks + job[1].blocks;
+    if (blocks == 0) return cudaSuccess;
+    if (p.dtype == CSA_F32) stage_kernel<float><<<blocks, 256, 0, st>>>(job[0], job[1]);
+    else stage_kernel<bf16><<<blocks, 256, 0, st>>>(job[0], job[1]);
     note_launches(1);
     return cudaGetLastError();
 }
@@ -289,31 +356,35 @@ cudaError_t operand(Operand *o, const csa_linear_params &p, const void *x, long 
 cudaError_t product(const Product &p, cudaStream_t st)
 {
     const cudaError_t e = launch_product_tc(p, kSms, st);
-    if (e != cudaSuccess || p.splits == 1) return e;
-    // four columns a thread where there are enough of them for that
-    const long long total = p.M * partial_stride(p.N);
-    const bool four = total >= 4 * 256 * kSms && (p.N & 3) == 0;
-    const long long blocks = (total / (four ? 4 : 1) + 255) / 256;
-    if (four) join_kernel<4><<<(unsigned)blocks, 256, 0, st>>>(p.e.partial, p.splits, p.M, p.N, p.e);
-    else join_kernel<1><<<(unsigned)blocks, 256, 0, st>>>(p.e.partial, p.splits, p.M, p.N, p.e);
+    if (e != cudaSuccess || p.plan.splits == 1) return e;
+    const long long blocks = (p.M * (partial_stride(p.N) / 4) + 255) / 256;
+    if (p.N % 4 == 0) join_kernel<true><<<(unsigned)blocks, 256, 0, st>>>(p.e.partial, p.plan.splits, p.M, p.N, p.e);
+    else join_kernel<false><<<(unsigned)blocks, 256, 0, st>>>(p.e.partial, p.plan.splits, p.M, p.N, p.e);
     note_launches(1);
     return cudaGetLastError();
 }
 
-template <typename V, typename O>
-cudaError_t run_dz(const csa_linear_params &p, const Bwd &b, const void *dy, const void *z, bf16 *dz, float *sums,
-                   cudaStream_t st)
+template <typename V, typename O, int TX, bool VEC>
+void run_dz_rows(const csa_linear_params &p, const Bwd &b, const void *dy, const void *z, bf16 *dz, float *sums, cudaStream_t st)
 {
     const int N = p.out_features;
     const long long ld = up8(N), plane = p.rows * ld;
+    const dim3 grid((N + 8 * TX - 1) / (8 * TX), b.blocks);
+    if (p.activation == CSA_ACT_NONE)
+        dz_kernel<V, O, TX, VEC, 1><<<grid, 256, 0, st>>>((const O *)dy, p.dy_stride, (const V *)z, 0, dz, ld, plane, sums, p.rows, N, b.per);
+    else
+        dz_kernel<V, O, TX, VEC, 2><<<grid, 256, 0, st>>>((const O *)dy, p.dy_stride, (const V *)z, p.activation, dz, ld, plane, sums, p.rows, N, b.per);
+}
+
+template <typename V, typename O>
+cudaError_t run_dz(const csa_linear_params &p, const Bwd &b, const void *dy, const void *z, bf16 *dz, float *sums, cudaStream_t st)
+{
+    const int N = p.out_features;
     const bool vec = (N & 7) == 0 && (p.dy_stride & 7) == 0;
-    const dim3 grid(N <= 64 ? 1 : (N + 255) / 256, b.blocks);
-    const O *g = (const O *)dy;
-    const V *q = (const V *)z;
-    if (N <= 64 && vec) dz_kernel<V, O, 8, true><<<grid, 256, 0, st>>>(g, p.dy_stride, q, p.activation, dz, ld, plane, sums, p.rows, N, b.per);
-    else if (N <= 64) dz_kernel<V, O, 8, false><<<grid, 256, 0, st>>>(g, p.dy_stride, q, p.activation, dz, ld, plane, sums, p.rows, N, b.per);
-    else if (vec) dz_kernel<V, O, 32, true><<<grid, 256, 0, st>>>(g, p.dy_stride, q, p.activation, dz, ld, plane, sums, p.rows, N, b.per);
-    else dz_kernel<V, O, 32, false><<<grid, 256, 0, st>>>(g, p.dy_stride, q, p.activation, dz, ld, plane, sums, p.rows, N, b.per);
+    if (N <= 64 && vec) run_dz_rows<V, O, 8, true>(p, b, dy, z, dz, sums, st);
+    else if (N <= 64) run_dz_rows<V, O, 8, false>(p, b, dy, z, dz, sums, st);
+    else if (vec) run_dz_rows<V, O, 32, true>(p, b, dy, z, dz, sums, st);
+    else run_dz_rows<V, O, 32, false>(p, b, dy, z, dz, sums, st);
     note_launches(1);
     return cudaGetLastError();
 }
@@ -351,13 +422,15 @@ cudaError_t launch_linear_fwd(const csa_linear_params &p, const void *x, const v
     note_path("tcgen05");
     const Fwd f = plan_fwd(p);
     char *w = static_cast<char *>(ws);
-    LIN_TRY(operand(&q.a, p, x, p.x_stride, p.rows, p.in_features, f.stage_x, w + f.off_x, true, st));
-    LIN_TRY(operand(&q.b, p, weight, p.in_features, p.out_features, p.in_features, f.stage_w, w + f.off_w, true, st));
+    Stage job[2] = {};
+    q.a = operand(p, x, p.x_stride, p.rows, p.in_features, f.stage_x, w + f.off_x, true, &job[0]);
+    q.b = operand(p, weight, p.in_features, p.out_features, p.in_features, f.stage_w, w + f.off_w, true, &job[1]);
+    LIN_TRY(run_stages(p, job, st));
     q.M = p.rows;
     q.N = p.out_features;
     q.K = p.in_features;
     q.planes = planes_of(p);
-    q.splits = f.splits;
+    q.plan = f.plan;
     q.e.partial = reinterpret_cast<float *>(w + f.off_part);
     return product(q, st);
 }
@@ -395,25 +468,30 @@ cudaError_t launch_linear_bwd(const csa_linear_params &p, const void *dy, const 
     q.e.alpha = p.alpha;
     q.e.out_f32 = p.dtype == CSA_F32;
     q.e.partial = reinterpret_cast<float *>(w + b.off_part);
+    Stage job[2] = {};
+    Operand ow = {}, ox = {};
+    if (dx != nullptr) ow = operand(p, weight, K, N, (int)K, b.stage_w, w + b.off_w, false, &job[0]);
+    if (dw != nullptr) ox = operand(p, x, p.x_stride, M, (int)K, b.stage_x, w + b.off_x, false, &job[1]);
+    LIN_TRY(run_stages(p, job, st));
     if (dx != nullptr) {
         q.a = d;
         q.a.k_major = true;
-        LIN_TRY(operand(&q.b, p, weight, K, N, (int)K, b.stage_w, w + b.off_w, false, st));
+        q.b = ow;
         q.M = M;
         q.N = K;
         q.K = N;
-        q.splits = b.splits_dx;
+        q.plan = b.dx;
         q.e.out = dx;
         LIN_TRY(product(q, st));
     }
     if (dw != nullptr) {
         q.a = d;
         q.a.k_major = false;
-        LIN_TRY(operand(&q.b, p, x, p.x_stride, M, (int)K, b.stage_x, w + b.off_x, false, st));
+        q.b = ox;
         q.M = N;
         q.N = K;
         q.K = M;
-        q.splits = b.splits_dw;
+        q.plan = b.dw;
         q.e.out = dw;
         LIN_TRY(product(q, st));
     }

@@ -79,17 +79,24 @@ struct Operand {
     bool k_major;
 };
 
-// D[m][n] = sum_k A(m, k) B(n, k), M x N x K, with `planes` = 1 or 3 and the k axis cut into `splits` pieces.
+// Tile and cut of the k axis of a product (see k_linear_tc.cu).
+enum Shape { LONE_64, PAIR_128, PAIR_256 };
+struct Plan {
+    Shape shape;
+    int splits;   // pieces of the k axis: above 1, the caller provides splits * M * partial_stride(N) floats and joins them
+    bool exact;   // sums kept in registers (see k_linear_tc.cu)
+};
+// out_f32: the result itself is fp32 (and not only its pieces)
+Plan plan_product(long long M, long long N, long long K, int planes, bool out_f32, int sms);
+
+// D[m][n] = sum_k A(m, k) B(n, k), M x N x K, with `planes` = 1 or 3.
 struct Product {
     Operand a, b;
     long long M, N, K;
-    int planes, splits;
+    int planes;
+    Plan plan;
     Epilogue e;
 };
-
-// How many pieces of the k axis the tensor-core kernel wants for this product (1: none; the caller provides
-// splits * M * partial_stride(N) floats in e.partial and reduces them).
-int product_splits(long long M, long long N, long long K, int planes, int sms);
 cudaError_t launch_product_tc(const Product &p, int sms, cudaStream_t st);
 
 // The forward of up to kSmallRows rows without tensor cores (k_linear_small.cu); operands where they are, no workspace.

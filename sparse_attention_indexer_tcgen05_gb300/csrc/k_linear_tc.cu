@@ -2,9 +2,14 @@
 //
 // D[m][n] = sum_k A(m, k) B(n, k) with bf16 operands and fp32 sums, for y = x W^T (both operands contiguous along
 // k), dx = dz W (B contiguous along n) and dW = dz^T x (both contiguous along m, n): the shared-memory descriptors
-// take either order, so no operand is transposed in memory.  fp32 values come as three bf16 planes and take six
-// passes over k, (l h) (h l) (m m) (m h) (h m) (h h), the smallest terms first; what is left out is below 2^-23 of
-// the terms.
+// take either order, so no operand is transposed in memory.  fp32 values come as three bf16 planes, x = h + m + l, and each
+// 64 k of them take six products, l h, h l, m m, m h, h m, h h, the smallest terms first; what is left out is below
+// 2^-23 of the terms.
+//
+// The tensor core cuts a sum off where it aligns it with a product (it does not round), so a TMEM accumulator loses about
+// 2^-24 / 3 of itself with every 16 k, always towards zero: 5e-6 at k = 8192.  That is nothing beside a bf16 result.  For
+// fp32 results (EXACT below) the accumulator starts anew every 64 k (three planes: the small terms then meet a small
+// sum; 2e-7 off at k = 65536) or every 512 k (5e-7), and the epilogue's warps add up the pieces in registers, rounded.
 //
 // Mapping.  A unit is one output tile and one piece of the k axis.  A CTA pair (two SMs) computes 256 x BN: each CTA
 // loads its 128 rows of A and its BN / 2 rows of B, so an operand byte brought to an SM feeds twice the MMAs of a
@@ -20,6 +25,7 @@
 #include "tc_ptx.cuh"
 
 #include <cuda.h>
+#include <math.h>
 
 namespace csa {
 
@@ -45,11 +51,11 @@ constexpr int BK = 64;         // k per stage: one 128-byte swizzle row
 constexpr int THREADS = 320;
 constexpr int EPI_WARPS = 8;
 
-template <int CG, int BN> struct Cfg {
+template <int CG, int BN, int P> struct Cfg {                  // P planes
     static constexpr int ROWS_B = BN / CG;                      // B rows this CTA loads
     static constexpr int A_BYTES = BM * BK * 2, B_BYTES = ROWS_B * BK * 2;
-    static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int STAGES = STAGE == 32768 ? 6 : 8;       // 192 KB
+    static constexpr int STAGE = P * (A_BYTES + B_BYTES);
+    static constexpr int STAGES = 196608 / STAGE;               // 192 KB: 6 or 8; 2 of three planes
     static constexpr int TURN = STAGES * STAGE;                 // the epilogue's buffers, 32 rows of 128 bytes a warp
     static constexpr int MISC = TURN + EPI_WARPS * 4096;
     static constexpr int SMEM = MISC + 512 + 1024;              // + alignment
@@ -58,9 +64,8 @@ template <int CG, int BN> struct Cfg {
 
 struct Args {
     long long M, N, ldo;        // the output's row stride
-    int ksteps;                 // stages of one plane pair over the whole k axis
-    int passes;                 // plane pairs: 1 or 6
-    int splits, per_split;      // k pieces, stages (over passes * ksteps) of each
+    int ksteps;                 // stages over the whole k axis
+    int splits, per_split;      // k pieces, stages of each
     int mt, nt;                 // tiles
     int whole, units;           // units that are whole tiles (times splits); the rest are halves of the last tiles
     int blocks_a, blocks_b;     // an m/n-contiguous operand's map has 64-wide blocks as an axis of their own
@@ -104,22 +109,9 @@ template <int BN> __device__ __forceinline__ Unit unit_of(const Args &a, int u)
     x.m = band * BAND + r % h;
     x.n0 = (long long)(r / h) * BN + half * (BN / 2);
     x.it0 = x.s * a.per_split;
-    x.it1 = min(a.passes * a.ksteps, x.it0 + a.per_split);
+    x.it1 = min(a.ksteps, x.it0 + a.per_split);
     return x;
 }
-
-// The plane pair of pass q, smallest terms first.
-__device__ __forceinline__ void planes_of(int passes, int q, int &pa, int &pb)
-{
-    if (passes == 1) {
-        pa = pb = 0;
-        return;
-    }
-    pa = (0x001102 >> (4 * q)) & 3;   // l h m m h h
-    pb = (0x010120 >> (4 * q)) & 3;   // h l m h m h
-}
-
-// ------------------------------------------------------------------ epilogue: 32 rows x 32 columns of a warp
 
 // Shared memory a warp stores from: 32 rows of 128 bytes.
 struct Buffer {
@@ -290,13 +282,15 @@ __device__ __forceinline__ void to_activation(const Args &a, float (&v)[C], long
     else if (e.act == CSA_ACT_GELU_TANH) activate<CSA_ACT_GELU_TANH>(v);
 }
 
-template <int CG, int BN, bool A_K, bool B_K>
+// EXACT: the sums are kept in the epilogue's registers, pieces of CHUNK stages of the k axis in TMEM.
+template <int CG, int BN, int P, bool EXACT, bool A_K, bool B_K>
 __global__ void __launch_bounds__(THREADS, 1)
 linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                  const __grid_constant__ CUtensorMap map_half, const __grid_constant__ CUtensorMap map_out, const Args a)
 {
-    using Z = Cfg<CG, BN>;
+    using Z = Cfg<CG, BN, P>;
     constexpr int S = Z::STAGES;
+    constexpr int CHUNK = !EXACT ? 0x40000000 : P == 3 ? 1 : 8;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = smem_align1024(smem_raw);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Z::MISC);
@@ -354,32 +348,28 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                 const bool half = x.bn != BN;
                 const int am = (x.m * CG + (int)rank) * BM;
                 const int rows_b = x.bn / CG, bn = (int)x.n0 + (int)rank * rows_b;
-                const uint32_t bytes = CG * (Z::A_BYTES + rows_b * BK * 2);
+                const uint32_t bytes = CG * P * (Z::A_BYTES + rows_b * BK * 2);
                 const CUtensorMap *mb = half ? &map_half : &map_b;
-                int q = x.it0 / a.ksteps, k = x.it0 - q * a.ksteps;
-                for (int it = x.it0; it < x.it1; it++) {
-                    int pa, pb;
-                    planes_of(a.passes, q, pa, pb);
+                for (int k = x.it0 * BK; k < x.it1 * BK; k += BK) {
                     wait_bar(empty + st, ph ^ 1, abort_flag, &g_lin_error, 601);
-                    unsigned char *sa = smem + st * Z::STAGE, *sb = sa + Z::A_BYTES;
                     if (rank == 0) mbar_expect_tx(full + st, bytes);
-                    if constexpr (A_K) {
-                        load3(sa, &map_a, st, k * BK, am, pa);
-                    } else if (a.blocks_a) {
-                        load4(sa, &map_a, st, 0, k * BK, am >> 6, pa);
-                    } else {
-                        for (int i = 0; i < BM; i += 64) load3(sa + i * 128, &map_a, st, am + i, k * BK, pa);
-                    }
-                    if constexpr (B_K) {
-                        load3(sb, mb, st, k * BK, bn, pb);
-                    } else if (a.blocks_b) {
-                        load4(sb, mb, st, 0, k * BK, bn >> 6, pb);
-                    } else {
-                        for (int i = 0; i < rows_b; i += 64) load3(sb + i * 128, mb, st, bn + i, k * BK, pb);
-                    }
-                    if (++k == a.ksteps) {
-                        k = 0;
-                        q++;
+#pragma unroll
+                    for (int q = 0; q < P; q++) {
+                        unsigned char *sa = smem + st * Z::STAGE + q * Z::A_BYTES, *sb = smem + st * Z::STAGE + P * Z::A_BYTES + q * Z::B_BYTES;
+                        if constexpr (A_K) {
+                            load3(sa, &map_a, st, k, am, q);
+                        } else if (a.blocks_a) {
+                            load4(sa, &map_a, st, 0, k, am >> 6, q);
+                        } else {
+                            for (int i = 0; i < BM; i += 64) load3(sa + i * 128, &map_a, st, am + i, k, q);
+                        }
+                        if constexpr (B_K) {
+                            load3(sb, mb, st, k, bn, q);
+                        } else if (a.blocks_b) {
+                            load4(sb, mb, st, 0, k, bn >> 6, q);
+                        } else {
+                            for (int i = 0; i < rows_b; i += 64) load3(sb + i * 128, mb, st, bn + i, k, q);
+                        }
                     }
                     used = max(used, st + 1);
                     if (++st == S) {
@@ -401,29 +391,36 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             for (int u = u0; u < a.units; u += ustep) {
                 const Unit x = unit_of<BN>(a, u);
                 const uint32_t idesc = x.bn == BN ? idesc_bf16(BM * CG, BN, !A_K, !B_K) : idesc_bf16(BM * CG, BN / 2, !A_K, !B_K);
-                const int tb = tc & 1;
-                wait_bar(t_empty + tb, ((tc >> 1) & 1) ^ 1, abort_flag, &g_lin_error, 602);
-                fence_after();
-                const uint32_t d = tmem + (uint32_t)(tb * BN);
-                for (int it = x.it0; it < x.it1; it++) {
-                    wait_bar(full + st, ph, abort_flag, &g_lin_error, 603);
+                for (int it0 = x.it0; it0 < x.it1; it0 += min(CHUNK, x.it1 - it0)) {
+                    const int it1 = min(CHUNK, x.it1 - it0) + it0, tb = tc & 1;
+                    wait_bar(t_empty + tb, ((tc >> 1) & 1) ^ 1, abort_flag, &g_lin_error, 602);
                     fence_after();
-                    const unsigned char *sa = smem + st * Z::STAGE, *sb = sa + Z::A_BYTES;
-                    // along k (16 values): 32 bytes of a k-major row, 16 rows of 128 bytes of an m/n-major tile
-                    const uint64_t da = A_K ? desc_kmajor(sa) : desc_sw128(sa, 8192, 1024);
-                    const uint64_t db = B_K ? desc_kmajor(sb) : desc_sw128(sb, 8192, 1024);
-                    if constexpr (CG == 2)
-                        mma4_ss_pair_w(d, da, A_K ? 2 : 128, db, B_K ? 2 : 128, idesc, it != x.it0, su32(empty + st));
-                    else
-                        mma4_ss_w(d, da, A_K ? 2 : 128, db, B_K ? 2 : 128, idesc, it != x.it0, su32(empty + st));
-                    if (++st == S) {
-                        st = 0;
-                        ph ^= 1;
+                    const uint32_t d = tmem + (uint32_t)(tb * BN);
+                    for (int it = it0; it < it1; it++) {
+                        wait_bar(full + st, ph, abort_flag, &g_lin_error, 603);
+                        fence_after();
+                        const unsigned char *sa = smem + st * Z::STAGE, *sb = sa + P * Z::A_BYTES;
+                        constexpr int PRODUCTS = P == 1 ? 1 : 6;
+#pragma unroll
+                        for (int i = 0; i < PRODUCTS; i++) {
+                            constexpr int PA[6] = {2, 0, 1, 1, 0, 0}, PB[6] = {0, 2, 1, 0, 1, 0};
+                            const unsigned char *pa = sa + (P == 1 ? 0 : PA[i]) * Z::A_BYTES, *pb = sb + (P == 1 ? 0 : PB[i]) * Z::B_BYTES;
+                            // along k (16 values): 32 bytes of a k-major row, 16 rows of 128 bytes of an m/n-major tile
+                            const uint64_t da = A_K ? desc_kmajor(pa) : desc_sw128(pa, 8192, 1024);
+                            const uint64_t db = B_K ? desc_kmajor(pb) : desc_sw128(pb, 8192, 1024);
+                            const uint32_t acc = i > 0 || it != it0, bar = i == PRODUCTS - 1 ? su32(empty + st) : 0u;
+                            if constexpr (CG == 2) mma4_ss_pair_w(d, da, A_K ? 2 : 128, db, B_K ? 2 : 128, idesc, acc, bar);
+                            else mma4_ss_w(d, da, A_K ? 2 : 128, db, B_K ? 2 : 128, idesc, acc, bar);
+                        }
+                        if (++st == S) {
+                            st = 0;
+                            ph ^= 1;
+                        }
                     }
+                    if constexpr (CG == 2) mma_commit_pair_w(t_full + tb);
+                    else mma_commit_w(t_full + tb);
+                    tc++;
                 }
-                if constexpr (CG == 2) mma_commit_pair_w(t_full + tb);
-                else mma_commit_w(t_full + tb);
-                tc++;
             }
             if constexpr (CG == 2) mma_commit_pair_w(done);
             else mma_commit_w(done);
@@ -434,51 +431,88 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         const int quad = warp & 3;               // TMEM lanes this warp may access
         const int side = (warp - 2) >> 2;        // half of the columns
         const Buffer b = {smem + Z::TURN + (warp - 2) * 4096, lane};
+        // asked once: each of these questions cost a step a miss in the constant and instruction caches
+        const bool plain = a.e.bias == nullptr && a.e.alpha == 1.f && a.e.preact == nullptr && a.e.act == CSA_ACT_NONE && a.e.res == nullptr;
+        const bool tma = a.tma_out != 0, with_res = a.e.res != nullptr;
         auto run = [&](auto type) {
             using O = decltype(type);
             int tc = 0;
-            for (int u = u0; u < a.units; u += ustep, tc++) {
+            for (int u = u0; u < a.units; u += ustep) {
                 const Unit x = unit_of<BN>(a, u);
-                const int tb = tc & 1, cols = x.bn / 2;
+                const int cols = x.bn / 2;
                 const long long m0 = ((long long)x.m * CG + rank) * BM + quad * 32, nb = x.n0 + side * cols;
-                const uint32_t t = tmem + (uint32_t)(tb * BN + side * cols) + ((uint32_t)(quad * 32) << 16);
-                Residual<O> res;
-                auto ask = [&](long long n0) {
-                    if (a.e.res != nullptr && m0 + lane < a.M && n0 < a.N) res.load(a, m0 + lane, n0);
+                const auto release = [&](int tb) {  // the accumulator is in registers: the next MMAs may have it
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (CG == 2) mbar_arrive_cluster(map_rank(t_empty + tb, 0));
+                        else mbar_arrive(t_empty + tb);
+                    }
                 };
-                ask(nb);
-                wait_bar(t_full + tb, (tc >> 1) & 1, abort_flag, &g_lin_error, 604);
-                fence_after();
-#pragma unroll 1
-                for (int c = 0; c < cols; c += C) {
+                const auto wait = [&] {
+                    wait_bar(t_full + (tc & 1), (tc >> 1) & 1, abort_flag, &g_lin_error, 604);
+                    fence_after();
+                    return tmem + (uint32_t)((tc & 1) * BN + side * cols) + ((uint32_t)(quad * 32) << 16);
+                };
+                Residual<O> res;
+                const auto ask = [&](long long n0) {
+                    if (with_res && m0 + lane < a.M && n0 < a.N) res.load(a, m0 + lane, n0);
+                };
+                // 32 columns from sums to memory
+                const auto step = [&](int c, float (&v)[C]) {
                     const long long n0 = nb + c;
-                    float v[C];
-                    tmem_ld32(t + c, v);
-                    if (c + C == cols) {  // the accumulator is in registers: the next tile's MMAs may have it
-                        fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if constexpr (CG == 2) mbar_arrive_cluster(map_rank(t_empty + tb, 0));
-                            else mbar_arrive(t_empty + tb);
+                    if (m0 >= a.M || n0 >= a.N) return;
+                    if (!plain) {
+                        to_activation(a, v, m0, n0, b);
+                        if (with_res) {
+                            res.add_to(v);
+                            if (c + C < cols) ask(n0 + C);
                         }
                     }
-                    if (m0 >= a.M || n0 >= a.N) continue;
-                    to_activation(a, v, m0, n0, b);
-                    if (a.e.res != nullptr) {
-                        res.add_to(v);
-                        if (c + C < cols) ask(n0 + C);
-                    }
-                    if (a.tma_out) {
+                    if (tma) {
                         const bool second = sizeof(O) == 2 && (c & C) != 0;
                         tma_tile<O>(&map_out, v, m0, n0, x.s, second, sizeof(O) == 4 || second || n0 + C >= a.N, b);
                     } else {
                         store_tile<O>((O *)a.e.out + (long long)x.s * a.M * a.ldo, a.ldo, a.M, a.N, v, m0, n0, b);
                     }
+                };
+                if constexpr (EXACT) {
+                    constexpr int G = BN / 2 / C;
+                    float sum[G][C] = {};
+                    for (int it = x.it0; it < x.it1; it += CHUNK, tc++) {
+                        const uint32_t t = wait();
+#pragma unroll
+                        for (int g = 0; g < G; g++) {
+                            float v[C];
+                            tmem_ld32(t + g * C, v);
+                            if (g == G - 1) release(tc & 1);
+#pragma unroll
+                            for (int k = 0; k < C; k++) sum[g][k] += v[k];
+                        }
+                    }
+                    ask(nb);
+#pragma unroll
+                    for (int g = 0; g < G; g++) step(g * C, sum[g]);
+                } else {
+                    ask(nb);
+                    const uint32_t t = wait();
+#pragma unroll 1
+                    for (int c = 0; c < cols; c += C) {
+                        float v[C];
+                        tmem_ld32(t + c, v);
+                        if (c + C == cols) release(tc & 1);
+                        step(c, v);
+                    }
+                    tc++;
                 }
             }
         };
-        if (a.e.out_f32) run(float());
-        else run(__nv_bfloat16());
+        if constexpr (EXACT) {
+            run(float());
+        } else {
+            if (a.e.out_f32) run(float());
+            else run(__nv_bfloat16());
+        }
         if (lane == 0) bulk_wait();
     }
     __syncwarp();
@@ -494,17 +528,6 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
 
 // ------------------------------------------------------------------ host side
 
-enum Shape { LONE_64, PAIR_128, PAIR_256 };
-
-// Which tile a product takes.  Lone CTAs of 128 x 64 when m fits one of them; pairs otherwise, 256 wide where that
-// leaves a tile for more than half of them (a 256-wide tile moves 64 bytes of operands per SM and cycle of MMAs, a
-// 128-wide one 96).
-static Shape shape_of(long long M, long long N, int sms)
-{
-    if (M <= 128) return LONE_64;
-    return N > 128 && (M + 255) / 256 * ((N + 255) / 256) * 2 > sms / 2 ? PAIR_256 : PAIR_128;
-}
-
 static void tile_counts(Shape s, long long M, long long N, int &mt, int &nt)
 {
     const int bm = s == LONE_64 ? 128 : 256, bn = s == LONE_64 ? 64 : s == PAIR_128 ? 128 : 256;
@@ -512,28 +535,53 @@ static void tile_counts(Shape s, long long M, long long N, int &mt, int &nt)
     nt = (int)((N + bn - 1) / bn);
 }
 
-int product_splits(long long M, long long N, long long K, int planes, int sms)
+// Tile and cut of the k axis by estimated time, of which this is the model (fitted to 40 timings of products from
+// 37 x 2048 x 8192 to 2048^3 and 64 x 512 x 16384, most of them within 10%; us):
+//   a stage of a unit: 128 x 64 and 256 x 128 tiles 0.20 (the loads), 256 x 256 0.28 (the MMAs' own 512 cycles); of three
+//   planes, six products, 0.72 and 0.90;
+//   a round is no shorter than its epilogue: 0.9, 1.7 and 2.9;
+//   launch, first loads and last epilogue: 3.8, 5.2 and 6.3;
+//   a cut k axis: another launch, 3.4, and the pieces' way to memory and back at 4 TB/s.
+// Units run in rounds of one per SM or pair.
+Plan plan_product(long long M, long long N, long long K, int planes, bool out_f32, int sms)
 {
-    int mt, nt;
-    const Shape s = shape_of(M, N, sms);
-    tile_counts(s, M, N, mt, nt);
-    const long long tiles = (long long)mt * nt, slots = s == LONE_64 ? sms : sms / 2;
-    const long long steps = (K + BK - 1) / BK * (planes == 3 ? 6 : 1);
-    if (tiles * 2 > slots || steps < 8) return 1;
-    const long long want = slots / tiles, most = steps / 4;
-    const long long per = (steps + (want < most ? want : most) - 1) / (want < most ? want : most);
-    return (int)((steps + per - 1) / per);  // no piece is empty
+    const long long steps = (K + BK - 1) / BK;
+    // the registers hold half a row of 128 columns, not of 256
+    Plan best = {PAIR_128, 1, planes == 3 || (out_f32 && K > 1024)};
+    double least = 1e300;
+    for (int s = LONE_64; s <= (best.exact ? PAIR_128 : PAIR_256); s++) {
+        const Shape shape = (Shape)s;
+        int mt, nt;
+        tile_counts(shape, M, N, mt, nt);
+        const double tiles = (double)mt * nt;
+        const long long slots = shape == LONE_64 ? sms : sms / 2;
+        constexpr double STEP[2][3] = {{0.20, 0.20, 0.28}, {0.72, 0.90, 0.0}}, FIXED[3] = {3.8, 5.2, 6.3}, EPILOGUE[3] = {0.9, 1.7, 2.9};
+        const double step = STEP[planes == 3][s];
+        for (long long cut = 1; cut <= steps && cut <= 64 && (cut == 1 || tiles * cut <= slots); cut++) {
+            const long long per = (steps + cut - 1) / cut, pieces = (steps + per - 1) / per;
+            double rounds = floor(tiles * pieces / slots), rest = tiles * pieces - rounds * slots;
+            if (rest > 0) rounds += shape == PAIR_256 && pieces == 1 && rounds > 0 && 2 * rest <= slots ? 0.5 : 1.0;
+            double us = rounds * fmax(per * step, EPILOGUE[s]) + FIXED[s];
+            if (pieces > 1) us += 3.4 + (double)M * N * 8 * pieces / 4e6;
+            if (us < least) {
+                least = us;
+                best.shape = shape;
+                best.splits = (int)pieces;
+            }
+        }
+    }
+    return best;
 }
 
 struct Maps {
     CUtensorMap a, b, half, out;
 };
 
-template <int CG, int BN, bool A_K, bool B_K>
+template <int CG, int BN, int P, bool EXACT, bool A_K, bool B_K>
 static cudaError_t launch(const Maps &m, const Args &a, int sms, cudaStream_t st)
 {
-    using Z = Cfg<CG, BN>;
-    auto *kernel = linear_tc_kernel<CG, BN, A_K, B_K>;
+    using Z = Cfg<CG, BN, P>;
+    auto *kernel = linear_tc_kernel<CG, BN, P, EXACT, A_K, B_K>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::SMEM);
     if (e != cudaSuccess) return e;
     const int slots = sms / CG;
@@ -553,11 +601,24 @@ static cudaError_t launch(const Maps &m, const Args &a, int sms, cudaStream_t st
     return e;
 }
 
-template <int CG, int BN>
+template <int CG, int BN, int P, bool EXACT>
 static cudaError_t launch_majors(const Product &p, const Maps &m, const Args &a, int sms, cudaStream_t st)
 {
-    if (p.a.k_major) return p.b.k_major ? launch<CG, BN, true, true>(m, a, sms, st) : launch<CG, BN, true, false>(m, a, sms, st);
-    return launch<CG, BN, false, false>(m, a, sms, st);
+    if (p.a.k_major && p.b.k_major) return launch<CG, BN, P, EXACT, true, true>(m, a, sms, st);
+    if constexpr (P == 3 || !EXACT) {  // gradients have their operands' type
+        if (p.a.k_major) return launch<CG, BN, P, EXACT, true, false>(m, a, sms, st);
+        return launch<CG, BN, P, EXACT, false, false>(m, a, sms, st);
+    }
+    return cudaErrorInvalidValue;
+}
+template <int CG, int BN>
+static cudaError_t launch_planes(const Product &p, const Maps &m, const Args &a, int sms, cudaStream_t st)
+{
+    if constexpr (BN < 256) {
+        if (p.planes == 3) return launch_majors<CG, BN, 3, true>(p, m, a, sms, st);
+        if (p.plan.exact) return launch_majors<CG, BN, 1, true>(p, m, a, sms, st);
+    }
+    return launch_majors<CG, BN, 1, false>(p, m, a, sms, st);
 }
 
 // Boxes of `rows` m or n indices and 64 values of k of an operand with `n` of them.  {contiguous, strided, plane}; an
@@ -589,26 +650,25 @@ static bool encode_out(CUtensorMap *m, bool f32, const void *base, long long n, 
 
 cudaError_t launch_product_tc(const Product &p, int sms, cudaStream_t st)
 {
-    const Shape s = shape_of(p.M, p.N, sms);
+    const Shape s = p.plan.shape;
+    const int splits = p.plan.splits;
     Args a = {};
     a.M = p.M;
     a.N = p.N;
     a.ksteps = (int)((p.K + BK - 1) / BK);
-    a.passes = p.planes == 3 ? 6 : 1;
-    const int steps = a.ksteps * a.passes;
-    a.per_split = (steps + p.splits - 1) / p.splits;
-    a.splits = p.splits;
+    a.per_split = (a.ksteps + splits - 1) / splits;
+    a.splits = splits;
     tile_counts(s, p.M, p.N, a.mt, a.nt);
-    const long long units = (long long)a.mt * a.nt * p.splits, slots = sms / 2, rest = units % slots;
+    const long long units = (long long)a.mt * a.nt * splits, slots = sms / 2, rest = units % slots;
     if (units > 0x3fffffffLL || (long long)BAND * a.nt > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
     a.units = a.whole = (int)units;
-    if (s == PAIR_256 && p.splits == 1 && units > slots && rest > 0 && 2 * rest <= slots) {
+    if (s == PAIR_256 && splits == 1 && units > slots && rest > 0 && 2 * rest <= slots) {
         a.whole -= (int)rest;
         a.units += (int)rest;
     }
     a.e = p.e;
     a.ldo = p.N;
-    if (p.splits > 1) {  // bare fp32 sums, piece by piece
+    if (splits > 1) {  // bare fp32 sums, piece by piece
         a.e = Epilogue();
         a.e.alpha = 1.f;
         a.e.out = p.e.partial;
@@ -625,11 +685,11 @@ cudaError_t launch_product_tc(const Product &p, int sms, cudaStream_t st)
     const int rows_b = s == PAIR_256 ? 128 : 64;
     bool ok = encode(&m.a, p.a, p.M, p.K, p.planes, BM, a.blocks_a) && encode(&m.b, p.b, p.N, p.K, p.planes, rows_b, a.blocks_b);
     if (a.units > a.whole) ok = ok && encode(&m.half, p.b, p.N, p.K, p.planes, rows_b / 2, a.blocks_b);
-    if (a.tma_out) ok = ok && encode_out(&m.out, a.e.out_f32, a.e.out, p.N, a.ldo, p.M, p.splits);
+    if (a.tma_out) ok = ok && encode_out(&m.out, a.e.out_f32, a.e.out, p.N, a.ldo, p.M, splits);
     if (!ok) return cudaErrorInvalidValue;
-    if (s == LONE_64) return launch_majors<1, 64>(p, m, a, sms, st);
-    if (s == PAIR_128) return launch_majors<2, 128>(p, m, a, sms, st);
-    return launch_majors<2, 256>(p, m, a, sms, st);
+    if (s == LONE_64) return launch_planes<1, 64>(p, m, a, sms, st);
+    if (s == PAIR_128) return launch_planes<2, 128>(p, m, a, sms, st);
+    return launch_planes<2, 256>(p, m, a, sms, st);
 }
 
 }  // namespace linear
