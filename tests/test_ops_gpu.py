@@ -591,3 +591,76 @@ def test_adamw_captured_with_device_scalars():
         for k in one:
             for a, b in zip(one[k], two[k]):
                 assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), k
+
+
+def test_linear_long_sums_keep_their_bits():
+    """fp32 results of long sums.  The tensor core cuts off, at most 2^-23 of the accumulator for each 16 k.  Three-part
+    products start anew every 64 k (4 cuts at full size, the parts left out another 2^-23), bf16 ones every 512 k (32
+    cuts); the pieces are added in fp32, whose roundings do not add up in one direction."""
+    g = gen(10)
+    for dtype, bound in (("f32", 6 * 2.0 ** -23), ("bf16", 33 * 2.0 ** -23)):
+        for M, K, N in ((40, 65536, 200), (300, 20000, 136)):
+            x, w = randn(g, M, K, dtype=DT[dtype]), randn(g, N, K, dtype=DT[dtype], scale=K ** -0.5)
+            y = B.csa_linear_fwd(B.LinearParams(M, K, N, dtype, "f32"), x, w).double()
+            want = x.double() @ w.double().t()
+            assert float((y - want).norm() / want.norm()) <= bound
+    x, dy = randn(g, 60000, 100), randn(g, 60000, 72)      # a gradient's sum over the rows
+    dw = B.csa_linear_bwd(B.LinearParams(60000, 100, 72, "f32"), dy, x, None, need_dx=False, need_db=False)[1].double()
+    want = dy.double().t() @ x.double()
+    assert float((dw - want).norm() / want.norm()) <= 6 * 2.0 ** -23
+
+
+def test_linear_captured_with_other_inputs():
+    """Captured calls with workspaces of their own, replayed in turn on new inputs."""
+    graphs = []
+    for k, (M, act) in enumerate(((200, "silu"), (3, "none"), (513, "relu"))):
+        t = linear_inputs(M, 136, 72, "bf16", "bf16", 20 + k)
+        p = B.LinearParams(M, 136, 72, activation=act)
+        B.csa_linear_fwd(p, t["x"], t["w"])
+        B.csa_linear_bwd(p, t["dy"], t["x"], t["w"], t["z"])
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            y = B.csa_linear_fwd(p, t["x"], t["w"], t["bias"], t["res"])
+            grads = B.csa_linear_bwd(p, t["dy"], t["x"], t["w"], t["z"])
+        graphs.append((graph, p, t, (y, *grads)))
+    for seed in (30, 40):
+        for k, (graph, p, t, _) in enumerate(graphs):
+            for name, v in linear_inputs(p.c.rows, 136, 72, "bf16", "bf16", seed + k).items():
+                t[name].copy_(v)
+            graph.replay()
+        torch.cuda.synchronize()
+        for graph, p, t, got in graphs:
+            want = (B.csa_linear_fwd(p, t["x"], t["w"], t["bias"], t["res"]), *B.csa_linear_bwd(p, t["dy"], t["x"], t["w"], t["z"]))
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_wrong_tensors_refused_by_the_bindings():
+    p = B.LinearParams(16, 32, 24)
+    x, w = torch.zeros(16, 32, device="cuda").bfloat16(), torch.zeros(24, 32, device="cuda").bfloat16()
+    for bad in (dict(x=x.float()), dict(x=x[:8]), dict(x=x.cpu()), dict(weight=w.t()), dict(weight=w.cpu()), dict(bias=torch.zeros(24, device="cuda").bfloat16()),
+                dict(residual=torch.zeros(16, 24, device="cuda")), dict(out=torch.empty(16, 23, device="cuda").bfloat16()),
+                dict(workspace=torch.empty(8, dtype=torch.uint8)), dict(preact=torch.empty(16, 24, device="cuda"))):
+        args = dict(x=x, weight=w)
+        args.update(bad)
+        with pytest.raises(ValueError):
+            B.csa_linear_fwd(p, args.pop("x"), args.pop("weight"), **args)
+    with pytest.raises(ValueError):   # an activation's gradient needs its argument
+        B.csa_linear_bwd(B.LinearParams(16, 32, 24, activation="relu"), torch.zeros(16, 24, device="cuda").bfloat16(), x, w)
+    r = B.RopeParams(4, 2, 16)
+    y, pos, f = torch.zeros(4, 2, 16, device="cuda").bfloat16(), torch.zeros(1, 4, device="cuda", dtype=torch.int32), torch.ones(8, device="cuda", dtype=torch.float64)
+    for bad in (dict(x=y.float()), dict(positions=pos.long()), dict(positions=pos[:, :3]), dict(inv_freq=f.float()), dict(x=y.transpose(0, 1)),
+                dict(out=y.float())):
+        args = dict(x=y, positions=pos, inv_freq=f)
+        args.update(bad)
+        with pytest.raises(ValueError):
+            B.csa_rope(r, **args)
+    z = B.AdamWTensors.zero_state([x])
+    t = B.AdamWTensors([x], [x.clone()], **z)
+    with pytest.raises(ValueError):
+        B.csa_adamw(t, torch.ones((), device="cuda"))                     # a step count is int64
+    with pytest.raises(ValueError):
+        t.set_grads([x[:3]])
+    with pytest.raises(B.CSAError):
+        B.csa_adamw(t, 0)
