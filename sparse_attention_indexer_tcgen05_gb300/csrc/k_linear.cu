@@ -87,6 +87,8 @@ template <typename V> __device__ __forceinline__ void put_planes8(bf16 *out, lon
 // Up to two operands in one launch.
 template <typename V> __global__ void __launch_bounds__(256) stage_kernel(const Stage s0, const Stage s1)
 {
+    chain_start();
+    chain_wait();
     const Stage &s = blockIdx.x < s0.blocks ? s0 : s1;
     const long long t = ((long long)(blockIdx.x - (blockIdx.x < s0.blocks ? 0u : s0.blocks)) * 256 + threadIdx.x) * (s.vec ? 8 : 1);
     const V *x = static_cast<const V *>(s.x);
@@ -129,6 +131,8 @@ dz_kernel(const O *dy, long long ldy, const V *z, int act, bf16 *dz, long long l
           long long M, int N, int per)
 {
     constexpr int TY = 256 / TX, W = VEC ? 8 : 1;
+    chain_start();
+    chain_wait();
     __shared__ float part[TY][8 * TX + 1];
     const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
     const int n0 = blockIdx.x * 8 * TX, n = n0 + W * tx;
@@ -178,6 +182,8 @@ dz_kernel(const O *dy, long long ldy, const V *z, int act, bf16 *dz, long long l
 __global__ void __launch_bounds__(256) db_kernel(const float *sums, int blocks, int N, float *db)
 {
     __shared__ float part[8][33];
+    chain_start();
+    chain_wait();
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, n = blockIdx.x * 32 + tx;
     float s = 0.f;
     if (n < N)
@@ -196,6 +202,8 @@ __global__ void __launch_bounds__(256) db_kernel(const float *sums, int blocks, 
 template <bool VEC>
 __global__ void __launch_bounds__(256) join_kernel(const float *partial, int splits, long long M, long long N, const Epilogue e)
 {
+    chain_start();
+    chain_wait();
     const long long ldp = partial_stride(N), t = (long long)blockIdx.x * 256 + threadIdx.x;
     const long long m = t / (ldp / 4), n = (t - m * (ldp / 4)) * 4;
     if (m >= M || n >= N) return;
@@ -347,10 +355,7 @@ cudaError_t run_stages(const csa_linear_params &p, const Stage (&job)[2], cudaSt
 {
     const unsigned blocks = job[0].blocks + job[1].blocks;
     if (blocks == 0) return cudaSuccess;
-    if (p.dtype == CSA_F32) stage_kernel<float><<<blocks, 256, 0, st>>>(job[0], job[1]);
-    else stage_kernel<bf16><<<blocks, 256, 0, st>>>(job[0], job[1]);
-    note_launches(1);
-    return cudaGetLastError();
+    return launch_chained(p.dtype == CSA_F32 ? stage_kernel<float> : stage_kernel<bf16>, dim3(blocks), 256, 0, 1, st, job[0], job[1]);
 }
 
 cudaError_t product(const Product &p, cudaStream_t st)
@@ -358,35 +363,26 @@ cudaError_t product(const Product &p, cudaStream_t st)
     const cudaError_t e = launch_product_tc(p, kSms, st);
     if (e != cudaSuccess || p.plan.splits == 1) return e;
     const long long blocks = (p.M * (partial_stride(p.N) / 4) + 255) / 256;
-    if (p.N % 4 == 0) join_kernel<true><<<(unsigned)blocks, 256, 0, st>>>(p.e.partial, p.plan.splits, p.M, p.N, p.e);
-    else join_kernel<false><<<(unsigned)blocks, 256, 0, st>>>(p.e.partial, p.plan.splits, p.M, p.N, p.e);
-    note_launches(1);
-    return cudaGetLastError();
+    return launch_chained(p.N % 4 == 0 ? join_kernel<true> : join_kernel<false>, dim3((unsigned)blocks), 256, 0, 1, st, p.e.partial,
+                          p.plan.splits, p.M, p.N, p.e);
 }
 
 template <typename V, typename O, int TX, bool VEC>
-void run_dz_rows(const csa_linear_params &p, const Bwd &b, const void *dy, const void *z, bf16 *dz, float *sums, cudaStream_t st)
+cudaError_t run_dz_rows(const csa_linear_params &p, const Bwd &b, const void *dy, const void *z, bf16 *dz, float *sums, cudaStream_t st)
 {
     const int N = p.out_features;
     const long long ld = up8(N), plane = p.rows * ld;
     const dim3 grid((N + 8 * TX - 1) / (8 * TX), b.blocks);
-    if (p.activation == CSA_ACT_NONE)
-        dz_kernel<V, O, TX, VEC, 1><<<grid, 256, 0, st>>>((const O *)dy, p.dy_stride, (const V *)z, 0, dz, ld, plane, sums, p.rows, N, b.per);
-    else
-        dz_kernel<V, O, TX, VEC, 2><<<grid, 256, 0, st>>>((const O *)dy, p.dy_stride, (const V *)z, p.activation, dz, ld, plane, sums, p.rows, N, b.per);
+    return launch_chained(p.activation == CSA_ACT_NONE ? dz_kernel<V, O, TX, VEC, 1> : dz_kernel<V, O, TX, VEC, 2>, grid, 256, 0, 1, st,
+                          (const O *)dy, p.dy_stride, (const V *)z, p.activation, dz, ld, plane, sums, p.rows, N, b.per);
 }
 
 template <typename V, typename O>
 cudaError_t run_dz(const csa_linear_params &p, const Bwd &b, const void *dy, const void *z, bf16 *dz, float *sums, cudaStream_t st)
 {
-    const int N = p.out_features;
-    const bool vec = (N & 7) == 0 && (p.dy_stride & 7) == 0;
-    if (N <= 64 && vec) run_dz_rows<V, O, 8, true>(p, b, dy, z, dz, sums, st);
-    else if (N <= 64) run_dz_rows<V, O, 8, false>(p, b, dy, z, dz, sums, st);
-    else if (vec) run_dz_rows<V, O, 32, true>(p, b, dy, z, dz, sums, st);
-    else run_dz_rows<V, O, 32, false>(p, b, dy, z, dz, sums, st);
-    note_launches(1);
-    return cudaGetLastError();
+    const bool vec = (p.out_features & 7) == 0 && (p.dy_stride & 7) == 0;
+    if (p.out_features <= 64) return vec ? run_dz_rows<V, O, 8, true>(p, b, dy, z, dz, sums, st) : run_dz_rows<V, O, 8, false>(p, b, dy, z, dz, sums, st);
+    return vec ? run_dz_rows<V, O, 32, true>(p, b, dy, z, dz, sums, st) : run_dz_rows<V, O, 32, false>(p, b, dy, z, dz, sums, st);
 }
 
 }  // namespace linear
@@ -455,9 +451,7 @@ cudaError_t launch_linear_bwd(const csa_linear_params &p, const void *dy, const 
         else LIN_TRY((run_dz<bf16, bf16>(p, b, dy, preact, dz, sums, st)));
     }
     if (db != nullptr) {
-        db_kernel<<<(p.out_features + 31) / 32, 256, 0, st>>>(sums, b.blocks, p.out_features, db);
-        note_launches(1);
-        LIN_TRY(cudaGetLastError());
+        LIN_TRY(launch_chained(db_kernel, dim3((p.out_features + 31) / 32), 256, 0, 1, st, sums, b.blocks, p.out_features, db));
     }
     Operand d = {};
     d.base = dz != nullptr ? dz : static_cast<const bf16 *>(dy);

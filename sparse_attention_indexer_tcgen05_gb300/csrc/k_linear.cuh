@@ -71,6 +71,32 @@ struct Epilogue {
 // Rows of partial sums start on 32-byte sectors whatever N is.
 __host__ __device__ inline long long partial_stride(long long N) { return (N + 7) & ~7LL; }
 
+// Kernels of one call follow one another closely: each lets the next one's CTAs start as soon as its own are all running
+// (they set up barriers and TMEM meanwhile) and waits for the whole of its predecessors before it touches memory.
+__device__ __forceinline__ void chain_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st, const A &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+    if (e == cudaSuccess) note_launches(1);
+    return e;
+}
+
 // One operand of a product over k: element (i, k) of plane q at base + q * plane + (k_major ? i ld + k : k ld + i).
 // fp32 values are held as three bf16 planes, x = h + m + l.
 struct Operand {

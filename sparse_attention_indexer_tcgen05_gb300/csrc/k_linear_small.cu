@@ -51,6 +51,8 @@ small_kernel(const V *x, long long ldx, const V *w, int M, int N, int K, int ks,
     constexpr int U = MT >= 4 ? 1 : 2;   // vectors along k in flight together
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n0 = (blockIdx.x * (WARPS / ks) + warp / ks) * ROWS, piece = warp % ks;
+    chain_start();
+    chain_wait();
     const V *wr[ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; r++) wr[r] = w + (long long)min(n0 + r, N - 1) * K;
@@ -129,12 +131,8 @@ static cudaError_t launch_rows(const V *x, long long ldx, const V *w, int M, int
     int ks = 1;
     while (ks < WARPS && groups * ks < 16LL * sms && K > 32 * E * ks) ks *= 2;
     const unsigned grid = (unsigned)((groups * ks + WARPS - 1) / WARPS);
-    if (M == 1) small_kernel<V, E, 1><<<grid, 32 * WARPS, 0, st>>>(x, ldx, w, M, N, K, ks, e);
-    else if (M == 2) small_kernel<V, E, 2><<<grid, 32 * WARPS, 0, st>>>(x, ldx, w, M, N, K, ks, e);
-    else if (M <= 4) small_kernel<V, E, 4><<<grid, 32 * WARPS, 0, st>>>(x, ldx, w, M, N, K, ks, e);
-    else small_kernel<V, E, 8><<<grid, 32 * WARPS, 0, st>>>(x, ldx, w, M, N, K, ks, e);
-    note_launches(1);
-    return cudaGetLastError();
+    auto *kernel = M == 1 ? small_kernel<V, E, 1> : M == 2 ? small_kernel<V, E, 2> : M <= 4 ? small_kernel<V, E, 4> : small_kernel<V, E, 8>;
+    return launch_chained(kernel, dim3(grid), 32 * WARPS, 0, 1, st, x, ldx, w, M, N, K, ks, e);
 }
 
 cudaError_t launch_linear_small(const csa_linear_params &p, const void *x, const void *w, const Epilogue &e, int sms,

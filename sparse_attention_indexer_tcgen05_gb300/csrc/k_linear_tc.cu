@@ -301,6 +301,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
     const int u0 = blockIdx.x / CG, ustep = gridDim.x / CG;
+    chain_start();
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; i++) {
@@ -324,6 +325,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     else __syncthreads();
     fence_after();
     const uint32_t tmem = *tmem_slot;
+    chain_wait();
 
     if (warp == 0) {
         // ---------------------------------------------------------- TMA producer
@@ -585,20 +587,7 @@ static cudaError_t launch(const Maps &m, const Args &a, int sms, cudaStream_t st
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::SMEM);
     if (e != cudaSuccess) return e;
     const int slots = sms / CG;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.units < slots ? a.units : slots) * CG));
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = Z::SMEM;
-    cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = CG;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = CG == 2 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, kernel, m.a, m.b, m.half, m.out, a);
-    if (e == cudaSuccess) note_launches(1);
-    return e;
+    return launch_chained(kernel, dim3((unsigned)((a.units < slots ? a.units : slots) * CG)), THREADS, Z::SMEM, CG, st, m.a, m.b, m.half, m.out, a);
 }
 
 template <int CG, int BN, int P, bool EXACT>
