@@ -247,32 +247,22 @@ __device__ __forceinline__ void tma_tile(const CUtensorMap *map, const float (&v
     }
 }
 
-// z = alpha sum + bias, kept if asked for; then act(z), in place.
+// A step's bias, asked for with the residual.  (Loaded where it is added, behind a question for each four columns, it
+// cost 50 us of a product of 8192 x 8192 x 512 that takes 51 without.)
+struct Bias {
+    float own;   // of column n0 + lane; the others come from their lanes (a register instead of 32)
+    __device__ __forceinline__ void load(const Args &a, long long n0, int lane) { own = n0 + lane < a.N ? __ldg(a.e.bias + n0 + lane) : 0.f; }
+    __device__ __forceinline__ void add_to(float alpha, float (&v)[C]) const
+    {
+#pragma unroll
+        for (int k = 0; k < C; k++) v[k] = fmaf(alpha, v[k], __shfl_sync(0xffffffffu, own, k));
+    }
+};
+
+// z kept if asked for, then act(z) in place.
 __device__ __forceinline__ void to_activation(const Args &a, float (&v)[C], long long m0, long long n0, const Buffer &b)
 {
     const Epilogue &e = a.e;
-    if (e.bias != nullptr) {
-#pragma unroll
-        for (int k = 0; k < C / 4; k++) {
-            float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-            const float *p = e.bias + n0 + 4 * k;
-            const long long left = a.N - n0 - 4 * k;
-            if (left >= 4) {
-                q = __ldg(reinterpret_cast<const float4 *>(p));
-            } else {
-                if (left > 0) q.x = __ldg(p);
-                if (left > 1) q.y = __ldg(p + 1);
-                if (left > 2) q.z = __ldg(p + 2);
-            }
-            v[4 * k] = fmaf(e.alpha, v[4 * k], q.x);
-            v[4 * k + 1] = fmaf(e.alpha, v[4 * k + 1], q.y);
-            v[4 * k + 2] = fmaf(e.alpha, v[4 * k + 2], q.z);
-            v[4 * k + 3] = fmaf(e.alpha, v[4 * k + 3], q.w);
-        }
-    } else if (e.alpha != 1.f) {
-#pragma unroll
-        for (int k = 0; k < C; k++) v[k] *= e.alpha;
-    }
     if (e.preact != nullptr) {
         if (e.preact_f32) store_tile<float>((float *)e.preact, a.N, a.M, a.N, v, m0, n0, b);
         else store_tile<__nv_bfloat16>((__nv_bfloat16 *)e.preact, a.N, a.M, a.N, v, m0, n0, b);
@@ -434,8 +424,8 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         const int side = (warp - 2) >> 2;        // half of the columns
         const Buffer b = {smem + Z::TURN + (warp - 2) * 4096, lane};
         // asked once: each of these questions cost a step a miss in the constant and instruction caches
-        const bool plain = a.e.bias == nullptr && a.e.alpha == 1.f && a.e.preact == nullptr && a.e.act == CSA_ACT_NONE && a.e.res == nullptr;
-        const bool tma = a.tma_out != 0, with_res = a.e.res != nullptr;
+        const bool tma = a.tma_out != 0, with_res = a.e.res != nullptr, with_bias = a.e.bias != nullptr, with_act = a.e.act != CSA_ACT_NONE || a.e.preact != nullptr;
+        const float alpha = a.e.alpha;
         auto run = [&](auto type) {
             using O = decltype(type);
             int tc = 0;
@@ -457,20 +447,24 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                     return tmem + (uint32_t)((tc & 1) * BN + side * cols) + ((uint32_t)(quad * 32) << 16);
                 };
                 Residual<O> res;
+                Bias bias;
                 const auto ask = [&](long long n0) {
+                    if (with_bias) bias.load(a, n0, lane);
                     if (with_res && m0 + lane < a.M && n0 < a.N) res.load(a, m0 + lane, n0);
                 };
                 // 32 columns from sums to memory
                 const auto step = [&](int c, float (&v)[C]) {
                     const long long n0 = nb + c;
                     if (m0 >= a.M || n0 >= a.N) return;
-                    if (!plain) {
-                        to_activation(a, v, m0, n0, b);
-                        if (with_res) {
-                            res.add_to(v);
-                            if (c + C < cols) ask(n0 + C);
-                        }
+                    if (with_bias) {
+                        bias.add_to(alpha, v);
+                    } else if (alpha != 1.f) {
+#pragma unroll
+                        for (int k = 0; k < C; k++) v[k] *= alpha;
                     }
+                    if (with_act) to_activation(a, v, m0, n0, b);
+                    if (with_res) res.add_to(v);
+                    if (c + C < cols) ask(n0 + C);
                     if (tma) {
                         const bool second = sizeof(O) == 2 && (c & C) != 0;
                         tma_tile<O>(&map_out, v, m0, n0, x.s, second, sizeof(O) == 4 || second || n0 + C >= a.N, b);
