@@ -267,7 +267,7 @@ struct Fwd {
 Fwd plan_fwd(const csa_linear_params &p)
 {
     Fwd f = {};
-    if (p.rows <= kSmallRows) return f;
+    if (small_linear(p)) return f;
     const long long M = p.rows, K = p.in_features, N = p.out_features;
     f.stage_x = staged(p.dtype, p.x_stride);
     f.stage_w = staged(p.dtype, K);
@@ -411,7 +411,7 @@ cudaError_t launch_linear_fwd(const csa_linear_params &p, const void *x, const v
     q.e.preact = preact;
     q.e.out_f32 = p.out_dtype == CSA_F32;
     q.e.preact_f32 = p.dtype == CSA_F32;
-    if (p.rows <= kSmallRows) {
+    if (small_linear(p)) {
         note_path("generic");
         return launch_linear_small(p, x, weight, q.e, kSms, st);
     }

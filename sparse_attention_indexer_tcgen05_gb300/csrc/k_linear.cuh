@@ -125,8 +125,9 @@ struct Product {
 };
 cudaError_t launch_product_tc(const Product &p, int sms, cudaStream_t st);
 
-// The forward of up to kSmallRows rows without tensor cores (k_linear_small.cu); operands where they are, no workspace.
-constexpr int kSmallRows = 8;
+// The forward of a few rows (k_linear_small.cu); operands where they are, no workspace.
+constexpr int kSmallRows = 8, kFewRows = 16;
+bool small_linear(const csa_linear_params &p);
 cudaError_t launch_linear_small(const csa_linear_params &p, const void *x, const void *w, const Epilogue &e, int sms,
                                 cudaStream_t st);
 

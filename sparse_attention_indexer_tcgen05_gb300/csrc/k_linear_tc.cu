@@ -12,12 +12,15 @@
 // sum; 2e-7 off at k = 65536) or every 512 k (5e-7), and the epilogue's warps add up the pieces in registers, rounded.
 //
 // Mapping.  A unit is one output tile and one piece of the k axis.  A CTA pair (two SMs) computes 256 x BN: each CTA
-// loads its 128 rows of A and its BN / 2 rows of B, so an operand byte brought to an SM feeds twice the MMAs of a
-// lone CTA's 128 x BN tile.  Small M takes lone CTAs with 128 x 64 tiles (more of them, for the memory's sake).
-// Roles: warp 0 the TMA producer, warp 1 the MMA issue (the pair's even CTA), warps 2..9 the epilogue, a row
-// of the tile a lane.  TMEM holds two accumulators, so that a
-// tile's epilogue runs under the next tile's MMAs.  Persistent: one CTA per SM, units
-// dealt round-robin in an order that keeps the running tiles' operands in L2.
+// loads its 128 rows of A and its BN / 2 rows of B, so an operand byte brought to an SM feeds twice the MMAs of a lone
+// CTA's 128 x BN tile.  Few tiles, or few rows, take lone CTAs with 128 x 64 tiles.  Roles: warp 0 the TMA producer,
+// warp 1 the MMA issue (the pair's even CTA), warps 2..9 the epilogue, a row of the tile a lane.  TMEM holds two
+// accumulators, so that a tile's epilogue runs under the next tile's MMAs.  Persistent: one CTA per SM, units dealt
+// round-robin in an order that keeps the running tiles' operands in L2.
+//
+// Measured (bf16, from and to bf16): 8192 x 8192 x 2048 142 us (1.94 PFLOP/s, what the library's product takes: 140 us),
+// its two gradients 151 and 163 us (153 and 163), 8192^3 591 us (592), 2048^3 15 us (22).  Bound by the MMAs (88% of the
+// cycles), and at the chip's power limit by its clock.
 //
 // Every mbarrier wait is bounded (see tc_ptx.cuh); site codes 600 + n.
 #include "csa_tc.cuh"
@@ -68,6 +71,7 @@ struct Args {
     int splits, per_split;      // k pieces, stages of each
     int mt, nt;                 // tiles
     int whole, units;           // units that are whole tiles (times splits); the rest are halves of the last tiles
+    int rows_a;                 // rows of A a CTA loads: BM, fewer where M is below BM
     int blocks_a, blocks_b;     // an m/n-contiguous operand's map has 64-wide blocks as an axis of their own
     int tma_out;                // the output goes by TMA
     int res32;                  // the residual's rows start on 32-byte sectors
@@ -215,8 +219,8 @@ __device__ __forceinline__ void store_tile(O *out, long long ld, long long M, lo
 }
 
 // The same by TMA, from rows of 128 bytes in shared memory (32 fp32 columns, or 64 bf16 ones: two steps), so that a
-// request to L2 carries four sectors.  (The lanes' own sectors slowed the loads of the next tile: 150 us a product
-// of 8192 x 8192 x 2048 instead of 148, and 640 instead of 572 at k = 8192.)  `second`: the right 64 bytes of bf16
+// request to L2 carries four sectors.  (The lanes' own sectors slowed the loads of the next tile: a product
+// of 8192 x 8192 x 8192 took 640 us instead of 572.)  `second`: the right 64 bytes of bf16
 // rows; `go`: the rows are complete.
 template <typename O>
 __device__ __forceinline__ void tma_tile(const CUtensorMap *map, const float (&v)[C], long long m0, long long n0, int s, bool second, bool go,
@@ -340,7 +344,12 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                 const bool half = x.bn != BN;
                 const int am = (x.m * CG + (int)rank) * BM;
                 const int rows_b = x.bn / CG, bn = (int)x.n0 + (int)rank * rows_b;
-                const uint32_t bytes = CG * P * (Z::A_BYTES + rows_b * BK * 2);
+                // rows of A that do not exist are not asked for (TMA would send their zeros over the crossbar: 100 MB
+                // instead of 45 for 37 rows against 8192 x 2048 weights); what lies in their place in shared memory
+                // reaches sums of such rows only
+                const bool with_a = am < a.M;
+                const int ctas_a = CG == 2 && (x.m * 2 + 1LL) * BM < a.M ? 2 : 1;
+                const uint32_t bytes = P * (ctas_a * a.rows_a + CG * rows_b) * BK * 2;
                 const CUtensorMap *mb = half ? &map_half : &map_b;
                 for (int k = x.it0 * BK; k < x.it1 * BK; k += BK) {
                     wait_bar(empty + st, ph ^ 1, abort_flag, &g_lin_error, 601);
@@ -348,12 +357,13 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
 #pragma unroll
                     for (int q = 0; q < P; q++) {
                         unsigned char *sa = smem + st * Z::STAGE + q * Z::A_BYTES, *sb = smem + st * Z::STAGE + P * Z::A_BYTES + q * Z::B_BYTES;
-                        if constexpr (A_K) {
+                        if (!with_a) {
+                        } else if constexpr (A_K) {
                             load3(sa, &map_a, st, k, am, q);
                         } else if (a.blocks_a) {
                             load4(sa, &map_a, st, 0, k, am >> 6, q);
                         } else {
-                            for (int i = 0; i < BM; i += 64) load3(sa + i * 128, &map_a, st, am + i, k, q);
+                            for (int i = 0; i < a.rows_a; i += 64) load3(sa + i * 128, &map_a, st, am + i, k, q);
                         }
                         if constexpr (B_K) {
                             load3(sb, mb, st, k, bn, q);
@@ -531,13 +541,14 @@ static void tile_counts(Shape s, long long M, long long N, int &mt, int &nt)
     nt = (int)((N + bn - 1) / bn);
 }
 
-// Tile and cut of the k axis by estimated time, of which this is the model (fitted to 40 timings of products from
-// 37 x 2048 x 8192 to 2048^3 and 64 x 512 x 16384, most of them within 10%; us):
+// Tile and cut of the k axis by estimated time, of which this is the model (fitted to the timings of 20 products, from
+// 37 x 2048 x 8192 to 2048^3 and 64 x 512 x 16384, with every tile and several cuts: its choice takes at most 15% more
+// than the best of them, mostly 2%; us):
 //   a stage of a unit: 128 x 64 and 256 x 128 tiles 0.20 (the loads), 256 x 256 0.28 (the MMAs' own 512 cycles); of three
 //   planes, six products, 0.72 and 0.90;
 //   a round is no shorter than its epilogue: 0.9, 1.7 and 2.9;
 //   launch, first loads and last epilogue: 3.8, 5.2 and 6.3;
-//   a cut k axis: another launch, 3.4, and the pieces' way to memory and back at 4 TB/s.
+//   a cut k axis: another launch, 2.5, and the pieces' way to memory and back at 4 TB/s.
 // Units run in rounds of one per SM or pair.
 Plan plan_product(long long M, long long N, long long K, int planes, bool out_f32, int sms)
 {
@@ -558,7 +569,7 @@ Plan plan_product(long long M, long long N, long long K, int planes, bool out_f3
             double rounds = floor(tiles * pieces / slots), rest = tiles * pieces - rounds * slots;
             if (rest > 0) rounds += shape == PAIR_256 && pieces == 1 && rounds > 0 && 2 * rest <= slots ? 0.5 : 1.0;
             double us = rounds * fmax(per * step, EPILOGUE[s]) + FIXED[s];
-            if (pieces > 1) us += 3.4 + (double)M * N * 8 * pieces / 4e6;
+            if (pieces > 1) us += 2.5 + (double)M * N * 8 * pieces / 4e6;
             if (us < least) {
                 least = us;
                 best.shape = shape;
@@ -664,9 +675,10 @@ cudaError_t launch_product_tc(const Product &p, int sms, cudaStream_t st)
                 (a.e.preact == nullptr || (p.N % (a.e.preact_f32 ? 8 : 16) == 0 && (reinterpret_cast<uintptr_t>(a.e.preact) & 31) == 0));
     a.blocks_a = !p.a.k_major && p.M % 64 == 0;
     a.blocks_b = !p.b.k_major && p.N % 64 == 0;
+    a.rows_a = p.M >= BM ? BM : p.a.k_major ? (int)((p.M + 7) & ~7LL) : p.M > 64 ? 128 : 64;
     Maps m = {};
     const int rows_b = s == PAIR_256 ? 128 : 64;
-    bool ok = encode(&m.a, p.a, p.M, p.K, p.planes, BM, a.blocks_a) && encode(&m.b, p.b, p.N, p.K, p.planes, rows_b, a.blocks_b);
+    bool ok = encode(&m.a, p.a, p.M, p.K, p.planes, a.rows_a, a.blocks_a) && encode(&m.b, p.b, p.N, p.K, p.planes, rows_b, a.blocks_b);
     if (a.units > a.whole) ok = ok && encode(&m.half, p.b, p.N, p.K, p.planes, rows_b / 2, a.blocks_b);
     if (a.tma_out) ok = ok && encode_out(&m.out, a.e.out_f32, a.e.out, p.N, a.ldo, p.M, splits);
     if (!ok) return cudaErrorInvalidValue;
