@@ -368,7 +368,8 @@ csa_status csa_selftest_bounded_wait(void *stream);
 int32_t csa_last_timeout_site(void);
 
 /* Name of the last kernel path csa_indexer_fwd, csa_teacher, csa_teacher_from_lse or csa_indexer_bwd chose
- * on this host thread ("tcgen05", "generic", ...; for csa_indexer_bwd, its backward's).  Static string. */
+ * on this host thread ("tcgen05", "generic", ...; for csa_indexer_bwd, its backward's), or of csa_linear_fwd ("tcgen05",
+ * or "generic" for few rows) and csa_linear_bwd.  Static string. */
 const char *csa_last_path(void);
 
 /* Message of the last CUDA runtime error that ended a call of this library with CSA_ERR_CUDA on this host

@@ -40,30 +40,42 @@ struct Stage {
     const void *x;
     bf16 *out;
     long long stride, rows, ld, plane;
-    int cols, vec;       // vec: whole vectors of 8, aligned
+    int cols, aligned;   // rows start on 16-byte boundaries
     unsigned blocks;     // of 256 threads, 8 values each
 };
 
-// 8 columns of one row: V neighbours from n on where V = 8, else every TX-th from n on; 0 behind the end.
-template <typename T, int V, int TX> __device__ __forceinline__ void load_cols(const T *row, int n, int N, float (&x)[8])
+// 8 neighbouring values from p on, of which `valid` (1 to 8) exist; the others 0.  ALIGNED: p lies on 16 bytes and all
+// exist.  Otherwise p lies anywhere: the aligned vectors that hold the existing values are loaded and shifted.
+template <typename T, bool ALIGNED> __device__ __forceinline__ void load8(const T *p, int valid, float (&x)[8])
 {
-    if constexpr (V == 8) {
-        if constexpr (sizeof(T) == 2) {
-            const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(row + n));
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+    constexpr int V = sizeof(T) == 2 ? 1 : 2;            // vectors of 8 values
+    const uint32_t sh = ALIGNED ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
+    const uint4 *q = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) - sh);
+    uint32_t w[4 * V + 4];
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
-                x[2 * k] = __uint_as_float(w[k] << 16);
-                x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-            }
-        } else {
-            const float4 a = __ldcs(reinterpret_cast<const float4 *>(row + n)), b = __ldcs(reinterpret_cast<const float4 *>(row + n) + 1);
-            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-            x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    for (int k = 0; k <= V; k++) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (ALIGNED ? k < V : sh + valid * (int)sizeof(T) > 16 * k) v = __ldcs(q + k);
+        w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
+    }
+    if (!ALIGNED) {
+        if (sh & 8) {
+#pragma unroll
+            for (int k = 0; k < 4 * V + 2; k++) w[k] = w[k + 2];
         }
-    } else {
+        if (sh & 4) {
 #pragma unroll
-        for (int j = 0; j < 8; j++) x[j] = n + TX * j < N ? ldf<T>(row, n + TX * j) : 0.f;
+            for (int k = 0; k < 4 * V + 1; k++) w[k] = w[k + 1];
+        }
+        if (sizeof(T) == 2 && (sh & 2)) {
+#pragma unroll
+            for (int k = 0; k < 4; k++) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+        const uint32_t b = sizeof(T) == 4 ? w[k] : k % 2 == 0 ? w[k / 2] << 16 : w[k / 2] & 0xffff0000u;
+        x[k] = ALIGNED || k < valid ? __uint_as_float(b) : 0.f;
     }
 }
 
@@ -84,58 +96,39 @@ template <typename V> __device__ __forceinline__ void put_planes8(bf16 *out, lon
     for (int q = 0; q < P; q++) *reinterpret_cast<uint4 *>(out + q * plane + at) = *reinterpret_cast<const uint4 *>(w[q]);
 }
 
-// Up to two operands in one launch.
+// Up to two operands in one launch; a thread makes 8 neighbouring values of a row.
 template <typename V> __global__ void __launch_bounds__(256) stage_kernel(const Stage s0, const Stage s1)
 {
     chain_start();
     chain_wait();
     const Stage &s = blockIdx.x < s0.blocks ? s0 : s1;
-    const long long t = ((long long)(blockIdx.x - (blockIdx.x < s0.blocks ? 0u : s0.blocks)) * 256 + threadIdx.x) * (s.vec ? 8 : 1);
-    const V *x = static_cast<const V *>(s.x);
-    if (s.vec) {
-        const long long r = t / s.cols, c = t - r * s.cols;
-        if (r >= s.rows) return;
-        float v[8];
-        load_cols<V, 8, 1>(x + r * s.stride, (int)c, s.cols, v);
-        put_planes8<V>(s.out, s.plane, r * s.ld + c, v);
-    } else {
-        // 8 values a thread, 256 apart
-        const long long first = (t / 256) * 2048 + t % 256;
-        long long r = first / s.cols;
-        int c = (int)(first - r * s.cols);
-        float v[8];
-        long long at[8];
-#pragma unroll
-        for (int k = 0; k < 8; k++) {
-            at[k] = r < s.rows ? r * s.ld + c : -1;
-            v[k] = r < s.rows ? ldf<V>(x, r * s.stride + c) : 0.f;
-            c += 256;
-            while (c >= s.cols) {
-                c -= s.cols;
-                r++;
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < 8; k++)
-            if (at[k] >= 0) put_planes<V>(s.out, s.plane, at[k], v[k]);
-    }
+    const long long t = (long long)(blockIdx.x - (blockIdx.x < s0.blocks ? 0u : s0.blocks)) * 256 + threadIdx.x;
+    const int chunks = (s.cols + 7) / 8;
+    const long long r = t <= 0xffffffffLL ? (long long)((uint32_t)t / (uint32_t)chunks) : t / chunks;
+    if (r >= s.rows) return;
+    const int c = (int)(t - r * chunks) * 8;
+    const V *x = static_cast<const V *>(s.x) + r * s.stride + c;
+    float v[8];
+    if (s.aligned && c + 8 <= s.cols) load8<V, true>(x, 8, v);
+    else load8<V, false>(x, min(8, s.cols - c), v);
+    put_planes8<V>(s.out, s.plane, r * s.ld + c, v);
 }
 
 // dz = dy act'(z) for `per` rows of a block and 8 TX columns, and their column sums for db.  Bound by memory: dy and
-// z are read once, dz is written once.  VEC: 8 neighbouring columns a thread (16-byte accesses), where the row strides
-// allow it.  ROWS of a thread are in flight together: two with an activation, one (and twice the CTAs on an SM) without:
+// z are read once, dz is written once, 8 neighbouring columns a thread (VEC: aligned ones).  ROWS of a thread are in flight together: two with an
+// activation and aligned rows, else one (and more CTAs on an SM):
 // db alone of 8192 x 8192 values takes 28 us so, and 52 with two.
 template <typename V, typename O, int TX, bool VEC, int ROWS>
-__global__ void __launch_bounds__(256, ROWS == 1 ? 6 : 3)
+__global__ void __launch_bounds__(256, ROWS == 2 ? 3 : VEC ? 6 : 4)
 dz_kernel(const O *dy, long long ldy, const V *z, int act, bf16 *dz, long long ld, long long plane, float *sums,
           long long M, int N, int per)
 {
-    constexpr int TY = 256 / TX, W = VEC ? 8 : 1;
+    constexpr int TY = 256 / TX;
     chain_start();
     chain_wait();
     __shared__ float part[TY][8 * TX + 1];
     const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
-    const int n0 = blockIdx.x * 8 * TX, n = n0 + W * tx;
+    const int n0 = blockIdx.x * 8 * TX, n = n0 + 8 * tx, valid = min(8, N - n);
     const long long r0 = (long long)blockIdx.y * per, r1 = min(M, r0 + per);
     float s[8] = {};
     if (n < N) {
@@ -144,8 +137,8 @@ dz_kernel(const O *dy, long long ldy, const V *z, int act, bf16 *dz, long long l
 #pragma unroll
             for (int i = 0; i < ROWS; i++)
                 if (r + TY * i < r1) {
-                    load_cols<O, W, TX>(dy + (r + TY * i) * ldy, n, N, d[i]);
-                    if (act != CSA_ACT_NONE) load_cols<V, W, TX>(z + (r + TY * i) * N, n, N, q[i]);
+                    load8<O, VEC>(dy + (r + TY * i) * ldy + n, valid, d[i]);
+                    if (act != CSA_ACT_NONE) load8<V, VEC>(z + (r + TY * i) * N + n, valid, q[i]);
                 }
 #pragma unroll
             for (int i = 0; i < ROWS; i++) {
@@ -156,20 +149,13 @@ dz_kernel(const O *dy, long long ldy, const V *z, int act, bf16 *dz, long long l
                     if (act != CSA_ACT_NONE) d[i][j] = __fmul_rn(d[i][j], act_grad(q[i][j], act));
                     s[j] += d[i][j];
                 }
-                if (dz == nullptr) continue;
-                if constexpr (VEC) {
-                    put_planes8<V>(dz, plane, (r + TY * i) * ld + n, d[i]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; j++)
-                        if (n + TX * j < N) put_planes<V>(dz, plane, (r + TY * i) * ld + n + TX * j, d[i][j]);
-                }
+                if (dz != nullptr) put_planes8<V>(dz, plane, (r + TY * i) * ld + n, d[i]);  // up to 7 values of padding
             }
         }
     }
     if (sums == nullptr) return;
 #pragma unroll
-    for (int j = 0; j < 8; j++) part[ty][VEC ? 8 * tx + j : tx + TX * j] = s[j];
+    for (int j = 0; j < 8; j++) part[ty][8 * tx + j] = s[j];
     __syncthreads();
     for (int c = threadIdx.x; c < 8 * TX; c += 256) {
         float t = 0.f;
@@ -179,20 +165,23 @@ dz_kernel(const O *dy, long long ldy, const V *z, int act, bf16 *dz, long long l
     }
 }
 
-__global__ void __launch_bounds__(256) db_kernel(const float *sums, int blocks, int N, float *db)
+__global__ void __launch_bounds__(1024) db_kernel(const float *sums, int blocks, int N, float *db)
 {
-    __shared__ float part[8][33];
+    __shared__ float part[32][33];
     chain_start();
     chain_wait();
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, n = blockIdx.x * 32 + tx;
     float s = 0.f;
-    if (n < N)
-        for (int b = ty; b < blocks; b += 8) s += sums[(long long)b * N + n];
+    if (n < N) {
+#pragma unroll 8
+        for (int b = ty; b < blocks; b += 32) s += sums[(long long)b * N + n];
+    }
     part[ty][tx] = s;
     __syncthreads();
     if (ty == 0 && n < N) {
         float t = 0.f;
-        for (int k = 0; k < 8; k++) t += part[k][tx];
+#pragma unroll
+        for (int k = 0; k < 32; k++) t += part[k][tx];
         db[n] = t;
     }
 }
@@ -346,8 +335,8 @@ Operand operand(const csa_linear_params &p, const void *x, long long stride, lon
     job->ld = o.ld;
     job->plane = o.plane;
     job->cols = cols;
-    job->vec = cols % 8 == 0 && stride % (p.dtype == CSA_F32 ? 4 : 8) == 0;
-    job->blocks = (unsigned)((rows * cols + 2047) / 2048);
+    job->aligned = stride % (p.dtype == CSA_F32 ? 4 : 8) == 0;
+    job->blocks = (unsigned)((rows * ((cols + 7) / 8) + 255) / 256);
     return o;
 }
 
@@ -373,7 +362,7 @@ cudaError_t run_dz_rows(const csa_linear_params &p, const Bwd &b, const void *dy
     const int N = p.out_features;
     const long long ld = up8(N), plane = p.rows * ld;
     const dim3 grid((N + 8 * TX - 1) / (8 * TX), b.blocks);
-    return launch_chained(p.activation == CSA_ACT_NONE ? dz_kernel<V, O, TX, VEC, 1> : dz_kernel<V, O, TX, VEC, 2>, grid, 256, 0, 1, st,
+    return launch_chained(p.activation != CSA_ACT_NONE && VEC ? dz_kernel<V, O, TX, VEC, VEC ? 2 : 1> : dz_kernel<V, O, TX, VEC, 1>, grid, 256, 0, 1, st,
                           (const O *)dy, p.dy_stride, (const V *)z, p.activation, dz, ld, plane, sums, p.rows, N, b.per);
 }
 
@@ -451,7 +440,7 @@ cudaError_t launch_linear_bwd(const csa_linear_params &p, const void *dy, const 
         else LIN_TRY((run_dz<bf16, bf16>(p, b, dy, preact, dz, sums, st)));
     }
     if (db != nullptr) {
-        LIN_TRY(launch_chained(db_kernel, dim3((p.out_features + 31) / 32), 256, 0, 1, st, sums, b.blocks, p.out_features, db));
+        LIN_TRY(launch_chained(db_kernel, dim3((p.out_features + 31) / 32), 1024, 0, 1, st, sums, b.blocks, p.out_features, db));
     }
     Operand d = {};
     d.base = dz != nullptr ? dz : static_cast<const bf16 *>(dy);

@@ -185,6 +185,32 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// The second half of a turn: V neighbouring columns a lane, 32 / V lanes a row.  Rows start on V values.
+template <typename O, int V>
+__device__ __forceinline__ void turned_rows(O *out, long long ld, long long M, long long N, long long m0, long long n0, int lane, const float *turn)
+{
+    constexpr int LANES = 32 / V;
+    const int c = lane % LANES * V;
+    if (n0 + c >= N) return;
+    const int rows = (int)min(32LL, M - m0);
+    O *p = out + m0 * ld + n0 + c;
+#pragma unroll 4
+    for (int r = lane / LANES; r < rows; r += V) {
+        float x[V];
+#pragma unroll
+        for (int k = 0; k < V; k++) x[k] = turn[r * 32 + ((c + k + r) & 31)];
+        O *q = p + r * ld;
+        if (V > 1 && n0 + c + V <= N) {
+            if constexpr (sizeof(O) == 4 && V == 2) *reinterpret_cast<float2 *>(q) = make_float2(x[0], x[1]);
+            else if constexpr (V == 2) *reinterpret_cast<uint32_t *>(q) = pack2(x[0], x[1]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < V; k++)
+                if (n0 + c + k < N) q[k] = from_f<O>(x[k]);
+        }
+    }
+}
+
 // A warp's 32 rows x 32 columns, a row a lane, to memory by the lanes' own stores; rows from M and columns from N on
 // are left out.  Rows on 32-byte boundaries: each lane its own sectors.  Else: turned in shared memory so that a warp
 // writes 32 neighbouring values at a time.
@@ -210,11 +236,9 @@ __device__ __forceinline__ void store_tile(O *out, long long ld, long long M, lo
 #pragma unroll
         for (int k = 0; k < C; k++) turn[lane * 32 + ((k + lane) & 31)] = v[k];
         __syncwarp();
-        if (n0 + lane < N) {
-#pragma unroll 8
-            for (int r = 0; r < 32; r++)
-                if (m0 + r < M) out[(m0 + r) * ld + n0 + lane] = from_f<O>(turn[r * 32 + ((lane + r) & 31)]);
-        }
+        const int odd = (int)(ld | (reinterpret_cast<uintptr_t>(out) / sizeof(O)));
+        if ((odd & 1) == 0) turned_rows<O, 2>(out, ld, M, N, m0, n0, lane, turn);
+        else turned_rows<O, 1>(out, ld, M, N, m0, n0, lane, turn);
     }
 }
 
