@@ -45,38 +45,53 @@ struct Stage {
 };
 
 // 8 neighbouring values from p on, of which `valid` (1 to 8) exist; the others 0.  ALIGNED: p lies on 16 bytes and all
-// exist.  Otherwise p lies anywhere: the aligned vectors that hold the existing values are loaded and shifted.
+// exist.  Otherwise p lies anywhere: the aligned vectors that hold the existing values are loaded, and shifted when the
+// values are taken.
+template <typename T, bool ALIGNED> struct Raw8 {
+    static constexpr int V = sizeof(T) == 2 ? 1 : 2;   // vectors of 8 values
+    uint32_t w[4 * V + (ALIGNED ? 0 : 4)], sh;
+    __device__ __forceinline__ void load(const T *p, int valid)
+    {
+        sh = ALIGNED ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
+        const uint4 *q = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) - sh);
+#pragma unroll
+        for (int k = 0; k < V + (ALIGNED ? 0 : 1); k++) {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (ALIGNED || (int)sh + valid * (int)sizeof(T) > 16 * k) v = __ldcs(q + k);
+            w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
+        }
+    }
+    __device__ __forceinline__ void floats(int valid, float (&x)[8]) const
+    {
+        uint32_t u[4 * V + 4];
+#pragma unroll
+        for (int k = 0; k < 4 * V + 4; k++) u[k] = k < 4 * V + (ALIGNED ? 0 : 4) ? w[k] : 0u;
+        if (!ALIGNED) {
+            if (sh & 8) {
+#pragma unroll
+                for (int k = 0; k < 4 * V + 2; k++) u[k] = u[k + 2];
+            }
+            if (sh & 4) {
+#pragma unroll
+                for (int k = 0; k < 4 * V + 1; k++) u[k] = u[k + 1];
+            }
+            if (sizeof(T) == 2 && (sh & 2)) {
+#pragma unroll
+                for (int k = 0; k < 4; k++) u[k] = __funnelshift_r(u[k], u[k + 1], 16);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            const uint32_t b = sizeof(T) == 4 ? u[k] : k % 2 == 0 ? u[k / 2] << 16 : u[k / 2] & 0xffff0000u;
+            x[k] = ALIGNED || k < valid ? __uint_as_float(b) : 0.f;
+        }
+    }
+};
 template <typename T, bool ALIGNED> __device__ __forceinline__ void load8(const T *p, int valid, float (&x)[8])
 {
-    constexpr int V = sizeof(T) == 2 ? 1 : 2;            // vectors of 8 values
-    const uint32_t sh = ALIGNED ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
-    const uint4 *q = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) - sh);
-    uint32_t w[4 * V + 4];
-#pragma unroll
-    for (int k = 0; k <= V; k++) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (ALIGNED ? k < V : sh + valid * (int)sizeof(T) > 16 * k) v = __ldcs(q + k);
-        w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
-    }
-    if (!ALIGNED) {
-        if (sh & 8) {
-#pragma unroll
-            for (int k = 0; k < 4 * V + 2; k++) w[k] = w[k + 2];
-        }
-        if (sh & 4) {
-#pragma unroll
-            for (int k = 0; k < 4 * V + 1; k++) w[k] = w[k + 1];
-        }
-        if (sizeof(T) == 2 && (sh & 2)) {
-#pragma unroll
-            for (int k = 0; k < 4; k++) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < 8; k++) {
-        const uint32_t b = sizeof(T) == 4 ? w[k] : k % 2 == 0 ? w[k / 2] << 16 : w[k / 2] & 0xffff0000u;
-        x[k] = ALIGNED || k < valid ? __uint_as_float(b) : 0.f;
-    }
+    Raw8<T, ALIGNED> r;
+    r.load(p, valid);
+    r.floats(valid, x);
 }
 
 template <typename V> __device__ __forceinline__ void put_planes8(bf16 *out, long long plane, long long at, const float (&x)[8])
@@ -115,11 +130,11 @@ template <typename V> __global__ void __launch_bounds__(256) stage_kernel(const 
 }
 
 // dz = dy act'(z) for `per` rows of a block and 8 TX columns, and their column sums for db.  Bound by memory: dy and
-// z are read once, dz is written once, 8 neighbouring columns a thread (VEC: aligned ones).  ROWS of a thread are in flight together: two with an
-// activation and aligned rows, else one (and more CTAs on an SM):
-// db alone of 8192 x 8192 values takes 28 us so, and 52 with two.
-template <typename V, typename O, int TX, bool VEC, int ROWS>
-__global__ void __launch_bounds__(256, ROWS == 2 ? 3 : VEC ? 6 : 4)
+// z are read once, dz is written once, 8 neighbouring columns a thread (VEC: aligned ones), the next row's on their way
+// while a row is worked on: bf16 silu of 8192 x 8192 values 65 us (403 MB), db alone 30.  (Two rows loaded and then worked on: 79
+// and 52.)
+template <typename V, typename O, int TX, bool VEC>
+__global__ void __launch_bounds__(256, 4)
 dz_kernel(const O *dy, long long ldy, const V *z, int act, bf16 *dz, long long ld, long long plane, float *sums,
           long long M, int N, int per)
 {
@@ -132,25 +147,28 @@ dz_kernel(const O *dy, long long ldy, const V *z, int act, bf16 *dz, long long l
     const long long r0 = (long long)blockIdx.y * per, r1 = min(M, r0 + per);
     float s[8] = {};
     if (n < N) {
-        for (long long r = r0 + ty; r < r1; r += TY * ROWS) {
-            float d[ROWS][8], q[ROWS][8];
+        Raw8<O, VEC> d0, d1;
+        Raw8<V, VEC> z0, z1;
+        const auto ask = [&](long long r) {
+            if (r >= r1) return;
+            d1.load(dy + r * ldy + n, valid);
+            if (act != CSA_ACT_NONE) z1.load(z + r * N + n, valid);
+        };
+        ask(r0 + ty);
+        for (long long r = r0 + ty; r < r1; r += TY) {
+            d0 = d1;
+            z0 = z1;
+            ask(r + TY);
+            float d[8], q[8];
+            d0.floats(valid, d);
+            if (act != CSA_ACT_NONE) z0.floats(valid, q);
 #pragma unroll
-            for (int i = 0; i < ROWS; i++)
-                if (r + TY * i < r1) {
-                    load8<O, VEC>(dy + (r + TY * i) * ldy + n, valid, d[i]);
-                    if (act != CSA_ACT_NONE) load8<V, VEC>(z + (r + TY * i) * N + n, valid, q[i]);
-                }
-#pragma unroll
-            for (int i = 0; i < ROWS; i++) {
-                if (r + TY * i >= r1) break;
-#pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    // rounded before it is added, whichever outputs are asked for
-                    if (act != CSA_ACT_NONE) d[i][j] = __fmul_rn(d[i][j], act_grad(q[i][j], act));
-                    s[j] += d[i][j];
-                }
-                if (dz != nullptr) put_planes8<V>(dz, plane, (r + TY * i) * ld + n, d[i]);  // up to 7 values of padding
+            for (int j = 0; j < 8; j++) {
+                // rounded before it is added, whichever outputs are asked for
+                if (act != CSA_ACT_NONE) d[j] = __fmul_rn(d[j], act_grad(q[j], act));
+                s[j] += d[j];
             }
+            if (dz != nullptr) put_planes8<V>(dz, plane, r * ld + n, d);  // up to 7 values of padding
         }
     }
     if (sums == nullptr) return;
@@ -287,9 +305,9 @@ Bwd plan_bwd(const csa_linear_params &p)
     b.stage_x = staged(p.dtype, p.x_stride);
     b.stage_w = staged(p.dtype, K);
     b.stage_dz = p.activation != CSA_ACT_NONE || p.dtype != p.out_dtype || staged(p.dtype, p.dy_stride);
-    // rows of a block of dz_kernel: enough blocks to fill the GPU many times, a row of each thread at least
+    // rows of a block of dz_kernel: enough blocks to fill the GPU twice, a row of each thread at least
     const long long cols = N <= 64 ? 1 : (N + 255) / 256, least = N <= 64 ? 32 : 8;
-    const long long want = (p.activation != CSA_ACT_NONE ? 24 : 8) * kSms;
+    const long long want = 8 * kSms;
     long long per = (M * cols + want - 1) / want;
     if (per < least) per = least;
     b.per = (int)(per < M ? per : M);
@@ -362,7 +380,7 @@ cudaError_t run_dz_rows(const csa_linear_params &p, const Bwd &b, const void *dy
     const int N = p.out_features;
     const long long ld = up8(N), plane = p.rows * ld;
     const dim3 grid((N + 8 * TX - 1) / (8 * TX), b.blocks);
-    return launch_chained(p.activation != CSA_ACT_NONE && VEC ? dz_kernel<V, O, TX, VEC, VEC ? 2 : 1> : dz_kernel<V, O, TX, VEC, 1>, grid, 256, 0, 1, st,
+    return launch_chained(dz_kernel<V, O, TX, VEC>, grid, 256, 0, 1, st,
                           (const O *)dy, p.dy_stride, (const V *)z, p.activation, dz, ld, plane, sums, p.rows, N, b.per);
 }
 
