@@ -262,7 +262,8 @@ size_t csa_linear_bwd_workspace_size(const csa_linear_params *p);
  * Sums and the epilogue are fp32, rounded once (a bf16 result's sums are cut off where the tensor core aligns them,
  * 2^-24 of the sum for each 16 k; those of an fp32 result are kept).  fp32 values are multiplied as three bf16 parts
  * each (six products, about 2^-23 relative to the terms); an infinite fp32 value (or one above the largest bf16,
- * 3.39e38) gives its row NaN or an infinity.  y may be the residual itself when their row strides agree. */
+ * 3.39e38) gives its row NaN or an infinity.  y may be the residual itself when their row strides agree;
+ * an output given as another argument is refused otherwise.  rows and features up to 2^31 - 2^16. */
 csa_status csa_linear_fwd(const csa_linear_params *p, const void *x, const void *weight, const float *bias,
                           const void *residual, void *y, void *preact, void *workspace, size_t workspace_bytes,
                           void *stream);
@@ -296,9 +297,10 @@ typedef struct {
 } csa_rope_params;
 
 /*   x, positions [axes, rows], inv_freq [rot_dim / 2] fp64 -> out.
- * out may be x itself with the same strides (the values outside the rotation are then left as they are).  Angles are
- * exact modulo one turn for every position the type holds, negative ones too: a frequency is kept as a 64-bit
- * fraction of a turn and multiplied in integers.  inv_freq holds finite values. */
+ * out may be x itself with the same strides (the values outside the rotation are then left as they are).  An angle is
+ * the position times the frequency as fp64 and 64 bits of a turn hold it (off by 2^-53 of frequency / 2 pi and 2^-65),
+ * multiplied in integers: whole turns drop out without a rounding for every position, negative ones too.  inv_freq
+ * holds finite values. */
 csa_status csa_rope(const csa_rope_params *p, const void *x, const void *positions, const double *inv_freq, void *out,
                     void *stream);
 
@@ -328,7 +330,7 @@ typedef struct {
     double lr, beta1, beta2, eps, weight_decay;  /* finite; 0 <= beta < 1, eps >= 0 */
     int64_t step;                /* 1 for the first step */
     const float *lr_dev;         /* device scalar that replaces lr, or NULL (for a captured graph) */
-    const int64_t *step_dev;     /* device scalar that replaces step, or NULL */
+    const int64_t *step_dev;     /* device scalar that replaces step, or NULL; below 1 it counts as 1 */
     const float *grad_scale;     /* device scalar that every gradient is multiplied by (clipping), or NULL */
     const float *found_inf;      /* device scalar or NULL: not 0 leaves every tensor and state as it is */
 } csa_adamw_params;

@@ -17,8 +17,9 @@ Around the step (what makes q_idx, w and k_idx out of hidden states, and updates
     csa_rope(params, x, positions, inv_freq)                        -> out          (rotary positions; also their gradient)
     csa_adamw(tensors, step, ...)                                                   (AdamW over many tensors, in place)
 
-with ``CSALinear`` / ``csa_linear`` and ``CSARope`` / ``csa_rotary`` as their autograd forms, and ``CSAIndexerLoss`` wraps the step as an autograd function (forward returns ids and the loss; backward
-returns the stored indexer gradients scaled by the incoming gradient).
+with ``CSALinear`` / ``csa_linear`` and ``CSARope`` / ``csa_rotary`` as their autograd forms.  ``CSAIndexerLoss`` wraps
+the step as an autograd function (forward returns ids and the loss; backward returns the stored indexer gradients
+scaled by the incoming gradient).
 
 Importing this module loads the library and raises ImportError if it has not been built: there is no
 fallback implementation.
@@ -30,6 +31,7 @@ import ctypes
 import os
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libcsa_indexer.so")
@@ -800,6 +802,12 @@ def csa_adamw(tensors: AdamWTensors, step, lr=1e-3, beta1=0.9, beta2=0.999, eps=
     _invoke("csa_adamw", _lib.csa_adamw, index, ctypes.byref(p), tensors.table, tensors.count)
 
 
+def _own(grad):
+    """A gradient as the kernels read it: contiguous, and on 16 bytes (autograd may hand over a slice of a larger one)."""
+    grad = grad.contiguous()
+    return grad.clone() if grad.data_ptr() % 16 else grad
+
+
 class CSALinear(torch.autograd.Function):
     """y = CSALinear.apply(x, weight, bias, residual, params): gradients flow to all four tensors (bias and residual
     may be None)."""
@@ -812,24 +820,27 @@ class CSALinear(torch.autograd.Function):
             preact = torch.empty((c.rows, c.out_features), dtype=params.value_dtype, device=x.device)
         y = csa_linear_fwd(params, x, weight.contiguous(), bias, residual, preact=preact)
         ctx.params, ctx.x_shape = params, x.shape
+        ctx.bias_shape = bias.shape if bias is not None else None
         ctx.residual_shape = residual.shape if residual is not None else None
         ctx.save_for_backward(x, weight, preact)
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, preact = ctx.saved_tensors
         c = ctx.params.c
         need = ctx.needs_input_grad
         dx = dw = db = None
-        dy = dy.contiguous()
+        dy = _own(dy)
         if any(need[:3]):
             p = ctx.params
             if c.dy_stride:  # autograd hands contiguous gradients over
                 p = LinearParams(c.rows, c.in_features, c.out_features, c.dtype, c.out_dtype, c.activation, c.alpha,
                                  c.x_stride)
             dx, dw, db = csa_linear_bwd(p, dy, x, weight.contiguous(), preact, need[0], need[1], need[2])
-        return (dx.view(ctx.x_shape) if dx is not None else None, dw.view(weight.shape) if dw is not None else None, db,
+        return (dx.view(ctx.x_shape) if dx is not None else None, dw.view(weight.shape) if dw is not None else None,
+                db.view(ctx.bias_shape) if db is not None else None,
                 dy.view(ctx.residual_shape) if need[3] else None, None)
 
 
@@ -847,9 +858,10 @@ class CSARope(torch.autograd.Function):
         return csa_rope(params, x, positions, inv_freq)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         positions, inv_freq = ctx.saved_tensors
-        return csa_rope(ctx.params.inverted(), dout.contiguous(), positions, inv_freq), None, None, None
+        return csa_rope(ctx.params.inverted(), _own(dout), positions, inv_freq), None, None, None
 
 
 def csa_rotary(x, positions, inv_freq, params: RopeParams):

@@ -54,11 +54,22 @@ csa_status check_linear(const csa_linear_params *p, csa_linear_params *q)
     if (q->x_stride < p->in_features || q->residual_stride < p->out_features || q->dy_stride < p->out_features)
         return CSA_ERR_INVALID_ARG;
     if (p->out_dtype != p->dtype && p->out_dtype != CSA_F32) return CSA_ERR_UNSUPPORTED;
-    // rows and features are TMA coordinates, strides TMA byte strides (below 2^40)
-    if (p->rows > 0x7fffff00LL || p->in_features > 0x7fffff00 || p->out_features > 0x7fffff00) return CSA_ERR_UNSUPPORTED;
+    // rows and features are TMA coordinates and 32-bit loop counters, which run a step of at most 32768 beyond them;
+    // strides are TMA byte strides (below 2^40)
+    constexpr int most = 0x7fff0000;
+    if (p->rows > most || p->in_features > most || p->out_features > most) return CSA_ERR_UNSUPPORTED;
     const long long far = 1LL << 36;
     if (q->x_stride > far || q->residual_stride > far || q->dy_stride > far) return CSA_ERR_UNSUPPORTED;
     return CSA_OK;
+}
+
+// An output that is another argument's buffer would be written while others still read it.
+bool shares(const void *out, const void *const *others, int n)
+{
+    if (out == nullptr) return false;
+    for (int i = 0; i < n; i++)
+        if (others[i] == out) return true;
+    return false;
 }
 
 // ------------------------------------------------------------------ rotary positions
@@ -194,8 +205,12 @@ csa_status csa_linear_fwd(const csa_linear_params *p, const void *x, const void 
     const size_t ws = linear_fwd_workspace(q);
     if (workspace_bytes < ws || (ws > 0 && workspace == nullptr)) return CSA_ERR_WORKSPACE;
     CSA_TRY(need_opt(workspace));
-    if (residual == y && q.residual_stride != q.out_features && q.rows > 1) return CSA_ERR_INVALID_ARG;
     if (q.rows == 0) return CSA_OK;
+    if (residual == y && q.residual_stride != q.out_features && q.rows > 1) return CSA_ERR_INVALID_ARG;
+    const void *inputs[] = {x, weight, bias, preact, residual};
+    if (shares(y, inputs, 4)) return CSA_ERR_INVALID_ARG;
+    inputs[3] = y;
+    if (shares(preact, inputs, 5)) return CSA_ERR_INVALID_ARG;
     CSA_CUDA(launch_linear_fwd(q, x, weight, bias, residual, y, preact, workspace, static_cast<cudaStream_t>(stream)));
     return CSA_OK;
 }
@@ -217,6 +232,9 @@ csa_status csa_linear_bwd(const csa_linear_params *p, const void *dy, const void
     const size_t ws = linear_bwd_workspace(q);
     if (workspace_bytes < ws || (ws > 0 && workspace == nullptr)) return CSA_ERR_WORKSPACE;
     CSA_TRY(need_opt(workspace));
+    const void *inputs[] = {q.rows > 0 ? dy : nullptr, dw != nullptr ? x : nullptr, dx != nullptr ? weight : nullptr,
+                            q.activation != CSA_ACT_NONE ? preact : nullptr, dx, dw};
+    if (shares(dx, inputs, 4) || shares(dw, inputs, 5) || shares(db, inputs, 6)) return CSA_ERR_INVALID_ARG;
     CSA_CUDA(launch_linear_bwd(q, dy, x, weight, preact, dx, dw, db, workspace, static_cast<cudaStream_t>(stream)));
     return CSA_OK;
 }

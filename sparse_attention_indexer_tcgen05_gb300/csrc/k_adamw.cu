@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(THREADS, 12) adamw_kernel(const __grid_constan
         // 1 - b^t without cancellation for small t: -expm1(t log b)
         const float lr = h.lr_dev != nullptr ? *h.lr_dev : h.lr;
         if (h.step_dev != nullptr) {
-            const float t = (float)*h.step_dev;
+            const float t = fmaxf((float)*h.step_dev, 1.f);
             c1 = lr / -expm1f(t * h.log_b1);
             rs2 = rsqrtf(-expm1f(t * h.log_b2));
         } else {

@@ -22,19 +22,6 @@ template <typename V> struct Planes;
 template <> struct Planes<bf16> { static constexpr int N = 1; };
 template <> struct Planes<float> { static constexpr int N = 3; };
 
-template <typename V> __device__ __forceinline__ void put_planes(bf16 *out, long long plane, long long at, float x)
-{
-    if constexpr (sizeof(V) == 2) {
-        out[at] = __float2bfloat16_rn(x);
-    } else {
-        bf16 h, m, l;
-        split3(x, h, m, l);
-        out[at] = h;
-        out[plane + at] = m;
-        out[2 * plane + at] = l;
-    }
-}
-
 // What a staged operand is made of: rows x cols values, rows `stride` apart -> planes of rows `ld` apart.
 struct Stage {
     const void *x;
@@ -94,6 +81,8 @@ template <typename T, bool ALIGNED> __device__ __forceinline__ void load8(const 
     r.floats(valid, x);
 }
 
+// 8 neighbouring values to the planes
+
 template <typename V> __device__ __forceinline__ void put_planes8(bf16 *out, long long plane, long long at, const float (&x)[8])
 {
     constexpr int P = Planes<V>::N;
@@ -131,8 +120,8 @@ template <typename V> __global__ void __launch_bounds__(256) stage_kernel(const 
 
 // dz = dy act'(z) for `per` rows of a block and 8 TX columns, and their column sums for db.  Bound by memory: dy and
 // z are read once, dz is written once, 8 neighbouring columns a thread (VEC: aligned ones), the next row's on their way
-// while a row is worked on: bf16 silu of 8192 x 8192 values 65 us (403 MB), db alone 30.  (Two rows loaded and then worked on: 79
-// and 52.)
+// while a row is worked on: bf16 silu of 8192 x 8192 values 65 us (403 MB), db alone 30.  (Two rows loaded and then
+// worked on: 79 and 52.)
 template <typename V, typename O, int TX, bool VEC>
 __global__ void __launch_bounds__(256, 4)
 dz_kernel(const O *dy, long long ldy, const V *z, int act, bf16 *dz, long long ld, long long plane, float *sums,

@@ -35,6 +35,7 @@ class IndexerTrainer:
                 raise ValueError(f"{name} must be {dt} [{n}, {hidden}], got {t.dtype} {tuple(t.shape)}")
         self.hyper = dict(lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay)
         self.step_count = torch.zeros((), dtype=torch.int64, device=dev)
+        self.taken = torch.empty((), dtype=torch.bool, device=dev)  # whether a step with found_inf counted
 
         self.p_q = B.LinearParams(rows, hidden, heads * dim, c.dtype)
         self.p_k = B.LinearParams(keys, hidden, dim, c.dtype)
@@ -89,8 +90,12 @@ class IndexerTrainer:
 
     def step(self, x, x_c, q, kv, kv_c, sink, positions=None, key_positions=None, inv_freq=None, grad_scale=None,
              found_inf=None):
-        """gradients() and the weights' AdamW step.  Returns the loss, a device scalar."""
+        """gradients() and the weights' AdamW step.  Returns the loss, a device scalar.  found_inf (f32 device scalar),
+        when not 0, leaves weights, state and step count as they are."""
         self.gradients(x, x_c, q, kv, kv_c, sink, positions, key_positions, inv_freq)
-        self.step_count.add_(1)
+        if found_inf is None:
+            self.step_count.add_(1)
+        else:
+            self.step_count.add_(torch.eq(found_inf.view(()), 0, out=self.taken))
         B.csa_adamw(self.tensors, self.step_count, grad_scale=grad_scale, found_inf=found_inf, **self.hyper)
         return self.loss

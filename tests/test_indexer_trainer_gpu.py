@@ -137,6 +137,23 @@ def test_captured_steps_equal_eager_ones():
     B.csa_check_device_status()
 
 
+def test_a_step_with_found_inf_leaves_everything():
+    """Two steps of which the second is skipped equal the first alone, the step count included."""
+    d, weights, i = case("bshd", "bf16", seed=13)
+    t = trainer(d, weights, eight_bit=True)
+    found = torch.zeros(1, device="cuda")
+    t.step(*call(d, i), found_inf=found)
+    kept = [x.clone().view(torch.uint8) for name, c in t.tensors.tensors.items() if name != "grad" for x in c]
+    assert int(t.step_count) == 1
+    found.fill_(float("inf"))
+    t.step(*call(d, i), found_inf=found)
+    after = [x.view(torch.uint8) for name, c in t.tensors.tensors.items() if name != "grad" for x in c]
+    assert int(t.step_count) == 1 and all(torch.equal(a, b) for a, b in zip(kept, after))
+    found.zero_()
+    t.step(*call(d, i), found_inf=found)
+    assert int(t.step_count) == 2 and not torch.equal(kept[0], t.wq.view(torch.uint8))
+
+
 def test_wrong_weights_refused():
     d, weights, _ = case("bshd", "bf16")
     with pytest.raises(ValueError, match="wk"):

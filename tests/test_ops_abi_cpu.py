@@ -46,7 +46,8 @@ def linear_bwd(B, p, dy=addr(1), x=addr(2), w=addr(3), z=addr(4), dx=addr(5), dw
 @pytest.mark.parametrize("field,value,status", [
     ("dtype", 5, 1), ("out_dtype", -1, 1), ("activation", 4, 1), ("in_features", 0, 1), ("out_features", 0, 1),
     ("rows", -1, 1), ("alpha", float("nan"), 1), ("x_stride", 63, 1), ("residual_stride", 47, 1), ("dy_stride", 47, 1),
-    ("rows", 1 << 31, 2), ("x_stride", 1 << 37, 2)])
+    ("rows", 1 << 31, 2), ("x_stride", 1 << 37, 2), ("rows", 0x7fff0001, 2), ("in_features", 0x7fff0001, 2),
+    ("out_features", 0x7fff0001, 2)])
 def test_linear_params_refused(B, field, value, status):
     p = linear(B)
     setattr(p.c, field, value)
@@ -70,6 +71,22 @@ def test_linear_pointers_refused(B):
         assert linear_bwd(B, p, **{name: addr(9) + 4}) == 3, name
     # the residual as the output: only with the output's own row stride
     assert linear_fwd(B, linear(B, residual_stride=56), res=addr(5)) == 1
+
+
+def test_linear_an_output_over_another_argument_refused(B):
+    p = linear(B)
+    for name in ("x", "w", "bias", "z"):
+        assert linear_fwd(B, p, **{name: addr(5)}) == 1, name       # y
+    for name in ("x", "w", "bias", "res"):
+        assert linear_fwd(B, p, **{name: addr(6)}) == 1, name       # preact
+    assert linear_fwd(B, p, res=addr(5), z=None) == 5               # the residual in place: past the checks, no GPU
+    for out in (5, 6, 7):
+        for name in ("dy", "x", "w", "z"):
+            assert linear_bwd(B, p, **{name: addr(out)}) == 1, (out, name)
+    assert linear_bwd(B, p, dw=addr(5)) == linear_bwd(B, p, db=addr(5)) == linear_bwd(B, p, db=addr(6)) == 1
+    # what is not read may hold a gradient
+    assert linear_bwd(B, p, dx=addr(2), dw=None) == linear_bwd(B, p, dx=None, dw=addr(3)) == 5
+    assert linear_bwd(B, linear(B, activation="none"), dx=addr(4)) == 5
 
 
 def test_linear_workspace_refused(B):

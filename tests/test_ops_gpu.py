@@ -636,6 +636,91 @@ def test_linear_captured_with_other_inputs():
             assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_autograd_takes_slices_of_a_larger_gradient():
+    """The gradient of a concatenation is a slice that need not start on 16 bytes; a bias of another shape."""
+    g = gen(50)
+    x, w, b = (randn(g, *s).requires_grad_(True) for s in ((6, 8), (9, 8), (1, 9)))
+    p = B.LinearParams(6, 8, 9, "f32")
+    head = torch.ones(5, 9, device="cuda")
+    torch.cat([head, B.csa_linear(x, w, b, params=p)]).square().sum().backward()
+    x64, w64 = x.detach().double(), w.detach().double()
+    d = 2 * (x64 @ w64.t() + b.detach().double())                # the gradient of y, off by what y is off by, doubled
+    e = 2 * product_tol(x64.abs() @ w64.abs().t() + b.detach().double().abs(), 9)
+    ones = torch.ones(1, 6, device="cuda", dtype=torch.float64)
+    for name, got, left, right, err in (("dx", x.grad, d, w64, e @ w64.abs()), ("dw", w.grad, d.t(), x64, e.t() @ x64.abs()),
+                                        ("db", b.grad, ones, d, ones @ e)):
+        close(got, left @ right, err + product_tol(left.abs() @ right.abs() + err, 9), name)
+    r = B.RopeParams(3, 1, 6, "f32")
+    v = randn(g, 3, 1, 6).requires_grad_(True)
+    pos, f = torch.arange(3, device="cuda", dtype=torch.int32)[None], torch.ones(3, device="cuda", dtype=torch.float64)
+    weight = randn(g, 4, 1, 6)
+    (torch.cat([v.detach()[:1], B.csa_rotary(v, pos, f, r)]) * weight).sum().backward()
+    assert torch.equal(v.grad, B.csa_rope(r.inverted(), weight[1:].clone(), pos, f))
+
+
+def test_adamw_step_on_the_device_below_one_counts_as_one():
+    g = gen(51)
+    sides = []
+    for first in (0, 1):
+        w = [randn(gen(52), 300)]
+        t = B.AdamWTensors(w, [randn(gen(53), 300)], **B.AdamWTensors.zero_state(w))
+        B.csa_adamw(t, torch.tensor(first, device="cuda"))
+        sides.append(w[0])
+    assert torch.equal(*sides) and bool(sides[0].isfinite().all())
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^31 elements in an operand, an output or a workspace: the first and the last rows."""
+    g = gen(60)
+    bf = torch.bfloat16
+    # y, z, dy and dz of 264000 x 8200
+    M, K, N, T = 264000, 64, 8200, 40
+    x, w = randn(g, M, K, dtype=bf), randn(g, N, K, dtype=bf)
+    p = B.LinearParams(M, K, N, activation="relu")
+    z = torch.empty(M, N, dtype=bf, device="cuda")
+    y = B.csa_linear_fwd(p, x, w, preact=z)
+    dx = B.csa_linear_bwd(p, y, x, w, z, need_dw=False)[0]
+    w64 = w.double()
+    for rows in (slice(0, T), slice(M - T, M)):
+        want = x[rows].double() @ w64.t()
+        tol = product_tol(x[rows].double().abs() @ w64.abs().t(), K)
+        close(z[rows], want, tol + U[bf] * (want.abs() + tol), "z")
+        close(y[rows], want.clamp(min=0), tol + U[bf] * (want.abs() + tol), "y")
+        d = y[rows].double() * (z[rows] > 0)                     # exact in bf16
+        want, tol = d @ w64, product_tol(d.abs() @ w64.abs(), N)
+        close(dx[rows], want, tol + U[bf] * (want.abs() + tol), "dx")
+    del y, z, dx
+    # weights of 1050000 x 2056 and a few rows
+    N, K = 1050000, 2056
+    w = torch.randn(N, K, generator=g, device="cuda", dtype=torch.bfloat16)
+    x = randn(g, 3, K, dtype=torch.bfloat16)
+    y = B.csa_linear_fwd(B.LinearParams(3, K, N, out_dtype="f32"), x, w)
+    last = w[-50:].double()
+    close(y[:, -50:], x.double() @ last.t(), product_tol(x.double().abs() @ last.abs().t(), K), "y of the last weights")
+    del w, y
+    # rotary positions on 2^31 + some values
+    rows, heads, dim = 262150, 64, 128
+    x = torch.randn(rows, heads, dim, generator=g, device="cuda", dtype=torch.bfloat16)
+    pos = torch.randint(0, 1 << 20, (1, rows), generator=g, device="cuda", dtype=torch.int32)
+    f = 10000.0 ** (-torch.arange(64, dtype=torch.float64, device="cuda") / 64)
+    out = B.csa_rope(B.RopeParams(rows, heads, dim), x, pos, f)
+    assert torch.equal(out[-20:], B.csa_rope(B.RopeParams(20, heads, dim), x[-20:].clone(), pos[:, -20:].contiguous(), f))
+    del x, out
+    # a tensor of 2^31 + 2^16 + 77 weights with 8-bit state
+    n, t = (1 << 31) + (1 << 16) + 77, (1 << 16) + 77
+    state = lambda w: B.AdamWTensors.zero_state(w, eight_bit=True)  # noqa: E731
+    w = [torch.randn(n, generator=g, device="cuda", dtype=torch.bfloat16)]
+    gr = [torch.randn(n, generator=g, device="cuda", dtype=torch.bfloat16)]
+    small, sg = [w[0][-t:].clone()], [gr[0][-t:].clone()]
+    big = B.AdamWTensors(w, gr, **state(w))
+    B.csa_adamw(big, 1)
+    ref = B.AdamWTensors(small, sg, **state(small))
+    B.csa_adamw(ref, 1)
+    assert torch.equal(w[0][-t:], small[0])
+    for name in ("m", "v"):
+        assert torch.equal(big.tensors[name][0].view(torch.uint8)[-t:], ref.tensors[name][0].view(torch.uint8))
+
+
 def test_wrong_tensors_refused_by_the_bindings():
     p = B.LinearParams(16, 32, 24)
     x, w = torch.zeros(16, 32, device="cuda").bfloat16(), torch.zeros(24, 32, device="cuda").bfloat16()
