@@ -100,13 +100,11 @@ template <typename V> __device__ __forceinline__ void put_planes8(bf16 *out, lon
     for (int q = 0; q < P; q++) *reinterpret_cast<uint4 *>(out + q * plane + at) = *reinterpret_cast<const uint4 *>(w[q]);
 }
 
-// Up to two operands in one launch; a thread makes 8 neighbouring values of a row.
-template <typename V> __global__ void __launch_bounds__(256) stage_kernel(const Stage s0, const Stage s1)
+// Block `b` of up to two operands; a thread makes 8 neighbouring values of a row.
+template <typename V> __device__ __forceinline__ void stage_block(const Stage &s0, const Stage &s1, unsigned b)
 {
-    chain_start();
-    chain_wait();
-    const Stage &s = blockIdx.x < s0.blocks ? s0 : s1;
-    const long long t = (long long)(blockIdx.x - (blockIdx.x < s0.blocks ? 0u : s0.blocks)) * 256 + threadIdx.x;
+    const Stage &s = b < s0.blocks ? s0 : s1;
+    const long long t = (long long)(b - (b < s0.blocks ? 0u : s0.blocks)) * 256 + threadIdx.x;
     const int chunks = (s.cols + 7) / 8;
     const long long r = t <= 0xffffffffLL ? (long long)((uint32_t)t / (uint32_t)chunks) : t / chunks;
     if (r >= s.rows) return;
@@ -118,22 +116,34 @@ template <typename V> __global__ void __launch_bounds__(256) stage_kernel(const 
     put_planes8<V>(s.out, s.plane, r * s.ld + c, v);
 }
 
+template <typename V> __global__ void __launch_bounds__(256) stage_kernel(const Stage s0, const Stage s1)
+{
+    chain_start();
+    chain_wait();
+    stage_block<V>(s0, s1, blockIdx.x);
+}
+
 // dz = dy act'(z) for `per` rows of a block and 8 TX columns, and their column sums for db.  Bound by memory: dy and
 // z are read once, dz is written once, 8 neighbouring columns a thread (VEC: aligned ones), the next row's on their way
 // while a row is worked on: bf16 silu of 8192 x 8192 values 65 us (403 MB), db alone 30.  (Two rows loaded and then
-// worked on: 79 and 52.)
+// worked on: 79 and 52.)  Blocks behind the `across` x `down` ones stage operands of the products.
 template <typename V, typename O, int TX, bool VEC>
 __global__ void __launch_bounds__(256, 4)
 dz_kernel(const O *dy, long long ldy, const V *z, int act, bf16 *dz, long long ld, long long plane, float *sums,
-          long long M, int N, int per)
+          long long M, int N, int per, unsigned across, unsigned down, const Stage s0, const Stage s1)
 {
     constexpr int TY = 256 / TX;
     chain_start();
     chain_wait();
+    if (blockIdx.x >= across * down) {
+        stage_block<V>(s0, s1, blockIdx.x - across * down);
+        return;
+    }
+    const unsigned block_n = blockIdx.x % across, block_m = blockIdx.x / across;
     __shared__ float part[TY][8 * TX + 1];
     const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
-    const int n0 = blockIdx.x * 8 * TX, n = n0 + 8 * tx, valid = min(8, N - n);
-    const long long r0 = (long long)blockIdx.y * per, r1 = min(M, r0 + per);
+    const int n0 = block_n * 8 * TX, n = n0 + 8 * tx, valid = min(8, N - n);
+    const long long r0 = (long long)block_m * per, r1 = min(M, r0 + per);
     float s[8] = {};
     if (n < N) {
         Raw8<O, VEC> d0, d1;
@@ -168,7 +178,7 @@ dz_kernel(const O *dy, long long ldy, const V *z, int act, bf16 *dz, long long l
         float t = 0.f;
 #pragma unroll
         for (int k = 0; k < TY; k++) t += part[k][c];
-        if (n0 + c < N) sums[(long long)blockIdx.y * N + n0 + c] = t;
+        if (n0 + c < N) sums[(long long)block_m * N + n0 + c] = t;
     }
 }
 
@@ -364,21 +374,24 @@ cudaError_t product(const Product &p, cudaStream_t st)
 }
 
 template <typename V, typename O, int TX, bool VEC>
-cudaError_t run_dz_rows(const csa_linear_params &p, const Bwd &b, const void *dy, const void *z, bf16 *dz, float *sums, cudaStream_t st)
+cudaError_t run_dz_rows(const csa_linear_params &p, const Bwd &b, const void *dy, const void *z, bf16 *dz, float *sums,
+                        const Stage (&job)[2], cudaStream_t st)
 {
     const int N = p.out_features;
     const long long ld = up8(N), plane = p.rows * ld;
-    const dim3 grid((N + 8 * TX - 1) / (8 * TX), b.blocks);
-    return launch_chained(dz_kernel<V, O, TX, VEC>, grid, 256, 0, 1, st,
-                          (const O *)dy, p.dy_stride, (const V *)z, p.activation, dz, ld, plane, sums, p.rows, N, b.per);
+    const unsigned across = (N + 8 * TX - 1) / (8 * TX), down = b.blocks;
+    return launch_chained(dz_kernel<V, O, TX, VEC>, dim3(across * down + job[0].blocks + job[1].blocks), 256, 0, 1, st, (const O *)dy,
+                          p.dy_stride, (const V *)z, p.activation, dz, ld, plane, sums, p.rows, N, b.per, across, down, job[0], job[1]);
 }
 
 template <typename V, typename O>
-cudaError_t run_dz(const csa_linear_params &p, const Bwd &b, const void *dy, const void *z, bf16 *dz, float *sums, cudaStream_t st)
+cudaError_t run_dz(const csa_linear_params &p, const Bwd &b, const void *dy, const void *z, bf16 *dz, float *sums, const Stage (&job)[2],
+                   cudaStream_t st)
 {
     const bool vec = (p.out_features & 7) == 0 && (p.dy_stride & 7) == 0;
-    if (p.out_features <= 64) return vec ? run_dz_rows<V, O, 8, true>(p, b, dy, z, dz, sums, st) : run_dz_rows<V, O, 8, false>(p, b, dy, z, dz, sums, st);
-    return vec ? run_dz_rows<V, O, 32, true>(p, b, dy, z, dz, sums, st) : run_dz_rows<V, O, 32, false>(p, b, dy, z, dz, sums, st);
+    auto *run = p.out_features <= 64 ? (vec ? run_dz_rows<V, O, 8, true> : run_dz_rows<V, O, 8, false>)
+                                     : (vec ? run_dz_rows<V, O, 32, true> : run_dz_rows<V, O, 32, false>);
+    return run(p, b, dy, z, dz, sums, job, st);
 }
 
 }  // namespace linear
@@ -441,10 +454,20 @@ cudaError_t launch_linear_bwd(const csa_linear_params &p, const void *dy, const 
     char *w = static_cast<char *>(ws);
     bf16 *dz = b.stage_dz && (dx != nullptr || dw != nullptr) ? reinterpret_cast<bf16 *>(w + b.off_dz) : nullptr;
     float *sums = db != nullptr ? reinterpret_cast<float *>(w + b.off_sums) : nullptr;
-    if (dz != nullptr || sums != nullptr) {
-        if (p.dtype == CSA_F32) LIN_TRY((run_dz<float, float>(p, b, dy, preact, dz, sums, st)));
-        else if (p.out_dtype == CSA_F32) LIN_TRY((run_dz<bf16, float>(p, b, dy, preact, dz, sums, st)));
-        else LIN_TRY((run_dz<bf16, bf16>(p, b, dy, preact, dz, sums, st)));
+    Stage job[2] = {};
+    Operand ow = {}, ox = {};
+    if (dx != nullptr) ow = operand(p, weight, K, N, (int)K, b.stage_w, w + b.off_w, false, &job[0]);
+    if (dw != nullptr) ox = operand(p, x, p.x_stride, M, (int)K, b.stage_x, w + b.off_x, false, &job[1]);
+    // A few staged blocks join dz's launch (1013 x 1023 x 777 in fp32: 47.1 us before, 43.8 so); many have their own, with
+    // twice the warps an SM (62578 x 684 x 585 in bf16: 204 us, joined 213).
+    const bool any_dz = dz != nullptr || sums != nullptr;
+    if (!any_dz || job[0].blocks + job[1].blocks > 16u * kSms) {
+        LIN_TRY(run_stages(p, job, st));
+        job[0].blocks = job[1].blocks = 0;
+    }
+    if (any_dz) {
+        auto *run = p.dtype == CSA_F32 ? run_dz<float, float> : p.out_dtype == CSA_F32 ? run_dz<bf16, float> : run_dz<bf16, bf16>;
+        LIN_TRY(run(p, b, dy, preact, dz, sums, job, st));
     }
     if (db != nullptr) {
         LIN_TRY(launch_chained(db_kernel, dim3((p.out_features + 31) / 32), 1024, 0, 1, st, sums, b.blocks, p.out_features, db));
@@ -458,11 +481,6 @@ cudaError_t launch_linear_bwd(const csa_linear_params &p, const void *dy, const 
     q.e.alpha = p.alpha;
     q.e.out_f32 = p.dtype == CSA_F32;
     q.e.partial = reinterpret_cast<float *>(w + b.off_part);
-    Stage job[2] = {};
-    Operand ow = {}, ox = {};
-    if (dx != nullptr) ow = operand(p, weight, K, N, (int)K, b.stage_w, w + b.off_w, false, &job[0]);
-    if (dw != nullptr) ox = operand(p, x, p.x_stride, M, (int)K, b.stage_x, w + b.off_x, false, &job[1]);
-    LIN_TRY(run_stages(p, job, st));
     if (dx != nullptr) {
         q.a = d;
         q.a.k_major = true;
