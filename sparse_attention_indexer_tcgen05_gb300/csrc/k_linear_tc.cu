@@ -14,7 +14,7 @@
 // Mapping.  A unit is one output tile and one piece of the k axis.  A CTA pair (two SMs) computes 256 x BN: each CTA
 // loads its 128 rows of A and its BN / 2 rows of B, so an operand byte brought to an SM feeds twice the MMAs of a lone
 // CTA's 128 x BN tile.  Few tiles, or few rows, take lone CTAs with 128 x 64 tiles.  Roles: warp 0 the TMA producer,
-// warp 1 the MMA issue (the pair's even CTA), warps 2..9 the epilogue, a row of the tile a lane.  TMEM holds two
+// warp 1 the MMA issue (the pair's even CTA), warps 2..9 (2..17) the epilogue, a row of the tile a lane.  TMEM holds two
 // accumulators, so that a tile's epilogue runs under the next tile's MMAs.  Persistent: one CTA per SM, units dealt
 // round-robin in an order that keeps the running tiles' operands in L2.
 //
@@ -51,16 +51,16 @@ using namespace ptx;
 
 constexpr int BM = 128;        // rows of one CTA's accumulator
 constexpr int BK = 64;         // k per stage: one 128-byte swizzle row
-constexpr int THREADS = 320;
-constexpr int EPI_WARPS = 8;
 
-template <int CG, int BN, int P> struct Cfg {                  // P planes
+// P planes, EW epilogue warps
+template <int CG, int BN, int P, int EW> struct Cfg {
+    static constexpr int THREADS = 64 + 32 * EW;
     static constexpr int ROWS_B = BN / CG;                      // B rows this CTA loads
     static constexpr int A_BYTES = BM * BK * 2, B_BYTES = ROWS_B * BK * 2;
     static constexpr int STAGE = P * (A_BYTES + B_BYTES);
-    static constexpr int STAGES = 196608 / STAGE;               // 192 KB: 6 or 8; 2 of three planes
+    static constexpr int STAGES = (229376 - EW * 4096) / STAGE; // of 192 KB (EW 8): 6 or 8; 2 of three planes
     static constexpr int TURN = STAGES * STAGE;                 // the epilogue's buffers, 32 rows of 128 bytes a warp
-    static constexpr int MISC = TURN + EPI_WARPS * 4096;
+    static constexpr int MISC = TURN + EW * 4096;
     static constexpr int SMEM = MISC + 512 + 1024;              // + alignment
     static constexpr int TMEM = 2 * BN < 512 ? (2 * BN < 128 ? 128 : 2 * BN) : 512;
 };
@@ -74,6 +74,7 @@ struct Args {
     int rows_a;                 // rows of A a CTA loads: BM, fewer where M is below BM
     int blocks_a, blocks_b;     // an m/n-contiguous operand's map has 64-wide blocks as an axis of their own
     int tma_out;                // the output goes by TMA
+    int many;                   // 16 epilogue warps
     int res32;                  // the residual's rows start on 32-byte sectors
     Epilogue e;
 };
@@ -140,35 +141,57 @@ __device__ __forceinline__ void ld32(const void *p, uint32_t *w)
 
 constexpr int C = 32;   // columns of an epilogue step
 
-// 32 columns of one row of the residual (those behind N: 0), asked for a step before they are used.
+// 32 columns of one row of the residual.  Whole sectors are asked for a step before they are used; other rows (and the
+// last columns) are read where they are added, as the aligned vectors that hold the columns that exist, shifted.  (Value
+// by value, bias, GELU and residual of 8200 x 4104 x 264 took 125 us instead of 70.)
 template <typename O> struct Residual {
-    uint32_t r[C * sizeof(O) / 4];
-    __device__ __forceinline__ void load(const Args &a, long long m, long long n0)
-    {
-        constexpr int E = 32 / sizeof(O);   // values of a sector
-        const O *p = (const O *)a.e.res + m * a.e.ldr + n0;
-        if (a.res32 && n0 + C <= a.N) {
-#pragma unroll
-            for (int k = 0; k < C / E; k++) ld32(p + E * k, r + 8 * k);
-        } else {
-#pragma unroll
-            for (int k = 0; k < C; k++) {
-                if constexpr (sizeof(O) == 4) {
-                    r[k] = n0 + k < a.N ? __float_as_uint(p[k]) : 0u;
-                } else {
-                    const uint32_t h = n0 + k < a.N ? (uint32_t)reinterpret_cast<const unsigned short *>(p)[k] : 0u;
-                    if (k % 2 == 0) r[k / 2] = h;
-                    else r[k / 2] |= h << 16;
-                }
-            }
-        }
-    }
-    __device__ __forceinline__ void add_to(float (&v)[C]) const
+    static constexpr int W = C * sizeof(O) / 4;
+    uint32_t r[W];
+    static __device__ __forceinline__ bool early(const Args &a, long long n0) { return a.res32 && n0 + C <= a.N; }
+    static __device__ __forceinline__ const O *at(const Args &a, long long m, long long n0) { return (const O *)a.e.res + m * a.e.ldr + n0; }
+    static __device__ __forceinline__ void add(const uint32_t *r, float (&v)[C])
     {
 #pragma unroll
         for (int k = 0; k < C; k++) {
             if constexpr (sizeof(O) == 4) v[k] += __uint_as_float(r[k]);
             else v[k] += __uint_as_float(k % 2 == 0 ? r[k / 2] << 16 : r[k / 2] & 0xffff0000u);
+        }
+    }
+    __device__ __forceinline__ void load(const Args &a, long long m, long long n0)
+    {
+        if (m >= a.M || !early(a, n0)) return;
+        const O *p = at(a, m, n0);
+#pragma unroll
+        for (int k = 0; k < W / 8; k++) ld32(p + 32 / sizeof(O) * k, r + 8 * k);
+    }
+    __device__ __forceinline__ void add_to(const Args &a, long long m, long long n0, float (&v)[C]) const
+    {
+        if (early(a, n0)) {
+            add(r, v);
+        } else if (m < a.M) {
+            const O *p = at(a, m, n0);
+            const int sh = (int)(reinterpret_cast<uintptr_t>(p) & 15), end = sh + (int)min((long long)C, a.N - n0) * (int)sizeof(O);
+            const uint4 *q = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) - sh);
+            uint32_t u[W + 4];
+#pragma unroll
+            for (int k = 0; k <= W / 4; k++) {
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (end > 16 * k) x = q[k];
+                u[4 * k] = x.x; u[4 * k + 1] = x.y; u[4 * k + 2] = x.z; u[4 * k + 3] = x.w;
+            }
+            if (sh & 8) {
+#pragma unroll
+                for (int k = 0; k < W + 2; k++) u[k] = u[k + 2];
+            }
+            if (sh & 4) {
+#pragma unroll
+                for (int k = 0; k < W + 1; k++) u[k] = u[k + 1];
+            }
+            if (sizeof(O) == 2 && (sh & 2)) {
+#pragma unroll
+                for (int k = 0; k < W; k++) u[k] = __funnelshift_r(u[k], u[k + 1], 16);
+            }
+            add(u, v);
         }
     }
 };
@@ -301,12 +324,12 @@ __device__ __forceinline__ void to_activation(const Args &a, float (&v)[C], long
 }
 
 // EXACT: the sums are kept in the epilogue's registers, pieces of CHUNK stages of the k axis in TMEM.
-template <int CG, int BN, int P, bool EXACT, bool A_K, bool B_K>
-__global__ void __launch_bounds__(THREADS, 1)
+template <int CG, int BN, int P, int EW, bool EXACT, bool A_K, bool B_K>
+__global__ void __launch_bounds__(64 + 32 * EW, 1)
 linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                  const __grid_constant__ CUtensorMap map_half, const __grid_constant__ CUtensorMap map_out, const Args a)
 {
-    using Z = Cfg<CG, BN, P>;
+    using Z = Cfg<CG, BN, P, EW>;
     constexpr int S = Z::STAGES;
     constexpr int CHUNK = !EXACT ? 0x40000000 : P == 3 ? 1 : 8;
     extern __shared__ unsigned char smem_raw[];
@@ -328,7 +351,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(t_full + i, 1);
-            mbar_init(t_empty + i, EPI_WARPS * CG);
+            mbar_init(t_empty + i, EW * CG);
         }
         mbar_init(done, 1);
         *abort_flag = 0;
@@ -453,9 +476,9 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             drain_bar(done, 0, &g_lin_error);
         }
     } else {
-        // ---------------------------------------------------------- epilogue (warps 2..9)
+        // ---------------------------------------------------------- epilogue (8 or 16 warps)
         const int quad = warp & 3;               // TMEM lanes this warp may access
-        const int side = (warp - 2) >> 2;        // half of the columns
+        const int side = (warp - 2) >> 2;        // part of the columns
         const Buffer b = {smem + Z::TURN + (warp - 2) * 4096, lane};
         // asked once: each of these questions cost a step a miss in the constant and instruction caches
         const bool tma = a.tma_out != 0, with_res = a.e.res != nullptr, with_bias = a.e.bias != nullptr, with_act = a.e.act != CSA_ACT_NONE || a.e.preact != nullptr;
@@ -465,7 +488,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             int tc = 0;
             for (int u = u0; u < a.units; u += ustep) {
                 const Unit x = unit_of<BN>(a, u);
-                const int cols = x.bn / 2;
+                const int cols = x.bn / (EW / 4);
                 const long long m0 = ((long long)x.m * CG + rank) * BM + quad * 32, nb = x.n0 + side * cols;
                 const auto release = [&](int tb) {  // the accumulator is in registers: the next MMAs may have it
                     fence_before();
@@ -484,7 +507,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                 Bias bias;
                 const auto ask = [&](long long n0) {
                     if (with_bias) bias.load(a, n0, lane);
-                    if (with_res && m0 + lane < a.M && n0 < a.N) res.load(a, m0 + lane, n0);
+                    if (with_res) res.load(a, m0 + lane, n0);
                 };
                 // 32 columns from sums to memory
                 const auto step = [&](int c, float (&v)[C]) {
@@ -497,7 +520,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                         for (int k = 0; k < C; k++) v[k] *= alpha;
                     }
                     if (with_act) to_activation(a, v, m0, n0, b);
-                    if (with_res) res.add_to(v);
+                    if (with_res) res.add_to(a, m0 + lane, n0, v);
                     if (c + C < cols) ask(n0 + C);
                     if (tma) {
                         const bool second = sizeof(O) == 2 && (c & C) != 0;
@@ -608,24 +631,24 @@ struct Maps {
     CUtensorMap a, b, half, out;
 };
 
-template <int CG, int BN, int P, bool EXACT, bool A_K, bool B_K>
+template <int CG, int BN, int P, int EW, bool EXACT, bool A_K, bool B_K>
 static cudaError_t launch(const Maps &m, const Args &a, int sms, cudaStream_t st)
 {
-    using Z = Cfg<CG, BN, P>;
-    auto *kernel = linear_tc_kernel<CG, BN, P, EXACT, A_K, B_K>;
+    using Z = Cfg<CG, BN, P, EW>;
+    auto *kernel = linear_tc_kernel<CG, BN, P, EW, EXACT, A_K, B_K>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::SMEM);
     if (e != cudaSuccess) return e;
     const int slots = sms / CG;
-    return launch_chained(kernel, dim3((unsigned)((a.units < slots ? a.units : slots) * CG)), THREADS, Z::SMEM, CG, st, m.a, m.b, m.half, m.out, a);
+    return launch_chained(kernel, dim3((unsigned)((a.units < slots ? a.units : slots) * CG)), Z::THREADS, Z::SMEM, CG, st, m.a, m.b, m.half, m.out, a);
 }
 
-template <int CG, int BN, int P, bool EXACT>
+template <int CG, int BN, int P, int EW, bool EXACT>
 static cudaError_t launch_majors(const Product &p, const Maps &m, const Args &a, int sms, cudaStream_t st)
 {
-    if (p.a.k_major && p.b.k_major) return launch<CG, BN, P, EXACT, true, true>(m, a, sms, st);
+    if (p.a.k_major && p.b.k_major) return launch<CG, BN, P, EW, EXACT, true, true>(m, a, sms, st);
     if constexpr (P == 3 || !EXACT) {  // gradients have their operands' type
-        if (p.a.k_major) return launch<CG, BN, P, EXACT, true, false>(m, a, sms, st);
-        return launch<CG, BN, P, EXACT, false, false>(m, a, sms, st);
+        if (p.a.k_major) return launch<CG, BN, P, EW, EXACT, true, false>(m, a, sms, st);
+        return launch<CG, BN, P, EW, EXACT, false, false>(m, a, sms, st);
     }
     return cudaErrorInvalidValue;
 }
@@ -633,10 +656,13 @@ template <int CG, int BN>
 static cudaError_t launch_planes(const Product &p, const Maps &m, const Args &a, int sms, cudaStream_t st)
 {
     if constexpr (BN < 256) {
-        if (p.planes == 3) return launch_majors<CG, BN, 3, true>(p, m, a, sms, st);
-        if (p.plan.exact) return launch_majors<CG, BN, 1, true>(p, m, a, sms, st);
+        if (p.planes == 3) return launch_majors<CG, BN, 3, 8, true>(p, m, a, sms, st);
+        if (p.plan.exact) return launch_majors<CG, BN, 1, 8, true>(p, m, a, sms, st);
     }
-    return launch_majors<CG, BN, 1, false>(p, m, a, sms, st);
+    if constexpr (BN == 256) {
+        if (a.many) return launch_majors<CG, BN, 1, 16, false>(p, m, a, sms, st);
+    }
+    return launch_majors<CG, BN, 1, 8, false>(p, m, a, sms, st);
 }
 
 // Boxes of `rows` m or n indices and 64 values of k of an operand with `n` of them.  {contiguous, strided, plane}; an
@@ -680,7 +706,10 @@ cudaError_t launch_product_tc(const Product &p, int sms, cudaStream_t st)
     const long long units = (long long)a.mt * a.nt * splits, slots = sms / 2, rest = units % slots;
     if (units > 0x3fffffffLL || (long long)BAND * a.nt > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
     a.units = a.whole = (int)units;
-    if (s == PAIR_256 && splits == 1 && units > slots && rest > 0 && 2 * rest <= slots) {
+    // Up to 256 k a tile's epilogue is longer than its MMAs: 16 warps instead of 8, for a stage less and no half tiles
+    // (8192 x 8192 x 128 33.7 -> 27.5 us, with bias, GELU and residual 97 -> 86; x 512 would go from 44.5 to 51).
+    a.many = s == PAIR_256 && a.per_split <= 4;
+    if (s == PAIR_256 && !a.many && splits == 1 && units > slots && rest > 0 && 2 * rest <= slots) {
         a.whole -= (int)rest;
         a.units += (int)rest;
     }
