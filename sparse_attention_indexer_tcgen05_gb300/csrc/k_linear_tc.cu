@@ -51,6 +51,7 @@ using namespace ptx;
 
 constexpr int BM = 128;        // rows of one CTA's accumulator
 constexpr int BK = 64;         // k per stage: one 128-byte swizzle row
+constexpr int MANY_STEPS = 4;  // stages of a unit up to which 256-wide tiles have 16 epilogue warps
 
 // P planes, EW epilogue warps
 template <int CG, int BN, int P, int EW> struct Cfg {
@@ -234,7 +235,8 @@ __device__ __forceinline__ void turned_rows(O *out, long long ld, long long M, l
 }
 
 // A warp's 32 rows x 32 columns, a row a lane, to memory by the lanes' own stores; rows from M and columns from N on
-// are left out.  Rows on 32-byte boundaries: each lane its own sectors.  Else: turned in shared memory so that a warp
+// are left out.  Rows on 32-byte boundaries: each lane its own sectors; on 16-byte ones: half sectors (kept z of 8200 x
+// 4104 x 264: 90 us with everything instead of 123).  Else: turned in shared memory so that a warp
 // writes 32 neighbouring values at a time.
 template <typename O>
 __device__ __forceinline__ void store_tile(O *out, long long ld, long long M, long long N, const float (&v)[C], long long m0, long long n0,
@@ -251,6 +253,16 @@ __device__ __forceinline__ void store_tile(O *out, long long ld, long long M, lo
 #pragma unroll
             for (int j = 0; j < 8; j++) w[j] = sizeof(O) == 2 ? pack2(v[E * k + 2 * j % E], v[E * k + (2 * j + 1) % E]) : __float_as_uint(v[E * k + j]);
             if (n0 + E * k < N) st32(p + E * k, w);
+        }
+    } else if (ld % (E / 2) == 0) {
+        if (m0 + lane >= M) return;
+        O *p = out + (m0 + lane) * ld + n0;
+#pragma unroll
+        for (int k = 0; k < 2 * C / E; k++) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) w[j] = sizeof(O) == 2 ? pack2(v[E / 2 * k + 2 * j % E], v[E / 2 * k + (2 * j + 1) % E]) : __float_as_uint(v[E / 2 * k + j]);
+            if (n0 + E / 2 * k < N) *reinterpret_cast<uint4 *>(p + E / 2 * k) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     } else {
         float *turn = reinterpret_cast<float *>(b.p);
@@ -593,7 +605,7 @@ static void tile_counts(Shape s, long long M, long long N, int &mt, int &nt)
 // than the best of them, mostly 2%; us):
 //   a stage of a unit: 128 x 64 and 256 x 128 tiles 0.20 (the loads), 256 x 256 0.28 (the MMAs' own 512 cycles); of three
 //   planes, six products, 0.72 and 0.90;
-//   a round is no shorter than its epilogue: 0.9, 1.7 and 2.9;
+//   a round is no shorter than its epilogue: 0.9, 1.7 and 2.9 (1.8 with 16 warps);
 //   launch, first loads and last epilogue: 3.8, 5.2 and 6.3;
 //   a cut k axis: another launch, 2.5, and the pieces' way to memory and back at 4 TB/s.
 // Units run in rounds of one per SM or pair.
@@ -614,8 +626,9 @@ Plan plan_product(long long M, long long N, long long K, int planes, bool out_f3
         for (long long cut = 1; cut <= steps && cut <= 64 && (cut == 1 || tiles * cut <= slots); cut++) {
             const long long per = (steps + cut - 1) / cut, pieces = (steps + per - 1) / per;
             double rounds = floor(tiles * pieces / slots), rest = tiles * pieces - rounds * slots;
-            if (rest > 0) rounds += shape == PAIR_256 && pieces == 1 && rounds > 0 && 2 * rest <= slots ? 0.5 : 1.0;
-            double us = rounds * fmax(per * step, EPILOGUE[s]) + FIXED[s];
+            if (rest > 0) rounds += shape == PAIR_256 && pieces == 1 && per > MANY_STEPS && rounds > 0 && 2 * rest <= slots ? 0.5 : 1.0;
+            const double epilogue = shape == PAIR_256 && per <= MANY_STEPS ? 1.8 : EPILOGUE[s];
+            double us = rounds * fmax(per * step, epilogue) + FIXED[s];
             if (pieces > 1) us += 2.5 + (double)M * N * 8 * pieces / 4e6;
             if (us < least) {
                 least = us;
@@ -708,7 +721,7 @@ cudaError_t launch_product_tc(const Product &p, int sms, cudaStream_t st)
     a.units = a.whole = (int)units;
     // Up to 256 k a tile's epilogue is longer than its MMAs: 16 warps instead of 8, for a stage less and no half tiles
     // (8192 x 8192 x 128 33.7 -> 27.5 us, with bias, GELU and residual 97 -> 86; x 512 would go from 44.5 to 51).
-    a.many = s == PAIR_256 && a.per_split <= 4;
+    a.many = s == PAIR_256 && a.per_split <= MANY_STEPS;
     if (s == PAIR_256 && !a.many && splits == 1 && units > slots && rest > 0 && 2 * rest <= slots) {
         a.whole -= (int)rest;
         a.units += (int)rest;
@@ -723,9 +736,9 @@ cudaError_t launch_product_tc(const Product &p, int sms, cudaStream_t st)
         a.ldo = partial_stride(p.N);
     }
     a.res32 = (reinterpret_cast<uintptr_t>(a.e.res) & 31) == 0 && a.e.ldr % (a.e.out_f32 ? 8 : 16) == 0;
-    // a warp of the 128 x 64 tile has half a row of bf16 columns; a kept z off the sectors needs the buffer for itself
-    a.tma_out = s != LONE_64 && a.ldo % (a.e.out_f32 ? 4 : 8) == 0 && 
-                (a.e.preact == nullptr || (p.N % (a.e.preact_f32 ? 8 : 16) == 0 && (reinterpret_cast<uintptr_t>(a.e.preact) & 31) == 0));
+    // a warp of the 128 x 64 tile has half a row of bf16 columns; a kept z off 16-byte rows needs the buffer for itself
+    a.tma_out = s != LONE_64 && a.ldo % (a.e.out_f32 ? 4 : 8) == 0 &&
+                (a.e.preact == nullptr || p.N % (a.e.preact_f32 ? 4 : 8) == 0);
     a.blocks_a = !p.a.k_major && p.M % 64 == 0;
     a.blocks_b = !p.b.k_major && p.N % 64 == 0;
     a.rows_a = p.M >= BM ? BM : p.a.k_major ? (int)((p.M + 7) & ~7LL) : p.M > 64 ? 128 : 64;

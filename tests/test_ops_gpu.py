@@ -135,6 +135,13 @@ def test_linear_epilogue(M, K, N, act, dtype, out):
         check_linear(M, K, N, dtype, out, act, bias, residual, alpha=0.375, preact=preact, seed=i, backward=bias and residual)
 
 
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("K", [200, 600])
+def test_linear_epilogue_of_large_tiles(K, dtype, out):
+    """Tiles of 256 x 256 with 16 and with 8 epilogue warps, the last ones partly filled, rows on 16 bytes only."""
+    check_linear(4200, K, 4104, dtype, out, act="silu", residual=True, alpha=0.5, preact=True, seed=6)
+
+
 @pytest.mark.parametrize("xs,rs,ds", [(80, 0, 0), (0, 112, 120), (72, 104, 136), (67, 99, 101), (65, 0, 97)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("M", [3, 70])
