@@ -18,9 +18,9 @@
 // accumulators, so that a tile's epilogue runs under the next tile's MMAs.  Persistent: one CTA per SM, units dealt
 // round-robin in an order that keeps the running tiles' operands in L2.
 //
-// Measured (bf16, from and to bf16): 8192 x 8192 x 2048 142 us (1.94 PFLOP/s, what the library's product takes: 140 us),
-// its two gradients 151 and 163 us (153 and 163), 8192^3 591 us (592), 2048^3 15 us (22).  Bound by the MMAs (88% of the
-// cycles), and at the chip's power limit by its clock.
+// Measured (bf16, from and to bf16): 8192 x 8192 x 2048 142 us (1.94 PFLOP/s; the library's product takes 140), its two
+// gradients 151 and 163 us (153 and 163), 8192^3 590 to 610 us (577 to 592), 2048^3 16.6 us (22).  Bound by the MMAs (87%
+// of the cycles), and at the chip's power limit by its clock; up to 256 k by the epilogue.
 //
 // Every mbarrier wait is bounded (see tc_ptx.cuh); site codes 600 + n.
 #include "csa_tc.cuh"
