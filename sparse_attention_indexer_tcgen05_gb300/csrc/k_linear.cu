@@ -203,22 +203,38 @@ __global__ void __launch_bounds__(1024) db_kernel(const float *sums, int blocks,
     }
 }
 
-// The pieces of a split k axis joined, 4 columns a thread, and the epilogue.  VEC: rows of y, preact and the residual
-// hold whole vectors of 4.
-template <bool VEC>
+// The pieces of a split k axis joined, 4 columns a thread, and the epilogue.  Few outputs take GROUPS warps for each 32 of
+// these threads, every one of them a part of the pieces.  VEC: rows of y, preact and the residual hold whole vectors of 4.
+template <bool VEC, int GROUPS>
 __global__ void __launch_bounds__(256) join_kernel(const float *partial, int splits, long long M, long long N, const Epilogue e)
 {
+    constexpr int Q = 256 / GROUPS;
+    __shared__ float4 part[GROUPS == 1 ? 1 : GROUPS][GROUPS == 1 ? 1 : Q];
     chain_start();
     chain_wait();
-    const long long ldp = partial_stride(N), t = (long long)blockIdx.x * 256 + threadIdx.x;
+    const int q = threadIdx.x % Q, group = threadIdx.x / Q;
+    const long long ldp = partial_stride(N), t = (long long)blockIdx.x * Q + q;
     const long long m = t / (ldp / 4), n = (t - m * (ldp / 4)) * 4;
-    if (m >= M || n >= N) return;
+    const bool live = m < M && n < N;
     float v[4] = {};
+    if (live) {
 #pragma unroll 4
-    for (int s = 0; s < splits; s++) {
-        const float4 x = __ldcs(reinterpret_cast<const float4 *>(partial + (s * M + m) * ldp + n));
-        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        for (int s = group; s < splits; s += GROUPS) {
+            const float4 x = __ldcs(reinterpret_cast<const float4 *>(partial + (s * M + m) * ldp + n));
+            v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        }
     }
+    if constexpr (GROUPS > 1) {
+        part[group][q] = make_float4(v[0], v[1], v[2], v[3]);
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int g = 1; g < GROUPS; g++) {
+            const float4 x = part[g][q];
+            v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        }
+    }
+    if (!live) return;
     const long long i = m * N + n;
     float z[4];
 #pragma unroll
@@ -368,9 +384,12 @@ cudaError_t product(const Product &p, cudaStream_t st)
 {
     const cudaError_t e = launch_product_tc(p, kSms, st);
     if (e != cudaSuccess || p.plan.splits == 1) return e;
-    const long long blocks = (p.M * (partial_stride(p.N) / 4) + 255) / 256;
-    return launch_chained(p.N % 4 == 0 ? join_kernel<true> : join_kernel<false>, dim3((unsigned)blocks), 256, 0, 1, st, p.e.partial,
-                          p.plan.splits, p.M, p.N, p.e);
+    // Too few whole sums to fill the GPU: cut them (the backward of 15401 x 48 x 24, dW from 61 pieces: 28.9 -> 17.0 us).
+    const long long threads = p.M * (partial_stride(p.N) / 4);
+    const bool vec = p.N % 4 == 0, cut = threads <= 256LL * kSms && p.plan.splits >= 4;
+    auto *kernel = cut ? (vec ? join_kernel<true, 8> : join_kernel<false, 8>) : vec ? join_kernel<true, 1> : join_kernel<false, 1>;
+    const unsigned each = cut ? 32 : 256;
+    return launch_chained(kernel, dim3((unsigned)((threads + each - 1) / each)), 256, 0, 1, st, p.e.partial, p.plan.splits, p.M, p.N, p.e);
 }
 
 template <typename V, typename O, int TX, bool VEC>
