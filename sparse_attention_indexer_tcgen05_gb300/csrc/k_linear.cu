@@ -161,12 +161,16 @@ dz_kernel(const O *dy, long long ldy, const V *z, int act, bf16 *dz, long long l
             float d[8], q[8];
             d0.floats(valid, d);
             if (act != CSA_ACT_NONE) z0.floats(valid, q);
+            if (act != CSA_ACT_NONE) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                // rounded before it is added, whichever outputs are asked for
-                if (act != CSA_ACT_NONE) d[j] = __fmul_rn(d[j], act_grad(q[j], act));
-                s[j] += d[j];
+                for (int j = 0; j < 8; j += 2) {
+                    const float2 g = act_grad2(make_float2(q[j], q[j + 1]), act);
+                    d[j] = __fmul_rn(d[j], g.x);  // rounded before it is added, whichever outputs are asked for
+                    d[j + 1] = __fmul_rn(d[j + 1], g.y);
+                }
             }
+#pragma unroll
+            for (int j = 0; j < 8; j++) s[j] += d[j];
             if (dz != nullptr) put_planes8<V>(dz, plane, r * ld + n, d);  // up to 7 values of padding
         }
     }

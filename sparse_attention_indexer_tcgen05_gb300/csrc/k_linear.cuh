@@ -2,6 +2,7 @@
 #pragma once
 
 #include "csa_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace csa {
 namespace linear {
@@ -39,19 +40,25 @@ __device__ __forceinline__ float act_fwd(float z, int act)
     return z;
 }
 
-__device__ __forceinline__ float act_grad(float z, int act)
+// act'(z) of two values, in paired arithmetic: the gradient's pass over dy and z is short of issue slots.
+//   SILU: s (1 + z (1 - s)), s = s(z);  GELU: s + z s (1 - s) kGelu (1 + 3 kCubic z^2), s = gelu_sigmoid(z)
+__device__ __forceinline__ float2 act_grad2(float2 z, int act)
 {
-    if (act == CSA_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+    using ptx::fma2;
+    using ptx::mul2;
+    const auto both = [](float x) { return make_float2(x, x); };
     if (act == CSA_ACT_SILU) {
-        const float s = sigmoid(z);
-        return s * (1.f + z * (1.f - s));
+        const float2 t = mul2(z, both(-kLog2e)), s = make_float2(sigmoid2(t.x), sigmoid2(t.y));
+        return mul2(s, fma2(z, fma2(s, both(-1.f), both(1.f)), both(1.f)));
     }
     if (act == CSA_ACT_GELU_TANH) {
-        const float s = gelu_sigmoid(z);
-        const float q = s * (1.f - s);  // 0 far out, where z^2 may overflow
-        return q > 0.f ? s + z * q * kGelu * (1.f + 3.f * kCubic * z * z) : s;
+        const float2 zz = mul2(z, z), t = mul2(z, fma2(zz, both(-kLog2e * kGelu * kCubic), both(-kLog2e * kGelu)));
+        const float2 s = make_float2(sigmoid2(t.x), sigmoid2(t.y));
+        const float2 q = mul2(s, fma2(s, both(-1.f), both(1.f)));  // 0 far out, where z^2 may overflow
+        const float2 g = fma2(mul2(z, q), fma2(zz, both(3.f * kCubic * kGelu), both(kGelu)), s);
+        return make_float2(q.x > 0.f ? g.x : s.x, q.y > 0.f ? g.y : s.y);
     }
-    return 1.f;
+    return make_float2(z.x > 0.f ? 1.f : 0.f, z.y > 0.f ? 1.f : 0.f);  // ReLU
 }
 
 // Where a product's sums go.  y = act(alpha sum + bias[n]) + res; with `partial` the bare sums of split s go to
