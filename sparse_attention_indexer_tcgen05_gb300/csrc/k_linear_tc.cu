@@ -199,7 +199,11 @@ template <typename O> struct Residual {
 template <int ACT> __device__ __forceinline__ void activate(float (&v)[C])
 {
 #pragma unroll
-    for (int k = 0; k < C; k++) v[k] = act_fwd<ACT>(v[k]);
+    for (int k = 0; k < C; k += 2) {
+        const float2 y = act_fwd2<ACT>(make_float2(v[k], v[k + 1]));
+        v[k] = y.x;
+        v[k + 1] = y.y;
+    }
 }
 
 __device__ __forceinline__ uint32_t pack2(float a, float b)
