@@ -138,7 +138,6 @@ small_kernel(const V *x, long long ldx, const V *w, int M, int N, int K, int ks,
 
 // ------------------------------------------------------------------ bf16, up to 16 rows
 
-
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -146,8 +145,9 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// MT tiles of 8 rows of x, WARPS_K warps of a CTA on the same rows of W, DEPTH pieces of 32 k of a warp in flight.  Lane (g, t) = (lane / 4, lane % 4) holds row g (and g + 8) of W's fragments, column g of x's
-// and, of the sums, rows g and g + 8 of W at columns 2 t and 2 t + 1 of x.
+// MT tiles of 8 rows of x, WARPS_K warps of a CTA on the same rows of W, DEPTH pieces of 32 k of a warp in flight.  Lane
+// (g, t) = (lane / 4, lane % 4) holds row g (and g + 8) of W's fragments, column g of x's and, of the sums, rows g and
+// g + 8 of W at columns 2 t and 2 t + 1 of x.
 template <int MT, int WARPS_K, int DEPTH>
 __global__ void __launch_bounds__(32 * WARPS_K)
 few_kernel(const bf16 *x, long long ldx, const bf16 *w, int M, int N, int K, const Epilogue e)
