@@ -176,6 +176,19 @@ def test_linear_residual_in_place():
         assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("M,K,N", [(12, 200, 77), (300, 64, 1003), (3000, 128, 2053), (2600, 600, 2056), (40, 8192, 49)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_linear_residual_in_place_of_odd_rows(M, K, N, dtype):
+    """Rows off the 16-byte boundaries, whose vectors hold other rows' ends; tiles of every kind and a cut k axis."""
+    t = linear_inputs(M, K, N, dtype, dtype, 8)
+    p = B.LinearParams(M, K, N, dtype, activation="gelu_tanh")
+    want = B.csa_linear_fwd(p, t["x"], t["w"], t["bias"], t["res"])
+    for _ in range(3):
+        got = t["res"].clone()
+        B.csa_linear_fwd(p, t["x"], t["w"], t["bias"], got, out=got)
+        assert torch.equal(got, want)
+
+
 def test_linear_writes_its_rows_only():
     """Outputs inside larger buffers: nothing before or behind them is written."""
     for M, K, N in ((5, 40, 56), (130, 136, 200), (131, 77, 33)):
