@@ -261,8 +261,8 @@ size_t csa_linear_bwd_workspace_size(const csa_linear_params *p);
  *      activation reads.
  * Sums and the epilogue are fp32, rounded once (a bf16 result's sums are cut off where the tensor core aligns them,
  * 2^-24 of the sum for each 16 k; those of an fp32 result are kept).  fp32 values are multiplied as three bf16 parts
- * each (six products, about 2^-23 relative to the terms); an infinite fp32 value (or one above the largest bf16,
- * 3.39e38) gives its row NaN or an infinity.  y may be the residual itself when their row strides agree;
+ * each (six products, about 2^-23 relative to the terms); an infinite fp32 value gives its row NaN or
+ * an infinity.  y may be the residual itself when their row strides agree;
  * an output given as another argument is refused otherwise.  rows and features up to 2^31 - 2^16. */
 csa_status csa_linear_fwd(const csa_linear_params *p, const void *x, const void *weight, const float *bias,
                           const void *residual, void *y, void *preact, void *workspace, size_t workspace_bytes,

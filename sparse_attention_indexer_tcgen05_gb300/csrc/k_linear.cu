@@ -8,10 +8,12 @@ namespace linear {
 
 using bf16 = __nv_bfloat16;
 
-// x = h + m + l with bf16 parts: 8 bits of the significand each.  What h cannot hold as a finite number stays in h.
+// x = h + m + l with bf16 parts: 8 bits of the significand each.  Infinities and NaN stay in h; a finite x that would
+// round to an infinity is cut off instead.
 __device__ __forceinline__ void split3(float x, bf16 &h, bf16 &m, bf16 &l)
 {
     h = __float2bfloat16_rn(x);
+    if (fabsf(x) > 3.38e38f && fabsf(x) < INFINITY) h = __ushort_as_bfloat16((unsigned short)(__float_as_uint(x) >> 16));
     const float r = x - __bfloat162float(h);
     const bool fine = fabsf(r) <= 3.0e38f;  // false for NaN and infinities
     m = __float2bfloat16_rn(fine ? r : 0.f);

@@ -219,6 +219,20 @@ def test_linear_nan_and_infinity_stay_in_their_rows():
             assert torch.equal(y[keep], clean[keep])
 
 
+def test_linear_largest_fp32_values():
+    """Finite values that the nearest bf16 number would overflow."""
+    top = torch.finfo(torch.float32).max
+    x = torch.zeros(20, 16, device="cuda")
+    x[:, 3] = torch.tensor([top, -top, 3.395e38, 3.3895e38, 3.38e38] * 4, device="cuda")
+    w = torch.zeros(24, 16, device="cuda")
+    w[:, 3] = torch.linspace(-0.9, 0.9, 24, device="cuda")
+    y = B.csa_linear_fwd(B.LinearParams(20, 16, 24, "f32"), x, w)
+    want = x.double() @ w.double().t()
+    close(y, want, product_tol(want.abs(), 1), "y")
+    dw = B.csa_linear_bwd(B.LinearParams(20, 16, 24, "f32"), torch.full((20, 24), 2.0 ** -6, device="cuda"), x, w, need_dx=False)[1]
+    close(dw, x.double().sum(0).expand(24, 16) * 2.0 ** -6, product_tol(x.double().abs().sum(0) * 2.0 ** -6, 20), "dw")
+
+
 def test_linear_the_same_bits_again_and_from_two_streams():
     t = linear_inputs(700, 512, 264, "bf16", "bf16", 6)
     p = B.LinearParams(700, 512, 264, activation="gelu_tanh")
