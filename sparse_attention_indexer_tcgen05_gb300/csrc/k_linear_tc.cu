@@ -443,9 +443,12 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                     }
                 }
             }
-            // the copies must have landed before the CTAs of the pair exit (the leader's barriers count both CTAs')
-            if (rank == 0)
-                for (int i = 0; i < (wrapped ? S : used); i++) drain_bar(full + i, i < st ? ph : ph ^ 1, &g_lin_error);
+            // the copies must have landed before the CTAs of the pair exit (the leader's barriers count both CTAs'), and so
+            // must the arrivals that the leader's commits send to this CTA's barriers: its shared memory is another's then
+            for (int i = 0; i < (wrapped ? S : used); i++) {
+                if (rank == 0) drain_bar(full + i, i < st ? ph : ph ^ 1, &g_lin_error);
+                drain_bar(empty + i, i < st ? ph : ph ^ 1, &g_lin_error);
+            }
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMA issue (whole warp, the pair's even CTA)
@@ -488,8 +491,8 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             }
             if constexpr (CG == 2) mma_commit_pair_w(done);
             else mma_commit_w(done);
-            drain_bar(done, 0, &g_lin_error);
         }
+        drain_bar(done, 0, &g_lin_error);  // in either CTA: the commit arrives in both
     } else {
         // ---------------------------------------------------------- epilogue (8 or 16 warps)
         const int quad = warp & 3;               // TMEM lanes this warp may access

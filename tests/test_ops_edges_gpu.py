@@ -1,0 +1,47 @@
+"""The operators around the step where they can go wrong: kernels close behind one another, ends of buffers, infinities,
+sums over very many rows, gradients that share memory.
+
+Tolerances are worst cases of the arithmetic, as in test_ops_gpu.py: u(t) = finfo(t).eps / 2.
+"""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from sparse_attention_indexer_tcgen05_gb300 import binding as B  # noqa: E402
+
+BF, F32 = torch.bfloat16, torch.float32
+U = {BF: 2.0 ** -8, F32: 2.0 ** -24}
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def randn(g, *shape, dtype=F32, scale=1.0):
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def test_products_close_behind_one_another():
+    """Products of every tile shape in one stream with nothing between them: each starts on the SMs that its predecessor
+    leaves, with barriers in the same places of shared memory."""
+    g = gen(1)
+    calls = []
+    for M, K, N, dt, out in ((2048, 1024, 2048, "bf16", "bf16"), (1024, 512, 1024, "bf16", "bf16"), (512, 2048, 512, "bf16", "f32"),
+                             (300, 512, 640, "f32", "f32"), (64, 256, 512, "bf16", "bf16"), (4096, 64, 4096, "bf16", "bf16")):
+        t = BF if dt == "bf16" else F32
+        p = B.LinearParams(M, K, N, dt, out)
+        x, w = randn(g, M, K, dtype=t), randn(g, N, K, dtype=t, scale=K ** -0.5)
+        ws = torch.empty(max(1, p.fwd_workspace_bytes), dtype=torch.uint8, device="cuda")
+        first = B.csa_linear_fwd(p, x, w, workspace=ws)
+        want = x.double() @ w.double().t()
+        assert float((first.double() - want).norm() / want.norm()) <= U[first.dtype] + (K // 16 + 8) * 2.0 ** -23
+        calls.append((p, x, w, ws, first, torch.empty_like(first)))
+    torch.cuda.synchronize()
+    for r in range(60):
+        for p, x, w, ws, _, y in calls if r % 2 else calls[::-1]:
+            B.csa_linear_fwd(p, x, w, workspace=ws, out=y)
+    for *_, first, y in calls:
+        assert torch.equal(first, y)
+    B.csa_check_device_status()
