@@ -34,19 +34,20 @@ struct Stage {
 };
 
 // 8 neighbouring values from p on, of which `valid` (1 to 8) exist; the others 0.  ALIGNED: p lies on 16 bytes and all
-// exist.  Otherwise p lies anywhere: the aligned vectors that hold the existing values are loaded, and shifted when the
-// values are taken.
+// exist.  Otherwise p lies anywhere: the aligned vectors that hold the existing values are loaded, up to the argument's
+// `end`, and shifted when the values are taken.
 template <typename T, bool ALIGNED> struct Raw8 {
     static constexpr int V = sizeof(T) == 2 ? 1 : 2;   // vectors of 8 values
     uint32_t w[4 * V + (ALIGNED ? 0 : 4)], sh;
-    __device__ __forceinline__ void load(const T *p, int valid)
+    __device__ __forceinline__ void load(const T *p, int valid, const T *end)
     {
         sh = ALIGNED ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
         const uint4 *q = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) - sh);
 #pragma unroll
         for (int k = 0; k < V + (ALIGNED ? 0 : 1); k++) {
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (ALIGNED || (int)sh + valid * (int)sizeof(T) > 16 * k) v = __ldcs(q + k);
+            if (ALIGNED) v = __ldcs(q + k);
+            else if ((int)sh + valid * (int)sizeof(T) > 16 * k) v = load16(q + k, end);
             w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
         }
     }
@@ -76,10 +77,10 @@ template <typename T, bool ALIGNED> struct Raw8 {
         }
     }
 };
-template <typename T, bool ALIGNED> __device__ __forceinline__ void load8(const T *p, int valid, float (&x)[8])
+template <typename T, bool ALIGNED> __device__ __forceinline__ void load8(const T *p, int valid, const T *end, float (&x)[8])
 {
     Raw8<T, ALIGNED> r;
-    r.load(p, valid);
+    r.load(p, valid, end);
     r.floats(valid, x);
 }
 
@@ -111,10 +112,10 @@ template <typename V> __device__ __forceinline__ void stage_block(const Stage &s
     const long long r = t <= 0xffffffffLL ? (long long)((uint32_t)t / (uint32_t)chunks) : t / chunks;
     if (r >= s.rows) return;
     const int c = (int)(t - r * chunks) * 8;
-    const V *x = static_cast<const V *>(s.x) + r * s.stride + c;
+    const V *x = static_cast<const V *>(s.x) + r * s.stride + c, *end = static_cast<const V *>(s.x) + (s.rows - 1) * s.stride + s.cols;
     float v[8];
-    if (s.aligned && c + 8 <= s.cols) load8<V, true>(x, 8, v);
-    else load8<V, false>(x, min(8, s.cols - c), v);
+    if (s.aligned && c + 8 <= s.cols) load8<V, true>(x, 8, end, v);
+    else load8<V, false>(x, min(8, s.cols - c), end, v);
     put_planes8<V>(s.out, s.plane, r * s.ld + c, v);
 }
 
@@ -152,8 +153,8 @@ dz_kernel(const O *dy, long long ldy, const V *z, int act, bf16 *dz, long long l
         Raw8<V, VEC> z0, z1;
         const auto ask = [&](long long r) {
             if (r >= r1) return;
-            d1.load(dy + r * ldy + n, valid);
-            if (act != CSA_ACT_NONE) z1.load(z + r * N + n, valid);
+            d1.load(dy + r * ldy + n, valid, dy + (M - 1) * ldy + N);
+            if (act != CSA_ACT_NONE) z1.load(z + r * N + n, valid, z + M * N);
         };
         ask(r0 + ty);
         for (long long r = r0 + ty; r < r1; r += TY) {

@@ -117,6 +117,19 @@ cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, int threads, size_t 
     return e;
 }
 
+// The aligned 16 bytes at q of an argument that ends at `end`: nothing from there on is read (its place holds 0).
+__device__ __forceinline__ uint4 load16(const uint4 *q, const void *end)
+{
+    if (q + 1 <= end) return __ldcs(q);
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const uint32_t *p = reinterpret_cast<const uint32_t *>(q) + k;
+        w[k] = p + 1 <= end ? *p : reinterpret_cast<const unsigned short *>(p) + 1 <= end ? *reinterpret_cast<const unsigned short *>(p) : 0u;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // One operand of a product over k: element (i, k) of plane q at base + q * plane + (k_major ? i ld + k : k ld + i).
 // fp32 values are held as three bf16 planes, x = h + m + l.
 struct Operand {

@@ -176,7 +176,7 @@ template <typename O> struct Residual {
 #pragma unroll
             for (int k = 0; k <= W / 4; k++) {
                 uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (end > 16 * k) x = q[k];
+                if (end > 16 * k) x = load16(q + k, at(a, a.M - 1, a.N));
                 u[4 * k] = x.x; u[4 * k + 1] = x.y; u[4 * k + 2] = x.z; u[4 * k + 3] = x.w;
             }
             if (sh & 8) {

@@ -45,3 +45,28 @@ def test_products_close_behind_one_another():
     for *_, first, y in calls:
         assert torch.equal(first, y)
     B.csa_check_device_status()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,K,N", [(129, 77, 33), (40, 1001, 8), (33, 9, 1001), (300, 65, 771)])
+def test_arguments_that_end_inside_a_vector(M, K, N, dtype):
+    """Arguments whose last value is the last of a buffer of which only they are defined: what lies behind them is NaN in
+    one run and 7 in another, which changes nothing."""
+    t = BF if dtype == "bf16" else F32
+    g = gen(M + K + N)
+    p = B.LinearParams(M, K, N, dtype, activation="silu")
+
+    def put(x, behind):
+        buf = torch.full((x.numel() + 64,), behind, dtype=x.dtype, device="cuda")
+        v = buf[:x.numel()].view(x.shape)
+        v.copy_(x)
+        return v
+
+    args = [randn(g, M, K, dtype=t), randn(g, N, K, dtype=t), randn(g, N), randn(g, M, N, dtype=t), randn(g, M, N, dtype=t),
+            randn(g, M, N, dtype=t)]
+    got = []
+    for behind in (7.0, float("nan")):
+        x, w, b, res, dy, z = (put(a, behind) for a in args)
+        got.append((B.csa_linear_fwd(p, x, w, b, res), *B.csa_linear_bwd(p, dy, x, w, z)))
+    for a, b in zip(*got):
+        assert bool(a.isfinite().all()) and torch.equal(a, b)
