@@ -831,8 +831,14 @@ class CSALinear(torch.autograd.Function):
         x, weight, preact = ctx.saved_tensors
         c = ctx.params.c
         need = ctx.needs_input_grad
-        dx = dw = db = None
-        dy = _own(dy)
+        dx = dw = db = dres = None
+        given, dy = dy, _own(dy)
+        if need[3]:
+            # Autograd may keep what it is handed as a .grad and add to it, unless it is the incoming tensor itself: a view
+            # of that one would share its memory with the caller's gradient and with other leaves' .grad.
+            dres = dy if dy.shape == ctx.residual_shape else dy.reshape(ctx.residual_shape)
+            if dres is not given and dres.data_ptr() == given.data_ptr():
+                dres = dres.clone()
         if any(need[:3]):
             p = ctx.params
             if c.dy_stride:  # autograd hands contiguous gradients over
@@ -841,7 +847,7 @@ class CSALinear(torch.autograd.Function):
             dx, dw, db = csa_linear_bwd(p, dy, x, weight.contiguous(), preact, need[0], need[1], need[2])
         return (dx.view(ctx.x_shape) if dx is not None else None, dw.view(weight.shape) if dw is not None else None,
                 db.view(ctx.bias_shape) if db is not None else None,
-                dy.view(ctx.residual_shape) if need[3] else None, None)
+                dres, None)
 
 
 def csa_linear(x, weight, bias=None, residual=None, *, params: LinearParams):
