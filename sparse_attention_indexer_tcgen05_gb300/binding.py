@@ -471,6 +471,11 @@ _current_device = torch._C._cuda_getDevice
 _quick_empty = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
 
 
+# Kernels write through addresses.  Autograd learns from its version counter that a tensor of the caller's has changed, and
+# refuses a backward pass that would read what a forward pass saved of it.
+_changed = torch.autograd.graph.increment_version
+
+
 def _empty(shape, strides, dtype, index):
     if _quick_empty is not None and _current_device() == index:
         return _quick_empty(shape, strides, dtype)
@@ -590,7 +595,8 @@ def csa_linear_fwd(p: LinearParams, x, weight, bias=None, residual=None, workspa
         _check_flat(bias, "bias", torch.float32, dev, N)
     if residual is not None:
         _check_rows(residual, "residual", p.out_value_dtype, dev, M, N, c.residual_stride)
-    if out is None:
+    given = out is not None
+    if not given:
         out = _empty((M, N), (N, 1), p.out_value_dtype, dev)
     else:
         _check_flat(out, "out", p.out_value_dtype, dev, M * N)
@@ -601,6 +607,10 @@ def csa_linear_fwd(p: LinearParams, x, weight, bias=None, residual=None, workspa
     ws, nws = _check_workspace(workspace, dev)
     _invoke("csa_linear_fwd", _lib.csa_linear_fwd, dev, p.ref, x.data_ptr(), weight.data_ptr(), _ptr(bias),
             _ptr(residual), out.data_ptr(), _ptr(preact), ws, nws)
+    if given:
+        _changed(out)
+    if preact is not None:
+        _changed(preact)
     return out
 
 
@@ -635,6 +645,8 @@ def csa_linear_bwd(p: LinearParams, dy, x, weight, preact=None, need_dx=True, ne
     ws, nws = _check_workspace(workspace, dev)
     _invoke("csa_linear_bwd", _lib.csa_linear_bwd, dev, p.ref, dy.data_ptr(), _ptr(x), _ptr(weight), _ptr(preact),
             _ptr(dx), _ptr(dw), _ptr(db), ws, nws)
+    if out is not None:
+        _changed([t for t in (dx, dw, db) if t is not None])
     return dx, dw, db
 
 
@@ -695,7 +707,8 @@ def csa_rope(p: RopeParams, x, positions, inv_freq, out=None):
     _check_heads(x, "x", p, dev, c.x_row_stride, c.x_head_stride)
     _check_flat(positions, "positions", torch.int64 if c.positions_64 else torch.int32, dev, c.axes * c.rows)
     _check_flat(inv_freq, "inv_freq", torch.float64, dev, c.rot_dim // 2)
-    if out is None:
+    given = out is not None
+    if not given:
         if c.out_row_stride or c.out_head_stride:
             raise ValueError("out is required where RopeParams gives its strides")
         out = _empty(tuple(x.shape), x.stride(), x.dtype, dev) if x.is_contiguous() else \
@@ -703,6 +716,8 @@ def csa_rope(p: RopeParams, x, positions, inv_freq, out=None):
     else:
         _check_heads(out, "out", p, dev, c.out_row_stride, c.out_head_stride)
     _invoke("csa_rope", _lib.csa_rope, dev, p.ref, x.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), out.data_ptr())
+    if given:
+        _changed(out)
     return out
 
 
@@ -742,6 +757,7 @@ class AdamWTensors:
             e.m, e.v, e.m_scale, e.v_scale = _ptr(t["m"]), _ptr(t["v"]), _ptr(t["m_scale"]), _ptr(t["v_scale"])
             e.numel, e.param_dtype, e.grad_dtype = numel, DTYPES[t["param"].dtype], DTYPES[t["grad"].dtype]
             e.state_dtype = STATE_E4M3 if eight else STATE_F32
+        self.written = [t for name in ("param", "master") for t in columns[name] if t is not None]  # what a graph may have saved
         spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name, i)
                        for name, c in columns.items() if name != "grad" for i, t in enumerate(c)
                        if t is not None and t.numel())
@@ -800,6 +816,7 @@ def csa_adamw(tensors: AdamWTensors, step, lr=1e-3, beta1=0.9, beta2=0.999, eps=
         _check_flat(found_inf, "found_inf", torch.float32, index, 1)
         p.found_inf = found_inf.data_ptr()
     _invoke("csa_adamw", _lib.csa_adamw, index, ctypes.byref(p), tensors.table, tensors.count)
+    _changed(tensors.written)  # after the launch: 50 ns a tensor
 
 
 def _own(grad):

@@ -70,3 +70,31 @@ def test_arguments_that_end_inside_a_vector(M, K, N, dtype):
         got.append((B.csa_linear_fwd(p, x, w, b, res), *B.csa_linear_bwd(p, dy, x, w, z)))
     for a, b in zip(*got):
         assert bool(a.isfinite().all()) and torch.equal(a, b)
+
+
+def test_autograd_sees_what_the_calls_write():
+    """A graph kept over an optimizer step, or over a call that writes to one of its tensors, refuses its backward pass."""
+    g = gen(3)
+    p = B.LinearParams(24, 16, 16, "f32")
+    x, w = randn(g, 24, 16).requires_grad_(True), randn(g, 16, 16).requires_grad_(True)
+    y = B.csa_linear(x, w, params=p)
+    state = B.AdamWTensors.zero_state([w])
+    B.csa_adamw(B.AdamWTensors([w.detach()], [torch.ones(16, 16, device="cuda")], **state), 1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    r = B.RopeParams(24, 1, 16, "f32")
+    pos, f = torch.arange(24, device="cuda", dtype=torch.int32)[None], torch.ones(8, device="cuda", dtype=torch.float64)
+    dy = randn(g, 24, 16)
+    for write in (lambda t: B.csa_rope(r, t, pos, f, out=t), lambda t: B.csa_linear_fwd(p, dy, w.detach(), residual=t, out=t),
+                  lambda t: B.csa_linear_fwd(p, dy, w.detach(), preact=t),
+                  lambda t: B.csa_linear_bwd(p, dy, dy.clone(), w.detach(), out=(t, None, None))):
+        x = randn(g, 24, 16)
+        y = B.csa_linear(x, w, params=p)
+        write(x)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.sum().backward()
+    with torch.inference_mode():                 # tensors without a counter
+        out = torch.empty(24, 16, device="cuda")
+        assert B.csa_linear_fwd(p, dy, w.detach(), out=out) is out and B.csa_rope(r, out, pos, f, out=out) is out
+    # an unchanged graph goes through
+    B.csa_linear(randn(g, 24, 16), w, params=p).sum().backward()
