@@ -333,12 +333,20 @@ typedef struct {
     const int64_t *step_dev;     /* device scalar that replaces step, or NULL; below 1 it counts as 1 */
     const float *grad_scale;     /* device scalar that every gradient is multiplied by (clipping), or NULL */
     const float *found_inf;      /* device scalar or NULL: not 0 leaves every tensor and state as it is */
+    uint64_t seed;               /* of the stochastic rounding */
+    int32_t stochastic;          /* 0 or 1: how 8-bit codes are rounded (below) */
 } csa_adamw_params;
 
 /* One AdamW step over `count` tensors, t = step:
  *   g = grad_scale grad;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
  *   p = p - lr weight_decay p - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
- * in fp32, with the unrounded m and v in the update.  `tensors` is a host array, read before the call returns.  No
+ * in fp32, with the unrounded m and v in the update.
+ * 8-bit codes are rounded to nearest, or with `stochastic` so that the expected m and v are what the formula gives, by
+ * random numbers that depend on seed, the tensor's place in the list, the element (modulo 2^31) and the step alone.  Over
+ * many steps only stochastic codes follow the recurrences: half a step of a code is up to 5.6% of its value, so nearest
+ * codes stand still under changes below that, all that a step makes of v with beta2 above 0.89 and of m with beta1 above
+ * 0.94.
+ *  `tensors` is a host array, read before the call returns.  No
  * workspace.  Two tensors that name the same param, master, m, v or scale are refused; buffers that overlap in any
  * other way are the caller's error. */
 csa_status csa_adamw(const csa_adamw_params *p, const csa_adamw_tensor *tensors, int32_t count, void *stream);

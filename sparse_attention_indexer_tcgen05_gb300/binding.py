@@ -29,6 +29,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import warnings
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -73,6 +74,7 @@ class csa_params(ctypes.Structure):
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu_tanh": 3}
 STATE_F32, STATE_E4M3 = 0, 1
 ADAMW_BLOCK = 256      # elements that share one scale of an 8-bit state
+NEAREST_BETA2 = 0.89   # up to here a step without gradient moves every e4m3 root by more than half a code
 ROPE_MAX_AXES = 4
 
 
@@ -109,6 +111,7 @@ class csa_adamw_params(ctypes.Structure):
         ("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
         ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64), ("lr_dev", ctypes.c_void_p),
         ("step_dev", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p), ("found_inf", ctypes.c_void_p),
+        ("seed", ctypes.c_uint64), ("stochastic", ctypes.c_int32),
     ]
 
 
@@ -725,9 +728,13 @@ class AdamWTensors:
     """The tensors of csa_adamw, checked and laid out once.  Lists of equal length: param (f32 or bf16), grad (f32 or
     bf16), the moments m and v (both f32, or both float8_e4m3fn with their f32 scales m_scale and v_scale, one per
     ADAMW_BLOCK elements, last block short), and master: an f32 copy that the step updates, param being its rounding
-    (a list, with None for a tensor that has none).  ``AdamWTensors.zero_state`` makes m, v and scales."""
+    (a list, with None for a tensor that has none).  ``AdamWTensors.zero_state`` makes m, v and scales.
 
-    def __init__(self, param, grad, m, v, m_scale=None, v_scale=None, master=None):
+    seed (an integer; zero_state gives one with 8-bit moments) rounds 8-bit moments stochastically, by a hash of seed,
+    tensor, element and step: they then follow their recurrences.  None rounds to nearest, which over many steps follows
+    changes of more than half a code (5.6 %) a step only: beta2 up to NEAREST_BETA2."""
+
+    def __init__(self, param, grad, m, v, m_scale=None, v_scale=None, master=None, seed=None):
         n = len(param)
         none = [None] * n
         columns = dict(param=list(param), grad=list(grad), m=list(m), v=list(v), m_scale=list(m_scale or none),
@@ -738,6 +745,8 @@ class AdamWTensors:
         self.tensors = columns                       # keeps the buffers alive
         self.device = param[0].device if n else None
         self.count = n
+        self.seed = None if seed is None else int(seed) % 2 ** 64
+        self.nearest = False                         # whether 8-bit moments are rounded to nearest
         self.table = (csa_adamw_tensor * n)()
         for i, e in enumerate(self.table):
             t = {name: c[i] for name, c in columns.items()}
@@ -747,6 +756,7 @@ class AdamWTensors:
                     raise ValueError(f"{name}[{i}] must be f32 or bf16, got {t[name].dtype}")
                 _check_tensor(t[name], f"{name}[{i}]", t[name].dtype, self.device, numel)
             eight = t["m"].dtype == torch.float8_e4m3fn
+            self.nearest = self.nearest or (eight and seed is None)
             for name in ("m", "v"):
                 _check_tensor(t[name], f"{name}[{i}]", torch.float8_e4m3fn if eight else torch.float32, self.device, numel)
             for name in ("m_scale", "v_scale") if eight else ():
@@ -766,14 +776,15 @@ class AdamWTensors:
                 raise ValueError(f"{a}[{i}] and {b}[{j}] overlap")
 
     @staticmethod
-    def zero_state(param, eight_bit=False):
-        """m, v (and their scales) before the first step, as keyword arguments of AdamWTensors."""
+    def zero_state(param, eight_bit=False, seed=0):
+        """m, v (for 8 bits also their scales and the seed of their rounding) before the first step, as keyword arguments
+        of AdamWTensors."""
         dt = torch.float8_e4m3fn if eight_bit else torch.float32
         state = {k: [torch.zeros(t.shape, dtype=torch.uint8, device=t.device).view(dt) if eight_bit
                      else torch.zeros(t.shape, dtype=dt, device=t.device) for t in param] for k in ("m", "v")}
         if eight_bit:
             state.update({k: [torch.zeros(-(-t.numel() // ADAMW_BLOCK), dtype=torch.float32, device=t.device)
-                              for t in param] for k in ("m_scale", "v_scale")})
+                              for t in param] for k in ("m_scale", "v_scale")}, seed=seed)
         return state
 
     def set_grads(self, grad):
@@ -794,7 +805,12 @@ def csa_adamw(tensors: AdamWTensors, step, lr=1e-3, beta1=0.9, beta2=0.999, eps=
     """One AdamW step over all tensors, in place.  step (1 for the first) and lr are numbers, or device scalars (int64,
     f32) that are read when the step runs, for a captured graph; grad_scale (f32 device scalar) multiplies every
     gradient; found_inf (f32 device scalar), when not 0, leaves everything as it is."""
-    p = csa_adamw_params(0.0, float(beta1), float(beta2), float(eps), float(weight_decay), 1, None, None, None, None)
+    p = csa_adamw_params(0.0, float(beta1), float(beta2), float(eps), float(weight_decay), 1, None, None, None, None,
+                         tensors.seed or 0, tensors.seed is not None)
+    if tensors.nearest and p.beta2 > NEAREST_BETA2:
+        tensors.nearest = False  # said once
+        warnings.warn(f"8-bit moments rounded to nearest do not follow beta2 = {p.beta2} over many steps: give AdamWTensors "
+                      "a seed", stacklevel=2)
     dev = tensors.device
     if dev is None:
         return

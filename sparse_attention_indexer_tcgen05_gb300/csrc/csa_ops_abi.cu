@@ -143,6 +143,7 @@ csa_status check_adamw(const csa_adamw_params *p, const csa_adamw_tensor *t, int
     if (!isfinite(p->lr) || !isfinite(p->eps) || !isfinite(p->weight_decay) || p->eps < 0) return CSA_ERR_INVALID_ARG;
     if (!(p->beta1 >= 0 && p->beta1 < 1) || !(p->beta2 >= 0 && p->beta2 < 1)) return CSA_ERR_INVALID_ARG;
     if (p->step_dev == nullptr && p->step < 1) return CSA_ERR_INVALID_ARG;
+    if (p->stochastic & ~1) return CSA_ERR_INVALID_ARG;
     CSA_TRY(need_scalar(p->lr_dev, 4));
     CSA_TRY(need_scalar(p->step_dev, 8));
     CSA_TRY(need_scalar(p->grad_scale, 4));

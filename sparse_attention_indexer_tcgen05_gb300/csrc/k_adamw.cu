@@ -8,6 +8,13 @@
 // a factor of 448 / 2^-9 = 2.3e5 of it (the square would leave a factor of 480 in the root).  A code of v > 0 is at
 // least the smallest one, 2^-9: a root that rounded to 0 while m did not would leave eps alone in the divisor.
 //
+// Codes are rounded to nearest or stochastically.  A step changes the root by a factor of sqrt(b2) at most downwards (2.5%
+// at 0.95, 0.05% at 0.999) and half an e4m3 step is 3 to 6% of a value, so nearest codes go back to where they were: a root
+// whose gradients shrink tenfold stays up to twelve times too large (b2 = 0.99).  Stochastic codes take the upper neighbour
+// with the probability that makes the expected m, and the expected v (the square of the held root), what the formula gives:
+// the recurrences are linear in both, so the held moments follow them without a bias, whatever the betas; a root then
+// scatters by about a code.  The random number is a hash of seed, tensor, element and step: the same bits every time.
+//
 // Bound by memory: every state, weight and gradient is read and written once.  A warp owns one block of 256 elements,
 // 8 consecutive ones per lane, so each tensor is read and written in 8- or 16-byte accesses, the block's two maxima
 // are warp reductions and no shared memory is needed.  The tensors' pointers travel in the kernel's parameters (no
@@ -19,6 +26,7 @@
 
 #include <cuda_fp8.h>
 #include <math.h>
+#include <type_traits>
 
 namespace csa {
 namespace adamw {
@@ -33,6 +41,8 @@ constexpr int CHUNK = THREADS * VEC;           // elements per CTA
 constexpr float E4M3_MAX = 448.f;
 constexpr float E4M3_TINY = 0.001953125f;      // 2^-9
 
+enum State { F32, NEAREST, STOCHASTIC };  // how a launch's tensors hold their moments
+
 struct Entry {
     void *param;
     const void *grad;
@@ -41,6 +51,7 @@ struct Entry {
     float *m_scale, *v_scale;
     long long numel;
     unsigned first;  // the tensor's first chunk
+    unsigned id;     // its place in the caller's list
 };
 
 struct Hyper {
@@ -49,6 +60,8 @@ struct Hyper {
     float wd, log_b1, log_b2;                // for lr and step on the device
     const float *lr_dev, *grad_scale, *found_inf;
     const int64_t *step_dev;
+    unsigned long long seed;
+    long long step;
 };
 
 template <int CAP> struct Table {
@@ -183,9 +196,76 @@ __device__ __forceinline__ float2 quotient(float2 x, float d, float y)
     return fma2(fma2(q, make_float2(-d, -d), x), yy, q);
 }
 
-template <typename PT, typename GT, bool E4M3, int CAP>
+// A bijection of 32-bit words whose output bits each depend on all input bits: shifts and odd multipliers, twice.
+__device__ __forceinline__ uint32_t mixed(uint32_t x)
+{
+    x = (x ^ (x >> 16)) * 0x9e3779b1u;
+    x = (x ^ (x >> 13)) * 0xc2b2ae3du;
+    return x ^ (x >> 16);
+}
+// The random words of one tensor's step.
+__device__ __forceinline__ uint32_t step_key(unsigned long long seed, unsigned id, long long step)
+{
+    uint32_t k = mixed((uint32_t)seed + 0x68e31da4u);
+    k = mixed(k + (uint32_t)(seed >> 32));
+    k = mixed(k + (uint32_t)step);
+    k = mixed(k + (uint32_t)(step >> 32));
+    return mixed(k + id);
+}
+
+// e4m3 neighbours of a >= 0: codes keep 3 mantissa bits, and below 2^-6 are 2^-9 apart, as fp32 numbers with 3 mantissa
+// bits are from 2^-6 on; so those are taken 2^-6 higher.
+constexpr float E4M3_NORMAL = 0.015625f;
+constexpr uint32_t E4M3_REST = 0xfffffu;       // mantissa bits that a code drops
+
+// Two values with the code above each in magnitude taken with the probability of its place between its neighbours.  A word
+// of the random ones serves an element: 12 bits for m, 23 for the root, whose steps are the shorter ones (1 - b2 of a code).
+// ALL: every value is finite and E4M3_NORMAL at least.  (412 million weights: 1254 us; 1516 by the general path alone; codes
+// to nearest 1086.)
+template <bool ALL> __device__ __forceinline__ float2 stochastic(float2 x, uint32_t w0, uint32_t w1)
+{
+    const uint32_t r0 = (w0 & 0xfffu) << 8 | 0x80u, r1 = (w1 & 0xfffu) << 8 | 0x80u;
+    if constexpr (ALL)
+        return make_float2(__uint_as_float((__float_as_uint(x.x) + r0) & ~E4M3_REST), __uint_as_float((__float_as_uint(x.y) + r1) & ~E4M3_REST));
+    const auto one = [](float v, uint32_t r) {
+        const float a = fabsf(v), off = a < E4M3_NORMAL ? E4M3_NORMAL : 0.f;
+        const float c = __uint_as_float((__float_as_uint(a + off) + r) & ~E4M3_REST) - off;
+        return a <= 3.40282347e38f ? copysignf(c, v) : v;  // NaN stays
+    };
+    return make_float2(one(x.x, r0), one(x.y, r1));
+}
+// The same of two roots whose squares are to keep their expected values: hi with (x^2 - lo^2) / (hi^2 - lo^2).
+template <bool ALL> __device__ __forceinline__ float2 stochastic_root(float2 x, uint32_t w0, uint32_t w1)
+{
+    const float2 off = make_float2(!ALL && x.x < E4M3_NORMAL ? E4M3_NORMAL : 0.f, !ALL && x.y < E4M3_NORMAL ? E4M3_NORMAL : 0.f);
+    const float2 y = ALL ? x : add2(x, off);
+    const uint32_t b0 = __float_as_uint(y.x) & ~E4M3_REST, b1 = __float_as_uint(y.y) & ~E4M3_REST;
+    float2 lo = make_float2(__uint_as_float(b0), __uint_as_float(b1));
+    float2 hi = make_float2(__uint_as_float(b0 + E4M3_REST + 1u), __uint_as_float(b1 + E4M3_REST + 1u));
+    if constexpr (!ALL) {
+        lo = make_float2(lo.x - off.x, lo.y - off.y);
+        hi = make_float2(hi.x - off.x, hi.y - off.y);
+    }
+    // u in [1, 2): hi where (u - 1) (hi^2 - lo^2) < x^2 - lo^2
+    const float2 u = make_float2(__uint_as_float(0x3f800000u | w0 >> 9), __uint_as_float(0x3f800000u | w1 >> 9));
+    const float2 minus = make_float2(-lo.x, -lo.y), q = mul2(add2(hi, minus), add2(hi, lo));
+    const float2 d = fma2(make_float2(-u.x, -u.y), q, fma2(add2(x, minus), add2(x, lo), q));
+    const float2 c = make_float2(d.x > 0.f ? hi.x : lo.x, d.y > 0.f ? hi.y : lo.y);
+    if constexpr (ALL) return c;
+    return make_float2(x.x <= 3.40282347e38f ? c.x : x.x, x.y <= 3.40282347e38f ? c.y : x.y);
+}
+// min(a, |b|); NaN if one is
+__device__ __forceinline__ float least(float a, float b)
+{
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+    return r;
+}
+
+template <typename PT, typename GT, State STATE, int CAP>
 __global__ void __launch_bounds__(THREADS, 12) adamw_kernel(const __grid_constant__ Table<CAP> tab, const Hyper h)
 {
+    constexpr bool E4M3 = STATE != F32;
     if (h.found_inf != nullptr && *h.found_inf != 0.f) return;
     int lo = 0, hi = tab.n - 1;
     while (lo < hi) {
@@ -263,9 +343,31 @@ __global__ void __launch_bounds__(THREADS, 12) adamw_kernel(const __grid_constan
 #pragma unroll
         for (int k = 0; k < PAIRS; k++) {
             m[k] = quotient(m[k], sm, ym);
-            const float2 c = quotient(r[k], sr, yr);
-            v[k].x = r[k].x > 0.f ? fmaxf(c.x, E4M3_TINY) : c.x;  // keeps NaN
-            v[k].y = r[k].y > 0.f ? fmaxf(c.y, E4M3_TINY) : c.y;
+            v[k] = quotient(r[k], sr, yr);
+        }
+        if constexpr (STATE == STOCHASTIC) {
+            const uint32_t key = step_key(h.seed, e.id, h.step_dev != nullptr ? max(*h.step_dev, (int64_t)1) : h.step);
+            float low = E4M3_MAX;
+#pragma unroll
+            for (int k = 0; k < PAIRS; k++) low = least(least(low, m[k].x), least(least(low, m[k].y), least(v[k].x, v[k].y)));
+            const auto draw = [&](auto all) {
+#pragma unroll
+                for (int k = 0; k < PAIRS; k++) {
+                    // elements 2^31 apart share their word; a pair's second word is the first one mixed on
+                    const uint32_t w0 = mixed(key + (uint32_t)(i + 2 * k));
+                    uint32_t w1 = w0 * 0x85ebca77u;
+                    w1 ^= w1 >> 15;
+                    m[k] = stochastic<decltype(all)::value>(m[k], w0, w1);
+                    v[k] = stochastic_root<decltype(all)::value>(v[k], w0, w1);
+                }
+            };
+            if (low >= E4M3_NORMAL) draw(std::true_type());
+            else draw(std::false_type());
+        }
+#pragma unroll
+        for (int k = 0; k < PAIRS; k++) {
+            v[k].x = r[k].x > 0.f ? fmaxf(v[k].x, E4M3_TINY) : v[k].x;  // keeps NaN
+            v[k].y = r[k].y > 0.f ? fmaxf(v[k].y, E4M3_TINY) : v[k].y;
         }
         store_codes(e.m, i, n, encode8(m));
         store_codes(e.v, i, n, encode8(v));
@@ -283,7 +385,7 @@ __global__ void __launch_bounds__(THREADS, 12) adamw_kernel(const __grid_constan
 // table, whose upload is part of every launch.
 constexpr int CAP_SMALL = 48, CAP_MIDDLE = 128, CAP_LARGE = 440;
 
-template <int CAP> void fill(Table<CAP> &tab, const csa_adamw_tensor *const *t, int n)
+template <int CAP> void fill(Table<CAP> &tab, const csa_adamw_tensor *all, const csa_adamw_tensor *const *t, int n)
 {
     unsigned first = 0;
     for (int k = 0; k < n; k++) {
@@ -297,44 +399,49 @@ template <int CAP> void fill(Table<CAP> &tab, const csa_adamw_tensor *const *t, 
         e.v_scale = t[k]->v_scale;
         e.numel = t[k]->numel;
         e.first = first;
+        e.id = (unsigned)(t[k] - all);
         first += (unsigned)((t[k]->numel + CHUNK - 1) / CHUNK);
     }
     tab.n = n;
 }
 
-template <typename PT, typename GT, bool Q>
-cudaError_t launch_group(const csa_adamw_tensor *const *t, int n, unsigned chunks, const Hyper &h, cudaStream_t st)
+template <typename PT, typename GT, State Q>
+cudaError_t launch_group(const csa_adamw_tensor *all, const csa_adamw_tensor *const *t, int n, unsigned chunks, const Hyper &h, cudaStream_t st)
 {
     if (n <= CAP_SMALL) {
         Table<CAP_SMALL> tab;
-        fill(tab, t, n);
+        fill(tab, all, t, n);
         adamw_kernel<PT, GT, Q, CAP_SMALL><<<chunks, THREADS, 0, st>>>(tab, h);
     } else if (n <= CAP_MIDDLE) {
         Table<CAP_MIDDLE> tab;
-        fill(tab, t, n);
+        fill(tab, all, t, n);
         adamw_kernel<PT, GT, Q, CAP_MIDDLE><<<chunks, THREADS, 0, st>>>(tab, h);
     } else {
         Table<CAP_LARGE> tab;
-        fill(tab, t, n);
+        fill(tab, all, t, n);
         adamw_kernel<PT, GT, Q, CAP_LARGE><<<chunks, THREADS, 0, st>>>(tab, h);
     }
     note_launches(1);
     return cudaGetLastError();
 }
 
-cudaError_t launch_kind(int kind, const csa_adamw_tensor *const *t, int n, unsigned chunks, const Hyper &h,
-                        cudaStream_t st)
+// kind: 4 (param is bf16) + 2 (grad is bf16) + (8-bit states)
+cudaError_t launch_kind(int kind, bool stochastic, const csa_adamw_tensor *all, const csa_adamw_tensor *const *t, int n,
+                        unsigned chunks, const Hyper &h, cudaStream_t st)
 {
     using bf = __nv_bfloat16;
-    switch (kind) {
-    case 0: return launch_group<float, float, false>(t, n, chunks, h, st);
-    case 1: return launch_group<float, float, true>(t, n, chunks, h, st);
-    case 2: return launch_group<float, bf, false>(t, n, chunks, h, st);
-    case 3: return launch_group<float, bf, true>(t, n, chunks, h, st);
-    case 4: return launch_group<bf, float, false>(t, n, chunks, h, st);
-    case 5: return launch_group<bf, float, true>(t, n, chunks, h, st);
-    case 6: return launch_group<bf, bf, false>(t, n, chunks, h, st);
-    default: return launch_group<bf, bf, true>(t, n, chunks, h, st);
+    const auto run = [&](auto param, auto grad) {
+        using P = decltype(param);
+        using G = decltype(grad);
+        if ((kind & 1) == 0) return launch_group<P, G, F32>(all, t, n, chunks, h, st);
+        if (stochastic) return launch_group<P, G, STOCHASTIC>(all, t, n, chunks, h, st);
+        return launch_group<P, G, NEAREST>(all, t, n, chunks, h, st);
+    };
+    switch (kind >> 1) {
+    case 0: return run(float(), float());
+    case 1: return run(float(), bf());
+    case 2: return run(bf(), float());
+    default: return run(bf(), bf());
     }
 }
 
@@ -359,6 +466,8 @@ cudaError_t launch_adamw(const csa_adamw_params &p, const csa_adamw_tensor *t, i
     h.log_b2 = (float)log(p.beta2);
     h.lr_dev = p.lr_dev;
     h.step_dev = p.step_dev;
+    h.seed = p.seed;
+    h.step = p.step;
     h.grad_scale = p.grad_scale;
     h.found_inf = p.found_inf;
     for (int kind = 0; kind < 8; kind++) {
@@ -373,7 +482,7 @@ cudaError_t launch_adamw(const csa_adamw_params &p, const csa_adamw_tensor *t, i
             }
             const unsigned long long c = k < count ? (unsigned long long)(t[k].numel + CHUNK - 1) / CHUNK : 0;
             if (n > 0 && (k == count || n == CAP_LARGE || chunks + c > 0x7fffffffull)) {
-                const cudaError_t e = launch_kind(kind, group, n, (unsigned)chunks, h, st);
+                const cudaError_t e = launch_kind(kind, p.stochastic != 0, t, group, n, (unsigned)chunks, h, st);
                 if (e != cudaSuccess) return e;
                 n = 0;
                 chunks = 0;

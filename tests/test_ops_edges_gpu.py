@@ -98,3 +98,164 @@ def test_autograd_sees_what_the_calls_write():
         assert B.csa_linear_fwd(p, dy, w.detach(), out=out) is out and B.csa_rope(r, out, pos, f, out=out) is out
     # an unchanged graph goes through
     B.csa_linear(randn(g, 24, 16), w, params=p).sum().backward()
+
+
+# ------------------------------------------------------------------ AdamW with 8-bit moments over many steps
+
+def held(t, i=0):
+    """m and v that an 8-bit state stands for."""
+    c = {k: t.tensors[k][i] for k in ("m", "v", "m_scale", "v_scale")}
+    blk = torch.arange(c["m"].numel(), device="cuda") // 256
+    return c["m"].double() * c["m_scale"].double()[blk], (c["v"].double() * c["v_scale"].double()[blk]) ** 2
+
+
+def recurrences(beta2, steps, gradient, n=256 * 16):
+    """An 8-bit and an fp32 state after the same gradients (gradient(step, out) writes them)."""
+    w, grad = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    sides = [B.AdamWTensors([w.clone()], [grad], **B.AdamWTensors.zero_state([w], eight)) for eight in (True, False)]
+    for t in range(steps):
+        gradient(t, grad)
+        for s in sides:
+            B.csa_adamw(s, t + 1, beta1=0.9, beta2=beta2)
+    return sides
+
+
+@pytest.mark.parametrize("beta2,steps", [(0.95, 1500), (0.98, 1500), (0.99, 2000), (0.999, 6000)])
+def test_adamw_8_bit_second_moments_follow_smaller_gradients(beta2, steps):
+    """240 of each 256 gradients become ten times smaller after 300 steps; the held v has fp32's mean all the same.
+
+    A held v is unbiased.  A step moves it by (1 - beta2) |g^2 / v - 1|, about 1 - beta2 of itself on average, through
+    codes at most 27 % of v apart: a variance of 0.27 (1 - beta2) a step, of which 1 / (2 (1 - beta2)) steps remain, so
+    0.14, and as much again for the scale's own moves.  A standard deviation of 0.5, over 3840 elements 0.8 % of the mean;
+    5 % are six of them.  (Rounded to nearest, v stays up to 140 times too large.)"""
+    g = gen(5)
+    few = torch.arange(256 * 16, device="cuda") % 256 < 16
+    size = torch.where(few, 1.0, 0.1)
+
+    def gradient(t, out):
+        out.normal_(generator=g)
+        if t >= 300:
+            out.mul_(size)
+
+    eight, full = recurrences(beta2, steps, gradient)
+    v, want = held(eight)[1], full.tensors["v"][0].double()
+    # 256 of the unchanged ones: 3.1 % of the mean, six times that
+    for part, most in ((few, 0.19), (~few, 0.05)):
+        assert abs(float(v[part].mean() / want[part].mean()) - 1) <= most
+    root = (v / want).sqrt()[~few]
+    assert 0.85 <= float(root.median()) <= 1.1
+    m, want = held(eight)[0], full.tensors["m"][0].double()
+    assert float((m - want).norm() / want.norm()) <= 0.2
+
+
+def test_adamw_8_bit_first_moments_follow_steady_gradients():
+    """m goes all the way to a steady gradient that is up to 30 % off the one before (to nearest it stays where a tenth of
+    what is missing is less than half a code).  Codes are at most an eighth of m apart: a scatter of 6 % about the
+    gradient, that of an average over 200 steps, of which 10 each tell the same, 1.4 %; six times that for every element,
+    over their mean less than 1 %."""
+    g = gen(6)
+    steady = randn(g, 256 * 16).abs() + 0.5
+    steady[::256] = 6.0                                         # the largest of each block: the scale stays
+    off = 1 + 0.3 * (2 * torch.rand(256 * 16, generator=g, device="cuda") - 1)
+    off[::256] = 1.0
+    sums = torch.zeros(256 * 16, device="cuda", dtype=torch.float64)
+    w, grad = torch.zeros(256 * 16, device="cuda"), torch.empty(256 * 16, device="cuda")
+    t = B.AdamWTensors([w], [grad], **B.AdamWTensors.zero_state([w], True))
+    for k in range(500):
+        torch.mul(steady, off if k < 150 else 1.0, out=grad)
+        B.csa_adamw(t, k + 1, beta1=0.9, beta2=0.99)
+        if k >= 300:
+            sums += held(t)[0]
+    off = sums / 200 / steady.double() - 1
+    assert abs(float(off.mean())) <= 0.01 and float(off.abs().max()) <= 0.085
+
+
+def test_adamw_8_bit_stochastic_codes_are_neighbours_and_unbiased():
+    """One step from a known state: each code is next to the value it stands for, on either side of it as often as its
+    place asks; sums over 100000 elements are within six standard deviations."""
+    g = gen(7)
+    n = 256 * 400
+    w, grad = torch.zeros(n, device="cuda"), randn(g, n)
+    t = B.AdamWTensors([w], [grad], **B.AdamWTensors.zero_state([w], True, seed=11))
+    B.csa_adamw(t, 1, beta1=0.9, beta2=0.99)
+    m, v = held(t)
+    want_m = grad.double() * (1 - 0.9)
+    want_v = grad.double() ** 2 * (1 - 0.99)
+    blk = torch.arange(n, device="cuda") // 256
+    for got, want, scale in ((m, want_m, t.tensors["m_scale"][0]), (v.sqrt(), want_v.sqrt(), t.tensors["v_scale"][0])):
+        x = want.abs() / scale.double()[blk]
+        step = torch.exp2(torch.floor(torch.log2(x.clamp_min(2.0 ** -6))) - 3)
+        assert bool(((got.abs() / scale.double()[blk] - x).abs() <= step * (1 + 2.0 ** -16)).all())
+    big = (want_m.abs() / t.tensors["m_scale"][0].double()[blk] > 2.0 ** -6)       # not raised to the smallest code
+    for got, want in ((m.abs(), want_m.abs()), (v, want_v)):
+        d = (got - want)[big]
+        # the fp32 formula's own roundings of v, 2^-21, are one-sided at worst
+        assert abs(float(d.sum())) <= 6 * float(d.norm()) + 2.0 ** -20 * float(want.sum())
+        assert float(d.norm()) > 0.02 * float(want[big].norm())                    # and it is not to nearest
+    # The random words of neighbouring elements, and of m and v of one, do not go together: "up" less its probability p has
+    # the mean 0 for every element, and the mean square p (1 - p) <= 1/4, so products of two have at most 1/16.  (Signs alone
+    # would not do for m and v of one: from a zero state their places p are the same, and E (2 p - 1)^2 = 1/3.)
+    def less_p(x, up):
+        lo = torch.exp2(torch.floor(torch.log2(x.clamp_min(2.0 ** -6))) - 3)
+        return up.double() - (x / lo - torch.floor(x / lo))
+
+    sm, sv = (t.tensors[k][0].double()[blk] for k in ("m_scale", "v_scale"))
+    s = less_p(want_m.abs() / sm, m.abs() > want_m.abs())[big]
+    lo = torch.exp2(torch.floor(torch.log2((want_v.sqrt() / sv).clamp_min(2.0 ** -6))) - 3)
+    x = want_v.sqrt() / sv
+    low = torch.floor(x / lo) * lo
+    r = ((v > want_v).double() - (x - low) * (x + low) / (lo * (2 * low + lo)))[big]
+    for a, b in ((s[1:], s[:-1]), (r[1:], r[:-1]), (s, r), (s[256:], s[:-256])):
+        assert abs(float((a * b).mean())) <= 6 * 0.25 * a.numel() ** -0.5
+
+
+def test_adamw_8_bit_stochastic_codes_are_the_same_every_time():
+    """The same bits from the same seed, tensor and step, replayed from a graph too; others from another seed, step or place
+    in the list."""
+    g = gen(8)
+    w0, grads = randn(g, 5000), [randn(g, 5000), randn(g, 5000)]
+
+    def make(seed, count=1):
+        w = [w0.clone() for _ in range(count)]
+        return B.AdamWTensors(w, [grads[0]] * count, **B.AdamWTensors.zero_state(w, True, seed=seed))
+
+    def codes(t, i=0):
+        return torch.cat([t.tensors[k][i].view(torch.uint8) for k in ("m", "v")])
+
+    step = torch.ones((), dtype=torch.int64, device="cuda")
+    a, b, other, later, pair = make(3), make(3), make(4), make(3), make(3, 2)
+    for t, k in ((a, 1), (b, step), (other, 1), (later, 2), (pair, 1)):
+        B.csa_adamw(t, k)
+    assert torch.equal(codes(a), codes(b)) and torch.equal(codes(a), codes(pair))
+    for t in (codes(other), codes(later), codes(pair, 1)):
+        assert not torch.equal(codes(a), t)
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=s):
+        B.csa_adamw(b, step)
+    for k in (2, 3):
+        step.fill_(k)
+        graph.replay()
+        B.csa_adamw(a, k)
+        torch.cuda.synchronize()
+        assert torch.equal(codes(a), codes(b))
+
+
+def test_adamw_8_bit_nan_gradient_stays_in_its_element_when_stochastic():
+    g = gen(9)
+    w, grad = [randn(g, 600)], [randn(g, 600)]
+    grad[0][10] = float("nan")
+    t = B.AdamWTensors(w, grad, **B.AdamWTensors.zero_state(w, True))
+    for k in (1, 2):
+        B.csa_adamw(t, k)
+        assert int(w[0].isnan().sum()) == int(t.tensors["m"][0].float().isnan().sum()) == int(t.tensors["v"][0].float().isnan().sum()) == 1
+
+
+def test_adamw_8_bit_to_nearest_says_what_it_cannot_follow():
+    g = gen(10)
+    w, grad = [randn(g, 600)], [randn(g, 600)]
+    s = B.AdamWTensors.zero_state(w, True)
+    del s["seed"]
+    t = B.AdamWTensors(w, grad, **s)
+    with pytest.warns(UserWarning, match="beta2"):
+        B.csa_adamw(t, 1)
