@@ -312,7 +312,7 @@ csa_status csa_rope(const csa_rope_params *p, const void *x, const void *positio
  *   CSA_STATE_E4M3: one e4m3 byte per element and one fp32 scale per CSA_ADAMW_BLOCK elements (the last block may be
  *     short): m holds m / m_scale, v holds sqrt(v) / v_scale, each scale the block's largest magnitude / 448.  The
  *     code of a v > 0 is never 0 (it is raised to the smallest one, 2^-9), so that a step is never divided by a
- *     second moment that rounding lost. */
+ *     second moment that rounding lost.  An infinite moment becomes NaN, and counts for no scale. */
 typedef enum { CSA_STATE_F32 = 0, CSA_STATE_E4M3 = 1 } csa_state_dtype;
 
 /* One tensor of an AdamW step; device pointers.  A zero-filled state is the state before the first step. */

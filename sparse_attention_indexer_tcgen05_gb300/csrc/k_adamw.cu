@@ -60,7 +60,7 @@ struct Hyper {
     float wd, log_b1, log_b2;                // for lr and step on the device
     const float *lr_dev, *grad_scale, *found_inf;
     const int64_t *step_dev;
-    unsigned long long seed;
+    uint32_t seed;
     long long step;
 };
 
@@ -197,20 +197,16 @@ __device__ __forceinline__ float2 quotient(float2 x, float d, float y)
 }
 
 // A bijection of 32-bit words whose output bits each depend on all input bits: shifts and odd multipliers, twice.
-__device__ __forceinline__ uint32_t mixed(uint32_t x)
+__host__ __device__ __forceinline__ uint32_t mixed(uint32_t x)
 {
     x = (x ^ (x >> 16)) * 0x9e3779b1u;
     x = (x ^ (x >> 13)) * 0xc2b2ae3du;
     return x ^ (x >> 16);
 }
-// The random words of one tensor's step.
-__device__ __forceinline__ uint32_t step_key(unsigned long long seed, unsigned id, long long step)
+// Where the random words of one tensor's step start.
+__device__ __forceinline__ uint32_t step_key(uint32_t seed, unsigned id, long long step)
 {
-    uint32_t k = mixed((uint32_t)seed + 0x68e31da4u);
-    k = mixed(k + (uint32_t)(seed >> 32));
-    k = mixed(k + (uint32_t)step);
-    k = mixed(k + (uint32_t)(step >> 32));
-    return mixed(k + id);
+    return mixed(mixed(seed + (uint32_t)step) + id * 0x9e3779b1u + (uint32_t)(step >> 32));
 }
 
 // e4m3 neighbours of a >= 0: codes keep 3 mantissa bits, and below 2^-6 are 2^-9 apart, as fp32 numbers with 3 mantissa
@@ -220,8 +216,8 @@ constexpr uint32_t E4M3_REST = 0xfffffu;       // mantissa bits that a code drop
 
 // Two values with the code above each in magnitude taken with the probability of its place between its neighbours.  A word
 // of the random ones serves an element: 12 bits for m, 23 for the root, whose steps are the shorter ones (1 - b2 of a code).
-// ALL: every value is finite and E4M3_NORMAL at least.  (412 million weights: 1254 us; 1516 by the general path alone; codes
-// to nearest 1086.)
+// ALL: every value is finite and E4M3_NORMAL at least.  (412 million weights: 1234 us; 1516 by the general path alone; codes
+// to nearest 1090.)
 template <bool ALL> __device__ __forceinline__ float2 stochastic(float2 x, uint32_t w0, uint32_t w1)
 {
     const uint32_t r0 = (w0 & 0xfffu) << 8 | 0x80u, r1 = (w1 & 0xfffu) << 8 | 0x80u;
@@ -253,6 +249,19 @@ template <bool ALL> __device__ __forceinline__ float2 stochastic_root(float2 x, 
     const float2 c = make_float2(d.x > 0.f ? hi.x : lo.x, d.y > 0.f ? hi.y : lo.y);
     if constexpr (ALL) return c;
     return make_float2(x.x <= 3.40282347e38f ? c.x : x.x, x.y <= 3.40282347e38f ? c.y : x.y);
+}
+// The largest of `top` and those of a, b >= 0 that are finite: with 2^23 added, their bits are positive numbers alone.
+__device__ __forceinline__ float largest_finite(float top, float a, float b)
+{
+    const auto place = [](float x) { return (int)(__float_as_uint(x) + 0x00800000u); };
+    return __int_as_float(max(place(top), max(place(a), place(b))) - 0x00800000);
+}
+// At least the smallest code; NaN stays
+__device__ __forceinline__ float raised(float x)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(E4M3_TINY));
+    return r;
 }
 // min(a, |b|); NaN if one is
 __device__ __forceinline__ float least(float a, float b)
@@ -329,14 +338,31 @@ __global__ void __launch_bounds__(THREADS, 12) adamw_kernel(const __grid_constan
         const float2 d = fma2(r[k], both(rs2), both(h.eps));
         const float2 step = make_float2(__fdividef(m[k].x, d.x), __fdividef(m[k].y, d.y));
         p[k] = fma2(both(-c1), step, fma2(both(-lr_wd), p[k], p[k]));
-        top_m = fmaxf(top_m, fmaxf(fabsf(m[k].x), fabsf(m[k].y)));
-        top_r = fmaxf(top_r, fmaxf(r[k].x, r[k].y));
+        if constexpr (STATE == STOCHASTIC) {
+            top_m = largest_finite(top_m, fabsf(m[k].x), fabsf(m[k].y));
+            top_r = largest_finite(top_r, r[k].x, r[k].y);
+        } else {
+            top_m = fmaxf(top_m, fmaxf(fabsf(m[k].x), fabsf(m[k].y)));
+            top_r = fmaxf(top_r, fmaxf(r[k].x, r[k].y));
+        }
     }
     if (e.master != nullptr) store8<float>(e.master, i, n, p);
     store8<PT>(param, i, n, p);
     if constexpr (E4M3) {
         top_m = warp_max(top_m);
         top_r = warp_max(top_r);
+        // An infinity has no code (it becomes NaN) and is no scale for its block.  (Asked for each value to nearest: 1103 us
+        // instead of 1090; this branch in the stochastic kernel, which lacks the registers: 1351 instead of 1234.)
+        if (STATE == NEAREST && __builtin_expect(!(fmaxf(top_m, top_r) <= 3.40282347e38f), 0)) {
+            top_m = top_r = 0.f;
+#pragma unroll
+            for (int k = 0; k < PAIRS; k++) {
+                top_m = largest_finite(top_m, fabsf(m[k].x), fabsf(m[k].y));
+                top_r = largest_finite(top_r, r[k].x, r[k].y);
+            }
+            top_m = warp_max(top_m);
+            top_r = warp_max(top_r);
+        }
         const float sm = top_m * (1.f / E4M3_MAX), sr = top_r * (1.f / E4M3_MAX);
         // a block of magnitudes below 448e-36 keeps the codes of zeros (its reciprocal would leave the normal range)
         const float ym = sm >= 1e-36f ? 1.f / sm : 0.f, yr = sr >= 1e-36f ? 1.f / sr : 0.f;
@@ -366,8 +392,8 @@ __global__ void __launch_bounds__(THREADS, 12) adamw_kernel(const __grid_constan
         }
 #pragma unroll
         for (int k = 0; k < PAIRS; k++) {
-            v[k].x = r[k].x > 0.f ? fmaxf(v[k].x, E4M3_TINY) : v[k].x;  // keeps NaN
-            v[k].y = r[k].y > 0.f ? fmaxf(v[k].y, E4M3_TINY) : v[k].y;
+            v[k].x = r[k].x > 0.f ? raised(v[k].x) : v[k].x;
+            v[k].y = r[k].y > 0.f ? raised(v[k].y) : v[k].y;
         }
         store_codes(e.m, i, n, encode8(m));
         store_codes(e.v, i, n, encode8(v));
@@ -466,7 +492,7 @@ cudaError_t launch_adamw(const csa_adamw_params &p, const csa_adamw_tensor *t, i
     h.log_b2 = (float)log(p.beta2);
     h.lr_dev = p.lr_dev;
     h.step_dev = p.step_dev;
-    h.seed = p.seed;
+    h.seed = mixed(mixed((uint32_t)p.seed + 0x68e31da4u) + (uint32_t)(p.seed >> 32));
     h.step = p.step;
     h.grad_scale = p.grad_scale;
     h.found_inf = p.found_inf;

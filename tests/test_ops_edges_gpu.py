@@ -259,3 +259,32 @@ def test_adamw_8_bit_to_nearest_says_what_it_cannot_follow():
     t = B.AdamWTensors(w, grad, **s)
     with pytest.warns(UserWarning, match="beta2"):
         B.csa_adamw(t, 1)
+
+
+@pytest.mark.parametrize("seed", [None, 1])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), 3e30, float("nan")])
+def test_adamw_8_bit_infinite_moment_stays_in_its_element(bad, seed):
+    """A gradient that is infinite, or whose square is: the other elements and their codes are those without it."""
+    g = gen(12)
+    w0, grad = randn(g, 700), randn(g, 700)
+    grad[300] = 0.0
+    sides = []
+    for value in (0.0, bad):
+        w, gr = [w0.clone()], [grad.clone()]
+        gr[0][300] = value
+        s = B.AdamWTensors.zero_state(w, True)
+        s["seed"] = seed
+        t = B.AdamWTensors(w, gr, **s)
+        for k in (1, 2):
+            B.csa_adamw(t, k, beta2=0.8)
+        sides.append((w[0], *held(t)))
+    other = torch.arange(700, device="cuda") != 300
+    outside = other.clone()
+    outside[256:512] = False
+    for name, a, b in zip(("param", "m", "v"), *sides):
+        # 3e30 is finite: its m takes its block's scale, and the block's other m their codes; v is infinite as before
+        keep = outside if bad == 3e30 and name != "v" else other
+        assert torch.equal(a[keep], b[keep]), name
+    assert bool(sides[1][2][300].isnan())
+    if bad != 3e30:
+        assert bool(sides[1][1][300].isnan()) and bool(sides[1][0][300].isnan())
