@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(THREADS, 12) adamw_kernel(const __grid_constan
 #pragma unroll
                 for (int k = 0; k < PAIRS; k++) {
                     // elements 2^31 apart share their word; a pair's second word is the first one mixed on
-                    const uint32_t w0 = mixed(key + (uint32_t)(i + 2 * k));
+                    const uint32_t w0 = mixed(key + 2u * (uint32_t)(i + 2 * k));
                     uint32_t w1 = w0 * 0x85ebca77u;
                     w1 ^= w1 >> 15;
                     m[k] = stochastic<decltype(all)::value>(m[k], w0, w1);
