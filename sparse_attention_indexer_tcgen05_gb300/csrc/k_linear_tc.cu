@@ -7,9 +7,11 @@
 // 2^-23 of the terms.
 //
 // The tensor core cuts a sum off where it aligns it with a product (it does not round), so a TMEM accumulator loses about
-// 2^-24 / 3 of itself with every 16 k, always towards zero: 5e-6 at k = 8192.  That is nothing beside a bf16 result.  For
-// fp32 results (EXACT below) the accumulator starts anew every 64 k (three planes: the small terms then meet a small
-// sum; 2e-7 off at k = 65536) or every 512 k (5e-7), and the epilogue's warps add up the pieces in registers, rounded.
+// 2^-24 / 3 of itself with every 16 k, always towards zero: 5e-6 at k = 8192.  That is nothing beside a bf16 result up to
+// LONGEST k (8e-5, a fiftieth of the largest rounding); longer axes are cut into pieces, joined in fp32 (dW of 2^20 rows
+// would be 1.3e-3 too small).  For fp32 results (EXACT below) the accumulator starts anew every 64 k (three planes: the
+// small terms then meet a small sum; 2e-7 off at k = 65536) or every 512 k (5e-7), and the epilogue's warps add up the
+// pieces in registers, rounded.
 //
 // Mapping.  A unit is one output tile and one piece of the k axis.  A CTA pair (two SMs) computes 256 x BN: each CTA
 // loads its 128 rows of A and its BN / 2 rows of B, so an operand byte brought to an SM feeds twice the MMAs of a lone
@@ -51,6 +53,8 @@ using namespace ptx;
 
 constexpr int BM = 128;        // rows of one CTA's accumulator
 constexpr int BK = 64;         // k per stage: one 128-byte swizzle row
+constexpr long long LONGEST = 65536;  // k that a bf16 result sums in one accumulator
+constexpr int CHUNK_1 = 8;     // stages (512 k) that an fp32 result of one plane does
 constexpr int MANY_STEPS = 4;  // stages of a unit up to which 256-wide tiles have 16 epilogue warps
 
 // P planes, EW epilogue warps
@@ -346,7 +350,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
 {
     using Z = Cfg<CG, BN, P, EW>;
     constexpr int S = Z::STAGES;
-    constexpr int CHUNK = !EXACT ? 0x40000000 : P == 3 ? 1 : 8;
+    constexpr int CHUNK = !EXACT ? 0x40000000 : P == 3 ? 1 : CHUNK_1;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = smem_align1024(smem_raw);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Z::MISC);
@@ -615,12 +619,14 @@ static void tile_counts(Shape s, long long M, long long N, int &mt, int &nt)
 //   a round is no shorter than its epilogue: 0.9, 1.7 and 2.9 (1.8 with 16 warps);
 //   launch, first loads and last epilogue: 3.8, 5.2 and 6.3;
 //   a cut k axis: another launch, 2.5, and the pieces' way to memory and back at 4 TB/s.
+// A bf16 result's axis is cut into pieces of LONGEST at most, whatever that takes.
 // Units run in rounds of one per SM or pair.
 Plan plan_product(long long M, long long N, long long K, int planes, bool out_f32, int sms)
 {
     const long long steps = (K + BK - 1) / BK;
     // the registers hold half a row of 128 columns, not of 256
-    Plan best = {PAIR_128, 1, planes == 3 || (out_f32 && K > 1024)};
+    Plan best = {PAIR_128, 1, planes == 3 || (out_f32 && steps > CHUNK_1)};
+    const long long least_cut = best.exact ? 1 : (K + LONGEST - 1) / LONGEST;
     double least = 1e300;
     for (int s = LONE_64; s <= (best.exact ? PAIR_128 : PAIR_256); s++) {
         const Shape shape = (Shape)s;
@@ -630,7 +636,7 @@ Plan plan_product(long long M, long long N, long long K, int planes, bool out_f3
         const long long slots = shape == LONE_64 ? sms : sms / 2;
         constexpr double STEP[2][3] = {{0.20, 0.20, 0.28}, {0.72, 0.90, 0.0}}, FIXED[3] = {3.8, 5.2, 6.3}, EPILOGUE[3] = {0.9, 1.7, 2.9};
         const double step = STEP[planes == 3][s];
-        for (long long cut = 1; cut <= steps && cut <= 64 && (cut == 1 || tiles * cut <= slots); cut++) {
+        for (long long cut = least_cut; cut <= steps && (cut == least_cut || (cut <= 64 && tiles * cut <= slots)); cut++) {
             const long long per = (steps + cut - 1) / cut, pieces = (steps + per - 1) / per;
             double rounds = floor(tiles * pieces / slots), rest = tiles * pieces - rounds * slots;
             if (rest > 0) rounds += shape == PAIR_256 && pieces == 1 && per > MANY_STEPS && rounds > 0 && 2 * rest <= slots ? 0.5 : 1.0;

@@ -288,3 +288,40 @@ def test_adamw_8_bit_infinite_moment_stays_in_its_element(bad, seed):
     assert bool(sides[1][2][300].isnan())
     if bad != 3e30:
         assert bool(sides[1][1][300].isnan()) and bool(sides[1][0][300].isnan())
+
+
+# ------------------------------------------------------------------ projections: long sums, infinities
+
+def test_linear_bf16_gradients_of_a_million_rows():
+    """Sums of 2^20 positive terms in as many tiles as the GPU runs at once, none of them too small.  What the tensor core
+    cuts off is below 2^-24 of the sum for each 16 k of 65536 at most: 2.4e-4; roundings to bf16 (2^-8 at most, 1.2e-3
+    rms) go either way, six times their mean over 1536 outputs is 1.8e-4."""
+    M, K, N = 1 << 20, 2048, 2048
+    g = gen(20)
+    x = torch.rand(M, K, generator=g, device="cuda", dtype=BF)
+    dy = torch.rand(M, N, generator=g, device="cuda", dtype=BF)
+    x[:, :48] *= 1 + torch.arange(48, device="cuda", dtype=BF) / 48          # sums of every place between two bf16 values
+    p = B.LinearParams(M, K, N)
+    dw = B.csa_linear_bwd(p, dy, x, None, need_dx=False, need_db=False)[1][:32, :48].double()
+    want = torch.zeros(32, 48, device="cuda", dtype=torch.float64)
+    for i in range(0, M, 1 << 16):
+        want += dy[i:i + (1 << 16), :32].double().t() @ x[i:i + (1 << 16), :48].double()
+    off = dw / want - 1
+    assert float(off.abs().max()) <= 2.0 ** -8 * (1 + 2.0 ** -8) + 4096 * 2.0 ** -24
+    assert abs(float(off.mean())) <= 4.2e-4
+
+
+@pytest.mark.parametrize("M,K,N", [(200, 70000, 4096), (8, 131080, 24), (300, 65544, 264)])
+def test_linear_axes_longer_than_one_accumulator(M, K, N):
+    """Cut axes forward and in dx (where the features are summed), with the epilogue behind the join."""
+    g = gen(21)
+    x, w, b, res = randn(g, M, K, dtype=BF), randn(g, N, K, dtype=BF, scale=K ** -0.5), randn(g, N), randn(g, M, N, dtype=BF)
+    y = B.csa_linear_fwd(B.LinearParams(M, K, N, activation="relu"), x, w, b, res)
+    z = (x.float() @ w.float().t()).double() + b.double()
+    want = z.clamp(min=0) + res.double()
+    terms = x.double().norm() * w.double().norm() / (M * N) ** 0.5
+    assert float((y.double() - want).norm() / want.norm()) <= 2.0 ** -8
+    assert float((y.double() - want).abs().max()) <= 2.0 ** -8 * float(want.abs().max()) + 2.0 ** -12 * float(terms) * 6
+    dx = B.csa_linear_bwd(B.LinearParams(M, N, K), x, None, w.t().contiguous().view(K, N), need_dw=False, need_db=False)[0]
+    want = x.double() @ w.double().t()
+    assert float((dx.double() - want).norm() / want.norm()) <= 2.0 ** -8
