@@ -7,10 +7,11 @@
 // 2^-23 of the terms.
 //
 // The tensor core cuts a sum off where it aligns it with a product (it does not round), so a TMEM accumulator loses about
-// 2^-24 / 3 of itself with every 16 k, always towards zero: 5e-6 at k = 8192.  That is nothing beside a bf16 result up to
-// LONGEST k (8e-5, a fiftieth of the largest rounding); longer axes are cut into pieces, joined in fp32 (dW of 2^20 rows
-// would be 1.3e-3 too small).  For fp32 results (EXACT below) the accumulator starts anew every 64 k (three planes: the
-// small terms then meet a small sum; 2e-7 off at k = 65536) or every 512 k (5e-7), and the epilogue's warps add up the
+// 2^-24 / 3 of itself with every 16 k, always towards zero, and, once it is large beside the products, which are cut off too,
+// four times that: 7e-7 at k = 512, 3e-4 at k = 65536 (positive terms).  That is little beside a bf16 result up to LONGEST k
+// (a thirteenth of the largest rounding); longer axes are cut into pieces, joined in fp32 (dW of 2^20 rows came out 6e-3 too
+// small in one).  For fp32 results (EXACT below) the accumulator starts anew every 64 k (three planes: the
+// small terms then meet a small sum; 9e-8 to 1.5e-7 off, k = 64 to 65536) or every 512 k (4e-7 to 7e-7), and the epilogue's warps add up the
 // pieces in registers, rounded.
 //
 // Mapping.  A unit is one output tile and one piece of the k axis.  A CTA pair (two SMs) computes 256 x BN: each CTA
