@@ -20,9 +20,22 @@ __device__ __forceinline__ void split3(float x, bf16 &h, bf16 &m, bf16 &l)
     l = __float2bfloat16_rn(fine ? r - __bfloat162float(m) : 0.f);
 }
 
+// x = h + m to 2^-16.  h is cut off and m never 0 unless x is, so that both have x's sign: an infinite factor then gives an
+// infinity of that sign, not NaN.
+__device__ __forceinline__ void split2(float x, bf16 &h, bf16 &m)
+{
+    h = __ushort_as_bfloat16((unsigned short)(__float_as_uint(x) >> 16));
+    const float top = __bfloat162float(h), r = x - top;
+    m = __float2bfloat16_rn(r != 0.f && fabsf(x) < INFINITY ? r : top * 5.9604644775390625e-8f);
+}
+
+// What holds a staged operand of values V
 template <typename V> struct Planes;
 template <> struct Planes<bf16> { static constexpr int N = 1; };
 template <> struct Planes<float> { static constexpr int N = 3; };
+// and dz, of values V and gradients O.  fp32 gradients of bf16 values keep 16 bits of it, for twice the MMAs; bf16 ones
+// come with 8 bits, and dz has no more.
+template <typename V, typename O> struct DzPlanes { static constexpr int N = sizeof(V) == 4 ? 3 : sizeof(O) == 4 ? 2 : 1; };
 
 // What a staged operand is made of: rows x cols values, rows `stride` apart -> planes of rows `ld` apart.
 struct Stage {
@@ -86,14 +99,16 @@ template <typename T, bool ALIGNED> __device__ __forceinline__ void load8(const 
 
 // 8 neighbouring values to the planes
 
-template <typename V> __device__ __forceinline__ void put_planes8(bf16 *out, long long plane, long long at, const float (&x)[8])
+template <int P> __device__ __forceinline__ void put_planes8(bf16 *out, long long plane, long long at, const float (&x)[8])
 {
-    constexpr int P = Planes<V>::N;
     __nv_bfloat162 w[P][4];
 #pragma unroll
     for (int k = 0; k < 4; k++) {
         if constexpr (P == 1) {
             w[0][k] = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+        } else if constexpr (P == 2) {
+            split2(x[2 * k], w[0][k].x, w[1][k].x);
+            split2(x[2 * k + 1], w[0][k].y, w[1][k].y);
         } else {
             split3(x[2 * k], w[0][k].x, w[1][k].x, w[2][k].x);
             split3(x[2 * k + 1], w[0][k].y, w[1][k].y, w[2][k].y);
@@ -116,7 +131,7 @@ template <typename V> __device__ __forceinline__ void stage_block(const Stage &s
     float v[8];
     if (s.aligned && c + 8 <= s.cols) load8<V, true>(x, 8, end, v);
     else load8<V, false>(x, min(8, s.cols - c), end, v);
-    put_planes8<V>(s.out, s.plane, r * s.ld + c, v);
+    put_planes8<Planes<V>::N>(s.out, s.plane, r * s.ld + c, v);
 }
 
 template <typename V> __global__ void __launch_bounds__(256) stage_kernel(const Stage s0, const Stage s1)
@@ -174,7 +189,7 @@ dz_kernel(const O *dy, long long ldy, const V *z, int act, bf16 *dz, long long l
             }
 #pragma unroll
             for (int j = 0; j < 8; j++) s[j] += d[j];
-            if (dz != nullptr) put_planes8<V>(dz, plane, r * ld + n, d);  // up to 7 values of padding
+            if (dz != nullptr) put_planes8<DzPlanes<V, O>::N>(dz, plane, r * ld + n, d);  // up to 7 values of padding
         }
     }
     if (sums == nullptr) return;
@@ -287,6 +302,7 @@ inline size_t staged_bytes(int dtype, long long rows, long long cols)
 constexpr int kSms = 152;  // the split of a k axis is chosen for the whole GPU, the same on every call
 
 inline int planes_of(const csa_linear_params &p) { return p.dtype == CSA_F32 ? 3 : 1; }
+inline int dz_passes(const csa_linear_params &p) { return p.dtype == CSA_BF16 && p.out_dtype == CSA_F32 ? 2 : 1; }
 
 struct Fwd {
     bool stage_x, stage_w;
@@ -305,7 +321,7 @@ Fwd plan_fwd(const csa_linear_params &p)
     if (f.stage_x) at += staged_bytes(p.dtype, M, K);
     f.off_w = at;
     if (f.stage_w) at += staged_bytes(p.dtype, N, K);
-    f.plan = plan_product(M, N, K, planes_of(p), p.out_dtype == CSA_F32, kSms);
+    f.plan = plan_product(M, N, K, planes_of(p), 1, p.out_dtype == CSA_F32, kSms);
     f.off_part = at;
     if (f.plan.splits > 1) at += up256((size_t)f.plan.splits * M * partial_stride(N) * 4);
     f.total = at;
@@ -340,12 +356,12 @@ Bwd plan_bwd(const csa_linear_params &p)
     b.off_w = at;
     if (b.stage_w) at += staged_bytes(p.dtype, N, K);
     b.off_dz = at;
-    if (b.stage_dz) at += staged_bytes(p.dtype, M, N);
+    if (b.stage_dz) at += staged_bytes(p.dtype, M, N) * dz_passes(p);
     b.off_sums = at;
     at += up256((size_t)b.blocks * N * 4);
     b.off_part = at;
-    b.dx = plan_product(M, K, N, planes_of(p), p.dtype == CSA_F32, kSms);
-    b.dw = plan_product(N, K, M, planes_of(p), p.dtype == CSA_F32, kSms);
+    b.dx = plan_product(M, K, N, planes_of(p), dz_passes(p), p.dtype == CSA_F32, kSms);
+    b.dw = plan_product(N, K, M, planes_of(p), dz_passes(p), p.dtype == CSA_F32, kSms);
     const size_t dx = b.dx.splits > 1 ? (size_t)b.dx.splits * M * partial_stride(K) * 4 : 0;
     const size_t dw = b.dw.splits > 1 ? (size_t)b.dw.splits * N * partial_stride(K) * 4 : 0;
     at += up256(dx > dw ? dx : dw);  // one product after the other
@@ -461,6 +477,7 @@ cudaError_t launch_linear_fwd(const csa_linear_params &p, const void *x, const v
     q.N = p.out_features;
     q.K = p.in_features;
     q.planes = planes_of(p);
+    q.passes = 1;
     q.plan = f.plan;
     q.e.partial = reinterpret_cast<float *>(w + f.off_part);
     return product(q, st);
@@ -504,6 +521,7 @@ cudaError_t launch_linear_bwd(const csa_linear_params &p, const void *dy, const 
     d.plane = dz != nullptr ? M * up8(N) : 0;
     Product q = {};
     q.planes = planes_of(p);
+    q.passes = dz_passes(p);
     q.e.alpha = p.alpha;
     q.e.out_f32 = p.dtype == CSA_F32;
     q.e.partial = reinterpret_cast<float *>(w + b.off_part);

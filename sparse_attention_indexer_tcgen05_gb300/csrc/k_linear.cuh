@@ -146,13 +146,14 @@ struct Plan {
     bool exact;   // sums kept in registers (see k_linear_tc.cu)
 };
 // out_f32: the result itself is fp32 (and not only its pieces)
-Plan plan_product(long long M, long long N, long long K, int planes, bool out_f32, int sms);
+Plan plan_product(long long M, long long N, long long K, int planes, int passes, bool out_f32, int sms);
 
-// D[m][n] = sum_k A(m, k) B(n, k), M x N x K, with `planes` = 1 or 3.
+// D[m][n] = sum_k A(m, k) B(n, k), M x N x K, with `planes` = 1 or 3.  One plane, two passes: A is the sum of two planes, and
+// each stage of the k axis takes the second one and B, then the first one and B.
 struct Product {
     Operand a, b;
     long long M, N, K;
-    int planes;
+    int planes, passes;
     Plan plan;
     Epilogue e;
 };

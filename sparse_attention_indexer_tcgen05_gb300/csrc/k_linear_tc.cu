@@ -73,7 +73,7 @@ template <int CG, int BN, int P, int EW> struct Cfg {
 
 struct Args {
     long long M, N, ldo;        // the output's row stride
-    int ksteps;                 // stages over the whole k axis
+    int ksteps;                 // stages over the whole k axis, all passes
     int splits, per_split;      // k pieces, stages of each
     int mt, nt;                 // tiles
     int whole, units;           // units that are whole tiles (times splits); the rest are halves of the last tiles
@@ -343,8 +343,9 @@ __device__ __forceinline__ void to_activation(const Args &a, float (&v)[C], long
     else if (e.act == CSA_ACT_GELU_TANH) activate<CSA_ACT_GELU_TANH>(v);
 }
 
-// EXACT: the sums are kept in the epilogue's registers, pieces of CHUNK stages of the k axis in TMEM.
-template <int CG, int BN, int P, int EW, bool EXACT, bool A_K, bool B_K>
+// EXACT: the sums are kept in the epilogue's registers, pieces of CHUNK stages of the k axis in TMEM.  TWO: two passes, whose
+// stages take turns (B's second one comes from L2).  (As an argument instead, it cost a product of 37 rows 0.7 us of 11.6.)
+template <int CG, int BN, int P, int EW, bool EXACT, bool A_K, bool B_K, bool TWO>
 __global__ void __launch_bounds__(64 + 32 * EW, 1)
 linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                  const __grid_constant__ CUtensorMap map_half, const __grid_constant__ CUtensorMap map_out, const Args a)
@@ -418,19 +419,21 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                 const int ctas_a = CG == 2 && (x.m * 2 + 1LL) * BM < a.M ? 2 : 1;
                 const uint32_t bytes = P * (ctas_a * a.rows_a + CG * rows_b) * BK * 2;
                 const CUtensorMap *mb = half ? &map_half : &map_b;
-                for (int k = x.it0 * BK; k < x.it1 * BK; k += BK) {
+                for (int it = x.it0; it < x.it1; it++) {
+                    const int k = (TWO ? it >> 1 : it) * BK, plane_a = TWO ? ~it & 1 : 0;
                     wait_bar(empty + st, ph ^ 1, abort_flag, &g_lin_error, 601);
                     if (rank == 0) mbar_expect_tx(full + st, bytes);
 #pragma unroll
                     for (int q = 0; q < P; q++) {
                         unsigned char *sa = smem + st * Z::STAGE + q * Z::A_BYTES, *sb = smem + st * Z::STAGE + P * Z::A_BYTES + q * Z::B_BYTES;
+                        const int qa = P == 1 ? plane_a : q;
                         if (!with_a) {
                         } else if constexpr (A_K) {
-                            load3(sa, &map_a, st, k, am, q);
+                            load3(sa, &map_a, st, k, am, qa);
                         } else if (a.blocks_a) {
-                            load4(sa, &map_a, st, 0, k, am >> 6, q);
+                            load4(sa, &map_a, st, 0, k, am >> 6, qa);
                         } else {
-                            for (int i = 0; i < a.rows_a; i += 64) load3(sa + i * 128, &map_a, st, am + i, k, q);
+                            for (int i = 0; i < a.rows_a; i += 64) load3(sa + i * 128, &map_a, st, am + i, k, qa);
                         }
                         if constexpr (B_K) {
                             load3(sb, mb, st, k, bn, q);
@@ -622,12 +625,12 @@ static void tile_counts(Shape s, long long M, long long N, int &mt, int &nt)
 //   a cut k axis: another launch, 2.5, and the pieces' way to memory and back at 4 TB/s.
 // A bf16 result's axis is cut into pieces of LONGEST at most, whatever that takes.
 // Units run in rounds of one per SM or pair.
-Plan plan_product(long long M, long long N, long long K, int planes, bool out_f32, int sms)
+Plan plan_product(long long M, long long N, long long K, int planes, int passes, bool out_f32, int sms)
 {
-    const long long steps = (K + BK - 1) / BK;
+    const long long steps = (K + BK - 1) / BK * passes;
     // the registers hold half a row of 128 columns, not of 256
     Plan best = {PAIR_128, 1, planes == 3 || (out_f32 && steps > CHUNK_1)};
-    const long long least_cut = best.exact ? 1 : (K + LONGEST - 1) / LONGEST;
+    const long long least_cut = best.exact ? 1 : (steps * BK + LONGEST - 1) / LONGEST;
     double least = 1e300;
     for (int s = LONE_64; s <= (best.exact ? PAIR_128 : PAIR_256); s++) {
         const Shape shape = (Shape)s;
@@ -658,11 +661,11 @@ struct Maps {
     CUtensorMap a, b, half, out;
 };
 
-template <int CG, int BN, int P, int EW, bool EXACT, bool A_K, bool B_K>
+template <int CG, int BN, int P, int EW, bool EXACT, bool A_K, bool B_K, bool TWO = false>
 static cudaError_t launch(const Maps &m, const Args &a, int sms, cudaStream_t st)
 {
     using Z = Cfg<CG, BN, P, EW>;
-    auto *kernel = linear_tc_kernel<CG, BN, P, EW, EXACT, A_K, B_K>;
+    auto *kernel = linear_tc_kernel<CG, BN, P, EW, EXACT, A_K, B_K, TWO>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::SMEM);
     if (e != cudaSuccess) return e;
     const int slots = sms / CG;
@@ -673,6 +676,10 @@ template <int CG, int BN, int P, int EW, bool EXACT>
 static cudaError_t launch_majors(const Product &p, const Maps &m, const Args &a, int sms, cudaStream_t st)
 {
     if (p.a.k_major && p.b.k_major) return launch<CG, BN, P, EW, EXACT, true, true>(m, a, sms, st);
+    if constexpr (P == 1 && !EXACT) {
+        if (p.passes == 2 && p.a.k_major) return launch<CG, BN, P, EW, EXACT, true, false, true>(m, a, sms, st);
+        if (p.passes == 2) return launch<CG, BN, P, EW, EXACT, false, false, true>(m, a, sms, st);
+    }
     if constexpr (P == 3 || !EXACT) {  // gradients have their operands' type
         if (p.a.k_major) return launch<CG, BN, P, EW, EXACT, true, false>(m, a, sms, st);
         return launch<CG, BN, P, EW, EXACT, false, false>(m, a, sms, st);
@@ -726,7 +733,7 @@ cudaError_t launch_product_tc(const Product &p, int sms, cudaStream_t st)
     Args a = {};
     a.M = p.M;
     a.N = p.N;
-    a.ksteps = (int)((p.K + BK - 1) / BK);
+    a.ksteps = (int)((p.K + BK - 1) / BK * p.passes);
     a.per_split = (a.ksteps + splits - 1) / splits;
     a.splits = splits;
     tile_counts(s, p.M, p.N, a.mt, a.nt);
@@ -758,7 +765,7 @@ cudaError_t launch_product_tc(const Product &p, int sms, cudaStream_t st)
     a.rows_a = p.M >= BM ? BM : p.a.k_major ? (int)((p.M + 7) & ~7LL) : p.M > 64 ? 128 : 64;
     Maps m = {};
     const int rows_b = s == PAIR_256 ? 128 : 64;
-    bool ok = encode(&m.a, p.a, p.M, p.K, p.planes, a.rows_a, a.blocks_a) && encode(&m.b, p.b, p.N, p.K, p.planes, rows_b, a.blocks_b);
+    bool ok = encode(&m.a, p.a, p.M, p.K, p.planes * p.passes, a.rows_a, a.blocks_a) && encode(&m.b, p.b, p.N, p.K, p.planes, rows_b, a.blocks_b);
     if (a.units > a.whole) ok = ok && encode(&m.half, p.b, p.N, p.K, p.planes, rows_b / 2, a.blocks_b);
     if (a.tma_out) ok = ok && encode_out(&m.out, a.e.out_f32, a.e.out, p.N, a.ldo, p.M, splits);
     if (!ok) return cudaErrorInvalidValue;

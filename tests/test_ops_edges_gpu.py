@@ -326,3 +326,50 @@ def test_linear_axes_longer_than_one_accumulator(M, K, N):
     dx = B.csa_linear_bwd(B.LinearParams(M, N, K), x, None, w.t().contiguous().view(K, N), need_dw=False, need_db=False)[0]
     want = x.double() @ w.double().t()
     assert float((dx.double() - want).norm() / want.norm()) <= 2.0 ** -8
+
+
+@pytest.mark.parametrize("M,K,N", [(64, 40, 128), (2048, 512, 1024), (1002, 33, 70), (16384, 256, 64)])
+def test_linear_fp32_gradients_of_bf16_values_keep_their_bits(M, K, N):
+    """dy of 1 + 2^-10 and -1 in turn along rows and columns: what is left of its sums is what bf16 would drop."""
+    p = B.LinearParams(M, K, N, "bf16", "f32")
+    sign = (torch.arange(M, device="cuda")[:, None] + torch.arange(N, device="cuda")) % 2
+    dy = torch.where(sign == 0, 1 + 2.0 ** -10, -1.0)
+    x, w = torch.ones(M, K, dtype=BF, device="cuda"), torch.ones(N, K, dtype=BF, device="cuda")
+    dx, dw, db = B.csa_linear_bwd(p, dy, x, w)
+    # every partial sum is a multiple of 2^-10 below 2^14: exact but for the one rounding
+    assert torch.equal(dx, torch.full((M, K), N / 2 * 2.0 ** -10, device="cuda").to(BF))
+    assert torch.equal(dw, torch.full((N, K), M / 2 * 2.0 ** -10, device="cuda").to(BF))
+    assert torch.equal(db, torch.full((N,), M / 2 * 2.0 ** -10, device="cuda"))
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_linear_fp32_gradients_are_rounded_once(act):
+    """With fp32 dy the bf16 gradients are as near the formula as its own rounding to bf16; dz's 2^-16, the activation's
+    2^-19 and what the tensor core cuts off (below 2^-16 at these lengths) are beside that nothing: 1 % and 2^-15."""
+    M, K, N = 3000, 264, 520
+    g = gen(22)
+    p = B.LinearParams(M, K, N, "bf16", "f32", act)
+    x, w, z, dy = randn(g, M, K, dtype=BF), randn(g, N, K, dtype=BF), randn(g, M, N, dtype=BF), randn(g, M, N)
+    dx, dw, _ = B.csa_linear_bwd(p, dy, x, w, z if act != "none" else None)
+    d = dy.double()
+    if act == "silu":
+        s = torch.sigmoid(z.double())
+        d = d * s * (1 + z.double() * (1 - s))
+    for got, want in ((dx, d @ w.double()), (dw, d.t() @ x.double())):
+        best = float((want.to(BF).double() - want).norm())
+        assert float((got.double() - want).norm()) <= 1.01 * best + 2.0 ** -15 * float(want.norm())
+
+
+def test_linear_infinite_factors_of_fp32_gradients():
+    """An infinite weight or x beside an fp32 dy: the infinity of the product's sign, as in a plain product."""
+    g = gen(23)
+    M, K, N = 40, 24, 16
+    p = B.LinearParams(M, K, N, "bf16", "f32")
+    x, w, dy = randn(g, M, K, dtype=BF), randn(g, N, K, dtype=BF), randn(g, M, N)
+    dy[:, 3] = torch.where(torch.arange(M, device="cuda") % 2 == 0, 1.0, -0.75)    # exact in bf16
+    w[3, 5], x[7, 2] = float("inf"), float("-inf")
+    dx, dw, _ = B.csa_linear_bwd(p, dy, x, w)
+    assert torch.equal(dx[:, 5].float(), torch.where(dy[:, 3] > 0, float("inf"), float("-inf")))
+    assert torch.equal(dw[:, 2].float(), torch.where(dy[7] > 0, float("-inf"), float("inf")))
+    keep = [k for k in range(K) if k not in (2, 5)]
+    assert bool(dx[:, keep].isfinite().all()) and bool(dw[:, keep].isfinite().all())
