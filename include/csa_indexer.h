@@ -262,9 +262,10 @@ size_t csa_linear_bwd_workspace_size(const csa_linear_params *p);
  * Sums and the epilogue are fp32, rounded once.  The tensor core cuts sums and products off at the sum's last place,
  * towards zero (measured: 7e-7 of a sum of 512 positive terms, 3e-4 of one of 65536).  A sum there starts anew every 65536 k
  * for a bf16 result, every 512 k for an fp32 result of bf16 values and every 64 k for fp32 values, and the pieces are added
- * in fp32.  fp32 values are multiplied as three bf16 parts each (six products, about 2^-23 relative to the terms); an infinite fp32 value gives its row NaN or
- * an infinity.  y may be the residual itself when their row strides agree;
- * an output given as another argument is refused otherwise.  rows and features up to 2^31 - 2^16. */
+ * in fp32.  fp32 values are multiplied as three bf16 parts each (six products, about 2^-23 relative to the terms).
+ * Infinities and NaN give what plain products give.
+ * y may be the residual itself when their row strides agree; an output given as another argument is refused otherwise.
+ * rows and features up to 2^31 - 2^16. */
 csa_status csa_linear_fwd(const csa_linear_params *p, const void *x, const void *weight, const float *bias,
                           const void *residual, void *y, void *preact, void *workspace, size_t workspace_bytes,
                           void *stream);

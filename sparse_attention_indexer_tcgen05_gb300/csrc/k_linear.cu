@@ -8,8 +8,10 @@ namespace linear {
 
 using bf16 = __nv_bfloat16;
 
-// x = h + m + l with bf16 parts: 8 bits of the significand each.  Infinities and NaN stay in h; a finite x that would
-// round to an infinity is cut off instead.
+// x = h + m + l with bf16 parts: 8 bits of the significand each.  NaN stays in h; a finite x that would round to an infinity
+// is cut off instead.  An infinity goes to l, which meets the other factor's h alone, and h is 1 of its sign: the product is
+// then an infinity of the right sign for every other factor that is not 0, infinite ones too (whose l meets this h).  In h it
+// would meet the other's m and l, which may be 0 or of the other sign.
 __device__ __forceinline__ void split3(float x, bf16 &h, bf16 &m, bf16 &l)
 {
     h = __float2bfloat16_rn(x);
@@ -18,6 +20,10 @@ __device__ __forceinline__ void split3(float x, bf16 &h, bf16 &m, bf16 &l)
     const bool fine = fabsf(r) <= 3.0e38f;  // false for NaN and infinities
     m = __float2bfloat16_rn(fine ? r : 0.f);
     l = __float2bfloat16_rn(fine ? r - __bfloat162float(m) : 0.f);
+    if (fabsf(x) == INFINITY) {
+        l = h;
+        h = __float2bfloat16_rn(copysignf(1.f, x));
+    }
 }
 
 // x = h + m to 2^-16.  h is cut off and m never 0 unless x is, so that both have x's sign: an infinite factor then gives an

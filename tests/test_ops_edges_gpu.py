@@ -12,6 +12,7 @@ if torch.cuda.is_available():
     from sparse_attention_indexer_tcgen05_gb300 import binding as B  # noqa: E402
 
 BF, F32 = torch.bfloat16, torch.float32
+DT = {"bf16": BF, "f32": F32}
 U = {BF: 2.0 ** -8, F32: 2.0 ** -24}
 
 
@@ -373,3 +374,37 @@ def test_linear_infinite_factors_of_fp32_gradients():
     assert torch.equal(dw[:, 2].float(), torch.where(dy[7] > 0, float("-inf"), float("inf")))
     keep = [k for k in range(K) if k not in (2, 5)]
     assert bool(dx[:, keep].isfinite().all()) and bool(dw[:, keep].isfinite().all())
+
+
+def same_kinds(got, want, what):
+    """The same NaN, and infinities of the same sign, in the same places."""
+    got, want = got.double(), want.double()
+    assert torch.equal(got.isnan(), want.isnan()), what
+    assert torch.equal(got.isinf(), want.isinf()), what
+    at = want.isinf()
+    assert torch.equal(got[at], want[at]), what
+
+
+@pytest.mark.parametrize("dtype,out", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("M", [1, 8, 9, 16, 40, 300])
+def test_linear_infinities_are_those_of_plain_products(M, dtype, out):
+    """Infinite values beside factors of either sign, 0 and infinite ones: the same answers whatever the number of rows."""
+    K, N = 72, 40
+    inf, t = float("inf"), DT[dtype]
+    g = gen(30)
+    x, w, dy = randn(g, M, K, dtype=t), randn(g, N, K, dtype=t), randn(g, M, N, dtype=DT[out])
+    x[0, 3] = inf
+    w[2, 3], w[5, 3], w[6, 3] = 0.0, inf, -inf
+    if M > 1:
+        x[M - 1, 70], x[M // 2, 9], x[M // 2, 11] = -inf, inf, -inf
+        w[7, 9] = 0.0
+        dy[1, 4], dy[M - 1, 4] = -inf, inf
+        dy[1, 30] = float("nan")
+    w[8, 1] = -inf
+    x[0, 1] = 1.0 + 2.0 ** -7                                # its second part is 0
+    y = B.csa_linear_fwd(B.LinearParams(M, K, N, dtype, out), x, w)
+    same_kinds(y, x.double() @ w.double().t(), "y")
+    dx, dw, db = B.csa_linear_bwd(B.LinearParams(M, K, N, dtype, out), dy, x, w)
+    same_kinds(dx, dy.double() @ w.double(), "dx")
+    same_kinds(dw, dy.double().t() @ x.double(), "dw")
+    same_kinds(db, dy.double().sum(0), "db")
