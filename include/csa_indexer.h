@@ -273,7 +273,7 @@ csa_status csa_linear_fwd(const csa_linear_params *p, const void *x, const void 
 /* The gradients of csa_linear_fwd for dy = dloss/dy (the residual's own gradient is dy itself):
  *   dz = dy act'(z);  dx = alpha dz W [M, K];  dw = alpha dz^T x [N, K];  db = sum over rows of dz [N] fp32.
  * Each of dx, dw, db may be NULL and is then not computed.  preact is z from the forward; NULL only without an
- * activation.  ReLU'(0) = 0.  With bf16 values and a bf16 dy, dz is rounded to bf16 before the two products, as dy was; an fp32 dy
+ * activation.  ReLU gives dz = dy where z > 0, else 0, whatever dy is.  With bf16 values and a bf16 dy, dz is rounded to bf16 before the two products, as dy was; an fp32 dy
  * (out_dtype) keeps 16 bits of it, for twice the operations.  db sums it unrounded.  M = 0 gives dw = 0 and db = 0.  The same call gives the same bits every time (no atomics). */
 csa_status csa_linear_bwd(const csa_linear_params *p, const void *dy, const void *x, const void *weight,
                           const void *preact, void *dx, void *dw, float *db, void *workspace, size_t workspace_bytes,

@@ -185,7 +185,10 @@ dz_kernel(const O *dy, long long ldy, const V *z, int act, bf16 *dz, long long l
             float d[8], q[8];
             d0.floats(valid, d);
             if (act != CSA_ACT_NONE) z0.floats(valid, q);
-            if (act != CSA_ACT_NONE) {
+            if (act == CSA_ACT_RELU) {  // nothing passes where z <= 0, an infinite dy neither
+#pragma unroll
+                for (int j = 0; j < 8; j++) d[j] = q[j] > 0.f ? d[j] : 0.f;
+            } else if (act != CSA_ACT_NONE) {
 #pragma unroll
                 for (int j = 0; j < 8; j += 2) {
                     const float2 g = act_grad2(make_float2(q[j], q[j + 1]), act);

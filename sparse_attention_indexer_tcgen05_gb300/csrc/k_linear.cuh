@@ -53,7 +53,7 @@ template <int ACT> __device__ __forceinline__ float2 act_fwd2(float2 z)
     return make_float2(act_fwd<ACT>(z.x), act_fwd<ACT>(z.y));
 }
 
-// act'(z) of two values, in paired arithmetic: the gradient's pass over dy and z is short of issue slots.
+// act'(z) of two values (SILU or GELU_TANH), in paired arithmetic: the gradient's pass over dy and z is short of issue slots.
 //   SILU: s (1 + z (1 - s)), s = s(z);  GELU: s + z s (1 - s) kGelu (1 + 3 kCubic z^2), s = gelu_sigmoid(z)
 __device__ __forceinline__ float2 act_grad2(float2 z, int act)
 {
@@ -64,14 +64,11 @@ __device__ __forceinline__ float2 act_grad2(float2 z, int act)
         const float2 t = mul2(z, both(-kLog2e)), s = make_float2(sigmoid2(t.x), sigmoid2(t.y));
         return mul2(s, fma2(z, fma2(s, both(-1.f), both(1.f)), both(1.f)));
     }
-    if (act == CSA_ACT_GELU_TANH) {
-        const float2 zz = mul2(z, z), t = mul2(z, fma2(zz, both(-kLog2e * kGelu * kCubic), both(-kLog2e * kGelu)));
-        const float2 s = make_float2(sigmoid2(t.x), sigmoid2(t.y));
-        const float2 q = mul2(s, fma2(s, both(-1.f), both(1.f)));  // 0 far out, where z^2 may overflow
-        const float2 g = fma2(mul2(z, q), fma2(zz, both(3.f * kCubic * kGelu), both(kGelu)), s);
-        return make_float2(q.x > 0.f ? g.x : s.x, q.y > 0.f ? g.y : s.y);
-    }
-    return make_float2(z.x > 0.f ? 1.f : 0.f, z.y > 0.f ? 1.f : 0.f);  // ReLU
+    const float2 zz = mul2(z, z), t = mul2(z, fma2(zz, both(-kLog2e * kGelu * kCubic), both(-kLog2e * kGelu)));
+    const float2 s = make_float2(sigmoid2(t.x), sigmoid2(t.y));
+    const float2 q = mul2(s, fma2(s, both(-1.f), both(1.f)));  // 0 far out, where z^2 may overflow
+    const float2 g = fma2(mul2(z, q), fma2(zz, both(3.f * kCubic * kGelu), both(kGelu)), s);
+    return make_float2(q.x > 0.f ? g.x : s.x, q.y > 0.f ? g.y : s.y);
 }
 
 // Where a product's sums go.  y = act(alpha sum + bias[n]) + res; with `partial` the bare sums of split s go to

@@ -408,3 +408,20 @@ def test_linear_infinities_are_those_of_plain_products(M, dtype, out):
     same_kinds(dx, dy.double() @ w.double(), "dx")
     same_kinds(dw, dy.double().t() @ x.double(), "dw")
     same_kinds(db, dy.double().sum(0), "db")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_linear_relu_lets_no_infinite_gradient_pass(dtype):
+    """Where z <= 0 the gradient is 0 for an infinite or undefined dy too."""
+    M, K, N = 50, 24, 33
+    g = gen(31)
+    x, w, dy, z = (randn(g, *s, dtype=DT[dtype]) for s in ((M, K), (N, K), (M, N), (M, N)))
+    z[3, 4], z[5, 6], z[7, 8], z[9, 10] = -1.0, 0.0, -2.0, 1.0
+    p = B.LinearParams(M, K, N, dtype, activation="relu")
+    dy[3, 4] = dy[5, 6] = dy[7, 8] = 0.0
+    clean = B.csa_linear_bwd(p, dy, x, w, z)
+    dy[3, 4], dy[5, 6], dy[7, 8] = float("inf"), float("-inf"), float("nan")
+    for a, b in zip(clean, B.csa_linear_bwd(p, dy, x, w, z)):
+        assert torch.equal(a, b)
+    dy[9, 10] = float("inf")
+    assert B.csa_linear_bwd(p, dy, x, w, z)[2][10] == float("inf")
