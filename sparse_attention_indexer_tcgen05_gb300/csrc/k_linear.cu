@@ -308,7 +308,7 @@ inline size_t staged_bytes(int dtype, long long rows, long long cols)
     return up256((size_t)rows * up8(cols) * 2 * (dtype == CSA_F32 ? 3 : 1));
 }
 
-constexpr int kSms = 152;  // the split of a k axis is chosen for the whole GPU, the same on every call
+constexpr int kSms = 152;  // the split of a k axis is chosen for the whole GPU, the same on every call and device
 
 inline int planes_of(const csa_linear_params &p) { return p.dtype == CSA_F32 ? 3 : 1; }
 inline int dz_passes(const csa_linear_params &p) { return p.dtype == CSA_BF16 && p.out_dtype == CSA_F32 ? 2 : 1; }
@@ -414,7 +414,12 @@ cudaError_t run_stages(const csa_linear_params &p, const Stage (&job)[2], cudaSt
 
 cudaError_t product(const Product &p, cudaStream_t st)
 {
-    const cudaError_t e = launch_product_tc(p, kSms, st);
+    // The persistent kernel deals its units to the SMs that are there: CTAs beyond them would start when the first have
+    // finished their whole share.
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = launch_product_tc(p, sms > 2 ? sms : 2, st);
     if (e != cudaSuccess || p.plan.splits == 1) return e;
     // Too few whole sums to fill the GPU: cut them (the backward of 15401 x 48 x 24, dW from 61 pieces: 28.9 -> 17.0 us).
     const long long threads = p.M * (partial_stride(p.N) / 4);
