@@ -514,6 +514,13 @@ def _check_flat(t, name, dtype, index, numel):
     _check_tensor(t, name, dtype, torch.device("cuda", index), numel)
 
 
+def _check_weight(t, dtype, index, out_features, in_features):
+    """[out_features, in_features]; one of as many values that lies the other way round is refused."""
+    _check_flat(t, "weight", dtype, index, out_features * in_features)
+    if t.shape[-1] != in_features and t.dim() > 1:
+        raise ValueError(f"weight has shape {tuple(t.shape)}, expected [{out_features}, {in_features}]")
+
+
 def _dtype(d):
     if isinstance(d, int) and d in TORCH_DTYPE:
         return d
@@ -593,7 +600,7 @@ def csa_linear_fwd(p: LinearParams, x, weight, bias=None, residual=None, workspa
     c, dev = p.c, _on_cuda(x, "x")
     M, K, N = c.rows, c.in_features, c.out_features
     _check_rows(x, "x", p.value_dtype, dev, M, K, c.x_stride)
-    _check_flat(weight, "weight", p.value_dtype, dev, N * K)
+    _check_weight(weight, p.value_dtype, dev, N, K)
     if bias is not None:
         _check_flat(bias, "bias", torch.float32, dev, N)
     if residual is not None:
@@ -628,7 +635,7 @@ def csa_linear_bwd(p: LinearParams, dy, x, weight, preact=None, need_dx=True, ne
     if need_dw:
         _check_rows(x, "x", p.value_dtype, dev, M, K, c.x_stride)
     if need_dx:
-        _check_flat(weight, "weight", p.value_dtype, dev, N * K)
+        _check_weight(weight, p.value_dtype, dev, N, K)
     if c.activation != 0:
         _check_flat(preact, "preact", p.value_dtype, dev, M * N)
     else:
@@ -709,6 +716,8 @@ def csa_rope(p: RopeParams, x, positions, inv_freq, out=None):
     c, dev = p.c, _on_cuda(x, "x")
     _check_heads(x, "x", p, dev, c.x_row_stride, c.x_head_stride)
     _check_flat(positions, "positions", torch.int64 if c.positions_64 else torch.int32, dev, c.axes * c.rows)
+    if c.axes > 1 and positions.dim() > 1 and positions.shape[0] != c.axes:
+        raise ValueError(f"positions has shape {tuple(positions.shape)}, expected [{c.axes}, {c.rows}]")
     _check_flat(inv_freq, "inv_freq", torch.float64, dev, c.rot_dim // 2)
     given = out is not None
     if not given:

@@ -425,3 +425,25 @@ def test_linear_relu_lets_no_infinite_gradient_pass(dtype):
         assert torch.equal(a, b)
     dy[9, 10] = float("inf")
     assert B.csa_linear_bwd(p, dy, x, w, z)[2][10] == float("inf")
+
+
+def test_weights_and_positions_the_other_way_round_refused():
+    """Contiguous tensors of the right number of values whose axes lie the other way round."""
+    g = gen(40)
+    x, w, dy = randn(g, 12, 32), randn(g, 24, 32), randn(g, 12, 24)
+    p = B.LinearParams(12, 32, 24, "f32")
+    y = B.csa_linear_fwd(p, x, w)
+    assert torch.equal(B.csa_linear_fwd(p, x, w.flatten()), y)
+    for bad in (w.t().contiguous(), w.view(48, 16)):
+        with pytest.raises(ValueError, match="weight"):
+            B.csa_linear_fwd(p, x, bad)
+        with pytest.raises(ValueError, match="weight"):
+            B.csa_linear_bwd(p, dy, x, bad)
+    q = randn(g, 12, 2, 8)
+    r = B.RopeParams(12, 2, 8, "f32", sections=[1, 1, 2])
+    f = torch.ones(4, device="cuda", dtype=torch.float64)
+    pos = torch.arange(36, device="cuda", dtype=torch.int32).view(3, 12)
+    out = B.csa_rope(r, q, pos, f)
+    assert torch.equal(B.csa_rope(r, q, pos.flatten(), f), out) and torch.equal(B.csa_rope(r, q, pos.view(3, 4, 3), f), out)
+    with pytest.raises(ValueError, match="positions"):
+        B.csa_rope(r, q, pos.t().contiguous(), f)
