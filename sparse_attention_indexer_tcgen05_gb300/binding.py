@@ -909,6 +909,8 @@ class CSARope(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dout):
         positions, inv_freq = ctx.saved_tensors
+        if ctx.needs_input_grad[2]:
+            raise ValueError("inv_freq has no gradient here: detach it")
         return csa_rope(ctx.params.inverted(), _own(dout), positions, inv_freq), None, None, None
 
 

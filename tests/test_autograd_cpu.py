@@ -75,3 +75,15 @@ def test_a_gradient_off_the_16_byte_boundary_or_strided(B, shape):
         res.grad = None
         y.backward(g, retain_graph=True)
         assert torch.equal(res.grad, g.reshape(shape))
+
+
+def test_frequencies_that_ask_for_a_gradient_refused(B, monkeypatch):
+    """The rotation has no gradient for them: silence would leave them as they are."""
+    monkeypatch.setattr(B, "csa_rope", lambda p, x, positions, inv_freq, out=None: x.clone())
+    r = B.RopeParams(3, 1, 4, "f32")
+    x, pos, f = torch.ones(3, 1, 4, requires_grad=True), torch.zeros(1, 3, dtype=torch.int32), torch.ones(2, dtype=torch.float64)
+    B.csa_rotary(x, pos, f, r).sum().backward()
+    assert torch.equal(x.grad, torch.ones(3, 1, 4))
+    y = B.csa_rotary(x, pos, f.requires_grad_(True), r)
+    with pytest.raises(ValueError, match="inv_freq"):
+        y.sum().backward()
