@@ -516,6 +516,9 @@ def _check_flat(t, name, dtype, index, numel):
 
 def _check_weight(t, dtype, index, out_features, in_features):
     """[out_features, in_features]; one of as many values that lies the other way round is refused."""
+    if (t is not None and t.dtype is dtype and t.get_device() == index and t.shape == (out_features, in_features) and
+            t.is_contiguous()):
+        return
     _check_flat(t, "weight", dtype, index, out_features * in_features)
     if t.shape[-1] != in_features and t.dim() > 1:
         raise ValueError(f"weight has shape {tuple(t.shape)}, expected [{out_features}, {in_features}]")
@@ -776,7 +779,9 @@ class AdamWTensors:
             e.m, e.v, e.m_scale, e.v_scale = _ptr(t["m"]), _ptr(t["v"]), _ptr(t["m_scale"]), _ptr(t["v_scale"])
             e.numel, e.param_dtype, e.grad_dtype = numel, DTYPES[t["param"].dtype], DTYPES[t["grad"].dtype]
             e.state_dtype = STATE_E4M3 if eight else STATE_F32
-        self.written = [t for name in ("param", "master") for t in columns[name] if t is not None]  # what a graph may have saved
+        # what a graph may have saved; views of one buffer share its version counter
+        saved = (t if t._base is None else t._base for name in ("param", "master") for t in columns[name] if t is not None)
+        self.written = list({id(t): t for t in saved}.values())
         spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name, i)
                        for name, c in columns.items() if name != "grad" for i, t in enumerate(c)
                        if t is not None and t.numel())

@@ -151,7 +151,8 @@ template <typename V> __global__ void __launch_bounds__(256) stage_kernel(const 
 // z are read once, dz is written once, 8 neighbouring columns a thread (VEC: aligned ones), the next row's on their way
 // while a row is worked on: bf16 silu of 8192 x 8192 values 65 us (403 MB), db alone 30.  (Two rows loaded and then
 // worked on: 79 and 52.)  Blocks behind the `across` x `down` ones stage operands of the products.
-template <typename V, typename O, int TX, bool VEC>
+// SMOOTH: SiLU or GELU; else ReLU or none.  (One kernel for all of them: db of 8192 x 8192 values with GELU 59 us, two kernels 49 to 57.)
+template <typename V, typename O, int TX, bool VEC, bool SMOOTH>
 __global__ void __launch_bounds__(256, 4)
 dz_kernel(const O *dy, long long ldy, const V *z, int act, bf16 *dz, long long ld, long long plane, float *sums,
           long long M, int N, int per, unsigned across, unsigned down, const Stage s0, const Stage s1)
@@ -175,7 +176,7 @@ dz_kernel(const O *dy, long long ldy, const V *z, int act, bf16 *dz, long long l
         const auto ask = [&](long long r) {
             if (r >= r1) return;
             d1.load(dy + r * ldy + n, valid, dy + (M - 1) * ldy + N);
-            if (act != CSA_ACT_NONE) z1.load(z + r * N + n, valid, z + M * N);
+            if (SMOOTH || act != CSA_ACT_NONE) z1.load(z + r * N + n, valid, z + M * N);
         };
         ask(r0 + ty);
         for (long long r = r0 + ty; r < r1; r += TY) {
@@ -184,17 +185,17 @@ dz_kernel(const O *dy, long long ldy, const V *z, int act, bf16 *dz, long long l
             ask(r + TY);
             float d[8], q[8];
             d0.floats(valid, d);
-            if (act != CSA_ACT_NONE) z0.floats(valid, q);
-            if (act == CSA_ACT_RELU) {  // nothing passes where z <= 0, an infinite dy neither
-#pragma unroll
-                for (int j = 0; j < 8; j++) d[j] = q[j] > 0.f ? d[j] : 0.f;
-            } else if (act != CSA_ACT_NONE) {
+            if (SMOOTH || act != CSA_ACT_NONE) z0.floats(valid, q);
+            if constexpr (SMOOTH) {
 #pragma unroll
                 for (int j = 0; j < 8; j += 2) {
                     const float2 g = act_grad2(make_float2(q[j], q[j + 1]), act);
                     d[j] = __fmul_rn(d[j], g.x);  // rounded before it is added, whichever outputs are asked for
                     d[j + 1] = __fmul_rn(d[j + 1], g.y);
                 }
+            } else if (act == CSA_ACT_RELU) {  // nothing passes where z <= 0, an infinite dy neither
+#pragma unroll
+                for (int j = 0; j < 8; j++) d[j] = q[j] > 0.f ? d[j] : 0.f;
             }
 #pragma unroll
             for (int j = 0; j < 8; j++) s[j] += d[j];
@@ -429,25 +430,33 @@ cudaError_t product(const Product &p, cudaStream_t st)
     return launch_chained(kernel, dim3((unsigned)((threads + each - 1) / each)), 256, 0, 1, st, p.e.partial, p.plan.splits, p.M, p.N, p.e);
 }
 
-template <typename V, typename O, int TX, bool VEC>
+template <typename V, typename O, int TX, bool VEC, bool SMOOTH>
 cudaError_t run_dz_rows(const csa_linear_params &p, const Bwd &b, const void *dy, const void *z, bf16 *dz, float *sums,
                         const Stage (&job)[2], cudaStream_t st)
 {
     const int N = p.out_features;
     const long long ld = up8(N), plane = p.rows * ld;
     const unsigned across = (N + 8 * TX - 1) / (8 * TX), down = b.blocks;
-    return launch_chained(dz_kernel<V, O, TX, VEC>, dim3(across * down + job[0].blocks + job[1].blocks), 256, 0, 1, st, (const O *)dy,
+    return launch_chained(dz_kernel<V, O, TX, VEC, SMOOTH>, dim3(across * down + job[0].blocks + job[1].blocks), 256, 0, 1, st, (const O *)dy,
                           p.dy_stride, (const V *)z, p.activation, dz, ld, plane, sums, p.rows, N, b.per, across, down, job[0], job[1]);
+}
+
+template <typename V, typename O, bool SMOOTH>
+cudaError_t run_dz_act(const csa_linear_params &p, const Bwd &b, const void *dy, const void *z, bf16 *dz, float *sums,
+                       const Stage (&job)[2], cudaStream_t st)
+{
+    const bool vec = (p.out_features & 7) == 0 && (p.dy_stride & 7) == 0;
+    auto *run = p.out_features <= 64 ? (vec ? run_dz_rows<V, O, 8, true, SMOOTH> : run_dz_rows<V, O, 8, false, SMOOTH>)
+                                     : (vec ? run_dz_rows<V, O, 32, true, SMOOTH> : run_dz_rows<V, O, 32, false, SMOOTH>);
+    return run(p, b, dy, z, dz, sums, job, st);
 }
 
 template <typename V, typename O>
 cudaError_t run_dz(const csa_linear_params &p, const Bwd &b, const void *dy, const void *z, bf16 *dz, float *sums, const Stage (&job)[2],
                    cudaStream_t st)
 {
-    const bool vec = (p.out_features & 7) == 0 && (p.dy_stride & 7) == 0;
-    auto *run = p.out_features <= 64 ? (vec ? run_dz_rows<V, O, 8, true> : run_dz_rows<V, O, 8, false>)
-                                     : (vec ? run_dz_rows<V, O, 32, true> : run_dz_rows<V, O, 32, false>);
-    return run(p, b, dy, z, dz, sums, job, st);
+    const bool smooth = p.activation == CSA_ACT_SILU || p.activation == CSA_ACT_GELU_TANH;
+    return (smooth ? run_dz_act<V, O, true> : run_dz_act<V, O, false>)(p, b, dy, z, dz, sums, job, st);
 }
 
 }  // namespace linear
