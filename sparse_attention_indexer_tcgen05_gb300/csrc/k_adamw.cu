@@ -20,7 +20,8 @@
 // are warp reductions and no shared memory is needed.  The tensors' pointers travel in the kernel's parameters (no
 // copy, no device table that must outlive the call, any stream capture keeps them); a CTA finds its tensor by a
 // binary search over the first chunk of each.  Measured: 412 million bf16 weights with fp32 masters and 8-bit states
-// 1077 us (6.15 TB/s, 91% of a copy's rate; two thirds of the issue slots are taken); 96 small fp32 tensors 5.3 us.
+// to nearest 1090 us (6.1 TB/s, 89% of a copy's rate; two thirds of the issue slots are taken), stochastic 1235 us (83% of
+// the issue slots); 96 small fp32 tensors 6.2 us.
 #include "csa_internal.cuh"
 #include "tc_ptx.cuh"
 

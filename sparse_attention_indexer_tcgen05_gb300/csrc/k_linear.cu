@@ -149,7 +149,7 @@ template <typename V> __global__ void __launch_bounds__(256) stage_kernel(const 
 
 // dz = dy act'(z) for `per` rows of a block and 8 TX columns, and their column sums for db.  Bound by memory: dy and
 // z are read once, dz is written once, 8 neighbouring columns a thread (VEC: aligned ones), the next row's on their way
-// while a row is worked on: bf16 silu of 8192 x 8192 values 65 us (403 MB), db alone 30.  (Two rows loaded and then
+// while a row is worked on: bf16 silu of 8192 x 8192 values 62 us (403 MB), db alone 35.  (Two rows loaded and then
 // worked on: 79 and 52.)  Blocks behind the `across` x `down` ones stage operands of the products.
 // SMOOTH: SiLU or GELU; else ReLU or none.  (One kernel for all of them: db of 8192 x 8192 values with GELU 59 us, two kernels 49 to 57.)
 template <typename V, typename O, int TX, bool VEC, bool SMOOTH>
@@ -524,7 +524,7 @@ cudaError_t launch_linear_bwd(const csa_linear_params &p, const void *dy, const 
     Operand ow = {}, ox = {};
     if (dx != nullptr) ow = operand(p, weight, K, N, (int)K, b.stage_w, w + b.off_w, false, &job[0]);
     if (dw != nullptr) ox = operand(p, x, p.x_stride, M, (int)K, b.stage_x, w + b.off_x, false, &job[1]);
-    // A few staged blocks join dz's launch (1013 x 1023 x 777 in fp32: 47.1 us before, 43.8 so); many have their own, with
+    // A few staged blocks join dz's launch (1013 x 1023 x 777 in fp32: 47.1 -> 43.8 us); many have their own, with
     // twice the warps an SM (62578 x 684 x 585 in bf16: 204 us, joined 213).
     const bool any_dz = dz != nullptr || sums != nullptr;
     if (!any_dz || job[0].blocks + job[1].blocks > 16u * kSms) {

@@ -9,13 +9,14 @@
 // 16 rows of W and cut the k axis among them (their sums are joined in a fixed order: the same bits every time); sums
 // move to fp32 registers of their own every 32 MMAs, which cut off rather than round.  The tensor cores are far from
 // busy; what counts is the bytes in flight and the few instructions.  Bound by the start-up and W's way from DRAM: 8192
-// outputs of 2048 values (33.6 MB) take 8.0 us for one row and 9.4 us for 16 with W in DRAM, 5.3 us for one with W in L2
+// outputs of 2048 values (33.6 MB) take 7.6 us for one row and 9.2 us for 16 with W in DRAM, 5.0 us for one with W in L2
 // (with fp32 multiply-adds, 8 rows took 24 us; on a tcgen05 tile, 16).
 //
 // Other types and strides, up to 8 rows (small_kernel): a warp takes two rows of W and runs along k with 16-byte loads, a
 // lane every 32nd of them, and holds the sums in registers, in fp32, as pairs of even and odd k.  x is a few KB and
 // comes from L1.  Where N gives too few warps for the GPU, the warps of a CTA share the rows and cut the k axis.  fp32,
-// 4096 outputs of 2048 values (33.6 MB): 7.6 us for one row, 11 us for 8.
+// 4096 outputs of 2048 values (33.6 MB): 7.0 us for one row, 10.6 us for 8.  bf16 rows off the 16-byte boundaries are loaded value by
+// value: 8192 outputs of 2047 values 26 us for one row, 50 for 8.
 #include "k_linear.cuh"
 #include "tc_ptx.cuh"
 

@@ -22,7 +22,7 @@
 // round-robin in an order that keeps the running tiles' operands in L2.
 //
 // Measured (bf16, from and to bf16): 8192 x 8192 x 2048 142 us (1.94 PFLOP/s; the library's product takes 140), its two
-// gradients 151 and 163 us (153 and 163), 8192^3 590 to 610 us (577 to 592), 2048^3 16.6 us (22).  Bound by the MMAs (87%
+// gradients 151 to 170 and 163 to 175 us (153 and 163), 8192^3 590 to 634 us (577 to 592), 2048^3 17 to 20 us (22).  Bound by the MMAs (87%
 // of the cycles), and at the chip's power limit by its clock; up to 256 k by the epilogue.
 //
 // Every mbarrier wait is bounded (see tc_ptx.cuh); site codes 600 + n.
@@ -245,7 +245,7 @@ __device__ __forceinline__ void turned_rows(O *out, long long ld, long long M, l
 
 // A warp's 32 rows x 32 columns, a row a lane, to memory by the lanes' own stores; rows from M and columns from N on
 // are left out.  Rows on 32-byte boundaries: each lane its own sectors; on 16-byte ones: half sectors (kept z of 8200 x
-// 4104 x 264: 90 us with everything instead of 123).  Else: turned in shared memory so that a warp
+// 4104 x 264: 90 us with everything instead of 123; 103 in a loop at the power limit).  Else: turned in shared memory so that a warp
 // writes 32 neighbouring values at a time.
 template <typename O>
 __device__ __forceinline__ void store_tile(O *out, long long ld, long long M, long long N, const float (&v)[C], long long m0, long long n0,

@@ -13,7 +13,7 @@
 // first values are on their way, and shares them among the heads; warps do not wait for one another.  An item of work
 // is two vectors of V elements: the two halves of V pairs (or, interleaved, V whole pairs), or two vectors of values
 // that are copied.  V is the widest vector (32 bytes at most) that offset, dimensions and strides allow.  Measured (bf16):
-// 16384 rows of 64 heads of 128 values, half of which rotate, 82 us (6.6 TB/s, 97% of a copy's rate); 5 rows 2.9 us.
+// 16384 rows of 64 heads of 128 values, half of which rotate, 83 us (6.5 TB/s, 95% of a copy's rate); 5 rows 3.5 us.
 #include "csa_internal.cuh"
 
 namespace csa {
