@@ -260,9 +260,9 @@ size_t csa_linear_bwd_workspace_size(const csa_linear_params *p);
  *   -> y [M, N] out_dtype contiguous, preact [M, N] dtype contiguous or NULL: z, which the backward of an
  *      activation reads.
  * Sums and the epilogue are fp32, rounded once.  The tensor core cuts sums and products off at the sum's last place,
- * towards zero (measured: 7e-7 of a sum of 512 positive terms, 3e-4 of one of 65536).  A sum there starts anew every 65536 k
- * for a bf16 result, every 512 k for an fp32 result of bf16 values and every 64 k for fp32 values, and the pieces are added
- * in fp32.  fp32 values are multiplied as three bf16 parts each (six products, about 2^-23 relative to the terms).
+ * towards zero (measured: 7e-7 of a sum of 512 positive terms, 3e-4 of one of 65536).  A sum there starts anew every
+ * 65536 k for a bf16 result, every 512 k for an fp32 result of bf16 values and every 64 k for fp32 values, and the pieces
+ * are added in fp32.  fp32 values are multiplied as three bf16 parts each (six products, about 2^-23 relative to the terms).
  * Infinities and NaN give what plain products give.
  * y may be the residual itself when their row strides agree; an output given as another argument is refused otherwise.
  * rows and features up to 2^31 - 2^16. */
@@ -273,8 +273,9 @@ csa_status csa_linear_fwd(const csa_linear_params *p, const void *x, const void 
 /* The gradients of csa_linear_fwd for dy = dloss/dy (the residual's own gradient is dy itself):
  *   dz = dy act'(z);  dx = alpha dz W [M, K];  dw = alpha dz^T x [N, K];  db = sum over rows of dz [N] fp32.
  * Each of dx, dw, db may be NULL and is then not computed.  preact is z from the forward; NULL only without an
- * activation.  ReLU gives dz = dy where z > 0, else 0, whatever dy is.  With bf16 values and a bf16 dy, dz is rounded to bf16 before the two products, as dy was; an fp32 dy
- * (out_dtype) keeps 16 bits of it, for twice the operations.  db sums it unrounded.  M = 0 gives dw = 0 and db = 0.  The same call gives the same bits every time (no atomics). */
+ * activation.  ReLU gives dz = dy where z > 0, else 0, whatever dy is.  With bf16 values and a bf16 dy, dz is rounded to
+ * bf16 before the two products, as dy was; an fp32 dy (out_dtype) keeps 16 bits of it, for twice the operations.  db sums
+ * it unrounded.  M = 0 gives dw = 0 and db = 0.  The same call gives the same bits every time (no atomics). */
 csa_status csa_linear_bwd(const csa_linear_params *p, const void *dy, const void *x, const void *weight,
                           const void *preact, void *dx, void *dw, float *db, void *workspace, size_t workspace_bytes,
                           void *stream);
@@ -348,8 +349,7 @@ typedef struct {
  * many steps only stochastic codes follow the recurrences: half a step of a code is up to 5.6% of its value, so nearest
  * codes stand still under changes below that, all that a step makes of v with beta2 above 0.89 and of m with beta1 above
  * 0.94.
- *  `tensors` is a host array, read before the call returns.  No
- * workspace.  Two tensors that name the same param, master, m, v or scale are refused; buffers that overlap in any
+ * `tensors` is a host array, read before the call returns.  No workspace.  Two tensors that name the same param, master, m, v or scale are refused; buffers that overlap in any
  * other way are the caller's error. */
 csa_status csa_adamw(const csa_adamw_params *p, const csa_adamw_tensor *tensors, int32_t count, void *stream);
 

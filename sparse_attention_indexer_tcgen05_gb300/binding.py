@@ -520,7 +520,7 @@ def _check_weight(t, dtype, index, out_features, in_features):
             t.is_contiguous()):
         return
     _check_flat(t, "weight", dtype, index, out_features * in_features)
-    if t.shape[-1] != in_features and t.dim() > 1:
+    if t.dim() > 1 and t.shape[-1] != in_features:
         raise ValueError(f"weight has shape {tuple(t.shape)}, expected [{out_features}, {in_features}]")
 
 
