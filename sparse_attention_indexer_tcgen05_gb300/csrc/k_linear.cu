@@ -2,127 +2,14 @@
 // around the products: operands made fit for TMA (rows on 16-byte boundaries, fp32 values as three bf16 planes),
 // dz = dy act'(z) with the bias gradient, and the join of a split k axis with the epilogue.
 #include "k_linear.cuh"
+#include "k_rows.cuh"
 
 namespace csa {
 namespace linear {
 
-using bf16 = __nv_bfloat16;
-
-// x = h + m + l with bf16 parts: 8 bits of the significand each.  NaN stays in h; a finite x that would round to an infinity
-// is cut off instead.  An infinity goes to l, which meets the other factor's h alone, and h is 1 of its sign: the product is
-// then an infinity of the right sign for every other factor that is not 0, infinite ones too (whose l meets this h).  In h it
-// would meet the other's m and l, which may be 0 or of the other sign.
-__device__ __forceinline__ void split3(float x, bf16 &h, bf16 &m, bf16 &l)
-{
-    h = __float2bfloat16_rn(x);
-    if (fabsf(x) > 3.38e38f && fabsf(x) < INFINITY) h = __ushort_as_bfloat16((unsigned short)(__float_as_uint(x) >> 16));
-    const float r = x - __bfloat162float(h);
-    const bool fine = fabsf(r) <= 3.0e38f;  // false for NaN and infinities
-    m = __float2bfloat16_rn(fine ? r : 0.f);
-    l = __float2bfloat16_rn(fine ? r - __bfloat162float(m) : 0.f);
-    if (fabsf(x) == INFINITY) {
-        l = h;
-        h = __float2bfloat16_rn(copysignf(1.f, x));
-    }
-}
-
-// x = h + m to 2^-16.  h is cut off and m never 0 unless x is, so that both have x's sign: an infinite factor then gives an
-// infinity of that sign, not NaN.
-__device__ __forceinline__ void split2(float x, bf16 &h, bf16 &m)
-{
-    h = __ushort_as_bfloat16((unsigned short)(__float_as_uint(x) >> 16));
-    const float top = __bfloat162float(h), r = x - top;
-    m = __float2bfloat16_rn(r != 0.f && fabsf(x) < INFINITY ? r : top * 5.9604644775390625e-8f);
-}
-
-// What holds a staged operand of values V
-template <typename V> struct Planes;
-template <> struct Planes<bf16> { static constexpr int N = 1; };
-template <> struct Planes<float> { static constexpr int N = 3; };
-// and dz, of values V and gradients O.  fp32 gradients of bf16 values keep 16 bits of it, for twice the MMAs; bf16 ones
+// What holds dz, of values V and gradients O.  fp32 gradients of bf16 values keep 16 bits of it, for twice the MMAs; bf16 ones
 // come with 8 bits, and dz has no more.
 template <typename V, typename O> struct DzPlanes { static constexpr int N = sizeof(V) == 4 ? 3 : sizeof(O) == 4 ? 2 : 1; };
-
-// What a staged operand is made of: rows x cols values, rows `stride` apart -> planes of rows `ld` apart.
-struct Stage {
-    const void *x;
-    bf16 *out;
-    long long stride, rows, ld, plane;
-    int cols, aligned;   // rows start on 16-byte boundaries
-    unsigned blocks;     // of 256 threads, 8 values each
-};
-
-// 8 neighbouring values from p on, of which `valid` (1 to 8) exist; the others 0.  ALIGNED: p lies on 16 bytes and all
-// exist.  Otherwise p lies anywhere: the aligned vectors that hold the existing values are loaded, up to the argument's
-// `end`, and shifted when the values are taken.
-template <typename T, bool ALIGNED> struct Raw8 {
-    static constexpr int V = sizeof(T) == 2 ? 1 : 2;   // vectors of 8 values
-    uint32_t w[4 * V + (ALIGNED ? 0 : 4)], sh;
-    __device__ __forceinline__ void load(const T *p, int valid, const T *end)
-    {
-        sh = ALIGNED ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
-        const uint4 *q = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) - sh);
-#pragma unroll
-        for (int k = 0; k < V + (ALIGNED ? 0 : 1); k++) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (ALIGNED) v = __ldcs(q + k);
-            else if ((int)sh + valid * (int)sizeof(T) > 16 * k) v = load16(q + k, end);
-            w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
-        }
-    }
-    __device__ __forceinline__ void floats(int valid, float (&x)[8]) const
-    {
-        uint32_t u[4 * V + 4];
-#pragma unroll
-        for (int k = 0; k < 4 * V + 4; k++) u[k] = k < 4 * V + (ALIGNED ? 0 : 4) ? w[k] : 0u;
-        if (!ALIGNED) {
-            if (sh & 8) {
-#pragma unroll
-                for (int k = 0; k < 4 * V + 2; k++) u[k] = u[k + 2];
-            }
-            if (sh & 4) {
-#pragma unroll
-                for (int k = 0; k < 4 * V + 1; k++) u[k] = u[k + 1];
-            }
-            if (sizeof(T) == 2 && (sh & 2)) {
-#pragma unroll
-                for (int k = 0; k < 4; k++) u[k] = __funnelshift_r(u[k], u[k + 1], 16);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < 8; k++) {
-            const uint32_t b = sizeof(T) == 4 ? u[k] : k % 2 == 0 ? u[k / 2] << 16 : u[k / 2] & 0xffff0000u;
-            x[k] = ALIGNED || k < valid ? __uint_as_float(b) : 0.f;
-        }
-    }
-};
-template <typename T, bool ALIGNED> __device__ __forceinline__ void load8(const T *p, int valid, const T *end, float (&x)[8])
-{
-    Raw8<T, ALIGNED> r;
-    r.load(p, valid, end);
-    r.floats(valid, x);
-}
-
-// 8 neighbouring values to the planes
-
-template <int P> __device__ __forceinline__ void put_planes8(bf16 *out, long long plane, long long at, const float (&x)[8])
-{
-    __nv_bfloat162 w[P][4];
-#pragma unroll
-    for (int k = 0; k < 4; k++) {
-        if constexpr (P == 1) {
-            w[0][k] = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
-        } else if constexpr (P == 2) {
-            split2(x[2 * k], w[0][k].x, w[1][k].x);
-            split2(x[2 * k + 1], w[0][k].y, w[1][k].y);
-        } else {
-            split3(x[2 * k], w[0][k].x, w[1][k].x, w[2][k].x);
-            split3(x[2 * k + 1], w[0][k].y, w[1][k].y, w[2][k].y);
-        }
-    }
-#pragma unroll
-    for (int q = 0; q < P; q++) *reinterpret_cast<uint4 *>(out + q * plane + at) = *reinterpret_cast<const uint4 *>(w[q]);
-}
 
 // Block `b` of up to two operands; a thread makes 8 neighbouring values of a row.
 template <typename V> __device__ __forceinline__ void stage_block(const Stage &s0, const Stage &s1, unsigned b)
@@ -299,18 +186,6 @@ __global__ void __launch_bounds__(256) join_kernel(const float *partial, int spl
 
 // ------------------------------------------------------------------ host side
 
-inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
-inline long long up8(long long x) { return (x + 7) & ~7LL; }
-
-// Rows that TMA cannot read where they are: fp32 values, or row strides off the 16-byte boundaries.
-inline bool staged(int dtype, long long stride) { return dtype == CSA_F32 || (stride & 7) != 0; }
-inline size_t staged_bytes(int dtype, long long rows, long long cols)
-{
-    return up256((size_t)rows * up8(cols) * 2 * (dtype == CSA_F32 ? 3 : 1));
-}
-
-constexpr int kSms = 152;  // the split of a k axis is chosen for the whole GPU, the same on every call and device
-
 inline int planes_of(const csa_linear_params &p) { return p.dtype == CSA_F32 ? 3 : 1; }
 inline int dz_passes(const csa_linear_params &p) { return p.dtype == CSA_BF16 && p.out_dtype == CSA_F32 ? 2 : 1; }
 
@@ -379,8 +254,7 @@ Bwd plan_bwd(const csa_linear_params &p)
     return b;
 }
 
-// The operand of `rows` x `cols` values, where they are or staged (`job` then says how; no blocks: it is not).
-Operand operand(const csa_linear_params &p, const void *x, long long stride, long long rows, int cols, bool stage, void *to, bool k_major,
+Operand operand(int dtype, const void *x, long long stride, long long rows, int cols, bool stage, void *to, bool k_major,
                 Stage *job)
 {
     Operand o;
@@ -401,16 +275,16 @@ Operand operand(const csa_linear_params &p, const void *x, long long stride, lon
     job->ld = o.ld;
     job->plane = o.plane;
     job->cols = cols;
-    job->aligned = stride % (p.dtype == CSA_F32 ? 4 : 8) == 0;
+    job->aligned = stride % (dtype == CSA_F32 ? 4 : 8) == 0;
     job->blocks = (unsigned)((rows * ((cols + 7) / 8) + 255) / 256);
     return o;
 }
 
-cudaError_t run_stages(const csa_linear_params &p, const Stage (&job)[2], cudaStream_t st)
+cudaError_t run_stages(int dtype, const Stage (&job)[2], cudaStream_t st)
 {
     const unsigned blocks = job[0].blocks + job[1].blocks;
     if (blocks == 0) return cudaSuccess;
-    return launch_chained(p.dtype == CSA_F32 ? stage_kernel<float> : stage_kernel<bf16>, dim3(blocks), 256, 0, 1, st, job[0], job[1]);
+    return launch_chained(dtype == CSA_F32 ? stage_kernel<float> : stage_kernel<bf16>, dim3(blocks), 256, 0, 1, st, job[0], job[1]);
 }
 
 cudaError_t product(const Product &p, cudaStream_t st)
@@ -493,9 +367,9 @@ cudaError_t launch_linear_fwd(const csa_linear_params &p, const void *x, const v
     const Fwd f = plan_fwd(p);
     char *w = static_cast<char *>(ws);
     Stage job[2] = {};
-    q.a = operand(p, x, p.x_stride, p.rows, p.in_features, f.stage_x, w + f.off_x, true, &job[0]);
-    q.b = operand(p, weight, p.in_features, p.out_features, p.in_features, f.stage_w, w + f.off_w, true, &job[1]);
-    LIN_TRY(run_stages(p, job, st));
+    q.a = operand(p.dtype, x, p.x_stride, p.rows, p.in_features, f.stage_x, w + f.off_x, true, &job[0]);
+    q.b = operand(p.dtype, weight, p.in_features, p.out_features, p.in_features, f.stage_w, w + f.off_w, true, &job[1]);
+    LIN_TRY(run_stages(p.dtype, job, st));
     q.M = p.rows;
     q.N = p.out_features;
     q.K = p.in_features;
@@ -522,13 +396,13 @@ cudaError_t launch_linear_bwd(const csa_linear_params &p, const void *dy, const 
     float *sums = db != nullptr ? reinterpret_cast<float *>(w + b.off_sums) : nullptr;
     Stage job[2] = {};
     Operand ow = {}, ox = {};
-    if (dx != nullptr) ow = operand(p, weight, K, N, (int)K, b.stage_w, w + b.off_w, false, &job[0]);
-    if (dw != nullptr) ox = operand(p, x, p.x_stride, M, (int)K, b.stage_x, w + b.off_x, false, &job[1]);
+    if (dx != nullptr) ow = operand(p.dtype, weight, K, N, (int)K, b.stage_w, w + b.off_w, false, &job[0]);
+    if (dw != nullptr) ox = operand(p.dtype, x, p.x_stride, M, (int)K, b.stage_x, w + b.off_x, false, &job[1]);
     // A few staged blocks join dz's launch (1013 x 1023 x 777 in fp32: 47.1 -> 43.8 us); many have their own, with
     // twice the warps an SM (62578 x 684 x 585 in bf16: 204 us, joined 213).
     const bool any_dz = dz != nullptr || sums != nullptr;
     if (!any_dz || job[0].blocks + job[1].blocks > 16u * kSms) {
-        LIN_TRY(run_stages(p, job, st));
+        LIN_TRY(run_stages(p.dtype, job, st));
         job[0].blocks = job[1].blocks = 0;
     }
     if (any_dz) {

@@ -7,6 +7,8 @@
 namespace csa {
 namespace linear {
 
+using bf16 = __nv_bfloat16;
+
 // s(u) = 1 / (1 + 2^t), t = -u log2(e), with the hardware's base-2 exponential and reciprocal (2 units in the last
 // place each)
 __device__ __forceinline__ float sigmoid2(float t)
@@ -155,6 +157,33 @@ struct Product {
     Epilogue e;
 };
 cudaError_t launch_product_tc(const Product &p, int sms, cudaStream_t st);
+
+// What a staged operand is made of: rows x cols values, rows `stride` apart -> planes of rows `ld` apart.
+struct Stage {
+    const void *x;
+    bf16 *out;
+    long long stride, rows, ld, plane;
+    int cols, aligned;   // rows start on 16-byte boundaries
+    unsigned blocks;     // of 256 threads, 8 values each
+};
+
+inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+inline long long up8(long long x) { return (x + 7) & ~7LL; }
+
+// Rows that TMA cannot read where they are: fp32 values, or row strides off the 16-byte boundaries.
+inline bool staged(int dtype, long long stride) { return dtype == CSA_F32 || (stride & 7) != 0; }
+inline size_t staged_bytes(int dtype, long long rows, long long cols)
+{
+    return up256((size_t)rows * up8(cols) * 2 * (dtype == CSA_F32 ? 3 : 1));
+}
+
+constexpr int kSms = 152;  // the split of a k axis is chosen for the whole GPU, the same on every call and device
+
+// The operand of `rows` x `cols` values, where they are or staged (`job` then says how; no blocks: it is not).
+Operand operand(int dtype, const void *x, long long stride, long long rows, int cols, bool stage, void *to, bool k_major, Stage *job);
+cudaError_t run_stages(int dtype, const Stage (&job)[2], cudaStream_t st);
+// launch_product_tc on the SMs that are there, and the join of a split k axis with the epilogue.
+cudaError_t product(const Product &p, cudaStream_t st);
 
 // The forward of a few rows (k_linear_small.cu); operands where they are, no workspace.
 constexpr int kSmallRows = 8, kFewRows = 16;

@@ -27,8 +27,7 @@
 //
 // Every mbarrier wait is bounded (see tc_ptx.cuh); site codes 600 + n.
 #include "csa_tc.cuh"
-#include "k_linear.cuh"
-#include "tc_ptx.cuh"
+#include "k_linear_pipe.cuh"
 
 #include <cuda.h>
 #include <math.h>
@@ -52,83 +51,9 @@ namespace linear {
 
 using namespace ptx;
 
-constexpr int BM = 128;        // rows of one CTA's accumulator
-constexpr int BK = 64;         // k per stage: one 128-byte swizzle row
 constexpr long long LONGEST = 65536;  // k that a bf16 result sums in one accumulator
 constexpr int CHUNK_1 = 8;     // stages (512 k) that an fp32 result of one plane does
 constexpr int MANY_STEPS = 4;  // stages of a unit up to which 256-wide tiles have 16 epilogue warps
-
-// P planes, EW epilogue warps
-template <int CG, int BN, int P, int EW> struct Cfg {
-    static constexpr int THREADS = 64 + 32 * EW;
-    static constexpr int ROWS_B = BN / CG;                      // B rows this CTA loads
-    static constexpr int A_BYTES = BM * BK * 2, B_BYTES = ROWS_B * BK * 2;
-    static constexpr int STAGE = P * (A_BYTES + B_BYTES);
-    static constexpr int STAGES = (229376 - EW * 4096) / STAGE; // of 192 KB (EW 8): 6 or 8; 2 of three planes
-    static constexpr int TURN = STAGES * STAGE;                 // the epilogue's buffers, 32 rows of 128 bytes a warp
-    static constexpr int MISC = TURN + EW * 4096;
-    static constexpr int SMEM = MISC + 512 + 1024;              // + alignment
-    static constexpr int TMEM = 2 * BN < 512 ? (2 * BN < 128 ? 128 : 2 * BN) : 512;
-};
-
-struct Args {
-    long long M, N, ldo;        // the output's row stride
-    int ksteps;                 // stages over the whole k axis, all passes
-    int splits, per_split;      // k pieces, stages of each
-    int mt, nt;                 // tiles
-    int whole, units;           // units that are whole tiles (times splits); the rest are halves of the last tiles
-    int rows_a;                 // rows of A a CTA loads: BM, fewer where M is below BM
-    int blocks_a, blocks_b;     // an m/n-contiguous operand's map has 64-wide blocks as an axis of their own
-    int tma_out;                // the output goes by TMA
-    int many;                   // 16 epilogue warps
-    int res32;                  // the residual's rows start on 32-byte sectors
-    Epilogue e;
-};
-
-struct Unit {
-    int m, s, it0, it1;
-    int bn;                     // columns: BN, or BN / 2 for half a tile
-    long long n0;               // first column
-};
-
-// Tiles in bands of 8 along m, m fastest: the tiles that run together share a few rows of A tiles and a few of B.
-// When the last round of whole tiles would leave half of the SMs idle or more, its tiles are cut in two along n.
-constexpr int BAND = 8;
-template <int BN> __device__ __forceinline__ Unit unit_of(const Args &a, int u)
-{
-    Unit x;
-    const int tiles = a.mt * a.nt;
-    int t, half = 0;
-    x.bn = BN;
-    x.s = 0;
-    if (u < a.whole) {
-        if (a.splits > 1) {
-            x.s = u / tiles;
-            t = u - x.s * tiles;
-        } else {
-            t = u;
-        }
-    } else {
-        t = a.whole + ((u - a.whole) >> 1);
-        half = (u - a.whole) & 1;
-        x.bn = BN / 2;
-    }
-    const int per_band = BAND * a.nt;
-    const int band = t / per_band;
-    const int r = t - band * per_band;
-    const int h = min(BAND, a.mt - band * BAND);
-    x.m = band * BAND + r % h;
-    x.n0 = (long long)(r / h) * BN + half * (BN / 2);
-    x.it0 = x.s * a.per_split;
-    x.it1 = min(a.ksteps, x.it0 + a.per_split);
-    return x;
-}
-
-// Shared memory a warp stores from: 32 rows of 128 bytes.
-struct Buffer {
-    unsigned char *p;
-    int lane;
-};
 
 // 256-bit accesses, whole sectors
 __device__ __forceinline__ void st32(void *p, const uint32_t (&w)[8])
@@ -144,8 +69,6 @@ __device__ __forceinline__ void ld32(const void *p, uint32_t *w)
                  : "l"(p)
                  : "memory");
 }
-
-constexpr int C = 32;   // columns of an epilogue step
 
 // 32 columns of one row of the residual.  Whole sectors are asked for a step before they are used (`early`); other rows
 // (and a warp's columns that end behind N) are read where they are added, as the aligned vectors that hold the columns that exist, shifted.  (Value
@@ -209,12 +132,6 @@ template <int ACT> __device__ __forceinline__ void activate(float (&v)[C])
         v[k] = y.x;
         v[k + 1] = y.y;
     }
-}
-
-__device__ __forceinline__ uint32_t pack2(float a, float b)
-{
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 // The second half of a turn: V neighbouring columns a lane, 32 / V lanes a row.  Rows start on V values.
@@ -285,39 +202,6 @@ __device__ __forceinline__ void store_tile(O *out, long long ld, long long M, lo
     }
 }
 
-// The same by TMA, from rows of 128 bytes in shared memory (32 fp32 columns, or 64 bf16 ones: two steps), so that a
-// request to L2 carries four sectors.  (The lanes' own sectors slowed the loads of the next tile: a product
-// of 8192 x 8192 x 8192 took 640 us instead of 572.)  `second`: the right 64 bytes of bf16
-// rows; `go`: the rows are complete.
-template <typename O>
-__device__ __forceinline__ void tma_tile(const CUtensorMap *map, const float (&v)[C], long long m0, long long n0, int s, bool second, bool go,
-                                         const Buffer &b)
-{
-    const int lane = b.lane;
-    if (!second) {
-        if (lane == 0) bulk_wait_read();  // the last tile has left the buffer
-        __syncwarp();
-    }
-    const int first = sizeof(O) == 2 && second ? 4 : 0;
-#pragma unroll
-    for (int k = 0; k < (int)(2 * sizeof(O)); k++) {
-        uint4 w;
-        if constexpr (sizeof(O) == 2)
-            w = make_uint4(pack2(v[8 * k], v[8 * k + 1]), pack2(v[8 * k + 2], v[8 * k + 3]), pack2(v[8 * k + 4], v[8 * k + 5]),
-                           pack2(v[8 * k + 6], v[8 * k + 7]));
-        else
-            w = make_uint4(__float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]), __float_as_uint(v[4 * k + 2]), __float_as_uint(v[4 * k + 3]));
-        *reinterpret_cast<uint4 *>(b.p + lane * 128 + (((first + k) ^ (lane & 7)) << 4)) = w;
-    }
-    if (!go) return;
-    fence_proxy_async();
-    __syncwarp();
-    if (lane == 0) {
-        tma_store_3d(map, b.p, (int)n0 - (sizeof(O) == 2 && second ? C : 0), (int)m0, s);
-        bulk_commit();
-    }
-}
-
 // A step's bias, asked for with the residual.  (Loaded where it is added, behind a question for each four columns, it
 // cost 50 us of a product of 8192 x 8192 x 512 that takes 51 without.)
 struct Bias {
@@ -351,160 +235,25 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                  const __grid_constant__ CUtensorMap map_half, const __grid_constant__ CUtensorMap map_out, const Args a)
 {
     using Z = Cfg<CG, BN, P, EW>;
-    constexpr int S = Z::STAGES;
     constexpr int CHUNK = !EXACT ? 0x40000000 : P == 3 ? 1 : CHUNK_1;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = smem_align1024(smem_raw);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Z::MISC);
-    uint64_t *full = bars, *empty = bars + S, *t_full = bars + 2 * S, *t_empty = bars + 2 * S + 2, *done = bars + 2 * S + 4;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Z::MISC + 256);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Z::MISC + 264);
-
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
-    const int u0 = blockIdx.x / CG, ustep = gridDim.x / CG;
+    using Pipe = Pipeline<CG, BN, P, EW, CHUNK>;
+    const Pipe p(smem, &g_lin_error, 600);
+    const int warp = p.warp, lane = p.lane;
     chain_start();
-
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < S; i++) {
-            mbar_init(full + i, 1);
-            mbar_init(empty + i, 1);
-        }
-        for (int i = 0; i < 2; i++) {
-            mbar_init(t_full + i, 1);
-            mbar_init(t_empty + i, EW * CG);
-        }
-        mbar_init(done, 1);
-        *abort_flag = 0;
-        init_fence();
-    }
-    if (warp == 1) {
-        if constexpr (CG == 2) tmem_alloc_pair(tmem_slot, Z::TMEM);
-        else tmem_alloc(tmem_slot, Z::TMEM);
-    }
-    fence_before();
-    if constexpr (CG == 2) cluster_sync();
-    else __syncthreads();
-    fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = p.begin();
     chain_wait();
 
     if (warp == 0) {
-        // ---------------------------------------------------------- TMA producer
-        // Few and large copies: with B in two boxes of 64 rows instead of one of 128 the same product took 164 us
-        // instead of 150 (8192 x 8192 x 2048).
-        if (lane == 0) {
-            int st = 0;
-            uint32_t ph = 0;
-            bool wrapped = false;
-            int used = 0;
-            const uint32_t bar0 = CG == 2 ? map_rank(full, 0) : su32(full);  // the barriers are the even CTA's
-            auto load3 = [&](void *to, const CUtensorMap *map, int i, int x, int y, int z) {
-                if constexpr (CG == 2) tma_load_3d_pair(to, map, bar0 + 8 * i, x, y, z);
-                else tma_load_3d(to, map, full + i, x, y, z);
-            };
-            auto load4 = [&](void *to, const CUtensorMap *map, int i, int x, int y, int z, int w) {
-                if constexpr (CG == 2) tma_load_4d_pair(to, map, bar0 + 8 * i, x, y, z, w);
-                else tma_load_4d(to, map, full + i, x, y, z, w);
-            };
-            for (int u = u0; u < a.units; u += ustep) {
-                const Unit x = unit_of<BN>(a, u);
-                const bool half = x.bn != BN;
-                const int am = (x.m * CG + (int)rank) * BM;
-                const int rows_b = x.bn / CG, bn = (int)x.n0 + (int)rank * rows_b;
-                // rows of A that do not exist are not asked for (TMA would send their zeros over the crossbar: 100 MB
-                // instead of 45 for 37 rows against 8192 x 2048 weights); what lies in their place in shared memory
-                // reaches sums of such rows only
-                const bool with_a = am < a.M;
-                const int ctas_a = CG == 2 && (x.m * 2 + 1LL) * BM < a.M ? 2 : 1;
-                const uint32_t bytes = P * (ctas_a * a.rows_a + CG * rows_b) * BK * 2;
-                const CUtensorMap *mb = half ? &map_half : &map_b;
-                for (int it = x.it0; it < x.it1; it++) {
-                    const int k = (TWO ? it >> 1 : it) * BK, plane_a = TWO ? ~it & 1 : 0;
-                    wait_bar(empty + st, ph ^ 1, abort_flag, &g_lin_error, 601);
-                    if (rank == 0) mbar_expect_tx(full + st, bytes);
-#pragma unroll
-                    for (int q = 0; q < P; q++) {
-                        unsigned char *sa = smem + st * Z::STAGE + q * Z::A_BYTES, *sb = smem + st * Z::STAGE + P * Z::A_BYTES + q * Z::B_BYTES;
-                        const int qa = P == 1 ? plane_a : q;
-                        if (!with_a) {
-                        } else if constexpr (A_K) {
-                            load3(sa, &map_a, st, k, am, qa);
-                        } else if (a.blocks_a) {
-                            load4(sa, &map_a, st, 0, k, am >> 6, qa);
-                        } else {
-                            for (int i = 0; i < a.rows_a; i += 64) load3(sa + i * 128, &map_a, st, am + i, k, qa);
-                        }
-                        if constexpr (B_K) {
-                            load3(sb, mb, st, k, bn, q);
-                        } else if (a.blocks_b) {
-                            load4(sb, mb, st, 0, k, bn >> 6, q);
-                        } else {
-                            for (int i = 0; i < rows_b; i += 64) load3(sb + i * 128, mb, st, bn + i, k, q);
-                        }
-                    }
-                    used = max(used, st + 1);
-                    if (++st == S) {
-                        st = 0;
-                        ph ^= 1;
-                        wrapped = true;
-                    }
-                }
-            }
-            // the copies must have landed before the CTAs of the pair exit (the leader's barriers count both CTAs'), and so
-            // must the arrivals that the leader's commits send to this CTA's barriers: its shared memory is another's then
-            for (int i = 0; i < (wrapped ? S : used); i++) {
-                if (rank == 0) drain_bar(full + i, i < st ? ph : ph ^ 1, &g_lin_error);
-                drain_bar(empty + i, i < st ? ph : ph ^ 1, &g_lin_error);
-            }
-        }
+        p.template produce<A_K, B_K, TWO>(map_a, map_b, map_half, a);
     } else if (warp == 1) {
-        // ---------------------------------------------------------- MMA issue (whole warp, the pair's even CTA)
-        if (rank == 0) {
-            int st = 0, tc = 0;
-            uint32_t ph = 0;
-            for (int u = u0; u < a.units; u += ustep) {
-                const Unit x = unit_of<BN>(a, u);
-                const uint32_t idesc = x.bn == BN ? idesc_bf16(BM * CG, BN, !A_K, !B_K) : idesc_bf16(BM * CG, BN / 2, !A_K, !B_K);
-                for (int it0 = x.it0; it0 < x.it1; it0 += min(CHUNK, x.it1 - it0)) {
-                    const int it1 = min(CHUNK, x.it1 - it0) + it0, tb = tc & 1;
-                    wait_bar(t_empty + tb, ((tc >> 1) & 1) ^ 1, abort_flag, &g_lin_error, 602);
-                    fence_after();
-                    const uint32_t d = tmem + (uint32_t)(tb * BN);
-                    for (int it = it0; it < it1; it++) {
-                        wait_bar(full + st, ph, abort_flag, &g_lin_error, 603);
-                        fence_after();
-                        const unsigned char *sa = smem + st * Z::STAGE, *sb = sa + P * Z::A_BYTES;
-                        constexpr int PRODUCTS = P == 1 ? 1 : 6;
-#pragma unroll
-                        for (int i = 0; i < PRODUCTS; i++) {
-                            constexpr int PA[6] = {2, 0, 1, 1, 0, 0}, PB[6] = {0, 2, 1, 0, 1, 0};
-                            const unsigned char *pa = sa + (P == 1 ? 0 : PA[i]) * Z::A_BYTES, *pb = sb + (P == 1 ? 0 : PB[i]) * Z::B_BYTES;
-                            // along k (16 values): 32 bytes of a k-major row, 16 rows of 128 bytes of an m/n-major tile
-                            const uint64_t da = A_K ? desc_kmajor(pa) : desc_sw128(pa, 8192, 1024);
-                            const uint64_t db = B_K ? desc_kmajor(pb) : desc_sw128(pb, 8192, 1024);
-                            const uint32_t acc = i > 0 || it != it0, bar = i == PRODUCTS - 1 ? su32(empty + st) : 0u;
-                            if constexpr (CG == 2) mma4_ss_pair_w(d, da, A_K ? 2 : 128, db, B_K ? 2 : 128, idesc, acc, bar);
-                            else mma4_ss_w(d, da, A_K ? 2 : 128, db, B_K ? 2 : 128, idesc, acc, bar);
-                        }
-                        if (++st == S) {
-                            st = 0;
-                            ph ^= 1;
-                        }
-                    }
-                    if constexpr (CG == 2) mma_commit_pair_w(t_full + tb);
-                    else mma_commit_w(t_full + tb);
-                    tc++;
-                }
-            }
-            if constexpr (CG == 2) mma_commit_pair_w(done);
-            else mma_commit_w(done);
-        }
-        drain_bar(done, 0, &g_lin_error);  // in either CTA: the commit arrives in both
+        p.template issue<A_K, B_K>(tmem, a);
     } else {
         // ---------------------------------------------------------- epilogue (8 or 16 warps)
         const int quad = warp & 3;               // TMEM lanes this warp may access
         const int side = (warp - 2) >> 2;        // part of the columns
+        const uint32_t rank = p.rank;
         const Buffer b = {smem + Z::TURN + (warp - 2) * 4096, lane};
         // asked once: each of these questions cost a step a miss in the constant and instruction caches
         const bool tma = a.tma_out != 0, with_res = a.e.res != nullptr, with_bias = a.e.bias != nullptr, with_act = a.e.act != CSA_ACT_NONE || a.e.preact != nullptr;
@@ -512,21 +261,12 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         auto run = [&](auto type) {
             using O = decltype(type);
             int tc = 0;
-            for (int u = u0; u < a.units; u += ustep) {
+            for (int u = p.u0; u < a.units; u += p.ustep) {
                 const Unit x = unit_of<BN>(a, u);
                 const int cols = x.bn / (EW / 4);
                 const long long m0 = ((long long)x.m * CG + rank) * BM + quad * 32, nb = x.n0 + side * cols;
-                const auto release = [&](int tb) {  // the accumulator is in registers: the next MMAs may have it
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (CG == 2) mbar_arrive_cluster(map_rank(t_empty + tb, 0));
-                        else mbar_arrive(t_empty + tb);
-                    }
-                };
                 const auto wait = [&] {
-                    wait_bar(t_full + (tc & 1), (tc >> 1) & 1, abort_flag, &g_lin_error, 604);
-                    fence_after();
+                    p.wait_sums(tc);
                     return tmem + (uint32_t)((tc & 1) * BN + side * cols) + ((uint32_t)(quad * 32) << 16);
                 };
                 const bool early = with_res && a.res32 && nb + cols <= a.N;
@@ -565,7 +305,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                         for (int g = 0; g < G; g++) {
                             float v[C];
                             tmem_ld32(t + g * C, v);
-                            if (g == G - 1) release(tc & 1);
+                            if (g == G - 1) p.release_sums(tc);
 #pragma unroll
                             for (int k = 0; k < C; k++) sum[g][k] += v[k];
                         }
@@ -580,7 +320,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                     for (int c = 0; c < cols; c += C) {
                         float v[C];
                         tmem_ld32(t + c, v);
-                        if (c + C == cols) release(tc & 1);
+                        if (c + C == cols) p.release_sums(tc);
                         step(c, v);
                     }
                     tc++;
@@ -595,25 +335,10 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         }
         if (lane == 0) bulk_wait();
     }
-    __syncwarp();
-    fence_before();
-    if constexpr (CG == 2) cluster_sync();
-    else __syncthreads();
-    fence_after();
-    if (warp == 1) {
-        if constexpr (CG == 2) tmem_dealloc_pair(tmem, Z::TMEM);
-        else tmem_dealloc(tmem, Z::TMEM);
-    }
+    p.end(tmem);
 }
 
 // ------------------------------------------------------------------ host side
-
-static void tile_counts(Shape s, long long M, long long N, int &mt, int &nt)
-{
-    const int bm = s == LONE_64 ? 128 : 256, bn = s == LONE_64 ? 64 : s == PAIR_128 ? 128 : 256;
-    mt = (int)((M + bm - 1) / bm);
-    nt = (int)((N + bn - 1) / bn);
-}
 
 // Tile and cut of the k axis by estimated time, of which this is the model (fitted to the timings of 20 products, from
 // 37 x 2048 x 8192 to 2048^3 and 64 x 512 x 16384, with every tile and several cuts: its choice takes at most 15% more
@@ -657,10 +382,6 @@ Plan plan_product(long long M, long long N, long long K, int planes, int passes,
     return best;
 }
 
-struct Maps {
-    CUtensorMap a, b, half, out;
-};
-
 template <int CG, int BN, int P, int EW, bool EXACT, bool A_K, bool B_K, bool TWO = false>
 static cudaError_t launch(const Maps &m, const Args &a, int sms, cudaStream_t st)
 {
@@ -697,33 +418,6 @@ static cudaError_t launch_planes(const Product &p, const Maps &m, const Args &a,
         if (a.many) return launch_majors<CG, BN, 1, 16, false>(p, m, a, sms, st);
     }
     return launch_majors<CG, BN, 1, 8, false>(p, m, a, sms, st);
-}
-
-// Boxes of `rows` m or n indices and 64 values of k of an operand with `n` of them.  {contiguous, strided, plane}; an
-// m/n-contiguous operand of whole 64-wide blocks has these as an axis of their own (one copy then brings several).
-static bool encode(CUtensorMap *m, const Operand &o, long long n, long long K, int planes, int rows, bool blocks)
-{
-    const long long inner = o.k_major ? K : n, outer = o.k_major ? n : K;
-    // one plane: its stride is never used, but has to be a legal one (below 2^40 bytes)
-    const long long far = 1LL << 38, whole = outer > far / o.ld ? far : outer * o.ld;
-    const cuuint64_t ld = (cuuint64_t)o.ld * 2, plane = (cuuint64_t)(planes > 1 ? o.plane : whole) * 2;
-    if (blocks) {
-        const cuuint64_t dims[4] = {64, (cuuint64_t)K, (cuuint64_t)(n / 64), (cuuint64_t)planes}, strides[3] = {ld, 128, plane};
-        const cuuint32_t box[4] = {64, 64, (cuuint32_t)(rows / 64), 1};
-        return tc_encode_bf16(m, o.base, 4, dims, strides, box);
-    }
-    const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)outer, (cuuint64_t)planes}, strides[2] = {ld, plane};
-    const cuuint32_t box[3] = {64, (cuuint32_t)(o.k_major ? rows : 64), 1};
-    return tc_encode_bf16(m, o.base, 3, dims, strides, box);
-}
-
-// An output of M rows of n values, `ld` apart, z of them.
-static bool encode_out(CUtensorMap *m, bool f32, const void *base, long long n, long long ld, long long M, int z)
-{
-    const long long size = f32 ? 4 : 2;
-    const cuuint64_t dims[3] = {(cuuint64_t)n, (cuuint64_t)M, (cuuint64_t)z};
-    const cuuint64_t strides[2] = {(cuuint64_t)(ld * size), (cuuint64_t)(M * ld * size)};
-    return tc_encode_store(m, f32, base, dims, strides);
 }
 
 cudaError_t launch_product_tc(const Product &p, int sms, cudaStream_t st)
