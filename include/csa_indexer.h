@@ -353,6 +353,39 @@ typedef struct {
  * m, v or scale are refused; buffers that overlap in any other way are the caller's error. */
 csa_status csa_adamw(const csa_adamw_params *p, const csa_adamw_tensor *tensors, int32_t count, void *stream);
 
+/* ------------------------------------------------------------------ layer norm */
+
+/* The norm of rows: of the indexer's keys between their projection and their rotation, of hidden states before the
+ * vocabulary's weight.  Conventions as above. */
+typedef struct {
+    int32_t dtype;          /* csa_dtype of x, y, dy and dx */
+    int32_t param_dtype;    /* csa_dtype of weight, bias and their gradients */
+    int32_t cols;           /* >= 1 */
+    float eps;              /* >= 0 */
+    int64_t rows;           /* >= 0 */
+    int64_t x_stride;       /* elements from one row of x to the next; 0: cols.  At least cols */
+    int64_t dy_stride;      /* the same for dy */
+} csa_layernorm_params;
+
+/* Bytes of device workspace the backward needs (the forward needs none).  0 on invalid params. */
+size_t csa_layernorm_bwd_workspace_size(const csa_layernorm_params *p);
+
+/* mean = sum_j x_j / cols,  rstd = 1 / sqrt(sum_j (x_j - mean)^2 / cols + eps),  y_j = (x_j - mean) rstd weight_j + bias_j
+ *   x [rows, cols], weight [cols] or NULL (ones), bias [cols] or NULL (zeros)
+ *   -> y [rows, cols] contiguous, stats [2, rows] fp32 or NULL: the rows' means, then their rstd, which the backward reads.
+ * Sums are fp32 over the row's values themselves (the variance over their differences from the mean).  y may be x where
+ * x_stride is cols. */
+csa_status csa_layernorm_fwd(const csa_layernorm_params *p, const void *x, const void *weight, const void *bias, void *y,
+                             float *stats, void *stream);
+
+/* The gradients for dy, with h_j = (x_j - mean) rstd and a_j = dy_j weight_j:
+ *   dx_j = rstd (a_j - mean(a) - h_j mean(a h)) [rows, cols],  dweight = sum over rows of dy_j h_j [cols],  dbias = sum of dy_j
+ * Each of dx, dweight, dbias may be NULL and is then not computed.  dx may be dy or x where its stride is cols.  rows = 0
+ * gives dweight = 0 and dbias = 0.  The same call gives the same bits every time (no atomics). */
+csa_status csa_layernorm_bwd(const csa_layernorm_params *p, const void *dy, const void *x, const void *weight,
+                             const float *stats, void *dx, void *dweight, void *dbias, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
 /* ------------------------------------------------------------------ diagnostics */
 
 /* Test aid: the fp32 scores exactly as csa_indexer_fwd computes them, for rows

@@ -16,8 +16,11 @@ Around the step (what makes q_idx, w and k_idx out of hidden states, and updates
     csa_linear_bwd(params, dy, x, weight[, preact])                 -> (dx, dw, db)
     csa_rope(params, x, positions, inv_freq)                        -> out          (rotary positions; also their gradient)
     csa_adamw(tensors, step, ...)                                                   (AdamW over many tensors, in place)
+    csa_layernorm_fwd(params, x[, weight, bias])                    -> y            (the norm of rows)
+    csa_layernorm_bwd(params, dy, x, weight, stats)                 -> (dx, dweight, dbias)
 
-with ``CSALinear`` / ``csa_linear`` and ``CSARope`` / ``csa_rotary`` as their autograd forms.  ``CSAIndexerLoss`` wraps
+with ``CSALinear`` / ``csa_linear``, ``CSARope`` / ``csa_rotary`` and ``CSALayerNorm`` / ``csa_layernorm`` as their autograd
+forms.  ``CSAIndexerLoss`` wraps
 the step as an autograd function (forward returns ids and the loss; backward returns the stored indexer gradients
 scaled by the incoming gradient).
 
@@ -98,6 +101,13 @@ class csa_rope_params(ctypes.Structure):
     ]
 
 
+class csa_layernorm_params(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32), ("cols", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("rows", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("dy_stride", ctypes.c_int64),
+    ]
+
+
 class csa_adamw_tensor(ctypes.Structure):
     _fields_ = [
         ("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("master", ctypes.c_void_p), ("m", ctypes.c_void_p),
@@ -117,6 +127,7 @@ class csa_adamw_params(ctypes.Structure):
 
 _P = ctypes.POINTER(csa_params)
 _PL, _PR, _PA = (ctypes.POINTER(t) for t in (csa_linear_params, csa_rope_params, csa_adamw_params))
+_PN = ctypes.POINTER(csa_layernorm_params)
 _vp, _sz, _i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int64
 for _name, _args, _res in [
     ("csa_topk_width", [_P], ctypes.c_int32),
@@ -140,6 +151,9 @@ for _name, _args, _res in [
     ("csa_linear_bwd", [_PL, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
     ("csa_rope", [_PR, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
     ("csa_adamw", [_PA, _vp, ctypes.c_int32, _vp], ctypes.c_int),
+    ("csa_layernorm_bwd_workspace_size", [_PN], ctypes.c_size_t),
+    ("csa_layernorm_fwd", [_PN, _vp, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
+    ("csa_layernorm_bwd", [_PN, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
     ("csa_check_device_status", [_vp], ctypes.c_int),
     ("csa_selftest_bounded_wait", [_vp], ctypes.c_int),
     ("csa_last_timeout_site", [], ctypes.c_int32),
@@ -158,6 +172,7 @@ EXPORTED = ("csa_topk_width", "csa_key_width", "csa_teacher_width", "csa_rows", 
             "csa_indexer_bwd_noalloc",
             "csa_linear_fwd_workspace_size", "csa_linear_bwd_workspace_size", "csa_linear_fwd", "csa_linear_bwd",
             "csa_rope", "csa_adamw",
+            "csa_layernorm_bwd_workspace_size", "csa_layernorm_fwd", "csa_layernorm_bwd",
             "csa_check_device_status", "csa_selftest_bounded_wait", "csa_last_timeout_site", "csa_last_path",
             "csa_last_cuda_error",
             "csa_kernel_launches",
@@ -736,6 +751,83 @@ def csa_rope(p: RopeParams, x, positions, inv_freq, out=None):
     return out
 
 
+class LayerNormParams:
+    """The norm of rows of `cols` values (the C struct csa_layernorm_params).  param_dtype is that of weight, bias and their
+    gradients.  Strides are elements from row to row, 0 for contiguous rows."""
+
+    def __init__(self, rows, cols, dtype="bf16", param_dtype="f32", eps=1e-5, x_stride=0, dy_stride=0):
+        self.c = csa_layernorm_params(_dtype(dtype), _dtype(param_dtype), int(cols), float(eps), int(rows), int(x_stride),
+                                      int(dy_stride))
+        self.ref = ctypes.byref(self.c)
+        self.value_dtype, self.param_value_dtype = TORCH_DTYPE[self.c.dtype], TORCH_DTYPE[self.c.param_dtype]
+
+    @property
+    def bwd_workspace_bytes(self) -> int:
+        return _lib.csa_layernorm_bwd_workspace_size(self.ref)
+
+
+def csa_layernorm_fwd(p: LayerNormParams, x, weight=None, bias=None, out=None, stats=None):
+    """y = (x - mean) rstd weight + bias of each row of x [rows, cols] (weight None: ones, bias None: zeros).  Returns y.
+    stats (a [2, rows] fp32 tensor) receives the rows' means and rstd, which csa_layernorm_bwd reads.  out may be x itself
+    (contiguous)."""
+    c, dev = p.c, _on_cuda(x, "x")
+    M, N = c.rows, c.cols
+    _check_rows(x, "x", p.value_dtype, dev, M, N, c.x_stride)
+    if weight is not None:
+        _check_flat(weight, "weight", p.param_value_dtype, dev, N)
+    if bias is not None:
+        _check_flat(bias, "bias", p.param_value_dtype, dev, N)
+    given = out is not None
+    if not given:
+        out = _empty((M, N), (N, 1), p.value_dtype, dev)
+    else:
+        _check_flat(out, "out", p.value_dtype, dev, M * N)
+    if stats is not None:
+        _check_flat(stats, "stats", torch.float32, dev, 2 * M)
+    _invoke("csa_layernorm_fwd", _lib.csa_layernorm_fwd, dev, p.ref, x.data_ptr(), _ptr(weight), _ptr(bias), out.data_ptr(),
+            _ptr(stats))
+    if given:
+        _changed(out)
+    if stats is not None:
+        _changed(stats)
+    return out
+
+
+def csa_layernorm_bwd(p: LayerNormParams, dy, x, weight=None, stats=None, need_dx=True, need_dweight=True, need_dbias=True,
+                      workspace=None, out=None):
+    """The gradients of csa_layernorm_fwd for dy: (dx [rows, cols], dweight [cols], dbias [cols]), None in the place of one
+    that is not asked for.  stats is what the forward wrote there.  out: a tuple of the three to write to; dx may be dy or x
+    (contiguous)."""
+    c, dev = p.c, _on_cuda(dy, "dy")
+    M, N = c.rows, c.cols
+    _check_rows(dy, "dy", p.value_dtype, dev, M, N, c.dy_stride)
+    if need_dx or need_dweight:
+        _check_rows(x, "x", p.value_dtype, dev, M, N, c.x_stride)
+        _check_flat(stats, "stats", torch.float32, dev, 2 * M)
+    if weight is not None:
+        _check_flat(weight, "weight", p.param_value_dtype, dev, N)
+
+    def output(i, name, need, shape, strides, dtype):
+        if not need:
+            return None
+        if out is None or out[i] is None:
+            return _empty(shape, strides, dtype, dev)
+        _check_flat(out[i], name, dtype, dev, M * N if i == 0 else N)
+        return out[i]
+
+    dx = output(0, "dx", need_dx, (M, N), (N, 1), p.value_dtype)
+    dw = output(1, "dweight", need_dweight, (N,), (1,), p.param_value_dtype)
+    db = output(2, "dbias", need_dbias, (N,), (1,), p.param_value_dtype)
+    if workspace is None:
+        workspace = _empty((p.bwd_workspace_bytes,), (1,), torch.uint8, dev)
+    ws, nws = _check_workspace(workspace, dev)
+    _invoke("csa_layernorm_bwd", _lib.csa_layernorm_bwd, dev, p.ref, dy.data_ptr(), _ptr(x), _ptr(weight), _ptr(stats), _ptr(dx),
+            _ptr(dw), _ptr(db), ws, nws)
+    if out is not None:
+        _changed([t for t in (dx, dw, db) if t is not None])
+    return dx, dw, db
+
+
 class AdamWTensors:
     """The tensors of csa_adamw, checked and laid out once.  Lists of equal length: param (f32 or bf16), grad (f32 or
     bf16), the moments m and v (both f32, or both float8_e4m3fn with their f32 scales m_scale and v_scale, one per
@@ -921,3 +1013,31 @@ class CSARope(torch.autograd.Function):
 
 def csa_rotary(x, positions, inv_freq, params: RopeParams):
     return CSARope.apply(x, positions, inv_freq, params)
+
+
+class CSALayerNorm(torch.autograd.Function):
+    """y = CSALayerNorm.apply(x, weight, bias, params): gradients flow to all three tensors (weight and bias may be None)."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, params):
+        stats = torch.empty((2, params.c.rows), dtype=torch.float32, device=x.device) if any(ctx.needs_input_grad[:3]) else None
+        y = csa_layernorm_fwd(params, x, weight, bias, stats=stats)
+        ctx.params, ctx.x_shape = params, x.shape
+        ctx.shapes = [t.shape if t is not None else None for t in (weight, bias)]
+        ctx.save_for_backward(x, weight, stats)
+        return y.view(x.shape)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, weight, stats = ctx.saved_tensors
+        p, need = ctx.params, ctx.needs_input_grad
+        c = p.c
+        if c.dy_stride:  # autograd hands contiguous gradients over
+            p = LayerNormParams(c.rows, c.cols, c.dtype, c.param_dtype, c.eps, c.x_stride)
+        grads = csa_layernorm_bwd(p, _own(dy), x, weight, stats, need[0], need[1], need[2])
+        return (*(g.view(shape) if g is not None else None for g, shape in zip(grads, (ctx.x_shape, *ctx.shapes))), None)
+
+
+def csa_layernorm(x, weight=None, bias=None, *, params: LayerNormParams):
+    return CSALayerNorm.apply(x, weight, bias, params)

@@ -225,6 +225,11 @@ cudaError_t launch_linear_bwd(const csa_linear_params &p, const void *dy, const 
 cudaError_t launch_rope(const csa_rope_params &p, const void *x, const void *positions, const double *inv_freq,
                         void *out, cudaStream_t st);
 cudaError_t launch_adamw(const csa_adamw_params &p, const csa_adamw_tensor *t, int count, cudaStream_t st);
+size_t layernorm_bwd_workspace(const csa_layernorm_params &p);
+cudaError_t launch_layernorm_fwd(const csa_layernorm_params &p, const void *x, const void *weight, const void *bias, void *y,
+                                 float *stats, cudaStream_t st);
+cudaError_t launch_layernorm_bwd(const csa_layernorm_params &p, const void *dy, const void *x, const void *weight,
+                                 const float *stats, void *dx, void *dweight, void *dbias, void *ws, cudaStream_t st);
 
 // ---------------------------------------------------------------- launchers (k_generic.cu)
 

@@ -1,4 +1,4 @@
-// csa_ops_abi.cu -- the entry points around the step (projections, rotary positions, AdamW): argument checks and
+// csa_ops_abi.cu -- the entry points around the step (projections, rotary positions, AdamW, layer norm): argument checks and
 // dispatch.  Everything is checked on the host before anything is enqueued; no device memory is allocated and the
 // stream is never synchronised.
 #include "csa_internal.cuh"
@@ -70,6 +70,23 @@ bool shares(const void *out, const void *const *others, int n)
     for (int i = 0; i < n; i++)
         if (others[i] == out) return true;
     return false;
+}
+
+// ------------------------------------------------------------------ layer norm
+
+csa_status check_layernorm(const csa_layernorm_params *p, csa_layernorm_params *q)
+{
+    if (p == nullptr) return CSA_ERR_INVALID_ARG;
+    *q = *p;
+    if (!value_dtype(p->dtype) || !value_dtype(p->param_dtype)) return CSA_ERR_INVALID_ARG;
+    if (p->cols < 1 || p->rows < 0 || !(p->eps >= 0) || !isfinite(p->eps)) return CSA_ERR_INVALID_ARG;
+    if (q->x_stride == 0) q->x_stride = p->cols;
+    if (q->dy_stride == 0) q->dy_stride = p->cols;
+    if (q->x_stride < p->cols || q->dy_stride < p->cols) return CSA_ERR_INVALID_ARG;
+    constexpr int most = 0x7fff0000;  // 32-bit loop counters, which run up to 16384 beyond it
+    const long long far = 1LL << 36;
+    if (p->rows > most || p->cols > most || q->x_stride > far || q->dy_stride > far) return CSA_ERR_UNSUPPORTED;
+    return CSA_OK;
 }
 
 // ------------------------------------------------------------------ rotary positions
@@ -256,6 +273,59 @@ csa_status csa_rope(const csa_rope_params *p, const void *x, const void *positio
     if (x == out && (q.x_row_stride != q.out_row_stride || q.x_head_stride != q.out_head_stride)) return CSA_ERR_INVALID_ARG;
     if (q.rows == 0) return CSA_OK;
     CSA_CUDA(launch_rope(q, x, positions, inv_freq, out, static_cast<cudaStream_t>(stream)));
+    return CSA_OK;
+}
+
+size_t csa_layernorm_bwd_workspace_size(const csa_layernorm_params *p)
+{
+    csa_layernorm_params q;
+    return check_layernorm(p, &q) == CSA_OK ? layernorm_bwd_workspace(q) : 0;
+}
+
+csa_status csa_layernorm_fwd(const csa_layernorm_params *p, const void *x, const void *weight, const void *bias, void *y,
+                             float *stats, void *stream)
+{
+    CSA_TRY(injected_fault());
+    csa_layernorm_params q;
+    CSA_TRY(check_layernorm(p, &q));
+    CSA_TRY(need(x, q.rows));
+    CSA_TRY(need_opt(weight));
+    CSA_TRY(need_opt(bias));
+    CSA_TRY(need(y, q.rows));
+    CSA_TRY(need_scalar(stats, 4));
+    if (q.rows == 0) return CSA_OK;
+    if (x == y && q.x_stride != q.cols && q.rows > 1) return CSA_ERR_INVALID_ARG;
+    const void *inputs[] = {weight, bias, y, x};
+    if (shares(y, inputs, 2) || shares(stats, inputs, 4)) return CSA_ERR_INVALID_ARG;
+    CSA_CUDA(launch_layernorm_fwd(q, x, weight, bias, y, stats, static_cast<cudaStream_t>(stream)));
+    return CSA_OK;
+}
+
+csa_status csa_layernorm_bwd(const csa_layernorm_params *p, const void *dy, const void *x, const void *weight,
+                             const float *stats, void *dx, void *dweight, void *dbias, void *workspace,
+                             size_t workspace_bytes, void *stream)
+{
+    CSA_TRY(injected_fault());
+    csa_layernorm_params q;
+    CSA_TRY(check_layernorm(p, &q));
+    CSA_TRY(need(dy, q.rows));
+    if (dx != nullptr || dweight != nullptr) {
+        CSA_TRY(need(x, q.rows));
+        if (q.rows > 0 && stats == nullptr) return CSA_ERR_INVALID_ARG;
+        CSA_TRY(need_scalar(stats, 4));
+    }
+    CSA_TRY(need_opt(weight));
+    CSA_TRY(need_opt(dx));
+    CSA_TRY(need_opt(dweight));
+    CSA_TRY(need_opt(dbias));
+    const size_t ws = layernorm_bwd_workspace(q);
+    if (workspace_bytes < ws || (ws > 0 && workspace == nullptr)) return CSA_ERR_WORKSPACE;
+    CSA_TRY(need_opt(workspace));
+    if (q.rows > 1 && dx != nullptr && ((dx == dy && q.dy_stride != q.cols) || (dx == x && q.x_stride != q.cols)))
+        return CSA_ERR_INVALID_ARG;
+    const void *inputs[] = {weight, stats, q.rows > 0 ? dy : nullptr, q.rows > 0 ? x : nullptr, dx, dweight};
+    if (shares(dx, inputs, 2) || shares(dweight, inputs, 5) || shares(dbias, inputs, 6)) return CSA_ERR_INVALID_ARG;
+    CSA_CUDA(launch_layernorm_bwd(q, dy, x, weight, stats, dx, dweight, dbias, workspace, static_cast<cudaStream_t>(stream)));
     return CSA_OK;
 }
 
