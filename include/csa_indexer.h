@@ -386,6 +386,64 @@ csa_status csa_layernorm_bwd(const csa_layernorm_params *p, const void *dy, cons
                              const float *stats, void *dx, void *dweight, void *dbias, void *workspace,
                              size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------ losses of a vocabulary */
+
+/* The model's own loss beside the indexer's: softmax cross entropy with labels, and distillation from the largest logits of
+ * a teacher (the dense model of a sparse one), of hidden states x and the vocabulary's weight.  The scores x weight^T are
+ * never kept as a whole.  Conventions as above.
+ *   z = alpha x weight^T [rows, vocab];  lse_r = log sum_v exp z_rv
+ *   label v of row r:     L_r = lse_r - z_rv; a row whose label is negative has none
+ *   teacher of row r:     candidates v_s with logits l_s, s < slots; t_s = exp(l_s - N_r) with N_r the teacher's own log-sum-exp
+ *                         (teacher_lse), or log sum_s exp l_s without it;  L_r = sum_s t_s (log t_s - z_{r, v_s} + lse_r), of
+ *                         the candidates alone: what the teacher gives to other columns is in neither sum.  A slot with a negative id holds
+ *                         none, one with the logit -inf has t = 0; a row without candidates has no teacher.  Columns that a row names
+ *                         twice count twice.
+ *   loss = label_weight sum L / n + teacher_weight sum L / n, n the rows that have a label, or a teacher (at least 1), or 1
+ * An id of vocab or more, of a label or a candidate, makes the row's loss, the loss and the gradients NaN; nothing is read
+ * or written there. */
+typedef struct {
+    int32_t dtype;              /* csa_dtype of x, weight, dx and dw */
+    int32_t features, vocab;    /* >= 1 */
+    int32_t slots;              /* candidates of a row, at most 1024; 0: no teacher */
+    int32_t labels_64, ids_64;  /* 0: labels (teacher_ids) are int32, 1: int64 */
+    int32_t reduction;          /* 0: n as above (mean).  1: n = 1 (sum) */
+    float alpha;                /* scales the scores (1 / temperature); finite, not 0 */
+    float label_weight, teacher_weight;   /* finite, >= 0 */
+    int64_t rows;               /* >= 0 */
+    int64_t x_stride;           /* elements from one row of x to the next; 0: features.  At least features */
+    int64_t piece_rows;         /* rows whose scores are held at a time; 0: as many as 4 GiB hold (at least 256) */
+} csa_vocab_loss_params;
+
+/* Device pointers.  labels or the teacher's (or both) must be given; without slots the teacher's are NULL. */
+typedef struct {
+    const void *labels;            /* [rows] or NULL */
+    const void *teacher_ids;       /* [rows, slots] or NULL */
+    const float *teacher_logits;   /* [rows, slots] or NULL */
+    const float *teacher_lse;      /* [rows] or NULL */
+} csa_vocab_targets;
+
+/* Bytes of device workspace a call needs.  0 on invalid params. */
+size_t csa_vocab_loss_fwd_workspace_size(const csa_vocab_loss_params *p);
+size_t csa_vocab_loss_bwd_workspace_size(const csa_vocab_loss_params *p);
+
+/*   x [rows, features], weight [vocab, features] contiguous -> loss_out, one device fp32; row_loss_out [2, rows] fp32 or
+ *   NULL: the rows' unweighted label losses, then their teacher losses (0 for a row without).
+ * Scores are sums in fp32 (fp32 values as three bf16 parts each); sums leave the tensor core every 512 k (fp32 values: every
+ * 64) and are added up rounded. */
+csa_status csa_vocab_loss_fwd(const csa_vocab_loss_params *p, const void *x, const void *weight,
+                              const csa_vocab_targets *targets, float *loss_out, float *row_loss_out, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* The same, and the gradients of the loss (not of its parts), dz_rv = c_r softmax(z_r)_v - tau_rv with tau the weights of the
+ * row's targets in the loss and c_r their sum:  dx = alpha dz weight [rows, features],  dw = alpha dz^T x [vocab, features].
+ * Each of dx and dw may be NULL and is then not computed.  With bf16 values the exponentials are held in fp16 relative to the
+ * largest of their 64 columns, and dz is rounded to bf16 before the two products; the columns that targets name come from their fp32
+ * scores.  A row whose targets weigh nothing passes no gradient, whatever its scores are.  rows = 0 gives loss = 0 and dw = 0.
+ * The same call gives the same bits every time (no atomics). */
+csa_status csa_vocab_loss_bwd(const csa_vocab_loss_params *p, const void *x, const void *weight,
+                              const csa_vocab_targets *targets, float *loss_out, float *row_loss_out, void *dx, void *dw,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
 /* ------------------------------------------------------------------ diagnostics */
 
 /* Test aid: the fp32 scores exactly as csa_indexer_fwd computes them, for rows
@@ -408,7 +466,7 @@ csa_status csa_selftest_bounded_wait(void *stream);
 
 /* Where the last timeout that csa_check_device_status reported on this host thread happened, as
  * 100 x kernel + wait site: kernel 1 the score / top-k kernel, 2 the backward, 3 the 64-head teacher, 4 the
- * 128-head teacher, 5 the gathered row-owner backward, 6 the projections, 9 the bounded-wait self-test; site 99 is a drain of the
+ * 128-head teacher, 5 the gathered row-owner backward, 6 the projections, 7 the vocabulary's scores, 9 the bounded-wait self-test; site 99 is a drain of the
  * kernel's own copies that ran out after an abort.  0 before the first timeout; not cleared by later calls. */
 int32_t csa_last_timeout_site(void);
 

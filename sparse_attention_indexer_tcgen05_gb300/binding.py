@@ -17,12 +17,17 @@ Around the step (what makes q_idx, w and k_idx out of hidden states, and updates
     csa_rope(params, x, positions, inv_freq)                        -> out          (rotary positions; also their gradient)
     csa_adamw(tensors, step, ...)                                                   (AdamW over many tensors, in place)
     csa_layernorm_fwd(params, x[, weight, bias])                    -> y            (the norm of rows)
+    csa_layernorm_fwd(params, x[, weight, bias])                    -> y            (the norm of rows)
     csa_layernorm_bwd(params, dy, x, weight, stats)                 -> (dx, dweight, dbias)
 
-with ``CSALinear`` / ``csa_linear``, ``CSARope`` / ``csa_rotary`` and ``CSALayerNorm`` / ``csa_layernorm`` as their autograd
-forms.  ``CSAIndexerLoss`` wraps
-the step as an autograd function (forward returns ids and the loss; backward returns the stored indexer gradients
-scaled by the incoming gradient).
+The model's own loss (labels, a teacher's top logits, or both; scores of a vocabulary that are never kept):
+
+    csa_vocab_loss_fwd(params, x, weight[, labels, teacher_ids, teacher_logits, teacher_lse])   -> loss
+    csa_vocab_loss_bwd(params, x, weight[, ...])                                                -> (loss, dx, dw)
+
+with ``CSALinear`` / ``csa_linear``, ``CSARope`` / ``csa_rotary``, ``CSALayerNorm`` / ``csa_layernorm`` and ``CSAVocabLoss`` /
+``csa_vocab_loss`` as their autograd forms.  ``CSAIndexerLoss`` wraps the step as an autograd function (forward returns ids and
+the loss; backward returns the stored indexer gradients scaled by the incoming gradient).
 
 Importing this module loads the library and raises ImportError if it has not been built: there is no
 fallback implementation.
@@ -108,6 +113,22 @@ class csa_layernorm_params(ctypes.Structure):
     ]
 
 
+class csa_vocab_loss_params(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("features", ctypes.c_int32), ("vocab", ctypes.c_int32), ("slots", ctypes.c_int32),
+        ("labels_64", ctypes.c_int32), ("ids_64", ctypes.c_int32), ("reduction", ctypes.c_int32), ("alpha", ctypes.c_float),
+        ("label_weight", ctypes.c_float), ("teacher_weight", ctypes.c_float), ("rows", ctypes.c_int64),
+        ("x_stride", ctypes.c_int64), ("piece_rows", ctypes.c_int64),
+    ]
+
+
+class csa_vocab_targets(ctypes.Structure):
+    _fields_ = [
+        ("labels", ctypes.c_void_p), ("teacher_ids", ctypes.c_void_p), ("teacher_logits", ctypes.c_void_p),
+        ("teacher_lse", ctypes.c_void_p),
+    ]
+
+
 class csa_adamw_tensor(ctypes.Structure):
     _fields_ = [
         ("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("master", ctypes.c_void_p), ("m", ctypes.c_void_p),
@@ -127,7 +148,7 @@ class csa_adamw_params(ctypes.Structure):
 
 _P = ctypes.POINTER(csa_params)
 _PL, _PR, _PA = (ctypes.POINTER(t) for t in (csa_linear_params, csa_rope_params, csa_adamw_params))
-_PN = ctypes.POINTER(csa_layernorm_params)
+_PN, _PV, _PT = (ctypes.POINTER(t) for t in (csa_layernorm_params, csa_vocab_loss_params, csa_vocab_targets))
 _vp, _sz, _i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int64
 for _name, _args, _res in [
     ("csa_topk_width", [_P], ctypes.c_int32),
@@ -154,6 +175,10 @@ for _name, _args, _res in [
     ("csa_layernorm_bwd_workspace_size", [_PN], ctypes.c_size_t),
     ("csa_layernorm_fwd", [_PN, _vp, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
     ("csa_layernorm_bwd", [_PN, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    ("csa_vocab_loss_fwd_workspace_size", [_PV], ctypes.c_size_t),
+    ("csa_vocab_loss_bwd_workspace_size", [_PV], ctypes.c_size_t),
+    ("csa_vocab_loss_fwd", [_PV, _vp, _vp, _PT, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    ("csa_vocab_loss_bwd", [_PV, _vp, _vp, _PT, _vp, _vp, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
     ("csa_check_device_status", [_vp], ctypes.c_int),
     ("csa_selftest_bounded_wait", [_vp], ctypes.c_int),
     ("csa_last_timeout_site", [], ctypes.c_int32),
@@ -173,6 +198,8 @@ EXPORTED = ("csa_topk_width", "csa_key_width", "csa_teacher_width", "csa_rows", 
             "csa_linear_fwd_workspace_size", "csa_linear_bwd_workspace_size", "csa_linear_fwd", "csa_linear_bwd",
             "csa_rope", "csa_adamw",
             "csa_layernorm_bwd_workspace_size", "csa_layernorm_fwd", "csa_layernorm_bwd",
+            "csa_vocab_loss_fwd_workspace_size", "csa_vocab_loss_bwd_workspace_size", "csa_vocab_loss_fwd",
+            "csa_vocab_loss_bwd",
             "csa_check_device_status", "csa_selftest_bounded_wait", "csa_last_timeout_site", "csa_last_path",
             "csa_last_cuda_error",
             "csa_kernel_launches",
@@ -828,6 +855,113 @@ def csa_layernorm_bwd(p: LayerNormParams, dy, x, weight=None, stats=None, need_d
     return dx, dw, db
 
 
+class VocabLossParams:
+    """Losses of the scores z = alpha x W^T (the C struct csa_vocab_loss_params): x [rows, features], W [vocab, features].
+    slots: a teacher's candidates a row (0: labels alone).  reduction "mean": each loss over the rows that have it; "sum".
+    piece_rows: rows whose scores are held at a time (0: as many as 4 GiB hold)."""
+
+    def __init__(self, rows, features, vocab, dtype="bf16", slots=0, alpha=1.0, label_weight=1.0, teacher_weight=1.0,
+                 reduction="mean", labels_64=False, ids_64=False, x_stride=0, piece_rows=0):
+        if reduction not in ("mean", "sum"):
+            raise ValueError(f"reduction must be mean or sum, got {reduction}")
+        self.c = csa_vocab_loss_params(_dtype(dtype), int(features), int(vocab), int(slots), 1 if labels_64 else 0,
+                                       1 if ids_64 else 0, 0 if reduction == "mean" else 1, float(alpha), float(label_weight),
+                                       float(teacher_weight), int(rows), int(x_stride), int(piece_rows))
+        self.ref = ctypes.byref(self.c)
+        self.value_dtype = TORCH_DTYPE[self.c.dtype]
+
+    @property
+    def fwd_workspace_bytes(self) -> int:
+        return _lib.csa_vocab_loss_fwd_workspace_size(self.ref)
+
+    @property
+    def bwd_workspace_bytes(self) -> int:
+        return _lib.csa_vocab_loss_bwd_workspace_size(self.ref)
+
+
+def _vocab_targets(p, dev, labels, teacher_ids, teacher_logits, teacher_lse):
+    """The targets' addresses.  Without slots the teacher's tensors are refused, with them ids and logits are required."""
+    c = p.c
+    if labels is not None:
+        _check_flat(labels, "labels", torch.int64 if c.labels_64 else torch.int32, dev, c.rows)
+    if c.slots:
+        for name, t, dtype in (("teacher_ids", teacher_ids, torch.int64 if c.ids_64 else torch.int32),
+                               ("teacher_logits", teacher_logits, torch.float32)):
+            _check_flat(t, name, dtype, dev, c.rows * c.slots)
+            if t.dim() > 1 and t.shape[-1] != c.slots:
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{c.rows}, {c.slots}]")
+        if teacher_lse is not None:
+            _check_flat(teacher_lse, "teacher_lse", torch.float32, dev, c.rows)
+    elif teacher_ids is not None or teacher_logits is not None or teacher_lse is not None:
+        raise ValueError("a teacher needs VocabLossParams(slots=...)")
+    elif labels is None:
+        raise ValueError("labels or a teacher are required")
+    return csa_vocab_targets(_ptr(labels), _ptr(teacher_ids), _ptr(teacher_logits), _ptr(teacher_lse))
+
+
+def csa_vocab_loss_fwd(p: VocabLossParams, x, weight, labels=None, teacher_ids=None, teacher_logits=None, teacher_lse=None,
+                       row_loss=None, workspace=None, out=None):
+    """The loss (a device scalar) of labels [rows] (negative: none), of a teacher's candidates teacher_ids [rows, slots]
+    (negative: none) with their teacher_logits (f32), or of both.  teacher_lse [rows]: the teacher's own log-sum-exp; without
+    it the candidates' shares sum to 1.  row_loss (a [2, rows] f32 tensor) receives the rows' label and teacher losses."""
+    c, dev = p.c, _on_cuda(x, "x")
+    _check_rows(x, "x", p.value_dtype, dev, c.rows, c.features, c.x_stride)
+    _check_weight(weight, p.value_dtype, dev, c.vocab, c.features)
+    targets = _vocab_targets(p, dev, labels, teacher_ids, teacher_logits, teacher_lse)
+    given = out is not None
+    if not given:
+        out = _empty((), (), torch.float32, dev)
+    else:
+        _check_flat(out, "out", torch.float32, dev, 1)
+    if row_loss is not None:
+        _check_flat(row_loss, "row_loss", torch.float32, dev, 2 * c.rows)
+    if workspace is None:
+        workspace = _empty((p.fwd_workspace_bytes,), (1,), torch.uint8, dev)
+    ws, nws = _check_workspace(workspace, dev)
+    _invoke("csa_vocab_loss_fwd", _lib.csa_vocab_loss_fwd, dev, p.ref, x.data_ptr(), weight.data_ptr(), ctypes.byref(targets),
+            out.data_ptr(), _ptr(row_loss), ws, nws)
+    if given:
+        _changed(out)
+    if row_loss is not None:
+        _changed(row_loss)
+    return out
+
+
+def csa_vocab_loss_bwd(p: VocabLossParams, x, weight, labels=None, teacher_ids=None, teacher_logits=None, teacher_lse=None,
+                       row_loss=None, need_dx=True, need_dw=True, workspace=None, out=None):
+    """The loss of csa_vocab_loss_fwd and its gradients: (loss, dx [rows, features], dw [vocab, features]), None in the place
+    of one that is not asked for.  out: a tuple of the three to write to."""
+    c, dev = p.c, _on_cuda(x, "x")
+    M, K, V = c.rows, c.features, c.vocab
+    _check_rows(x, "x", p.value_dtype, dev, M, K, c.x_stride)
+    _check_weight(weight, p.value_dtype, dev, V, K)
+    targets = _vocab_targets(p, dev, labels, teacher_ids, teacher_logits, teacher_lse)
+
+    def output(i, name, need, shape, strides, dtype, numel):
+        if not need:
+            return None
+        if out is None or out[i] is None:
+            return _empty(shape, strides, dtype, dev)
+        _check_flat(out[i], name, dtype, dev, numel)
+        return out[i]
+
+    loss = output(0, "loss", True, (), (), torch.float32, 1)
+    dx = output(1, "dx", need_dx, (M, K), (K, 1), p.value_dtype, M * K)
+    dw = output(2, "dw", need_dw, (V, K), (K, 1), p.value_dtype, V * K)
+    if row_loss is not None:
+        _check_flat(row_loss, "row_loss", torch.float32, dev, 2 * M)
+    if workspace is None:
+        workspace = _empty((p.bwd_workspace_bytes,), (1,), torch.uint8, dev)
+    ws, nws = _check_workspace(workspace, dev)
+    _invoke("csa_vocab_loss_bwd", _lib.csa_vocab_loss_bwd, dev, p.ref, x.data_ptr(), weight.data_ptr(), ctypes.byref(targets),
+            loss.data_ptr(), _ptr(row_loss), _ptr(dx), _ptr(dw), ws, nws)
+    if out is not None:
+        _changed([t for t in (loss, dx, dw) if t is not None])
+    if row_loss is not None:
+        _changed(row_loss)
+    return loss, dx, dw
+
+
 class AdamWTensors:
     """The tensors of csa_adamw, checked and laid out once.  Lists of equal length: param (f32 or bf16), grad (f32 or
     bf16), the moments m and v (both f32, or both float8_e4m3fn with their f32 scales m_scale and v_scale, one per
@@ -1041,3 +1175,31 @@ class CSALayerNorm(torch.autograd.Function):
 
 def csa_layernorm(x, weight=None, bias=None, *, params: LayerNormParams):
     return CSALayerNorm.apply(x, weight, bias, params)
+
+
+class CSAVocabLoss(torch.autograd.Function):
+    """loss = CSAVocabLoss.apply(x, weight, labels, teacher_ids, teacher_logits, teacher_lse, params): gradients flow to x and
+    weight.  As with CSAIndexerLoss the forward makes them with the loss and keeps nothing else for the backward; the teacher's
+    side receives none."""
+
+    @staticmethod
+    def forward(ctx, x, weight, labels, teacher_ids, teacher_logits, teacher_lse, params):
+        need_dx, need_dw = ctx.needs_input_grad[:2]
+        targets = [t.contiguous() if t is not None else None for t in (labels, teacher_ids, teacher_logits, teacher_lse)]
+        weight = weight.contiguous()
+        if not (need_dx or need_dw):
+            return csa_vocab_loss_fwd(params, x, weight, *targets)
+        loss, dx, dw = csa_vocab_loss_bwd(params, x, weight, *targets, need_dx=need_dx, need_dw=need_dw)
+        ctx.save_for_backward(dx.view(x.shape) if need_dx else None, dw.view(weight.shape) if need_dw else None)
+        return loss
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, gloss):
+        dx, dw = ctx.saved_tensors
+        # scaled in fp32: gloss in bf16 would be off by one factor for all of a gradient's values
+        return (*((g.float() * gloss).to(g.dtype) if g is not None else None for g in (dx, dw)), None, None, None, None, None)
+
+
+def csa_vocab_loss(x, weight, labels=None, teacher_ids=None, teacher_logits=None, teacher_lse=None, *, params: VocabLossParams):
+    return CSAVocabLoss.apply(x, weight, labels, teacher_ids, teacher_logits, teacher_lse, params)

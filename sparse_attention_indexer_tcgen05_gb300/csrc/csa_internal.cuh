@@ -230,6 +230,10 @@ cudaError_t launch_layernorm_fwd(const csa_layernorm_params &p, const void *x, c
                                  float *stats, cudaStream_t st);
 cudaError_t launch_layernorm_bwd(const csa_layernorm_params &p, const void *dy, const void *x, const void *weight,
                                  const float *stats, void *dx, void *dweight, void *dbias, void *ws, cudaStream_t st);
+size_t vocab_loss_workspace(const csa_vocab_loss_params &p, bool backward);
+// dx or dw null: not computed; both: the loss alone, in the workspace of `backward`
+cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, const void *weight, const csa_vocab_targets &t,
+                              float *loss, float *row_loss, void *dx, void *dw, bool backward, void *ws, cudaStream_t st);
 
 // ---------------------------------------------------------------- launchers (k_generic.cu)
 

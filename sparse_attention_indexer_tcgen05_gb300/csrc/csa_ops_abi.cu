@@ -1,4 +1,4 @@
-// csa_ops_abi.cu -- the entry points around the step (projections, rotary positions, AdamW, layer norm): argument checks and
+// csa_ops_abi.cu -- the entry points around the step (projections, rotary positions, AdamW, layer norm, vocabulary losses): argument checks and
 // dispatch.  Everything is checked on the host before anything is enqueued; no device memory is allocated and the
 // stream is never synchronised.
 #include "csa_internal.cuh"
@@ -86,6 +86,61 @@ csa_status check_layernorm(const csa_layernorm_params *p, csa_layernorm_params *
     constexpr int most = 0x7fff0000;  // 32-bit loop counters, which run up to 16384 beyond it
     const long long far = 1LL << 36;
     if (p->rows > most || p->cols > most || q->x_stride > far || q->dy_stride > far) return CSA_ERR_UNSUPPORTED;
+    return CSA_OK;
+}
+
+// ------------------------------------------------------------------ losses of a vocabulary
+
+csa_status check_vocab(const csa_vocab_loss_params *p, csa_vocab_loss_params *q)
+{
+    if (p == nullptr) return CSA_ERR_INVALID_ARG;
+    *q = *p;
+    if (!value_dtype(p->dtype) || p->features < 1 || p->vocab < 1 || p->slots < 0 || p->rows < 0 || p->piece_rows < 0) return CSA_ERR_INVALID_ARG;
+    if ((p->labels_64 & ~1) || (p->ids_64 & ~1) || (p->reduction & ~1)) return CSA_ERR_INVALID_ARG;
+    if (!isfinite(p->alpha) || p->alpha == 0.f) return CSA_ERR_INVALID_ARG;
+    if (!isfinite(p->label_weight) || !isfinite(p->teacher_weight) || p->label_weight < 0.f || p->teacher_weight < 0.f) return CSA_ERR_INVALID_ARG;
+    if (q->x_stride == 0) q->x_stride = p->features;
+    if (q->x_stride < p->features) return CSA_ERR_INVALID_ARG;
+    constexpr int most = 0x7fff0000;  // as of the projections, whose products these are
+    if (p->rows > most || p->features > most || p->vocab > most || q->x_stride > (1LL << 36) || p->slots > 1024) return CSA_ERR_UNSUPPORTED;
+    return CSA_OK;
+}
+
+csa_status check_targets(const csa_vocab_loss_params &p, const csa_vocab_targets *t)
+{
+    if (t == nullptr) return CSA_ERR_INVALID_ARG;
+    if (p.slots == 0 && (t->teacher_ids != nullptr || t->teacher_logits != nullptr || t->teacher_lse != nullptr)) return CSA_ERR_INVALID_ARG;
+    if (p.rows == 0) return CSA_OK;
+    if (p.slots > 0 && (t->teacher_ids == nullptr || t->teacher_logits == nullptr)) return CSA_ERR_INVALID_ARG;
+    if (p.slots == 0 && t->labels == nullptr) return CSA_ERR_INVALID_ARG;
+    CSA_TRY(need_scalar(t->labels, p.labels_64 ? 8 : 4));
+    CSA_TRY(need_scalar(t->teacher_ids, p.ids_64 ? 8 : 4));
+    CSA_TRY(need_scalar(t->teacher_logits, 4));
+    return need_scalar(t->teacher_lse, 4);
+}
+
+csa_status run_vocab_loss(const csa_vocab_loss_params *p, const void *x, const void *weight, const csa_vocab_targets *t, float *loss,
+                          float *row_loss, void *dx, void *dw, bool backward, void *workspace, size_t workspace_bytes, void *stream)
+{
+    CSA_TRY(injected_fault());
+    csa_vocab_loss_params q;
+    CSA_TRY(check_vocab(p, &q));
+    CSA_TRY(check_targets(q, t));
+    CSA_TRY(need(x, q.rows));
+    CSA_TRY(need(weight, q.rows));
+    if (loss == nullptr) return CSA_ERR_INVALID_ARG;
+    CSA_TRY(need_scalar(loss, 4));
+    CSA_TRY(need_scalar(row_loss, 4));
+    CSA_TRY(need_opt(dx));
+    CSA_TRY(need_opt(dw));
+    const size_t ws = vocab_loss_workspace(q, backward);
+    if (workspace_bytes < ws || (ws > 0 && workspace == nullptr)) return CSA_ERR_WORKSPACE;
+    CSA_TRY(need_opt(workspace));
+    if (q.rows > 0) {
+        const void *inputs[] = {x, weight, t->labels, t->teacher_ids, t->teacher_logits, t->teacher_lse, loss, row_loss, dx};
+        if (shares(loss, inputs, 6) || shares(row_loss, inputs, 7) || shares(dx, inputs, 8) || shares(dw, inputs, 9)) return CSA_ERR_INVALID_ARG;
+    }
+    CSA_CUDA(launch_vocab_loss(q, x, weight, *t, loss, row_loss, dx, dw, backward, workspace, static_cast<cudaStream_t>(stream)));
     return CSA_OK;
 }
 
@@ -327,6 +382,32 @@ csa_status csa_layernorm_bwd(const csa_layernorm_params *p, const void *dy, cons
     if (shares(dx, inputs, 2) || shares(dweight, inputs, 5) || shares(dbias, inputs, 6)) return CSA_ERR_INVALID_ARG;
     CSA_CUDA(launch_layernorm_bwd(q, dy, x, weight, stats, dx, dweight, dbias, workspace, static_cast<cudaStream_t>(stream)));
     return CSA_OK;
+}
+
+size_t csa_vocab_loss_fwd_workspace_size(const csa_vocab_loss_params *p)
+{
+    csa_vocab_loss_params q;
+    return check_vocab(p, &q) == CSA_OK ? vocab_loss_workspace(q, false) : 0;
+}
+
+size_t csa_vocab_loss_bwd_workspace_size(const csa_vocab_loss_params *p)
+{
+    csa_vocab_loss_params q;
+    return check_vocab(p, &q) == CSA_OK ? vocab_loss_workspace(q, true) : 0;
+}
+
+csa_status csa_vocab_loss_fwd(const csa_vocab_loss_params *p, const void *x, const void *weight,
+                              const csa_vocab_targets *targets, float *loss_out, float *row_loss_out, void *workspace,
+                              size_t workspace_bytes, void *stream)
+{
+    return run_vocab_loss(p, x, weight, targets, loss_out, row_loss_out, nullptr, nullptr, false, workspace, workspace_bytes, stream);
+}
+
+csa_status csa_vocab_loss_bwd(const csa_vocab_loss_params *p, const void *x, const void *weight,
+                              const csa_vocab_targets *targets, float *loss_out, float *row_loss_out, void *dx, void *dw,
+                              void *workspace, size_t workspace_bytes, void *stream)
+{
+    return run_vocab_loss(p, x, weight, targets, loss_out, row_loss_out, dx, dw, true, workspace, workspace_bytes, stream);
 }
 
 csa_status csa_adamw(const csa_adamw_params *p, const csa_adamw_tensor *tensors, int32_t count, void *stream)

@@ -89,6 +89,9 @@ cudaError_t teacher_h128_read_clear_error(int *flag);
 // The projections' products (k_linear_tc.cu).
 cudaError_t linear_tc_read_clear_error(int *flag);
 
+// The vocabulary's scores (k_vocab_tc.cu).
+cudaError_t vocab_tc_read_clear_error(int *flag);
+
 // One tiny kernel whose bounded wait (about 1 ms) on a barrier nothing arrives on runs out (k_selftest.cu), and
 // the read-and-clear of the word it sets.
 cudaError_t launch_bounded_wait_selftest(cudaStream_t st);

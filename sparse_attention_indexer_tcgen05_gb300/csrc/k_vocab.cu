@@ -1,0 +1,538 @@
+// k_vocab.cu -- the vocabulary's losses: cross entropy with labels and distillation from a teacher's top logits, from hidden
+// states and the vocabulary's weight, with their gradients.
+//
+//   z = alpha x W^T,  lse_r = log sum_v exp z_rv,  p = exp(z - lse)
+//   label of row r:  L_r = lse_r - z_label
+//   teacher of row r, candidates v_s with logits l_s:  t_s = exp(l_s - N_r), N_r given or log sum_s exp l_s;
+//       L_r = sum_s t_s (log t_s - z_{v_s} + lse_r)
+//   loss = sum of both, each with its weight and over the rows that have it
+//   dz_rv = c_r p_rv - sum over the row's targets at v of tau,  dx = alpha dz W,  dW = alpha dz^T x
+//
+// with tau the label's or candidate's weight in the loss and c_r their sum.  The losses need a row's lse and the few scores that
+// its targets name; the gradient needs p.  Rows go piece by piece: the scores of a piece are made once and reduced where
+// they are made (k_vocab_tc.cu), and what the backward keeps of them is 16 bits a value, exp(z - largest of its group), which
+// the pass below turns into dz in place.  So a piece takes three products, where pieces of the vocabulary would need its scores a second
+// time, once the lse is known: four.  dW sums over pieces in fp32.
+#include "k_rows.cuh"
+#include "k_vocab.cuh"
+
+#include <cuda_fp16.h>
+
+namespace csa {
+namespace vocab {
+
+using namespace linear;
+
+constexpr int PREP_ROWS = 8;     // rows of a block of prepare_kernel, a warp each
+constexpr float kLn2 = 0.69314718055994531f;
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Targets as they are given, and what they become: a row's columns in ascending order, with their weights.
+struct Targets {
+    const void *labels, *ids;    // [M], [M][slots]; int32 or int64
+    const float *logits, *lse;   // [M][slots], [M] or null
+    int labels_64, ids_64, slots, width;   // width: slots and the label's
+    long long rows, vocab;
+    int *sorted;                 // [width][rows]
+    float *weight;               // [width][rows]: t of a candidate, -1 for the label; NaN and -inf where the id is not a column
+    int2 *counts;                // [blocks]: rows with a label, rows with a candidate
+};
+
+// A warp a row.  Each target's place is the number of targets before it (smaller column, or the same and earlier).
+__global__ void __launch_bounds__(32 * PREP_ROWS) vocab_prepare_kernel(const Targets a)
+{
+    extern __shared__ int ids_raw[];
+    __shared__ int have[PREP_ROWS][2];
+    chain_start();
+    chain_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long r = (long long)blockIdx.x * PREP_ROWS + warp;
+    int *ids = ids_raw + warp * a.width;
+    int label = NONE, any = 0;
+    bool taught = false;
+    float label_weight = 0.f;
+    if (r < a.rows) {
+        if (a.labels != nullptr) {
+            const long long v = a.labels_64 ? static_cast<const long long *>(a.labels)[r] : static_cast<const int *>(a.labels)[r];
+            if (v >= 0) {
+                label = v < a.vocab ? (int)v : NONE;
+                label_weight = v < a.vocab ? -1.f : -INFINITY;
+            }
+        }
+        const long long at = r * a.slots;
+        const auto candidate = [&](int s) { return a.ids_64 ? static_cast<const long long *>(a.ids)[at + s] : static_cast<const int *>(a.ids)[at + s]; };
+        float top = -INFINITY;
+        for (int s = lane; s < a.slots; s += 32) {
+            const long long v = candidate(s);
+            ids[s] = v >= 0 && v < a.vocab ? (int)v : NONE;
+            any |= v >= 0;
+            if (v >= 0) top = fmaxf(top, __ldg(a.logits + at + s));
+        }
+        float log_sum;
+        if (a.lse != nullptr) {
+            log_sum = __ldg(a.lse + r);
+        } else {
+            top = warp_max(top);
+            float sum = 0.f;
+            for (int s = lane; s < a.slots; s += 32)
+                if (candidate(s) >= 0) sum += expf(__ldg(a.logits + at + s) - top);
+            sum = warp_sum(sum);
+            log_sum = top + logf(sum);
+        }
+        taught = __any_sync(0xffffffffu, any);
+        if (lane == 0 && a.width > a.slots) ids[a.slots] = label;
+        __syncwarp();
+        for (int s = lane; s < a.width; s += 32) {
+            const int id = ids[s];
+            float t = label_weight;
+            if (s < a.slots) {
+                const long long v = candidate(s);
+                const float l = v >= 0 ? __ldg(a.logits + at + s) : -INFINITY;
+                t = l == -INFINITY ? 0.f : expf(l - log_sum);   // also where no logit is finite
+                if (v >= a.vocab) t = NAN;
+            }
+            int place = 0;
+            for (int j = 0; j < a.width; j++) place += ids[j] < id || (ids[j] == id && j < s);
+            a.sorted[place * a.rows + r] = id;
+            a.weight[place * a.rows + r] = t;
+        }
+    }
+    if (lane == 0) {
+        have[warp][0] = label_weight != 0.f;
+        have[warp][1] = taught;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int2 n = make_int2(0, 0);
+#pragma unroll
+        for (int w = 0; w < PREP_ROWS; w++) {
+            n.x += have[w][0];
+            n.y += have[w][1];
+        }
+        a.counts[blockIdx.x] = n;
+    }
+}
+
+// What a row with a label, or with candidates, weighs in the loss.
+struct Weights {
+    const int2 *counts;
+    int blocks, mean;
+    float label, teacher;
+};
+// By a block of 1024 threads: x the label's, y the teacher's.
+__device__ __forceinline__ float2 weigh(const Weights &w, int2 *part)
+{
+    if (!w.mean) return make_float2(w.label, w.teacher);
+    int2 n = make_int2(0, 0);
+    for (int b = threadIdx.x; b < w.blocks; b += 1024) {
+        const int2 c = w.counts[b];
+        n.x += c.x;
+        n.y += c.y;
+    }
+    n.x = __reduce_add_sync(0xffffffffu, n.x);
+    n.y = __reduce_add_sync(0xffffffffu, n.y);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = n;
+    __syncthreads();
+    n = part[threadIdx.x & 31];
+    n.x = __reduce_add_sync(0xffffffffu, n.x);
+    n.y = __reduce_add_sync(0xffffffffu, n.y);
+    return make_float2(w.label / (float)max(n.x, 1), w.teacher / (float)max(n.y, 1));
+}
+
+// The rows of a piece: their lse, losses and the weights of their gradients.
+struct Rows {
+    const float2 *parts;         // [groups][count]
+    int groups, width;
+    long long first, count, all; // the piece's first row, its rows, the call's rows
+    const int *sorted;           // from here on of the piece's first row, `all` apart
+    float *weight;               // becomes tau for a backward pass
+    const float *z;
+    float2 *info;                // [count]: lse in base-2 units, c; null: no backward
+    float *losses;               // [2][all]
+    Weights w;
+};
+
+// 32 rows a block; 32 threads join a row's groups, then a warp takes its targets.
+__global__ void __launch_bounds__(1024) vocab_rows_kernel(const Rows a)
+{
+    __shared__ float2 part[32][33];
+    __shared__ int2 counted[32];
+    chain_start();
+    chain_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float2 w = weigh(a.w, counted);
+    const long long r0 = (long long)blockIdx.x * 32;
+    float top = -INFINITY, sum = 0.f;
+    const auto join = [&](float2 q) {   // a group without a finite score has the sum 0, or NaN
+        if (q.x > top) {
+            sum = sum * ex2(top - q.x) + q.y;
+            top = q.x;
+        } else {
+            sum += q.x == -INFINITY ? q.y : q.y * ex2(q.x - top);
+        }
+    };
+    if (r0 + lane < a.count) {
+#pragma unroll 4
+        for (int g = warp; g < a.groups; g += 32) join(__ldcs(a.parts + g * a.count + r0 + lane));
+    }
+    part[warp][lane] = make_float2(top, sum);
+    __syncthreads();
+    const long long r = r0 + warp;
+    if (r >= a.count) return;
+    const float2 q = part[lane][warp];
+    top = warp_max(q.x);
+    sum = warp_sum(q.x == -INFINITY ? q.y : q.y * ex2(q.x - top));
+    const float lse2 = top + log2f(sum), lse = lse2 * kLn2;
+
+    float label = 0.f, teacher = 0.f, c = 0.f;
+    for (int s = lane; s < a.width; s += 32) {
+        const long long at = s * a.all + r;
+        const float t = a.weight[at];
+        float tau = 0.f;
+        if (t == -1.f) {
+            label = lse - a.z[at];
+            tau = w.x;
+        } else if (t != 0.f) {
+            // a candidate that is no column: NaN; a label: -inf
+            if (t == -INFINITY) label = NAN;
+            else teacher = t == t ? fmaf(t, logf(t) + (lse - a.z[at]), teacher) : NAN;
+            tau = t == -INFINITY ? NAN : w.y * t;
+        }
+        c += tau;
+        if (a.info != nullptr) a.weight[at] = tau;
+    }
+    label = warp_sum(label);
+    teacher = warp_sum(teacher);
+    c = warp_sum(c);
+    if (lane > 0) return;
+    a.losses[a.first + r] = label;
+    a.losses[a.all + a.first + r] = teacher;
+    if (a.info != nullptr) a.info[r] = make_float2(lse2, c);
+}
+
+__global__ void __launch_bounds__(1024) vocab_loss_kernel(const float *losses, long long rows, const Weights weights, float *loss)
+{
+    __shared__ double part[32];
+    __shared__ int2 counted[32];
+    chain_start();
+    chain_wait();
+    const float2 w = weigh(weights, counted);
+    double label = 0., teacher = 0.;
+    for (long long r = threadIdx.x; r < rows; r += 1024) {
+        label += losses[r];
+        teacher += losses[rows + r];
+    }
+    double s = w.x * label + w.y * teacher;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    s = part[threadIdx.x];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (threadIdx.x == 0) *loss = rows > 0 ? (float)s : 0.f;
+}
+
+struct Dz {
+    const void *e;               // [count][ld] fp16 or fp32
+    bf16 *dz;                    // [count][ld], planes apart for fp32 values
+    long long ld, plane, vocab;
+    const float2 *parts, *info;
+    long long count, all;
+    const int *sorted;
+    const float *tau, *z;
+    int width;
+    int cols;                    // columns of a block, a multiple of 2048
+};
+
+// dz = c exp(z - lse) - tau of one row's columns, 8 a thread at a time; then the columns that targets name, from their own
+// scores.  Bound by memory: 2 bytes read and written a value (fp32: 4 and 6).
+template <typename V> __global__ void __launch_bounds__(256) vocab_dz_kernel(const Dz a)
+{
+    constexpr int P = Planes<V>::N;
+    chain_start();
+    chain_wait();
+    const long long r = blockIdx.x, c0 = (long long)blockIdx.y * a.cols, c1 = min(a.vocab, c0 + a.cols);
+    const float2 info = a.info[r];
+    for (long long v = c0 + 8 * threadIdx.x; v < c1; v += 8 * 256) {
+        const long long at = r * a.ld + v;
+        float x[8];
+        if (info.y == 0.f) {   // nothing passes, whatever the scores are
+#pragma unroll
+            for (int k = 0; k < 8; k++) x[k] = 0.f;
+        } else {
+            const float f = info.y * ex2(__ldg(&a.parts[v / GROUP * a.count + r].x) - info.x);
+            if constexpr (P == 1) {
+                const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const __half *>(a.e) + at);
+                const uint32_t h[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&h[k]));
+                    x[2 * k] = f * y.x;
+                    x[2 * k + 1] = f * y.y;
+                }
+            } else {
+                const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(a.e) + at);
+                const float4 y = q[0], z = q[1];
+                x[0] = f * y.x; x[1] = f * y.y; x[2] = f * y.z; x[3] = f * y.w;
+                x[4] = f * z.x; x[5] = f * z.y; x[6] = f * z.z; x[7] = f * z.w;
+            }
+        }
+        put_planes8<P>(a.dz, a.plane, at, x);   // up to 7 values of padding
+    }
+    if (info.y == 0.f) return;
+    __syncthreads();
+    for (int s = threadIdx.x; s < a.width; s += 256) {
+        const int id = a.sorted[s * a.all + r];
+        if (id < c0 || id >= c1) continue;
+        if (s > 0 && a.sorted[(s - 1) * a.all + r] == id) continue;   // the first of its column takes them all
+        float tau = a.tau[s * a.all + r];
+        for (int j = s + 1; j < a.width && a.sorted[j * a.all + r] == id; j++) tau += a.tau[j * a.all + r];
+        const float d = fmaf(info.y, ex2(fmaf(a.z[s * a.all + r], kLog2e, -info.x)), -tau);
+        bf16 *out = a.dz + r * a.ld + id;
+        if constexpr (P == 1) {
+            *out = __float2bfloat16_rn(d);
+        } else {
+            split3(d, out[0], out[a.plane], out[2 * a.plane]);
+        }
+    }
+}
+
+// The sums of dW over pieces, rounded.
+__global__ void __launch_bounds__(256) vocab_round_kernel(const float *sum, long long n, bf16 *out)
+{
+    chain_start();
+    chain_wait();
+    const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 8;
+    if (i >= n) return;
+    if (i + 8 <= n) {
+        const float4 a = __ldcs(reinterpret_cast<const float4 *>(sum + i)), b = __ldcs(reinterpret_cast<const float4 *>(sum + i + 4));
+        const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        put_planes8<1>(out, 0, i, x);
+    } else {
+        for (long long j = i; j < n; j++) out[j] = __float2bfloat16_rn(sum[j]);
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+inline int planes_of(const csa_vocab_loss_params &p) { return p.dtype == CSA_F32 ? 3 : 1; }
+
+// Bytes of the scores that a backward pass keeps at once, unless the caller names the rows of a piece: small beside the GPU's
+// memory, and large enough that dW's sums are read and written again but once in 16384 rows of a vocabulary of 131072.
+constexpr long long kKept = 4LL << 30;
+
+struct Layout {
+    bool stage_x, stage_w;
+    long long piece;     // rows of a piece
+    int pieces, width, groups;
+    linear::Plan dx, dw;
+    size_t off_x, off_w, off_sorted, off_weight, off_z, off_counts, off_losses, off_info, off_parts, off_e, off_dz, off_sum, off_part, total;
+};
+Layout plan(const csa_vocab_loss_params &p, bool backward)
+{
+    Layout b = {};
+    const long long M = p.rows, K = p.features, V = p.vocab, ld = up8(V);
+    if (M == 0) return b;
+    b.width = p.slots + 1;
+    b.groups = (int)((V + GROUP - 1) / GROUP);
+    // a piece's bytes a row: the scores, or the groups' sums alone
+    const long long row = backward ? ld * (p.dtype == CSA_F32 ? 10 : 2) : (long long)b.groups * 8;
+    long long most = p.piece_rows > 0 ? p.piece_rows : kKept / row / 256 * 256;
+    if (most < 256 && p.piece_rows <= 0) most = 256;
+    b.piece = M < most ? M : most;
+    b.pieces = (int)((M + b.piece - 1) / b.piece);
+    if (p.piece_rows <= 0 && b.pieces > 1) {  // of one size, whole tiles
+        b.piece = ((M + b.pieces - 1) / b.pieces + 255) / 256 * 256;
+        b.pieces = (int)((M + b.piece - 1) / b.piece);
+    }
+    b.stage_x = staged(p.dtype, p.x_stride);
+    b.stage_w = staged(p.dtype, K);
+    size_t at = 0;
+    const auto take = [&](size_t &off, size_t bytes) {
+        off = at;
+        at += up256(bytes);
+    };
+    take(b.off_x, b.stage_x ? staged_bytes(p.dtype, M, K) : 0);
+    take(b.off_w, b.stage_w ? staged_bytes(p.dtype, V, K) : 0);
+    take(b.off_sorted, (size_t)M * b.width * 4);
+    take(b.off_weight, (size_t)M * b.width * 4);
+    take(b.off_z, (size_t)M * b.width * 4);
+    take(b.off_counts, (size_t)((M + PREP_ROWS - 1) / PREP_ROWS) * 8);
+    take(b.off_losses, (size_t)M * 8);
+    take(b.off_info, (size_t)b.piece * 8);
+    take(b.off_parts, (size_t)b.piece * b.groups * 8);
+    if (backward) {
+        take(b.off_e, (size_t)b.piece * ld * (p.dtype == CSA_F32 ? 4 : 2));
+        b.off_dz = b.off_e;
+        if (p.dtype == CSA_F32) take(b.off_dz, (size_t)b.piece * ld * 6);
+        take(b.off_sum, b.pieces > 1 && p.dtype == CSA_BF16 ? (size_t)V * K * 4 : 0);
+        b.dx = plan_product(b.piece, K, V, planes_of(p), 1, p.dtype == CSA_F32, kSms);
+        b.dw = plan_product(V, K, b.piece, planes_of(p), 1, p.dtype == CSA_F32, kSms);
+        const size_t dx = b.dx.splits > 1 ? (size_t)b.dx.splits * b.piece * partial_stride(K) * 4 : 0;
+        const size_t dw = b.dw.splits > 1 ? (size_t)b.dw.splits * V * partial_stride(K) * 4 : 0;
+        take(b.off_part, dx > dw ? dx : dw);
+    }
+    b.total = at;
+    return b;
+}
+
+cudaError_t sms_here(int *sms)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    if (*sms < 2) *sms = 2;
+    return e;
+}
+
+}  // namespace vocab
+
+using namespace vocab;
+
+#define VOC_TRY(x)                        \
+    do {                                  \
+        const cudaError_t e_ = (x);       \
+        if (e_ != cudaSuccess) return e_; \
+    } while (0)
+
+size_t vocab_loss_workspace(const csa_vocab_loss_params &p, bool backward) { return plan(p, backward).total; }
+
+cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, const void *weight, const csa_vocab_targets &t, float *loss,
+                              float *row_loss, void *dx, void *dw, bool backward, void *ws, cudaStream_t st)
+{
+    const long long M = p.rows, K = p.features, V = p.vocab, ld = up8(V);
+    const int planes = planes_of(p);
+    const size_t size = p.dtype == CSA_F32 ? 4 : 2;
+    if (M == 0) {
+        if (dw != nullptr) VOC_TRY(cudaMemsetAsync(dw, 0, (size_t)V * K * size, st));
+        return cudaMemsetAsync(loss, 0, 4, st);
+    }
+    note_path("tcgen05");
+    int sms = 0;
+    VOC_TRY(sms_here(&sms));
+    const Layout b = plan(p, backward);
+    char *w = static_cast<char *>(ws);
+    Stage job[2] = {};
+    Operand ox = operand(p.dtype, x, p.x_stride, M, (int)K, b.stage_x, w + b.off_x, true, &job[0]);
+    Operand ow = operand(p.dtype, weight, K, V, (int)K, b.stage_w, w + b.off_w, true, &job[1]);
+    VOC_TRY(run_stages(p.dtype, job, st));
+
+    Targets g = {};
+    g.labels = t.labels;
+    g.ids = t.teacher_ids;
+    g.logits = t.teacher_logits;
+    g.lse = t.teacher_lse;
+    g.labels_64 = p.labels_64;
+    g.ids_64 = p.ids_64;
+    g.slots = p.slots;
+    g.width = p.slots + (t.labels != nullptr);
+    g.rows = M;
+    g.vocab = V;
+    g.sorted = reinterpret_cast<int *>(w + b.off_sorted);
+    g.weight = reinterpret_cast<float *>(w + b.off_weight);
+    g.counts = reinterpret_cast<int2 *>(w + b.off_counts);
+    const unsigned blocks = (unsigned)((M + PREP_ROWS - 1) / PREP_ROWS);
+    VOC_TRY(launch_chained(vocab_prepare_kernel, dim3(blocks), 32 * PREP_ROWS, (size_t)g.width * PREP_ROWS * 4, 1, st, g));
+
+    const bool grads = dx != nullptr || dw != nullptr;
+    const Weights weights = {g.counts, (int)blocks, p.reduction == 0, p.label_weight, p.teacher_weight};
+    float *losses = row_loss != nullptr ? row_loss : reinterpret_cast<float *>(w + b.off_losses);
+    float *z = reinterpret_cast<float *>(w + b.off_z);
+    float2 *parts = reinterpret_cast<float2 *>(w + b.off_parts), *info = grads ? reinterpret_cast<float2 *>(w + b.off_info) : nullptr;
+    for (long long first = 0; first < M; first += b.piece) {
+        const long long count = M - first < b.piece ? M - first : b.piece;
+        Operand px = ox;
+        px.base += first * ox.ld;
+        Scores s = {};
+        s.ids = g.sorted + first;
+        s.z = z + first;
+        s.slots = g.width;
+        s.ld = M;
+        s.parts = parts;
+        s.alpha = p.alpha;
+        s.e = grads ? w + b.off_e : nullptr;
+        s.lde = ld;
+        VOC_TRY(launch_scores(px, ow, count, V, K, planes, s, sms, st));
+        const Rows rows = {parts, b.groups, g.width, first, count, M, g.sorted + first, g.weight + first, z + first, info, losses, weights};
+        VOC_TRY(launch_chained(vocab_rows_kernel, dim3((unsigned)((count + 31) / 32)), 1024, 0, 1, st, rows));
+        if (!grads) continue;
+        Dz d = {};
+        d.e = w + b.off_e;
+        d.dz = reinterpret_cast<bf16 *>(w + b.off_dz);
+        d.ld = ld;
+        d.plane = b.piece * ld;
+        d.vocab = V;
+        d.parts = parts;
+        d.info = info;
+        d.count = count;
+        d.all = M;
+        d.sorted = rows.sorted;
+        d.tau = rows.weight;
+        d.z = rows.z;
+        d.width = g.width;
+        // few rows: several blocks each
+        const long long chunks = (V + 2047) / 2048, per_row = (4LL * kSms + count - 1) / count;
+        d.cols = (int)((chunks + per_row - 1) / per_row) * 2048;
+        const dim3 grid((unsigned)count, (unsigned)((V + d.cols - 1) / d.cols));
+        VOC_TRY(launch_chained(p.dtype == CSA_F32 ? vocab_dz_kernel<float> : vocab_dz_kernel<bf16>, grid, 256, 0, 1, st, d));
+        Product q = {};
+        q.planes = planes;
+        q.passes = 1;
+        q.e.partial = reinterpret_cast<float *>(w + b.off_part);
+        Operand od = {};
+        od.base = d.dz;
+        od.ld = ld;
+        od.plane = d.plane;
+        if (dx != nullptr) {
+            q.a = od;
+            q.a.k_major = true;
+            q.b = ow;
+            q.b.k_major = false;
+            q.M = count;
+            q.N = K;
+            q.K = V;
+            q.plan = b.dx;
+            q.e.alpha = p.alpha;
+            q.e.out_f32 = p.dtype == CSA_F32;
+            q.e.out = static_cast<char *>(dx) + (size_t)first * K * size;
+            VOC_TRY(product(q, st));
+        }
+        if (dw != nullptr) {
+            q.a = od;
+            q.a.k_major = false;
+            q.b = px;
+            q.b.k_major = false;
+            q.M = V;
+            q.N = K;
+            q.K = count;
+            q.plan = b.dw;
+            // the last piece's k axis may be shorter: no part of it is empty
+            const long long steps = (count + 63) / 64, each = (steps + b.dw.splits - 1) / b.dw.splits;
+            q.plan.splits = (int)((steps + each - 1) / each);
+            q.e.alpha = p.alpha;
+            q.e.out_f32 = p.dtype == CSA_F32 || b.pieces > 1;
+            q.e.out = p.dtype == CSA_BF16 && b.pieces > 1 ? w + b.off_sum : dw;
+            if (first > 0) {   // dW so far
+                q.e.res = q.e.out;
+                q.e.ldr = K;
+            }
+            VOC_TRY(product(q, st));
+        }
+    }
+    VOC_TRY(launch_chained(vocab_loss_kernel, dim3(1), 1024, 0, 1, st, losses, M, weights, loss));
+    if (dw != nullptr && b.pieces > 1 && p.dtype == CSA_BF16) {
+        const long long n = V * K;
+        VOC_TRY(launch_chained(vocab_round_kernel, dim3((unsigned)((n + 2047) / 2048)), 256, 0, 1, st, reinterpret_cast<float *>(w + b.off_sum), n, (bf16 *)dw));
+    }
+    return cudaSuccess;
+}
+
+}  // namespace csa
