@@ -23,7 +23,7 @@ namespace vocab {
 
 using namespace linear;
 
-constexpr int PREP_ROWS = 8;     // rows of a block of prepare_kernel, a warp each
+constexpr int ROWS = 8;          // rows of a block of prepare_kernel and rows_kernel, a warp each
 constexpr float kLn2 = 0.69314718055994531f;
 
 __device__ __forceinline__ float ex2(float x)
@@ -41,39 +41,82 @@ struct Targets {
     long long rows, vocab;
     int *sorted;                 // [width][rows]
     float *weight;               // [width][rows]: t of a candidate, -1 for the label; NaN and -inf where the id is not a column
+    unsigned short *starts;      // [rows][marks]: how many targets lie before each group of columns, and before the end
+    int marks;
     int2 *counts;                // [blocks]: rows with a label, rows with a candidate
+    int *done;                   // set to 0: blocks of rows_kernel that have finished
 };
 
-// A warp a row.  Each target's place is the number of targets before it (smaller column, or the same and earlier).
-__global__ void __launch_bounds__(32 * PREP_ROWS) vocab_prepare_kernel(const Targets a)
+__device__ __forceinline__ long long label_of(const Targets &a, long long r)
 {
-    extern __shared__ int ids_raw[];
-    __shared__ int have[PREP_ROWS][2];
+    if (a.labels == nullptr) return -1;
+    return a.labels_64 ? static_cast<const long long *>(a.labels)[r] : static_cast<const int *>(a.labels)[r];
+}
+// Counts of a block's threads or warps, joined.
+__device__ __forceinline__ void count(const Targets &a, bool label, bool taught)
+{
+    __shared__ int2 have[32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int2 n = make_int2(__popc(__ballot_sync(0xffffffffu, label)), __popc(__ballot_sync(0xffffffffu, taught)));
+    if (lane == 0) have[warp] = n;
+    __syncthreads();
+    if (threadIdx.x > 0) return;
+    int2 sum = make_int2(0, 0);
+    for (int w = 0; w < (int)blockDim.x / 32; w++) {
+        sum.x += have[w].x;
+        sum.y += have[w].y;
+    }
+    a.counts[blockIdx.x] = sum;
+    if (blockIdx.x == 0) *a.done = 0;
+}
+
+// Labels alone: a thread a row.
+__global__ void __launch_bounds__(256) vocab_labels_kernel(const Targets a)
+{
     chain_start();
     chain_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long r = (long long)blockIdx.x * PREP_ROWS + warp;
-    int *ids = ids_raw + warp * a.width;
-    int label = NONE, any = 0;
-    bool taught = false;
-    float label_weight = 0.f;
+    const long long r = (long long)blockIdx.x * 256 + threadIdx.x;
+    const long long v = r < a.rows ? label_of(a, r) : -1;
     if (r < a.rows) {
-        if (a.labels != nullptr) {
-            const long long v = a.labels_64 ? static_cast<const long long *>(a.labels)[r] : static_cast<const int *>(a.labels)[r];
-            if (v >= 0) {
-                label = v < a.vocab ? (int)v : NONE;
-                label_weight = v < a.vocab ? -1.f : -INFINITY;
-            }
-        }
+        a.sorted[r] = v >= 0 && v < a.vocab ? (int)v : NONE;
+        a.weight[r] = v < 0 ? 0.f : v < a.vocab ? -1.f : -INFINITY;
+    }
+    count(a, v >= 0, false);
+}
+
+// A warp a row.  Each target's place is the number of targets before it (smaller column, or the same and earlier).
+__global__ void __launch_bounds__(32 * ROWS) vocab_prepare_kernel(const Targets a)
+{
+    extern __shared__ int raw[];
+    chain_start();
+    chain_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, room = (a.width + 3) & ~3;
+    const long long r = (long long)blockIdx.x * ROWS + warp;
+    int *ids = raw + warp * 3 * room, *sorted = ids + room;
+    float *logits = reinterpret_cast<float *>(sorted + room);
+    bool taught = false;
+    long long label = -1;
+    if (r < a.rows) {
+        label = label_of(a, r);
         const long long at = r * a.slots;
-        const auto candidate = [&](int s) { return a.ids_64 ? static_cast<const long long *>(a.ids)[at + s] : static_cast<const int *>(a.ids)[at + s]; };
         float top = -INFINITY;
-        for (int s = lane; s < a.slots; s += 32) {
-            const long long v = candidate(s);
+        int any = 0;
+#pragma unroll 4
+        for (int s = lane; s < room; s += 32) {
+            long long v = s == a.slots ? label : -1;
+            float l = 0.f;
+            if (s < a.slots) {
+                v = a.ids_64 ? static_cast<const long long *>(a.ids)[at + s] : static_cast<const int *>(a.ids)[at + s];
+                l = __ldg(a.logits + at + s);
+                any |= v >= 0;
+                if (v < 0) l = -INFINITY;
+                if (v >= a.vocab) l = NAN;
+                else top = fmaxf(top, l);
+            }
             ids[s] = v >= 0 && v < a.vocab ? (int)v : NONE;
-            any |= v >= 0;
-            if (v >= 0) top = fmaxf(top, __ldg(a.logits + at + s));
+            logits[s] = l;
         }
+        taught = __any_sync(0xffffffffu, any);
         float log_sum;
         if (a.lse != nullptr) {
             log_sum = __ldg(a.lse + r);
@@ -81,42 +124,34 @@ __global__ void __launch_bounds__(32 * PREP_ROWS) vocab_prepare_kernel(const Tar
             top = warp_max(top);
             float sum = 0.f;
             for (int s = lane; s < a.slots; s += 32)
-                if (candidate(s) >= 0) sum += expf(__ldg(a.logits + at + s) - top);
+                if (logits[s] > -INFINITY) sum += expf(logits[s] - top);
             sum = warp_sum(sum);
             log_sum = top + logf(sum);
         }
-        taught = __any_sync(0xffffffffu, any);
-        if (lane == 0 && a.width > a.slots) ids[a.slots] = label;
         __syncwarp();
         for (int s = lane; s < a.width; s += 32) {
             const int id = ids[s];
-            float t = label_weight;
-            if (s < a.slots) {
-                const long long v = candidate(s);
-                const float l = v >= 0 ? __ldg(a.logits + at + s) : -INFINITY;
-                t = l == -INFINITY ? 0.f : expf(l - log_sum);   // also where no logit is finite
-                if (v >= a.vocab) t = NAN;
-            }
+            float t = label < 0 ? 0.f : label < a.vocab ? -1.f : -INFINITY;
+            if (s < a.slots) t = logits[s] == -INFINITY ? 0.f : expf(logits[s] - log_sum);   // also where no logit is finite
             int place = 0;
-            for (int j = 0; j < a.width; j++) place += ids[j] < id || (ids[j] == id && j < s);
+            for (int j = 0; j < room; j += 4) {   // places from width on hold NONE and lie behind every target
+                const int4 q = *reinterpret_cast<const int4 *>(ids + j);
+                place += q.x < id || (q.x == id && j < s);
+                place += q.y < id || (q.y == id && j + 1 < s);
+                place += q.z < id || (q.z == id && j + 2 < s);
+                place += q.w < id || (q.w == id && j + 3 < s);
+            }
+            sorted[place] = id;
             a.sorted[place * a.rows + r] = id;
             a.weight[place * a.rows + r] = t;
         }
-    }
-    if (lane == 0) {
-        have[warp][0] = label_weight != 0.f;
-        have[warp][1] = taught;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        int2 n = make_int2(0, 0);
-#pragma unroll
-        for (int w = 0; w < PREP_ROWS; w++) {
-            n.x += have[w][0];
-            n.y += have[w][1];
+        __syncwarp();
+        for (int g = lane, at = 0; g < a.marks; g += 32) {
+            while (at < a.width && sorted[at] < g * (long long)GROUP) at++;
+            a.starts[r * a.marks + g] = (unsigned short)at;
         }
-        a.counts[blockIdx.x] = n;
     }
+    count(a, lane == 0 && label >= 0, lane == 0 && taught);
 }
 
 // What a row with a label, or with candidates, weighs in the loss.
@@ -125,12 +160,13 @@ struct Weights {
     int blocks, mean;
     float label, teacher;
 };
-// By a block of 1024 threads: x the label's, y the teacher's.
+// By a block of 32 ROWS threads: x the label's, y the teacher's.
 __device__ __forceinline__ float2 weigh(const Weights &w, int2 *part)
 {
     if (!w.mean) return make_float2(w.label, w.teacher);
     int2 n = make_int2(0, 0);
-    for (int b = threadIdx.x; b < w.blocks; b += 1024) {
+#pragma unroll 4
+    for (int b = threadIdx.x; b < w.blocks; b += 32 * ROWS) {
         const int2 c = w.counts[b];
         n.x += c.x;
         n.y += c.y;
@@ -139,9 +175,12 @@ __device__ __forceinline__ float2 weigh(const Weights &w, int2 *part)
     n.y = __reduce_add_sync(0xffffffffu, n.y);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = n;
     __syncthreads();
-    n = part[threadIdx.x & 31];
-    n.x = __reduce_add_sync(0xffffffffu, n.x);
-    n.y = __reduce_add_sync(0xffffffffu, n.y);
+    n = make_int2(0, 0);
+#pragma unroll
+    for (int i = 0; i < ROWS; i++) {
+        n.x += part[i].x;
+        n.y += part[i].y;
+    }
     return make_float2(w.label / (float)max(n.x, 1), w.teacher / (float)max(n.y, 1));
 }
 
@@ -150,24 +189,29 @@ struct Rows {
     const float2 *parts;         // [groups][count]
     int groups, width;
     long long first, count, all; // the piece's first row, its rows, the call's rows
-    const int *sorted;           // from here on of the piece's first row, `all` apart
-    float *weight;               // becomes tau for a backward pass
-    const float *z;
+    float *weight;               // [width][all] from the piece's first row on; becomes tau for a backward pass
+    const float *z;              // the same places
     float2 *info;                // [count]: lse in base-2 units, c; null: no backward
     float *losses;               // [2][all]
     Weights w;
+    int *done;
+    int blocks;                  // of all pieces
+    float *loss;
 };
 
-// 32 rows a block; 32 threads join a row's groups, then a warp takes its targets.
-__global__ void __launch_bounds__(1024) vocab_rows_kernel(const Rows a)
+// A block joins the groups of its rows, 32 threads a row, then a warp takes a row's targets.  The block that finishes last
+// adds up the rows' losses, in the same order whichever block it is and however the rows were cut.
+__global__ void __launch_bounds__(32 * ROWS) vocab_rows_kernel(const Rows a)
 {
-    __shared__ float2 part[32][33];
-    __shared__ int2 counted[32];
+    __shared__ float2 part[32][ROWS + 1];
+    __shared__ int2 counted[ROWS];
+    __shared__ float2 lost[ROWS];
+    __shared__ int last;
     chain_start();
     chain_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = threadIdx.x % ROWS, each = threadIdx.x / ROWS;
     const float2 w = weigh(a.w, counted);
-    const long long r0 = (long long)blockIdx.x * 32;
+    const long long r0 = (long long)blockIdx.x * ROWS;
     float top = -INFINITY, sum = 0.f;
     const auto join = [&](float2 q) {   // a group without a finite score has the sum 0, or NaN
         if (q.x > top) {
@@ -177,67 +221,83 @@ __global__ void __launch_bounds__(1024) vocab_rows_kernel(const Rows a)
             sum += q.x == -INFINITY ? q.y : q.y * ex2(q.x - top);
         }
     };
-    if (r0 + lane < a.count) {
-#pragma unroll 4
-        for (int g = warp; g < a.groups; g += 32) join(__ldcs(a.parts + g * a.count + r0 + lane));
+    if (r0 + row < a.count) {
+        const float2 *p = a.parts + r0 + row;
+        int g = each;
+        for (; g + 7 * 32 < a.groups; g += 8 * 32) {
+            float2 q[8];
+#pragma unroll
+            for (int k = 0; k < 8; k++) q[k] = __ldcs(p + (g + k * 32LL) * a.count);
+#pragma unroll
+            for (int k = 0; k < 8; k++) join(q[k]);
+        }
+        for (; g < a.groups; g += 32) join(__ldcs(p + g * a.count));
     }
-    part[warp][lane] = make_float2(top, sum);
+    part[each][row] = make_float2(top, sum);
     __syncthreads();
     const long long r = r0 + warp;
-    if (r >= a.count) return;
-    const float2 q = part[lane][warp];
-    top = warp_max(q.x);
-    sum = warp_sum(q.x == -INFINITY ? q.y : q.y * ex2(q.x - top));
-    const float lse2 = top + log2f(sum), lse = lse2 * kLn2;
-
-    float label = 0.f, teacher = 0.f, c = 0.f;
-    for (int s = lane; s < a.width; s += 32) {
-        const long long at = s * a.all + r;
-        const float t = a.weight[at];
-        float tau = 0.f;
-        if (t == -1.f) {
-            label = lse - a.z[at];
-            tau = w.x;
-        } else if (t != 0.f) {
-            // a candidate that is no column: NaN; a label: -inf
-            if (t == -INFINITY) label = NAN;
-            else teacher = t == t ? fmaf(t, logf(t) + (lse - a.z[at]), teacher) : NAN;
-            tau = t == -INFINITY ? NAN : w.y * t;
+    float label = 0.f, teacher = 0.f;
+    if (r < a.count) {
+        const float2 q = part[lane][warp];
+        top = warp_max(q.x);
+        sum = warp_sum(q.x == -INFINITY ? q.y : q.y * ex2(q.x - top));
+        const float lse2 = top + log2f(sum), lse = lse2 * kLn2;
+        float c = 0.f;
+        for (int s = lane; s < a.width; s += 32) {
+            const long long at = s * a.all + r;
+            const float t = a.weight[at];
+            float tau = 0.f;
+            if (t == -1.f) {
+                label = lse - a.z[at];
+                tau = w.x;
+            } else if (t != 0.f) {
+                // a candidate that is no column: NaN; a label: -inf
+                if (t == -INFINITY) label = NAN;
+                else teacher = t == t ? fmaf(t, logf(t) + (lse - a.z[at]), teacher) : NAN;
+                tau = t == -INFINITY ? NAN : w.y * t;
+            }
+            c += tau;
+            if (a.info != nullptr) a.weight[at] = tau;
         }
-        c += tau;
-        if (a.info != nullptr) a.weight[at] = tau;
+        label = warp_sum(label);
+        teacher = warp_sum(teacher);
+        c = warp_sum(c);
+        if (lane == 0) {
+            a.losses[a.first + r] = label;
+            a.losses[a.all + a.first + r] = teacher;
+            if (a.info != nullptr) a.info[r] = make_float2(lse2, c);
+        }
     }
-    label = warp_sum(label);
-    teacher = warp_sum(teacher);
-    c = warp_sum(c);
-    if (lane > 0) return;
-    a.losses[a.first + r] = label;
-    a.losses[a.all + a.first + r] = teacher;
-    if (a.info != nullptr) a.info[r] = make_float2(lse2, c);
-}
-
-__global__ void __launch_bounds__(1024) vocab_loss_kernel(const float *losses, long long rows, const Weights weights, float *loss)
-{
-    __shared__ double part[32];
-    __shared__ int2 counted[32];
-    chain_start();
-    chain_wait();
-    const float2 w = weigh(weights, counted);
-    double label = 0., teacher = 0.;
-    for (long long r = threadIdx.x; r < rows; r += 1024) {
-        label += losses[r];
-        teacher += losses[rows + r];
-    }
-    double s = w.x * label + w.y * teacher;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+    __threadfence();
     __syncthreads();
-    if (threadIdx.x >= 32) return;
-    s = part[threadIdx.x];
+    if (threadIdx.x == 0) last = atomicAdd(a.done, 1) == a.blocks - 1;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    // compensated, so that millions of rows lose nothing
+    float2 s = make_float2(0.f, 0.f), low = s;
+    const auto add = [](float &sum, float &low, float x) {
+        const float y = x - low, t = sum + y;
+        low = fabsf(t) < INFINITY ? (t - sum) - y : 0.f;
+        sum = t;
+    };
+#pragma unroll 8
+    for (long long i = threadIdx.x; i < a.all; i += 32 * ROWS) {
+        add(s.x, low.x, __ldcg(a.losses + i));
+        add(s.y, low.y, __ldcg(a.losses + a.all + i));
+    }
+    s.x = warp_sum(s.x);
+    s.y = warp_sum(s.y);
+    if (lane == 0) lost[warp] = s;
+    __syncthreads();
+    if (threadIdx.x > 0) return;
+    s = lost[0];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (threadIdx.x == 0) *loss = rows > 0 ? (float)s : 0.f;
+    for (int i = 1; i < ROWS; i++) {
+        s.x += lost[i].x;
+        s.y += lost[i].y;
+    }
+    *a.loss = w.x * s.x + w.y * s.y;
 }
 
 struct Dz {
@@ -334,7 +394,8 @@ struct Layout {
     long long piece;     // rows of a piece
     int pieces, width, groups;
     linear::Plan dx, dw;
-    size_t off_x, off_w, off_sorted, off_weight, off_z, off_counts, off_losses, off_info, off_parts, off_e, off_dz, off_sum, off_part, total;
+    int marks;
+    size_t off_x, off_w, off_sorted, off_weight, off_starts, off_z, off_counts, off_losses, off_info, off_parts, off_e, off_dz, off_sum, off_part, total;
 };
 Layout plan(const csa_vocab_loss_params &p, bool backward)
 {
@@ -364,8 +425,10 @@ Layout plan(const csa_vocab_loss_params &p, bool backward)
     take(b.off_w, b.stage_w ? staged_bytes(p.dtype, V, K) : 0);
     take(b.off_sorted, (size_t)M * b.width * 4);
     take(b.off_weight, (size_t)M * b.width * 4);
+    b.marks = b.groups + 1;
+    take(b.off_starts, p.slots > 0 ? (size_t)M * b.marks * 2 : 0);
     take(b.off_z, (size_t)M * b.width * 4);
-    take(b.off_counts, (size_t)((M + PREP_ROWS - 1) / PREP_ROWS) * 8);
+    take(b.off_counts, (size_t)((M + ROWS - 1) / ROWS) * 8 + 8);   // and the count of finished blocks
     take(b.off_losses, (size_t)M * 8);
     take(b.off_info, (size_t)b.piece * 8);
     take(b.off_parts, (size_t)b.piece * b.groups * 8);
@@ -438,21 +501,35 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
     g.vocab = V;
     g.sorted = reinterpret_cast<int *>(w + b.off_sorted);
     g.weight = reinterpret_cast<float *>(w + b.off_weight);
-    g.counts = reinterpret_cast<int2 *>(w + b.off_counts);
-    const unsigned blocks = (unsigned)((M + PREP_ROWS - 1) / PREP_ROWS);
-    VOC_TRY(launch_chained(vocab_prepare_kernel, dim3(blocks), 32 * PREP_ROWS, (size_t)g.width * PREP_ROWS * 4, 1, st, g));
+    g.starts = reinterpret_cast<unsigned short *>(w + b.off_starts);
+    g.marks = b.marks;
+    g.done = reinterpret_cast<int *>(w + b.off_counts);
+    g.counts = reinterpret_cast<int2 *>(w + b.off_counts) + 1;
+    const bool single = p.slots == 0;
+    const unsigned blocks = (unsigned)(single ? (M + 255) / 256 : (M + ROWS - 1) / ROWS);
+    if (single) {
+        VOC_TRY(launch_chained(vocab_labels_kernel, dim3(blocks), 256, 0, 1, st, g));
+    } else {
+        const size_t smem = (size_t)((g.width + 3) & ~3) * ROWS * 12;
+        if (smem > 48 << 10) VOC_TRY(cudaFuncSetAttribute(vocab_prepare_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+        VOC_TRY(launch_chained(vocab_prepare_kernel, dim3(blocks), 32 * ROWS, smem, 1, st, g));
+    }
 
     const bool grads = dx != nullptr || dw != nullptr;
     const Weights weights = {g.counts, (int)blocks, p.reduction == 0, p.label_weight, p.teacher_weight};
     float *losses = row_loss != nullptr ? row_loss : reinterpret_cast<float *>(w + b.off_losses);
     float *z = reinterpret_cast<float *>(w + b.off_z);
     float2 *parts = reinterpret_cast<float2 *>(w + b.off_parts), *info = grads ? reinterpret_cast<float2 *>(w + b.off_info) : nullptr;
+    int all_blocks = 0;
+    for (long long first = 0; first < M; first += b.piece) all_blocks += (int)(((M - first < b.piece ? M - first : b.piece) + ROWS - 1) / ROWS);
     for (long long first = 0; first < M; first += b.piece) {
         const long long count = M - first < b.piece ? M - first : b.piece;
         Operand px = ox;
         px.base += first * ox.ld;
         Scores s = {};
         s.ids = g.sorted + first;
+        s.starts = single ? nullptr : g.starts + first * g.marks;
+        s.lds = g.marks;
         s.z = z + first;
         s.slots = g.width;
         s.ld = M;
@@ -461,8 +538,10 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
         s.e = grads ? w + b.off_e : nullptr;
         s.lde = ld;
         VOC_TRY(launch_scores(px, ow, count, V, K, planes, s, sms, st));
-        const Rows rows = {parts, b.groups, g.width, first, count, M, g.sorted + first, g.weight + first, z + first, info, losses, weights};
-        VOC_TRY(launch_chained(vocab_rows_kernel, dim3((unsigned)((count + 31) / 32)), 1024, 0, 1, st, rows));
+        const int row_blocks = (int)((count + ROWS - 1) / ROWS);
+        const Rows rows = {parts, b.groups, g.width, first, count, M, g.weight + first, z + first, info, losses, weights,
+                           g.done, all_blocks, loss};
+        VOC_TRY(launch_chained(vocab_rows_kernel, dim3((unsigned)row_blocks), 32 * ROWS, 0, 1, st, rows));
         if (!grads) continue;
         Dz d = {};
         d.e = w + b.off_e;
@@ -474,7 +553,7 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
         d.info = info;
         d.count = count;
         d.all = M;
-        d.sorted = rows.sorted;
+        d.sorted = g.sorted + first;
         d.tau = rows.weight;
         d.z = rows.z;
         d.width = g.width;
@@ -527,7 +606,6 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
             VOC_TRY(product(q, st));
         }
     }
-    VOC_TRY(launch_chained(vocab_loss_kernel, dim3(1), 1024, 0, 1, st, losses, M, weights, loss));
     if (dw != nullptr && b.pieces > 1 && p.dtype == CSA_BF16) {
         const long long n = V * K;
         VOC_TRY(launch_chained(vocab_round_kernel, dim3((unsigned)((n + 2047) / 2048)), 256, 0, 1, st, reinterpret_cast<float *>(w + b.off_sum), n, (bf16 *)dw));

@@ -10,8 +10,8 @@
 // scores.  The exponentials of a group are at most 1, so that fp16 holds them to 2^-12 where they count (bf16 to 2^-9; the
 // gradient is rounded to bf16 once more).
 //
-// A row's targets are few columns among many: their list is sorted, each lane finds its group's part of it before the
-// sums are there, and looks for the columns only where a lane of its warp has one.
+// A row's targets are few columns among many: their list is sorted, and marks say which part of it a group has.  Where a
+// lane of a warp has a target, every lane selects one of its 64 registers.
 #include "k_linear_pipe.cuh"
 #include "k_vocab.cuh"
 
@@ -58,6 +58,26 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// v[col] of 64 registers, 0 <= col < 64 (anything else: some of them): every lane its own, in 63 selections
+__device__ __forceinline__ float pick(const float (&v)[GROUP], int col)
+{
+    float r[4];
+#pragma unroll
+    for (int c = 0; c < 4; c++) {
+        float t[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++) t[k] = col & 1 ? v[16 * c + 2 * k + 1] : v[16 * c + 2 * k];
+#pragma unroll
+        for (int k = 0; k < 4; k++) t[k] = col & 2 ? t[2 * k + 1] : t[2 * k];
+        t[0] = col & 4 ? t[1] : t[0];
+        t[1] = col & 4 ? t[3] : t[2];
+        r[c] = col & 8 ? t[1] : t[0];
+    }
+    r[0] = col & 16 ? r[1] : r[0];
+    r[1] = col & 16 ? r[3] : r[2];
+    return col & 32 ? r[1] : r[0];
+}
+
 template <int CG, int BN, int P, int EW>
 __global__ void __launch_bounds__(64 + 32 * EW, 1)
 vocab_scores_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
@@ -81,21 +101,46 @@ vocab_scores_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     } else {
         const int quad = warp & 3, side = (warp - 2) >> 2;
         const Buffer b = {smem + Z::TURN + (warp - 2) * 4096, lane};
-        const float c2 = s.alpha * kLog2e;
+        const float c2 = fabsf(s.alpha) * kLog2e;   // > 0
+        // Rows, columns and slots are below 2^31, and so are a tile's ends.
+        const int M = (int)a.M, N = (int)a.N;
+        const auto place = [&](int u, int &m, int &n0) {
+            const Unit x = unit_of<BN>(a, u);
+            m = (x.m * CG + (int)p.rank) * BM + quad * 32 + lane;
+            n0 = (int)x.n0 + side * GROUP;
+        };
+        // A unit's targets of this lane: where they begin and end is asked for a unit ahead, the first two while the last
+        // unit's scores are reduced.  (Found when their unit came, 64 of 32768 columns cost a product of 4096 x 1024 50 us of 227.)
+        int first = 0, end = 0, next = NONE, after = NONE;
+        const auto ask_marks = [&](int u, int &b, int &e) {
+            int m, n0;
+            b = e = 0;
+            if (u >= a.units) return;
+            place(u, m, n0);
+            if (m >= M || n0 >= N) return;
+            e = 1;
+            if (s.starts != nullptr) {
+                const unsigned short *mark = s.starts + m * (long long)s.lds + n0 / GROUP;
+                b = __ldg(mark);
+                e = __ldg(mark + 1);
+            }
+        };
+        const auto ask_targets = [&](int u, int b, int e) {
+            int m, n0;
+            next = after = NONE;
+            if (b >= e) return;
+            place(u, m, n0);
+            next = __ldg(s.ids + b * s.ld + m);
+            if (b + 1 < e) after = __ldg(s.ids + (b + 1) * s.ld + m);
+        };
+        ask_marks(p.u0, first, end);
+        ask_targets(p.u0, first, end);
         int tc = 0;
         for (int u = p.u0; u < a.units; u += p.ustep) {
-            const Unit x = unit_of<BN>(a, u);
-            const long long m0 = ((long long)x.m * CG + p.rank) * BM + quad * 32, m = m0 + lane, n0 = x.n0 + side * GROUP;
-            // the row's first target from n0 on
-            int at = 0, next = NONE;
-            if (m < a.M && n0 < a.N) {
-                for (int end = s.slots; at < end;) {
-                    const int mid = (at + end) >> 1;
-                    if (__ldg(s.ids + mid * s.ld + m) < n0) at = mid + 1;
-                    else end = mid;
-                }
-                if (at < s.slots) next = __ldg(s.ids + at * s.ld + m);
-            }
+            int m, n0, first_then, end_then;
+            place(u, m, n0);
+            const int m0 = m - lane;
+            ask_marks(u + p.ustep, first_then, end_then);
             float v[GROUP] = {};
             for (int it = 0; it < a.ksteps; it += CHUNK, tc++) {
                 p.wait_sums(tc);
@@ -109,26 +154,42 @@ vocab_scores_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
                     for (int k = 0; k < 16; k++) v[g + k] += w[k];
                 }
             }
-            if (m0 >= a.M || n0 >= a.N) continue;
-            if (__any_sync(0xffffffffu, next < n0 + GROUP)) {
-#pragma unroll
-                for (int k = 0; k < GROUP; k++) {
-                    while (next == n0 + k) {   // a column may be named more than once
-                        s.z[at * s.ld + m] = s.alpha * v[k];
-                        next = ++at < s.slots ? __ldg(s.ids + at * s.ld + m) : NONE;
+            // this unit's targets, whose scores are wanted; then the next unit's are asked for
+            int left = end - first, col = next - n0, col2 = after - n0;
+            if (s.starts == nullptr && (col < 0 || col >= GROUP)) left = 0;
+            float *z = s.z + first * s.ld + m;
+            const int *rest = s.ids + (first + 2) * s.ld + m;
+            first = first_then;
+            end = end_then;
+            ask_targets(u + p.ustep, first, end);
+            if (m0 >= M || n0 >= N) continue;
+            while (__any_sync(0xffffffffu, left > 0)) {
+                const float x = pick(v, col);
+                if (left > 0) {
+                    *z = s.alpha * x;
+                    z += s.ld;
+                    col = col2;
+                    if (--left > 1) {
+                        col2 = __ldg(rest) - n0;
+                        rest += s.ld;
                     }
                 }
             }
-            if (n0 + GROUP > a.N) {   // columns that do not exist
-                const int valid = (int)(a.N - n0);
-                const float none = c2 < 0.f ? INFINITY : -INFINITY;
+            if (s.alpha < 0.f) {
+#pragma unroll
+                for (int k = 0; k < GROUP; k++) v[k] = -v[k];
+            }
+            if (N - n0 < GROUP) {   // columns that do not exist
+                const int valid = N - n0;
 #pragma unroll
                 for (int k = 0; k < GROUP; k++)
-                    if (k >= valid) v[k] = none;
+                    if (k >= valid) v[k] = -INFINITY;
             }
-            float top = -INFINITY;
+            float top = v[0];
 #pragma unroll
-            for (int k = 0; k < GROUP; k++) top = fmaxf(top, v[k] * c2);
+            for (int k = 1; k + 1 < GROUP; k += 2) top = fmaxf(top, fmaxf(v[k], v[k + 1]));
+            top = fmaxf(top, v[GROUP - 1]);
+            top = top == top ? top * c2 : -INFINITY;   // of NaN alone: their sum is NaN
             const float ref = top == -INFINITY ? 0.f : top;
             float2 sum = make_float2(0.f, 0.f), more = sum;
 #pragma unroll
@@ -142,7 +203,7 @@ vocab_scores_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
                 sum = add2(sum, make_float2(v[k], v[k + 1]));
                 more = add2(more, make_float2(v[k + 2], v[k + 3]));
             }
-            if (m < a.M) s.parts[n0 / GROUP * a.M + m] = make_float2(top, (sum.x + more.x) + (sum.y + more.y));
+            if (m < M) s.parts[n0 / GROUP * a.M + m] = make_float2(top, (sum.x + more.x) + (sum.y + more.y));
             if (s.e == nullptr) continue;
             if constexpr (P == 1) {
                 if (lane == 0) bulk_wait_read();   // the last group has left the buffer
@@ -160,7 +221,7 @@ vocab_scores_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) {
-                    tma_store_3d(&map_e, b.p, (int)n0, (int)m0, 0);
+                    tma_store_3d(&map_e, b.p, n0, m0, 0);
                     bulk_commit();
                 }
             } else {
@@ -169,7 +230,7 @@ vocab_scores_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
                     float w[C];
 #pragma unroll
                     for (int k = 0; k < C; k++) w[k] = v[g + k];
-                    if (n0 + g < a.N) tma_tile<float>(&map_e, w, m0, n0 + g, 0, false, true, b);
+                    if (n0 + g < N) tma_tile<float>(&map_e, w, m0, n0 + g, 0, false, true, b);
                 }
             }
         }
