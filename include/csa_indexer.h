@@ -380,7 +380,8 @@ csa_status csa_layernorm_fwd(const csa_layernorm_params *p, const void *x, const
 
 /* The gradients for dy, with h_j = (x_j - mean) rstd and a_j = dy_j weight_j:
  *   dx_j = rstd (a_j - mean(a) - h_j mean(a h)) [rows, cols],  dweight = sum over rows of dy_j h_j [cols],  dbias = sum of dy_j
- * Each of dx, dweight, dbias may be NULL and is then not computed.  dx may be dy or x where its stride is cols.  rows = 0
+ * Each of dx, dweight, dbias may be NULL and is then not computed; x and stats are read for any of them.  dx may be dy or x
+ * where its stride is cols.  rows = 0
  * gives dweight = 0 and dbias = 0.  The same call gives the same bits every time (no atomics). */
 csa_status csa_layernorm_bwd(const csa_layernorm_params *p, const void *dy, const void *x, const void *weight,
                              const float *stats, void *dx, void *dweight, void *dbias, void *workspace,

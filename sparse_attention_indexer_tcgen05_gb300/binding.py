@@ -828,7 +828,7 @@ def csa_layernorm_bwd(p: LayerNormParams, dy, x, weight=None, stats=None, need_d
     c, dev = p.c, _on_cuda(dy, "dy")
     M, N = c.rows, c.cols
     _check_rows(dy, "dy", p.value_dtype, dev, M, N, c.dy_stride)
-    if need_dx or need_dweight:
+    if need_dx or need_dweight or need_dbias:
         _check_rows(x, "x", p.value_dtype, dev, M, N, c.x_stride)
         _check_flat(stats, "stats", torch.float32, dev, 2 * M)
     if weight is not None:

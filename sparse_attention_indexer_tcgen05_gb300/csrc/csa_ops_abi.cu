@@ -364,7 +364,7 @@ csa_status csa_layernorm_bwd(const csa_layernorm_params *p, const void *dy, cons
     csa_layernorm_params q;
     CSA_TRY(check_layernorm(p, &q));
     CSA_TRY(need(dy, q.rows));
-    if (dx != nullptr || dweight != nullptr) {
+    if (dx != nullptr || dweight != nullptr || dbias != nullptr) {
         CSA_TRY(need(x, q.rows));
         if (q.rows > 0 && stats == nullptr) return CSA_ERR_INVALID_ARG;
         CSA_TRY(need_scalar(stats, 4));

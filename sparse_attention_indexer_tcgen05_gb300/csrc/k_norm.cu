@@ -3,10 +3,14 @@
 //   mean = sum_j x_j / n,  rstd = 1 / sqrt(sum_j (x_j - mean)^2 / n + eps),  h_j = (x_j - mean) rstd,  y_j = h_j w_j + b_j
 //   a_j = dy_j w_j,  dx_j = rstd (a_j - mean(a) - h_j mean(a h)),  dw_j = sum over rows of dy_j h_j,  db_j = sum of dy_j
 //
-// Bound by memory: x read and y written once (backward: x and dy read, dx written).  A row's values stay in the registers of
-// LANES threads, so that the variance is a second pass over registers and not a difference of two large sums.  The backward's
-// threads keep their columns over all the rows that their block takes, and so the gradients of their weights; the blocks'
-// sums are joined in a fixed order by a second kernel: the same bits every time.
+// Bound by memory: x read and y written once (backward: x and dy read, dx written).  The variance is a second pass over the row
+// where it lies (registers or shared memory), not a difference of two large sums.  The backward's threads keep their columns over all the
+// rows that their block takes, and so the gradients of their weights; the blocks' sums are joined in a fixed order by a
+// second kernel: the same bits every time.
+//
+// Rows of up to 512 values lie in the registers of a part of a warp.  Longer ones pass through a ring of rows in a block's
+// shared memory, filled by asynchronous copies, in steps: while a row's sum is taken, the row before it is a step further,
+// so that no step waits for a sum across the block and a row costs one barrier.
 #include "k_linear.cuh"
 
 #include <type_traits>
@@ -18,122 +22,151 @@ using bf16 = __nv_bfloat16;
 using linear::chain_start;
 using linear::chain_wait;
 using linear::launch_chained;
+using ptx::add2;
+using ptx::fma2;
+using ptx::mul2;
 
 __device__ __forceinline__ float from_value(float x) { return x; }
 __device__ __forceinline__ float from_value(bf16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// The two parameters, of either type
-__device__ __forceinline__ float param(const void *p, int f32, long long i)
-{
-    return f32 ? __ldg(static_cast<const float *>(p) + i) : __bfloat162float(static_cast<const bf16 *>(p)[i]);
-}
-
-// Values of a row that a thread holds: CH pieces of 8.  VEC: 8 neighbouring ones each, as vectors (rows on 16-byte
-// boundaries, whole pieces); else every LANES-th one, so that a warp's accesses are neighbours whatever the alignment.
-template <int LANES, int CH, bool VEC> __device__ __forceinline__ int column(int t, int c, int k)
-{
-    return VEC ? (c * LANES + t) * 8 + k : (c * 8 + k) * LANES + t;
-}
-
-template <typename T> __device__ __forceinline__ void load_vec(const T *p, float (&x)[8])
-{
-    if constexpr (sizeof(T) == 4) {
-        const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    } else {
-        const uint4 a = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+// 8 neighbouring values as they lie in memory, and as four pairs
+template <typename T> struct Eight;
+template <> struct Eight<bf16> {
+    uint4 r;
+    __device__ __forceinline__ void load(const void *p) { r = *static_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void pairs(float2 (&x)[4]) const
+    {
+        const uint32_t u[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-        for (int k = 0; k < 8; k++) x[k] = __uint_as_float(k % 2 == 0 ? u[k / 2] << 16 : u[k / 2] & 0xffff0000u);
+        for (int k = 0; k < 4; k++) x[k] = make_float2(__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xffff0000u));
     }
-}
-template <typename T> __device__ __forceinline__ void store_vec(T *p, const float (&x)[8])
+};
+template <> struct Eight<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const void *p)
+    {
+        a = static_cast<const float4 *>(p)[0];
+        b = static_cast<const float4 *>(p)[1];
+    }
+    __device__ __forceinline__ void pairs(float2 (&x)[4]) const
+    {
+        x[0] = make_float2(a.x, a.y);
+        x[1] = make_float2(a.z, a.w);
+        x[2] = make_float2(b.x, b.y);
+        x[3] = make_float2(b.z, b.w);
+    }
+};
+__device__ __forceinline__ void store_pairs(bf16 *p, const float2 (&x)[4])
 {
-    if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
-        *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
-        uint32_t u[4];
+    uint32_t u[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[k].x, x[k].y);
+        u[k] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+__device__ __forceinline__ void store_pairs(float *p, const float2 (&x)[4])
+{
+    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+}
+
+// The columns of a thread: pieces of 8 neighbouring ones, as they lie in the aligned vectors of memory.  SHIFT: rows of a block
+// (or of a part of a warp) start `shift` values behind a 16-byte boundary, all of them the same, because the rows that it takes
+// are a multiple of 8 apart; the vectors at a row's ends hold columns that are not its own.  So rows of any length
+// move in whole vectors (value by value, 5003 x 1537 in fp32 took 62 us backward).
+template <int LANES, bool SHIFT> struct Columns {
+    int n, shift, t;
+    __device__ __forceinline__ int first(int c) const { return (c * LANES + t) * 8 - (SHIFT ? shift : 0); }
+    __device__ __forceinline__ bool has(int c) const { return first(c) < n; }
+    __device__ __forceinline__ bool full(int c) const { return !SHIFT || (first(c) >= 0 && first(c) + 8 <= n); }
+    // 0 where columns are not the row's
+    __device__ __forceinline__ void clip(float2 (&x)[4], int c) const
+    {
+        if (full(c)) return;
+        const int j = first(c);
 #pragma unroll
         for (int k = 0; k < 4; k++) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
-            u[k] = *reinterpret_cast<const uint32_t *>(&h);
+            if ((unsigned)(j + 2 * k) >= (unsigned)n) x[k].x = 0.f;
+            if ((unsigned)(j + 2 * k + 1) >= (unsigned)n) x[k].y = 0.f;
         }
-        *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    template <typename T> __device__ __forceinline__ void store(T *row, int c, const float2 (&x)[4]) const
+    {
+        const int j = first(c);
+        if (full(c)) {
+            store_pairs(row + j, x);
+            return;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            if ((unsigned)(j + 2 * k) < (unsigned)n) row[j + 2 * k] = from_f<T>(x[k].x);
+            if ((unsigned)(j + 2 * k + 1) < (unsigned)n) row[j + 2 * k + 1] = from_f<T>(x[k].y);
+        }
+    }
+    // a parameter, of either type (as scalars they took longer than the rows: 65536 x 4096 forward 603 us)
+    __device__ __forceinline__ void param(const void *p, int f32, int c, float missing, float2 (&w)[4]) const
+    {
+#pragma unroll
+        for (int k = 0; k < 4; k++) w[k] = both(missing);
+        if (p == nullptr || !has(c)) return;
+        const int j = first(c);
+        if constexpr (SHIFT) {
+            const auto at = [&](int i) {
+                if ((unsigned)i >= (unsigned)n) return 0.f;
+                return f32 ? __ldg(static_cast<const float *>(p) + i) : __bfloat162float(static_cast<const bf16 *>(p)[i]);
+            };
+#pragma unroll
+            for (int k = 0; k < 4; k++) w[k] = make_float2(at(j + 2 * k), at(j + 2 * k + 1));
+        } else if (f32) {
+            Eight<float> e;
+            e.load(static_cast<const float *>(p) + j);
+            e.pairs(w);
+        } else {
+            Eight<bf16> e;
+            e.load(static_cast<const bf16 *>(p) + j);
+            e.pairs(w);
+        }
+    }
+};
+// Values between a row's start and the 16-byte boundary before it
+template <typename T> __device__ __forceinline__ int shift_of(long long r, long long stride) { return (int)(r * stride & (16 / sizeof(T) - 1)); }
+
+// The piece of 8 values at p that may lie across an argument's `end`: nothing from there on is read.
+template <typename T> __device__ __forceinline__ void load_piece(Eight<T> &e, const T *p, const T *end)
+{
+    if (p + 8 <= end) {
+        e.load(p);
+        return;
+    }
+    const uint4 *q = reinterpret_cast<const uint4 *>(p);
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (sizeof(T) == 2) {
+        e.r = linear::load16(q, end);
+    } else {
+        const uint4 u = (const void *)q < (const void *)end ? linear::load16(q, end) : zero, v = (const void *)(q + 1) < (const void *)end ? linear::load16(q + 1, end) : zero;
+        e.a = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
+        e.b = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
     }
 }
 
-// Columns that do not exist hold 0.
-template <typename T, int LANES, int CH, bool VEC> __device__ __forceinline__ void load_row(const T *row, int n, int t, float (&x)[CH][8])
+__device__ __forceinline__ float sum8(const float2 (&x)[4])
 {
-#pragma unroll
-    for (int c = 0; c < CH; c++) {
-        if constexpr (VEC) {
-            if (column<LANES, CH, true>(t, c, 0) < n) {
-                load_vec(row + column<LANES, CH, true>(t, c, 0), x[c]);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; k++) x[c][k] = 0.f;
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; k++) {
-                const int j = column<LANES, CH, false>(t, c, k);
-                x[c][k] = j < n ? from_value(row[j]) : 0.f;
-            }
-        }
-    }
+    const float2 s = add2(add2(x[0], x[1]), add2(x[2], x[3]));
+    return s.x + s.y;
 }
-template <typename T, int LANES, int CH, bool VEC> __device__ __forceinline__ void store_row(T *row, int n, int t, const float (&y)[CH][8])
+__device__ __forceinline__ float dot8(const float2 (&x)[4], const float2 (&y)[4])
 {
-#pragma unroll
-    for (int c = 0; c < CH; c++) {
-        if constexpr (VEC) {
-            if (column<LANES, CH, true>(t, c, 0) < n) store_vec(row + column<LANES, CH, true>(t, c, 0), y[c]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; k++) {
-                const int j = column<LANES, CH, false>(t, c, k);
-                if (j < n) row[j] = from_f<T>(y[c][k]);
-            }
-        }
-    }
+    const float2 s = fma2(x[3], y[3], fma2(x[2], y[2], fma2(x[1], y[1], mul2(x[0], y[0]))));
+    return s.x + s.y;
 }
-template <int LANES, int CH, bool VEC>
-__device__ __forceinline__ void load_param(const void *p, int f32, int n, int t, float missing, float (&w)[CH][8])
+template <int LANES> __device__ __forceinline__ float lane_sum(float s)
 {
 #pragma unroll
-    for (int c = 0; c < CH; c++)
-#pragma unroll
-        for (int k = 0; k < 8; k++) {
-            const int j = column<LANES, CH, VEC>(t, c, k);
-            w[c][k] = p != nullptr && j < n ? param(p, f32, j) : missing;
-        }
-}
-
-// Sums over the LANES threads of a row, of V values at once.  Rows of more than a warp have the block to themselves.
-template <int LANES, int V> __device__ __forceinline__ void row_sums(float (&s)[V], float *part)
-{
-#pragma unroll
-    for (int v = 0; v < V; v++)
-#pragma unroll
-        for (int o = (LANES < 32 ? LANES : 32) / 2; o > 0; o >>= 1) s[v] += __shfl_xor_sync(0xffffffffu, s[v], o);
-    if constexpr (LANES > 32) {
-        constexpr int W = LANES / 32;
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        __syncthreads();  // the last sums have been read
-        if (lane == 0) {
-#pragma unroll
-            for (int v = 0; v < V; v++) part[v * W + warp] = s[v];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int v = 0; v < V; v++) {
-            s[v] = lane < W ? part[v * W + lane] : 0.f;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s[v] += __shfl_xor_sync(0xffffffffu, s[v], o);
-        }
-    }
+    for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
 }
 
 struct Fwd {
@@ -144,52 +177,6 @@ struct Fwd {
     int n, param_f32;
     float eps;
 };
-
-constexpr int threads_of(int lanes) { return lanes <= 32 ? 256 : lanes; }
-
-template <typename T, int LANES, int CH, bool VEC> __global__ void __launch_bounds__(threads_of(LANES)) norm_fwd_kernel(const Fwd a)
-{
-    constexpr int R = threads_of(LANES) / LANES;
-    __shared__ float part[2 * (LANES / 32 + 1)];
-    chain_start();
-    chain_wait();
-    const int t = threadIdx.x % LANES;
-    const long long r = (long long)blockIdx.x * R + threadIdx.x / LANES;
-    const bool live = r < a.rows;   // the warp's shuffles need all of its lanes
-    const int n = live ? a.n : 0;
-    float x[CH][8];
-    load_row<T, LANES, CH, VEC>(static_cast<const T *>(a.x) + r * a.stride, n, t, x);
-    float s[1] = {0.f};
-#pragma unroll
-    for (int c = 0; c < CH; c++)
-#pragma unroll
-        for (int k = 0; k < 8; k++) s[0] += x[c][k];
-    row_sums<LANES>(s, part);
-    const float mean = s[0] / (float)a.n;
-    s[0] = 0.f;
-#pragma unroll
-    for (int c = 0; c < CH; c++)
-#pragma unroll
-        for (int k = 0; k < 8; k++) {
-            x[c][k] = column<LANES, CH, VEC>(t, c, k) < n ? x[c][k] - mean : 0.f;
-            s[0] = fmaf(x[c][k], x[c][k], s[0]);
-        }
-    row_sums<LANES>(s, part);
-    const float rstd = 1.f / sqrtf(s[0] / (float)a.n + a.eps);
-    float w[CH][8], b[CH][8];
-    load_param<LANES, CH, VEC>(a.weight, a.param_f32, n, t, 1.f, w);
-    load_param<LANES, CH, VEC>(a.bias, a.param_f32, n, t, 0.f, b);
-#pragma unroll
-    for (int c = 0; c < CH; c++)
-#pragma unroll
-        for (int k = 0; k < 8; k++) x[c][k] = fmaf(x[c][k] * rstd, w[c][k], b[c][k]);
-    store_row<T, LANES, CH, VEC>(static_cast<T *>(a.y) + r * a.n, n, t, x);
-    if (a.stats != nullptr && live && t == 0) {
-        a.stats[r] = mean;
-        a.stats[a.rows + r] = rstd;
-    }
-}
-
 struct Bwd {
     const void *dy, *x, *weight;
     const float *stats;
@@ -199,128 +186,611 @@ struct Bwd {
     int n, param_f32;
 };
 
-template <typename T, int LANES, int CH, bool VEC> __global__ void __launch_bounds__(threads_of(LANES)) norm_bwd_kernel(const Bwd a)
+// ------------------------------------------------------------------ rows of up to 512 values
+
+constexpr int U = 2;   // rows of a thread on their way at a time
+
+template <typename T, int LANES, int CH, bool SHIFT> __global__ void __launch_bounds__(256) norm_fwd_short_kernel(const Fwd a)
 {
-    constexpr int R = threads_of(LANES) / LANES;
-    __shared__ float part[2 * (LANES / 32 + 1)];
-    __shared__ float across[R > 1 ? R : 1][R > 1 ? 2 : 1][R > 1 ? LANES * CH * 8 : 1];
+    constexpr int R = 256 / LANES;   // a multiple of 8, as is the grid times it: the shift is the group's own
     chain_start();
     chain_wait();
-    const int t = threadIdx.x % LANES, group = threadIdx.x / LANES;
-    float w[CH][8], dw[CH][8] = {}, db[CH][8] = {};
-    load_param<LANES, CH, VEC>(a.weight, a.param_f32, a.n, t, 1.f, w);
+    const int group = threadIdx.x / LANES;
+    const Columns<LANES, SHIFT> cols = {a.n, shift_of<T>(group, a.stride), (int)threadIdx.x % LANES};
+    const T *end = static_cast<const T *>(a.x) + (a.rows - 1) * a.stride + a.n;
     const float inv_n = 1.f / (float)a.n;
-    for (long long r0 = (long long)blockIdx.x * R; r0 < a.rows; r0 += (long long)gridDim.x * R) {
-        const long long r = r0 + group;
-        const bool live = r < a.rows;
-        const int n = live ? a.n : 0;
-        float x[CH][8], d[CH][8];
-        load_row<T, LANES, CH, VEC>(static_cast<const T *>(a.x) + r * a.x_stride, n, t, x);
-        load_row<T, LANES, CH, VEC>(static_cast<const T *>(a.dy) + r * a.dy_stride, n, t, d);
-        const float mean = live ? __ldg(a.stats + r) : 0.f, rstd = live ? __ldg(a.stats + a.rows + r) : 0.f;
-        float s[2] = {0.f, 0.f};
+    float2 w[CH][4], b[CH][4];
+    bool loaded = false;
+    for (long long r0 = (long long)blockIdx.x * R * U; r0 < a.rows; r0 += (long long)gridDim.x * R * U) {
+        Eight<T> raw[U][CH];
 #pragma unroll
-        for (int c = 0; c < CH; c++)
+        for (int u = 0; u < U; u++) {
+            const long long r = r0 + u * R + group;
+            const T *row = static_cast<const T *>(a.x) + r * a.stride;
 #pragma unroll
-            for (int k = 0; k < 8; k++) {
-                x[c][k] = column<LANES, CH, VEC>(t, c, k) < n ? (x[c][k] - mean) * rstd : 0.f;
-                dw[c][k] = fmaf(d[c][k], x[c][k], dw[c][k]);
-                db[c][k] += d[c][k];
-                d[c][k] *= w[c][k];
-                s[0] += d[c][k];
-                s[1] = fmaf(d[c][k], x[c][k], s[1]);
+            for (int c = 0; c < CH; c++) {
+                raw[u][c] = Eight<T>();
+                if (r < a.rows && cols.has(c)) load_piece(raw[u][c], row + cols.first(c), end);
             }
-        if (a.dx != nullptr) {
-            row_sums<LANES>(s, part);
-            const float ma = s[0] * inv_n, mh = s[1] * inv_n;
-#pragma unroll
-            for (int c = 0; c < CH; c++)
-#pragma unroll
-                for (int k = 0; k < 8; k++) x[c][k] = rstd * (d[c][k] - ma - x[c][k] * mh);
-            store_row<T, LANES, CH, VEC>(static_cast<T *>(a.dx) + r * a.n, n, t, x);
         }
-    }
-    if (a.parts == nullptr) return;
-    float *out = a.parts + (long long)blockIdx.x * 2 * a.n;
-    if constexpr (R > 1) {
+        if (!loaded) {
 #pragma unroll
-        for (int c = 0; c < CH; c++)
-#pragma unroll
-            for (int k = 0; k < 8; k++) {
-                across[group][0][column<LANES, CH, VEC>(t, c, k)] = dw[c][k];
-                across[group][1][column<LANES, CH, VEC>(t, c, k)] = db[c][k];
+            for (int c = 0; c < CH; c++) {
+                cols.param(a.weight, a.param_f32, c, 1.f, w[c]);
+                cols.param(a.bias, a.param_f32, c, 0.f, b[c]);
             }
-        __syncthreads();
-        for (int i = threadIdx.x; i < 2 * a.n; i += blockDim.x) {
-            const int which = i >= a.n, j = i - which * a.n;
-            float v = 0.f;
-#pragma unroll
-            for (int g = 0; g < R; g++) v += across[g][which][j];
-            out[i] = v;
+            loaded = true;
         }
-    } else {
 #pragma unroll
-        for (int c = 0; c < CH; c++)
+        for (int u = 0; u < U; u++) {
+            const long long r = r0 + u * R + group;
+            float2 x[CH][4];
+            float s = 0.f;
 #pragma unroll
-            for (int k = 0; k < 8; k++) {
-                const int j = column<LANES, CH, VEC>(t, c, k);
-                if (j < a.n) {
-                    out[j] = dw[c][k];
-                    out[a.n + j] = db[c][k];
-                }
+            for (int c = 0; c < CH; c++) {
+                raw[u][c].pairs(x[c]);
+                cols.clip(x[c], c);
+                s += sum8(x[c]);
             }
+            const float mean = lane_sum<LANES>(s) * inv_n;
+            s = 0.f;
+#pragma unroll
+            for (int c = 0; c < CH; c++) {
+#pragma unroll
+                for (int k = 0; k < 4; k++) x[c][k] = add2(x[c][k], both(-mean));
+                cols.clip(x[c], c);
+                if (cols.has(c)) s += dot8(x[c], x[c]);
+            }
+            const float rstd = 1.f / sqrtf(lane_sum<LANES>(s) * inv_n + a.eps);
+            if (r >= a.rows) continue;
+#pragma unroll
+            for (int c = 0; c < CH; c++) {
+#pragma unroll
+                for (int k = 0; k < 4; k++) x[c][k] = fma2(mul2(x[c][k], both(rstd)), w[c][k], b[c][k]);
+                if (cols.has(c)) cols.store(static_cast<T *>(a.y) + r * a.n, c, x[c]);
+            }
+            if (a.stats != nullptr && cols.t == 0) {
+                a.stats[r] = mean;
+                a.stats[a.rows + r] = rstd;
+            }
+        }
     }
 }
 
-// The blocks' sums joined: 32 columns a block, 32 threads a column.
-__global__ void __launch_bounds__(1024) norm_join_kernel(const float *parts, int blocks, int n, void *dw, void *db, int param_f32)
+template <typename T, int LANES, int CH, bool SHIFT> __global__ void __launch_bounds__(256, CH == 1 ? 3 : 2) norm_bwd_short_kernel(const Bwd a)
 {
-    __shared__ float part[32][33];
+    constexpr int R = 256 / LANES;
+    __shared__ float across[R][2][LANES * CH * 8];
     chain_start();
     chain_wait();
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const long long i = (long long)blockIdx.x * 32 + tx;
+    const int group = threadIdx.x / LANES;
+    const Columns<LANES, SHIFT> cols = {a.n, shift_of<T>(group, a.x_stride), (int)threadIdx.x % LANES};
+    const T *end_x = static_cast<const T *>(a.x) + (a.rows - 1) * a.x_stride + a.n, *end_d = static_cast<const T *>(a.dy) + (a.rows - 1) * a.dy_stride + a.n;
+    const float inv_n = 1.f / (float)a.n;
+    float2 w[CH][4], dw[CH][4], db[CH][4];
+#pragma unroll
+    for (int c = 0; c < CH; c++)
+#pragma unroll
+        for (int k = 0; k < 4; k++) dw[c][k] = db[c][k] = both(0.f);
+    bool loaded = false;
+    for (long long r0 = (long long)blockIdx.x * R * U; r0 < a.rows; r0 += (long long)gridDim.x * R * U) {
+        Eight<T> rx[U][CH], rd[U][CH];
+        float mean[U], rstd[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const long long r = r0 + u * R + group;
+            const bool live = r < a.rows;
+#pragma unroll
+            for (int c = 0; c < CH; c++) {
+                rx[u][c] = rd[u][c] = Eight<T>();
+                if (live && cols.has(c)) {
+                    load_piece(rx[u][c], static_cast<const T *>(a.x) + r * a.x_stride + cols.first(c), end_x);
+                    load_piece(rd[u][c], static_cast<const T *>(a.dy) + r * a.dy_stride + cols.first(c), end_d);
+                }
+            }
+            mean[u] = live ? __ldg(a.stats + r) : 0.f;
+            rstd[u] = live ? __ldg(a.stats + a.rows + r) : 0.f;
+        }
+        if (!loaded) {
+#pragma unroll
+            for (int c = 0; c < CH; c++) cols.param(a.weight, a.param_f32, c, 1.f, w[c]);
+            loaded = true;
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const long long r = r0 + u * R + group;
+            float2 h[CH][4], d[CH][4];
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int c = 0; c < CH; c++) {
+                rx[u][c].pairs(h[c]);
+                rd[u][c].pairs(d[c]);
+                cols.clip(h[c], c);   // what lies beside the row need not be finite
+                cols.clip(d[c], c);   // d is 0 where there is no row or column
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    h[c][k] = mul2(add2(h[c][k], both(-mean[u])), both(rstd[u]));
+                    dw[c][k] = fma2(d[c][k], h[c][k], dw[c][k]);
+                    db[c][k] = add2(db[c][k], d[c][k]);
+                    d[c][k] = mul2(d[c][k], w[c][k]);
+                }
+                s0 += sum8(d[c]);
+                s1 += dot8(d[c], h[c]);
+            }
+            if (a.dx == nullptr) continue;
+            const float ma = lane_sum<LANES>(s0) * inv_n, mh = lane_sum<LANES>(s1) * inv_n;
+            if (r >= a.rows) continue;
+#pragma unroll
+            for (int c = 0; c < CH; c++) {
+#pragma unroll
+                for (int k = 0; k < 4; k++) h[c][k] = mul2(both(rstd[u]), fma2(h[c][k], both(-mh), add2(d[c][k], both(-ma))));
+                if (cols.has(c)) cols.store(static_cast<T *>(a.dx) + r * a.n, c, h[c]);
+            }
+        }
+    }
+    if (a.parts == nullptr) return;
+    // by column: the groups' shifts differ
+    if constexpr (SHIFT) {
+        for (int i = threadIdx.x; i < R * 2 * LANES * CH * 8; i += 256) (&across[0][0][0])[i] = 0.f;
+        __syncthreads();
+    }
+#pragma unroll
+    for (int c = 0; c < CH; c++) {
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            const int j = cols.first(c) + k;
+            if ((unsigned)j < (unsigned)a.n) {
+                across[group][0][j] = k % 2 == 0 ? dw[c][k / 2].x : dw[c][k / 2].y;
+                across[group][1][j] = k % 2 == 0 ? db[c][k / 2].x : db[c][k / 2].y;
+            }
+        }
+    }
+    __syncthreads();
+    float *out = a.parts + (long long)blockIdx.x * 2 * a.n;
+    for (int i = threadIdx.x; i < 2 * a.n; i += 256) {
+        const int which = i >= a.n, j = i - which * a.n;
+        float v = 0.f;
+#pragma unroll 16
+        for (int g = 0; g < R; g++) v += across[g][which][j];
+        out[i] = v;
+    }
+}
+
+// ------------------------------------------------------------------ longer rows: a block a row
+
+// The first `bytes` of 16, zeros behind them, as one asynchronous copy
+__device__ __forceinline__ void cp_async16_part(void *dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::su32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+
+// Rows of an argument on their way through a block's shared memory, a thread's own pieces by its own copies: no thread reads what
+// another one copied.  Copies are of 16 bytes, up to the argument's last value.
+template <typename T, int LANES, int CH, bool SHIFT> struct Ring {
+    static constexpr int V = sizeof(T) / 2;   // vectors of 8 values; apart in shared memory, so that a warp's accesses are neighbours
+    const T *at, *end;      // the thread's place in the next row that is asked for; the argument's end
+    long long step;         // from row to row of the block
+    __device__ __forceinline__ Ring(const void *x, long long stride, long long rows, const Columns<LANES, SHIFT> &cols)
+        : at(static_cast<const T *>(x) + blockIdx.x * stride + cols.first(0)), end(static_cast<const T *>(x) + (rows - 1) * stride + cols.n),
+          step(gridDim.x * stride)
+    {
+    }
+    __device__ __forceinline__ void ask(const Columns<LANES, SHIFT> &cols, unsigned char *to)
+    {
+#pragma unroll
+        for (int c = 0; c < CH; c++) {
+            if (cols.has(c)) {
+                const T *p = at + c * LANES * 8;
+                unsigned char *q = to + (c * V * LANES + cols.t) * 16;
+                if (!SHIFT || p + 8 <= end) {
+#pragma unroll
+                    for (int v = 0; v < V; v++) ptx::cp_async16(q + v * LANES * 16, p + v * 8 / V);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < V; v++) {
+                        const int left = (int)(end - (p + v * 8 / V)) * (int)sizeof(T);
+                        cp_async16_part(q + v * LANES * 16, left > 0 ? p + v * 8 / V : p, left < 0 ? 0 : left < 16 ? left : 16);
+                    }
+                }
+            }
+        }
+        at += step;
+    }
+    static __device__ __forceinline__ void take(const Columns<LANES, SHIFT> &cols, const unsigned char *from, int c, float2 (&x)[4])
+    {
+        const unsigned char *q = from + (c * V * LANES + cols.t) * 16;
+        Eight<T> e;
+        if constexpr (V == 1) {
+            e.load(q);
+        } else {
+            e.a = *reinterpret_cast<const float4 *>(q);
+            e.b = *reinterpret_cast<const float4 *>(q + LANES * 16);
+        }
+        e.pairs(x);
+        cols.clip(x, c);
+    }
+};
+
+__device__ __forceinline__ void wait_copies(int pending)   // all but that many of the latest groups
+{
+    switch (pending) {
+    case 0: ptx::cp_async_wait<0>(); break;
+    case 1: ptx::cp_async_wait<1>(); break;
+    case 2: ptx::cp_async_wait<2>(); break;
+    default: ptx::cp_async_wait<3>(); break;
+    }
+}
+constexpr int MOST_PENDING = 3;
+
+// Sums of two values over a warp: lanes 0 to 15 get a's, the others b's.
+__device__ __forceinline__ float warp_sum2(float a, float b)
+{
+    const bool low = (threadIdx.x & 16) == 0;
+    float s = (low ? a : b) + __shfl_xor_sync(0xffffffffu, low ? b : a, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+// Two sums over the W warps' parts, for every thread.
+template <int W> __device__ __forceinline__ void block_sum2(const float *pa, const float *pb, float &a, float &b)
+{
+    const int lane = threadIdx.x & 31;
+    if constexpr (W <= 16) {
+        const int i = lane & 15;
+        float s = i < W ? (lane < 16 ? pa[i] : pb[i]) : 0.f;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1)
+            if (o < W) s += __shfl_xor_sync(0xffffffffu, s, o);
+        a = __shfl_sync(0xffffffffu, s, 0);
+        b = __shfl_sync(0xffffffffu, s, 16);
+    } else {
+        a = warp_sum(pa[lane]);
+        b = warp_sum(pb[lane]);
+    }
+}
+
+constexpr int blocks_of(int lanes) { return lanes >= 512 ? 1024 / lanes : 768 / lanes; }   // of an SM
+
+// Step i: the sum of row i, the squared differences of row i - 1, the result of row i - 2.
+template <typename T, int LANES, int CH, bool SHIFT>
+__global__ void __launch_bounds__(LANES, blocks_of(LANES)) norm_fwd_ring_kernel(const Fwd a, int stages)
+{
+    constexpr int W = LANES / 32, ROOM = LANES * CH * 8 * sizeof(T);
+    extern __shared__ __align__(16) unsigned char ring[];   // [stages][ROOM]
+    __shared__ float part[2][2][W];
+    chain_start();
+    chain_wait();
+    const Columns<LANES, SHIFT> cols = {a.n, shift_of<T>(blockIdx.x, a.stride), (int)threadIdx.x};
+    using Rows = Ring<T, LANES, CH, SHIFT>;
+    Rows rows(a.x, a.stride, a.rows, cols);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int count = (int)((a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x);   // of this block
+    const unsigned char *ring_end = ring + stages * ROOM;
+    const auto next = [&](unsigned char *p) { return p + ROOM == ring_end ? ring : p + ROOM; };
+    unsigned char *fresh = ring;
+    int asked = 0;
+    const auto ask = [&] {
+        if (asked < count) rows.ask(cols, fresh);
+        ptx::cp_async_commit();
+        fresh = next(fresh);
+        asked++;
+    };
+    for (int i = 0; i < stages - 3; i++) ask();
+    float2 w[CH][4], b[CH][4];
+#pragma unroll
+    for (int c = 0; c < CH; c++) {
+        cols.param(a.weight, a.param_f32, c, 1.f, w[c]);
+        cols.param(a.bias, a.param_f32, c, 0.f, b[c]);
+    }
+    const float inv_n = 1.f / (float)a.n;
+    unsigned char *p0 = ring, *p1 = ring, *p2 = ring;
+    float mean1 = 0.f, mean2 = 0.f;
+    T *y = static_cast<T *>(a.y) + (long long)blockIdx.x * a.n;
+    float *stats = a.stats != nullptr ? a.stats + blockIdx.x : nullptr;
+    int p = 0;
+    for (int i = 0; i < count + 2; i++) {
+        float sum = 0.f, squares = 0.f, var;
+        if (i > 0) {
+            mean2 = mean1;
+            block_sum2<W>(part[p ^ 1][0], part[p ^ 1][1], mean1, var);   // of row i - 1, of row i - 2
+            mean1 *= inv_n;
+        }
+        if (i < count) {
+            wait_copies(stages - 4);
+            ask();   // where row i - 3 was
+#pragma unroll
+            for (int c = 0; c < CH; c++) {
+                if (!cols.has(c)) continue;
+                float2 x[4];
+                Rows::take(cols, p0, c, x);
+                sum += sum8(x);
+            }
+        }
+        if (i >= 1 && i <= count) {
+#pragma unroll
+            for (int c = 0; c < CH; c++) {
+                if (!cols.has(c)) continue;
+                float2 x[4];
+                Rows::take(cols, p1, c, x);
+#pragma unroll
+                for (int k = 0; k < 4; k++) x[k] = add2(x[k], both(-mean1));
+                cols.clip(x, c);
+                squares += dot8(x, x);
+            }
+        }
+        if (i >= 2) {
+            const float rstd = 1.f / sqrtf(var * inv_n + a.eps);
+#pragma unroll
+            for (int c = 0; c < CH; c++) {
+                if (!cols.has(c)) continue;
+                float2 x[4];
+                Rows::take(cols, p2, c, x);
+#pragma unroll
+                for (int k = 0; k < 4; k++) x[k] = fma2(mul2(add2(x[k], both(-mean2)), both(rstd)), w[c][k], b[c][k]);
+                cols.store(y, c, x);
+            }
+            y += gridDim.x * (long long)a.n;
+            if (stats != nullptr) {
+                if (threadIdx.x == 0) {
+                    stats[0] = mean2;
+                    stats[a.rows] = rstd;
+                }
+                stats += gridDim.x;
+            }
+        }
+        const float s = warp_sum2(sum, squares);
+        if ((lane & 15) == 0) part[p][lane >> 4][warp] = s;
+        p ^= 1;
+        p2 = p1;
+        p1 = p0;
+        p0 = next(p0);
+        __syncthreads();
+    }
+    ptx::cp_async_wait<0>();
+}
+
+// Step i: the sums of row i, dx of row i - 1.  (With dx right behind its own sums, two blocks of 512 threads waited for one another's
+// barriers: 65536 rows of 4096 took 460 us.)
+template <typename T, int LANES, int CH, bool SHIFT>
+__global__ void __launch_bounds__(LANES, blocks_of(LANES)) norm_bwd_ring_kernel(const Bwd a, int stages)
+{
+    constexpr int W = LANES / 32, ROOM = LANES * CH * 8 * sizeof(T);
+    extern __shared__ __align__(16) unsigned char ring[];   // [stages][x, dy][ROOM]
+    __shared__ float part[2][2][W];
+    chain_start();
+    chain_wait();
+    const Columns<LANES, SHIFT> cols = {a.n, shift_of<T>(blockIdx.x, a.x_stride), (int)threadIdx.x};
+    using Rows = Ring<T, LANES, CH, SHIFT>;
+    Rows xs(a.x, a.x_stride, a.rows, cols), ds(a.dy, a.dy_stride, a.rows, cols);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int count = (int)((a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x);
+    const unsigned char *ring_end = ring + stages * 2 * ROOM;
+    const auto next = [&](unsigned char *p) { return p + 2 * ROOM == ring_end ? ring : p + 2 * ROOM; };
+    unsigned char *fresh = ring;
+    int asked = 0;
+    const auto ask = [&] {
+        if (asked < count) {
+            xs.ask(cols, fresh);
+            ds.ask(cols, fresh + ROOM);
+        }
+        ptx::cp_async_commit();
+        fresh = next(fresh);
+        asked++;
+    };
+    for (int i = 0; i < stages - 2; i++) ask();
+    float2 w[CH][4], dw[CH][4], db[CH][4];
+#pragma unroll
+    for (int c = 0; c < CH; c++) {
+        cols.param(a.weight, a.param_f32, c, 1.f, w[c]);
+#pragma unroll
+        for (int k = 0; k < 4; k++) dw[c][k] = db[c][k] = both(0.f);
+    }
+    const float inv_n = 1.f / (float)a.n;
+    unsigned char *p0 = ring, *p1 = ring;
+    const float *stats = a.stats + blockIdx.x;
+    float mean = __ldg(stats), rstd = __ldg(stats + a.rows), mean1 = 0.f, rstd1 = 0.f;
+    T *out = a.dx != nullptr ? static_cast<T *>(a.dx) + (long long)blockIdx.x * a.n : nullptr;
+    int p = 0;
+    // h and dy of a piece
+    const auto take = [&](const unsigned char *from, int c, float m, float q, float2 (&h)[4], float2 (&d)[4]) {
+        Rows::take(cols, from, c, h);
+        Rows::take(cols, from + ROOM, c, d);
+#pragma unroll
+        for (int k = 0; k < 4; k++) h[k] = mul2(add2(h[k], both(-m)), both(q));
+    };
+    for (int i = 0; i <= count; i++) {
+        float sa = 0.f, sh = 0.f;
+        const float m = mean, q = rstd;
+        if (i < count) {
+            wait_copies(stages - 3);
+            ask();   // where row i - 2 was
+            stats += gridDim.x;
+            if (i + 1 < count) {
+                mean = __ldg(stats);
+                rstd = __ldg(stats + a.rows);
+            }
+#pragma unroll
+            for (int c = 0; c < CH; c++) {
+                if (!cols.has(c)) continue;
+                float2 h[4], d[4];
+                take(p0, c, m, q, h, d);
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    dw[c][k] = fma2(d[k], h[k], dw[c][k]);
+                    db[c][k] = add2(db[c][k], d[k]);
+                    d[k] = mul2(d[k], w[c][k]);
+                }
+                sa += sum8(d);
+                sh += dot8(d, h);
+            }
+        }
+        if (out != nullptr) {
+            if (i > 0) {
+                float ma, mh;
+                block_sum2<W>(part[p ^ 1][0], part[p ^ 1][1], ma, mh);
+                ma *= inv_n;
+                mh *= inv_n;
+#pragma unroll
+                for (int c = 0; c < CH; c++) {
+                    if (!cols.has(c)) continue;
+                    float2 h[4], d[4];
+                    take(p1, c, mean1, rstd1, h, d);
+#pragma unroll
+                    for (int k = 0; k < 4; k++) h[k] = mul2(both(rstd1), fma2(h[k], both(-mh), fma2(d[k], w[c][k], both(-ma))));
+                    cols.store(out, c, h);
+                }
+                out += gridDim.x * (long long)a.n;
+            }
+            const float s = warp_sum2(sa, sh);
+            if ((lane & 15) == 0) part[p][lane >> 4][warp] = s;
+            p ^= 1;
+            __syncthreads();
+        }
+        mean1 = m;
+        rstd1 = q;
+        p1 = p0;
+        p0 = next(p0);
+    }
+    ptx::cp_async_wait<0>();
+    if (a.parts == nullptr) return;
+    float *sums = a.parts + (long long)blockIdx.x * 2 * a.n;
+#pragma unroll
+    for (int c = 0; c < CH; c++) {
+        if (!cols.has(c)) continue;
+        if constexpr (SHIFT) {
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                const int j = cols.first(c) + k;
+                if ((unsigned)j >= (unsigned)a.n) continue;
+                sums[j] = k % 2 == 0 ? dw[c][k / 2].x : dw[c][k / 2].y;
+                sums[a.n + j] = k % 2 == 0 ? db[c][k / 2].x : db[c][k / 2].y;
+            }
+        } else {
+            store_pairs(sums + cols.first(c), dw[c]);
+            store_pairs(sums + a.n + cols.first(c), db[c]);
+        }
+    }
+}
+
+// Few rows, a block each: the row in registers, nothing to overlap.
+template <typename T, int LANES, int CH, bool SHIFT> __global__ void __launch_bounds__(LANES) norm_fwd_few_kernel(const Fwd a)
+{
+    constexpr int W = LANES / 32;
+    __shared__ float part[2][W];
+    chain_start();
+    chain_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long r = blockIdx.x;
+    const Columns<LANES, SHIFT> cols = {a.n, shift_of<T>(r, a.stride), (int)threadIdx.x};
+    const T *row = static_cast<const T *>(a.x) + r * a.stride, *end = static_cast<const T *>(a.x) + (a.rows - 1) * a.stride + a.n;
+    float2 x[CH][4], w[CH][4], b[CH][4];
+#pragma unroll
+    for (int c = 0; c < CH; c++) {
+        Eight<T> e = Eight<T>();
+        if (cols.has(c)) load_piece(e, row + cols.first(c), end);
+        e.pairs(x[c]);
+        cols.clip(x[c], c);
+        cols.param(a.weight, a.param_f32, c, 1.f, w[c]);
+        cols.param(a.bias, a.param_f32, c, 0.f, b[c]);
+    }
+    const auto total = [&](float s, float *part) {
+        s = warp_sum(s);
+        if (lane == 0) part[warp] = s;
+        __syncthreads();
+        return warp_sum(lane < W ? part[lane] : 0.f);
+    };
+    float s = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; c++) s += sum8(x[c]);
+    const float mean = total(s, part[0]) / (float)a.n;
+    s = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; c++) {
+#pragma unroll
+        for (int k = 0; k < 4; k++) x[c][k] = add2(x[c][k], both(-mean));
+        cols.clip(x[c], c);
+        if (cols.has(c)) s += dot8(x[c], x[c]);
+    }
+    const float rstd = 1.f / sqrtf(total(s, part[1]) / (float)a.n + a.eps);
+#pragma unroll
+    for (int c = 0; c < CH; c++) {
+#pragma unroll
+        for (int k = 0; k < 4; k++) x[c][k] = fma2(mul2(x[c][k], both(rstd)), w[c][k], b[c][k]);
+        if (cols.has(c)) cols.store(static_cast<T *>(a.y) + r * a.n, c, x[c]);
+    }
+    if (a.stats != nullptr && threadIdx.x == 0) {
+        a.stats[r] = mean;
+        a.stats[a.rows + r] = rstd;
+    }
+}
+
+// The blocks' sums joined: 8 columns a block (a sector), 128 threads a column.
+__global__ void __launch_bounds__(1024) norm_join_kernel(const float *parts, int blocks, int n, void *dw, void *db, int param_f32)
+{
+    __shared__ float part[128][9];
+    chain_start();
+    chain_wait();
+    const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long i = (long long)blockIdx.x * 8 + tx;
     float s = 0.f;
     if (i < 2LL * n) {
 #pragma unroll 4
-        for (int b = ty; b < blocks; b += 32) s += parts[(long long)b * 2 * n + i];
+        for (int b = ty; b < blocks; b += 128) s += parts[(long long)b * 2 * n + i];
     }
     part[ty][tx] = s;
     __syncthreads();
-    if (ty > 0 || i >= 2LL * n) return;
-    float v = 0.f;
-#pragma unroll
-    for (int k = 0; k < 32; k++) v += part[k][tx];
-    void *out = i < n ? dw : db;
-    const long long j = i < n ? i : i - n;
-    if (out == nullptr) return;
+    if (warp >= 8) return;
+    const float v = warp_sum((part[lane][warp] + part[lane + 32][warp]) + (part[lane + 64][warp] + part[lane + 96][warp]));
+    const long long at = (long long)blockIdx.x * 8 + warp;
+    void *out = at < n ? dw : db;
+    if (lane > 0 || at >= 2LL * n || out == nullptr) return;
+    const long long j = at < n ? at : at - n;
     if (param_f32) static_cast<float *>(out)[j] = v;
     else static_cast<bf16 *>(out)[j] = __float2bfloat16_rn(v);
 }
 
-// ------------------------------------------------------------------ rows longer than the registers hold
+// ------------------------------------------------------------------ any rows, value by value: longer than a block's shared memory holds a few of,
+// or with strides that put the rows of x, dy and the result differently between 16-byte boundaries
+
+template <int V> __device__ __forceinline__ void block_sums(float (&s)[V], float *part)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __syncthreads();  // the last sums have been read
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+        s[v] = warp_sum(s[v]);
+        if (lane == 0) part[v * 32 + warp] = s[v];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < V; v++) s[v] = warp_sum(lane < (int)blockDim.x / 32 ? part[v * 32 + lane] : 0.f);
+}
+__device__ __forceinline__ float param(const void *p, int f32, long long i)
+{
+    return f32 ? __ldg(static_cast<const float *>(p) + i) : __bfloat162float(static_cast<const bf16 *>(p)[i]);
+}
 
 // A block a row, read again for each of its sums (from L2 mostly).
 template <typename T> __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(const Fwd a)
 {
-    __shared__ float part[2 * 33];
+    __shared__ float part[2 * 32];
     chain_start();
     chain_wait();
     const long long r = blockIdx.x;
     const T *x = static_cast<const T *>(a.x) + r * a.stride;
     float s[1] = {0.f};
-    for (int j = threadIdx.x; j < a.n; j += 1024) s[0] += from_value(x[j]);
-    row_sums<1024>(s, part);
+    for (int j = threadIdx.x; j < a.n; j += blockDim.x) s[0] += from_value(x[j]);
+    block_sums(s, part);
     const float mean = s[0] / (float)a.n;
     s[0] = 0.f;
-    for (int j = threadIdx.x; j < a.n; j += 1024) {
+    for (int j = threadIdx.x; j < a.n; j += blockDim.x) {
         const float d = from_value(x[j]) - mean;
         s[0] = fmaf(d, d, s[0]);
     }
-    row_sums<1024>(s, part);
+    block_sums(s, part);
     const float rstd = 1.f / sqrtf(s[0] / (float)a.n + a.eps);
     T *y = static_cast<T *>(a.y) + r * a.n;
-    for (int j = threadIdx.x; j < a.n; j += 1024) {
+    for (int j = threadIdx.x; j < a.n; j += blockDim.x) {
         const float w = a.weight != nullptr ? param(a.weight, a.param_f32, j) : 1.f, b = a.bias != nullptr ? param(a.bias, a.param_f32, j) : 0.f;
         y[j] = from_f<T>(fmaf((from_value(x[j]) - mean) * rstd, w, b));
     }
@@ -331,7 +801,7 @@ template <typename T> __global__ void __launch_bounds__(1024) norm_fwd_long_kern
 }
 template <typename T> __global__ void __launch_bounds__(1024) norm_dx_long_kernel(const Bwd a)
 {
-    __shared__ float part[2 * 33];
+    __shared__ float part[2 * 32];
     chain_start();
     chain_wait();
     const long long r = blockIdx.x;
@@ -342,16 +812,16 @@ template <typename T> __global__ void __launch_bounds__(1024) norm_dx_long_kerne
         h = (from_value(x[j]) - mean) * rstd;
         d = from_value(dy[j]) * (a.weight != nullptr ? param(a.weight, a.param_f32, j) : 1.f);
     };
-    for (int j = threadIdx.x; j < a.n; j += 1024) {
+    for (int j = threadIdx.x; j < a.n; j += blockDim.x) {
         float h, d;
         at(j, h, d);
         s[0] += d;
         s[1] = fmaf(d, h, s[1]);
     }
-    row_sums<1024>(s, part);
+    block_sums(s, part);
     const float ma = s[0] / (float)a.n, mh = s[1] / (float)a.n;
     T *dx = static_cast<T *>(a.dx) + r * a.n;
-    for (int j = threadIdx.x; j < a.n; j += 1024) {
+    for (int j = threadIdx.x; j < a.n; j += blockDim.x) {
         float h, d;
         at(j, h, d);
         dx[j] = from_f<T>(rstd * (d - ma - h * mh));
@@ -378,56 +848,114 @@ template <typename T> __global__ void __launch_bounds__(256) norm_params_long_ke
 
 // ------------------------------------------------------------------ host side
 
-constexpr int kLongest = 16384;  // columns that a block's registers hold
-
-// Blocks of the backward, the same on every device: four for each of the GPU's SMs, or a part of the rows each.
-int bwd_blocks(const csa_layernorm_params &p)
+// How rows of n values are taken: threads of a row and pieces of 8 of each; for rows of a block the stages of its ring, as many
+// as its part of the SM's shared memory holds; blocks, the same on every device.
+struct How {
+    int lanes, pieces, stages, blocks;   // lanes 0: value by value
+    bool shift, few;
+};
+How how(const csa_layernorm_params &p, bool backward)
 {
-    const long long most = 4LL * linear::kSms;
-    if (p.cols > kLongest) return (int)(p.rows < 64 ? (p.rows > 0 ? p.rows : 1) : 64);
-    const long long each = p.cols <= 128 ? 16 : p.cols <= 512 ? 8 : 1;
-    const long long want = (p.rows + each - 1) / each;
-    return (int)(want < 1 ? 1 : want < most ? want : most);
+    How h = {};
+    const int n = p.cols, size = p.dtype == CSA_F32 ? 4 : 2, vector = 16 / size;
+    const auto blocks = [&](long long each, long long most) {
+        const long long want = (p.rows + each - 1) / each;
+        h.blocks = (int)(want < 1 ? 1 : want < most ? want : most);
+    };
+    // rows of all arguments lie alike between boundaries
+    const bool alike = (p.x_stride - n) % vector == 0 && (!backward || (p.dy_stride - n) % vector == 0);
+    h.shift = n % 8 != 0;
+    const int held = n + (h.shift && p.rows > 1 ? vector - 1 : 0);
+    if (!alike || held > (size == 4 ? 8192 : 16384)) {
+        blocks(1, 64);
+        return h;
+    }
+    h.pieces = held > 256 ? 2 : 1;
+    h.lanes = held <= 32 ? 4 : held <= 64 ? 8 : held <= 128 ? 16 : held <= 512 ? 32 : held <= 1024 ? 64 : held <= 2048 ? 128 : held <= 4096 ? 256 : held <= 8192 ? 512 : 1024;
+    if (h.lanes <= 32) {
+        blocks(256 / h.lanes * U, backward ? 3LL * linear::kSms : 4LL * linear::kSms);
+        return h;
+    }
+    const int live = backward ? 2 : 3, room = h.lanes * 16 * size * (backward ? 2 : 1);
+    int per_sm = blocks_of(h.lanes);
+    while ((225000 / per_sm - 1600) / room < live + 1) per_sm--;   // a row on its way at least; one block holds 3 of the longest
+    h.stages = (225000 / per_sm - 1600) / room;
+    if (h.stages > live + 1 + MOST_PENDING) h.stages = live + 1 + MOST_PENDING;
+    blocks(1, (long long)per_sm * linear::kSms);   // a multiple of 8, or a row each
+    // one row a block needs no ring (37 x 4096: 2.2 us, through the ring NNN)
+    h.few = !backward && p.rows <= h.blocks;
+    return h;
 }
 
-// Calls f with the number of a row's threads and of their pieces.
-template <typename F> cudaError_t by_cols(int n, const F &f)
+template <int L, int C> struct Shape {
+    static constexpr int LANES = L, PIECES = C;
+};
+template <typename F> cudaError_t short_shape(const How &h, const F &f)
 {
-    using std::integral_constant;
-#define CSA_SHAPE(l, c) f(integral_constant<int, l>(), integral_constant<int, c>())
-    if (n <= 128) return CSA_SHAPE(16, 1);
-    if (n <= 256) return CSA_SHAPE(32, 1);
-    if (n <= 512) return CSA_SHAPE(32, 2);
-    if (n <= 1024) return CSA_SHAPE(128, 1);
-    if (n <= 2048) return CSA_SHAPE(128, 2);
-    if (n <= 4096) return CSA_SHAPE(256, 2);
-    if (n <= 8192) return CSA_SHAPE(512, 2);
-    return CSA_SHAPE(512, 4);
-#undef CSA_SHAPE
+    if (h.lanes == 4) return f(Shape<4, 1>());
+    if (h.lanes == 8) return f(Shape<8, 1>());
+    if (h.lanes == 16) return f(Shape<16, 1>());
+    return h.pieces == 1 ? f(Shape<32, 1>()) : f(Shape<32, 2>());
 }
-
-template <typename T> cudaError_t fwd(const Fwd &a, bool vec, cudaStream_t st)
+template <typename T, typename F> cudaError_t block_shape(const How &h, const F &f)
 {
-    if (a.n > kLongest) return launch_chained(norm_fwd_long_kernel<T>, dim3((unsigned)a.rows), 1024, 0, 1, st, a);
-    return by_cols(a.n, [&](auto lanes, auto pieces) {
-        constexpr int L = decltype(lanes)::value, C = decltype(pieces)::value, R = threads_of(L) / L;
-        const dim3 grid((unsigned)((a.rows + R - 1) / R));
-        return launch_chained(vec ? norm_fwd_kernel<T, L, C, true> : norm_fwd_kernel<T, L, C, false>, grid, threads_of(L), 0, 1, st, a);
+    if (h.lanes == 64) return f(Shape<64, 2>());
+    if (h.lanes == 128) return f(Shape<128, 2>());
+    if (h.lanes == 256) return f(Shape<256, 2>());
+    if constexpr (sizeof(T) == 2) {
+        if (h.lanes == 1024) return f(Shape<1024, 2>());
+    }
+    return f(Shape<512, 2>());
+}
+inline int long_threads(int n) { return n <= 2048 ? 128 : 1024; }
+
+template <typename T> cudaError_t fwd(const Fwd &a, const How &h, cudaStream_t st)
+{
+    if (h.lanes == 0) return launch_chained(norm_fwd_long_kernel<T>, dim3((unsigned)a.rows), long_threads(a.n), 0, 1, st, a);
+    if (h.lanes <= 32) {
+        return short_shape(h, [&](auto shape) {
+            using S = decltype(shape);
+            auto *kernel = h.shift ? norm_fwd_short_kernel<T, S::LANES, S::PIECES, true> : norm_fwd_short_kernel<T, S::LANES, S::PIECES, false>;
+            return launch_chained(kernel, dim3((unsigned)h.blocks), 256, 0, 1, st, a);
+        });
+    }
+    return block_shape<T>(h, [&](auto shape) {
+        using S = decltype(shape);
+        if (h.few) {
+            auto *kernel = h.shift ? norm_fwd_few_kernel<T, S::LANES, S::PIECES, true> : norm_fwd_few_kernel<T, S::LANES, S::PIECES, false>;
+            return launch_chained(kernel, dim3((unsigned)a.rows), S::LANES, 0, 1, st, a);
+        }
+        auto *kernel = h.shift ? norm_fwd_ring_kernel<T, S::LANES, S::PIECES, true> : norm_fwd_ring_kernel<T, S::LANES, S::PIECES, false>;
+        const int smem = h.stages * S::LANES * S::PIECES * 8 * (int)sizeof(T);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        return launch_chained(kernel, dim3((unsigned)h.blocks), S::LANES, smem, 1, st, a, h.stages);
     });
 }
-template <typename T> cudaError_t bwd(const Bwd &a, bool vec, int blocks, cudaStream_t st)
+template <typename T> cudaError_t bwd(const Bwd &a, const How &h, cudaStream_t st)
 {
-    if (a.n > kLongest) {
+    if (h.lanes == 0) {
         // dx last: it may lie where dy or x do
         cudaError_t e = cudaSuccess;
         if (a.parts != nullptr)
-            e = launch_chained(norm_params_long_kernel<T>, dim3((unsigned)((a.n + 255) / 256), (unsigned)blocks), 256, 0, 1, st, a);
+            e = launch_chained(norm_params_long_kernel<T>, dim3((unsigned)((a.n + 255) / 256), (unsigned)h.blocks), 256, 0, 1, st, a);
         if (e != cudaSuccess || a.dx == nullptr) return e;
-        return launch_chained(norm_dx_long_kernel<T>, dim3((unsigned)a.rows), 1024, 0, 1, st, a);
+        return launch_chained(norm_dx_long_kernel<T>, dim3((unsigned)a.rows), long_threads(a.n), 0, 1, st, a);
     }
-    return by_cols(a.n, [&](auto lanes, auto pieces) {
-        constexpr int L = decltype(lanes)::value, C = decltype(pieces)::value;
-        return launch_chained(vec ? norm_bwd_kernel<T, L, C, true> : norm_bwd_kernel<T, L, C, false>, dim3((unsigned)blocks), threads_of(L), 0, 1, st, a);
+    if (h.lanes <= 32) {
+        return short_shape(h, [&](auto shape) {
+            using S = decltype(shape);
+            auto *kernel = h.shift ? norm_bwd_short_kernel<T, S::LANES, S::PIECES, true> : norm_bwd_short_kernel<T, S::LANES, S::PIECES, false>;
+            return launch_chained(kernel, dim3((unsigned)h.blocks), 256, 0, 1, st, a);
+        });
+    }
+    return block_shape<T>(h, [&](auto shape) {
+        using S = decltype(shape);
+        auto *kernel = h.shift ? norm_bwd_ring_kernel<T, S::LANES, S::PIECES, true> : norm_bwd_ring_kernel<T, S::LANES, S::PIECES, false>;
+        const int smem = h.stages * 2 * S::LANES * S::PIECES * 8 * (int)sizeof(T);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        return launch_chained(kernel, dim3((unsigned)h.blocks), S::LANES, smem, 1, st, a, h.stages);
     });
 }
 
@@ -435,7 +963,7 @@ template <typename T> cudaError_t bwd(const Bwd &a, bool vec, int blocks, cudaSt
 
 size_t layernorm_bwd_workspace(const csa_layernorm_params &p)
 {
-    return p.rows == 0 ? 0 : linear::up256((size_t)norm::bwd_blocks(p) * 2 * p.cols * 4);
+    return p.rows == 0 ? 0 : linear::up256((size_t)norm::how(p, true).blocks * 2 * p.cols * 4);
 }
 
 cudaError_t launch_layernorm_fwd(const csa_layernorm_params &p, const void *x, const void *weight, const void *bias, void *y, float *stats,
@@ -443,9 +971,8 @@ cudaError_t launch_layernorm_fwd(const csa_layernorm_params &p, const void *x, c
 {
     note_path("generic");
     const norm::Fwd a = {x, weight, bias, y, stats, p.rows, p.x_stride, p.cols, p.param_dtype == CSA_F32, p.eps};
-    const int each = p.dtype == CSA_F32 ? 4 : 8;
-    const bool vec = p.cols % 8 == 0 && p.x_stride % each == 0;
-    return p.dtype == CSA_F32 ? norm::fwd<float>(a, vec, st) : norm::fwd<__nv_bfloat16>(a, vec, st);
+    const norm::How h = norm::how(p, false);
+    return p.dtype == CSA_F32 ? norm::fwd<float>(a, h, st) : norm::fwd<__nv_bfloat16>(a, h, st);
 }
 
 cudaError_t launch_layernorm_bwd(const csa_layernorm_params &p, const void *dy, const void *x, const void *weight, const float *stats, void *dx,
@@ -462,11 +989,10 @@ cudaError_t launch_layernorm_bwd(const csa_layernorm_params &p, const void *dy, 
     if (dx == nullptr && !params) return cudaSuccess;
     const norm::Bwd a = {dy, x, weight, stats, dx, params ? static_cast<float *>(ws) : nullptr, p.rows, p.x_stride, p.dy_stride, p.cols,
                          p.param_dtype == CSA_F32};
-    const int each = p.dtype == CSA_F32 ? 4 : 8, blocks = norm::bwd_blocks(p);
-    const bool vec = p.cols % 8 == 0 && p.x_stride % each == 0 && p.dy_stride % each == 0;
-    const cudaError_t e = p.dtype == CSA_F32 ? norm::bwd<float>(a, vec, blocks, st) : norm::bwd<__nv_bfloat16>(a, vec, blocks, st);
+    const norm::How h = norm::how(p, true);
+    const cudaError_t e = p.dtype == CSA_F32 ? norm::bwd<float>(a, h, st) : norm::bwd<__nv_bfloat16>(a, h, st);
     if (e != cudaSuccess || !params) return e;
-    return linear::launch_chained(norm::norm_join_kernel, dim3((unsigned)((2LL * p.cols + 31) / 32)), 1024, 0, 1, st, a.parts, blocks, p.cols, dweight,
+    return linear::launch_chained(norm::norm_join_kernel, dim3((unsigned)((2LL * p.cols + 7) / 8)), 1024, 0, 1, st, a.parts, h.blocks, p.cols, dweight,
                                   dbias, a.param_f32);
 }
 
