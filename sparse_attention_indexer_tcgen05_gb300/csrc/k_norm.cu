@@ -190,7 +190,7 @@ struct Bwd {
 
 constexpr int U = 2;   // rows of a thread on their way at a time
 
-template <typename T, int LANES, int CH, bool SHIFT> __global__ void __launch_bounds__(256) norm_fwd_short_kernel(const Fwd a)
+template <typename T, int LANES, int CH, bool SHIFT> __global__ void __launch_bounds__(256, sizeof(T) == 2 && CH == 1 ? 4 : 1) norm_fwd_short_kernel(const Fwd a)
 {
     constexpr int R = 256 / LANES;   // a multiple of 8, as is the grid times it: the shift is the group's own
     chain_start();
@@ -356,7 +356,7 @@ template <typename T, int LANES, int CH, bool SHIFT> __global__ void __launch_bo
     }
 }
 
-// ------------------------------------------------------------------ longer rows: a block a row
+// ------------------------------------------------------------------ longer rows: several warps a row
 
 // The first `bytes` of 16, zeros behind them, as one asynchronous copy
 __device__ __forceinline__ void cp_async16_part(void *dst, const void *src, int bytes)
@@ -364,15 +364,17 @@ __device__ __forceinline__ void cp_async16_part(void *dst, const void *src, int 
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::su32(dst)), "l"(src), "r"(bytes) : "memory");
 }
 
-// Rows of an argument on their way through a block's shared memory, a thread's own pieces by its own copies: no thread reads what
+constexpr int CH = 2;    // pieces of a thread
+
+// Rows of an argument on their way through shared memory, a thread's own pieces by its own copies: no thread reads what
 // another one copied.  Copies are of 16 bytes, up to the argument's last value.
-template <typename T, int LANES, int CH, bool SHIFT> struct Ring {
+template <typename T, int LANES, bool SHIFT> struct Ring {
     static constexpr int V = sizeof(T) / 2;   // vectors of 8 values; apart in shared memory, so that a warp's accesses are neighbours
     const T *at, *end;      // the thread's place in the next row that is asked for; the argument's end
-    long long step;         // from row to row of the block
-    __device__ __forceinline__ Ring(const void *x, long long stride, long long rows, const Columns<LANES, SHIFT> &cols)
-        : at(static_cast<const T *>(x) + blockIdx.x * stride + cols.first(0)), end(static_cast<const T *>(x) + (rows - 1) * stride + cols.n),
-          step(gridDim.x * stride)
+    long long step;         // from row to row
+    __device__ __forceinline__ Ring(const void *x, long long stride, long long rows, long long first, long long apart, const Columns<LANES, SHIFT> &cols)
+        : at(static_cast<const T *>(x) + first * stride + cols.first(0)), end(static_cast<const T *>(x) + (rows - 1) * stride + cols.n),
+          step(apart * stride)
     {
     }
     __device__ __forceinline__ void ask(const Columns<LANES, SHIFT> &cols, unsigned char *to)
@@ -396,7 +398,7 @@ template <typename T, int LANES, int CH, bool SHIFT> struct Ring {
         }
         at += step;
     }
-    static __device__ __forceinline__ void take(const Columns<LANES, SHIFT> &cols, const unsigned char *from, int c, float2 (&x)[4])
+    static __device__ __forceinline__ Eight<T> raw(const Columns<LANES, SHIFT> &cols, const unsigned char *from, int c)
     {
         const unsigned char *q = from + (c * V * LANES + cols.t) * 16;
         Eight<T> e;
@@ -406,8 +408,23 @@ template <typename T, int LANES, int CH, bool SHIFT> struct Ring {
             e.a = *reinterpret_cast<const float4 *>(q);
             e.b = *reinterpret_cast<const float4 *>(q + LANES * 16);
         }
-        e.pairs(x);
-        cols.clip(x, c);
+        return e;
+    }
+    static __device__ __forceinline__ void take(const Columns<LANES, SHIFT> &cols, const unsigned char *from, int c, float2 (&x)[4]) { raw(cols, from, c).pairs(x); }
+    // What lies beside a row in its first and last vectors becomes 0, once, where it has arrived: it may be anything.
+    static __device__ __forceinline__ void clean(const Columns<LANES, SHIFT> &cols, unsigned char *from)
+    {
+        if constexpr (SHIFT) {
+#pragma unroll
+            for (int c = 0; c < CH; c++) {
+                if (!cols.has(c) || cols.full(c)) continue;
+                T *q = reinterpret_cast<T *>(from + (c * V * LANES + cols.t) * 16);
+                const int j = cols.first(c);
+#pragma unroll
+                for (int k = 0; k < 8; k++)
+                    if ((unsigned)(j + k) >= (unsigned)cols.n) q[k / (8 / V) * (LANES * 16 / (int)sizeof(T)) + k % (8 / V)] = from_f<T>(0.f);
+            }
+        }
     }
 };
 
@@ -431,43 +448,57 @@ __device__ __forceinline__ float warp_sum2(float a, float b)
     for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return s;
 }
-// Two sums over the W warps' parts, for every thread.
-template <int W> __device__ __forceinline__ void block_sum2(const float *pa, const float *pb, float &a, float &b)
+// Two sums over the W warps' parts, for every thread; parts up to the next power of two hold 0.
+template <int W> __device__ __forceinline__ void group_sum2(const float (&part)[2][32], float &a, float &b)
 {
     const int lane = threadIdx.x & 31;
-    if constexpr (W <= 16) {
-        const int i = lane & 15;
-        float s = i < W ? (lane < 16 ? pa[i] : pb[i]) : 0.f;
+    float s = part[lane >> 4][lane & 15];
+    if constexpr (W > 16) s += part[lane >> 4][16 + (lane & 15)];
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1)
-            if (o < W) s += __shfl_xor_sync(0xffffffffu, s, o);
-        a = __shfl_sync(0xffffffffu, s, 0);
-        b = __shfl_sync(0xffffffffu, s, 16);
-    } else {
-        a = warp_sum(pa[lane]);
-        b = warp_sum(pb[lane]);
-    }
+    for (int o = 8; o > 0; o >>= 1)
+        if (o < W) s += __shfl_xor_sync(0xffffffffu, s, o);
+    a = __shfl_sync(0xffffffffu, s, 0);
+    b = __shfl_sync(0xffffffffu, s, 16);
 }
 
-constexpr int blocks_of(int lanes) { return lanes >= 512 ? 1024 / lanes : 768 / lanes; }   // of an SM
+// One block an SM, of several groups of LANES threads, each of which takes rows of its own (with a block for each, 1824 blocks
+// left 15 MB of sums for 16384 rows of 1000).  What a group needs of this:
+template <int LANES> struct Group {
+    int index, t, warp, lane;
+    long long first, apart;     // its first row, from there to its next one
+    int count;                  // its rows
+    __device__ __forceinline__ Group(long long rows)
+    {
+        index = threadIdx.x / LANES;
+        t = threadIdx.x - index * LANES;
+        warp = t >> 5;
+        lane = t & 31;
+        first = (long long)index * gridDim.x + blockIdx.x;
+        apart = (long long)(blockDim.x / LANES) * gridDim.x;
+        count = first < rows ? (int)((rows - first + apart - 1) / apart) : 0;
+    }
+    __device__ __forceinline__ void sync() const { ptx::named_bar(1 + index, LANES); }
+};
+// Threads of a block: backward 512 of 128 registers (768 of 80 spilled: 65536 x 4096 636 us instead of 281), forward 768
+__host__ __device__ constexpr int most_threads(int lanes, bool backward) { return lanes > 512 ? 1024 : backward ? 512 : 768; }
+constexpr int GROUPS = 12;
 
 // Step i: the sum of row i, the squared differences of row i - 1, the result of row i - 2.
-template <typename T, int LANES, int CH, bool SHIFT>
-__global__ void __launch_bounds__(LANES, blocks_of(LANES)) norm_fwd_ring_kernel(const Fwd a, int stages)
+template <typename T, int LANES, bool SHIFT> __global__ void __launch_bounds__(most_threads(LANES, false), 1) norm_fwd_ring_kernel(const Fwd a, int stages)
 {
-    constexpr int W = LANES / 32, ROOM = LANES * CH * 8 * sizeof(T);
-    extern __shared__ __align__(16) unsigned char ring[];   // [stages][ROOM]
-    __shared__ float part[2][2][W];
+    extern __shared__ __align__(16) unsigned char ring[];   // [groups][stages][room]
+    __shared__ float parts[GROUPS][2][2][32];
     chain_start();
     chain_wait();
-    const Columns<LANES, SHIFT> cols = {a.n, shift_of<T>(blockIdx.x, a.stride), (int)threadIdx.x};
-    using Rows = Ring<T, LANES, CH, SHIFT>;
-    Rows rows(a.x, a.stride, a.rows, cols);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int count = (int)((a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x);   // of this block
-    const unsigned char *ring_end = ring + stages * ROOM;
-    const auto next = [&](unsigned char *p) { return p + ROOM == ring_end ? ring : p + ROOM; };
-    unsigned char *fresh = ring;
+    const Group<LANES> g(a.rows);
+    const Columns<LANES, SHIFT> cols = {a.n, shift_of<T>(g.first, a.stride), g.t};
+    using Rows = Ring<T, LANES, SHIFT>;
+    Rows rows(a.x, a.stride, a.rows, g.first, g.apart, cols);
+    constexpr int room = LANES * CH * 8 * (int)sizeof(T);
+    const int count = g.count;
+    unsigned char *const ring_start = ring + g.index * stages * room, *const ring_end = ring_start + stages * room;
+    const auto next = [&](unsigned char *p) { return p + room == ring_end ? ring_start : p + room; };
+    unsigned char *fresh = ring_start;
     int asked = 0;
     const auto ask = [&] {
         if (asked < count) rows.ask(cols, fresh);
@@ -482,22 +513,26 @@ __global__ void __launch_bounds__(LANES, blocks_of(LANES)) norm_fwd_ring_kernel(
         cols.param(a.weight, a.param_f32, c, 1.f, w[c]);
         cols.param(a.bias, a.param_f32, c, 0.f, b[c]);
     }
+    for (int i = threadIdx.x; i < GROUPS * 128; i += blockDim.x) (&parts[0][0][0][0])[i] = 0.f;
+    __syncthreads();
+    float(*const part)[2][32] = parts[g.index];
     const float inv_n = 1.f / (float)a.n;
-    unsigned char *p0 = ring, *p1 = ring, *p2 = ring;
+    unsigned char *p0 = ring_start, *p1 = ring_start, *p2 = ring_start;
     float mean1 = 0.f, mean2 = 0.f;
-    T *y = static_cast<T *>(a.y) + (long long)blockIdx.x * a.n;
-    float *stats = a.stats != nullptr ? a.stats + blockIdx.x : nullptr;
+    T *y = static_cast<T *>(a.y) + g.first * a.n;
+    float *stats = a.stats != nullptr ? a.stats + g.first : nullptr;
     int p = 0;
-    for (int i = 0; i < count + 2; i++) {
+    for (int i = 0; i < count + 2 && count > 0; i++) {
         float sum = 0.f, squares = 0.f, var;
         if (i > 0) {
             mean2 = mean1;
-            block_sum2<W>(part[p ^ 1][0], part[p ^ 1][1], mean1, var);   // of row i - 1, of row i - 2
+            group_sum2<LANES / 32>(part[p ^ 1], mean1, var);   // of row i - 1, of row i - 2
             mean1 *= inv_n;
         }
         if (i < count) {
             wait_copies(stages - 4);
             ask();   // where row i - 3 was
+            Rows::clean(cols, p0);
 #pragma unroll
             for (int c = 0; c < CH; c++) {
                 if (!cols.has(c)) continue;
@@ -529,49 +564,48 @@ __global__ void __launch_bounds__(LANES, blocks_of(LANES)) norm_fwd_ring_kernel(
                 for (int k = 0; k < 4; k++) x[k] = fma2(mul2(add2(x[k], both(-mean2)), both(rstd)), w[c][k], b[c][k]);
                 cols.store(y, c, x);
             }
-            y += gridDim.x * (long long)a.n;
+            y += g.apart * a.n;
             if (stats != nullptr) {
-                if (threadIdx.x == 0) {
+                if (g.t == 0) {
                     stats[0] = mean2;
                     stats[a.rows] = rstd;
                 }
-                stats += gridDim.x;
+                stats += g.apart;
             }
         }
         const float s = warp_sum2(sum, squares);
-        if ((lane & 15) == 0) part[p][lane >> 4][warp] = s;
+        if ((g.lane & 15) == 0) part[p][g.lane >> 4][g.warp] = s;
         p ^= 1;
         p2 = p1;
         p1 = p0;
         p0 = next(p0);
-        __syncthreads();
+        g.sync();
     }
     ptx::cp_async_wait<0>();
 }
 
 // Step i: the sums of row i, dx of row i - 1.  (With dx right behind its own sums, two blocks of 512 threads waited for one another's
 // barriers: 65536 rows of 4096 took 460 us.)
-template <typename T, int LANES, int CH, bool SHIFT>
-__global__ void __launch_bounds__(LANES, blocks_of(LANES)) norm_bwd_ring_kernel(const Bwd a, int stages)
+template <typename T, int LANES, bool SHIFT> __global__ void __launch_bounds__(most_threads(LANES, true), 1) norm_bwd_ring_kernel(const Bwd a, int stages)
 {
-    constexpr int W = LANES / 32, ROOM = LANES * CH * 8 * sizeof(T);
-    extern __shared__ __align__(16) unsigned char ring[];   // [stages][x, dy][ROOM]
-    __shared__ float part[2][2][W];
+    extern __shared__ __align__(16) unsigned char ring[];   // [groups][stages][x, dy][room]; at the end [groups][dw, db][n]
+    __shared__ float parts[GROUPS][2][2][32];
     chain_start();
     chain_wait();
-    const Columns<LANES, SHIFT> cols = {a.n, shift_of<T>(blockIdx.x, a.x_stride), (int)threadIdx.x};
-    using Rows = Ring<T, LANES, CH, SHIFT>;
-    Rows xs(a.x, a.x_stride, a.rows, cols), ds(a.dy, a.dy_stride, a.rows, cols);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int count = (int)((a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x);
-    const unsigned char *ring_end = ring + stages * 2 * ROOM;
-    const auto next = [&](unsigned char *p) { return p + 2 * ROOM == ring_end ? ring : p + 2 * ROOM; };
-    unsigned char *fresh = ring;
+    const Group<LANES> g(a.rows);
+    const Columns<LANES, SHIFT> cols = {a.n, shift_of<T>(g.first, a.x_stride), g.t};
+    using Rows = Ring<T, LANES, SHIFT>;
+    Rows xs(a.x, a.x_stride, a.rows, g.first, g.apart, cols), ds(a.dy, a.dy_stride, a.rows, g.first, g.apart, cols);
+    constexpr int room = LANES * CH * 8 * (int)sizeof(T);
+    const int count = g.count;
+    unsigned char *const ring_start = ring + g.index * stages * 2 * room, *const ring_end = ring_start + stages * 2 * room;
+    const auto next = [&](unsigned char *p) { return p + 2 * room == ring_end ? ring_start : p + 2 * room; };
+    unsigned char *fresh = ring_start;
     int asked = 0;
     const auto ask = [&] {
         if (asked < count) {
             xs.ask(cols, fresh);
-            ds.ask(cols, fresh + ROOM);
+            ds.ask(cols, fresh + room);
         }
         ptx::cp_async_commit();
         fresh = next(fresh);
@@ -585,26 +619,31 @@ __global__ void __launch_bounds__(LANES, blocks_of(LANES)) norm_bwd_ring_kernel(
 #pragma unroll
         for (int k = 0; k < 4; k++) dw[c][k] = db[c][k] = both(0.f);
     }
+    for (int i = threadIdx.x; i < GROUPS * 128; i += blockDim.x) (&parts[0][0][0][0])[i] = 0.f;
+    __syncthreads();
+    float(*const part)[2][32] = parts[g.index];
     const float inv_n = 1.f / (float)a.n;
-    unsigned char *p0 = ring, *p1 = ring;
-    const float *stats = a.stats + blockIdx.x;
-    float mean = __ldg(stats), rstd = __ldg(stats + a.rows), mean1 = 0.f, rstd1 = 0.f;
-    T *out = a.dx != nullptr ? static_cast<T *>(a.dx) + (long long)blockIdx.x * a.n : nullptr;
+    unsigned char *p0 = ring_start, *p1 = ring_start;
+    const float *stats = a.stats + g.first;
+    float mean = count > 0 ? __ldg(stats) : 0.f, rstd = count > 0 ? __ldg(stats + a.rows) : 0.f, mean1 = 0.f, rstd1 = 0.f;
+    T *out = a.dx != nullptr ? static_cast<T *>(a.dx) + g.first * a.n : nullptr;
     int p = 0;
     // h and dy of a piece
     const auto take = [&](const unsigned char *from, int c, float m, float q, float2 (&h)[4], float2 (&d)[4]) {
         Rows::take(cols, from, c, h);
-        Rows::take(cols, from + ROOM, c, d);
+        Rows::take(cols, from + room, c, d);
 #pragma unroll
         for (int k = 0; k < 4; k++) h[k] = mul2(add2(h[k], both(-m)), both(q));
     };
-    for (int i = 0; i <= count; i++) {
+    for (int i = 0; i <= count && count > 0; i++) {
         float sa = 0.f, sh = 0.f;
         const float m = mean, q = rstd;
         if (i < count) {
             wait_copies(stages - 3);
             ask();   // where row i - 2 was
-            stats += gridDim.x;
+            Rows::clean(cols, p0);
+            Rows::clean(cols, p0 + room);
+            stats += g.apart;
             if (i + 1 < count) {
                 mean = __ldg(stats);
                 rstd = __ldg(stats + a.rows);
@@ -627,7 +666,7 @@ __global__ void __launch_bounds__(LANES, blocks_of(LANES)) norm_bwd_ring_kernel(
         if (out != nullptr) {
             if (i > 0) {
                 float ma, mh;
-                block_sum2<W>(part[p ^ 1][0], part[p ^ 1][1], ma, mh);
+                group_sum2<LANES / 32>(part[p ^ 1], ma, mh);
                 ma *= inv_n;
                 mh *= inv_n;
 #pragma unroll
@@ -639,12 +678,12 @@ __global__ void __launch_bounds__(LANES, blocks_of(LANES)) norm_bwd_ring_kernel(
                     for (int k = 0; k < 4; k++) h[k] = mul2(both(rstd1), fma2(h[k], both(-mh), fma2(d[k], w[c][k], both(-ma))));
                     cols.store(out, c, h);
                 }
-                out += gridDim.x * (long long)a.n;
+                out += g.apart * a.n;
             }
             const float s = warp_sum2(sa, sh);
-            if ((lane & 15) == 0) part[p][lane >> 4][warp] = s;
+            if ((g.lane & 15) == 0) part[p][g.lane >> 4][g.warp] = s;
             p ^= 1;
-            __syncthreads();
+            g.sync();
         }
         mean1 = m;
         rstd1 = q;
@@ -653,55 +692,60 @@ __global__ void __launch_bounds__(LANES, blocks_of(LANES)) norm_bwd_ring_kernel(
     }
     ptx::cp_async_wait<0>();
     if (a.parts == nullptr) return;
-    float *sums = a.parts + (long long)blockIdx.x * 2 * a.n;
+    // by column: the groups' shifts differ
+    const int groups = blockDim.x / LANES;
+    float *sums = a.parts + (long long)blockIdx.x * 2 * a.n, *mine = groups == 1 ? sums : reinterpret_cast<float *>(ring) + g.index * 2 * a.n;
+    __syncthreads();
 #pragma unroll
     for (int c = 0; c < CH; c++) {
         if (!cols.has(c)) continue;
-        if constexpr (SHIFT) {
 #pragma unroll
-            for (int k = 0; k < 8; k++) {
-                const int j = cols.first(c) + k;
-                if ((unsigned)j >= (unsigned)a.n) continue;
-                sums[j] = k % 2 == 0 ? dw[c][k / 2].x : dw[c][k / 2].y;
-                sums[a.n + j] = k % 2 == 0 ? db[c][k / 2].x : db[c][k / 2].y;
-            }
-        } else {
-            store_pairs(sums + cols.first(c), dw[c]);
-            store_pairs(sums + a.n + cols.first(c), db[c]);
+        for (int k = 0; k < 8; k++) {
+            const int j = cols.first(c) + k;
+            if (SHIFT && (unsigned)j >= (unsigned)a.n) continue;
+            mine[j] = k % 2 == 0 ? dw[c][k / 2].x : dw[c][k / 2].y;
+            mine[a.n + j] = k % 2 == 0 ? db[c][k / 2].x : db[c][k / 2].y;
         }
+    }
+    if (groups == 1) return;
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * a.n; i += blockDim.x) {
+        float v = 0.f;
+        for (int k = 0; k < groups; k++) v += reinterpret_cast<const float *>(ring)[k * 2 * a.n + i];
+        sums[i] = v;
     }
 }
 
 // Few rows, a block each: the row in registers, nothing to overlap.
-template <typename T, int LANES, int CH, bool SHIFT> __global__ void __launch_bounds__(LANES) norm_fwd_few_kernel(const Fwd a)
+template <typename T, int LANES, bool SHIFT> __global__ void __launch_bounds__(LANES) norm_fwd_few_kernel(const Fwd a)
 {
-    constexpr int W = LANES / 32;
-    __shared__ float part[2][W];
+    __shared__ float part[2][32];
     chain_start();
     chain_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long r = blockIdx.x;
     const Columns<LANES, SHIFT> cols = {a.n, shift_of<T>(r, a.stride), (int)threadIdx.x};
     const T *row = static_cast<const T *>(a.x) + r * a.stride, *end = static_cast<const T *>(a.x) + (a.rows - 1) * a.stride + a.n;
-    float2 x[CH][4], w[CH][4], b[CH][4];
+    Eight<T> raw[CH];
+    float2 x[CH][4], w[4], b[4];
 #pragma unroll
     for (int c = 0; c < CH; c++) {
-        Eight<T> e = Eight<T>();
-        if (cols.has(c)) load_piece(e, row + cols.first(c), end);
-        e.pairs(x[c]);
-        cols.clip(x[c], c);
-        cols.param(a.weight, a.param_f32, c, 1.f, w[c]);
-        cols.param(a.bias, a.param_f32, c, 0.f, b[c]);
+        raw[c] = Eight<T>();
+        if (cols.has(c)) load_piece(raw[c], row + cols.first(c), end);
     }
     const auto total = [&](float s, float *part) {
         s = warp_sum(s);
         if (lane == 0) part[warp] = s;
         __syncthreads();
-        return warp_sum(lane < W ? part[lane] : 0.f);
+        return warp_sum(lane < LANES / 32 ? part[lane] : 0.f);
     };
     float s = 0.f;
 #pragma unroll
-    for (int c = 0; c < CH; c++) s += sum8(x[c]);
+    for (int c = 0; c < CH; c++) {
+        raw[c].pairs(x[c]);
+        cols.clip(x[c], c);
+        s += sum8(x[c]);
+    }
     const float mean = total(s, part[0]) / (float)a.n;
     s = 0.f;
 #pragma unroll
@@ -714,9 +758,12 @@ template <typename T, int LANES, int CH, bool SHIFT> __global__ void __launch_bo
     const float rstd = 1.f / sqrtf(total(s, part[1]) / (float)a.n + a.eps);
 #pragma unroll
     for (int c = 0; c < CH; c++) {
+        if (!cols.has(c)) continue;
+        cols.param(a.weight, a.param_f32, c, 1.f, w);
+        cols.param(a.bias, a.param_f32, c, 0.f, b);
 #pragma unroll
-        for (int k = 0; k < 4; k++) x[c][k] = fma2(mul2(x[c][k], both(rstd)), w[c][k], b[c][k]);
-        if (cols.has(c)) cols.store(static_cast<T *>(a.y) + r * a.n, c, x[c]);
+        for (int k = 0; k < 4; k++) x[c][k] = fma2(mul2(x[c][k], both(rstd)), w[k], b[k]);
+        cols.store(static_cast<T *>(a.y) + r * a.n, c, x[c]);
     }
     if (a.stats != nullptr && threadIdx.x == 0) {
         a.stats[r] = mean;
@@ -848,10 +895,10 @@ template <typename T> __global__ void __launch_bounds__(256) norm_params_long_ke
 
 // ------------------------------------------------------------------ host side
 
-// How rows of n values are taken: threads of a row and pieces of 8 of each; for rows of a block the stages of its ring, as many
-// as its part of the SM's shared memory holds; blocks, the same on every device.
+// How rows of n values are taken: threads of a row, its groups in a block, the stages of a group's ring; blocks, the same on every
+// device.
 struct How {
-    int lanes, pieces, stages, blocks;   // lanes 0: value by value
+    int lanes, pieces, groups, stages, smem, blocks;   // lanes 0: value by value
     bool shift, few;
 };
 How how(const csa_layernorm_params &p, bool backward)
@@ -865,25 +912,29 @@ How how(const csa_layernorm_params &p, bool backward)
     // rows of all arguments lie alike between boundaries
     const bool alike = (p.x_stride - n) % vector == 0 && (!backward || (p.dy_stride - n) % vector == 0);
     h.shift = n % 8 != 0;
-    const int held = n + (h.shift && p.rows > 1 ? vector - 1 : 0);
+    const long long held = (long long)n + (h.shift && p.rows > 1 ? vector - 1 : 0);
     if (!alike || held > (size == 4 ? 8192 : 16384)) {
         blocks(1, 64);
         return h;
     }
-    h.pieces = held > 256 ? 2 : 1;
-    h.lanes = held <= 32 ? 4 : held <= 64 ? 8 : held <= 128 ? 16 : held <= 512 ? 32 : held <= 1024 ? 64 : held <= 2048 ? 128 : held <= 4096 ? 256 : held <= 8192 ? 512 : 1024;
-    if (h.lanes <= 32) {
+    if (held <= 512) {
+        h.pieces = held > 256 ? 2 : 1;
+        h.lanes = held <= 32 ? 4 : held <= 64 ? 8 : held <= 128 ? 16 : 32;
         blocks(256 / h.lanes * U, backward ? 3LL * linear::kSms : 4LL * linear::kSms);
         return h;
     }
-    const int live = backward ? 2 : 3, room = h.lanes * 16 * size * (backward ? 2 : 1);
-    int per_sm = blocks_of(h.lanes);
-    while ((225000 / per_sm - 1600) / room < live + 1) per_sm--;   // a row on its way at least; one block holds 3 of the longest
-    h.stages = (225000 / per_sm - 1600) / room;
+    const int live = backward ? 2 : 3;
+    h.lanes = held <= 1024 ? 64 : held <= 2048 ? 128 : held <= 3 * 1024 ? 192 : held <= 4096 ? 256 : held <= 6 * 1024 ? 384 : held <= 8192 ? 512 : 1024;
+    h.groups = most_threads(h.lanes, backward) / h.lanes;
+    const int room = h.lanes * CH * 8 * size * (backward ? 2 : 1);
+    constexpr int shared = 225000 - GROUPS * 512;
+    while (shared / h.groups / room < live + 1) h.groups--;   // a row on its way at least; the longest rows' ring holds 3 or 6
+    h.stages = shared / h.groups / room;
     if (h.stages > live + 1 + MOST_PENDING) h.stages = live + 1 + MOST_PENDING;
-    blocks(1, (long long)per_sm * linear::kSms);   // a multiple of 8, or a row each
+    h.smem = h.groups * h.stages * room;
+    blocks(1, linear::kSms);   // a multiple of 8, or a row of a group each
     // one row a block needs no ring (37 x 4096: 2.2 us, through the ring NNN)
-    h.few = !backward && p.rows <= h.blocks;
+    h.few = !backward && p.rows <= 4 * linear::kSms;
     return h;
 }
 
@@ -897,15 +948,17 @@ template <typename F> cudaError_t short_shape(const How &h, const F &f)
     if (h.lanes == 16) return f(Shape<16, 1>());
     return h.pieces == 1 ? f(Shape<32, 1>()) : f(Shape<32, 2>());
 }
-template <typename T, typename F> cudaError_t block_shape(const How &h, const F &f)
+template <typename T, typename F> cudaError_t ring_shape(const How &h, const F &f)
 {
-    if (h.lanes == 64) return f(Shape<64, 2>());
-    if (h.lanes == 128) return f(Shape<128, 2>());
-    if (h.lanes == 256) return f(Shape<256, 2>());
+    if (h.lanes == 64) return f(Shape<64, CH>());
+    if (h.lanes == 128) return f(Shape<128, CH>());
+    if (h.lanes == 192) return f(Shape<192, CH>());
+    if (h.lanes == 256) return f(Shape<256, CH>());
+    if (h.lanes == 384) return f(Shape<384, CH>());
     if constexpr (sizeof(T) == 2) {
-        if (h.lanes == 1024) return f(Shape<1024, 2>());
+        if (h.lanes == 1024) return f(Shape<1024, CH>());
     }
-    return f(Shape<512, 2>());
+    return f(Shape<512, CH>());
 }
 inline int long_threads(int n) { return n <= 2048 ? 128 : 1024; }
 
@@ -919,17 +972,13 @@ template <typename T> cudaError_t fwd(const Fwd &a, const How &h, cudaStream_t s
             return launch_chained(kernel, dim3((unsigned)h.blocks), 256, 0, 1, st, a);
         });
     }
-    return block_shape<T>(h, [&](auto shape) {
-        using S = decltype(shape);
-        if (h.few) {
-            auto *kernel = h.shift ? norm_fwd_few_kernel<T, S::LANES, S::PIECES, true> : norm_fwd_few_kernel<T, S::LANES, S::PIECES, false>;
-            return launch_chained(kernel, dim3((unsigned)a.rows), S::LANES, 0, 1, st, a);
-        }
-        auto *kernel = h.shift ? norm_fwd_ring_kernel<T, S::LANES, S::PIECES, true> : norm_fwd_ring_kernel<T, S::LANES, S::PIECES, false>;
-        const int smem = h.stages * S::LANES * S::PIECES * 8 * (int)sizeof(T);
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return ring_shape<T>(h, [&](auto shape) {
+        constexpr int L = decltype(shape)::LANES;
+        if (h.few) return launch_chained(h.shift ? norm_fwd_few_kernel<T, L, true> : norm_fwd_few_kernel<T, L, false>, dim3((unsigned)a.rows), L, 0, 1, st, a);
+        auto *kernel = h.shift ? norm_fwd_ring_kernel<T, L, true> : norm_fwd_ring_kernel<T, L, false>;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, h.smem);
         if (e != cudaSuccess) return e;
-        return launch_chained(kernel, dim3((unsigned)h.blocks), S::LANES, smem, 1, st, a, h.stages);
+        return launch_chained(kernel, dim3((unsigned)h.blocks), L * h.groups, h.smem, 1, st, a, h.stages);
     });
 }
 template <typename T> cudaError_t bwd(const Bwd &a, const How &h, cudaStream_t st)
@@ -949,13 +998,12 @@ template <typename T> cudaError_t bwd(const Bwd &a, const How &h, cudaStream_t s
             return launch_chained(kernel, dim3((unsigned)h.blocks), 256, 0, 1, st, a);
         });
     }
-    return block_shape<T>(h, [&](auto shape) {
-        using S = decltype(shape);
-        auto *kernel = h.shift ? norm_bwd_ring_kernel<T, S::LANES, S::PIECES, true> : norm_bwd_ring_kernel<T, S::LANES, S::PIECES, false>;
-        const int smem = h.stages * 2 * S::LANES * S::PIECES * 8 * (int)sizeof(T);
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return ring_shape<T>(h, [&](auto shape) {
+        constexpr int L = decltype(shape)::LANES;
+        auto *kernel = h.shift ? norm_bwd_ring_kernel<T, L, true> : norm_bwd_ring_kernel<T, L, false>;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, h.smem);
         if (e != cudaSuccess) return e;
-        return launch_chained(kernel, dim3((unsigned)h.blocks), S::LANES, smem, 1, st, a, h.stages);
+        return launch_chained(kernel, dim3((unsigned)h.blocks), L * h.groups, h.smem, 1, st, a, h.stages);
     });
 }
 
