@@ -771,23 +771,25 @@ template <typename T, int LANES, bool SHIFT> __global__ void __launch_bounds__(L
     }
 }
 
-// The blocks' sums joined: 8 columns a block (a sector), 128 threads a column.
-__global__ void __launch_bounds__(1024) norm_join_kernel(const float *parts, int blocks, int n, void *dw, void *db, int param_f32)
+// The blocks' sums joined: 8 columns a block (a sector), EACH threads a column.
+template <int EACH> __global__ void __launch_bounds__(8 * EACH) norm_join_kernel(const float *parts, int blocks, int n, void *dw, void *db, int param_f32)
 {
-    __shared__ float part[128][9];
+    __shared__ float part[EACH][9];
     chain_start();
     chain_wait();
     const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long i = (long long)blockIdx.x * 8 + tx;
     float s = 0.f;
     if (i < 2LL * n) {
-#pragma unroll 4
-        for (int b = ty; b < blocks; b += 128) s += parts[(long long)b * 2 * n + i];
+#pragma unroll 5
+        for (int b = ty; b < blocks; b += EACH) s += parts[(long long)b * 2 * n + i];
     }
     part[ty][tx] = s;
     __syncthreads();
     if (warp >= 8) return;
-    const float v = warp_sum((part[lane][warp] + part[lane + 32][warp]) + (part[lane + 64][warp] + part[lane + 96][warp]));
+    float v = part[lane][warp];
+    if constexpr (EACH == 128) v = (v + part[lane + 32][warp]) + (part[lane + 64][warp] + part[lane + 96][warp]);
+    v = warp_sum(v);
     const long long at = (long long)blockIdx.x * 8 + warp;
     void *out = at < n ? dw : db;
     if (lane > 0 || at >= 2LL * n || out == nullptr) return;
@@ -1040,7 +1042,9 @@ cudaError_t launch_layernorm_bwd(const csa_layernorm_params &p, const void *dy, 
     const norm::How h = norm::how(p, true);
     const cudaError_t e = p.dtype == CSA_F32 ? norm::bwd<float>(a, h, st) : norm::bwd<__nv_bfloat16>(a, h, st);
     if (e != cudaSuccess || !params) return e;
-    return linear::launch_chained(norm::norm_join_kernel, dim3((unsigned)((2LL * p.cols + 7) / 8)), 1024, 0, 1, st, a.parts, h.blocks, p.cols, dweight,
+    // many columns come from a block an SM, few from more
+    const bool wide = p.cols > 512;
+    return linear::launch_chained(wide ? norm::norm_join_kernel<32> : norm::norm_join_kernel<128>, dim3((unsigned)((2LL * p.cols + 7) / 8)), wide ? 256 : 1024, 0, 1, st, a.parts, h.blocks, p.cols, dweight,
                                   dbias, a.param_f32);
 }
 

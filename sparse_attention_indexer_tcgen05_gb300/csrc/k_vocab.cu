@@ -17,6 +17,7 @@
 #include "k_vocab.cuh"
 
 #include <cuda_fp16.h>
+#include <math.h>
 
 namespace csa {
 namespace vocab {
@@ -300,6 +301,123 @@ __global__ void __launch_bounds__(32 * ROWS) vocab_rows_kernel(const Rows a)
     *a.loss = w.x * s.x + w.y * s.y;
 }
 
+// ------------------------------------------------------------------ few rows, forward
+
+// A block a row whose scores lie in memory (a few rows' scores are small): its lse, and its targets' scores where they are.
+// Nothing has to be sorted or counted before: one token's loss is two launches.
+struct Few {
+    Targets t;
+    const float *z;              // [rows][vocab]
+    float label, teacher;        // weights of the losses
+    int mean;
+    float *losses, *loss;        // loss: of one row; null: there are more
+};
+
+__device__ __forceinline__ long long candidate_of(const Targets &a, long long at)
+{
+    return a.ids_64 ? static_cast<const long long *>(a.ids)[at] : static_cast<const int *>(a.ids)[at];
+}
+
+constexpr int FEW = 1024;        // threads of a row
+template <typename F> __device__ __forceinline__ float block_join(float x, float *part, const F &join)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = join(x, __shfl_xor_sync(0xffffffffu, x, o));
+    __syncthreads();
+    if (lane == 0) part[warp] = x;
+    __syncthreads();
+    x = part[lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = join(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+
+__global__ void __launch_bounds__(FEW) vocab_few_kernel(const Few a)
+{
+    __shared__ float part[32];
+    chain_start();
+    chain_wait();
+    const Targets &t = a.t;
+    const auto add = [](float x, float y) { return x + y; };
+    const auto most = [](float x, float y) { return fmaxf(x, y); };
+    const long long r = blockIdx.x;
+    const float *z = a.z + r * t.vocab;
+    float top = -INFINITY, sum = 0.f;
+    const auto take = [&](float x) {   // NaN ends up in the sum
+        if (x > top) {
+            sum *= ex2((top - x) * kLog2e);
+            top = x;
+        }
+        sum += x == -INFINITY ? 0.f : ex2((x - top) * kLog2e);
+    };
+    long long v = threadIdx.x;
+    for (; v + 7 * FEW < t.vocab; v += 8 * FEW) {
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++) x[k] = __ldcg(z + v + k * FEW);
+#pragma unroll
+        for (int k = 0; k < 8; k++) take(x[k]);
+    }
+    for (; v < t.vocab; v += FEW) take(__ldcg(z + v));
+    const float all = block_join(top, part, most);
+    const float lse = all + logf(block_join(top == -INFINITY ? sum : sum * ex2((top - all) * kLog2e), part, add));
+
+    const long long l = label_of(t, r);
+    const float label = l < 0 ? 0.f : l < t.vocab ? lse - __ldcg(z + l) : NAN;
+    // the candidates
+    float teacher = 0.f;
+    if (t.slots > 0) {
+        const int s = threadIdx.x;   // at most 1024
+        const long long at = r * t.slots + s, id = s < t.slots ? candidate_of(t, at) : -1;
+        const float logit = id >= 0 ? __ldg(t.logits + at) : -INFINITY;
+        float norm;
+        if (t.lse != nullptr) {
+            norm = __ldg(t.lse + r);
+        } else {
+            const float high = block_join(id < t.vocab ? logit : -INFINITY, part, most);
+            norm = high + logf(block_join(logit > -INFINITY && id < t.vocab ? expf(logit - high) : 0.f, part, add));
+        }
+        const float share = logit == -INFINITY ? 0.f : expf(logit - norm);
+        if (id >= t.vocab) teacher = NAN;
+        else if (share != 0.f) teacher = share * (logf(share) + (lse - __ldcg(z + id)));
+        teacher = block_join(teacher, part, add);
+    }
+    if (threadIdx.x > 0) return;
+    a.losses[r] = label;
+    a.losses[t.rows + r] = teacher;
+    if (a.loss != nullptr) *a.loss = a.label * label + a.teacher * teacher;   // one row: a mean is the row's own
+}
+
+// The loss of a few rows: what they have is counted here.
+__global__ void __launch_bounds__(32 * ROWS) vocab_few_loss_kernel(const Few a, float *loss)
+{
+    chain_start();
+    chain_wait();
+    const Targets &t = a.t;
+    __shared__ int labelled, taught;
+    if (threadIdx.x == 0) labelled = taught = 0;
+    __syncthreads();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int r = warp; r < (int)t.rows; r += ROWS) {   // a warp a row
+        int any = 0;
+        for (int s = lane; s < t.slots; s += 32) any |= candidate_of(t, (long long)r * t.slots + s) >= 0;
+        any = __any_sync(0xffffffffu, any);
+        if (lane == 0) {
+            atomicAdd(&labelled, label_of(t, r) >= 0);
+            atomicAdd(&taught, any);
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x > 0) return;
+    float x = 0.f, y = 0.f;
+    for (int r = 0; r < (int)t.rows; r++) {
+        x += a.losses[r];
+        y += a.losses[t.rows + r];
+    }
+    *loss = a.label / (float)(a.mean ? max(labelled, 1) : 1) * x + a.teacher / (float)(a.mean ? max(taught, 1) : 1) * y;
+}
+
 struct Dz {
     const void *e;               // [count][ld] fp16 or fp32
     bf16 *dz;                    // [count][ld], planes apart for fp32 values
@@ -389,6 +507,41 @@ inline int planes_of(const csa_vocab_loss_params &p) { return p.dtype == CSA_F32
 // memory, and large enough that dW's sums are read and written again but once in 16384 rows of a vocabulary of 131072.
 constexpr long long kKept = 4LL << 30;
 
+// A gradient's product with its k axis cut for more than one round of tiles too, where that fills the last one: dx of 3001 x 1024
+// over 50257 columns has 48 tiles for 76 pairs, in three pieces 144 (220 us -> NNN).  Times as in plan_product.
+Plan cut_further(Plan p, long long M, long long N, long long K)
+{
+    if (p.shape != PAIR_256) return p;
+    const double tiles = (double)((M + 255) / 256) * ((N + 255) / 256), slots = kSms / 2;
+    const long long steps = (K + 63) / 64;
+    const auto time = [&](long long cut) {
+        const long long per = (steps + cut - 1) / cut;
+        return ceil(tiles * cut / slots) * per * 0.28 + (cut > 1 ? 2.5 + (double)M * N * 8 * cut / 4e6 : 0.0);
+    };
+    long long best = p.splits;
+    for (long long cut = p.splits; cut <= 16 && cut * 16 <= steps; cut++)
+        if (time(cut) < 0.97 * time(best)) best = cut;
+    const long long per = (steps + best - 1) / best;
+    p.splits = (int)((steps + per - 1) / per);
+    return p;
+}
+
+// Few rows' scores by the projections' kernels for few rows, which run at the speed of the pass over the weight (a token over
+// 32000 x 2048: NNN us; on tiles 37).
+inline csa_linear_params product_of(const csa_vocab_loss_params &p)
+{
+    csa_linear_params q = {};
+    q.dtype = p.dtype;
+    q.out_dtype = CSA_F32;
+    q.in_features = p.features;
+    q.out_features = p.vocab;
+    q.alpha = p.alpha;
+    q.rows = p.rows;
+    q.x_stride = p.x_stride;
+    return q;
+}
+inline bool few_rows(const csa_vocab_loss_params &p) { return small_linear(product_of(p)); }
+
 struct Layout {
     bool stage_x, stage_w;
     long long piece;     // rows of a piece
@@ -402,6 +555,17 @@ Layout plan(const csa_vocab_loss_params &p, bool backward)
     Layout b = {};
     const long long M = p.rows, K = p.features, V = p.vocab, ld = up8(V);
     if (M == 0) return b;
+    size_t at = 0;
+    const auto take = [&](size_t &off, size_t bytes) {
+        off = at;
+        at += up256(bytes);
+    };
+    if (!backward && few_rows(p)) {
+        take(b.off_z, (size_t)M * V * 4);
+        take(b.off_losses, (size_t)M * 8);
+        b.total = at;
+        return b;
+    }
     b.width = p.slots + 1;
     b.groups = (int)((V + GROUP - 1) / GROUP);
     // a piece's bytes a row: the scores, or the groups' sums alone
@@ -416,11 +580,6 @@ Layout plan(const csa_vocab_loss_params &p, bool backward)
     }
     b.stage_x = staged(p.dtype, p.x_stride);
     b.stage_w = staged(p.dtype, K);
-    size_t at = 0;
-    const auto take = [&](size_t &off, size_t bytes) {
-        off = at;
-        at += up256(bytes);
-    };
     take(b.off_x, b.stage_x ? staged_bytes(p.dtype, M, K) : 0);
     take(b.off_w, b.stage_w ? staged_bytes(p.dtype, V, K) : 0);
     take(b.off_sorted, (size_t)M * b.width * 4);
@@ -437,8 +596,8 @@ Layout plan(const csa_vocab_loss_params &p, bool backward)
         b.off_dz = b.off_e;
         if (p.dtype == CSA_F32) take(b.off_dz, (size_t)b.piece * ld * 6);
         take(b.off_sum, b.pieces > 1 && p.dtype == CSA_BF16 ? (size_t)V * K * 4 : 0);
-        b.dx = plan_product(b.piece, K, V, planes_of(p), 1, p.dtype == CSA_F32, kSms);
-        b.dw = plan_product(V, K, b.piece, planes_of(p), 1, p.dtype == CSA_F32, kSms);
+        b.dx = cut_further(plan_product(b.piece, K, V, planes_of(p), 1, p.dtype == CSA_F32, kSms), b.piece, K, V);
+        b.dw = cut_further(plan_product(V, K, b.piece, planes_of(p), 1, p.dtype == CSA_F32, kSms), V, K, b.piece);
         const size_t dx = b.dx.splits > 1 ? (size_t)b.dx.splits * b.piece * partial_stride(K) * 4 : 0;
         const size_t dw = b.dw.splits > 1 ? (size_t)b.dw.splits * V * partial_stride(K) * 4 : 0;
         take(b.off_part, dx > dw ? dx : dw);
@@ -478,16 +637,8 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
         if (dw != nullptr) VOC_TRY(cudaMemsetAsync(dw, 0, (size_t)V * K * size, st));
         return cudaMemsetAsync(loss, 0, 4, st);
     }
-    note_path("tcgen05");
-    int sms = 0;
-    VOC_TRY(sms_here(&sms));
     const Layout b = plan(p, backward);
     char *w = static_cast<char *>(ws);
-    Stage job[2] = {};
-    Operand ox = operand(p.dtype, x, p.x_stride, M, (int)K, b.stage_x, w + b.off_x, true, &job[0]);
-    Operand ow = operand(p.dtype, weight, K, V, (int)K, b.stage_w, w + b.off_w, true, &job[1]);
-    VOC_TRY(run_stages(p.dtype, job, st));
-
     Targets g = {};
     g.labels = t.labels;
     g.ids = t.teacher_ids;
@@ -496,9 +647,29 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
     g.labels_64 = p.labels_64;
     g.ids_64 = p.ids_64;
     g.slots = p.slots;
-    g.width = p.slots + (t.labels != nullptr);
     g.rows = M;
     g.vocab = V;
+    float *losses = row_loss != nullptr ? row_loss : reinterpret_cast<float *>(w + b.off_losses);
+    if (!backward && few_rows(p)) {
+        note_path("generic");
+        Epilogue e = {};
+        e.alpha = p.alpha;
+        e.out = w + b.off_z;
+        e.out_f32 = 1;
+        VOC_TRY(launch_linear_small(product_of(p), x, weight, e, kSms, st));
+        const Few f = {g, reinterpret_cast<const float *>(w + b.off_z), p.label_weight, p.teacher_weight, p.reduction == 0, losses, M == 1 ? loss : nullptr};
+        VOC_TRY(launch_chained(vocab_few_kernel, dim3((unsigned)M), FEW, 0, 1, st, f));
+        return M == 1 ? cudaSuccess : launch_chained(vocab_few_loss_kernel, dim3(1), 32 * ROWS, 0, 1, st, f, loss);
+    }
+    note_path("tcgen05");
+    int sms = 0;
+    VOC_TRY(sms_here(&sms));
+    Stage job[2] = {};
+    Operand ox = operand(p.dtype, x, p.x_stride, M, (int)K, b.stage_x, w + b.off_x, true, &job[0]);
+    Operand ow = operand(p.dtype, weight, K, V, (int)K, b.stage_w, w + b.off_w, true, &job[1]);
+    VOC_TRY(run_stages(p.dtype, job, st));
+
+    g.width = p.slots + (t.labels != nullptr);
     g.sorted = reinterpret_cast<int *>(w + b.off_sorted);
     g.weight = reinterpret_cast<float *>(w + b.off_weight);
     g.starts = reinterpret_cast<unsigned short *>(w + b.off_starts);
@@ -517,7 +688,6 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
 
     const bool grads = dx != nullptr || dw != nullptr;
     const Weights weights = {g.counts, (int)blocks, p.reduction == 0, p.label_weight, p.teacher_weight};
-    float *losses = row_loss != nullptr ? row_loss : reinterpret_cast<float *>(w + b.off_losses);
     float *z = reinterpret_cast<float *>(w + b.off_z);
     float2 *parts = reinterpret_cast<float2 *>(w + b.off_parts), *info = grads ? reinterpret_cast<float2 *>(w + b.off_info) : nullptr;
     int all_blocks = 0;

@@ -123,7 +123,9 @@ def check(t, params, alpha=1.0, wl=1.0, wt=1.0, mean=True, need=(True, True), **
     close(loss, r["loss"], loss_tol, "loss")
 
     loss2, dx, dw = B.csa_vocab_loss_bwd(params, t["x"], t["weight"], **targets, need_dx=need[0], need_dw=need[1], **kw)
-    assert torch.equal(loss2, loss)
+    if M > 16:   # few rows' forward runs on kernels of its own
+        assert torch.equal(loss2, loss)
+    close(loss2, r["loss"], loss_tol, "loss of the backward")
     bf16 = params.value_dtype is torch.bfloat16
     # p: the scores' and lse's errors, the exponential's; kept in fp16 against its group's largest; c and tau are fp32
     p_tol = r["p"] * ((z_tol + lse_tol[:, None]) * 1.1 + (r["z"] - r["z"].amax(1, keepdim=True)).abs() * 2.0 ** -23 + 2.0 ** -20)
