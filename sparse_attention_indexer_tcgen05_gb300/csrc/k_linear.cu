@@ -257,7 +257,7 @@ Bwd plan_bwd(const csa_linear_params &p)
 Operand operand(int dtype, const void *x, long long stride, long long rows, int cols, bool stage, void *to, bool k_major,
                 Stage *job)
 {
-    Operand o;
+    Operand o = {};
     o.k_major = k_major;
     if (!stage) {
         o.base = static_cast<const bf16 *>(x);

@@ -135,6 +135,7 @@ struct Operand {
     const __nv_bfloat16 *base;
     long long ld, plane;   // elements; multiples of 8
     bool k_major;
+    long long held;        // indices i that memory holds, where they are more than the product takes (they may be anything); 0: as many
 };
 
 // Tile and cut of the k axis of a product (see k_linear_tc.cu).

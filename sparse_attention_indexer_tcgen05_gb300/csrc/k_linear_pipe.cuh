@@ -358,6 +358,7 @@ inline void tile_counts(Shape s, long long M, long long N, int &mt, int &nt)
 // m/n-contiguous operand of whole 64-wide blocks has these as an axis of their own (one copy then brings several).
 inline bool encode(CUtensorMap *m, const Operand &o, long long n, long long K, int planes, int rows, bool blocks)
 {
+    if (o.held > n) n = o.held;
     const long long inner = o.k_major ? K : n, outer = o.k_major ? n : K;
     // one plane: its stride is never used, but has to be a legal one (below 2^40 bytes)
     const long long far = 1LL << 38, whole = outer > far / o.ld ? far : outer * o.ld;

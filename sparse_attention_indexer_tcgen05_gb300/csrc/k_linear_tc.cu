@@ -454,7 +454,7 @@ cudaError_t launch_product_tc(const Product &p, int sms, cudaStream_t st)
     // a warp of the 128 x 64 tile has half a row of bf16 columns; a kept z off 16-byte rows needs the buffer for itself
     a.tma_out = s != LONE_64 && a.ldo % (a.e.out_f32 ? 4 : 8) == 0 &&
                 (a.e.preact == nullptr || p.N % (a.e.preact_f32 ? 4 : 8) == 0);
-    a.blocks_a = !p.a.k_major && p.M % 64 == 0;
+    a.blocks_a = !p.a.k_major && (p.a.held > p.M ? p.a.held : p.M) % 64 == 0;
     a.blocks_b = !p.b.k_major && p.N % 64 == 0;
     a.rows_a = p.M >= BM ? BM : p.a.k_major ? (int)((p.M + 7) & ~7LL) : p.M > 64 ? 128 : 64;
     Maps m = {};

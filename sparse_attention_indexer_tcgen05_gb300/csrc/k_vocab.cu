@@ -42,8 +42,8 @@ struct Targets {
     long long rows, vocab;
     int *sorted;                 // [width][rows]
     float *weight;               // [width][rows]: t of a candidate, -1 for the label; NaN and -inf where the id is not a column
-    unsigned short *starts;      // [rows][marks]: how many targets lie before each group of columns, and before the end
-    int marks;
+    int *marks;                  // [rows][groups]: how many targets lie before each group of columns, and from bit 16 on in it
+    int groups;
     int2 *counts;                // [blocks]: rows with a label, rows with a candidate
     int *done;                   // set to 0: blocks of rows_kernel that have finished
 };
@@ -147,9 +147,25 @@ __global__ void __launch_bounds__(32 * ROWS) vocab_prepare_kernel(const Targets 
             a.weight[place * a.rows + r] = t;
         }
         __syncwarp();
-        for (int g = lane, at = 0; g < a.marks; g += 32) {
-            while (at < a.width && sorted[at] < g * (long long)GROUP) at++;
-            a.starts[r * a.marks + g] = (unsigned short)at;
+        // how many targets lie before group g: steps of halves, five searches at a time under one another's latency (as a walk
+        // along the targets, 786 groups of 3001 rows took 20 us)
+        int half = 1;
+        while (2 * half <= a.width) half *= 2;
+        for (int g0 = 0; g0 < a.groups; g0 += 128) {
+            int at[5] = {};
+            for (int step = half; step > 0; step /= 2) {
+#pragma unroll
+                for (int q = 0; q < 5; q++) {
+                    const int k = at[q] + step;
+                    if (k <= a.width && sorted[k - 1] < (g0 + 32 * q + lane) * (long long)GROUP) at[q] = k;
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const int g = g0 + 32 * q + lane;
+                const int first_then = __shfl_sync(0xffffffffu, at[q + 1], 0), beside = __shfl_down_sync(0xffffffffu, at[q], 1);
+                if (g < a.groups) a.marks[r * a.groups + g] = at[q] | ((lane < 31 ? beside : first_then) - at[q]) << 16;
+            }
         }
     }
     count(a, lane == 0 && label >= 0, lane == 0 && taught);
@@ -542,18 +558,21 @@ inline csa_linear_params product_of(const csa_vocab_loss_params &p)
 }
 inline bool few_rows(const csa_vocab_loss_params &p) { return small_linear(product_of(p)); }
 
+// A row of scores ends with a whole block of 64, as one copy of the product that makes dW takes them (50257 columns of 3001 rows
+// by 1024: 200 us in copies of 64 columns, NNN in one).
+inline long long ld_of(long long vocab) { return (vocab + 63) & ~63LL; }
+
 struct Layout {
     bool stage_x, stage_w;
     long long piece;     // rows of a piece
     int pieces, width, groups;
     linear::Plan dx, dw;
-    int marks;
-    size_t off_x, off_w, off_sorted, off_weight, off_starts, off_z, off_counts, off_losses, off_info, off_parts, off_e, off_dz, off_sum, off_part, total;
+    size_t off_x, off_w, off_sorted, off_weight, off_marks, off_z, off_counts, off_losses, off_info, off_parts, off_e, off_dz, off_sum, off_part, total;
 };
 Layout plan(const csa_vocab_loss_params &p, bool backward)
 {
     Layout b = {};
-    const long long M = p.rows, K = p.features, V = p.vocab, ld = up8(V);
+    const long long M = p.rows, K = p.features, V = p.vocab, ld = ld_of(V);
     if (M == 0) return b;
     size_t at = 0;
     const auto take = [&](size_t &off, size_t bytes) {
@@ -584,8 +603,7 @@ Layout plan(const csa_vocab_loss_params &p, bool backward)
     take(b.off_w, b.stage_w ? staged_bytes(p.dtype, V, K) : 0);
     take(b.off_sorted, (size_t)M * b.width * 4);
     take(b.off_weight, (size_t)M * b.width * 4);
-    b.marks = b.groups + 1;
-    take(b.off_starts, p.slots > 0 ? (size_t)M * b.marks * 2 : 0);
+    take(b.off_marks, p.slots > 0 ? (size_t)M * b.groups * 4 : 0);
     take(b.off_z, (size_t)M * b.width * 4);
     take(b.off_counts, (size_t)((M + ROWS - 1) / ROWS) * 8 + 8);   // and the count of finished blocks
     take(b.off_losses, (size_t)M * 8);
@@ -630,7 +648,7 @@ size_t vocab_loss_workspace(const csa_vocab_loss_params &p, bool backward) { ret
 cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, const void *weight, const csa_vocab_targets &t, float *loss,
                               float *row_loss, void *dx, void *dw, bool backward, void *ws, cudaStream_t st)
 {
-    const long long M = p.rows, K = p.features, V = p.vocab, ld = up8(V);
+    const long long M = p.rows, K = p.features, V = p.vocab, ld = ld_of(V);
     const int planes = planes_of(p);
     const size_t size = p.dtype == CSA_F32 ? 4 : 2;
     if (M == 0) {
@@ -672,8 +690,8 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
     g.width = p.slots + (t.labels != nullptr);
     g.sorted = reinterpret_cast<int *>(w + b.off_sorted);
     g.weight = reinterpret_cast<float *>(w + b.off_weight);
-    g.starts = reinterpret_cast<unsigned short *>(w + b.off_starts);
-    g.marks = b.marks;
+    g.marks = reinterpret_cast<int *>(w + b.off_marks);
+    g.groups = b.groups;
     g.done = reinterpret_cast<int *>(w + b.off_counts);
     g.counts = reinterpret_cast<int2 *>(w + b.off_counts) + 1;
     const bool single = p.slots == 0;
@@ -698,8 +716,8 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
         px.base += first * ox.ld;
         Scores s = {};
         s.ids = g.sorted + first;
-        s.starts = single ? nullptr : g.starts + first * g.marks;
-        s.lds = g.marks;
+        s.marks = single ? nullptr : g.marks + first * g.groups;
+        s.groups = g.groups;
         s.z = z + first;
         s.slots = g.width;
         s.ld = M;
@@ -757,6 +775,7 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
         if (dw != nullptr) {
             q.a = od;
             q.a.k_major = false;
+            q.a.held = ld;
             q.b = px;
             q.b.k_major = false;
             q.M = V;

@@ -13,9 +13,9 @@ constexpr int NONE = 0x7fffffff;   // a slot without a column
 // Where the scores of a piece of rows go.
 struct Scores {
     const int *ids;        // [slots][ld]: the columns that each row's targets name, ascending, NONE behind them
-    const unsigned short *starts;   // [M][lds]: how many of them lie before each group, and before the end; null: one slot a row
+    const int *marks;      // [M][groups]: how many of them lie before each group, and from bit 16 on in it; null: one slot a row
     float *z;              // [slots][ld]: the scores there
-    int slots, lds;
+    int slots, groups;
     long long ld;
     float2 *parts;         // [groups][M]: a group's largest score in base-2 units, and the sum of 2^(score - largest)
     float alpha;

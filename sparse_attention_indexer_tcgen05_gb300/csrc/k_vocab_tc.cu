@@ -104,43 +104,31 @@ vocab_scores_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         const float c2 = fabsf(s.alpha) * kLog2e;   // > 0
         // Rows, columns and slots are below 2^31, and so are a tile's ends.
         const int M = (int)a.M, N = (int)a.N;
-        const auto place = [&](int u, int &m, int &n0) {
+        const auto place = [&](int u, int &m, int &n0) {   // behind the last unit: none
+            m = M;
+            n0 = N;
+            if (u >= a.units) return;
             const Unit x = unit_of<BN>(a, u);
             m = (x.m * CG + (int)p.rank) * BM + quad * 32 + lane;
             n0 = (int)x.n0 + side * GROUP;
         };
-        // A unit's targets of this lane: where they begin and end is asked for a unit ahead, the first two while the last
-        // unit's scores are reduced.  (Found when their unit came, 64 of 32768 columns cost a product of 4096 x 1024 50 us of 227.)
-        int first = 0, end = 0, next = NONE, after = NONE;
-        const auto ask_marks = [&](int u, int &b, int &e) {
-            int m, n0;
-            b = e = 0;
-            if (u >= a.units) return;
-            place(u, m, n0);
-            if (m >= M || n0 >= N) return;
-            e = 1;
-            if (s.starts != nullptr) {
-                const unsigned short *mark = s.starts + m * (long long)s.lds + n0 / GROUP;
-                b = __ldg(mark);
-                e = __ldg(mark + 1);
-            }
+        // A unit's targets of this lane: where they begin and how many they are is asked for a unit ahead, the first while the
+        // last unit's scores are reduced.  (Found when their unit came, 64 of 32768 columns cost a product of 4096 x 1024 50 us
+        // of 227.)  Both in one register: kernels of 96 of them have few to spare.
+        const auto ask_marks = [&](int m, int n0) {
+            if (m >= M || n0 >= N) return 0;
+            if (s.marks == nullptr) return 1 << 16;
+            return __ldg(s.marks + m * (long long)s.groups + n0 / GROUP);
         };
-        const auto ask_targets = [&](int u, int b, int e) {
-            int m, n0;
-            next = after = NONE;
-            if (b >= e) return;
-            place(u, m, n0);
-            next = __ldg(s.ids + b * s.ld + m);
-            if (b + 1 < e) after = __ldg(s.ids + (b + 1) * s.ld + m);
-        };
-        ask_marks(p.u0, first, end);
-        ask_targets(p.u0, first, end);
+        const auto ask_target = [&](int m, int marks) { return marks >> 16 == 0 ? NONE : __ldg(s.ids + (marks & 0xffff) * s.ld + m); };
+        int m, n0;
+        place(p.u0, m, n0);
+        int marks = ask_marks(m, n0), next = ask_target(m, marks);
         int tc = 0;
         for (int u = p.u0; u < a.units; u += p.ustep) {
-            int m, n0, first_then, end_then;
-            place(u, m, n0);
-            const int m0 = m - lane;
-            ask_marks(u + p.ustep, first_then, end_then);
+            int m_then, n0_then;
+            place(u + p.ustep, m_then, n0_then);
+            const int marks_then = ask_marks(m_then, n0_then);
             float v[GROUP] = {};
             for (int it = 0; it < a.ksteps; it += CHUNK, tc++) {
                 p.wait_sums(tc);
@@ -154,33 +142,30 @@ vocab_scores_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
                     for (int k = 0; k < 16; k++) v[g + k] += w[k];
                 }
             }
-            // this unit's targets, whose scores are wanted; then the next unit's are asked for
-            int left = end - first, col = next - n0, col2 = after - n0;
-            if (s.starts == nullptr && (col < 0 || col >= GROUP)) left = 0;
-            float *z = s.z + first * s.ld + m;
-            const int *rest = s.ids + (first + 2) * s.ld + m;
-            first = first_then;
-            end = end_then;
-            ask_targets(u + p.ustep, first, end);
-            if (m0 >= M || n0 >= N) continue;
+            // this unit's targets, whose scores are wanted; then the next unit's first is asked for
+            int left = marks >> 16, col = next - n0;
+            if (s.marks == nullptr && (unsigned)col >= GROUP) left = 0;
+            long long at = (marks & 0xffff) * s.ld + m;
+            marks = marks_then;
+            next = ask_target(m_then, marks);
+            const int row = m, m0 = m - lane, col0 = n0;
+            m = m_then;
+            n0 = n0_then;
+            if (m0 >= M || col0 >= N) continue;
             while (__any_sync(0xffffffffu, left > 0)) {
                 const float x = pick(v, col);
                 if (left > 0) {
-                    *z = s.alpha * x;
-                    z += s.ld;
-                    col = col2;
-                    if (--left > 1) {
-                        col2 = __ldg(rest) - n0;
-                        rest += s.ld;
-                    }
+                    s.z[at] = s.alpha * x;
+                    at += s.ld;
+                    if (--left > 0) col = __ldg(s.ids + at) - col0;
                 }
             }
             if (s.alpha < 0.f) {
 #pragma unroll
                 for (int k = 0; k < GROUP; k++) v[k] = -v[k];
             }
-            if (N - n0 < GROUP) {   // columns that do not exist
-                const int valid = N - n0;
+            if (N - col0 < GROUP) {   // columns that do not exist
+                const int valid = N - col0;
 #pragma unroll
                 for (int k = 0; k < GROUP; k++)
                     if (k >= valid) v[k] = -INFINITY;
@@ -203,7 +188,7 @@ vocab_scores_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
                 sum = add2(sum, make_float2(v[k], v[k + 1]));
                 more = add2(more, make_float2(v[k + 2], v[k + 3]));
             }
-            if (m < M) s.parts[n0 / GROUP * a.M + m] = make_float2(top, (sum.x + more.x) + (sum.y + more.y));
+            if (row < M) s.parts[col0 / GROUP * a.M + row] = make_float2(top, (sum.x + more.x) + (sum.y + more.y));
             if (s.e == nullptr) continue;
             if constexpr (P == 1) {
                 if (lane == 0) bulk_wait_read();   // the last group has left the buffer
@@ -221,7 +206,7 @@ vocab_scores_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) {
-                    tma_store_3d(&map_e, b.p, n0, m0, 0);
+                    tma_store_3d(&map_e, b.p, col0, m0, 0);
                     bulk_commit();
                 }
             } else {
@@ -230,7 +215,7 @@ vocab_scores_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
                     float w[C];
 #pragma unroll
                     for (int k = 0; k < C; k++) w[k] = v[g + k];
-                    if (n0 + g < N) tma_tile<float>(&map_e, w, m0, n0 + g, 0, false, true, b);
+                    if (col0 + g < N) tma_tile<float>(&map_e, w, m0, col0 + g, 0, false, true, b);
                 }
             }
         }
