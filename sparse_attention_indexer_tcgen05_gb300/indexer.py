@@ -1,6 +1,7 @@
 """One training step of the indexer's own weights, from hidden states to updated weights.
 
     q_idx = rope(x Wq^T)         [rows, idx_heads, idx_dim]       k_idx = rope(x_c Wk^T)   [compressed rows, idx_dim]
+                                                                  (key_norm: k_idx = rope(norm(x_c Wk^T)))
     w     = scale x Ww^T         [rows, idx_heads] fp32            ids, scores = csa_indexer_fwd(q_idx, w, k_idx)
     loss, dq_idx, dw, dk_idx = csa_indexer_bwd(...)                the gradients go back through the rotation and the
                                                                    projections into the weights, which AdamW updates.
@@ -22,10 +23,13 @@ class IndexerTrainer:
     updated in place), their gradients and their AdamW state.
 
     rot_dim values of each indexer head rotate (0: none), by `sections` of the position axes.  weight_scale is the
-    indexer's scale, folded into w.  eight_bit holds the moments in e4m3; bf16 weights get fp32 master copies."""
+    indexer's scale, folded into w.  key_norm: (weight, bias) [idx_dim] of a layer norm of the keys between their projection
+    and their rotation, trained with the others (f32 or bf16; bias may be None).  eight_bit holds the moments in e4m3; bf16
+    weights get fp32 master copies."""
 
     def __init__(self, params: B.Params, wq, wk, ww, rot_dim=0, sections=None, interleaved=False, weight_scale=1.0,
-                 lr=1e-4, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.0, eight_bit=False, positions_64=False):
+                 lr=1e-4, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.0, eight_bit=False, positions_64=False,
+                 key_norm=None, key_norm_eps=1e-6):
         c = params.c
         self.params, self.wq, self.wk, self.ww = params, wq, wk, ww
         dev, dt = wq.device, params.value_dtype
@@ -53,18 +57,31 @@ class IndexerTrainer:
         self.ids, self.selscore = new(rows, params.K, dtype=torch.int32), new(rows, params.K, dtype=f32)
         self.loss = new(dtype=f32)
         self.dq_idx, self.dk_idx, self.dw = new(rows, heads, dim), new(keys, dim), new(rows, heads, dtype=f32)
-        self.grads = [torch.empty_like(t) for t in (wq, wk, ww)]
-        need = [params.workspace_bytes] + [p.workspace_bytes for p in (self.p_q, self.p_k, self.p_w)]
-        self.workspace = new(max(1, *need), dtype=torch.uint8)  # one call after the other uses it
-
         weights = [wq, wk, ww]
-        master = [t.float() for t in weights] if dt != f32 else None
+        need = [params.workspace_bytes] + [p.workspace_bytes for p in (self.p_q, self.p_k, self.p_w)]
+        self.norm = None
+        if key_norm is not None:
+            self.key_norm = tuple(key_norm)
+            for name, t in zip(("weight", "bias"), self.key_norm, strict=True):
+                if t is None and name == "bias":
+                    continue
+                if tuple(t.shape) != (dim,) or t.dtype != self.key_norm[0].dtype:
+                    raise ValueError(f"key_norm's {name} must be {self.key_norm[0].dtype} [{dim}], got {t.dtype} {tuple(t.shape)}")
+            self.norm = B.LayerNormParams(keys, dim, c.dtype, self.key_norm[0].dtype, key_norm_eps)
+            self.k_proj, self.k_stats = new(keys, dim), new(2, keys, dtype=f32)
+            weights += [t for t in self.key_norm if t is not None]
+            need.append(self.norm.bwd_workspace_bytes)
+        self.grads = [torch.empty_like(t) for t in weights]
+        self.workspace = new(max(1, *need), dtype=torch.uint8)  # one call after the other uses it
+        master = [t.float() if t.dtype != f32 else None for t in weights] if dt != f32 or self.norm is not None else None
         self.tensors = B.AdamWTensors(weights, self.grads, master=master, **B.AdamWTensors.zero_state(weights, eight_bit))
 
     def project(self, x, x_c, positions=None, key_positions=None, inv_freq=None):
         """q_idx, w and k_idx of the hidden states, into the trainer's buffers."""
         B.csa_linear_fwd(self.p_q, x, self.wq, workspace=self.workspace, out=self.q_idx)
-        B.csa_linear_fwd(self.p_k, x_c, self.wk, workspace=self.workspace, out=self.k_idx)
+        B.csa_linear_fwd(self.p_k, x_c, self.wk, workspace=self.workspace, out=self.k_idx if self.norm is None else self.k_proj)
+        if self.norm is not None:
+            B.csa_layernorm_fwd(self.norm, self.k_proj, *self.key_norm, out=self.k_idx, stats=self.k_stats)
         B.csa_linear_fwd(self.p_w, x, self.ww, workspace=self.workspace, out=self.w)
         if self.r_q is not None:
             B.csa_rope(self.r_q, self.q_idx, positions, inv_freq, out=self.q_idx)
@@ -72,8 +89,8 @@ class IndexerTrainer:
         return self.q_idx, self.w, self.k_idx
 
     def gradients(self, x, x_c, q, kv, kv_c, sink, positions=None, key_positions=None, inv_freq=None):
-        """Forward and backward: the loss (a device scalar) and the gradients of wq, wk and ww, in the trainer's
-        buffers."""
+        """Forward and backward: the loss (a device scalar) and the gradients of wq, wk and ww (and of the keys' norm), in the
+        trainer's buffers."""
         p = self.params
         q_idx, w, k_idx = self.project(x, x_c, positions, key_positions, inv_freq)
         B.csa_indexer_fwd(p, q_idx, w, k_idx, workspace=self.workspace, ids=self.ids, selscore=self.selscore)
@@ -82,6 +99,10 @@ class IndexerTrainer:
         if self.r_q is not None:
             B.csa_rope(self.r_dq, self.dq_idx, positions, inv_freq, out=self.dq_idx)
             B.csa_rope(self.r_dk, self.dk_idx, key_positions, inv_freq, out=self.dk_idx)
+        if self.norm is not None:
+            weight, bias = self.key_norm
+            B.csa_layernorm_bwd(self.norm, self.dk_idx, self.k_proj, weight, self.k_stats, need_dbias=bias is not None,
+                                workspace=self.workspace, out=(self.dk_idx, self.grads[3], self.grads[4] if bias is not None else None))
         for lp, dy, rows, weight, dw in ((self.p_q, self.dq_idx.view(-1, self.wq.shape[0]), x, self.wq, self.grads[0]),
                                          (self.p_k, self.dk_idx, x_c, self.wk, self.grads[1]),
                                          (self.p_w, self.dw, x, self.ww, self.grads[2])):
