@@ -155,10 +155,11 @@ __global__ void __launch_bounds__(256) join_kernel(const float *partial, int spl
     }
     if (!live) return;
     const long long i = m * N + n;
+    const float alpha = e.factor();
     float z[4];
 #pragma unroll
     for (int k = 0; k < 4; k++) {
-        z[k] = e.alpha * v[k] + (e.bias != nullptr && n + k < N ? __ldg(e.bias + n + k) : 0.f);
+        z[k] = alpha * v[k] + (e.bias != nullptr && n + k < N ? __ldg(e.bias + n + k) : 0.f);
         v[k] = act_fwd(z[k], e.act);
         if (e.res != nullptr && n + k < N)
             v[k] += e.out_f32 ? ((const float *)e.res)[m * e.ldr + n + k] : __bfloat162float(((const bf16 *)e.res)[m * e.ldr + n + k]);

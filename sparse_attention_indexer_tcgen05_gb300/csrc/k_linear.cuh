@@ -85,6 +85,8 @@ struct Epilogue {
     void *preact;        // [M][N] bf16 or fp32 as `preact_f32` says, or null
     int out_f32, preact_f32;
     float *partial;      // rows partial_stride(N) apart
+    const float *scale;  // a device scalar that multiplies the result too (products on tcgen05 and their joins, without a bias), or null
+    __device__ __forceinline__ float factor() const { return scale != nullptr ? alpha * __ldg(scale) : alpha; }
 };
 
 // Rows of partial sums start on 32-byte sectors whatever N is.

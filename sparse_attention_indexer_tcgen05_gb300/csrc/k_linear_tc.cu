@@ -286,6 +286,11 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
 #pragma unroll
                         for (int k = 0; k < C; k++) v[k] *= alpha;
                     }
+                    if (a.e.scale != nullptr) {
+                        const float f = __ldg(a.e.scale);
+#pragma unroll
+                        for (int k = 0; k < C; k++) v[k] *= f;
+                    }
                     if (with_act) to_activation(a, v, m0, n0, b);
                     if (with_res) res.add_to(a, m0 + lane, n0, early, v);
                     if (c + C < cols) ask(n0 + C);

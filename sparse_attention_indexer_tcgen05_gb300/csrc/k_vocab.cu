@@ -8,7 +8,8 @@
 //   loss = sum of both, each with its weight and over the rows that have it
 //   dz_rv = c_r p_rv - sum over the row's targets at v of tau,  dx = alpha dz W,  dW = alpha dz^T x
 //
-// with tau the label's or candidate's weight in the loss and c_r their sum.  The losses need a row's lse and the few scores that
+// with tau the label's or candidate's weight in the loss and c_r their sum.  A weight that all rows share (one over their number) is
+// a factor of the products and not of dz: rounded to bf16 with dz it would be off by up to 2^-9 for all of a gradient alike.  The losses need a row's lse and the few scores that
 // its targets name; the gradient needs p.  Rows go piece by piece: the scores of a piece are made once and reduced where
 // they are made (k_vocab_tc.cu), and what the backward keeps of them is 16 bits a value, exp(z - largest of its group), which
 // the pass below turns into dz in place.  So a piece takes three products, where pieces of the vocabulary would need its scores a second
@@ -228,6 +229,7 @@ struct Rows {
     float2 *info;                // [count]: lse in base-2 units, c; null: no backward
     float *losses;               // [2][all]
     Weights w;
+    float *factor;               // the weight that tau and c leave to the products
     int *done;
     int blocks;                  // of all pieces
     float *loss;
@@ -245,6 +247,9 @@ __global__ void __launch_bounds__(32 * ROWS) vocab_rows_kernel(const Rows a)
     chain_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = threadIdx.x % ROWS, each = threadIdx.x / ROWS;
     const float2 w = weigh(a.w, counted);
+    const float factor = w.x > 0.f ? w.x : w.y > 0.f ? w.y : 1.f;
+    const float2 share = make_float2(w.x > 0.f ? 1.f : 0.f, w.x > 0.f ? w.y / w.x : w.y > 0.f ? 1.f : 0.f);
+    if (blockIdx.x == 0 && threadIdx.x == 0 && a.info != nullptr) *a.factor = factor;
     const long long r0 = (long long)blockIdx.x * ROWS;
     float top = -INFINITY, sum = 0.f;
     const auto join = [&](float2 q) {   // a group without a finite score has the sum 0, or NaN
@@ -290,12 +295,12 @@ __global__ void __launch_bounds__(32 * ROWS) vocab_rows_kernel(const Rows a)
                 float tau = 0.f;
                 if (t[q] == -1.f) {
                     label = lse - z[q];
-                    tau = w.x;
+                    tau = share.x;
                 } else if (t[q] != 0.f) {
                     // a candidate that is no column: NaN; a label: -inf
                     if (t[q] == -INFINITY) label = NAN;
                     else teacher = t[q] == t[q] ? fmaf(t[q], logf(t[q]) + (lse - z[q]), teacher) : NAN;
-                    tau = t[q] == -INFINITY ? NAN : w.y * t[q];
+                    tau = t[q] == -INFINITY ? NAN : share.y * t[q];
                 }
                 c += tau;
                 if (a.info != nullptr && s0 + 32 * q < a.width) a.weight[(s0 + 32 * q) * a.all + r] = tau;
@@ -630,7 +635,7 @@ Layout plan(const csa_vocab_loss_params &p, bool backward)
     take(b.off_weight, (size_t)M * b.width * 4);
     take(b.off_marks, p.slots > 0 ? (size_t)M * b.groups * 4 : 0);
     take(b.off_z, (size_t)M * b.width * 4);
-    take(b.off_counts, (size_t)((M + ROWS - 1) / ROWS) * 8 + 8);   // and the count of finished blocks
+    take(b.off_counts, (size_t)((M + ROWS - 1) / ROWS) * 8 + 8);   // behind the count of finished blocks and the factor
     take(b.off_losses, (size_t)M * 8);
     take(b.off_info, (size_t)b.piece * 8);
     take(b.off_parts, (size_t)b.piece * b.groups * 8);
@@ -718,6 +723,7 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
     g.marks = reinterpret_cast<int *>(w + b.off_marks);
     g.groups = b.groups;
     g.done = reinterpret_cast<int *>(w + b.off_counts);
+    float *factor = reinterpret_cast<float *>(g.done + 1);
     g.counts = reinterpret_cast<int2 *>(w + b.off_counts) + 1;
     const bool single = p.slots == 0;
     const unsigned blocks = (unsigned)(single ? (M + 255) / 256 : (M + ROWS - 1) / ROWS);
@@ -753,7 +759,7 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
         VOC_TRY(launch_scores(px, ow, count, V, K, planes, s, sms, st));
         const int row_blocks = (int)((count + ROWS - 1) / ROWS);
         const Rows rows = {parts, b.groups, g.width, first, count, M, g.weight + first, z + first, info, losses, weights,
-                           g.done, all_blocks, loss};
+                           factor, g.done, all_blocks, loss};
         VOC_TRY(launch_chained(vocab_rows_kernel, dim3((unsigned)row_blocks), 32 * ROWS, 0, 1, st, rows));
         if (!grads) continue;
         Dz d = {};
@@ -779,6 +785,7 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
         q.planes = planes;
         q.passes = 1;
         q.e.partial = reinterpret_cast<float *>(w + b.off_part);
+        q.e.scale = factor;
         Operand od = {};
         od.base = d.dz;
         od.ld = ld;

@@ -295,6 +295,18 @@ def test_teacher_logits_at_their_limits():
     assert float(rows[1, 5]) == 0 and not bool(dx[5].any()) and abs(float(loss) * 6 - float(rows[1].sum())) < 1e-5 * float(rows[1].abs().sum())
 
 
+def test_the_losses_weight_is_not_rounded_with_dz():
+    """A weight halfway between two bf16 values: rounded with dz, whose largest parts it is, every gradient would be off by 2^-8 of
+    itself.  The roundings that are made, of dz and of the result, are random: 2^-8 / sqrt(3) each at most."""
+    M, K, V = 500, 64, 4000
+    t = inputs(M, K, V, scale=0.5)
+    p = B.VocabLossParams(M, K, V, label_weight=1.0039, reduction="sum", labels_64=True)
+    _, dx, dw = B.csa_vocab_loss_bwd(p, t["x"], t["weight"], t["labels"])
+    r = reference(t, wl=p.c.label_weight, mean=False)
+    near(dx, r["dz"] @ t["weight"].double(), 2.0 ** -8.6, "dx")
+    near(dw, r["dz"].t() @ t["x"].double(), 2.0 ** -8.6, "dw")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_large_scores(dtype):
     """Rows whose scores lie hundreds apart: most columns' exponentials vanish."""
