@@ -430,7 +430,8 @@ size_t csa_vocab_loss_bwd_workspace_size(const csa_vocab_loss_params *p);
 /*   x [rows, features], weight [vocab, features] contiguous -> loss_out, one device fp32; row_loss_out [2, rows] fp32 or
  *   NULL: the rows' unweighted label losses, then their teacher losses (0 for a row without).
  * Scores are sums in fp32 (fp32 values as three bf16 parts each); sums leave the tensor core every 512 k (fp32 values: every
- * 64) and are added up rounded. */
+ * 64) and are added up rounded.  The forward of few rows (up to 16, as of csa_linear_fwd) holds their scores in the workspace, and its
+ * loss agrees with the backward's to fp32 rounding, not bit for bit. */
 csa_status csa_vocab_loss_fwd(const csa_vocab_loss_params *p, const void *x, const void *weight,
                               const csa_vocab_targets *targets, float *loss_out, float *row_loss_out, void *workspace,
                               size_t workspace_bytes, void *stream);
@@ -438,8 +439,8 @@ csa_status csa_vocab_loss_fwd(const csa_vocab_loss_params *p, const void *x, con
 /* The same, and the gradients of the loss (not of its parts), dz_rv = c_r softmax(z_r)_v - tau_rv with tau the weights of the
  * row's targets in the loss and c_r their sum:  dx = alpha dz weight [rows, features],  dw = alpha dz^T x [vocab, features].
  * Each of dx and dw may be NULL and is then not computed.  With bf16 values the exponentials are held in fp16 relative to the
- * largest of their 64 columns, and dz is rounded to bf16 before the two products; the columns that targets name come from their fp32
- * scores.  A row whose targets weigh nothing passes no gradient, whatever its scores are.  rows = 0 gives loss = 0 and dw = 0.
+ * largest of their 64 columns, and dz, without the weight that all rows share, is rounded to bf16 before the two products; the
+ * columns that targets name come from their fp32 scores.  A row whose targets weigh nothing passes no gradient, whatever its scores are.  rows = 0 gives loss = 0 and dw = 0.
  * The same call gives the same bits every time (no atomics). */
 csa_status csa_vocab_loss_bwd(const csa_vocab_loss_params *p, const void *x, const void *weight,
                               const csa_vocab_targets *targets, float *loss_out, float *row_loss_out, void *dx, void *dw,
@@ -472,8 +473,9 @@ csa_status csa_selftest_bounded_wait(void *stream);
 int32_t csa_last_timeout_site(void);
 
 /* Name of the last kernel path csa_indexer_fwd, csa_teacher, csa_teacher_from_lse or csa_indexer_bwd chose
- * on this host thread ("tcgen05", "generic", ...; for csa_indexer_bwd, its backward's), or of csa_linear_fwd ("tcgen05",
- * or "generic" for few rows) and csa_linear_bwd.  Static string. */
+ * on this host thread ("tcgen05", "generic", ...; for csa_indexer_bwd, its backward's), or of csa_linear_fwd and
+ * csa_vocab_loss_fwd ("tcgen05", or "generic" for few rows), csa_linear_bwd, csa_vocab_loss_bwd and csa_layernorm_*
+ * ("generic").  Static string. */
 const char *csa_last_path(void);
 
 /* Message of the last CUDA runtime error that ended a call of this library with CSA_ERR_CUDA on this host

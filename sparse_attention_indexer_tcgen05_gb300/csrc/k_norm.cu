@@ -11,6 +11,10 @@
 // Rows of up to 512 values lie in the registers of a part of a warp.  Longer ones pass through a ring of rows in a block's
 // shared memory, filled by asynchronous copies, in steps: while a row's sum is taken, the row before it is a step further,
 // so that no step waits for a sum across the block and a row costs one barrier.
+//
+// Measured (GB/s of the bytes above; a plain copy moves 6795): bf16 65536 x 4096 forward 5500, backward 5900 (272 us), 65536 x 1024 backward
+// 4850; fp32 65536 x 4096 4200 and 4300 (two pieces of 16 bytes for 8 values: bound by shared memory's instructions); 5003 x
+// 1537 fp32 backward 33 us, 16384 x 128 bf16 forward 3.2 and backward 7.6 us, 1 x 4096 forward 2.2 us on the device.
 #include "k_linear.cuh"
 
 #include <type_traits>
@@ -892,7 +896,7 @@ template <typename T> __global__ void __launch_bounds__(256) norm_params_long_ke
     }
     float *out = a.parts + (long long)blockIdx.y * 2 * a.n;
     out[j] = dw;
-    out[a.n + j] = db;
+    out[(long long)a.n + j] = db;
 }
 
 // ------------------------------------------------------------------ host side
@@ -935,7 +939,7 @@ How how(const csa_layernorm_params &p, bool backward)
     if (h.stages > live + 1 + MOST_PENDING) h.stages = live + 1 + MOST_PENDING;
     h.smem = h.groups * h.stages * room;
     blocks(1, linear::kSms);   // a multiple of 8, or a row of a group each
-    // one row a block needs no ring (37 x 4096: 2.2 us, through the ring NNN)
+    // few rows: a block each, no ring to fill (37 x 4096: 2.3 us)
     h.few = !backward && p.rows <= 4 * linear::kSms;
     return h;
 }
