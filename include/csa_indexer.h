@@ -440,7 +440,10 @@ csa_status csa_vocab_loss_fwd(const csa_vocab_loss_params *p, const void *x, con
  * row's targets in the loss and c_r their sum:  dx = alpha dz weight [rows, features],  dw = alpha dz^T x [vocab, features].
  * Each of dx and dw may be NULL and is then not computed.  With bf16 values the exponentials are held in fp16 relative to the
  * largest of their 64 columns, and dz, without the weight that all rows share, is rounded to bf16 before the two products; the
- * columns that targets name come from their fp32 scores.  A row whose targets weigh nothing passes no gradient, whatever its scores are.  rows = 0 gives loss = 0 and dw = 0.
+ * columns that targets name come from their fp32 scores.  A row whose targets weigh nothing passes no gradient, whatever its
+ * scores are; x is still a factor of its zeros in dw and has to be finite.  Rows without a target (prompts, padding) are left out
+ * of the products, and their x out of both, with more than 256 rows (at most 2^18), 512 features and 16384 columns or more.
+ * rows = 0 gives loss = 0 and dw = 0.
  * The same call gives the same bits every time (no atomics). */
 csa_status csa_vocab_loss_bwd(const csa_vocab_loss_params *p, const void *x, const void *weight,
                               const csa_vocab_targets *targets, float *loss_out, float *row_loss_out, void *dx, void *dw,

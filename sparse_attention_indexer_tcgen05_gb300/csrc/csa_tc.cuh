@@ -89,6 +89,9 @@ cudaError_t teacher_h128_read_clear_error(int *flag);
 // The projections' products (k_linear_tc.cu).
 cudaError_t linear_tc_read_clear_error(int *flag);
 
+// Products of rows that the device counts (k_linear_counted.cu).
+cudaError_t linear_counted_read_clear_error(int *flag);
+
 // The vocabulary's scores (k_vocab_tc.cu).
 cudaError_t vocab_tc_read_clear_error(int *flag);
 

@@ -295,7 +295,7 @@ cudaError_t product(const Product &p, cudaStream_t st)
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = launch_product_tc(p, sms > 2 ? sms : 2, st);
+    if (e == cudaSuccess) e = (p.counted != nullptr ? launch_product_counted : launch_product_tc)(p, sms > 2 ? sms : 2, st);
     if (e != cudaSuccess || p.plan.splits == 1) return e;
     // Too few whole sums to fill the GPU: cut them (the backward of 15401 x 48 x 24, dW from 61 pieces: 28.9 -> 17.0 us).
     const long long threads = p.M * (partial_stride(p.N) / 4);

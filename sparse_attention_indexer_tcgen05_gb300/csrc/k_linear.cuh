@@ -158,8 +158,14 @@ struct Product {
     int planes, passes;
     Plan plan;
     Epilogue e;
+    // Rows that the device counts (null: M and K are what they are): *counted - first of them, at most M, or along k at most K, in
+    // whole stages, where what lies behind them is zeros.  Tiles of 256 x 256 (three planes: 128); along k in one piece.
+    const int *counted;
+    long long first;
+    bool along_k;
 };
 cudaError_t launch_product_tc(const Product &p, int sms, cudaStream_t st);
+cudaError_t launch_product_counted(const Product &p, int sms, cudaStream_t st);
 
 // What a staged operand is made of: rows x cols values, rows `stride` apart -> planes of rows `ld` apart.
 struct Stage {

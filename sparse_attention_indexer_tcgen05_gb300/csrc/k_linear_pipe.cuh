@@ -46,7 +46,30 @@ struct Args {
     int many;                   // 16 epilogue warps
     int res32;                  // the residual's rows start on 32-byte sectors
     Epilogue e;
+    // A number of rows (of M, or of k) that is known on the device alone: `counted` rows before `first` are another product's.  With
+    // `along_k` the k axis ends there, with whole stages (what lies behind the last row is zeros); never empty for the first.
+    const int *counted;
+    long long first;
+    int along_k;
 };
+
+// The arguments with the device's count in them; `bm` rows of a tile.
+__device__ __forceinline__ Args counted(const Args &given, int bm)
+{
+    Args a = given;
+    long long n = *a.counted - a.first;
+    if (a.along_k) {
+        const long long most = (long long)a.ksteps * BK;
+        n = n < 0 ? 0 : n > most ? most : n;
+        if (n == 0 && a.first > 0) a.units = a.whole = 0;   // nothing to add
+        a.ksteps = a.per_split = n > 0 ? (int)((n + BK - 1) / BK) : 1;
+    } else {
+        a.M = n < 0 ? 0 : n > a.M ? a.M : n;
+        a.mt = (int)((a.M + bm - 1) / bm);
+        a.units = a.whole = a.mt * a.nt * a.splits;
+    }
+    return a;
+}
 
 struct Unit {
     int m, s, it0, it1;

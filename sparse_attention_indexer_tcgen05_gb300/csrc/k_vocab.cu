@@ -16,9 +16,9 @@
 // three products, where pieces of the vocabulary would need its scores a second time, once the lse is known: four.  dW sums
 // over pieces in fp32.
 //
-// Bound by the three products (2 M K V operations each) at the tensor cores' power limit.  8192 rows of 2048 over 131072 columns: scores
-// 2.35 ms, this file's kernels 0.65 (dz: 4 bytes a score at 7.1 TB/s), dx and dW 2.15 and 2.18; 7.8 ms as one call, 8.2 to 8.8
-// in a loop of calls, where the clock falls.
+// Bound by the three products (2 M K V operations each) at the tensor cores' power limit.  8192 rows of 2048 over 131072 columns, a
+// fifth of them without a target and so left out: scores 2.00 ms, this file's kernels 0.60 (dz: 4 bytes a score at 6.4 TB/s), dx
+// and dW 1.96 and 1.94; 6.6 ms as one call, 7.0 to 7.3 in a loop of calls, where the clock falls.
 #include "k_rows.cuh"
 #include "k_vocab.cuh"
 
@@ -52,7 +52,22 @@ struct Targets {
     int groups;
     int2 *counts;                // [blocks]: rows with a label, rows with a candidate
     int *done;                   // set to 0: blocks of rows_kernel that have finished
+    // Rows that have a target, packed (below); null: every row stays where it is
+    uint32_t *activity;          // bits of rows with a target
+    int *active;                 // rows with a target
+    int *index, *place;          // [rows]: the row that a packed row was; where a row is packed, -1 without a target
+    float *losses;               // [2][rows], set to 0 for rows without a target
+    const void *x;
+    long long x_stride;
+    bf16 *packed;                // [rows + TAIL][ld], planes apart
+    long long ld, plane;
+    int features;
 };
+
+__device__ __forceinline__ long long candidate_of(const Targets &a, long long at)
+{
+    return a.ids_64 ? static_cast<const long long *>(a.ids)[at] : static_cast<const int *>(a.ids)[at];
+}
 
 __device__ __forceinline__ long long label_of(const Targets &a, long long r)
 {
@@ -91,8 +106,40 @@ __global__ void __launch_bounds__(256) vocab_labels_kernel(const Targets a)
     count(a, v >= 0, false);
 }
 
-// A warp a row.  Each target's place is the number of targets before it (smaller column, or the same and earlier).
-__global__ void __launch_bounds__(32 * ROWS) vocab_prepare_kernel(const Targets a)
+// Rows without a label or candidate (prompts, padding) take no part in the three products: of a large vocabulary the others are packed,
+// in their order, and the products' rows are what the device counts.  8192 rows of 2048 over 131072 columns, a fifth of them
+// without a label: 8.3 ms -> 7.0.
+//
+// First a bit for each row, and the counts of 32 rows, a warp a row.  Every block that packs rows then counts the bits before its
+// own: 8192 rows have 256 words of them.  (Summed by one block in a kernel between the two: 4 us more.)
+__global__ void __launch_bounds__(1024) vocab_count_kernel(const Targets a)
+{
+    chain_start();
+    chain_wait();
+    __shared__ int have[32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long r = (long long)blockIdx.x * 32 + warp;
+    int labelled = 0, any = 0;
+    if (r < a.rows) {
+        labelled = label_of(a, r) >= 0;
+#pragma unroll 4
+        for (int s = lane; s < a.slots; s += 32) any |= candidate_of(a, r * a.slots + s) >= 0;
+    }
+    any = __any_sync(0xffffffffu, any);
+    if (lane == 0) have[warp] = labelled | any << 1;
+    __syncthreads();
+    if (warp > 0) return;
+    const uint32_t l = __ballot_sync(0xffffffffu, have[lane] & 1), t = __ballot_sync(0xffffffffu, have[lane] & 2);
+    if (lane > 0) return;
+    a.counts[blockIdx.x] = make_int2(__popc(l), __popc(t));
+    a.activity[blockIdx.x] = l | t;
+}
+
+// A warp a row.  Each target's place is the number of targets before it (smaller column, or the same and earlier).  V: the
+// values' type, where rows are packed; the last TAIL warps then put zeros behind the last packed row, as the k axis of dW takes whole
+// stages of 64.
+constexpr int TAIL = 64;
+template <typename V, bool PACK> __global__ void __launch_bounds__(32 * ROWS) vocab_prepare_kernel(const Targets a)
 {
     extern __shared__ int raw[];
     chain_start();
@@ -102,7 +149,68 @@ __global__ void __launch_bounds__(32 * ROWS) vocab_prepare_kernel(const Targets 
     int *ids = raw + warp * 3 * room, *sorted = ids + room;
     float *logits = reinterpret_cast<float *>(sorted + room);
     bool taught = false;
-    long long label = -1;
+    long long label = -1, row = r;   // where the row's targets go
+    if constexpr (PACK) {
+        // rows before this block's
+        __shared__ int sums[ROWS];
+        const long long base = min((long long)blockIdx.x * ROWS, (a.rows + 31) / 32 * 32);
+        int before = 0;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < (int)(base / 32); i += 32 * ROWS) before += __popc(a.activity[i]);
+        before = __reduce_add_sync(0xffffffffu, before);
+        if (lane == 0) sums[warp] = before;
+        __syncthreads();
+        before = 0;
+#pragma unroll
+        for (int w = 0; w < ROWS; w++) before += sums[w];
+        const long long behind = r - (a.rows + 31) / 32 * 32;
+        if (behind >= 0) {
+            if (behind == 0 && lane == 0) {
+                *a.active = before;
+                *a.done = 0;
+            }
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            for (int q = 0; q < Planes<V>::N; q++) {
+                uint4 *to = reinterpret_cast<uint4 *>(a.packed + q * a.plane + (before + behind) * a.ld);
+                for (long long i = lane; i < a.ld / 8; i += 32) to[i] = zero;
+            }
+            return;
+        }
+        if (r >= a.rows) return;
+        const uint32_t bits = a.activity[r / 32];
+        if ((bits >> (r & 31) & 1) == 0) {
+            if (lane == 0) {
+                a.place[r] = -1;
+                a.losses[r] = a.losses[a.rows + r] = 0.f;
+            }
+            return;
+        }
+        row = before + __popc(bits & ((1u << (r & 31)) - 1));
+        if (lane == 0) {
+            a.place[r] = (int)row;
+            a.index[row] = (int)r;
+        }
+        const V *x = static_cast<const V *>(a.x) + r * a.x_stride, *end = static_cast<const V *>(a.x) + (a.rows - 1) * a.x_stride + a.features;
+        const bool aligned = a.x_stride % (16 / (int)sizeof(V)) == 0;
+        int c = 8 * lane;
+        for (; aligned && c + 3 * 256 + 8 <= a.features; c += 4 * 256) {   // four loads under one latency
+            Raw8<V, true> raw[4];
+#pragma unroll
+            for (int k = 0; k < 4; k++) raw[k].load(x + c + k * 256, 8, end);
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                float v[8];
+                raw[k].floats(8, v);
+                put_planes8<Planes<V>::N>(a.packed, a.plane, row * a.ld + c + k * 256, v);
+            }
+        }
+        for (; c < a.features; c += 256) {
+            float v[8];
+            if (aligned && c + 8 <= a.features) load8<V, true>(x + c, 8, end, v);
+            else load8<V, false>(x + c, min(8, a.features - c), end, v);
+            put_planes8<Planes<V>::N>(a.packed, a.plane, row * a.ld + c, v);
+        }
+    }
     if (r < a.rows) {
         label = label_of(a, r);
         const long long at = r * a.slots;
@@ -161,8 +269,8 @@ __global__ void __launch_bounds__(32 * ROWS) vocab_prepare_kernel(const Targets 
                     float t = label < 0 ? 0.f : label < a.vocab ? -1.f : -INFINITY;
                     if (s < a.slots) t = logits[s] == -INFINITY ? 0.f : expf(logits[s] - log_sum);   // also where no logit is finite
                     sorted[place[q]] = id[q];
-                    a.sorted[place[q] * a.rows + r] = id[q];
-                    a.weight[place[q] * a.rows + r] = t;
+                    a.sorted[place[q] * a.rows + row] = id[q];
+                    a.weight[place[q] * a.rows + row] = t;
                 }
             }
             __syncwarp();
@@ -174,7 +282,7 @@ __global__ void __launch_bounds__(32 * ROWS) vocab_prepare_kernel(const Targets 
         // along the targets, 786 groups of 3001 rows took 20 us)
         int half = 1;
         while (2 * half <= a.width) half *= 2;
-        for (int g0 = 0; g0 < a.groups; g0 += 128) {
+        for (int g0 = 0; g0 < a.groups && a.marks != nullptr; g0 += 128) {
             int at[5] = {};
             for (int step = half; step > 0; step /= 2) {
 #pragma unroll
@@ -187,11 +295,11 @@ __global__ void __launch_bounds__(32 * ROWS) vocab_prepare_kernel(const Targets 
             for (int q = 0; q < 4; q++) {
                 const int g = g0 + 32 * q + lane;
                 const int first_then = __shfl_sync(0xffffffffu, at[q + 1], 0), beside = __shfl_down_sync(0xffffffffu, at[q], 1);
-                if (g < a.groups) a.marks[r * a.groups + g] = at[q] | ((lane < 31 ? beside : first_then) - at[q]) << 16;
+                if (g < a.groups) a.marks[row * a.groups + g] = at[q] | ((lane < 31 ? beside : first_then) - at[q]) << 16;
             }
         }
     }
-    count(a, lane == 0 && label >= 0, lane == 0 && taught);
+    if constexpr (!PACK) count(a, lane == 0 && label >= 0, lane == 0 && taught);
 }
 
 // What a row with a label, or with candidates, weighs in the loss.
@@ -237,6 +345,7 @@ struct Rows {
     float *factor;               // the weight that tau and c leave to the products
     int *done;
     int blocks;                  // of all pieces
+    const int *active, *index;   // packed rows: how many there are, and which they were; null: every row is its own
     float *loss;
 };
 
@@ -255,7 +364,7 @@ __global__ void __launch_bounds__(32 * ROWS) vocab_rows_kernel(const Rows a)
     const float factor = w.x > 0.f ? w.x : w.y > 0.f ? w.y : 1.f;
     const float2 share = make_float2(w.x > 0.f ? 1.f : 0.f, w.x > 0.f ? w.y / w.x : w.y > 0.f ? 1.f : 0.f);
     if (blockIdx.x == 0 && threadIdx.x == 0 && a.info != nullptr) *a.factor = factor;
-    const long long r0 = (long long)blockIdx.x * ROWS;
+    const long long r0 = (long long)blockIdx.x * ROWS, count = a.active != nullptr ? min(a.count, *a.active - a.first) : a.count;
     float top = -INFINITY, sum = 0.f;
     const auto join = [&](float2 q) {   // a group without a finite score has the sum 0, or NaN
         if (q.x > top) {
@@ -265,7 +374,7 @@ __global__ void __launch_bounds__(32 * ROWS) vocab_rows_kernel(const Rows a)
             sum += q.x == -INFINITY ? q.y : q.y * ex2(q.x - top);
         }
     };
-    if (r0 + row < a.count) {
+    if (r0 + row < count) {
         const float2 *p = a.parts + r0 + row;
         int g = each;
         for (; g + 7 * 32 < a.groups; g += 8 * 32) {
@@ -281,7 +390,7 @@ __global__ void __launch_bounds__(32 * ROWS) vocab_rows_kernel(const Rows a)
     __syncthreads();
     const long long r = r0 + warp;
     float label = 0.f, teacher = 0.f;
-    if (r < a.count) {
+    if (r < count) {
         const float2 q = part[lane][warp];
         top = warp_max(q.x);
         sum = warp_sum(q.x == -INFINITY ? q.y : q.y * ex2(q.x - top));
@@ -315,8 +424,9 @@ __global__ void __launch_bounds__(32 * ROWS) vocab_rows_kernel(const Rows a)
         teacher = warp_sum(teacher);
         c = warp_sum(c);
         if (lane == 0) {
-            a.losses[a.first + r] = label;
-            a.losses[a.all + a.first + r] = teacher;
+            const long long was = a.index != nullptr ? a.index[a.first + r] : a.first + r;
+            a.losses[was] = label;
+            a.losses[a.all + was] = teacher;
             if (a.info != nullptr) a.info[r] = make_float2(lse2, c);
             __threadfence();
         }
@@ -363,11 +473,6 @@ struct Few {
     int mean;
     float *losses, *loss;        // loss: of one row; null: there are more
 };
-
-__device__ __forceinline__ long long candidate_of(const Targets &a, long long at)
-{
-    return a.ids_64 ? static_cast<const long long *>(a.ids)[at] : static_cast<const int *>(a.ids)[at];
-}
 
 constexpr int FEW = 1024;        // threads of a row
 template <typename F> __device__ __forceinline__ float block_join(float x, float *part, const F &join)
@@ -479,6 +584,8 @@ struct Dz {
     const float *tau, *z;
     int width;
     int cols;                    // columns of a block, a multiple of 2048
+    const int *active;           // packed rows: how many there are of all pieces; null: `count`
+    long long first;
 };
 
 // dz = c exp(z - lse) - tau of one row's columns, 8 a thread at a time; then the columns that targets name, from their own
@@ -489,7 +596,15 @@ template <typename V> __global__ void __launch_bounds__(256) vocab_dz_kernel(con
     chain_start();
     chain_wait();
     const long long r = blockIdx.x, c0 = (long long)blockIdx.y * a.cols, c1 = min(a.vocab, c0 + a.cols);
-    const float2 info = a.info[r];
+    float2 info = make_float2(0.f, 0.f);
+    if (a.active != nullptr) {
+        // zeros behind the last row, as many as dW's last stage along k takes
+        const long long n = min(a.count, max(0LL, *a.active - a.first));
+        if (r >= n && r >= (max(n, a.first == 0 ? 1LL : 0LL) + 63) / 64 * 64) return;
+        if (r < n) info = a.info[r];
+    } else {
+        info = a.info[r];
+    }
     for (long long v = c0 + 8 * threadIdx.x; v < c1; v += 8 * 256) {
         const long long at = r * a.ld + v;
         float x[8];
@@ -534,6 +649,17 @@ template <typename V> __global__ void __launch_bounds__(256) vocab_dz_kernel(con
     }
 }
 
+// dx of packed rows back in their places, zeros for the others.  W: a vector of a row's bytes, or 2 of them.
+template <typename W> __global__ void __launch_bounds__(256) vocab_unpack_kernel(const W *packed, const int *place, long long rows, int words, W *dx)
+{
+    chain_start();
+    chain_wait();
+    const long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (r >= rows) return;
+    const int from = place[r];
+    for (int i = threadIdx.x & 31; i < words; i += 32) dx[r * words + i] = from >= 0 ? packed[(long long)from * words + i] : W();
+}
+
 // The sums of dW over pieces, rounded.
 __global__ void __launch_bounds__(256) vocab_round_kernel(const float *sum, long long n, bf16 *out)
 {
@@ -562,12 +688,13 @@ constexpr long long kKept = 4LL << 30;
 // over 50257 columns has 48 tiles for 76 pairs, in three pieces 144 (220 us -> 170).  Times as in plan_product.
 Plan cut_further(Plan p, long long M, long long N, long long K)
 {
-    if (p.shape != PAIR_256) return p;
-    const double tiles = (double)((M + 255) / 256) * ((N + 255) / 256), slots = kSms / 2;
+    if (p.shape == LONE_64) return p;
+    const int bn = p.shape == PAIR_256 ? 256 : 128;
+    const double tiles = (double)((M + 255) / 256) * ((N + bn - 1) / bn), slots = kSms / 2, step = p.shape == PAIR_256 ? 0.28 : p.exact ? 0.90 : 0.20;
     const long long steps = (K + 63) / 64;
     const auto time = [&](long long cut) {
         const long long per = (steps + cut - 1) / cut;
-        return ceil(tiles * cut / slots) * per * 0.28 + (cut > 1 ? 2.5 + (double)M * N * 8 * cut / 4e6 : 0.0);
+        return ceil(tiles * cut / slots) * per * step + (cut > 1 ? 2.5 + (double)M * N * 8 * cut / 4e6 : 0.0);
     };
     long long best = p.splits;
     for (long long cut = p.splits; cut <= 16 && cut * 16 <= steps; cut++)
@@ -597,12 +724,24 @@ inline bool few_rows(const csa_vocab_loss_params &p) { return small_linear(produ
 // by 1024: 200 us in copies of 64 columns, 170 in one).
 inline long long ld_of(long long vocab) { return (vocab + 63) & ~63LL; }
 
+// Rows without a target are left out of the products where that costs little beside them: packing x and unpacking dx move 8 M K
+// bytes, 350 / V of the products' time (2 % at 16384 columns), and the products' kernels for counted rows have the largest tiles.
+// Counting costs 6 us a call (1000 rows of 2048 over 65536 columns, all with candidates: 192 us -> 198), and its bits, which every
+// block reads, 0.1 ms of 2^18 rows.
+inline bool packs(const csa_vocab_loss_params &p)
+{
+    return p.rows > 256 && p.rows <= 1 << 18 && p.vocab >= 16384 && p.features >= 512;
+}
+
 struct Layout {
+    bool packed;
     bool stage_x, stage_w;
     long long piece;     // rows of a piece
     int pieces, width, groups;
     linear::Plan dx, dw;
-    size_t off_x, off_w, off_sorted, off_weight, off_marks, off_z, off_counts, off_losses, off_info, off_parts, off_e, off_dz, off_sum, off_part, total;
+    long long e_rows;   // of the scores that are kept
+    size_t off_x, off_w, off_sorted, off_weight, off_marks, off_z, off_counts, off_activity, off_index, off_place, off_losses, off_info, off_parts, off_e,
+        off_dz, off_dx, off_sum, off_part, total;
 };
 Layout plan(const csa_vocab_loss_params &p, bool backward)
 {
@@ -626,6 +765,8 @@ Layout plan(const csa_vocab_loss_params &p, bool backward)
     const long long row = backward ? ld * (p.dtype == CSA_F32 ? 10 : 2) : (long long)b.groups * 8;
     long long most = p.piece_rows > 0 ? p.piece_rows : kKept / row / 256 * 256;
     if (most < 256 && p.piece_rows <= 0) most = 256;
+    b.packed = packs(p);
+    if (b.packed && most > 65536) most = 65536;   // dW's k axis in one piece
     b.piece = M < most ? M : most;
     b.pieces = (int)((M + b.piece - 1) / b.piece);
     if (p.piece_rows <= 0 && b.pieces > 1) {  // of one size, whole tiles
@@ -634,23 +775,35 @@ Layout plan(const csa_vocab_loss_params &p, bool backward)
     }
     b.stage_x = staged(p.dtype, p.x_stride);
     b.stage_w = staged(p.dtype, K);
-    take(b.off_x, b.stage_x ? staged_bytes(p.dtype, M, K) : 0);
+    b.e_rows = b.packed ? (b.piece + 63) / 64 * 64 : b.piece;
+    take(b.off_x, b.packed ? staged_bytes(p.dtype, M + TAIL, K) : b.stage_x ? staged_bytes(p.dtype, M, K) : 0);
     take(b.off_w, b.stage_w ? staged_bytes(p.dtype, V, K) : 0);
     take(b.off_sorted, (size_t)M * b.width * 4);
     take(b.off_weight, (size_t)M * b.width * 4);
     take(b.off_marks, p.slots > 0 ? (size_t)M * b.groups * 4 : 0);
     take(b.off_z, (size_t)M * b.width * 4);
-    take(b.off_counts, (size_t)((M + ROWS - 1) / ROWS) * 8 + 8);   // behind the count of finished blocks and the factor
+    take(b.off_counts, (size_t)((M + ROWS - 1) / ROWS) * 8 + 16);   // behind the count of finished blocks, the factor and the count of packed rows
+    if (b.packed) {
+        take(b.off_activity, (size_t)((M + 31) / 32) * 4);
+        take(b.off_index, (size_t)M * 4);
+        take(b.off_place, (size_t)M * 4);
+    }
     take(b.off_losses, (size_t)M * 8);
     take(b.off_info, (size_t)b.piece * 8);
     take(b.off_parts, (size_t)b.piece * b.groups * 8);
     if (backward) {
-        take(b.off_e, (size_t)b.piece * ld * (p.dtype == CSA_F32 ? 4 : 2));
+        take(b.off_e, (size_t)b.e_rows * ld * (p.dtype == CSA_F32 ? 4 : 2));
         b.off_dz = b.off_e;
-        if (p.dtype == CSA_F32) take(b.off_dz, (size_t)b.piece * ld * 6);
+        if (p.dtype == CSA_F32) take(b.off_dz, (size_t)b.e_rows * ld * 6);
+        if (b.packed) take(b.off_dx, (size_t)M * K * (p.dtype == CSA_F32 ? 4 : 2));
         take(b.off_sum, b.pieces > 1 && p.dtype == CSA_BF16 ? (size_t)V * K * 4 : 0);
         b.dx = cut_further(plan_product(b.piece, K, V, planes_of(p), 1, p.dtype == CSA_F32, kSms), b.piece, K, V);
         b.dw = cut_further(plan_product(V, K, b.piece, planes_of(p), 1, p.dtype == CSA_F32, kSms), V, K, b.piece);
+        if (b.packed) {
+            const Shape shape = p.dtype == CSA_F32 ? PAIR_128 : PAIR_256;
+            b.dx = cut_further({shape, p.dtype == CSA_F32 ? 1 : (int)((V + 65535) / 65536), p.dtype == CSA_F32}, b.piece, K, V);
+            b.dw = {shape, 1, p.dtype == CSA_F32};
+        }
         const size_t dx = b.dx.splits > 1 ? (size_t)b.dx.splits * b.piece * partial_stride(K) * 4 : 0;
         const size_t dw = b.dw.splits > 1 ? (size_t)b.dw.splits * V * partial_stride(K) * 4 : 0;
         take(b.off_part, dx > dw ? dx : dw);
@@ -718,7 +871,15 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
     int sms = 0;
     VOC_TRY(sms_here(&sms));
     Stage job[2] = {};
-    Operand ox = operand(p.dtype, x, p.x_stride, M, (int)K, b.stage_x, w + b.off_x, true, &job[0]);
+    Operand ox = {};
+    if (b.packed) {   // by the kernel that prepares the targets
+        ox.base = reinterpret_cast<bf16 *>(w + b.off_x);
+        ox.ld = up8(K);
+        ox.plane = (M + TAIL) * ox.ld;
+        ox.k_major = true;
+    } else {
+        ox = operand(p.dtype, x, p.x_stride, M, (int)K, b.stage_x, w + b.off_x, true, &job[0]);
+    }
     Operand ow = operand(p.dtype, weight, K, V, (int)K, b.stage_w, w + b.off_w, true, &job[1]);
     VOC_TRY(run_stages(p.dtype, job, st));
 
@@ -730,14 +891,37 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
     g.done = reinterpret_cast<int *>(w + b.off_counts);
     float *factor = reinterpret_cast<float *>(g.done + 1);
     g.counts = reinterpret_cast<int2 *>(w + b.off_counts) + 1;
+    g.losses = losses;
     const bool single = p.slots == 0;
-    const unsigned blocks = (unsigned)(single ? (M + 255) / 256 : (M + ROWS - 1) / ROWS);
-    if (single) {
+    if (single) g.marks = nullptr;
+    unsigned blocks = (unsigned)((M + ROWS - 1) / ROWS);
+    const size_t smem = (size_t)((g.width + 3) & ~3) * ROWS * 12;
+    const auto prepare = [&](void (*kernel)(Targets)) {
+        const cudaError_t e = smem > 48 << 10 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) : cudaSuccess;
+        return e != cudaSuccess ? e : launch_chained(kernel, dim3(blocks), 32 * ROWS, smem, 1, st, g);
+    };
+    if (b.packed) {
+        g.active = g.done + 2;
+        g.counts++;   // behind it
+        g.activity = reinterpret_cast<uint32_t *>(w + b.off_activity);
+        g.index = reinterpret_cast<int *>(w + b.off_index);
+        g.place = reinterpret_cast<int *>(w + b.off_place);
+        g.x = x;
+        g.x_stride = p.x_stride;
+        g.packed = const_cast<bf16 *>(ox.base);
+        g.ld = ox.ld;
+        g.plane = ox.plane;
+        g.features = (int)K;
+        const unsigned words = (unsigned)((M + 31) / 32);
+        VOC_TRY(launch_chained(vocab_count_kernel, dim3(words), 1024, 0, 1, st, g));
+        blocks = (words * 32 + TAIL) / ROWS;
+        VOC_TRY(prepare(p.dtype == CSA_F32 ? vocab_prepare_kernel<float, true> : vocab_prepare_kernel<bf16, true>));
+        blocks = words;   // of the counts
+    } else if (single) {
+        blocks = (unsigned)((M + 255) / 256);
         VOC_TRY(launch_chained(vocab_labels_kernel, dim3(blocks), 256, 0, 1, st, g));
     } else {
-        const size_t smem = (size_t)((g.width + 3) & ~3) * ROWS * 12;
-        if (smem > 48 << 10) VOC_TRY(cudaFuncSetAttribute(vocab_prepare_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-        VOC_TRY(launch_chained(vocab_prepare_kernel, dim3(blocks), 32 * ROWS, smem, 1, st, g));
+        VOC_TRY(prepare(vocab_prepare_kernel<bf16, false>));
     }
 
     const bool grads = dx != nullptr || dw != nullptr;
@@ -761,17 +945,21 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
         s.alpha = p.alpha;
         s.e = grads ? w + b.off_e : nullptr;
         s.lde = ld;
+        s.counted = g.active;
+        s.first = first;
         VOC_TRY(launch_scores(px, ow, count, V, K, planes, s, sms, st));
         const int row_blocks = (int)((count + ROWS - 1) / ROWS);
         const Rows rows = {parts, b.groups, g.width, first, count, M, g.weight + first, z + first, info, losses, weights,
-                           factor, g.done, all_blocks, loss};
+                           factor, g.done, all_blocks, g.active, g.index, loss};
         VOC_TRY(launch_chained(vocab_rows_kernel, dim3((unsigned)row_blocks), 32 * ROWS, 0, 1, st, rows));
         if (!grads) continue;
         Dz d = {};
         d.e = w + b.off_e;
         d.dz = reinterpret_cast<bf16 *>(w + b.off_dz);
         d.ld = ld;
-        d.plane = b.piece * ld;
+        d.plane = b.e_rows * ld;
+        d.active = g.active;
+        d.first = first;
         d.vocab = V;
         d.parts = parts;
         d.info = info;
@@ -784,13 +972,16 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
         // few rows: several blocks each
         const long long chunks = (V + 2047) / 2048, per_row = (4LL * kSms + count - 1) / count;
         d.cols = (int)((chunks + per_row - 1) / per_row) * 2048;
-        const dim3 grid((unsigned)count, (unsigned)((V + d.cols - 1) / d.cols));
+        const long long whole = (count + 63) / 64 * 64;   // stages of dW's k axis
+        const dim3 grid((unsigned)(b.packed ? whole : count), (unsigned)((V + d.cols - 1) / d.cols));
         VOC_TRY(launch_chained(p.dtype == CSA_F32 ? vocab_dz_kernel<float> : vocab_dz_kernel<bf16>, grid, 256, 0, 1, st, d));
         Product q = {};
         q.planes = planes;
         q.passes = 1;
         q.e.partial = reinterpret_cast<float *>(w + b.off_part);
         q.e.scale = factor;
+        q.counted = g.active;
+        q.first = first;
         Operand od = {};
         od.base = d.dz;
         od.ld = ld;
@@ -806,7 +997,8 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
             q.plan = b.dx;
             q.e.alpha = p.alpha;
             q.e.out_f32 = p.dtype == CSA_F32;
-            q.e.out = static_cast<char *>(dx) + (size_t)first * K * size;
+            q.along_k = false;
+            q.e.out = (b.packed ? w + b.off_dx : static_cast<char *>(dx)) + (size_t)first * K * size;
             VOC_TRY(product(q, st));
         }
         if (dw != nullptr) {
@@ -817,7 +1009,8 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
             q.b.k_major = false;
             q.M = V;
             q.N = K;
-            q.K = count;
+            q.K = b.packed ? whole : count;
+            q.along_k = true;
             q.plan = b.dw;
             // the last piece's k axis may be shorter: no part of it is empty
             const long long steps = (count + 63) / 64, each = (steps + b.dw.splits - 1) / b.dw.splits;
@@ -831,6 +1024,13 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
             }
             VOC_TRY(product(q, st));
         }
+    }
+    if (b.packed && dx != nullptr) {
+        const char *from = w + b.off_dx;
+        const long long bytes = K * (long long)size;
+        const dim3 grid((unsigned)((M + 7) / 8));
+        if (bytes % 16 == 0) VOC_TRY(launch_chained(vocab_unpack_kernel<uint4>, grid, 256, 0, 1, st, (const uint4 *)from, g.place, M, (int)(bytes / 16), (uint4 *)dx));
+        else VOC_TRY(launch_chained(vocab_unpack_kernel<unsigned short>, grid, 256, 0, 1, st, (const unsigned short *)from, g.place, M, (int)(bytes / 2), (unsigned short *)dx));
     }
     if (dw != nullptr && b.pieces > 1 && p.dtype == CSA_BF16) {
         const long long n = V * K;

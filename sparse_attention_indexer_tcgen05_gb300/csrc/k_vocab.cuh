@@ -17,10 +17,12 @@ struct Scores {
     float *z;              // [slots][ld]: the scores there
     int slots, groups;
     long long ld;
-    float2 *parts;         // [groups][M]: a group's largest score in base-2 units, and the sum of 2^(score - largest)
+    float2 *parts;         // [groups][M given]: a group's largest score in base-2 units, and the sum of 2^(score - largest)
     float alpha;
     void *e;               // [M][lde] 2^(score - largest): fp16 of bf16 values, fp32 of fp32 ones; null: not kept
     long long lde;
+    const int *counted;    // the device's count of rows, of which those before `first` are other pieces'; null: M rows
+    long long first;
 };
 
 // z = alpha x W^T of M rows and N columns, of operands contiguous along k.

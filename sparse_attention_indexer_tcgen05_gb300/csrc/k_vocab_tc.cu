@@ -82,10 +82,11 @@ __device__ __forceinline__ float pick(const float (&v)[GROUP], int col)
     return col & 32 ? r[1] : r[0];
 }
 
-template <int CG, int BN, int P, int EW>
+// DYNAMIC: the device counts the rows.
+template <int CG, int BN, int P, int EW, bool DYNAMIC>
 __global__ void __launch_bounds__(64 + 32 * EW, 1)
 vocab_scores_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
-                    const __grid_constant__ CUtensorMap map_e, const Args a, const Scores s)
+                    const __grid_constant__ CUtensorMap map_e, const Args args, const Scores s)
 {
     using Z = Cfg<CG, BN, P, EW>;
     constexpr int CHUNK = P == 3 ? 1 : CHUNK_SUMS;
@@ -97,6 +98,12 @@ vocab_scores_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     chain_start();
     const uint32_t tmem = p.begin();
     chain_wait();
+    __shared__ Args here[1];
+    if constexpr (DYNAMIC) {
+        if (threadIdx.x == 0) here[0] = counted(args, CG * BM);
+        __syncthreads();
+    }
+    const Args &a = DYNAMIC ? static_cast<const Args &>(here[0]) : args;
 
     if (warp == 0) {
         p.template produce<true, true, false>(map_x, map_w, map_w, a);
@@ -192,7 +199,7 @@ vocab_scores_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
                 sum = add2(sum, make_float2(v[k], v[k + 1]));
                 more = add2(more, make_float2(v[k + 2], v[k + 3]));
             }
-            if (row < M) s.parts[col0 / GROUP * a.M + row] = make_float2(top, (sum.x + more.x) + (sum.y + more.y));
+            if (row < M) s.parts[col0 / GROUP * args.M + row] = make_float2(top, (sum.x + more.x) + (sum.y + more.y));
             if (s.e == nullptr) continue;
             if constexpr (P == 1) {
                 if (lane == 0) bulk_wait_read();   // the last group has left the buffer
@@ -230,15 +237,20 @@ vocab_scores_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
 
 // ------------------------------------------------------------------ host side
 
-template <int CG, int BN, int P, int EW>
-static cudaError_t launch(const Maps &m, const Args &a, const Scores &s, int sms, cudaStream_t st)
+template <int CG, int BN, int P, int EW, bool DYNAMIC>
+static cudaError_t launch_one(const Maps &m, const Args &a, const Scores &s, int sms, cudaStream_t st)
 {
     using Z = Cfg<CG, BN, P, EW>;
-    auto *kernel = vocab_scores_kernel<CG, BN, P, EW>;
+    auto *kernel = vocab_scores_kernel<CG, BN, P, EW, DYNAMIC>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::SMEM);
     if (e != cudaSuccess) return e;
     const int slots = sms / CG;
     return launch_chained(kernel, dim3((unsigned)((a.units < slots ? a.units : slots) * CG)), Z::THREADS, Z::SMEM, CG, st, m.a, m.b, m.out, a, s);
+}
+
+template <int CG, int BN, int P, int EW> static cudaError_t launch(const Maps &m, const Args &a, const Scores &s, int sms, cudaStream_t st)
+{
+    return a.counted != nullptr ? launch_one<CG, BN, P, EW, true>(m, a, s, sms, st) : launch_one<CG, BN, P, EW, false>(m, a, s, sms, st);
 }
 
 // The tile by estimated time: the projections' model of a stage, a round no shorter than its epilogue.
@@ -275,6 +287,8 @@ cudaError_t launch_scores(const Operand &x, const Operand &w, long long M, long 
     if (units > 0x3fffffffLL || (long long)BAND * a.nt > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
     a.units = a.whole = (int)units;
     a.rows_a = M >= BM ? BM : (int)((M + 7) & ~7LL);
+    a.counted = s.counted;
+    a.first = s.first;
     Maps m = {};
     bool ok = encode(&m.a, x, M, K, planes, a.rows_a, false) && encode(&m.b, w, N, K, planes, shape == PAIR_256 ? 128 : 64, false);
     if (s.e != nullptr) ok = ok && encode_out(&m.out, planes == 3, s.e, N, s.lde, M, 1);

@@ -295,6 +295,82 @@ def test_teacher_logits_at_their_limits():
     assert float(rows[1, 5]) == 0 and not bool(dx[5].any()) and abs(float(loss) * 6 - float(rows[1].sum())) < 1e-5 * float(rows[1].abs().sum())
 
 
+# ------------------------------------------------------------------ rows without a target, packed away
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,K,V,slots,piece", [(700, 512, 16384, 0, 0), (700, 520, 16411, 5, 0), (513, 515, 16384, 3, 0), (1000, 512, 20001, 0, 300),
+                                               (260, 1024, 16400, 70, 100)])
+def test_packed_rows(M, K, V, slots, piece, dtype):
+    t = inputs(M, K, V, dtype, slots=slots, seed=M + V)
+    if slots:
+        t["teacher_ids"][torch.rand(M, device="cuda") < 0.5] = -1
+    p = B.VocabLossParams(M, K, V, dtype, slots=slots, labels_64=True, ids_64=True, piece_rows=piece)
+    _, dx, dw, r = check(t, p)
+    gone = (r["c"] == 0)[:, 0]
+    assert bool(gone.any()) and not bool(dx[gone].any())
+    B.csa_check_device_status()
+
+
+@pytest.mark.parametrize("held", ["none", "one", "first", "last", "all", 64, 256, 257, 384])
+@pytest.mark.parametrize("piece", [0, 128])
+def test_how_many_rows_are_packed(held, piece):
+    """No row, one, a block at either end, all, and numbers at the edges of tiles and of dW's stages."""
+    M, K, V = 600, 512, 16384
+    t = inputs(M, K, V, seed=1)
+    full = t["labels"].clamp(min=0)
+    keep = torch.zeros(M, dtype=torch.bool, device="cuda")
+    if held == "one":
+        keep[431] = True
+    elif held == "first":
+        keep[:300] = True
+    elif held == "last":
+        keep[-5:] = True
+    elif held == "all":
+        keep[:] = True
+    elif held != "none":
+        keep[torch.randperm(M, device="cuda")[:held]] = True
+    t["labels"] = torch.where(keep, full, -100)
+    check(t, B.VocabLossParams(M, K, V, labels_64=True, piece_rows=piece))
+    B.csa_check_device_status()
+
+
+def test_rows_that_are_packed_away_are_not_read():
+    M, K, V = 600, 512, 16384
+    t = inputs(M, K, V, seed=2)
+    p = B.VocabLossParams(M, K, V, labels_64=True)
+    want = B.csa_vocab_loss_bwd(p, t["x"], t["weight"], t["labels"])
+    t["x"][t["labels"] < 0] = float("nan")
+    got = B.csa_vocab_loss_bwd(p, t["x"], t["weight"], t["labels"])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_packed_rows_captured_with_other_targets():
+    """The number of packed rows is the device's: a replayed call takes that of the targets it finds."""
+    M, K, V = 700, 512, 16384
+    t = inputs(M, K, V, slots=4)
+    p = B.VocabLossParams(M, K, V, slots=4, labels_64=True, ids_64=True, piece_rows=256)
+    names = ("labels", "teacher_ids", "teacher_logits")
+    ws = torch.empty(p.bwd_workspace_bytes, dtype=torch.uint8, device="cuda")
+    out = tuple(torch.empty_like(o) for o in B.csa_vocab_loss_bwd(p, t["x"], t["weight"], **{k: t[k] for k in names}))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        B.csa_vocab_loss_bwd(p, t["x"], t["weight"], **{k: t[k] for k in names}, workspace=ws, out=out)
+    for share in (0.1, 0.9, 0.0, 1.0):
+        other = inputs(M, K, V, slots=4, seed=int(share * 10) + 3)
+        gone = torch.rand(M, device="cuda") >= share
+        other["labels"][gone], other["teacher_ids"][gone] = -1, -1
+        for k in ("x", "weight", *names):
+            t[k].copy_(other[k])
+        ws.fill_(255)
+        graph.replay()
+        want = B.csa_vocab_loss_bwd(p, t["x"], t["weight"], **{k: t[k] for k in names})
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), share
+        if share:
+            check(t, p)
+
+
 def test_the_losses_weight_is_not_rounded_with_dz():
     """A weight halfway between two bf16 values: rounded with dz, whose largest parts it is, every gradient would be off by 2^-8 of
     itself.  The roundings that are made, of dz and of the result, are random: 2^-8 / sqrt(3) each at most."""
