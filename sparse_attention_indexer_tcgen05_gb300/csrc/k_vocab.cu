@@ -685,17 +685,21 @@ inline int planes_of(const csa_vocab_loss_params &p) { return p.dtype == CSA_F32
 constexpr long long kKept = 4LL << 30;
 
 // A gradient's product with its k axis cut for more than one round of tiles too, where that fills the last one: dx of 3001 x 1024
-// over 50257 columns has 48 tiles for 76 pairs, in three pieces 144 (220 us -> 170).  Times as in plan_product.
-Plan cut_further(Plan p, long long M, long long N, long long K)
+// over 50257 columns has 48 tiles for 76 pairs, in three pieces 144 (220 us -> 170).  Times as in plan_product.  Of rows that the
+// device counts, a third of the weight goes to a count of three quarters of them (fp32 dx of 517 x 768 over 50257 columns, 414 rows
+// with a label: 224 us in 4 pieces, which fill the pairs with 517 rows, 162 in 12).
+Plan cut_further(Plan p, long long M, long long N, long long K, bool counted)
 {
     if (p.shape == LONE_64) return p;
     const int bn = p.shape == PAIR_256 ? 256 : 128;
-    const double tiles = (double)((M + 255) / 256) * ((N + bn - 1) / bn), slots = kSms / 2, step = p.shape == PAIR_256 ? 0.28 : p.exact ? 0.90 : 0.20;
+    const double slots = kSms / 2, step = p.shape == PAIR_256 ? 0.28 : p.exact ? 0.90 : 0.20;
     const long long steps = (K + 63) / 64;
-    const auto time = [&](long long cut) {
+    const auto of_rows = [&](long long m, long long cut) {
+        const double tiles = (double)((m + 255) / 256) * ((N + bn - 1) / bn);
         const long long per = (steps + cut - 1) / cut;
         return ceil(tiles * cut / slots) * per * step + (cut > 1 ? 2.5 + (double)M * N * 8 * cut / 4e6 : 0.0);
     };
+    const auto time = [&](long long cut) { return counted ? (2 * of_rows(M, cut) + of_rows(M - M / 4, cut)) / 3 : of_rows(M, cut); };
     long long best = p.splits;
     for (long long cut = p.splits; cut <= 16 && cut * 16 <= steps; cut++)
         if (time(cut) < 0.97 * time(best)) best = cut;
@@ -797,11 +801,11 @@ Layout plan(const csa_vocab_loss_params &p, bool backward)
         if (p.dtype == CSA_F32) take(b.off_dz, (size_t)b.e_rows * ld * 6);
         if (b.packed) take(b.off_dx, (size_t)M * K * (p.dtype == CSA_F32 ? 4 : 2));
         take(b.off_sum, b.pieces > 1 && p.dtype == CSA_BF16 ? (size_t)V * K * 4 : 0);
-        b.dx = cut_further(plan_product(b.piece, K, V, planes_of(p), 1, p.dtype == CSA_F32, kSms), b.piece, K, V);
-        b.dw = cut_further(plan_product(V, K, b.piece, planes_of(p), 1, p.dtype == CSA_F32, kSms), V, K, b.piece);
+        b.dx = cut_further(plan_product(b.piece, K, V, planes_of(p), 1, p.dtype == CSA_F32, kSms), b.piece, K, V, false);
+        b.dw = cut_further(plan_product(V, K, b.piece, planes_of(p), 1, p.dtype == CSA_F32, kSms), V, K, b.piece, false);
         if (b.packed) {
             const Shape shape = p.dtype == CSA_F32 ? PAIR_128 : PAIR_256;
-            b.dx = cut_further({shape, p.dtype == CSA_F32 ? 1 : (int)((V + 65535) / 65536), p.dtype == CSA_F32}, b.piece, K, V);
+            b.dx = cut_further({shape, p.dtype == CSA_F32 ? 1 : (int)((V + 65535) / 65536), p.dtype == CSA_F32}, b.piece, K, V, true);
             b.dw = {shape, 1, p.dtype == CSA_F32};
         }
         const size_t dx = b.dx.splits > 1 ? (size_t)b.dx.splits * b.piece * partial_stride(K) * 4 : 0;
