@@ -308,13 +308,13 @@ struct Weights {
     int blocks, mean;
     float label, teacher;
 };
-// By a block of 32 ROWS threads: x the label's, y the teacher's.
-__device__ __forceinline__ float2 weigh(const Weights &w, int2 *part)
+// By a block of T threads: x the label's, y the teacher's.
+template <int T> __device__ __forceinline__ float2 weigh(const Weights &w, int2 *part)
 {
     if (!w.mean) return make_float2(w.label, w.teacher);
     int2 n = make_int2(0, 0);
 #pragma unroll 4
-    for (int b = threadIdx.x; b < w.blocks; b += 32 * ROWS) {
+    for (int b = threadIdx.x; b < w.blocks; b += T) {
         const int2 c = w.counts[b];
         n.x += c.x;
         n.y += c.y;
@@ -325,7 +325,7 @@ __device__ __forceinline__ float2 weigh(const Weights &w, int2 *part)
     __syncthreads();
     n = make_int2(0, 0);
 #pragma unroll
-    for (int i = 0; i < ROWS; i++) {
+    for (int i = 0; i < T / 32; i++) {
         n.x += part[i].x;
         n.y += part[i].y;
     }
@@ -349,18 +349,19 @@ struct Rows {
     float *loss;
 };
 
-// A block joins the groups of its rows, 32 threads a row, then a warp takes a row's targets.  The block that finishes last
+// A block of T threads joins the groups of its ROWS rows, then a warp takes a row's targets.  The block that finishes last
 // adds up the rows' losses, in the same order whichever block it is and however the rows were cut.
-__global__ void __launch_bounds__(32 * ROWS) vocab_rows_kernel(const Rows a)
+template <int T> __global__ void __launch_bounds__(T) vocab_rows_kernel(const Rows a)
 {
-    __shared__ float2 part[32][ROWS + 1];
-    __shared__ int2 counted[ROWS];
-    __shared__ float2 lost[ROWS];
+    constexpr int E = T / ROWS;   // threads that share a row's groups
+    __shared__ float2 part[E][ROWS + 1];
+    __shared__ int2 counted[T / 32];
+    __shared__ float2 lost[T / 32];
     __shared__ int last;
     chain_start();
     chain_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = threadIdx.x % ROWS, each = threadIdx.x / ROWS;
-    const float2 w = weigh(a.w, counted);
+    const float2 w = weigh<T>(a.w, counted);
     const float factor = w.x > 0.f ? w.x : w.y > 0.f ? w.y : 1.f;
     const float2 share = make_float2(w.x > 0.f ? 1.f : 0.f, w.x > 0.f ? w.y / w.x : w.y > 0.f ? 1.f : 0.f);
     if (blockIdx.x == 0 && threadIdx.x == 0 && a.info != nullptr) *a.factor = factor;
@@ -376,24 +377,26 @@ __global__ void __launch_bounds__(32 * ROWS) vocab_rows_kernel(const Rows a)
     };
     if (r0 + row < count) {
         const float2 *p = a.parts + r0 + row;
-        int g = each;
-        for (; g + 7 * 32 < a.groups; g += 8 * 32) {
+        for (int g = each; g < a.groups; g += 8 * E) {
             float2 q[8];
 #pragma unroll
-            for (int k = 0; k < 8; k++) q[k] = __ldcs(p + (g + k * 32LL) * a.count);
+            for (int k = 0; k < 8; k++) q[k] = g + k * E < a.groups ? __ldcs(p + (g + k * (long long)E) * a.count) : make_float2(-INFINITY, 0.f);
 #pragma unroll
             for (int k = 0; k < 8; k++) join(q[k]);
         }
-        for (; g < a.groups; g += 32) join(__ldcs(p + g * a.count));
     }
     part[each][row] = make_float2(top, sum);
     __syncthreads();
     const long long r = r0 + warp;
     float label = 0.f, teacher = 0.f;
-    if (r < count) {
-        const float2 q = part[lane][warp];
-        top = warp_max(q.x);
-        sum = warp_sum(q.x == -INFINITY ? q.y : q.y * ex2(q.x - top));
+    if (warp < ROWS && r < count) {
+        top = -INFINITY;
+        sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < E; k += 32) join(part[k + lane][warp]);
+        const float all = warp_max(top);
+        sum = warp_sum(top == -INFINITY ? sum : sum * ex2(top - all));
+        top = all;
         const float lse2 = top + log2f(sum), lse = lse2 * kLn2;
         float c = 0.f;
         for (int s0 = lane; s0 < a.width; s0 += 128) {
@@ -444,7 +447,7 @@ __global__ void __launch_bounds__(32 * ROWS) vocab_rows_kernel(const Rows a)
         sum = t;
     };
 #pragma unroll 8
-    for (long long i = threadIdx.x; i < a.all; i += 32 * ROWS) {
+    for (long long i = threadIdx.x; i < a.all; i += T) {
         add(s.x, low.x, __ldcg(a.losses + i));
         add(s.y, low.y, __ldcg(a.losses + a.all + i));
     }
@@ -455,7 +458,7 @@ __global__ void __launch_bounds__(32 * ROWS) vocab_rows_kernel(const Rows a)
     if (threadIdx.x > 0) return;
     s = lost[0];
 #pragma unroll
-    for (int i = 1; i < ROWS; i++) {
+    for (int i = 1; i < T / 32; i++) {
         s.x += lost[i].x;
         s.y += lost[i].y;
     }
@@ -955,7 +958,10 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
         const int row_blocks = (int)((count + ROWS - 1) / ROWS);
         const Rows rows = {parts, b.groups, g.width, first, count, M, g.weight + first, z + first, info, losses, weights,
                            factor, g.done, all_blocks, g.active, g.index, loss};
-        VOC_TRY(launch_chained(vocab_rows_kernel, dim3((unsigned)row_blocks), 32 * ROWS, 0, 1, st, rows));
+        // Blocks of one or two rounds: more threads share a row (270 rows of 147322 columns with 180 candidates: 466 us -> 434 of the
+        // whole call, 2400 of 65536: 380 -> 368; but 4096 of 65536: 345 -> 365).
+        const bool wide = M <= 2LL * kSms * ROWS;
+        VOC_TRY(launch_chained(wide ? vocab_rows_kernel<1024> : vocab_rows_kernel<32 * ROWS>, dim3((unsigned)row_blocks), wide ? 1024 : 32 * ROWS, 0, 1, st, rows));
         if (!grads) continue;
         Dz d = {};
         d.e = w + b.off_e;
