@@ -13,8 +13,8 @@
 // so that no step waits for a sum across the block and a row costs one barrier.
 //
 // Measured (GB/s of the bytes above; a plain copy moves 6795): bf16 65536 x 4096 forward 5500, backward 5900 (272 us), 65536 x 1024 backward
-// 4850; fp32 65536 x 4096 4200 and 4300 (two pieces of 16 bytes for 8 values: bound by shared memory's instructions); 5003 x
-// 1537 fp32 backward 33 us, 16384 x 128 bf16 forward 3.2 and backward 7.6 us, 1 x 4096 forward 2.2 us on the device.
+// 4850; fp32 4096 x 4096 5700 and 5300; 5003 x
+// 1537 fp32 backward 27 us, 16384 x 128 bf16 forward 3.2 and backward 7.6 us, 1 x 4096 forward 2.2 us on the device.
 #include "k_linear.cuh"
 
 #include <type_traits>
@@ -34,9 +34,10 @@ __device__ __forceinline__ float from_value(float x) { return x; }
 __device__ __forceinline__ float from_value(bf16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// 8 neighbouring values as they lie in memory, and as four pairs
-template <typename T> struct Eight;
-template <> struct Eight<bf16> {
+// A piece of a row: the neighbouring values of 16 bytes, as they lie in memory and as pairs
+template <typename T> constexpr int PER = 16 / (int)sizeof(T);
+template <typename T> struct Piece;
+template <> struct Piece<bf16> {
     uint4 r;
     __device__ __forceinline__ void load(const void *p) { r = *static_cast<const uint4 *>(p); }
     __device__ __forceinline__ void pairs(float2 (&x)[4]) const
@@ -46,19 +47,13 @@ template <> struct Eight<bf16> {
         for (int k = 0; k < 4; k++) x[k] = make_float2(__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xffff0000u));
     }
 };
-template <> struct Eight<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const void *p)
+template <> struct Piece<float> {
+    uint4 r;
+    __device__ __forceinline__ void load(const void *p) { r = *static_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void pairs(float2 (&x)[2]) const
     {
-        a = static_cast<const float4 *>(p)[0];
-        b = static_cast<const float4 *>(p)[1];
-    }
-    __device__ __forceinline__ void pairs(float2 (&x)[4]) const
-    {
-        x[0] = make_float2(a.x, a.y);
-        x[1] = make_float2(a.z, a.w);
-        x[2] = make_float2(b.x, b.y);
-        x[3] = make_float2(b.z, b.w);
+        x[0] = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
+        x[1] = make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
     }
 };
 __device__ __forceinline__ void store_pairs(bf16 *p, const float2 (&x)[4])
@@ -71,33 +66,52 @@ __device__ __forceinline__ void store_pairs(bf16 *p, const float2 (&x)[4])
     }
     *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
-__device__ __forceinline__ void store_pairs(float *p, const float2 (&x)[4])
+__device__ __forceinline__ void store_pairs(float *p, const float2 (&x)[2])
 {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+    *reinterpret_cast<float4 *>(p) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+}
+// H pairs of a parameter, of either type
+template <int H> __device__ __forceinline__ void load_pairs(const float *p, float2 (&x)[H])
+{
+#pragma unroll
+    for (int k = 0; k < H; k += 2) {
+        const float4 v = *reinterpret_cast<const float4 *>(p + 2 * k);
+        x[k] = make_float2(v.x, v.y);
+        x[k + 1] = make_float2(v.z, v.w);
+    }
+}
+template <int H> __device__ __forceinline__ void load_pairs(const bf16 *p, float2 (&x)[H])
+{
+#pragma unroll
+    for (int k = 0; k < H; k += 2) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p + 2 * k);
+        x[k] = make_float2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u));
+        x[k + 1] = make_float2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+    }
 }
 
-// The columns of a thread: pieces of 8 neighbouring ones, as they lie in the aligned vectors of memory.  SHIFT: rows of a block
+// The columns of a thread: pieces, as they lie in the aligned vectors of memory.  SHIFT: rows of a block
 // (or of a part of a warp) start `shift` values behind a 16-byte boundary, all of them the same, because the rows that it takes
 // are a multiple of 8 apart; the vectors at a row's ends hold columns that are not its own.  So rows of any length
 // move in whole vectors (value by value, 5003 x 1537 in fp32 took 62 us backward).
-template <int LANES, bool SHIFT> struct Columns {
+template <typename T, int LANES, bool SHIFT> struct Columns {
+    static constexpr int H = PER<T> / 2;
     int n, shift, t;
-    __device__ __forceinline__ int first(int c) const { return (c * LANES + t) * 8 - (SHIFT ? shift : 0); }
+    __device__ __forceinline__ int first(int c) const { return (c * LANES + t) * PER<T> - (SHIFT ? shift : 0); }
     __device__ __forceinline__ bool has(int c) const { return first(c) < n; }
-    __device__ __forceinline__ bool full(int c) const { return !SHIFT || (first(c) >= 0 && first(c) + 8 <= n); }
+    __device__ __forceinline__ bool full(int c) const { return !SHIFT || (first(c) >= 0 && first(c) + PER<T> <= n); }
     // 0 where columns are not the row's
-    __device__ __forceinline__ void clip(float2 (&x)[4], int c) const
+    __device__ __forceinline__ void clip(float2 (&x)[H], int c) const
     {
         if (full(c)) return;
         const int j = first(c);
 #pragma unroll
-        for (int k = 0; k < 4; k++) {
+        for (int k = 0; k < H; k++) {
             if ((unsigned)(j + 2 * k) >= (unsigned)n) x[k].x = 0.f;
             if ((unsigned)(j + 2 * k + 1) >= (unsigned)n) x[k].y = 0.f;
         }
     }
-    template <typename T> __device__ __forceinline__ void store(T *row, int c, const float2 (&x)[4]) const
+    __device__ __forceinline__ void store(T *row, int c, const float2 (&x)[H]) const
     {
         const int j = first(c);
         if (full(c)) {
@@ -105,16 +119,16 @@ template <int LANES, bool SHIFT> struct Columns {
             return;
         }
 #pragma unroll
-        for (int k = 0; k < 4; k++) {
+        for (int k = 0; k < H; k++) {
             if ((unsigned)(j + 2 * k) < (unsigned)n) row[j + 2 * k] = from_f<T>(x[k].x);
             if ((unsigned)(j + 2 * k + 1) < (unsigned)n) row[j + 2 * k + 1] = from_f<T>(x[k].y);
         }
     }
     // a parameter, of either type (as scalars they took longer than the rows: 65536 x 4096 forward 603 us)
-    __device__ __forceinline__ void param(const void *p, int f32, int c, float missing, float2 (&w)[4]) const
+    __device__ __forceinline__ void param(const void *p, int f32, int c, float missing, float2 (&w)[H]) const
     {
 #pragma unroll
-        for (int k = 0; k < 4; k++) w[k] = both(missing);
+        for (int k = 0; k < H; k++) w[k] = both(missing);
         if (p == nullptr || !has(c)) return;
         const int j = first(c);
         if constexpr (SHIFT) {
@@ -123,47 +137,35 @@ template <int LANES, bool SHIFT> struct Columns {
                 return f32 ? __ldg(static_cast<const float *>(p) + i) : __bfloat162float(static_cast<const bf16 *>(p)[i]);
             };
 #pragma unroll
-            for (int k = 0; k < 4; k++) w[k] = make_float2(at(j + 2 * k), at(j + 2 * k + 1));
+            for (int k = 0; k < H; k++) w[k] = make_float2(at(j + 2 * k), at(j + 2 * k + 1));
         } else if (f32) {
-            Eight<float> e;
-            e.load(static_cast<const float *>(p) + j);
-            e.pairs(w);
+            load_pairs(static_cast<const float *>(p) + j, w);
         } else {
-            Eight<bf16> e;
-            e.load(static_cast<const bf16 *>(p) + j);
-            e.pairs(w);
+            load_pairs(static_cast<const bf16 *>(p) + j, w);
         }
     }
 };
 // Values between a row's start and the 16-byte boundary before it
 template <typename T> __device__ __forceinline__ int shift_of(long long r, long long stride) { return (int)(r * stride & (16 / sizeof(T) - 1)); }
 
-// The piece of 8 values at p that may lie across an argument's `end`: nothing from there on is read.
-template <typename T> __device__ __forceinline__ void load_piece(Eight<T> &e, const T *p, const T *end)
+// The piece at p that may lie across an argument's `end`: nothing from there on is read.
+template <typename T> __device__ __forceinline__ void load_piece(Piece<T> &e, const T *p, const T *end)
 {
-    if (p + 8 <= end) {
-        e.load(p);
-        return;
-    }
-    const uint4 *q = reinterpret_cast<const uint4 *>(p);
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    if constexpr (sizeof(T) == 2) {
-        e.r = linear::load16(q, end);
-    } else {
-        const uint4 u = (const void *)q < (const void *)end ? linear::load16(q, end) : zero, v = (const void *)(q + 1) < (const void *)end ? linear::load16(q + 1, end) : zero;
-        e.a = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
-        e.b = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
-    }
+    if (p + PER<T> <= end) e.load(p);
+    else e.r = linear::load16(reinterpret_cast<const uint4 *>(p), end);
 }
 
-__device__ __forceinline__ float sum8(const float2 (&x)[4])
+template <int H> __device__ __forceinline__ float sum_of(const float2 (&x)[H])
 {
-    const float2 s = add2(add2(x[0], x[1]), add2(x[2], x[3]));
+    float2 s = add2(x[0], x[1]);
+    if constexpr (H == 4) s = add2(s, add2(x[2], x[3]));
     return s.x + s.y;
 }
-__device__ __forceinline__ float dot8(const float2 (&x)[4], const float2 (&y)[4])
+template <int H> __device__ __forceinline__ float dot_of(const float2 (&x)[H], const float2 (&y)[H])
 {
-    const float2 s = fma2(x[3], y[3], fma2(x[2], y[2], fma2(x[1], y[1], mul2(x[0], y[0]))));
+    float2 s = mul2(x[0], y[0]);
+#pragma unroll
+    for (int k = 1; k < H; k++) s = fma2(x[k], y[k], s);
     return s.x + s.y;
 }
 template <int LANES> __device__ __forceinline__ float lane_sum(float s)
@@ -194,32 +196,33 @@ struct Bwd {
 
 constexpr int U = 2;   // rows of a thread on their way at a time
 
-template <typename T, int LANES, int CH, bool SHIFT> __global__ void __launch_bounds__(256, sizeof(T) == 2 && CH == 1 ? 4 : 1) norm_fwd_short_kernel(const Fwd a)
+template <typename T, int LANES, int EIGHTS, bool SHIFT> __global__ void __launch_bounds__(256, sizeof(T) == 2 && EIGHTS == 1 ? 4 : 1) norm_fwd_short_kernel(const Fwd a)
 {
+    constexpr int C = EIGHTS * 8 / PER<T>, H = PER<T> / 2;
     constexpr int R = 256 / LANES;   // a multiple of 8, as is the grid times it: the shift is the group's own
     chain_start();
     chain_wait();
     const int group = threadIdx.x / LANES;
-    const Columns<LANES, SHIFT> cols = {a.n, shift_of<T>(group, a.stride), (int)threadIdx.x % LANES};
+    const Columns<T, LANES, SHIFT> cols = {a.n, shift_of<T>(group, a.stride), (int)threadIdx.x % LANES};
     const T *end = static_cast<const T *>(a.x) + (a.rows - 1) * a.stride + a.n;
     const float inv_n = 1.f / (float)a.n;
-    float2 w[CH][4], b[CH][4];
+    float2 w[C][H], b[C][H];
     bool loaded = false;
     for (long long r0 = (long long)blockIdx.x * R * U; r0 < a.rows; r0 += (long long)gridDim.x * R * U) {
-        Eight<T> raw[U][CH];
+        Piece<T> raw[U][C];
 #pragma unroll
         for (int u = 0; u < U; u++) {
             const long long r = r0 + u * R + group;
             const T *row = static_cast<const T *>(a.x) + r * a.stride;
 #pragma unroll
-            for (int c = 0; c < CH; c++) {
-                raw[u][c] = Eight<T>();
+            for (int c = 0; c < C; c++) {
+                raw[u][c] = Piece<T>();
                 if (r < a.rows && cols.has(c)) load_piece(raw[u][c], row + cols.first(c), end);
             }
         }
         if (!loaded) {
 #pragma unroll
-            for (int c = 0; c < CH; c++) {
+            for (int c = 0; c < C; c++) {
                 cols.param(a.weight, a.param_f32, c, 1.f, w[c]);
                 cols.param(a.bias, a.param_f32, c, 0.f, b[c]);
             }
@@ -228,29 +231,29 @@ template <typename T, int LANES, int CH, bool SHIFT> __global__ void __launch_bo
 #pragma unroll
         for (int u = 0; u < U; u++) {
             const long long r = r0 + u * R + group;
-            float2 x[CH][4];
+            float2 x[C][H];
             float s = 0.f;
 #pragma unroll
-            for (int c = 0; c < CH; c++) {
+            for (int c = 0; c < C; c++) {
                 raw[u][c].pairs(x[c]);
                 cols.clip(x[c], c);
-                s += sum8(x[c]);
+                s += sum_of(x[c]);
             }
             const float mean = lane_sum<LANES>(s) * inv_n;
             s = 0.f;
 #pragma unroll
-            for (int c = 0; c < CH; c++) {
+            for (int c = 0; c < C; c++) {
 #pragma unroll
-                for (int k = 0; k < 4; k++) x[c][k] = add2(x[c][k], both(-mean));
+                for (int k = 0; k < H; k++) x[c][k] = add2(x[c][k], both(-mean));
                 cols.clip(x[c], c);
-                if (cols.has(c)) s += dot8(x[c], x[c]);
+                if (cols.has(c)) s += dot_of(x[c], x[c]);
             }
             const float rstd = 1.f / sqrtf(lane_sum<LANES>(s) * inv_n + a.eps);
             if (r >= a.rows) continue;
 #pragma unroll
-            for (int c = 0; c < CH; c++) {
+            for (int c = 0; c < C; c++) {
 #pragma unroll
-                for (int k = 0; k < 4; k++) x[c][k] = fma2(mul2(x[c][k], both(rstd)), w[c][k], b[c][k]);
+                for (int k = 0; k < H; k++) x[c][k] = fma2(mul2(x[c][k], both(rstd)), w[c][k], b[c][k]);
                 if (cols.has(c)) cols.store(static_cast<T *>(a.y) + r * a.n, c, x[c]);
             }
             if (a.stats != nullptr && cols.t == 0) {
@@ -261,32 +264,32 @@ template <typename T, int LANES, int CH, bool SHIFT> __global__ void __launch_bo
     }
 }
 
-template <typename T, int LANES, int CH, bool SHIFT> __global__ void __launch_bounds__(256, CH == 1 ? 3 : 2) norm_bwd_short_kernel(const Bwd a)
+template <typename T, int LANES, int EIGHTS, bool SHIFT> __global__ void __launch_bounds__(256, EIGHTS == 1 ? 3 : 2) norm_bwd_short_kernel(const Bwd a)
 {
-    constexpr int R = 256 / LANES;
-    __shared__ float across[R][2][LANES * CH * 8];
+    constexpr int C = EIGHTS * 8 / PER<T>, H = PER<T> / 2, R = 256 / LANES;
+    __shared__ float across[R][2][LANES * EIGHTS * 8];
     chain_start();
     chain_wait();
     const int group = threadIdx.x / LANES;
-    const Columns<LANES, SHIFT> cols = {a.n, shift_of<T>(group, a.x_stride), (int)threadIdx.x % LANES};
+    const Columns<T, LANES, SHIFT> cols = {a.n, shift_of<T>(group, a.x_stride), (int)threadIdx.x % LANES};
     const T *end_x = static_cast<const T *>(a.x) + (a.rows - 1) * a.x_stride + a.n, *end_d = static_cast<const T *>(a.dy) + (a.rows - 1) * a.dy_stride + a.n;
     const float inv_n = 1.f / (float)a.n;
-    float2 w[CH][4], dw[CH][4], db[CH][4];
+    float2 w[C][H], dw[C][H], db[C][H];
 #pragma unroll
-    for (int c = 0; c < CH; c++)
+    for (int c = 0; c < C; c++)
 #pragma unroll
-        for (int k = 0; k < 4; k++) dw[c][k] = db[c][k] = both(0.f);
+        for (int k = 0; k < H; k++) dw[c][k] = db[c][k] = both(0.f);
     bool loaded = false;
     for (long long r0 = (long long)blockIdx.x * R * U; r0 < a.rows; r0 += (long long)gridDim.x * R * U) {
-        Eight<T> rx[U][CH], rd[U][CH];
+        Piece<T> rx[U][C], rd[U][C];
         float mean[U], rstd[U];
 #pragma unroll
         for (int u = 0; u < U; u++) {
             const long long r = r0 + u * R + group;
             const bool live = r < a.rows;
 #pragma unroll
-            for (int c = 0; c < CH; c++) {
-                rx[u][c] = rd[u][c] = Eight<T>();
+            for (int c = 0; c < C; c++) {
+                rx[u][c] = rd[u][c] = Piece<T>();
                 if (live && cols.has(c)) {
                     load_piece(rx[u][c], static_cast<const T *>(a.x) + r * a.x_stride + cols.first(c), end_x);
                     load_piece(rd[u][c], static_cast<const T *>(a.dy) + r * a.dy_stride + cols.first(c), end_d);
@@ -297,37 +300,37 @@ template <typename T, int LANES, int CH, bool SHIFT> __global__ void __launch_bo
         }
         if (!loaded) {
 #pragma unroll
-            for (int c = 0; c < CH; c++) cols.param(a.weight, a.param_f32, c, 1.f, w[c]);
+            for (int c = 0; c < C; c++) cols.param(a.weight, a.param_f32, c, 1.f, w[c]);
             loaded = true;
         }
 #pragma unroll
         for (int u = 0; u < U; u++) {
             const long long r = r0 + u * R + group;
-            float2 h[CH][4], d[CH][4];
+            float2 h[C][H], d[C][H];
             float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-            for (int c = 0; c < CH; c++) {
+            for (int c = 0; c < C; c++) {
                 rx[u][c].pairs(h[c]);
                 rd[u][c].pairs(d[c]);
                 cols.clip(h[c], c);   // what lies beside the row need not be finite
                 cols.clip(d[c], c);   // d is 0 where there is no row or column
 #pragma unroll
-                for (int k = 0; k < 4; k++) {
+                for (int k = 0; k < H; k++) {
                     h[c][k] = mul2(add2(h[c][k], both(-mean[u])), both(rstd[u]));
                     dw[c][k] = fma2(d[c][k], h[c][k], dw[c][k]);
                     db[c][k] = add2(db[c][k], d[c][k]);
                     d[c][k] = mul2(d[c][k], w[c][k]);
                 }
-                s0 += sum8(d[c]);
-                s1 += dot8(d[c], h[c]);
+                s0 += sum_of(d[c]);
+                s1 += dot_of(d[c], h[c]);
             }
             if (a.dx == nullptr) continue;
             const float ma = lane_sum<LANES>(s0) * inv_n, mh = lane_sum<LANES>(s1) * inv_n;
             if (r >= a.rows) continue;
 #pragma unroll
-            for (int c = 0; c < CH; c++) {
+            for (int c = 0; c < C; c++) {
 #pragma unroll
-                for (int k = 0; k < 4; k++) h[c][k] = mul2(both(rstd[u]), fma2(h[c][k], both(-mh), add2(d[c][k], both(-ma))));
+                for (int k = 0; k < H; k++) h[c][k] = mul2(both(rstd[u]), fma2(h[c][k], both(-mh), add2(d[c][k], both(-ma))));
                 if (cols.has(c)) cols.store(static_cast<T *>(a.dx) + r * a.n, c, h[c]);
             }
         }
@@ -335,13 +338,13 @@ template <typename T, int LANES, int CH, bool SHIFT> __global__ void __launch_bo
     if (a.parts == nullptr) return;
     // by column: the groups' shifts differ
     if constexpr (SHIFT) {
-        for (int i = threadIdx.x; i < R * 2 * LANES * CH * 8; i += 256) (&across[0][0][0])[i] = 0.f;
+        for (int i = threadIdx.x; i < R * 2 * LANES * EIGHTS * 8; i += 256) (&across[0][0][0])[i] = 0.f;
         __syncthreads();
     }
 #pragma unroll
-    for (int c = 0; c < CH; c++) {
+    for (int c = 0; c < C; c++) {
 #pragma unroll
-        for (int k = 0; k < 8; k++) {
+        for (int k = 0; k < PER<T>; k++) {
             const int j = cols.first(c) + k;
             if ((unsigned)j < (unsigned)a.n) {
                 across[group][0][j] = k % 2 == 0 ? dw[c][k / 2].x : dw[c][k / 2].y;
@@ -368,65 +371,55 @@ __device__ __forceinline__ void cp_async16_part(void *dst, const void *src, int 
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::su32(dst)), "l"(src), "r"(bytes) : "memory");
 }
 
-constexpr int CH = 2;    // pieces of a thread
+constexpr int HELD = 16;   // values of a thread
 
 // Rows of an argument on their way through shared memory, a thread's own pieces by its own copies: no thread reads what
-// another one copied.  Copies are of 16 bytes, up to the argument's last value.
+// another one copied.  Copies are of 16 bytes, up to the argument's last value; a warp's are neighbours.  (Pieces of 8 values in fp32
+// too, two copies each with 16 bytes left out between threads: 4096 x 4096 forward 38 us, 23 so, backward 56 and 38.)
 template <typename T, int LANES, bool SHIFT> struct Ring {
-    static constexpr int V = sizeof(T) / 2;   // vectors of 8 values; apart in shared memory, so that a warp's accesses are neighbours
+    static constexpr int C = HELD / PER<T>, H = PER<T> / 2;
     const T *at, *end;      // the thread's place in the next row that is asked for; the argument's end
     long long step;         // from row to row
-    __device__ __forceinline__ Ring(const void *x, long long stride, long long rows, long long first, long long apart, const Columns<LANES, SHIFT> &cols)
+    __device__ __forceinline__ Ring(const void *x, long long stride, long long rows, long long first, long long apart, const Columns<T, LANES, SHIFT> &cols)
         : at(static_cast<const T *>(x) + first * stride + cols.first(0)), end(static_cast<const T *>(x) + (rows - 1) * stride + cols.n),
           step(apart * stride)
     {
     }
-    __device__ __forceinline__ void ask(const Columns<LANES, SHIFT> &cols, unsigned char *to)
+    __device__ __forceinline__ void ask(const Columns<T, LANES, SHIFT> &cols, unsigned char *to)
     {
 #pragma unroll
-        for (int c = 0; c < CH; c++) {
+        for (int c = 0; c < C; c++) {
             if (cols.has(c)) {
-                const T *p = at + c * LANES * 8;
-                unsigned char *q = to + (c * V * LANES + cols.t) * 16;
-                if (!SHIFT || p + 8 <= end) {
-#pragma unroll
-                    for (int v = 0; v < V; v++) ptx::cp_async16(q + v * LANES * 16, p + v * 8 / V);
+                const T *p = at + c * LANES * PER<T>;
+                unsigned char *q = to + (c * LANES + cols.t) * 16;
+                if (!SHIFT || p + PER<T> <= end) {
+                    ptx::cp_async16(q, p);
                 } else {
-#pragma unroll
-                    for (int v = 0; v < V; v++) {
-                        const int left = (int)(end - (p + v * 8 / V)) * (int)sizeof(T);
-                        cp_async16_part(q + v * LANES * 16, left > 0 ? p + v * 8 / V : p, left < 0 ? 0 : left < 16 ? left : 16);
-                    }
+                    const int left = (int)(end - p) * (int)sizeof(T);
+                    cp_async16_part(q, p, left < 0 ? 0 : left);
                 }
             }
         }
         at += step;
     }
-    static __device__ __forceinline__ Eight<T> raw(const Columns<LANES, SHIFT> &cols, const unsigned char *from, int c)
+    static __device__ __forceinline__ void take(const Columns<T, LANES, SHIFT> &cols, const unsigned char *from, int c, float2 (&x)[H])
     {
-        const unsigned char *q = from + (c * V * LANES + cols.t) * 16;
-        Eight<T> e;
-        if constexpr (V == 1) {
-            e.load(q);
-        } else {
-            e.a = *reinterpret_cast<const float4 *>(q);
-            e.b = *reinterpret_cast<const float4 *>(q + LANES * 16);
-        }
-        return e;
+        Piece<T> e;
+        e.load(from + (c * LANES + cols.t) * 16);
+        e.pairs(x);
     }
-    static __device__ __forceinline__ void take(const Columns<LANES, SHIFT> &cols, const unsigned char *from, int c, float2 (&x)[4]) { raw(cols, from, c).pairs(x); }
     // What lies beside a row in its first and last vectors becomes 0, once, where it has arrived: it may be anything.
-    static __device__ __forceinline__ void clean(const Columns<LANES, SHIFT> &cols, unsigned char *from)
+    static __device__ __forceinline__ void clean(const Columns<T, LANES, SHIFT> &cols, unsigned char *from)
     {
         if constexpr (SHIFT) {
 #pragma unroll
-            for (int c = 0; c < CH; c++) {
+            for (int c = 0; c < C; c++) {
                 if (!cols.has(c) || cols.full(c)) continue;
-                T *q = reinterpret_cast<T *>(from + (c * V * LANES + cols.t) * 16);
+                T *q = reinterpret_cast<T *>(from + (c * LANES + cols.t) * 16);
                 const int j = cols.first(c);
 #pragma unroll
-                for (int k = 0; k < 8; k++)
-                    if ((unsigned)(j + k) >= (unsigned)cols.n) q[k / (8 / V) * (LANES * 16 / (int)sizeof(T)) + k % (8 / V)] = from_f<T>(0.f);
+                for (int k = 0; k < PER<T>; k++)
+                    if ((unsigned)(j + k) >= (unsigned)cols.n) q[k] = from_f<T>(0.f);
             }
         }
     }
@@ -495,10 +488,10 @@ template <typename T, int LANES, bool SHIFT> __global__ void __launch_bounds__(m
     chain_start();
     chain_wait();
     const Group<LANES> g(a.rows);
-    const Columns<LANES, SHIFT> cols = {a.n, shift_of<T>(g.first, a.stride), g.t};
+    const Columns<T, LANES, SHIFT> cols = {a.n, shift_of<T>(g.first, a.stride), g.t};
     using Rows = Ring<T, LANES, SHIFT>;
     Rows rows(a.x, a.stride, a.rows, g.first, g.apart, cols);
-    constexpr int room = LANES * CH * 8 * (int)sizeof(T);
+    constexpr int C = Rows::C, H = Rows::H, room = LANES * HELD * (int)sizeof(T);
     const int count = g.count;
     unsigned char *const ring_start = ring + g.index * stages * room, *const ring_end = ring_start + stages * room;
     const auto next = [&](unsigned char *p) { return p + room == ring_end ? ring_start : p + room; };
@@ -511,9 +504,9 @@ template <typename T, int LANES, bool SHIFT> __global__ void __launch_bounds__(m
         asked++;
     };
     for (int i = 0; i < stages - 3; i++) ask();
-    float2 w[CH][4], b[CH][4];
+    float2 w[C][H], b[C][H];
 #pragma unroll
-    for (int c = 0; c < CH; c++) {
+    for (int c = 0; c < C; c++) {
         cols.param(a.weight, a.param_f32, c, 1.f, w[c]);
         cols.param(a.bias, a.param_f32, c, 0.f, b[c]);
     }
@@ -538,34 +531,34 @@ template <typename T, int LANES, bool SHIFT> __global__ void __launch_bounds__(m
             ask();   // where row i - 3 was
             Rows::clean(cols, p0);
 #pragma unroll
-            for (int c = 0; c < CH; c++) {
+            for (int c = 0; c < C; c++) {
                 if (!cols.has(c)) continue;
-                float2 x[4];
+                float2 x[H];
                 Rows::take(cols, p0, c, x);
-                sum += sum8(x);
+                sum += sum_of(x);
             }
         }
         if (i >= 1 && i <= count) {
 #pragma unroll
-            for (int c = 0; c < CH; c++) {
+            for (int c = 0; c < C; c++) {
                 if (!cols.has(c)) continue;
-                float2 x[4];
+                float2 x[H];
                 Rows::take(cols, p1, c, x);
 #pragma unroll
-                for (int k = 0; k < 4; k++) x[k] = add2(x[k], both(-mean1));
+                for (int k = 0; k < H; k++) x[k] = add2(x[k], both(-mean1));
                 cols.clip(x, c);
-                squares += dot8(x, x);
+                squares += dot_of(x, x);
             }
         }
         if (i >= 2) {
             const float rstd = 1.f / sqrtf(var * inv_n + a.eps);
 #pragma unroll
-            for (int c = 0; c < CH; c++) {
+            for (int c = 0; c < C; c++) {
                 if (!cols.has(c)) continue;
-                float2 x[4];
+                float2 x[H];
                 Rows::take(cols, p2, c, x);
 #pragma unroll
-                for (int k = 0; k < 4; k++) x[k] = fma2(mul2(add2(x[k], both(-mean2)), both(rstd)), w[c][k], b[c][k]);
+                for (int k = 0; k < H; k++) x[k] = fma2(mul2(add2(x[k], both(-mean2)), both(rstd)), w[c][k], b[c][k]);
                 cols.store(y, c, x);
             }
             y += g.apart * a.n;
@@ -597,10 +590,10 @@ template <typename T, int LANES, bool SHIFT> __global__ void __launch_bounds__(m
     chain_start();
     chain_wait();
     const Group<LANES> g(a.rows);
-    const Columns<LANES, SHIFT> cols = {a.n, shift_of<T>(g.first, a.x_stride), g.t};
+    const Columns<T, LANES, SHIFT> cols = {a.n, shift_of<T>(g.first, a.x_stride), g.t};
     using Rows = Ring<T, LANES, SHIFT>;
     Rows xs(a.x, a.x_stride, a.rows, g.first, g.apart, cols), ds(a.dy, a.dy_stride, a.rows, g.first, g.apart, cols);
-    constexpr int room = LANES * CH * 8 * (int)sizeof(T);
+    constexpr int C = Rows::C, H = Rows::H, room = LANES * HELD * (int)sizeof(T);
     const int count = g.count;
     unsigned char *const ring_start = ring + g.index * stages * 2 * room, *const ring_end = ring_start + stages * 2 * room;
     const auto next = [&](unsigned char *p) { return p + 2 * room == ring_end ? ring_start : p + 2 * room; };
@@ -616,12 +609,12 @@ template <typename T, int LANES, bool SHIFT> __global__ void __launch_bounds__(m
         asked++;
     };
     for (int i = 0; i < stages - 2; i++) ask();
-    float2 w[CH][4], dw[CH][4], db[CH][4];
+    float2 w[C][H], dw[C][H], db[C][H];
 #pragma unroll
-    for (int c = 0; c < CH; c++) {
+    for (int c = 0; c < C; c++) {
         cols.param(a.weight, a.param_f32, c, 1.f, w[c]);
 #pragma unroll
-        for (int k = 0; k < 4; k++) dw[c][k] = db[c][k] = both(0.f);
+        for (int k = 0; k < H; k++) dw[c][k] = db[c][k] = both(0.f);
     }
     for (int i = threadIdx.x; i < GROUPS * 128; i += blockDim.x) (&parts[0][0][0][0])[i] = 0.f;
     __syncthreads();
@@ -633,11 +626,11 @@ template <typename T, int LANES, bool SHIFT> __global__ void __launch_bounds__(m
     T *out = a.dx != nullptr ? static_cast<T *>(a.dx) + g.first * a.n : nullptr;
     int p = 0;
     // h and dy of a piece
-    const auto take = [&](const unsigned char *from, int c, float m, float q, float2 (&h)[4], float2 (&d)[4]) {
+    const auto take = [&](const unsigned char *from, int c, float m, float q, float2 (&h)[H], float2 (&d)[H]) {
         Rows::take(cols, from, c, h);
         Rows::take(cols, from + room, c, d);
 #pragma unroll
-        for (int k = 0; k < 4; k++) h[k] = mul2(add2(h[k], both(-m)), both(q));
+        for (int k = 0; k < H; k++) h[k] = mul2(add2(h[k], both(-m)), both(q));
     };
     for (int i = 0; i <= count && count > 0; i++) {
         float sa = 0.f, sh = 0.f;
@@ -653,18 +646,18 @@ template <typename T, int LANES, bool SHIFT> __global__ void __launch_bounds__(m
                 rstd = __ldg(stats + a.rows);
             }
 #pragma unroll
-            for (int c = 0; c < CH; c++) {
+            for (int c = 0; c < C; c++) {
                 if (!cols.has(c)) continue;
-                float2 h[4], d[4];
+                float2 h[H], d[H];
                 take(p0, c, m, q, h, d);
 #pragma unroll
-                for (int k = 0; k < 4; k++) {
+                for (int k = 0; k < H; k++) {
                     dw[c][k] = fma2(d[k], h[k], dw[c][k]);
                     db[c][k] = add2(db[c][k], d[k]);
                     d[k] = mul2(d[k], w[c][k]);
                 }
-                sa += sum8(d);
-                sh += dot8(d, h);
+                sa += sum_of(d);
+                sh += dot_of(d, h);
             }
         }
         if (out != nullptr) {
@@ -674,12 +667,12 @@ template <typename T, int LANES, bool SHIFT> __global__ void __launch_bounds__(m
                 ma *= inv_n;
                 mh *= inv_n;
 #pragma unroll
-                for (int c = 0; c < CH; c++) {
+                for (int c = 0; c < C; c++) {
                     if (!cols.has(c)) continue;
-                    float2 h[4], d[4];
+                    float2 h[H], d[H];
                     take(p1, c, mean1, rstd1, h, d);
 #pragma unroll
-                    for (int k = 0; k < 4; k++) h[k] = mul2(both(rstd1), fma2(h[k], both(-mh), fma2(d[k], w[c][k], both(-ma))));
+                    for (int k = 0; k < H; k++) h[k] = mul2(both(rstd1), fma2(h[k], both(-mh), fma2(d[k], w[c][k], both(-ma))));
                     cols.store(out, c, h);
                 }
                 out += g.apart * a.n;
@@ -701,10 +694,10 @@ template <typename T, int LANES, bool SHIFT> __global__ void __launch_bounds__(m
     float *sums = a.parts + (long long)blockIdx.x * 2 * a.n, *mine = groups == 1 ? sums : reinterpret_cast<float *>(ring) + g.index * 2 * a.n;
     __syncthreads();
 #pragma unroll
-    for (int c = 0; c < CH; c++) {
+    for (int c = 0; c < C; c++) {
         if (!cols.has(c)) continue;
 #pragma unroll
-        for (int k = 0; k < 8; k++) {
+        for (int k = 0; k < PER<T>; k++) {
             const int j = cols.first(c) + k;
             if (SHIFT && (unsigned)j >= (unsigned)a.n) continue;
             mine[j] = k % 2 == 0 ? dw[c][k / 2].x : dw[c][k / 2].y;
@@ -728,13 +721,14 @@ template <typename T, int LANES, bool SHIFT> __global__ void __launch_bounds__(L
     chain_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long r = blockIdx.x;
-    const Columns<LANES, SHIFT> cols = {a.n, shift_of<T>(r, a.stride), (int)threadIdx.x};
+    const Columns<T, LANES, SHIFT> cols = {a.n, shift_of<T>(r, a.stride), (int)threadIdx.x};
     const T *row = static_cast<const T *>(a.x) + r * a.stride, *end = static_cast<const T *>(a.x) + (a.rows - 1) * a.stride + a.n;
-    Eight<T> raw[CH];
-    float2 x[CH][4], w[4], b[4];
+    constexpr int C = HELD / PER<T>, H = PER<T> / 2;
+    Piece<T> raw[C];
+    float2 x[C][H], w[H], b[H];
 #pragma unroll
-    for (int c = 0; c < CH; c++) {
-        raw[c] = Eight<T>();
+    for (int c = 0; c < C; c++) {
+        raw[c] = Piece<T>();
         if (cols.has(c)) load_piece(raw[c], row + cols.first(c), end);
     }
     const auto total = [&](float s, float *part) {
@@ -745,28 +739,28 @@ template <typename T, int LANES, bool SHIFT> __global__ void __launch_bounds__(L
     };
     float s = 0.f;
 #pragma unroll
-    for (int c = 0; c < CH; c++) {
+    for (int c = 0; c < C; c++) {
         raw[c].pairs(x[c]);
         cols.clip(x[c], c);
-        s += sum8(x[c]);
+        s += sum_of(x[c]);
     }
     const float mean = total(s, part[0]) / (float)a.n;
     s = 0.f;
 #pragma unroll
-    for (int c = 0; c < CH; c++) {
+    for (int c = 0; c < C; c++) {
 #pragma unroll
-        for (int k = 0; k < 4; k++) x[c][k] = add2(x[c][k], both(-mean));
+        for (int k = 0; k < H; k++) x[c][k] = add2(x[c][k], both(-mean));
         cols.clip(x[c], c);
-        if (cols.has(c)) s += dot8(x[c], x[c]);
+        if (cols.has(c)) s += dot_of(x[c], x[c]);
     }
     const float rstd = 1.f / sqrtf(total(s, part[1]) / (float)a.n + a.eps);
 #pragma unroll
-    for (int c = 0; c < CH; c++) {
+    for (int c = 0; c < C; c++) {
         if (!cols.has(c)) continue;
         cols.param(a.weight, a.param_f32, c, 1.f, w);
         cols.param(a.bias, a.param_f32, c, 0.f, b);
 #pragma unroll
-        for (int k = 0; k < 4; k++) x[c][k] = fma2(mul2(x[c][k], both(rstd)), w[k], b[k]);
+        for (int k = 0; k < H; k++) x[c][k] = fma2(mul2(x[c][k], both(rstd)), w[k], b[k]);
         cols.store(static_cast<T *>(a.y) + r * a.n, c, x[c]);
     }
     if (a.stats != nullptr && threadIdx.x == 0) {
@@ -917,7 +911,7 @@ How how(const csa_layernorm_params &p, bool backward)
     };
     // rows of all arguments lie alike between boundaries
     const bool alike = (p.x_stride - n) % vector == 0 && (!backward || (p.dy_stride - n) % vector == 0);
-    h.shift = n % 8 != 0;
+    h.shift = n % vector != 0;
     const long long held = (long long)n + (h.shift && p.rows > 1 ? vector - 1 : 0);
     if (!alike || held > (size == 4 ? 8192 : 16384)) {
         blocks(1, 64);
@@ -932,7 +926,7 @@ How how(const csa_layernorm_params &p, bool backward)
     const int live = backward ? 2 : 3;
     h.lanes = held <= 1024 ? 64 : held <= 2048 ? 128 : held <= 3 * 1024 ? 192 : held <= 4096 ? 256 : held <= 6 * 1024 ? 384 : held <= 8192 ? 512 : 1024;
     h.groups = most_threads(h.lanes, backward) / h.lanes;
-    const int room = h.lanes * CH * 8 * size * (backward ? 2 : 1);
+    const int room = h.lanes * HELD * size * (backward ? 2 : 1);
     constexpr int shared = 225000 - GROUPS * 512;
     while (shared / h.groups / room < live + 1) h.groups--;   // a row on its way at least; the longest rows' ring holds 3 or 6
     h.stages = shared / h.groups / room;
@@ -956,15 +950,15 @@ template <typename F> cudaError_t short_shape(const How &h, const F &f)
 }
 template <typename T, typename F> cudaError_t ring_shape(const How &h, const F &f)
 {
-    if (h.lanes == 64) return f(Shape<64, CH>());
-    if (h.lanes == 128) return f(Shape<128, CH>());
-    if (h.lanes == 192) return f(Shape<192, CH>());
-    if (h.lanes == 256) return f(Shape<256, CH>());
-    if (h.lanes == 384) return f(Shape<384, CH>());
+    if (h.lanes == 64) return f(Shape<64, 2>());
+    if (h.lanes == 128) return f(Shape<128, 2>());
+    if (h.lanes == 192) return f(Shape<192, 2>());
+    if (h.lanes == 256) return f(Shape<256, 2>());
+    if (h.lanes == 384) return f(Shape<384, 2>());
     if constexpr (sizeof(T) == 2) {
-        if (h.lanes == 1024) return f(Shape<1024, CH>());
+        if (h.lanes == 1024) return f(Shape<1024, 2>());
     }
-    return f(Shape<512, CH>());
+    return f(Shape<512, 2>());
 }
 inline int long_threads(int n) { return n <= 2048 ? 128 : 1024; }
 

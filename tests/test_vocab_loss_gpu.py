@@ -334,6 +334,38 @@ def test_how_many_rows_are_packed(held, piece):
     B.csa_check_device_status()
 
 
+@pytest.mark.parametrize("dtype,x_stride", [("bf16", 515), ("bf16", 520), ("bf16", 700), ("f32", 513), ("f32", 516)])
+def test_packed_rows_with_strides(dtype, x_stride):
+    t = inputs(300, 512, 16384, dtype, slots=2, x_stride=x_stride, seed=x_stride)
+    check(t, B.VocabLossParams(300, 512, 16384, dtype, slots=2, labels_64=True, ids_64=True, x_stride=x_stride))
+
+
+@pytest.mark.parametrize("need", [(True, False), (False, True)])
+@pytest.mark.parametrize("piece", [0, 130])
+def test_packed_rows_one_gradient(need, piece):
+    t = inputs(300, 512, 16384)
+    p = B.VocabLossParams(300, 512, 16384, labels_64=True, piece_rows=piece)
+    want = B.csa_vocab_loss_bwd(p, t["x"], t["weight"], t["labels"])
+    got = B.csa_vocab_loss_bwd(p, t["x"], t["weight"], t["labels"], need_dx=need[0], need_dw=need[1])
+    for g, w, n in zip(got, want, (True, *need)):
+        assert torch.equal(g, w) if n else g is None
+
+
+def test_packed_rows_with_ids_outside_the_vocabulary():
+    """Such a row is NaN and no other row's loss is; nothing is read or written there."""
+    M, K, V = 300, 512, 16384
+    t = inputs(M, K, V, slots=3)
+    t["labels"][7], t["teacher_ids"][200, 1] = V, V + 5
+    p = B.VocabLossParams(M, K, V, slots=3, labels_64=True, ids_64=True)
+    rows = torch.empty(2, M, device="cuda")
+    loss = B.csa_vocab_loss_fwd(p, t["x"], t["weight"], t["labels"], t["teacher_ids"], t["teacher_logits"], row_loss=rows)
+    bad = rows.isnan()
+    assert bool(loss.isnan()) and bool(bad[0, 7]) and bool(bad[1, 200]) and int(bad.sum()) == 2
+    _, dx, _ = B.csa_vocab_loss_bwd(p, t["x"], t["weight"], t["labels"], t["teacher_ids"], t["teacher_logits"])
+    assert dx.isnan().any(dim=1).nonzero().flatten().tolist() == [7, 200]
+    B.csa_check_device_status()
+
+
 def test_rows_that_are_packed_away_are_not_read():
     M, K, V = 600, 512, 16384
     t = inputs(M, K, V, seed=2)
