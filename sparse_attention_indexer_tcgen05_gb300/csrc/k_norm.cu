@@ -590,7 +590,8 @@ template <typename T, int LANES, bool SHIFT> __global__ void __launch_bounds__(m
     chain_start();
     chain_wait();
     const Group<LANES> g(a.rows);
-    const Columns<T, LANES, SHIFT> cols = {a.n, shift_of<T>(g.first, a.x_stride), g.t};
+    // a group without rows adds zeros to every column: of a single row the threads hold no more columns than its own
+    const Columns<T, LANES, SHIFT> cols = {a.n, shift_of<T>(g.count > 0 ? g.first : 0, a.x_stride), g.t};
     using Rows = Ring<T, LANES, SHIFT>;
     Rows xs(a.x, a.x_stride, a.rows, g.first, g.apart, cols), ds(a.dy, a.dy_stride, a.rows, g.first, g.apart, cols);
     constexpr int C = Rows::C, H = Rows::H, room = LANES * HELD * (int)sizeof(T);

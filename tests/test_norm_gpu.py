@@ -158,6 +158,21 @@ def test_infinities_stay_in_their_row():
     assert bool(got[[2, 4]].isnan().any(1).all()) and torch.equal(got[[0, 1, 3, 5]], y[[0, 1, 3, 5]])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(1, 1023), (1, 2047), (2, 1017), (3, 2041)])
+def test_few_rows_after_many(rows, cols, dtype):
+    """What other rows left in shared memory is in no sum: parts of a block that have no row of their own add zeros."""
+    many = inputs(2000, cols, dtype, "f32")
+    many["x"] *= 1e15
+    many["dy"] *= 1e15
+    t, p, q = inputs(rows, cols, dtype, "f32", seed=1), B.LayerNormParams(rows, cols, dtype), B.LayerNormParams(2000, cols, dtype)
+    ones = torch.ones(2, 2000, device="cuda")
+    for _ in range(10):
+        B.csa_layernorm_bwd(q, many["dy"], many["x"], many["w"], ones)
+        _, stats = check_fwd(t, p)
+        check_bwd(t, p, stats)
+
+
 def test_no_rows():
     p = B.LayerNormParams(0, 24)
     x = torch.empty(0, 24, device="cuda", dtype=torch.bfloat16)
