@@ -135,19 +135,87 @@ __global__ void __launch_bounds__(1024) vocab_count_kernel(const Targets a)
     a.activity[blockIdx.x] = l | t;
 }
 
+using Key = unsigned long long;
+__device__ __forceinline__ void exchange(Key &x, Key &y, bool up)
+{
+    const bool swap = (x > y) == up;
+    const Key t = swap ? y : x;
+    y = swap ? x : y;
+    x = t;
+}
+// Ascending over a warp's lanes, R neighbouring ones each
+template <int R> __device__ __forceinline__ void sort_warp(Key (&x)[R])
+{
+    const int lane = threadIdx.x & 31;
+    const auto within = [&](auto &&up) {   // halves of R: one merge
+#pragma unroll
+        for (int j = R / 2; j > 0; j /= 2) {
+#pragma unroll
+            for (int r = 0; r < R; r++)
+                if ((r & j) == 0) exchange(x[r], x[r | j], up);
+        }
+    };
+#pragma unroll
+    for (int k = 2; k < R; k *= 2) {
+#pragma unroll
+        for (int j = k / 2; j > 0; j /= 2) {
+#pragma unroll
+            for (int r = 0; r < R; r++)
+                if ((r & j) == 0) exchange(x[r], x[r | j], (r & k) == 0);
+        }
+    }
+    within((lane & 1) == 0);
+#pragma unroll 1
+    for (int k = 2; k <= 32; k *= 2) {
+        const bool up = (lane & k) == 0;
+#pragma unroll 1
+        for (int d = k / 2; d > 0; d /= 2) {
+            const bool least = ((lane & d) == 0) == up;
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+                const Key y = __shfl_xor_sync(0xffffffffu, x[r], d);
+                if ((x[r] > y) == least) x[r] = y;
+            }
+        }
+        within(up);
+    }
+}
+
 // A warp a row.  Each target's place is the number of targets before it (smaller column, or the same and earlier).  V: the
 // values' type, where rows are packed; the last TAIL warps then put zeros behind the last packed row, as the k axis of dW takes whole
 // stages of 64.
 constexpr int TAIL = 64;
-template <typename V, bool PACK> __global__ void __launch_bounds__(32 * ROWS) vocab_prepare_kernel(const Targets a)
+
+// More candidates than this are sorted, by a bitonic network of their keys (column, then slot) in a warp's registers: comparing each
+// with each takes S^2 / 32 steps, the network S log^2 S / 128 longer ones.  4096 rows of 1024: 594 us -> 177 (the network in shared
+// memory 265), 2400 of 300: 75 -> 34, 3001 of 129: 40 -> 29; but of 100, four keys a lane: 22.6 -> 24.
+constexpr int MANY = 128;
+__host__ __device__ constexpr int keys_of(int slots)
 {
-    extern __shared__ int raw[];
+    int n = 2 * MANY;   // 8 keys a lane
+    while (n < slots) n *= 2;
+    return n;
+}
+// Shared memory of a row: columns, their order, and logits
+__host__ __device__ constexpr int prepare_bytes(int slots, int width)
+{
+    const int room = (width + 3) & ~3;
+    return slots > MANY ? 8 * keys_of(slots) + 4 * room : 12 * room;
+}
+// R: keys of a lane where candidates are sorted; 0: they are few.
+template <typename V, bool PACK, int R> __global__ void __launch_bounds__(32 * ROWS) vocab_prepare_kernel(const Targets a)
+{
+    extern __shared__ __align__(16) unsigned char raw[];
     chain_start();
     chain_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, room = (a.width + 3) & ~3;
     const long long r = (long long)blockIdx.x * ROWS + warp;
-    int *ids = raw + warp * 3 * room, *sorted = ids + room;
-    float *logits = reinterpret_cast<float *>(sorted + room);
+    constexpr bool many = R > 0;
+    constexpr int keyed = 32 * R;
+    unsigned char *const mine = raw + warp * prepare_bytes(a.slots, a.width);
+    int *ids = reinterpret_cast<int *>(mine), *sorted = ids + room;
+    Key *keys = reinterpret_cast<Key *>(mine);
+    float *logits = reinterpret_cast<float *>(mine + (many ? 8 * keyed : 8 * room));
     bool taught = false;
     long long label = -1, row = r;   // where the row's targets go
     if constexpr (PACK) {
@@ -228,10 +296,16 @@ template <typename V, bool PACK> __global__ void __launch_bounds__(32 * ROWS) vo
                 if (v >= a.vocab) l = NAN;
                 else top = fmaxf(top, l);
             }
-            ids[s] = v >= 0 && v < a.vocab ? (int)v : s < a.width ? NONE - s : NONE;   // behind every column, no two of the row alike
-            sorted[s] = -1;
+            const int id = v >= 0 && v < a.vocab ? (int)v : s < a.width ? NONE - s : NONE;   // behind every column, no two of the row alike
+            if (!many) {
+                ids[s] = id;
+                sorted[s] = -1;
+            } else if (s < a.slots) {
+                keys[s] = (Key)id << 32 | s;
+            }
             logits[s] = l;
         }
+        for (int s = a.slots + lane; s < keyed; s += 32) keys[s] = ~0ull;
         taught = __any_sync(0xffffffffu, any);
         float log_sum;
         if (a.lse != nullptr) {
@@ -245,6 +319,41 @@ template <typename V, bool PACK> __global__ void __launch_bounds__(32 * ROWS) vo
             log_sum = top + logf(sum);
         }
         __syncwarp();
+        const auto share = [&](int s) {
+            if (s < a.slots) return logits[s] == -INFINITY ? 0.f : expf(logits[s] - log_sum);   // also where no logit is finite
+            return label < 0 ? 0.f : label < a.vocab ? -1.f : -INFINITY;
+        };
+        const int own = label >= 0 && label < a.vocab ? (int)label : NONE;
+        if constexpr (many) {
+            Key x[R];
+#pragma unroll
+            for (int k = 0; k < R; k++) x[k] = keys[32 * k + lane];
+            sort_warp(x);
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < R; k++) keys[lane * R + k] = x[k];
+            __syncwarp();
+            // the label behind the candidates that name its column
+            for (int k = lane; k < a.slots; k += 32) {
+                const Key x = keys[k];
+                const int id = (int)(x >> 32);
+                const long long at = (k + (a.slots < a.width && id > own)) * a.rows + row;
+                a.sorted[at] = id;
+                a.weight[at] = share((int)(x & 0xffff));
+            }
+            if (a.slots < a.width) {
+                int low = 0, high = a.slots;   // candidates up to its column
+                while (low < high) {
+                    const int mid = (low + high) / 2;
+                    if ((int)(keys[mid] >> 32) <= own) low = mid + 1;
+                    else high = mid;
+                }
+                if (lane == 0) {
+                    a.sorted[low * a.rows + row] = own;
+                    a.weight[low * a.rows + row] = share(a.slots);
+                }
+            }
+        }
         // Places by smaller columns alone, four targets a lane at a time (one read of the others serves them all; with the question for
         // equal ones asked each time, 100 targets of 3001 rows took 30 us).  A place that nobody took tells that a column was
         // named twice: then the earlier one comes first.
@@ -266,31 +375,35 @@ template <typename V, bool PACK> __global__ void __launch_bounds__(32 * ROWS) vo
                 for (int q = 0; q < 4; q++) {
                     const int s = s0 + 32 * q;
                     if (s >= a.width) break;
-                    float t = label < 0 ? 0.f : label < a.vocab ? -1.f : -INFINITY;
-                    if (s < a.slots) t = logits[s] == -INFINITY ? 0.f : expf(logits[s] - log_sum);   // also where no logit is finite
                     sorted[place[q]] = id[q];
                     a.sorted[place[q] * a.rows + row] = id[q];
-                    a.weight[place[q] * a.rows + row] = t;
+                    a.weight[place[q] * a.rows + row] = share(s);
                 }
             }
             __syncwarp();
         };
-        put([](int x, int, int id, int) { return (int)(x < id); });
-        for (int s = lane; s < a.width; s += 32) twice |= sorted[s] < 0;
-        if (__any_sync(0xffffffffu, twice)) put([](int x, int j, int id, int s) { return (int)(x < id || (x == id && j < s)); });
+        if constexpr (!many) {
+            put([](int x, int, int id, int) { return (int)(x < id); });
+            for (int s = lane; s < a.width; s += 32) twice |= sorted[s] < 0;
+            if (__any_sync(0xffffffffu, twice)) put([](int x, int j, int id, int s) { return (int)(x < id || (x == id && j < s)); });
+        }
         // how many targets lie before group g: steps of halves, five searches at a time under one another's latency (as a walk
         // along the targets, 786 groups of 3001 rows took 20 us)
         int half = 1;
-        while (2 * half <= a.width) half *= 2;
+        const int entries = many ? a.slots : a.width;   // the label is beside the keys
+        while (2 * half <= entries) half *= 2;
+        const auto beyond = [&](int g) { return many && a.slots < a.width && (unsigned)own < (unsigned)g * GROUP ? 1 : 0; };
         for (int g0 = 0; g0 < a.groups && a.marks != nullptr; g0 += 128) {
             int at[5] = {};
             for (int step = half; step > 0; step /= 2) {
 #pragma unroll
                 for (int q = 0; q < 5; q++) {
                     const int k = at[q] + step;
-                    if (k <= a.width && (unsigned)sorted[k - 1] < (unsigned)(g0 + 32 * q + lane) * GROUP) at[q] = k;
+                    if (k <= entries && (unsigned)(many ? (int)(keys[k - 1] >> 32) : sorted[k - 1]) < (unsigned)(g0 + 32 * q + lane) * GROUP) at[q] = k;
                 }
             }
+#pragma unroll
+            for (int q = 0; q < 5; q++) at[q] += beyond(g0 + 32 * q + lane);
 #pragma unroll
             for (int q = 0; q < 4; q++) {
                 const int g = g0 + 32 * q + lane;
@@ -902,7 +1015,9 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
     const bool single = p.slots == 0;
     if (single) g.marks = nullptr;
     unsigned blocks = (unsigned)((M + ROWS - 1) / ROWS);
-    const size_t smem = (size_t)((g.width + 3) & ~3) * ROWS * 12;
+    const size_t smem = (size_t)prepare_bytes(p.slots, g.width) * ROWS;
+#define VOC_PREPARE(V, PACK) of_keys(vocab_prepare_kernel<V, PACK, 0>, vocab_prepare_kernel<V, PACK, 8>, vocab_prepare_kernel<V, PACK, 16>, vocab_prepare_kernel<V, PACK, 32>)
+    const auto of_keys = [&](auto few, auto r8, auto r16, auto r32) { return p.slots <= MANY ? few : p.slots <= 256 ? r8 : p.slots <= 512 ? r16 : r32; };
     const auto prepare = [&](void (*kernel)(Targets)) {
         const cudaError_t e = smem > 48 << 10 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) : cudaSuccess;
         return e != cudaSuccess ? e : launch_chained(kernel, dim3(blocks), 32 * ROWS, smem, 1, st, g);
@@ -922,13 +1037,13 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
         const unsigned words = (unsigned)((M + 31) / 32);
         VOC_TRY(launch_chained(vocab_count_kernel, dim3(words), 1024, 0, 1, st, g));
         blocks = (words * 32 + TAIL) / ROWS;
-        VOC_TRY(prepare(p.dtype == CSA_F32 ? vocab_prepare_kernel<float, true> : vocab_prepare_kernel<bf16, true>));
+        VOC_TRY(prepare(p.dtype == CSA_F32 ? VOC_PREPARE(float, true) : VOC_PREPARE(bf16, true)));
         blocks = words;   // of the counts
     } else if (single) {
         blocks = (unsigned)((M + 255) / 256);
         VOC_TRY(launch_chained(vocab_labels_kernel, dim3(blocks), 256, 0, 1, st, g));
     } else {
-        VOC_TRY(prepare(vocab_prepare_kernel<bf16, false>));
+        VOC_TRY(prepare(VOC_PREPARE(bf16, false)));
     }
 
     const bool grads = dx != nullptr || dw != nullptr;
@@ -959,8 +1074,8 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
         const Rows rows = {parts, b.groups, g.width, first, count, M, g.weight + first, z + first, info, losses, weights,
                            factor, g.done, all_blocks, g.active, g.index, loss};
         // Blocks of one or two rounds: more threads share a row (270 rows of 147322 columns with 180 candidates: 466 us -> 434 of the
-        // whole call, 2400 of 65536: 380 -> 368; but 4096 of 65536: 345 -> 365).
-        const bool wide = M <= 2LL * kSms * ROWS;
+        // whole call, 2400 of 65536: 380 -> 368; but 4096 of 65536: 345 -> 365), unless they have few (2400 of 16000: 35 -> 39).
+        const bool wide = M <= 2LL * kSms * ROWS && b.groups >= 512;
         VOC_TRY(launch_chained(wide ? vocab_rows_kernel<1024> : vocab_rows_kernel<32 * ROWS>, dim3((unsigned)row_blocks), wide ? 1024 : 32 * ROWS, 0, 1, st, rows));
         if (!grads) continue;
         Dz d = {};

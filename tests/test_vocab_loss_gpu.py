@@ -196,6 +196,19 @@ def test_both(M, K, V, slots, mean, labels_64, ids_64):
     check(t, p, 0.5, 0.3, 1.7, mean)
 
 
+@pytest.mark.parametrize("slots", [63, 64, 65, 127, 128, 129, 255, 256, 257, 512, 513, 1023, 1024])
+@pytest.mark.parametrize("M,K,V", [(37, 32, 100), (30, 64, 1100), (20, 32, 70000)])
+@pytest.mark.parametrize("labels", [True, False])
+def test_many_candidates(M, K, V, slots, labels):
+    """Around the numbers where targets are ordered in another way; columns named twice, by the label too, and slots without one."""
+    t = inputs(M, K, V, slots=slots, labels=labels, seed=slots + V)
+    if labels:
+        t["teacher_ids"][3:9, slots // 2] = t["labels"][3:9]
+        t["labels"][10], t["labels"][11] = 0, V - 1
+    t["teacher_ids"][12:15, 5:20] = t["teacher_ids"][12:15, 5:6]
+    check(t, B.VocabLossParams(M, K, V, slots=slots, labels_64=True, ids_64=True))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("M,piece", [(300, 100), (300, 256), (513, 256), (70, 7), (1025, 1024)])
 def test_pieces(M, piece, dtype):
