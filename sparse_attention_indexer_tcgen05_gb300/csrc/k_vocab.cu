@@ -147,7 +147,7 @@ __device__ __forceinline__ void exchange(Key &x, Key &y, bool up)
 template <int R> __device__ __forceinline__ void sort_warp(Key (&x)[R])
 {
     const int lane = threadIdx.x & 31;
-    const auto within = [&](auto &&up) {   // halves of R: one merge
+    const auto within = [&](bool up) {   // halves of R: one merge
 #pragma unroll
         for (int j = R / 2; j > 0; j /= 2) {
 #pragma unroll
@@ -181,11 +181,6 @@ template <int R> __device__ __forceinline__ void sort_warp(Key (&x)[R])
     }
 }
 
-// A warp a row.  Each target's place is the number of targets before it (smaller column, or the same and earlier).  V: the
-// values' type, where rows are packed; the last TAIL warps then put zeros behind the last packed row, as the k axis of dW takes whole
-// stages of 64.
-constexpr int TAIL = 64;
-
 // More candidates than this are sorted, by a bitonic network of their keys (column, then slot) in a warp's registers: comparing each
 // with each takes S^2 / 32 steps, the network S log^2 S / 128 longer ones.  4096 rows of 1024: 594 us -> 177 (the network in shared
 // memory 265), 2400 of 300: 75 -> 34, 3001 of 129: 40 -> 29; but of 100, four keys a lane: 22.6 -> 24.
@@ -202,7 +197,11 @@ __host__ __device__ constexpr int prepare_bytes(int slots, int width)
     const int room = (width + 3) & ~3;
     return slots > MANY ? 8 * keys_of(slots) + 4 * room : 12 * room;
 }
-// R: keys of a lane where candidates are sorted; 0: they are few.
+
+constexpr int TAIL = 64;
+// A warp a row.  Each target's place is the number of targets before it (smaller column, or the same and earlier).  V: the
+// values' type, where rows are packed; the last TAIL warps then put zeros behind the last packed row, as the k axis of dW takes whole
+// stages of 64.  R: keys of a lane where candidates are sorted; 0: they are few.
 template <typename V, bool PACK, int R> __global__ void __launch_bounds__(32 * ROWS) vocab_prepare_kernel(const Targets a)
 {
     extern __shared__ __align__(16) unsigned char raw[];
@@ -490,7 +489,15 @@ template <int T> __global__ void __launch_bounds__(T) vocab_rows_kernel(const Ro
     };
     if (r0 + row < count) {
         const float2 *p = a.parts + r0 + row;
-        for (int g = each; g < a.groups; g += 8 * E) {
+        int g = each;
+        for (; g + 7 * E < a.groups; g += 8 * E) {
+            float2 q[8];
+#pragma unroll
+            for (int k = 0; k < 8; k++) q[k] = __ldcs(p + (g + k * (long long)E) * a.count);
+#pragma unroll
+            for (int k = 0; k < 8; k++) join(q[k]);
+        }
+        if (g < a.groups) {
             float2 q[8];
 #pragma unroll
             for (int k = 0; k < 8; k++) q[k] = g + k * E < a.groups ? __ldcs(p + (g + k * (long long)E) * a.count) : make_float2(-INFINITY, 0.f);
@@ -1073,8 +1080,8 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
         const int row_blocks = (int)((count + ROWS - 1) / ROWS);
         const Rows rows = {parts, b.groups, g.width, first, count, M, g.weight + first, z + first, info, losses, weights,
                            factor, g.done, all_blocks, g.active, g.index, loss};
-        // Blocks of one or two rounds: more threads share a row (270 rows of 147322 columns with 180 candidates: 466 us -> 434 of the
-        // whole call, 2400 of 65536: 380 -> 368; but 4096 of 65536: 345 -> 365), unless they have few (2400 of 16000: 35 -> 39).
+        // Blocks of one or two rounds: more threads share a row (270 rows of 147322 columns with 180 candidates: 479 us -> 428 of the
+        // whole call, 2400 of 65536: 379 -> 367; but 4096 of 65536: 345 -> 365), unless they have few groups (2400 of 16000: 35 -> 39).
         const bool wide = M <= 2LL * kSms * ROWS && b.groups >= 512;
         VOC_TRY(launch_chained(wide ? vocab_rows_kernel<1024> : vocab_rows_kernel<32 * ROWS>, dim3((unsigned)row_blocks), wide ? 1024 : 32 * ROWS, 0, 1, st, rows));
         if (!grads) continue;
