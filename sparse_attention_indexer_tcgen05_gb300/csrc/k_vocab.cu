@@ -474,8 +474,10 @@ template <int T> __global__ void __launch_bounds__(T) vocab_rows_kernel(const Ro
     chain_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = threadIdx.x % ROWS, each = threadIdx.x / ROWS;
     const float2 w = weigh<T>(a.w, counted);
-    const float factor = w.x > 0.f ? w.x : w.y > 0.f ? w.y : 1.f;
-    const float2 share = make_float2(w.x > 0.f ? 1.f : 0.f, w.x > 0.f ? w.y / w.x : w.y > 0.f ? 1.f : 0.f);
+    // The larger weight is the products' factor: the other's ratio to it may vanish, but not overflow (1 to 1e-39), and what its rounding to
+    // bf16 with dz brings to all of its targets alike is a part of the smaller half of the gradient.
+    const float most = fmaxf(w.x, w.y), factor = most > 0.f ? most : 1.f;
+    const float2 share = make_float2(w.x / factor, w.y / factor);
     if (blockIdx.x == 0 && threadIdx.x == 0 && a.info != nullptr) *a.factor = factor;
     const long long r0 = (long long)blockIdx.x * ROWS, count = a.active != nullptr ? min(a.count, *a.active - a.first) : a.count;
     float top = -INFINITY, sum = 0.f;

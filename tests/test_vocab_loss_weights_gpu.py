@@ -93,3 +93,20 @@ def test_a_teachers_gradients_differ_by_random_roundings_alone(M, K, V, lse, dty
     limit = 2.0 ** -8.3 if dtype == "bf16" else 4e-6   # two roundings of 2^-8 / sqrt(3); fp32: sums of random signs
     near(dx, r["dz"] @ t["weight"].double(), limit, "dx")
     near(dw, r["dz"].t() @ t["x"].double(), limit, "dw")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("wl,wt", [(1e-39, 1.0), (1e-30, 1e10), (1.0, 1e-39), (1e10, 1e-30), (0.0, 0.7), (0.7, 0.0), (2.0 ** -126, 2.0 ** 20)])
+@pytest.mark.parametrize("mean", [True, False])
+def test_weights_far_apart(wl, wt, mean, dtype):
+    """Of each other: the smaller one's share of the gradient vanishes, and nothing else does."""
+    M, K, V = 300, 64, 700
+    t = inputs(M, K, V, dtype, slots=5, seed=5)
+    p = B.VocabLossParams(M, K, V, dtype, slots=5, labels_64=True, ids_64=True, label_weight=wl, teacher_weight=wt,
+                          reduction="mean" if mean else "sum")
+    loss, dx, dw = B.csa_vocab_loss_bwd(p, t["x"], t["weight"], **{k: t[k] for k in NAMES})
+    r = reference(t, wl=p.c.label_weight, wt=p.c.teacher_weight, mean=mean)
+    assert abs(float(loss) - float(r["loss"])) <= 1e-4 * abs(float(r["loss"]))
+    limit = 2.0 ** -8.3 if dtype == "bf16" else 4e-6
+    near(dx, r["dz"] @ t["weight"].double(), limit, "dx")
+    near(dw, r["dz"].t() @ t["x"].double(), limit, "dw")
