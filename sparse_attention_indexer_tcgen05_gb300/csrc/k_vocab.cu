@@ -414,6 +414,33 @@ template <typename V, bool PACK, int R> __global__ void __launch_bounds__(32 * R
     if constexpr (!PACK) count(a, lane == 0 && label >= 0, lane == 0 && taught);
 }
 
+// The blocks' counts joined into the first, where they are many: every block of vocab_rows_kernel reads them all, and their number grows with
+// the rows as that of the counts does.  Forward of rows of 8 over 64 columns with a candidate each, 8 rows a count: 2^21 rows 36.4 ms ->
+// 3.1, 2^17 273 us -> 209; 16384 (2048 counts) 39.6 -> 37.4, 8192 25.2 -> 27.2.
+constexpr int MANY_COUNTS = 2048;
+__global__ void __launch_bounds__(1024) vocab_sum_counts_kernel(int2 *counts, int blocks)
+{
+    __shared__ int2 part[32];
+    chain_start();
+    chain_wait();
+    int2 n = make_int2(0, 0);
+#pragma unroll 8
+    for (int b = threadIdx.x; b < blocks; b += 1024) {
+        const int2 c = counts[b];
+        n.x += c.x;
+        n.y += c.y;
+    }
+    n.x = __reduce_add_sync(0xffffffffu, n.x);
+    n.y = __reduce_add_sync(0xffffffffu, n.y);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = n;
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    n = part[threadIdx.x];
+    n.x = __reduce_add_sync(0xffffffffu, n.x);
+    n.y = __reduce_add_sync(0xffffffffu, n.y);
+    if (threadIdx.x == 0) counts[0] = n;
+}
+
 // What a row with a label, or with candidates, weighs in the loss; 0 where no row has one, so that what the others weigh is still a
 // factor of the products.  (With a label's weight beside a teacher alone, 1/n was in dz: at n = 3891 the whole gradient was 0.0019 off.)
 struct Weights {
@@ -1055,6 +1082,10 @@ cudaError_t launch_vocab_loss(const csa_vocab_loss_params &p, const void *x, con
         VOC_TRY(prepare(VOC_PREPARE(bf16, false)));
     }
 
+    if (blocks > MANY_COUNTS) {
+        VOC_TRY(launch_chained(vocab_sum_counts_kernel, dim3(1), 1024, 0, 1, st, const_cast<int2 *>(g.counts), (int)blocks));
+        blocks = 1;
+    }
     const bool grads = dx != nullptr || dw != nullptr;
     const Weights weights = {g.counts, (int)blocks, p.reduction == 0, p.label_weight, p.teacher_weight};
     float *z = reinterpret_cast<float *>(w + b.off_z);
