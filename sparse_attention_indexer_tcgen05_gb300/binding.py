@@ -1149,12 +1149,22 @@ def csa_rotary(x, positions, inv_freq, params: RopeParams):
     return CSARope.apply(x, positions, inv_freq, params)
 
 
-class CSALayerNorm(torch.autograd.Function):
+class _GradModeFunction(torch.autograd.Function):
+    """A function whose forward is told, by its last argument, whether autograd is on.  ctx.needs_input_grad is what the inputs ask
+    for, also under no_grad and inference_mode, and says nothing of whether there will be a backward pass."""
+
+    @classmethod
+    def apply(cls, *args):
+        return super().apply(*args, torch.is_grad_enabled())
+
+
+class CSALayerNorm(_GradModeFunction):
     """y = CSALayerNorm.apply(x, weight, bias, params): gradients flow to all three tensors (weight and bias may be None)."""
 
     @staticmethod
-    def forward(ctx, x, weight, bias, params):
-        stats = torch.empty((2, params.c.rows), dtype=torch.float32, device=x.device) if any(ctx.needs_input_grad[:3]) else None
+    def forward(ctx, x, weight, bias, params, grad):
+        keep = grad and any(ctx.needs_input_grad[:3])
+        stats = torch.empty((2, params.c.rows), dtype=torch.float32, device=x.device) if keep else None
         y = csa_layernorm_fwd(params, x, weight, bias, stats=stats)
         ctx.params, ctx.x_shape = params, x.shape
         ctx.shapes = [t.shape if t is not None else None for t in (weight, bias)]
@@ -1170,21 +1180,21 @@ class CSALayerNorm(torch.autograd.Function):
         if c.dy_stride:  # autograd hands contiguous gradients over
             p = LayerNormParams(c.rows, c.cols, c.dtype, c.param_dtype, c.eps, c.x_stride)
         grads = csa_layernorm_bwd(p, _own(dy), x, weight, stats, need[0], need[1], need[2])
-        return (*(g.view(shape) if g is not None else None for g, shape in zip(grads, (ctx.x_shape, *ctx.shapes))), None)
+        return (*(g.view(shape) if g is not None else None for g, shape in zip(grads, (ctx.x_shape, *ctx.shapes))), None, None)
 
 
 def csa_layernorm(x, weight=None, bias=None, *, params: LayerNormParams):
     return CSALayerNorm.apply(x, weight, bias, params)
 
 
-class CSAVocabLoss(torch.autograd.Function):
+class CSAVocabLoss(_GradModeFunction):
     """loss = CSAVocabLoss.apply(x, weight, labels, teacher_ids, teacher_logits, teacher_lse, params): gradients flow to x and
-    weight.  As with CSAIndexerLoss the forward makes them with the loss and keeps nothing else for the backward; the teacher's
-    side receives none."""
+    weight.  As with CSAIndexerLoss the forward makes them with the loss (the loss alone where autograd is off) and keeps nothing
+    else for the backward; the teacher's side receives none."""
 
     @staticmethod
-    def forward(ctx, x, weight, labels, teacher_ids, teacher_logits, teacher_lse, params):
-        need_dx, need_dw = ctx.needs_input_grad[:2]
+    def forward(ctx, x, weight, labels, teacher_ids, teacher_logits, teacher_lse, params, grad):
+        need_dx, need_dw = (grad and need for need in ctx.needs_input_grad[:2])
         targets = [t.contiguous() if t is not None else None for t in (labels, teacher_ids, teacher_logits, teacher_lse)]
         weight = weight.contiguous()
         if not (need_dx or need_dw):
@@ -1198,7 +1208,7 @@ class CSAVocabLoss(torch.autograd.Function):
     def backward(ctx, gloss):
         dx, dw = ctx.saved_tensors
         # scaled in fp32: gloss in bf16 would be off by one factor for all of a gradient's values
-        return (*((g.float() * gloss).to(g.dtype) if g is not None else None for g in (dx, dw)), None, None, None, None, None)
+        return (*((g.float() * gloss).to(g.dtype) if g is not None else None for g in (dx, dw)), *[None] * 6)
 
 
 def csa_vocab_loss(x, weight, labels=None, teacher_ids=None, teacher_logits=None, teacher_lse=None, *, params: VocabLossParams):
