@@ -1081,15 +1081,24 @@ def _own(grad):
     return grad.clone() if grad.data_ptr() % 16 else grad
 
 
-class CSALinear(torch.autograd.Function):
+class _GradModeFunction(torch.autograd.Function):
+    """A function whose forward is told, by its last argument, whether autograd is on.  ctx.needs_input_grad is what the inputs ask
+    for, also under no_grad and inference_mode, and says nothing of whether there will be a backward pass."""
+
+    @classmethod
+    def apply(cls, *args):
+        return super().apply(*args, torch.is_grad_enabled())
+
+
+class CSALinear(_GradModeFunction):
     """y = CSALinear.apply(x, weight, bias, residual, params): gradients flow to all four tensors (bias and residual
     may be None)."""
 
     @staticmethod
-    def forward(ctx, x, weight, bias, residual, params):
+    def forward(ctx, x, weight, bias, residual, params, grad):
         c = params.c
         preact = None
-        if c.activation != 0 and any(ctx.needs_input_grad[:3]):
+        if grad and c.activation != 0 and any(ctx.needs_input_grad[:3]):
             preact = torch.empty((c.rows, c.out_features), dtype=params.value_dtype, device=x.device)
         y = csa_linear_fwd(params, x, weight.contiguous(), bias, residual, preact=preact)
         ctx.params, ctx.x_shape = params, x.shape
@@ -1120,7 +1129,7 @@ class CSALinear(torch.autograd.Function):
             dx, dw, db = csa_linear_bwd(p, dy, x, weight.contiguous(), preact, need[0], need[1], need[2])
         return (dx.view(ctx.x_shape) if dx is not None else None, dw.view(weight.shape) if dw is not None else None,
                 db.view(ctx.bias_shape) if db is not None else None,
-                dres, None)
+                dres, None, None)
 
 
 def csa_linear(x, weight, bias=None, residual=None, *, params: LinearParams):
@@ -1147,15 +1156,6 @@ class CSARope(torch.autograd.Function):
 
 def csa_rotary(x, positions, inv_freq, params: RopeParams):
     return CSARope.apply(x, positions, inv_freq, params)
-
-
-class _GradModeFunction(torch.autograd.Function):
-    """A function whose forward is told, by its last argument, whether autograd is on.  ctx.needs_input_grad is what the inputs ask
-    for, also under no_grad and inference_mode, and says nothing of whether there will be a backward pass."""
-
-    @classmethod
-    def apply(cls, *args):
-        return super().apply(*args, torch.is_grad_enabled())
 
 
 class CSALayerNorm(_GradModeFunction):

@@ -45,3 +45,23 @@ def test_the_norm_keeps_no_statistics(B, monkeypatch, off, form):  # noqa: F811
     assert kept == [None] and not y.requires_grad
     z = call()
     assert kept[1] is not None and z.requires_grad and torch.equal(z, y)
+
+
+@pytest.mark.parametrize("off", OFF)
+@pytest.mark.parametrize("form", ["csa_linear", "apply"])
+def test_a_projection_keeps_no_z(B, monkeypatch, off, form):  # noqa: F811
+    x, w, b = leaves((6, 4), (5, 4), (5,))
+    p = B.LinearParams(6, 4, 5, "f32", activation="silu")
+    call = {"csa_linear": lambda: B.csa_linear(x, w, b, params=p), "apply": lambda: B.CSALinear.apply(x, w, b, None, p)}[form]
+    kept = []
+
+    def fwd(p, x, weight, bias=None, residual=None, preact=None, **_):
+        kept.append(preact)
+        return torch.nn.functional.silu(x @ weight.t() + bias)
+
+    monkeypatch.setattr(B, "csa_linear_fwd", fwd)
+    with off():
+        y = call()
+    assert kept == [None] and not y.requires_grad
+    z = call()
+    assert kept[1] is not None and z.requires_grad and torch.equal(z, y)
