@@ -415,7 +415,8 @@ typedef struct {
     int64_t piece_rows;         /* rows whose scores are held at a time; 0: as many as 4 GiB hold (at least 256) */
 } csa_vocab_loss_params;
 
-/* Device pointers.  labels or the teacher's (or both) must be given; without slots the teacher's are NULL. */
+/* Device pointers.  labels, or the teacher's ids and logits, or both must be given; without slots the teacher's are NULL, with them they
+ * may be, all three: the results are those of a call without slots. */
 typedef struct {
     const void *labels;            /* [rows] or NULL */
     const void *teacher_ids;       /* [rows, slots] or NULL */

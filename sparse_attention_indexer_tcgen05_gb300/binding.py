@@ -880,11 +880,14 @@ class VocabLossParams:
 
 
 def _vocab_targets(p, dev, labels, teacher_ids, teacher_logits, teacher_lse):
-    """The targets' addresses.  Without slots the teacher's tensors are refused, with them ids and logits are required."""
+    """The targets' addresses.  Without slots the teacher's tensors are refused; with them either target may be left out."""
     c = p.c
     if labels is not None:
         _check_flat(labels, "labels", torch.int64 if c.labels_64 else torch.int32, dev, c.rows)
-    if c.slots:
+    taught = teacher_ids is not None or teacher_logits is not None or teacher_lse is not None
+    if taught and not c.slots:
+        raise ValueError("a teacher needs VocabLossParams(slots=...)")
+    if taught:
         for name, t, dtype in (("teacher_ids", teacher_ids, torch.int64 if c.ids_64 else torch.int32),
                                ("teacher_logits", teacher_logits, torch.float32)):
             _check_flat(t, name, dtype, dev, c.rows * c.slots)
@@ -892,8 +895,6 @@ def _vocab_targets(p, dev, labels, teacher_ids, teacher_logits, teacher_lse):
                 raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{c.rows}, {c.slots}]")
         if teacher_lse is not None:
             _check_flat(teacher_lse, "teacher_lse", torch.float32, dev, c.rows)
-    elif teacher_ids is not None or teacher_logits is not None or teacher_lse is not None:
-        raise ValueError("a teacher needs VocabLossParams(slots=...)")
     elif labels is None:
         raise ValueError("labels or a teacher are required")
     return csa_vocab_targets(_ptr(labels), _ptr(teacher_ids), _ptr(teacher_logits), _ptr(teacher_lse))

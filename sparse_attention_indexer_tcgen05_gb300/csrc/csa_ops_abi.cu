@@ -111,8 +111,8 @@ csa_status check_targets(const csa_vocab_loss_params &p, const csa_vocab_targets
     if (t == nullptr) return CSA_ERR_INVALID_ARG;
     if (p.slots == 0 && (t->teacher_ids != nullptr || t->teacher_logits != nullptr || t->teacher_lse != nullptr)) return CSA_ERR_INVALID_ARG;
     if (p.rows == 0) return CSA_OK;
-    if (p.slots > 0 && (t->teacher_ids == nullptr || t->teacher_logits == nullptr)) return CSA_ERR_INVALID_ARG;
-    if (p.slots == 0 && t->labels == nullptr) return CSA_ERR_INVALID_ARG;
+    const bool ids = t->teacher_ids != nullptr, logits = t->teacher_logits != nullptr;
+    if (ids != logits || (!ids && (t->labels == nullptr || t->teacher_lse != nullptr))) return CSA_ERR_INVALID_ARG;
     CSA_TRY(need_scalar(t->labels, p.labels_64 ? 8 : 4));
     CSA_TRY(need_scalar(t->teacher_ids, p.ids_64 ? 8 : 4));
     CSA_TRY(need_scalar(t->teacher_logits, 4));
@@ -136,6 +136,7 @@ csa_status run_vocab_loss(const csa_vocab_loss_params *p, const void *x, const v
     const size_t ws = vocab_loss_workspace(q, backward);
     if (workspace_bytes < ws || (ws > 0 && workspace == nullptr)) return CSA_ERR_WORKSPACE;
     CSA_TRY(need_opt(workspace));
+    if (t->teacher_ids == nullptr) q.slots = 0;  // labels alone, in a part of the workspace
     if (q.rows > 0) {
         const void *inputs[] = {x, weight, t->labels, t->teacher_ids, t->teacher_logits, t->teacher_lse, loss, row_loss, dx};
         if (shares(loss, inputs, 6) || shares(row_loss, inputs, 7) || shares(dx, inputs, 8) || shares(dw, inputs, 9)) return CSA_ERR_INVALID_ARG;
