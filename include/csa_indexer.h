@@ -390,13 +390,16 @@ csa_status csa_layernorm_bwd(const csa_layernorm_params *p, const void *dy, cons
 /* ------------------------------------------------------------------ losses of a vocabulary */
 
 /* The model's own loss beside the indexer's: softmax cross entropy with labels, and distillation from the largest logits of
- * a teacher (the dense model of a sparse one), of hidden states x and the vocabulary's weight.  The scores x weight^T are
- * never kept as a whole.  Conventions as above.
+ * a teacher (the dense model of a sparse one), of hidden states x and the vocabulary's weight.  A forward keeps
+ * no scores (of few rows it does, in the workspace), a backward the exponentials of a piece of rows: 2 bytes a score (fp32 values 10),
+ * 4 GiB at most (or 256 rows) unless piece_rows says otherwise.  That is every row of a small call; fewer rows a piece take less memory
+ * and sum dw over more pieces.  Conventions as above.
  *   z = alpha x weight^T [rows, vocab];  lse_r = log sum_v exp z_rv
  *   label v of row r:     L_r = lse_r - z_rv; a row whose label is negative has none
  *   teacher of row r:     candidates v_s with logits l_s, s < slots; t_s = exp(l_s - N_r) with N_r the teacher's own log-sum-exp
  *                         (teacher_lse), or log sum_s exp l_s without it;  L_r = sum_s t_s (log t_s - z_{r, v_s} + lse_r), of
- *                         the candidates alone: what the teacher gives to other columns is in neither sum.  A slot with a negative id holds
+ *                         the candidates alone: what the teacher gives to other columns is in neither sum, so that with teacher_lse, where
+ *                         the t_s sum to less than 1, L_r may be negative.  A slot with a negative id holds
  *                         none, one with the logit -inf has t = 0; a row without candidates has no teacher.  Columns that a row names
  *                         twice count twice.
  *   loss = label_weight sum L / n + teacher_weight sum L / n, n the rows that have a label, or a teacher (at least 1), or 1
@@ -408,7 +411,9 @@ typedef struct {
     int32_t slots;              /* candidates of a row, at most 1024; 0: no teacher */
     int32_t labels_64, ids_64;  /* 0: labels (teacher_ids) are int32, 1: int64 */
     int32_t reduction;          /* 0: n as above (mean).  1: n = 1 (sum) */
-    float alpha;                /* scales the scores (1 / temperature); finite, not 0 */
+    float alpha;                /* scales the scores z of both losses, and no teacher's logit; finite, not 0.  Distillation at temperature T:
+                                 * 1 / T here, and teacher_logits / T with teacher_lse of such logits, by the caller.  Beside labels at
+                                 * temperature 1 that takes two calls */
     float label_weight, teacher_weight;   /* finite, >= 0 */
     int64_t rows;               /* >= 0 */
     int64_t x_stride;           /* elements from one row of x to the next; 0: features.  At least features */

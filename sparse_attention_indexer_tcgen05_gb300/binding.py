@@ -17,10 +17,10 @@ Around the step (what makes q_idx, w and k_idx out of hidden states, and updates
     csa_rope(params, x, positions, inv_freq)                        -> out          (rotary positions; also their gradient)
     csa_adamw(tensors, step, ...)                                                   (AdamW over many tensors, in place)
     csa_layernorm_fwd(params, x[, weight, bias])                    -> y            (the norm of rows)
-    csa_layernorm_fwd(params, x[, weight, bias])                    -> y            (the norm of rows)
     csa_layernorm_bwd(params, dy, x, weight, stats)                 -> (dx, dweight, dbias)
 
-The model's own loss (labels, a teacher's top logits, or both; scores of a vocabulary that are never kept):
+The model's own loss (labels, a teacher's top logits, or both).  The scores of a vocabulary go by without being kept; for gradients the
+exponentials of as many rows as 4 GiB hold are (VocabLossParams' piece_rows: of so many):
 
     csa_vocab_loss_fwd(params, x, weight[, labels, teacher_ids, teacher_logits, teacher_lse])   -> loss
     csa_vocab_loss_bwd(params, x, weight[, ...])                                                -> (loss, dx, dw)
@@ -857,8 +857,9 @@ def csa_layernorm_bwd(p: LayerNormParams, dy, x, weight=None, stats=None, need_d
 
 class VocabLossParams:
     """Losses of the scores z = alpha x W^T (the C struct csa_vocab_loss_params): x [rows, features], W [vocab, features].
-    slots: a teacher's candidates a row (0: labels alone).  reduction "mean": each loss over the rows that have it; "sum".
-    piece_rows: rows whose scores are held at a time (0: as many as 4 GiB hold)."""
+    alpha scales the scores of both losses; a teacher's logits are taken as they are given (at a temperature: divided by the caller).
+    slots: a teacher's candidates a row (0: labels alone; a call may leave the teacher, or the labels, out).  reduction "mean": each loss over the rows that have it; "sum".
+    piece_rows: rows whose scores' exponentials are held at a time for gradients (0: as many as 4 GiB hold)."""
 
     def __init__(self, rows, features, vocab, dtype="bf16", slots=0, alpha=1.0, label_weight=1.0, teacher_weight=1.0,
                  reduction="mean", labels_64=False, ids_64=False, x_stride=0, piece_rows=0):

@@ -18,7 +18,7 @@
 //
 // Bound by the three products (2 M K V operations each) at the tensor cores' power limit.  8192 rows of 2048 over 131072 columns, a
 // fifth of them without a target and so left out: scores 2.00 ms, this file's kernels 0.60 (dz: 4 bytes a score at 6.4 TB/s), dx
-// and dW 1.96 and 1.94; 6.6 ms as one call, 7.0 to 7.3 in a loop of calls, where the clock falls.
+// and dW 1.96 and 1.94; 6.6 ms as one call, 7.0 to 7.5 in a loop of calls, where the clock falls.
 #include "k_rows.cuh"
 #include "k_vocab.cuh"
 

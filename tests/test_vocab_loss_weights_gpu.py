@@ -1,6 +1,6 @@
 """What all rows' targets weigh in the vocabulary's losses: a factor of the gradients' products, rounded with no value of dz.
 
-A weight rounded with dz moves the whole gradient along itself by as much as the weight's rounding, up to 2^-9.  Of the roundings that
+A weight rounded with dz moves the whole gradient along itself by as much as the weight's rounding, up to 2^-8.  Of the roundings that
 are made, the result's cancel along it (2^-8 over the square root of the 2^17 and more values here), and so do the exponentials' in
 fp16.  dz's own do not where the values are alike: of targets with small p all 1 - p round the same way (5e-4 of the gradient where p
 is near 2^-9).  So what is compared with is the product of dz rounded as it should be: without the weight."""
